@@ -30,6 +30,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_BOUNDS = 0, 1, 2, 3, 4, 5
+ERR_RANGE = 6
 F32, BF16 = 0, 1
 CONTIGUOUS, ZIGZAG = 0, 1
 ZIGZAG_FWD, ZIGZAG_INV, A2A_FWD, A2A_INV = 0, 1, 2, 3
@@ -41,6 +42,13 @@ class CpattnDesc(ctypes.Structure):
                 ("a2a", ctypes.c_int32), ("layout", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("causal", ctypes.c_int32),
                 ("debug_fault", ctypes.c_int32)]
+
+
+class CpattnCacheDesc(ctypes.Structure):
+    _fields_ = [("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("page", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("o_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("causal", ctypes.c_int32)]
 
 
 class CpattnError(RuntimeError):
@@ -57,8 +65,22 @@ def make_desc(B, H_q, H_kv, T, D, cp, layout="zigzag", dtype="bf16", a2a=1, scal
                       1.0 / math.sqrt(D) if scale is None else scale, causal, debug_fault)
 
 
+def make_cache_desc(H_q, H_kv, D, page, n_pages, group=64, dtype="bf16", o_dtype=None, scale=None,
+                    causal=1) -> CpattnCacheDesc:
+    """Descriptor of one layer's 4-bit key/value cache; o_dtype defaults to dtype."""
+    dts = {"f32": F32, "bf16": BF16}
+    dt = dts.get(dtype, dtype)
+    odt = dt if o_dtype is None else dts.get(o_dtype, o_dtype)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D) if D > 0 else 0.0  # the calls refuse such a D
+    return CpattnCacheDesc(H_q, H_kv, D, group, page, n_pages, dt, odt, scale, causal)
+
+
 _vp = ctypes.c_void_p
 _st = ctypes.c_int
+_i = ctypes.c_int
+_i64 = ctypes.c_int64
+_cdesc = ctypes.POINTER(CpattnCacheDesc)
 _sigs = {
     "cpattn_partial_fwd": (_st, [ctypes.POINTER(CpattnDesc), ctypes.c_int, ctypes.c_int, _vp, _vp,
                                  _vp, _vp, _vp, _vp]),
@@ -93,6 +115,15 @@ _sigs = {
     "cpattn_layout_batch": (_st, [ctypes.c_int, ctypes.POINTER(CpattnDesc), ctypes.c_int,
                                   ctypes.POINTER(_vp), ctypes.POINTER(_vp),
                                   ctypes.POINTER(ctypes.c_int), _vp]),
+    "cpattn_cache_bytes": (ctypes.c_size_t, [_cdesc]),
+    "cpattn_cache_plan_workspace": (ctypes.c_size_t, [_cdesc, _i]),
+    "cpattn_cache_plan": (_st, [_cdesc, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp,
+                                ctypes.c_size_t, _vp]),
+    "cpattn_cache_append": (_st, [_cdesc, _i, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "cpattn_cache_read": (_st, [_cdesc, _i, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp]),
+    "cpattn_cache_attn_workspace": (ctypes.c_size_t, [_cdesc]),
+    "cpattn_cache_attn": (_st, [_cdesc, _i, _i, _i, _i, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _vp, ctypes.c_size_t, _vp]),
     "cpattn_check": (_st, [_vp]),
     "cpattn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "cpattn_timing_enable": (_st, [ctypes.c_int]),
@@ -259,6 +290,94 @@ def cpattn_layout_batch(permute, desc, srcs, dsts, n_heads, stream=None) -> int:
     heads = (ctypes.c_int * n)(*[int(h) for h in n_heads])
     return _lib.cpattn_layout_batch(permute, ctypes.byref(desc), n, src_arr, dst_arr, heads,
                                     _stream(stream))
+
+
+def cpattn_cache_bytes(desc) -> int:
+    return _lib.cpattn_cache_bytes(ctypes.byref(desc))
+
+
+def cpattn_cache_plan_workspace(desc, n_req) -> int:
+    return _lib.cpattn_cache_plan_workspace(ctypes.byref(desc), n_req)
+
+
+_DTYPE_NAMES = {F32: "torch.float32", BF16: "torch.bfloat16", "i32": "torch.int32"}
+
+
+def _typed(x, n, dtype, what) -> Optional[int]:
+    """Pointer of a contiguous tensor of the type with at least n numbers."""
+    if x is None or isinstance(x, int):
+        return x
+    name = _DTYPE_NAMES[dtype]
+    if str(x.dtype) != name or not x.is_contiguous() or x.numel() < n:
+        raise ValueError(f"{what} must be contiguous {name} with at least {n} entries")
+    return x.data_ptr()
+
+
+def _i32(x, n, what) -> Optional[int]:
+    return _typed(x, n, "i32", what)
+
+
+def _rows(x, n, heads, desc, what):
+    """(pointer, token stride, head stride) of a [n, heads, D] tensor of desc.dtype with
+    contiguous channels; a raw pointer stands for a contiguous one."""
+    if x is None or isinstance(x, int):
+        return x, heads * desc.D, desc.D
+    if (x.dim() != 3 or x.shape[0] < n or x.shape[1] != heads or x.shape[2] != desc.D or
+            x.stride(2) != 1 or str(x.dtype) != _DTYPE_NAMES.get(desc.dtype)):
+        raise ValueError(f"{what} must be [n_tokens, heads, D] of the descriptor's dtype with "
+                         "contiguous channels")
+    return x.data_ptr(), x.stride(0), x.stride(1)
+
+
+def _cache(x, desc) -> Optional[int]:
+    if x is not None and not isinstance(x, int):
+        if x.numel() * x.element_size() < cpattn_cache_bytes(desc):
+            raise ValueError("the cache is smaller than cpattn_cache_bytes(desc)")
+    return _ptr(x)
+
+
+def cpattn_cache_plan(desc, n_req, max_pages, len_old, len_new, table, free_list, n_free, n_free_out,
+                      len_out, q_start, slots, n_slots, workspace, ws_bytes=None, stream=None) -> int:
+    """Pages for requests that go from len_old to len_new tokens; block table, query
+    offsets and the slot of every new token."""
+    return _lib.cpattn_cache_plan(
+        ctypes.byref(desc), n_req, max_pages, _i32(len_old, n_req, "len_old"),
+        _i32(len_new, n_req, "len_new"), _i32(table, n_req * max_pages, "table"),
+        _i32(free_list, desc.n_pages, "free_list"), _i32(n_free, 1, "n_free"),
+        _i32(n_free_out, 1, "n_free_out"), _i32(len_out, n_req, "len_out"),
+        _i32(q_start, n_req + 1, "q_start"), _i32(slots, n_slots, "slots"), n_slots, _ptr(workspace),
+        _ws_bytes(workspace, ws_bytes), _stream(stream))
+
+
+def cpattn_cache_append(desc, n_tokens, k, v, slots, cache, stream=None) -> int:
+    """Quantises the rows of k and v ([n_tokens, H_kv, D], strided) into their slots."""
+    return _lib.cpattn_cache_append(ctypes.byref(desc), n_tokens, *_rows(k, n_tokens, desc.H_kv, desc, "k"),
+                                    *_rows(v, n_tokens, desc.H_kv, desc, "v"),
+                                    _i32(slots, n_tokens, "slots"), _cache(cache, desc), _stream(stream))
+
+
+def cpattn_cache_read(desc, n_tokens, slots, cache, k, v, stream=None) -> int:
+    """The rows of the slots as keys and values ([n_tokens, H_kv, D], strided)."""
+    return _lib.cpattn_cache_read(ctypes.byref(desc), n_tokens, _i32(slots, n_tokens, "slots"),
+                                  _cache(cache, desc), *_rows(k, n_tokens, desc.H_kv, desc, "k"),
+                                  *_rows(v, n_tokens, desc.H_kv, desc, "v"), _stream(stream))
+
+
+def cpattn_cache_attn_workspace(desc) -> int:
+    return _lib.cpattn_cache_attn_workspace(ctypes.byref(desc))
+
+
+def cpattn_cache_attn(desc, n_req, max_pages, n_tokens, max_q, q, q_start, kv_len, table, cache, o, lse,
+                      workspace, ws_bytes=None, stream=None) -> int:
+    """Attention of the new tokens q ([n_tokens, H_q, D], strided) over the cache; lse may
+    be None."""
+    return _lib.cpattn_cache_attn(
+        ctypes.byref(desc), n_req, max_pages, n_tokens, max_q, *_rows(q, n_tokens, desc.H_q, desc, "q"),
+        _i32(q_start, n_req + 1, "q_start"), _i32(kv_len, n_req, "kv_len"),
+        _i32(table, n_req * max_pages, "table"), _cache(cache, desc),
+        _typed(o, n_tokens * desc.H_q * desc.D, desc.o_dtype, "o"),
+        _typed(lse, n_tokens * desc.H_q, F32, "lse"), _ptr(workspace),
+        _ws_bytes(workspace, ws_bytes), _stream(stream))
 
 
 def cpattn_check(stream=None) -> int:

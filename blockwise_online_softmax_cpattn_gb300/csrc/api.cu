@@ -24,7 +24,7 @@ namespace cpattn {
 static std::mutex g_mu;
 static int* g_status_ptr[128];
 
-static int* status_ptr() {
+int* status_ptr() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return nullptr;
   std::lock_guard<std::mutex> lk(g_mu);
@@ -129,8 +129,6 @@ void timing_end(cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // validation
 // ---------------------------------------------------------------------------
-static bool aligned16(const void* p) { return p && ((uintptr_t)p % 16 == 0); }
-
 static cpattn_status validate(const cpattn_desc* d, Ring* R) {
   if (!d) return CPATTN_ERR_INVALID_ARG;
   if (d->B <= 0 || d->H_q <= 0 || d->H_kv <= 0 || d->T <= 0 || d->D <= 0 || d->cp <= 0 ||
@@ -161,10 +159,6 @@ static cpattn_status validate(const cpattn_desc* d, Ring* R) {
     R->debug_fault = d->debug_fault;
   }
   return CPATTN_OK;
-}
-
-static cpattn_status from_cuda(cudaError_t e) {
-  return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 
 }  // namespace cpattn
@@ -571,6 +565,7 @@ const char* cpattn_status_string(cpattn_status status) {
     case CPATTN_ERR_CUDA: return "CUDA error";
     case CPATTN_ERR_TIMEOUT: return "device wait timed out";
     case CPATTN_ERR_BOUNDS: return "device bounds check failed (debug build)";
+    case CPATTN_ERR_RANGE: return "value out of the cache's range";
     default: return "unknown status";
   }
 }

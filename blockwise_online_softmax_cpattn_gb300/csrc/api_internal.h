@@ -8,6 +8,15 @@
 
 namespace cpattn {
 
+// The current device's status word (null when it cannot be found).
+int* status_ptr();
+
+inline bool aligned16(const void* p) { return p && ((uintptr_t)p % 16 == 0); }
+
+inline cpattn_status from_cuda(cudaError_t e) {
+  return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
+}
+
 // cpattn_ring_bwd with optional work queued on its stream once dk and dv are final
 // (between the dK/dV and the dQ kernel on the tensor-core path, after both on the
 // exact path, which runs dQ first), and optionally the dQ kernel run in parts with

@@ -16,6 +16,7 @@ namespace cpattn {
 constexpr int kStatusLaunch = 3;   // a kernel found its launch unusable (reported as a CUDA error)
 constexpr int kStatusTimeout = 4;
 constexpr int kStatusBounds = 5;   // a bounds check of a CPATTN_DEBUG build failed
+constexpr int kStatusRange = 6;    // a value the 4-bit cache cannot hold
 
 // ---------------------------------------------------------------------------
 // Token position maps.  Slot = index on the layout-order token axis; position =

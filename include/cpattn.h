@@ -65,9 +65,11 @@ typedef enum cpattn_status {
   CPATTN_ERR_UNSUPPORTED = 2,
   CPATTN_ERR_CUDA = 3,
   CPATTN_ERR_TIMEOUT = 4,
-  CPATTN_ERR_BOUNDS = 5  /* only from a library built with CPATTN_DEBUG: a kernel's
+  CPATTN_ERR_BOUNDS = 5, /* only from a library built with CPATTN_DEBUG: a kernel's
                             bounds check on a computed tensor row failed, and the
                             access was skipped */
+  CPATTN_ERR_RANGE = 6    /* via cpattn_check: cpattn_cache_append met a NaN or a value
+                            beyond 2^120 (see there what it stored) */
 } cpattn_status;
 
 typedef enum cpattn_dtype { CPATTN_F32 = 0, CPATTN_BF16 = 1 } cpattn_dtype;
@@ -391,11 +393,151 @@ cpattn_status cpattn_layout_batch(int permute, const cpattn_desc* desc, int n,
                                   void* stream);
 
 /*
+ * A paged key/value cache held in 4 bits, for answering: the keys and values that
+ * the ring computed for a prompt (or a decoding step's new ones) are kept, and new
+ * tokens attend to them.  The pages this library follows define attention over whole
+ * sequences only: these calls are an addition of this library.
+ *
+ * The cache of one attention layer is one buffer of n_pages pages, `page` tokens
+ * each, handed out to requests in any order.  Slot s is token s % page of page
+ * s / page.  Per slot and K/V head it holds one row of keys and one of values, every
+ * `group` consecutive channels as 4-bit codes c with two bfloat16 numbers a and z.
+ * A channel stands for
+ *     round_bf16(a * (1 + c / 16) + z)                 (one rounding)
+ * and every call that reads the cache computes with exactly these values.  Bytes per
+ * slot and K/V head: D + 8 D / group (144 at D 128, group 64).
+ *
+ * Layout: [n_pages][H_kv] blocks; a block is page / 16 tiles of 16 tokens, a tile is
+ *     [K codes 16 x D/2 bytes][K (a, z) 16 x D/group words][V codes][V (a, z)]
+ * with 32-bit little-endian words.  Word W of a row of codes holds channels
+ * 8W .. 8W+7, channel 8W + 2p + e in bits 4(p + 4e) .. +3; words of keys are then
+ * rotated left by 3 bits.  An (a, z) word has a in its low half.  The rows of keys
+ * are in token order; of values, token 2t + e of every eight is in row t + 4e.
+ *
+ * Shared conventions: tokens are packed, one request's after the other's, and come
+ * first: q and o are [n_tokens][H_q][D], k and v [n_tokens][H_kv][D], lse
+ * [n_tokens][H_q].  Inputs q,
+ * k, v (and the outputs k, v of cpattn_cache_read) take strides in elements between
+ * tokens and between heads, multiples of 16 bytes, so slices of a fused projection
+ * or the ring's [H_kv][T][D] tensors are passed as they are; channels are contiguous.
+ * Lengths, tables and slots are device int32.  Lengths are taken as clamped to
+ * [0, max_pages * page].  A page or slot outside the cache is never touched: append
+ * skips it, read gives zeros, attention sees no key there.  All other rules (who owns
+ * buffers, alignment, streams, errors) are those of the calls above.
+ */
+typedef struct cpattn_cache_desc {
+  int32_t H_q;     /* query heads (a multiple of H_kv) */
+  int32_t H_kv;    /* key/value heads */
+  int32_t D;       /* head dimension: 64 or 128 */
+  int32_t group;   /* channels that share (a, z): 32, 64 or 128, at most D */
+  int32_t page;    /* tokens per page, a multiple of 16 */
+  int32_t n_pages; /* pages of the cache; n_pages * page < 2^31 */
+  int32_t dtype;   /* cpattn_dtype of q, k, v */
+  int32_t o_dtype; /* cpattn_dtype of o: dtype, or CPATTN_F32 (for cpattn_merge) */
+  float scale;     /* softmax scale, > 0 */
+  int32_t causal;  /* 1: query i of a request's n_q new tokens sees the keys up to position
+                      kv_len - n_q + i; 0: all kv_len keys (a shard of a cache that holds
+                      only keys before the queries; its o and lse merge by cpattn_merge) */
+} cpattn_cache_desc;
+
+/* Bytes of the cache of one layer (0 for an invalid descriptor). */
+size_t cpattn_cache_bytes(const cpattn_cache_desc* desc);
+
+/* Bytes of device workspace of cpattn_cache_plan for n_req requests. */
+size_t cpattn_cache_plan_workspace(const cpattn_cache_desc* desc, int n_req);
+
+/*
+ * Takes and returns pages for requests that go from len_old[r] to len_new[r] tokens
+ * (longer: new tokens; shorter: drafts taken back; 0: the request is over), and
+ * builds what the calls below take.  Everything stays on the device.
+ *   len_old, len_new : [n_req]
+ *   table      : [n_req][max_pages]; the first ceil(len_old[r] / page) entries of row r
+ *                are its pages.  A longer request's new pages are written behind them;
+ *                nothing else is, entries past a request's end are left as they are.
+ *   free_list  : [n_pages] ids of free pages, its first *n_free entries valid.
+ *   n_free     : the number of free pages before the call
+ *   n_free_out : after it.  May be n_free itself.
+ *   len_out    : [n_req]; may be len_old or len_new itself
+ *   q_start    : [n_req + 1] offsets of the requests' new tokens, max(new - old, 0) each,
+ *                in the packed order
+ *   slots      : [n_slots] slot of every new token, in the packed order; -1 behind the
+ *                last one (a padded batch)
+ * Pages a shorter request gives up go to the end of the list first, in the order of
+ * the requests and of their pages; then the requests take theirs in order, each from
+ * the list's end backwards.  The first request that finds too few pages left, and
+ * every later one that needs a page, keeps its old length in len_out, takes none, and
+ * its new tokens' slots are -1 (they still count in q_start); else len_out is len_new.
+ *   workspace  : at least cpattn_cache_plan_workspace(desc, n_req) bytes
+ * Total new tokens must stay below 2^31.  Of desc only page and n_pages matter.
+ */
+cpattn_status cpattn_cache_plan(const cpattn_cache_desc* desc, int n_req, int max_pages,
+                                const int32_t* len_old, const int32_t* len_new, int32_t* table,
+                                int32_t* free_list, const int32_t* n_free, int32_t* n_free_out,
+                                int32_t* len_out, int32_t* q_start, int32_t* slots, int n_slots,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Quantises n_tokens rows of keys and values into their slots.  Per group, in float32
+ * with every step rounded to nearest:  spread = max - min;  a = bf16(spread * (16/15)),
+ * 0 when that is below 2^-100;  z = bf16(min - a);  d = x - z;  c = how many of the 15
+ * borders a (33 + 2j) / 32, j = 0 .. 14, d is above (0 when a is 0).  A value is off by
+ * at most about a / 32, half a step, and the roundings to bfloat16.
+ *   slots : [n_tokens]; a slot outside [0, n_pages * page) skips its token.  Slots of
+ *           one call must differ: where two are the same, what that slot holds
+ *           afterwards is unspecified.  No other slot changes.
+ * The cache holds finite values only: a NaN is stored as 0 and a value beyond
+ * +-2^120 as that, and cpattn_check then reports CPATTN_ERR_RANGE.
+ */
+cpattn_status cpattn_cache_append(const cpattn_cache_desc* desc, int n_tokens, const void* k,
+                                  int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                                  int64_t v_token_stride, int64_t v_head_stride,
+                                  const int32_t* slots, void* cache, void* stream);
+
+/*
+ * Gives the rows of n_tokens slots back as keys and values of desc->dtype, for example
+ * a cached prefix for cpattn_ring_fwd.  A slot outside the cache gives rows of zeros.
+ */
+cpattn_status cpattn_cache_read(const cpattn_cache_desc* desc, int n_tokens, const int32_t* slots,
+                                const void* cache, void* k, int64_t k_token_stride,
+                                int64_t k_head_stride, void* v, int64_t v_token_stride,
+                                int64_t v_head_stride, void* stream);
+
+/* Bytes of device workspace of cpattn_cache_attn (partial results of long rows). */
+size_t cpattn_cache_attn_workspace(const cpattn_cache_desc* desc);
+
+/*
+ * Attention of the new tokens of n_req requests over their cached keys and values (the
+ * new tokens' own among them: append comes first), one decoding step, checked drafts
+ * or a chunk of a prompt:  o = softmax(scale q K^T) V,  lse = its log-sum-exp.
+ *   max_pages : row length of table
+ *   n_tokens  : rows of q, o and lse
+ *   max_q     : the largest number of new tokens of one request.  It only chooses the
+ *               kernel: the results hold for any q_start.
+ *   q_start   : [n_req + 1], non-decreasing: request r's new tokens are rows q_start[r]
+ *               .. q_start[r + 1] - 1.  Rows behind q_start[n_req] are left as they are.
+ *   kv_len    : [n_req] cached tokens, the new ones included
+ *   table     : [n_req][max_pages], as cpattn_cache_plan leaves it
+ *   o         : [n_tokens][H_q][D] of desc->o_dtype, contiguous
+ *   lse       : [n_tokens][H_q] float32 or null
+ *   workspace : at least cpattn_cache_attn_workspace(desc) bytes; calls that share it
+ *               must be ordered (one stream)
+ * A row that sees no key gets o = 0, lse = -inf.  Heads as above: query head h reads
+ * K/V head h / (H_q / H_kv).  The result does not depend on the order in which the
+ * GPU runs the work: repeated calls are bitwise equal.
+ */
+cpattn_status cpattn_cache_attn(const cpattn_cache_desc* desc, int n_req, int max_pages,
+                                int n_tokens, int max_q, const void* q, int64_t q_token_stride,
+                                int64_t q_head_stride, const int32_t* q_start,
+                                const int32_t* kv_len, const int32_t* table, const void* cache,
+                                void* o, float* lse, void* workspace, size_t ws_bytes,
+                                void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device status word of the
  * current device.  Returns the first device error since the last check
  * (CPATTN_ERR_TIMEOUT: a kernel's bounded wait ran out; CPATTN_ERR_BOUNDS: a
- * bounds check of a CPATTN_DEBUG build failed), CPATTN_ERR_CUDA on a CUDA error,
- * else CPATTN_OK.
+ * bounds check of a CPATTN_DEBUG build failed; CPATTN_ERR_RANGE: see
+ * cpattn_cache_append), CPATTN_ERR_CUDA on a CUDA error, else CPATTN_OK.
  */
 cpattn_status cpattn_check(void* stream);
 

@@ -22,10 +22,12 @@ What it computes, in plain numpy float64, following the pages' definitions:
   (tutorial, section "Zig-Zag Ring Attention") and the all-to-all
   head<->sequence re-layout of the hierarchical a2a+p2p mode (pull request #181,
   mode table row "a2a+p2p"; tutorial, section "Ulysses CP").
+* ``cache``: the 4-bit key/value cache (no counterpart on the pages): the format of
+  its rows, block tables from request lengths, attention over cached rows.
 
-Every function is pinned by CPU tests (``tests/test_oracle_*.py``) against closed
+Every function is pinned by CPU tests (``tests/test_oracle_*.py``, ``tests/test_cache_host.py``) against closed
 forms, invariants, finite differences, a library routine on the special cases it
 covers, brute force on tiny inputs and the values the pages print.  No function
 here is "parity unpinned".
 """
-from . import attention, layouts  # noqa: F401
+from . import attention, cache, layouts  # noqa: F401
