@@ -1,109 +1,897 @@
-// Attention of new tokens over the 4-bit cache.
+// Attention of new tokens over the 4-bit cache, for few query rows per K/V head
+// (decoding steps, drafts; float32 always).
 //
-// One warp per query row and head: the row's keys one after the other, each lane D / 32
-// channels, the running maximum and sum of the softmax in float32.
+// A row's answer needs every cached byte once and little else: at D = 128, group 64 a
+// token and K/V head is 144 bytes of HBM and 256 channels to turn into numbers, so the
+// kernel's two bounds are the memory and, close behind, the instructions that unpack
+// codes.  What it does about each:
+//
+//   Work.  An item is 8 NT query rows (new tokens x the heads of a K/V group) of one
+//   request and K/V head; it is cut into units of 32 cached tokens.  The units of all
+//   items are numbered through and every warp on the GPU takes an equal run of them, so
+//   neither ragged lengths nor few requests leave SMs idle, and nothing about lengths
+//   has to be known on the host.  A run ends anywhere: pieces of an item are joined by
+//   the (O, m, l) merge, first among the warps of a CTA in shared memory, then, for
+//   items that cross CTAs, by a second small kernel (a programmatic dependent) from the
+//   workspace.  Pieces are joined in their order: the result is the same every time.
+//
+//   Loads.  A tile of 16 tokens of one K/V head is contiguous (codes and their (a, z)):
+//   one bulk copy, of two tiles where a page holds both.  Each warp keeps a ring of
+//   its own of them in flight and waits for nobody else.
+//
+//   Arithmetic.  S^T = K Q^T and O^T = V^T P^T with mma.m16n8k16: the cached operand is
+//   the 16-row one, the query rows the 8 columns, so a decoding step's few rows fill
+//   the instruction as well as they can.  The cached operand goes from shared memory
+//   through registers: the layout of words and rows gives every lane the codes that
+//   its operand fragment needs by one wide load a row, without conflicts, and turning
+//   a pair of codes into a pair of bf16 values takes a shift, a logic operation and a
+//   packed FMA.  The query rows of S^T's fragment become the rows of P^T's by one
+//   8x8 transpose (movmatrix) a fragment.  (The fifth-generation MMA wants 64 or more
+//   rows and its operands written back to shared memory: a decoding step would fill a
+//   sixteenth of it.)
+//   The running maximum of a row moves only when a score exceeds it by more than 8 in
+//   log2 units; otherwise no lane needs to hear of the others' scores.
+//
+// float32 (NS = 3): q and P are sums of three bf16 numbers, the cached values are bf16
+// numbers anyway, so three MMAs give products of float32 quality.
 #include <math.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "cache.cuh"
 
 namespace cpattn {
 namespace cattn {
 
-constexpr int kThreads = 128;
+constexpr int kUnit = 32;            // cached tokens of a unit: two tiles
+constexpr int kSums = 256;           // entries of the prefix sums over requests
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr uint64_t kDrainTimeoutNs = 200000000ull;
+constexpr int kMaxSms = 160;         // of a GB300, and a few: the grid's and the workspace's size
 
-template <int D, typename T, bool OF32>
-__global__ void __launch_bounds__(kThreads) simple_kernel(Cache c, CacheAttnArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (id >= (int64_t)a.n_tokens * c.Hq) return;
-  const int row = (int)(id / c.Hq), hq = (int)(id - (int64_t)row * c.Hq);
-  const int h = hq / (c.Hq / c.Hkv);
-  if (row >= a.q_start[a.n_req]) return;
-  int lo = 0, hi = a.n_req;  // last request that starts at or before the row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.q_start[mid] <= row) lo = mid;
-    else hi = mid;
+struct Params {
+  Cache c;
+  CacheAttnArgs a;
+  int n_rep, stages;
+  int per_sum;                       // requests per entry of the prefix sums
+  float sl2;                         // scale * log2(e)
+};
+
+// ---------------------------------------------------------------------------
+// items
+// ---------------------------------------------------------------------------
+struct Req {
+  int begin, nq, len;
+};
+__device__ __forceinline__ Req request(const Params& p, int r) {
+  Req q;
+  const int b = min(max(p.a.q_start[r], 0), p.a.n_tokens);
+  const int e = min(max(p.a.q_start[r + 1], b), p.a.n_tokens);
+  q.begin = b;
+  q.nq = e - b;
+  q.len = min(max(p.a.kv_len[r], 0), p.a.max_pages * p.c.page);
+  return q;
+}
+// cached tokens that row block rb (RB rows) sees, and its units
+__device__ __forceinline__ int block_seen(const Params& p, const Req& q, int rb, int RB) {
+  if (!p.c.causal) return q.len;
+  const int64_t last = min((int64_t)q.nq * p.n_rep, (int64_t)(rb + 1) * RB) - 1;
+  const int64_t s = (int64_t)q.len - q.nq + last / p.n_rep + 1;
+  return (int)max((int64_t)0, min(s, (int64_t)q.len));
+}
+__device__ __forceinline__ int units_of(int seen) { return max(1, (seen + kUnit - 1) / kUnit); }
+__device__ __forceinline__ int64_t blocks_of(const Params& p, const Req& q, int RB) {
+  return ((int64_t)q.nq * p.n_rep + RB - 1) / RB;
+}
+// units of one K/V head of request r
+__device__ __forceinline__ int64_t head_units(const Params& p, const Req& q, int RB) {
+  const int nb = (int)blocks_of(p, q, RB);
+  int64_t n = 0;
+  for (int b = 0; b < nb; ++b) n += units_of(block_seen(p, q, b, RB));
+  return n;
+}
+
+// One item and a unit in it.  Items follow each other by row block, K/V head, request.
+struct Item {
+  Req q;
+  int r, h, rb, seen, units, u;
+  __device__ __forceinline__ void settle(const Params& p, int RB) {
+    seen = block_seen(p, q, rb, RB);
+    units = units_of(seen);
   }
-  const int r = lo;
-  const int begin = a.q_start[r], nq = a.q_start[r + 1] - begin;
-  if (row < begin || row >= begin + nq) return;
-  const int64_t most = (int64_t)a.max_pages * c.page;
-  int len = a.kv_len[r];
-  len = len < 0 ? 0 : len > most ? (int)most : len;
-  const int64_t seen = c.causal ? (int64_t)len - nq + (row - begin) + 1 : len;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) {
-    q[e] = (float)static_cast<const T*>(a.q)[row * a.qs.token + hq * a.qs.head + lane * E + e];
-    o[e] = 0.f;
-  }
-  const float sl2 = c.scale * 1.44269504088896340736f;
-  const int w = lane * E / 8;        // word of this lane's channels
-  for (int64_t p = 0; p < seen; ++p) {
-    const int pg = a.table[(int64_t)r * a.max_pages + p / c.page];
-    if (pg < 0 || pg >= c.n_pages) continue;
-    const int off = (int)(p % c.page), t = off % kCacheTile;
-    const uint8_t* tile = a.cache + c.tile_at(pg, h, off / kCacheTile);
-    float kv[2][E];
-    for (int x = 0; x < 2; ++x) {
-      const uint8_t* half = tile + x * c.half_tile();
-      const int rr = x ? cache_v_row(t) : t;
-      const uint32_t word = reinterpret_cast<const uint32_t*>(half)[rr * (D / 8) + w];
-      const uint32_t az = reinterpret_cast<const uint32_t*>(
-          half + kCacheTile * c.row_bytes())[rr * c.groups() + w * 8 / c.G];
-      uint32_t u[4];
-      if (x) codes_to_bf16<false>(word, u);
-      else codes_to_bf16<true>(word, u);
-      for (int e = 0; e < E; ++e) {
-        const int ch = (lane * E + e) & 7;
-        uint32_t y = 0;
-        for (int i = 0; i < 4; ++i)
-          if (i == ch >> 1) y = bf16x2_fma(u[i], az_a2(az), az_z2(az));
-        kv[x][e] = __uint_as_float((ch & 1) ? y & 0xffff0000u : y << 16);
+  __device__ __forceinline__ void next(const Params& p, int RB) {
+    u = 0;
+    if (++rb >= blocks_of(p, q, RB)) {
+      rb = 0;
+      if (++h == p.c.Hkv) {
+        h = 0;
+        do {
+          if (++r >= p.a.n_req) return;
+          q = request(p, r);
+        } while (q.nq == 0);
       }
     }
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], kv[0][e], s);
-    for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-    s *= sl2;
-    const float mn = max_nan(m, s);  // a NaN score makes its row NaN
-    const float f = mn == -INFINITY ? 1.f : exp2f(m - mn), pr = mn == -INFINITY ? 0.f : exp2f(s - mn);
-    l = l * f + pr;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + pr * kv[1][e];
-    m = mn;
+    settle(p, RB);
   }
-  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-  using O = std::conditional_t<OF32, float, T>;
-  for (int e = 0; e < E; ++e)
-    static_cast<O*>(a.o)[((int64_t)row * c.Hq + hq) * D + lane * E + e] = (O)(o[e] * inv);
-  if (lane == 0 && a.lse)
-    a.lse[(int64_t)row * c.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+};
+
+// ---------------------------------------------------------------------------
+// pieces: O (not divided by l), m and l of an item's rows
+// ---------------------------------------------------------------------------
+// slot: [rows][D] floats, then [rows] (m, l)
+template <int D, int RB>
+struct Slot {
+  static constexpr int kFloats = RB * (D + 2);
+  static __device__ __forceinline__ float2* ml(float* s) { return reinterpret_cast<float2*>(s + RB * D); }
+  static __device__ __forceinline__ const float2* ml(const float* s) {
+    return reinterpret_cast<const float2*>(s + RB * D);
+  }
+};
+// Workspace of a launch of at most `ctas` CTAs: a slot per warp (head pieces that other
+// work followed), a head and a tail slot per CTA, their states.
+template <int D, int RB, int WARPS>
+struct Work {
+  static constexpr size_t kSlot = (size_t)Slot<D, RB>::kFloats;
+  static __host__ __device__ size_t cta_slots(int ctas) { return (size_t)ctas * WARPS * kSlot; }
+  static __host__ __device__ size_t meta(int ctas) { return (size_t)ctas * (WARPS + 2) * kSlot; }
+};
+// What a CTA leaves for the second kernel: the state of its head piece (the part of an
+// item that an earlier CTA began) and whether a tail piece (of an item begun here)
+// is open.
+struct CtaMeta {
+  int head;   // 0 none, 1 ends the item, 2 the item goes on
+  int tail;   // 1: open
+  int begin, nq, h, rb;  // the tail's item
+};
+
+// Row rho of a block -> its row of q and o
+__device__ __forceinline__ int64_t out_row(const Params& p, int begin, int h, int rb, int RB, int rho) {
+  const int64_t x = (int64_t)rb * RB + rho;
+  const int64_t tok = x / p.n_rep;
+  return (begin + tok) * p.c.Hq + h * p.n_rep + (int)(x - tok * p.n_rep);
 }
+__device__ __forceinline__ int block_rows(const Params& p, int nq, int rb, int RB) {
+  return (int)min((int64_t)RB, (int64_t)nq * p.n_rep - (int64_t)rb * RB);
+}
+
+__device__ __forceinline__ void store4(const Params& p, int64_t row, int D, int ch, float4 v) {
+  if (p.c.bf16 && !p.c.o_f32)
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.o) + row * D + ch) =
+        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(p.a.o) + row * D + ch) = v;
+}
+// 1 / l for the rows that saw a key (NaN for those that met one)
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// An item's rows from their sums: divided and written, 4 channels a thread.
+template <int D>
+__device__ __forceinline__ void write_out(const Params& p, int64_t row, int ch, float m, float l, float4 o) {
+  const float inv = inverse(l);
+  store4(p, row, D, ch, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (ch == 0 && p.a.lse) p.a.lse[row] = lse_of(m, l);
+}
+
+// The sums of 4 channels of one row over pieces.  add() keeps the maximum so far.
+struct Acc {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float2 ml, float4 x) {
+    const float mn = max_nan(m, ml.x);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(m - base), w = ex2(ml.x - base);
+    m = mn;
+    l = fmaf(l, f, w * ml.y);
+    o.x = fmaf(o.x, f, w * x.x);
+    o.y = fmaf(o.y, f, w * x.y);
+    o.z = fmaf(o.z, f, w * x.z);
+    o.w = fmaf(o.w, f, w * x.w);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// MMA fragments
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// A pair of floats as NS bf16 pairs that sum to it
+template <int NS>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&u)[NS]) {
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    u[s] = pack_bf16(x, y);
+    if (s + 1 < NS) {
+      x -= __uint_as_float(u[s] << 16);
+      y -= __uint_as_float(u[s] & 0xffff0000u);
+    }
+  }
+}
+
+template <int D, int NT, int NS, int WARPS, int MINB>
+__global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) {
+  constexpr int RB = 8 * NT;
+  constexpr int KW = D / 32;    // words of a K row per lane (channels 8 KW t4 ..)
+  constexpr int VW = D / 64;    // words of a V row per lane (channels 8 VW g ..)
+  constexpr int MT = D / 16;    // 16-channel tiles of O^T
+  using S = Slot<D, RB>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t sums[kSums];      // inclusive prefix sums of units over requests
+  __shared__ int64_t warp_part[WARPS];
+  __shared__ uint64_t bars_[WARPS * 8];
+  __shared__ int abort_;
+  struct PieceMeta {
+    int head;         // 0 none, 1 ends the item, 2 goes on
+    int head_global;  // the head piece is in the workspace, not in shared memory
+    int tail;         // 1: open
+    int rows, begin, h, rb, nq;  // of the tail's item
+    int head_rows;
+  };
+  __shared__ PieceMeta meta[WARPS];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int tile_bytes = p.c.tile_bytes(), half = p.c.half_tile(), par_words = p.c.groups();
+  const int stage_bytes = 2 * tile_bytes;
+  volatile int* abort = &abort_;
+  if (threadIdx.x == 0) abort_ = 0;
+  if (lane == 0) {
+    for (int s = 0; s < p.stages; ++s) mbar_init(smem_u32(&bars_[warp * 8 + s]), 1);
+    fence_barrier_init();
+  }
+  griddep_launch_dependents();
+
+  // ---- prefix sums of units over the requests --------------------------------
+  int64_t total;
+  {
+    int64_t run = 0;
+    constexpr int PT = kSums / (WARPS * 32) > 0 ? kSums / (WARPS * 32) : 1;
+    // thread t's entries are PT neighbours, so one scan over threads gives all sums
+    int64_t mine[PT];
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int e = threadIdx.x * PT + i;
+      int64_t n = 0;
+      const int64_t r0 = (int64_t)e * p.per_sum;
+      for (int64_t r = r0; r < r0 + p.per_sum && r < p.a.n_req; ++r) {
+        const Req q = request(p, (int)r);
+        if (q.nq > 0) n += head_units(p, q, RB) * p.c.Hkv;
+      }
+      run += n;
+      mine[i] = run;
+    }
+    int64_t inc = run;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, m);
+      if (lane >= m) inc += y;
+    }
+    if (lane == 31) warp_part[warp] = inc;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += warp_part[w];
+      total += warp_part[w];
+    }
+#pragma unroll
+    for (int i = 0; i < PT; ++i) sums[threadIdx.x * PT + i] = before + inc - run + mine[i];
+    __syncthreads();
+  }
+
+  // ---- this warp's run of units ----------------------------------------------
+  // CTAs that would get none are not counted, so that an item's CTAs are neighbours
+  using W = Work<D, RB, WARPS>;
+  float* const ws = static_cast<float*>(p.a.ws);
+  CtaMeta* const out_meta = reinterpret_cast<CtaMeta*>(ws + W::meta(gridDim.x));
+  const int ctas = (int)min((int64_t)gridDim.x, total);
+  if ((int)blockIdx.x >= ctas) {
+    if (threadIdx.x == 0) out_meta[blockIdx.x].head = out_meta[blockIdx.x].tail = 0;
+    return;
+  }
+  const int64_t c0 = total * blockIdx.x / ctas, c1 = total * (blockIdx.x + 1) / ctas;
+  const int64_t v0 = c0 + (c1 - c0) * warp / WARPS, v1 = c0 + (c1 - c0) * (warp + 1) / WARPS;
+  int steps = (int)(v1 - v0);
+  float* const slot_smem = reinterpret_cast<float*>(smem + (size_t)warp * p.stages * stage_bytes);
+  float* const slot_ws = ws + ((size_t)blockIdx.x * WARPS + warp) * S::kFloats;
+  if (lane == 0) {
+    meta[warp].head = 0;
+    meta[warp].tail = 0;
+  }
+  Item in;       // of the copies
+  bool ok = true;
+  int64_t x = 0;
+  if (steps > 0) {
+    int lo = 0, hi = kSums - 1;  // first entry whose inclusive sum is past v0
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sums[mid] > v0) hi = mid;
+      else lo = mid + 1;
+    }
+    x = v0 - (lo ? sums[lo - 1] : 0);
+    // (the bounds of these searches matter only if lengths change under the kernel)
+    for (in.r = lo * p.per_sum; in.r < p.a.n_req; ++in.r) {
+      in.q = request(p, in.r);
+      if (in.q.nq == 0) continue;
+      const int64_t hu = head_units(p, in.q, RB);
+      if (x < hu * p.c.Hkv) {
+        in.h = (int)(x / hu);
+        x -= in.h * hu;
+        break;
+      }
+      x -= hu * p.c.Hkv;
+    }
+    if (in.r >= p.a.n_req) steps = 0;
+  }
+  if (steps > 0) {
+    const int64_t nb = blocks_of(p, in.q, RB);
+    for (in.rb = 0; in.rb < nb; ++in.rb) {
+      in.settle(p, RB);
+      if (x < in.units) break;
+      x -= in.units;
+    }
+    if (in.rb >= nb) steps = 0;
+  }
+  if (steps > 0) {
+    in.u = (int)x;
+
+    Item it = in;  // of the arithmetic
+    int to_issue = steps;
+    const uint32_t ring = smem_u32(slot_smem);
+    int stage_in = 0, stage = 0;
+    uint32_t parity = 0, valid = 0;  // two bits a stage: which tiles were loaded
+    int tab = -1, tab_at = -1000000; // pages of tiles tab_at + lane of in's request
+    // issues the copies of the next unit
+    auto issue = [&]() {
+      const int t0 = in.u * 2;
+      if (t0 - tab_at >= 32 || t0 < tab_at) {
+        tab_at = t0;
+        const int64_t tok = (int64_t)(t0 + lane) * kCacheTile;
+        tab = tok < in.seen && in.r < p.a.n_req ? p.a.table[(int64_t)in.r * p.a.max_pages + tok / p.c.page] : -1;
+      }
+      const int pg0 = __shfl_sync(0xffffffffu, tab, t0 - tab_at);
+      const int pg1 = __shfl_sync(0xffffffffu, tab, t0 + 1 - tab_at);
+      const bool ok0 = (unsigned)pg0 < (unsigned)p.c.n_pages, ok1 = (unsigned)pg1 < (unsigned)p.c.n_pages;
+      if (lane == 0) {
+        const uint32_t bar = smem_u32(&bars_[warp * 8 + stage_in]);
+        const uint32_t dst = ring + stage_in * stage_bytes;
+        mbar_expect_tx(bar, (uint32_t)(ok0 + ok1) * tile_bytes);
+        const int per = p.c.page / kCacheTile;
+        const int w0 = t0 % per;
+        if (ok0 && ok1 && pg0 == pg1 && w0 + 1 < per) {
+          bulk_load(dst, p.a.cache + p.c.tile_at(pg0, in.h, w0), 2 * tile_bytes, bar);
+        } else {
+          if (ok0) bulk_load(dst, p.a.cache + p.c.tile_at(pg0, in.h, w0), tile_bytes, bar);
+          if (ok1)
+            bulk_load(dst + tile_bytes, p.a.cache + p.c.tile_at(pg1, in.h, w0 + 1 < per ? w0 + 1 : 0),
+                      tile_bytes, bar);
+        }
+      }
+      valid = (valid & ~(3u << (2 * stage_in))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * stage_in);
+      if (++stage_in == p.stages) stage_in = 0;
+      --to_issue;
+      if (++in.u == in.units && to_issue > 0) {
+        in.next(p, RB);
+        tab_at = -1000000;
+      }
+    };
+    __syncwarp();
+    for (int s = 0; s < p.stages && to_issue > 0; ++s) issue();
+
+    while (steps > 0 && ok) {
+      const int here = min(steps, it.units - it.u);
+      const bool starts = it.u == 0, ends = it.u + here == it.units;
+      const int rows = block_rows(p, it.q.nq, it.rb, RB);
+      // query fragments: column g of every 8, channels 8 KW t4 ..
+      uint32_t qf[NT][NS][KW][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int rho = n * 8 + g;
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int w = 0; w < KW; ++w)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qf[n][s][w][i] = 0;
+        if (rho < rows) {
+          const int64_t x = (int64_t)it.rb * RB + rho;
+          const int64_t tok = x / p.n_rep;
+          const int64_t at = (it.q.begin + tok) * p.a.qs.token +
+                             (it.h * p.n_rep + (int)(x - tok * p.n_rep)) * p.a.qs.head + 8 * KW * t4;
+#pragma unroll
+          for (int w = 0; w < KW; ++w) {
+            if constexpr (NS == 1) {
+              const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) + at + 8 * w);
+              qf[n][0][w][0] = v.x, qf[n][0][w][1] = v.y, qf[n][0][w][2] = v.z, qf[n][0][w][3] = v.w;
+            } else {
+              const float* src = static_cast<const float*>(p.a.q) + at + 8 * w;
+              const float4 x0 = reinterpret_cast<const float4*>(src)[0], x1 = reinterpret_cast<const float4*>(src)[1];
+              const float f[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t u[NS];
+                split_pair<NS>(f[2 * i], f[2 * i + 1], u);
+#pragma unroll
+                for (int s = 0; s < NS; ++s) qf[n][s][w][i] = u[s];
+              }
+            }
+          }
+        }
+      }
+      // columns 2 t4, 2 t4 + 1 of every 8: how many keys the row sees
+      int lim[NT][2], least = it.seen;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int64_t tok = ((int64_t)it.rb * RB + n * 8 + 2 * t4 + e) / p.n_rep;
+          const int64_t s = p.c.causal ? (int64_t)it.q.len - it.q.nq + tok + 1 : it.q.len;
+          lim[n][e] = (int)max((int64_t)0, min(s, (int64_t)it.q.len));
+        }
+      if (p.c.causal) {
+        const int64_t tok = (int64_t)it.rb * RB / p.n_rep;
+        least = (int)max((int64_t)0, min((int64_t)it.q.len - it.q.nq + tok + 1, (int64_t)it.q.len));
+      }
+      float m[NT][2], mu[NT][2], l[NT][2], o[NT][MT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        mu[n][0] = mu[n][1] = 0.f;
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+      }
+
+      for (int k = 0; k < here; ++k, ++it.u) {
+        ok = mbar_wait(smem_u32(&bars_[warp * 8 + stage]), (parity >> stage) & 1u, abort, p.a.status, kTimeoutNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        parity ^= 1u << stage;
+        const uint32_t have = (valid >> (2 * stage)) & 3u;
+        const uint8_t* base = reinterpret_cast<const uint8_t*>(slot_smem) + stage * stage_bytes;
+        const int tok0 = it.u * kUnit;
+        // every row sees every token of the unit
+        const bool whole = have == 3u && tok0 + kUnit <= least;
+
+        // ---- S^T = K Q^T -------------------------------------------------------
+        float sc[2][NT][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* kt = base + i * tile_bytes;
+          uint32_t w0[KW], w1[KW];
+          if constexpr (KW == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(kt + g * (D / 2) + 16 * t4);
+            const uint4 y = *reinterpret_cast<const uint4*>(kt + (g + 8) * (D / 2) + 16 * t4);
+            w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
+            w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(kt + g * (D / 2) + 8 * t4);
+            const uint2 y = *reinterpret_cast<const uint2*>(kt + (g + 8) * (D / 2) + 8 * t4);
+            w0[0] = x.x, w0[1] = x.y;
+            w1[0] = y.x, w1[1] = y.y;
+          }
+          const uint32_t* par = reinterpret_cast<const uint32_t*>(kt + kCacheTile * (D / 2));
+          const int grp = 8 * KW * t4 / p.c.G;
+          const uint32_t az0 = par[g * par_words + grp], az1 = par[(g + 8) * par_words + grp];
+          const uint32_t a0 = az_a2(az0), z0 = az_z2(az0), a1 = az_a2(az1), z1 = az_z2(az1);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) sc[i][n][0] = sc[i][n][1] = sc[i][n][2] = sc[i][n][3] = 0.f;
+#pragma unroll
+          for (int w = 0; w < KW; ++w) {
+            uint32_t x[4], y[4];
+            codes_to_bf16<true>(w0[w], x);
+            codes_to_bf16<true>(w1[w], y);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              x[q] = bf16x2_fma(x[q], a0, z0);
+              y[q] = bf16x2_fma(y[q], a1, z1);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int s = NS - 1; s >= 0; --s) {
+                mma16816(sc[i][n], x[0], y[0], x[1], y[1], qf[n][s][w][0], qf[n][s][w][1]);
+                mma16816(sc[i][n], x[2], y[2], x[3], y[3], qf[n][s][w][2], qf[n][s][w][3]);
+              }
+          }
+        }
+
+        // ---- softmax -----------------------------------------------------------
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int tok = tok0 + i * kCacheTile + g + (j >> 1) * 8;
+                if (!((have >> i) & 1u) || tok >= lim[n][j & 1]) sc[i][n][j] = -INFINITY;
+              }
+        }
+        uint32_t pf[2][NT][NS][2];
+        {
+          float mx[NT][2];
+          bool over = false;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              mx[n][e] = max_nan(max_nan(sc[0][n][e], sc[0][n][e + 2]), max_nan(sc[1][n][e], sc[1][n][e + 2]));
+              mx[n][e] *= p.sl2;
+              over |= !(mx[n][e] <= m[n][e] + 8.f);
+            }
+          if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float x = mx[n][e];
+#pragma unroll
+                for (int q = 4; q < 32; q <<= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, q));
+                // rows whose maximum did not move that far keep it
+                const float mn = !(x <= m[n][e] + 8.f) ? max_nan(m[n][e], x) : m[n][e];
+                const float f = mn == m[n][e] ? 1.f : ex2(m[n][e] - mn);
+                m[n][e] = mn;
+                mu[n][e] = mn == -INFINITY ? 0.f : mn;
+                l[n][e] *= f;
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                  o[n][t][e] *= f;
+                  o[n][t][e + 2] *= f;
+                }
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float pr[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) pr[j] = ex2(fmaf(sc[i][n][j], p.sl2, -mu[n][j & 1]));
+              l[n][0] += pr[0] + pr[2];
+              l[n][1] += pr[1] + pr[3];
+              uint32_t u[NS], v[NS];
+              split_pair<NS>(pr[0], pr[1], u);
+              split_pair<NS>(pr[2], pr[3], v);
+#pragma unroll
+              for (int s = 0; s < NS; ++s) {
+                pf[i][n][s][0] = transpose8x8(u[s]);
+                pf[i][n][s][1] = transpose8x8(v[s]);
+              }
+            }
+        }
+
+        // ---- O^T += V^T P^T ----------------------------------------------------
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* vt = base + i * tile_bytes + half;
+          const uint32_t* par = reinterpret_cast<const uint32_t*>(vt + kCacheTile * (D / 2));
+          const int grp = 8 * VW * g / p.c.G;
+          // tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 are in rows t4, t4 + 4, t4 + 8, t4 + 12
+          uint32_t w[4][VW], az[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = t4 + 4 * e;
+            if constexpr (VW == 2) {
+              const uint2 x = *reinterpret_cast<const uint2*>(vt + row * (D / 2) + 8 * g);
+              w[e][0] = x.x, w[e][1] = x.y;
+            } else {
+              w[e][0] = *reinterpret_cast<const uint32_t*>(vt + row * (D / 2) + 4 * g);
+            }
+            az[e] = par[row * par_words + grp];
+          }
+          if (!whole) {
+            // rows nothing was appended to, or that were not loaded, hold anything: as zeros
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tok = tok0 + i * kCacheTile + 2 * t4 + (e & 1) + (e >> 1) * 8;
+              if (!((have >> i) & 1u) || tok >= it.q.len) az[e] = 0u;
+            }
+          }
+          const uint32_t a0 = __byte_perm(az[0], az[1], 0x5410), z0 = __byte_perm(az[0], az[1], 0x7632);
+          const uint32_t a1 = __byte_perm(az[2], az[3], 0x5410), z1 = __byte_perm(az[2], az[3], 0x7632);
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            uint32_t x0[4], x1[4], y0[4], y1[4];  // even and odd channels of tokens t.., of t + 8..
+            codes_to_bf16<false>(__byte_perm(w[0][j], w[1][j], 0x5410), x0);
+            codes_to_bf16<false>(__byte_perm(w[0][j], w[1][j], 0x7632), x1);
+            codes_to_bf16<false>(__byte_perm(w[2][j], w[3][j], 0x5410), y0);
+            codes_to_bf16<false>(__byte_perm(w[2][j], w[3][j], 0x7632), y1);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t f0 = bf16x2_fma(x0[q], a0, z0), f1 = bf16x2_fma(x1[q], a0, z0);
+              const uint32_t f2 = bf16x2_fma(y0[q], a1, z1), f3 = bf16x2_fma(y1[q], a1, z1);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int s = NS - 1; s >= 0; --s)
+                  mma16816(o[n][j * 4 + q], f0, f1, f2, f3, pf[i][n][s][0], pf[i][n][s][1]);
+            }
+          }
+        }
+        // the stage has been read
+        __syncwarp();
+        if (++stage == p.stages) stage = 0;
+        if (to_issue > 0) issue();
+      }
+      if (!ok) break;
+
+      // ---- the piece is done ---------------------------------------------------
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int q = 4; q < 32; q <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], q);
+      steps -= here;
+      const bool whole_item = starts && ends;
+      float* const to = steps == 0 ? slot_smem : slot_ws;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int rho = n * 8 + 2 * t4 + e;
+          if (rho < rows) {
+            const float f = whole_item ? inverse(l[n][e]) : 1.f;
+            const int64_t row = whole_item ? out_row(p, it.q.begin, it.h, it.rb, RB, rho) : rho;
+            const int ch0 = 8 * VW * g;
+#pragma unroll
+            for (int t = 0; t < MT; t += 2) {
+              const float4 v = make_float4(o[n][t][e] * f, o[n][t][e + 2] * f, o[n][t + 1][e] * f,
+                                           o[n][t + 1][e + 2] * f);
+              if (whole_item) store4(p, row, D, ch0 + 2 * t, v);
+              else *reinterpret_cast<float4*>(to + rho * D + ch0 + 2 * t) = v;
+            }
+            if (g == 0) {
+              if (!whole_item) S::ml(to)[rho] = make_float2(m[n][e], l[n][e]);
+              else if (p.a.lse) p.a.lse[row] = lse_of(m[n][e], l[n][e]);
+            }
+          }
+        }
+      if (lane == 0 && !whole_item) {
+        if (!starts) {
+          meta[warp].head = ends ? 1 : 2;
+          meta[warp].head_global = steps != 0;
+          meta[warp].head_rows = rows;
+        } else {
+          meta[warp].tail = 1;
+        }
+        // of the last open piece: the tail if there is one
+        meta[warp].rows = rows;
+        meta[warp].begin = it.q.begin;
+        meta[warp].nq = it.q.nq;
+        meta[warp].h = it.h;
+        meta[warp].rb = it.rb;
+      }
+      if (steps > 0) it.next(p, RB);
+    }
+    if (!ok && lane == 0) {
+      // never leave with a copy still writing into this CTA's shared memory
+      int never = 0;
+      for (int s = 0; s < p.stages; ++s)
+        mbar_wait(smem_u32(&bars_[warp * 8 + s]), (parity >> s) & 1u, &never, nullptr, kDrainTimeoutNs);
+    }
+  }
+  __syncthreads();
+  if (*abort) {
+    if (threadIdx.x == 0) out_meta[blockIdx.x].head = out_meta[blockIdx.x].tail = 0;
+    return;
+  }
+
+  // ---- the CTA's pieces -------------------------------------------------------
+  // Pieces in order; a tail begins a group, a head that ends the item closes one.
+  auto slot_of = [&](int id) -> const float* {  // id: 2 warp + (0 head, 1 tail)
+    const int w = id >> 1;
+    if ((id & 1) == 0 && meta[w].head_global) return ws + ((int64_t)blockIdx.x * WARPS + w) * S::kFloats;
+    return reinterpret_cast<const float*>(smem + (size_t)w * p.stages * stage_bytes);
+  };
+  float* const cta_slots = ws + W::cta_slots(gridDim.x) + 2 * (size_t)blockIdx.x * S::kFloats;
+  // joins the pieces `ids`, each thread 4 channels of a row at a time
+  auto join = [&](uint32_t ids, int rows, bool out, int owner, float* to) {
+    for (int e = threadIdx.x; e < rows * (D / 4); e += WARPS * 32) {
+      const int row = e / (D / 4), ch = (e - row * (D / 4)) * 4;
+      Acc acc;
+      for (uint32_t b = ids; b; b &= b - 1) {
+        const float* s = slot_of(__ffs(b) - 1);
+        acc.add(S::ml(s)[row], *reinterpret_cast<const float4*>(s + row * D + ch));
+      }
+      if (out) {
+        const PieceMeta& m = meta[owner];
+        write_out<D>(p, out_row(p, m.begin, m.h, m.rb, RB, row), ch, acc.m, acc.l, acc.o);
+      } else {
+        *reinterpret_cast<float4*>(to + row * D + ch) = acc.o;
+        if (ch == 0) S::ml(to)[row] = make_float2(acc.m, acc.l);
+      }
+    }
+  };
+  CtaMeta cm = {0, 0, 0, 0, 0, 0};
+  uint32_t group = 0;       // ids of the group's pieces, as bits
+  bool begun = false;       // the group's item began in this CTA
+  int rows = 0, owner = 0;  // owner: the warp that knows the begun item
+  for (int id = 0; id < 2 * WARPS; ++id) {
+    const int w = id >> 1;
+    const bool is_tail = id & 1;
+    const int state = is_tail ? meta[w].tail : meta[w].head;
+    if (state == 0) continue;
+    if (is_tail) begun = true, owner = w, group = 0;
+    rows = is_tail ? meta[w].rows : meta[w].head_rows;
+    group |= 1u << id;
+    if (is_tail || state == 2) continue;
+    join(group, rows, begun, owner, cta_slots);  // the item ends here
+    if (!begun) cm.head = 1;
+    group = 0;
+    begun = false;
+  }
+  if (group) {
+    join(group, rows, false, owner, cta_slots + (begun ? S::kFloats : 0));
+    if (begun) {
+      cm.tail = 1;
+      cm.begin = meta[owner].begin;
+      cm.nq = meta[owner].nq;
+      cm.h = meta[owner].h;
+      cm.rb = meta[owner].rb;
+    } else {
+      cm.head = 2;
+    }
+  }
+  if (threadIdx.x == 0) out_meta[blockIdx.x] = cm;
+}
+
+// Items that cross CTAs: CTA c of this grid joins the one that CTA c of the first began,
+// c's tail and the heads of the CTAs behind it up to the one that ends the item.  Few
+// rows leave threads over: those share the pieces and meet in shared memory.
+constexpr int kJoinThreads = 256;
+template <int D, int RB, int WARPS>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
+  using S = Slot<D, RB>;
+  using W = Work<D, RB, WARPS>;
+  __shared__ Acc meet[kJoinThreads];
+  griddep_wait();
+  const float* const ws = static_cast<const float*>(p.a.ws);
+  const CtaMeta* meta = reinterpret_cast<const CtaMeta*>(ws + W::meta(gridDim.x));
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const CtaMeta cm = meta[c];
+  if (!cm.tail) return;
+  int n = 1;
+  for (int i = c + 1; i < (int)gridDim.x; i += 32) {
+    const bool end = i + lane < (int)gridDim.x && meta[i + lane].head != 2;
+    const uint32_t b = __ballot_sync(0xffffffffu, end);
+    n = i - c + (b ? __ffs(b) : 32);
+    if (b) break;
+  }
+  n = min(n, (int)gridDim.x - c);
+  const float* const slots = ws + W::cta_slots(gridDim.x) + 2 * (size_t)c * S::kFloats;
+  const int rows = block_rows(p, cm.nq, cm.rb, RB), parts = rows * (D / 4);
+  const int shares = max(1, kJoinThreads / parts), share = threadIdx.x / parts;
+  for (int e = shares > 1 ? threadIdx.x % parts : threadIdx.x; e < parts; e += shares > 1 ? parts : kJoinThreads) {
+    const int row = e / (D / 4), ch = (e - row * (D / 4)) * 4;
+    Acc acc;
+    if (shares == 1 || share < shares) {
+#pragma unroll 4
+      for (int i = shares > 1 ? share : 0; i < n; i += shares) {
+        const float* s = slots + (i ? 2 * (size_t)i : 1) * S::kFloats;
+        acc.add(S::ml(s)[row], *reinterpret_cast<const float4*>(s + row * D + ch));
+      }
+    }
+    if (shares > 1) {
+      meet[threadIdx.x] = acc;
+    } else {
+      write_out<D>(p, out_row(p, cm.begin, cm.h, cm.rb, RB, row), ch, acc.m, acc.l, acc.o);
+    }
+  }
+  if (shares == 1) return;
+  __syncthreads();
+  if ((int)threadIdx.x >= parts) return;
+  Acc acc = meet[threadIdx.x];
+  for (int i = 1; i < shares; ++i) {
+    const Acc& x = meet[threadIdx.x + i * parts];
+    acc.add(make_float2(x.m, x.l), x.o);
+  }
+  const int row = threadIdx.x / (D / 4), ch = (threadIdx.x - row * (D / 4)) * 4;
+  write_out<D>(p, out_row(p, cm.begin, cm.h, cm.rb, RB, row), ch, acc.m, acc.l, acc.o);
+}
+
+// ---------------------------------------------------------------------------
+// variants
+// ---------------------------------------------------------------------------
+// NT 8-row blocks at a time, NS bf16 parts of q and P, CTAs of WARPS warps, MINB of them
+// on an SM: what the accumulators leave of the 64 K registers.
+template <int D, int NT, int NS, int WARPS, int MINB>
+struct Variant {
+  static constexpr int kCtas = kMaxSms * MINB;
+  static constexpr int kStatic = 4096;  // static shared memory and what the system keeps
+  using W = Work<D, 8 * NT, WARPS>;
+  static size_t workspace() { return W::meta(kCtas) * sizeof(float) + kCtas * sizeof(CtaMeta); }
+  static cudaError_t launch(Params p, int sms, cudaStream_t st) {
+    auto kern = attn_kernel<D, NT, NS, WARPS, MINB>;
+    const int stage = WARPS * 2 * p.c.tile_bytes();
+    const int room = 228 * 1024 / MINB - kStatic;
+    p.stages = room / stage < 8 ? room / stage : 8;
+    // the ring of a warp also takes the sums of its last piece
+    if (p.stages < 1 || (size_t)p.stages * stage < W::kSlot * WARPS * sizeof(float))
+      return cudaErrorInvalidConfiguration;
+    static std::atomic<uint64_t> set[2];  // devices whose limit is raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev >= 128 || !(set[dev >> 6].load() & bit)) {
+      if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, room)) != cudaSuccess)
+        return e;
+      if (dev < 128) set[dev >> 6].fetch_or(bit);
+    }
+    const int grid = sms * MINB < kCtas ? sms * MINB : kCtas;
+    kern<<<grid, WARPS * 32, p.stages * stage, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = kJoinThreads;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, 8 * NT, WARPS>, p);
+  }
+};
+template <int D>
+using Rows8 = Variant<D, 1, 1, 8, 2>;
+template <int D>
+using Rows16 = Variant<D, 2, 1, 4, 3>;
+template <int D>
+using Exact8 = Variant<D, 1, 3, 4, 3>;
 
 }  // namespace cattn
 
-size_t cache_attn_workspace(const Cache&) { return 256; }
+template <int D>
+static size_t attn_workspace(const Cache& c) {
+  using namespace cattn;
+  size_t n = c.bf16 ? std::max(Rows8<D>::workspace(), Rows16<D>::workspace()) : Exact8<D>::workspace();
+  return (n + 255) / 256 * 256;
+}
+size_t cache_attn_workspace(const Cache& c) { return c.D == 128 ? attn_workspace<128>(c) : attn_workspace<64>(c); }
 
 template <int D>
-static void launch_simple(const Cache& c, const CacheAttnArgs& a, cudaStream_t st) {
-  const int64_t rows = (int64_t)a.n_tokens * c.Hq;
-  const unsigned grid = (unsigned)((rows + 3) / 4);
-  if (!c.bf16)
-    cattn::simple_kernel<D, float, true><<<grid, cattn::kThreads, 0, st>>>(c, a);
-  else if (c.o_f32)
-    cattn::simple_kernel<D, __nv_bfloat16, true><<<grid, cattn::kThreads, 0, st>>>(c, a);
-  else
-    cattn::simple_kernel<D, __nv_bfloat16, false><<<grid, cattn::kThreads, 0, st>>>(c, a);
+static cudaError_t launch_attn(const cattn::Params& p, int sms, cudaStream_t st) {
+  using namespace cattn;
+  if (!p.c.bf16) return Exact8<D>::launch(p, sms, st);
+  // 8 rows at a time while that is all a request has
+  if ((int64_t)p.a.max_q * p.n_rep <= 8) return Rows8<D>::launch(p, sms, st);
+  return Rows16<D>::launch(p, sms, st);
 }
 
 cudaError_t launch_cache_attn(const Cache& c, const CacheAttnArgs& a, cudaStream_t st) {
+  cattn::Params p;
+  p.c = c;
+  p.a = a;
+  p.n_rep = c.Hq / c.Hkv;
+  p.stages = 0;
+  p.per_sum = (a.n_req + cattn::kSums - 1) / cattn::kSums;
+  p.sl2 = c.scale * 1.44269504088896340736f;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
   timing_begin("cache_attn", st);
-  if (c.D == 128) launch_simple<128>(c, a, st);
-  else launch_simple<64>(c, a, st);
+  e = c.D == 128 ? launch_attn<128>(p, sms, st) : launch_attn<64>(p, sms, st);
   timing_end(st);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace cpattn
