@@ -53,21 +53,24 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-__device__ __forceinline__ uint32_t code_to_bf16(uint32_t x) {  // codes at bits 3..6, 19..22
-  return (x & 0x00780078u) | 0x3F803F80u;
+// `ones` is kOnes in a register the compiler cannot see through: with two immediates
+// the and-or would become two instructions.
+constexpr uint32_t kOnes = 0x3F803F80u;
+__device__ __forceinline__ uint32_t code_to_bf16(uint32_t x, uint32_t ones) {  // codes at bits 3..6, 19..22
+  return (x & 0x00780078u) | ones;
 }
 template <bool K>
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t (&u)[4]) {
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t ones, uint32_t (&u)[4]) {
   if constexpr (K) {
-    u[0] = code_to_bf16(w);
-    u[1] = code_to_bf16(w >> 4);
-    u[2] = code_to_bf16(w >> 8);
-    u[3] = code_to_bf16(__funnelshift_r(w, w, 12));
+    u[0] = code_to_bf16(w, ones);
+    u[1] = code_to_bf16(w >> 4, ones);
+    u[2] = code_to_bf16(w >> 8, ones);
+    u[3] = code_to_bf16(__funnelshift_r(w, w, 12), ones);
   } else {
-    u[0] = code_to_bf16(w << 3);
-    u[1] = code_to_bf16(w >> 1);
-    u[2] = code_to_bf16(w >> 5);
-    u[3] = code_to_bf16(w >> 9);
+    u[0] = code_to_bf16(w << 3, ones);
+    u[1] = code_to_bf16(w >> 1, ones);
+    u[2] = code_to_bf16(w >> 5, ones);
+    u[3] = code_to_bf16(w >> 9, ones);
   }
 }
 // (a, a) and (z, z) of an (a, z) word
@@ -83,6 +86,12 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 

@@ -45,6 +45,7 @@ namespace cpattn {
 namespace cattn {
 
 constexpr int kUnit = 32;            // cached tokens of a unit: two tiles
+constexpr int kItemCost = 3;         // an item's start and end, in units (see below)
 constexpr int kSums = 256;           // entries of the prefix sums over requests
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
@@ -57,6 +58,7 @@ struct Params {
   int n_rep, stages;
   int per_sum;                       // requests per entry of the prefix sums
   float sl2;                         // scale * log2(e)
+  uint32_t ones;                     // kOnes
 };
 
 // ---------------------------------------------------------------------------
@@ -74,32 +76,77 @@ __device__ __forceinline__ Req request(const Params& p, int r) {
   q.len = min(max(p.a.kv_len[r], 0), p.a.max_pages * p.c.page);
   return q;
 }
-// cached tokens that row block rb (RB rows) sees, and its units
+// Rows of q are fewer than 2^31 (checked on the host), and so are a request's.
+// cached tokens that row x of the request sees
+__device__ __forceinline__ int seen_by(const Params& p, const Req& q, int x) {
+  if (!p.c.causal) return q.len;
+  return min(max(q.len - q.nq + (int)((unsigned)x / (unsigned)p.n_rep) + 1, 0), q.len);
+}
+// ... that row block rb (RB rows) sees, and its units
 __device__ __forceinline__ int block_seen(const Params& p, const Req& q, int rb, int RB) {
   if (!p.c.causal) return q.len;
-  const int64_t last = min((int64_t)q.nq * p.n_rep, (int64_t)(rb + 1) * RB) - 1;
-  const int64_t s = (int64_t)q.len - q.nq + last / p.n_rep + 1;
-  return (int)max((int64_t)0, min(s, (int64_t)q.len));
+  const int last = (int)min((int64_t)q.nq * p.n_rep, (int64_t)(rb + 1) * RB) - 1;
+  return seen_by(p, q, last);
 }
 __device__ __forceinline__ int units_of(int seen) { return max(1, (seen + kUnit - 1) / kUnit); }
-__device__ __forceinline__ int64_t blocks_of(const Params& p, const Req& q, int RB) {
-  return ((int64_t)q.nq * p.n_rep + RB - 1) / RB;
+__device__ __forceinline__ int blocks_of(const Params& p, const Req& q, int RB) {
+  return (int)(((unsigned)(q.nq * p.n_rep) + RB - 1) / RB);
 }
-// units of one K/V head of request r
-__device__ __forceinline__ int64_t head_units(const Params& p, const Req& q, int RB) {
-  const int nb = (int)blocks_of(p, q, RB);
+// cost of one K/V head of request r: its units and kItemCost for every item
+__device__ __forceinline__ int64_t head_cost(const Params& p, const Req& q, int RB) {
+  const int nb = blocks_of(p, q, RB);
   int64_t n = 0;
-  for (int b = 0; b < nb; ++b) n += units_of(block_seen(p, q, b, RB));
+  for (int b = 0; b < nb; ++b) n += units_of(block_seen(p, q, b, RB)) + kItemCost;
   return n;
 }
 
-// One item and a unit in it.  Items follow each other by row block, K/V head, request.
-struct Item {
+// Request, K/V head and row block of an item, and a unit in it.  Items follow each other by
+// row block, K/V head, request.
+struct Place {
+  int r, h, rb, u;
+};
+struct Item : Place {
   Req q;
-  int r, h, rb, seen, units, u;
+  int seen, units;
   __device__ __forceinline__ void settle(const Params& p, int RB) {
     seen = block_seen(p, q, rb, RB);
     units = units_of(seen);
+  }
+  __device__ __forceinline__ bool same(const Place& o) const { return r == o.r && h == o.h && rb == o.rb; }
+  // units of this item before `end`, from u on
+  __device__ __forceinline__ int left(const Place& end) const { return (same(end) ? end.u : units) - u; }
+  // The place at `x` in the numbering of cost that starts with request r0: an item's first
+  // kItemCost numbers are its first unit's.  (The bounds of the searches matter only if
+  // lengths change under the kernel.)
+  __device__ __forceinline__ void locate(const Params& p, int RB, int r0, int64_t x) {
+    h = rb = u = 0;
+    for (r = r0; r < p.a.n_req; ++r) {
+      q = request(p, r);
+      if (q.nq == 0) continue;
+      const int64_t c = head_cost(p, q, RB);
+      if (x < c * p.c.Hkv) {
+        h = (int)(x / c);
+        x -= h * c;
+        break;
+      }
+      x -= c * p.c.Hkv;
+    }
+    if (r >= p.a.n_req) return;  // behind the last item
+    const int nb = blocks_of(p, q, RB);
+    for (rb = 0;; ++rb) {
+      settle(p, RB);
+      if (rb == nb - 1 || x < units + kItemCost) break;
+      x -= units + kItemCost;
+    }
+    u = max(0, min((int)x - kItemCost, units - 1));
+  }
+  __device__ __forceinline__ Item from_lane(int src) const {
+    Item o;
+    const int* a = reinterpret_cast<const int*>(this);
+    int* b = reinterpret_cast<int*>(&o);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Item) / sizeof(int)); ++i) b[i] = __shfl_sync(0xffffffffu, a[i], src);
+    return o;
   }
   __device__ __forceinline__ void next(const Params& p, int RB) {
     u = 0;
@@ -148,9 +195,8 @@ struct CtaMeta {
 
 // Row rho of a block -> its row of q and o
 __device__ __forceinline__ int64_t out_row(const Params& p, int begin, int h, int rb, int RB, int rho) {
-  const int64_t x = (int64_t)rb * RB + rho;
-  const int64_t tok = x / p.n_rep;
-  return (begin + tok) * p.c.Hq + h * p.n_rep + (int)(x - tok * p.n_rep);
+  const unsigned x = (unsigned)rb * RB + rho, tok = x / (unsigned)p.n_rep;
+  return (int64_t)(begin + (int)tok) * p.c.Hq + h * p.n_rep + (int)(x - tok * p.n_rep);
 }
 __device__ __forceinline__ int block_rows(const Params& p, int nq, int rb, int RB) {
   return (int)min((int64_t)RB, (int64_t)nq * p.n_rep - (int64_t)rb * RB);
@@ -222,7 +268,7 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&u)[NS]) 
   }
 }
 
-template <int D, int NT, int NS, int WARPS, int MINB>
+template <int D, int G, int NT, int NS, int WARPS, int MINB>
 __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) {
   constexpr int RB = 8 * NT;
   constexpr int KW = D / 32;    // words of a K row per lane (channels 8 KW t4 ..)
@@ -245,8 +291,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
-  const int tile_bytes = p.c.tile_bytes(), half = p.c.half_tile(), par_words = p.c.groups();
-  const int stage_bytes = 2 * tile_bytes;
+  constexpr int par_words = D / G;
+  constexpr int half = kCacheTile * (D / 2 + 4 * par_words);
+  constexpr int tile_bytes = 2 * half, stage_bytes = 2 * tile_bytes;
   volatile int* abort = &abort_;
   if (threadIdx.x == 0) abort_ = 0;
   if (lane == 0) {
@@ -260,7 +307,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
   {
     int64_t run = 0;
     constexpr int PT = kSums / (WARPS * 32) > 0 ? kSums / (WARPS * 32) : 1;
-    // thread t's entries are PT neighbours, so one scan over threads gives all sums
+    // thread t's entries are PT neighbours, so one scan over threads gives all sums (threads
+    // past the last entry have no requests)
     int64_t mine[PT];
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
@@ -269,7 +317,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
       const int64_t r0 = (int64_t)e * p.per_sum;
       for (int64_t r = r0; r < r0 + p.per_sum && r < p.a.n_req; ++r) {
         const Req q = request(p, (int)r);
-        if (q.nq > 0) n += head_units(p, q, RB) * p.c.Hkv;
+        if (q.nq > 0) n += head_cost(p, q, RB) * p.c.Hkv;
       }
       run += n;
       mine[i] = run;
@@ -290,12 +338,15 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
       total += warp_part[w];
     }
 #pragma unroll
-    for (int i = 0; i < PT; ++i) sums[threadIdx.x * PT + i] = before + inc - run + mine[i];
+    for (int i = 0; i < PT; ++i)
+      if (threadIdx.x * PT + i < kSums) sums[threadIdx.x * PT + i] = before + inc - run + mine[i];
     __syncthreads();
   }
 
   // ---- this warp's run of units ----------------------------------------------
-  // CTAs that would get none are not counted, so that an item's CTAs are neighbours
+  // An item costs its units and some for its start and end (the request's numbers and its
+  // query rows come from memory, its result goes there); every warp gets an equal run of
+  // that.  CTAs that would get nothing are not counted, so an item's CTAs are neighbours.
   using W = Work<D, RB, WARPS>;
   float* const ws = static_cast<float*>(p.a.ws);
   CtaMeta* const out_meta = reinterpret_cast<CtaMeta*>(ws + W::meta(gridDim.x));
@@ -305,96 +356,104 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
     return;
   }
   const int64_t c0 = total * blockIdx.x / ctas, c1 = total * (blockIdx.x + 1) / ctas;
-  const int64_t v0 = c0 + (c1 - c0) * warp / WARPS, v1 = c0 + (c1 - c0) * (warp + 1) / WARPS;
-  int steps = (int)(v1 - v0);
   float* const slot_smem = reinterpret_cast<float*>(smem + (size_t)warp * p.stages * stage_bytes);
   float* const slot_ws = ws + ((size_t)blockIdx.x * WARPS + warp) * S::kFloats;
   if (lane == 0) {
     meta[warp].head = 0;
     meta[warp].tail = 0;
   }
-  Item in;       // of the copies
-  bool ok = true;
-  int64_t x = 0;
-  if (steps > 0) {
-    int lo = 0, hi = kSums - 1;  // first entry whose inclusive sum is past v0
+  // the run's first unit, and the next warp's: one half of the lanes looks for each
+  Item in;  // of the copies
+  Place end;
+  {
+    const int64_t v = c0 + (c1 - c0) * (warp + (lane >> 4)) / WARPS;
+    int lo = 0, hi = kSums;  // first entry whose inclusive sum is past v
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (sums[mid] > v0) hi = mid;
+      if (sums[mid] > v) hi = mid;
       else lo = mid + 1;
     }
-    x = v0 - (lo ? sums[lo - 1] : 0);
-    // (the bounds of these searches matter only if lengths change under the kernel)
-    for (in.r = lo * p.per_sum; in.r < p.a.n_req; ++in.r) {
-      in.q = request(p, in.r);
-      if (in.q.nq == 0) continue;
-      const int64_t hu = head_units(p, in.q, RB);
-      if (x < hu * p.c.Hkv) {
-        in.h = (int)(x / hu);
-        x -= in.h * hu;
-        break;
-      }
-      x -= hu * p.c.Hkv;
-    }
-    if (in.r >= p.a.n_req) steps = 0;
+    Item x;
+    x.seen = x.units = 0;
+    x.q = {0, 0, 0};
+    x.locate(p, RB, lo * p.per_sum, lo < kSums ? v - (lo ? sums[lo - 1] : 0) : 0);
+    in = x.from_lane(0);
+    end.r = __shfl_sync(0xffffffffu, x.r, 16);
+    end.h = __shfl_sync(0xffffffffu, x.h, 16);
+    end.rb = __shfl_sync(0xffffffffu, x.rb, 16);
+    end.u = __shfl_sync(0xffffffffu, x.u, 16);
   }
-  if (steps > 0) {
-    const int64_t nb = blocks_of(p, in.q, RB);
-    for (in.rb = 0; in.rb < nb; ++in.rb) {
-      in.settle(p, RB);
-      if (x < in.units) break;
-      x -= in.units;
-    }
-    if (in.rb >= nb) steps = 0;
-  }
-  if (steps > 0) {
-    in.u = (int)x;
-
+  bool ok = true;
+  if (in.r < p.a.n_req && !(in.same(end) && in.u == end.u)) {
     Item it = in;  // of the arithmetic
-    int to_issue = steps;
-    const uint32_t ring = smem_u32(slot_smem);
+    bool to_issue = true;
+    const uint32_t ring = smem_u32(slot_smem), bar0 = smem_u32(&bars_[warp * 8]);
     int stage_in = 0, stage = 0;
     uint32_t parity = 0, valid = 0;  // two bits a stage: which tiles were loaded
-    int tab = -1, tab_at = -1000000; // pages of tiles tab_at + lane of in's request
+    // Pages of the coming tiles: lane i knows that of tile tab_at + i, or where a unit is
+    // inside one page (a page is 32 tokens or a multiple), of unit tab_at + i.
+    const bool one_page = p.c.page % kUnit == 0;
+    const int per = p.c.page / kCacheTile;   // tiles of a page
+    const int per_lane = one_page ? 1 : 2;   // entries of a unit
+    int tab = 0, tab_at = 0, tab_end = 0;    // units [tab_at, tab_end) are known
+    int w0 = (in.u * 2) % per;               // the unit's first tile in its page
+    const uint8_t* from = nullptr;           // the request's K/V head in page 0
+    int64_t page_bytes = (int64_t)p.c.Hkv * p.c.block_bytes();
     // issues the copies of the next unit
     auto issue = [&]() {
-      const int t0 = in.u * 2;
-      if (t0 - tab_at >= 32 || t0 < tab_at) {
-        tab_at = t0;
-        const int64_t tok = (int64_t)(t0 + lane) * kCacheTile;
+      if (in.u >= tab_end) {
+        tab_at = in.u;
+        tab_end = in.u + 32 / per_lane;
+        const int64_t tok = ((int64_t)in.u * per_lane + lane) * (kUnit / per_lane);
         tab = tok < in.seen && in.r < p.a.n_req ? p.a.table[(int64_t)in.r * p.a.max_pages + tok / p.c.page] : -1;
+        from = p.a.cache + in.h * p.c.block_bytes();
       }
-      const int pg0 = __shfl_sync(0xffffffffu, tab, t0 - tab_at);
-      const int pg1 = __shfl_sync(0xffffffffu, tab, t0 + 1 - tab_at);
-      const bool ok0 = (unsigned)pg0 < (unsigned)p.c.n_pages, ok1 = (unsigned)pg1 < (unsigned)p.c.n_pages;
-      if (lane == 0) {
-        const uint32_t bar = smem_u32(&bars_[warp * 8 + stage_in]);
-        const uint32_t dst = ring + stage_in * stage_bytes;
-        mbar_expect_tx(bar, (uint32_t)(ok0 + ok1) * tile_bytes);
-        const int per = p.c.page / kCacheTile;
-        const int w0 = t0 % per;
-        if (ok0 && ok1 && pg0 == pg1 && w0 + 1 < per) {
-          bulk_load(dst, p.a.cache + p.c.tile_at(pg0, in.h, w0), 2 * tile_bytes, bar);
-        } else {
-          if (ok0) bulk_load(dst, p.a.cache + p.c.tile_at(pg0, in.h, w0), tile_bytes, bar);
-          if (ok1)
-            bulk_load(dst + tile_bytes, p.a.cache + p.c.tile_at(pg1, in.h, w0 + 1 < per ? w0 + 1 : 0),
-                      tile_bytes, bar);
+      const uint32_t bar = bar0 + 8 * stage_in;
+      const uint32_t dst = ring + stage_in * stage_bytes;
+      uint32_t have;
+      if (one_page) {
+        const int pg = __shfl_sync(0xffffffffu, tab, in.u - tab_at);
+        const bool page_ok = (unsigned)pg < (unsigned)p.c.n_pages;
+        const bool both = in.u * kUnit + kCacheTile < in.seen;  // else the second tile is not looked at
+        have = page_ok ? (both ? 3u : 1u) : 0u;
+        if (lane == 0) {
+          const uint32_t bytes = have == 3u ? 2 * tile_bytes : have * tile_bytes;
+          mbar_expect_tx(bar, bytes);
+          if (have) bulk_load(dst, from + pg * page_bytes + w0 * tile_bytes, bytes, bar);
         }
+        if ((w0 += 2) == per) w0 = 0;
+      } else {
+        // a lane a tile
+        const int pg = __shfl_sync(0xffffffffu, tab, (in.u - tab_at) * 2 + (lane & 1));
+        const bool page_ok = (unsigned)pg < (unsigned)p.c.n_pages;
+        have = __ballot_sync(0xffffffffu, page_ok) & 3u;
+        int w = w0 + (lane & 1);
+        if (w >= per) w -= per;
+        if (lane == 0) mbar_expect_tx(bar, __popc(have) * tile_bytes);
+        __syncwarp();
+        if (lane < 2 && page_ok)
+          bulk_load(dst + lane * tile_bytes, from + pg * page_bytes + w * tile_bytes, tile_bytes, bar);
+        w0 = w0 + 2 >= per ? w0 + 2 - per : w0 + 2;
+        if (per == 1) w0 = 0;
       }
-      valid = (valid & ~(3u << (2 * stage_in))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * stage_in);
+      valid = (valid & ~(3u << (2 * stage_in))) | have << (2 * stage_in);
       if (++stage_in == p.stages) stage_in = 0;
-      --to_issue;
-      if (++in.u == in.units && to_issue > 0) {
-        in.next(p, RB);
-        tab_at = -1000000;
+      ++in.u;
+      if (in.left(end) == 0) {
+        to_issue = !in.same(end);
+        if (to_issue) {
+          in.next(p, RB);
+          to_issue = in.r < p.a.n_req && in.left(end) > 0;
+          tab_end = 0;
+          w0 = 0;
+        }
       }
     };
     __syncwarp();
-    for (int s = 0; s < p.stages && to_issue > 0; ++s) issue();
+    for (int s = 0; s < p.stages && to_issue; ++s) issue();
 
-    while (steps > 0 && ok) {
-      const int here = min(steps, it.units - it.u);
+    for (bool more = true; more;) {
+      const int here = it.left(end);
       const bool starts = it.u == 0, ends = it.u + here == it.units;
       const int rows = block_rows(p, it.q.nq, it.rb, RB);
       // query fragments: column g of every 8, channels 8 KW t4 ..
@@ -409,9 +468,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
 #pragma unroll
             for (int i = 0; i < 4; ++i) qf[n][s][w][i] = 0;
         if (rho < rows) {
-          const int64_t x = (int64_t)it.rb * RB + rho;
-          const int64_t tok = x / p.n_rep;
-          const int64_t at = (it.q.begin + tok) * p.a.qs.token +
+          const unsigned x = (unsigned)it.rb * RB + rho, tok = x / (unsigned)p.n_rep;
+          const int64_t at = (it.q.begin + (int)tok) * p.a.qs.token +
                              (it.h * p.n_rep + (int)(x - tok * p.n_rep)) * p.a.qs.head + 8 * KW * t4;
 #pragma unroll
           for (int w = 0; w < KW; ++w) {
@@ -434,31 +492,27 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
         }
       }
       // columns 2 t4, 2 t4 + 1 of every 8: how many keys the row sees
-      int lim[NT][2], least = it.seen;
+      int lim[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int64_t tok = ((int64_t)it.rb * RB + n * 8 + 2 * t4 + e) / p.n_rep;
-          const int64_t s = p.c.causal ? (int64_t)it.q.len - it.q.nq + tok + 1 : it.q.len;
-          lim[n][e] = (int)max((int64_t)0, min(s, (int64_t)it.q.len));
-        }
-      if (p.c.causal) {
-        const int64_t tok = (int64_t)it.rb * RB / p.n_rep;
-        least = (int)max((int64_t)0, min((int64_t)it.q.len - it.q.nq + tok + 1, (int64_t)it.q.len));
-      }
-      float m[NT][2], mu[NT][2], l[NT][2], o[NT][MT][4];
+        for (int e = 0; e < 2; ++e) lim[n][e] = seen_by(p, it.q, it.rb * RB + n * 8 + 2 * t4 + e);
+      const int least = seen_by(p, it.q, it.rb * RB);
+      // m: the maximum in log2 units that P is formed against; top: the raw score above
+      // which it moves
+      const float slack = 8.f / p.sl2;
+      float m[NT][2], top[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         m[n][0] = m[n][1] = -INFINITY;
-        mu[n][0] = mu[n][1] = 0.f;
+        top[n][0] = top[n][1] = -INFINITY;
         l[n][0] = l[n][1] = 0.f;
 #pragma unroll
         for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
       }
 
       for (int k = 0; k < here; ++k, ++it.u) {
-        ok = mbar_wait(smem_u32(&bars_[warp * 8 + stage]), (parity >> stage) & 1u, abort, p.a.status, kTimeoutNs);
+        ok = mbar_wait(bar0 + 8 * stage, (parity >> stage) & 1u, abort, p.a.status, kTimeoutNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         parity ^= 1u << stage;
@@ -486,7 +540,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
             w1[0] = y.x, w1[1] = y.y;
           }
           const uint32_t* par = reinterpret_cast<const uint32_t*>(kt + kCacheTile * (D / 2));
-          const int grp = 8 * KW * t4 / p.c.G;
+          const int grp = 8 * KW * t4 / G;
           const uint32_t az0 = par[g * par_words + grp], az1 = par[(g + 8) * par_words + grp];
           const uint32_t a0 = az_a2(az0), z0 = az_z2(az0), a1 = az_a2(az1), z1 = az_z2(az1);
 #pragma unroll
@@ -494,8 +548,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
 #pragma unroll
           for (int w = 0; w < KW; ++w) {
             uint32_t x[4], y[4];
-            codes_to_bf16<true>(w0[w], x);
-            codes_to_bf16<true>(w1[w], y);
+            codes_to_bf16<true>(w0[w], p.ones, x);
+            codes_to_bf16<true>(w1[w], p.ones, y);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               x[q] = bf16x2_fma(x[q], a0, z0);
@@ -531,9 +585,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              mx[n][e] = max_nan(max_nan(sc[0][n][e], sc[0][n][e + 2]), max_nan(sc[1][n][e], sc[1][n][e + 2]));
-              mx[n][e] *= p.sl2;
-              over |= !(mx[n][e] <= m[n][e] + 8.f);
+              mx[n][e] = max3_nan(sc[0][n][e], sc[0][n][e + 2], max_nan(sc[1][n][e], sc[1][n][e + 2]));
+              over |= !(mx[n][e] <= top[n][e]);
             }
           if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -544,10 +597,11 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
 #pragma unroll
                 for (int q = 4; q < 32; q <<= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, q));
                 // rows whose maximum did not move that far keep it
-                const float mn = !(x <= m[n][e] + 8.f) ? max_nan(m[n][e], x) : m[n][e];
-                const float f = mn == m[n][e] ? 1.f : ex2(m[n][e] - mn);
+                if (x <= top[n][e]) continue;
+                const float mn = max_nan(m[n][e], x * p.sl2);
+                const float f = ex2(m[n][e] - mn);
                 m[n][e] = mn;
-                mu[n][e] = mn == -INFINITY ? 0.f : mn;
+                top[n][e] = x + slack;
                 l[n][e] *= f;
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
@@ -560,11 +614,16 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              float pr[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) pr[j] = ex2(fmaf(sc[i][n][j], p.sl2, -mu[n][j & 1]));
-              l[n][0] += pr[0] + pr[2];
-              l[n][1] += pr[1] + pr[3];
+              const float2 sl2 = make_float2(p.sl2, p.sl2);
+              const float2 nm = make_float2(m[n][0] == -INFINITY ? 0.f : -m[n][0],
+                                            m[n][1] == -INFINITY ? 0.f : -m[n][1]);
+              const float2 x = fma2(make_float2(sc[i][n][0], sc[i][n][1]), sl2, nm);
+              const float2 y = fma2(make_float2(sc[i][n][2], sc[i][n][3]), sl2, nm);
+              const float pr[4] = {ex2(x.x), ex2(x.y), ex2(y.x), ex2(y.y)};
+              const float2 sum = add2(make_float2(pr[0], pr[1]), make_float2(pr[2], pr[3]));
+              const float2 ll = add2(make_float2(l[n][0], l[n][1]), sum);
+              l[n][0] = ll.x;
+              l[n][1] = ll.y;
               uint32_t u[NS], v[NS];
               split_pair<NS>(pr[0], pr[1], u);
               split_pair<NS>(pr[2], pr[3], v);
@@ -581,7 +640,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
         for (int i = 0; i < 2; ++i) {
           const uint8_t* vt = base + i * tile_bytes + half;
           const uint32_t* par = reinterpret_cast<const uint32_t*>(vt + kCacheTile * (D / 2));
-          const int grp = 8 * VW * g / p.c.G;
+          const int grp = 8 * VW * g / G;
           // tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 are in rows t4, t4 + 4, t4 + 8, t4 + 12
           uint32_t w[4][VW], az[4];
 #pragma unroll
@@ -608,10 +667,10 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
 #pragma unroll
           for (int j = 0; j < VW; ++j) {
             uint32_t x0[4], x1[4], y0[4], y1[4];  // even and odd channels of tokens t.., of t + 8..
-            codes_to_bf16<false>(__byte_perm(w[0][j], w[1][j], 0x5410), x0);
-            codes_to_bf16<false>(__byte_perm(w[0][j], w[1][j], 0x7632), x1);
-            codes_to_bf16<false>(__byte_perm(w[2][j], w[3][j], 0x5410), y0);
-            codes_to_bf16<false>(__byte_perm(w[2][j], w[3][j], 0x7632), y1);
+            codes_to_bf16<false>(__byte_perm(w[0][j], w[1][j], 0x5410), p.ones, x0);
+            codes_to_bf16<false>(__byte_perm(w[0][j], w[1][j], 0x7632), p.ones, x1);
+            codes_to_bf16<false>(__byte_perm(w[2][j], w[3][j], 0x5410), p.ones, y0);
+            codes_to_bf16<false>(__byte_perm(w[2][j], w[3][j], 0x7632), p.ones, y1);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const uint32_t f0 = bf16x2_fma(x0[q], a0, z0), f1 = bf16x2_fma(x1[q], a0, z0);
@@ -627,7 +686,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
         // the stage has been read
         __syncwarp();
         if (++stage == p.stages) stage = 0;
-        if (to_issue > 0) issue();
+        if (to_issue) issue();
       }
       if (!ok) break;
 
@@ -638,9 +697,14 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int q = 4; q < 32; q <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], q);
-      steps -= here;
+      Item after = it;
+      more = !it.same(end);
+      if (more) {
+        after.next(p, RB);
+        more = after.r < p.a.n_req && after.left(end) > 0;
+      }
       const bool whole_item = starts && ends;
-      float* const to = steps == 0 ? slot_smem : slot_ws;
+      float* const to = more ? slot_ws : slot_smem;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -666,7 +730,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
       if (lane == 0 && !whole_item) {
         if (!starts) {
           meta[warp].head = ends ? 1 : 2;
-          meta[warp].head_global = steps != 0;
+          meta[warp].head_global = more;
           meta[warp].head_rows = rows;
         } else {
           meta[warp].tail = 1;
@@ -678,7 +742,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
         meta[warp].h = it.h;
         meta[warp].rb = it.rb;
       }
-      if (steps > 0) it.next(p, RB);
+      it = after;
     }
     if (!ok && lane == 0) {
       // never leave with a copy still writing into this CTA's shared memory
@@ -694,23 +758,52 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
   }
 
   // ---- the CTA's pieces -------------------------------------------------------
-  // Pieces in order; a tail begins a group, a head that ends the item closes one.
-  auto slot_of = [&](int id) -> const float* {  // id: 2 warp + (0 head, 1 tail)
-    const int w = id >> 1;
-    if ((id & 1) == 0 && meta[w].head_global) return ws + ((int64_t)blockIdx.x * WARPS + w) * S::kFloats;
-    return reinterpret_cast<const float*>(smem + (size_t)w * p.stages * stage_bytes);
-  };
+  // Pieces in order: number 2 w is warp w's head, 2 w + 1 its tail.  A tail begins a group
+  // of pieces of one item, a head that ends the item closes one.  RB D / 4 threads join a
+  // group, each 4 channels of a row; the groups are shared out among such sets of threads.
+  static_assert(2 * WARPS <= 32, "a bit per piece");
+  constexpr int V = D / 4, kSets = WARPS * 32 / (RB * V) > 0 ? WARPS * 32 / (RB * V) : 1;
+  const bool mine = lane < 2 * WARPS;
+  const int state = !mine ? 0 : (lane & 1) ? meta[lane >> 1].tail : meta[lane >> 1].head;
+  const uint32_t pieces = __ballot_sync(0xffffffffu, state != 0);
+  const uint32_t tails = __ballot_sync(0xffffffffu, (lane & 1) && state != 0);
+  const uint32_t closing = __ballot_sync(0xffffffffu, !(lane & 1) && state == 1);
   float* const cta_slots = ws + W::cta_slots(gridDim.x) + 2 * (size_t)blockIdx.x * S::kFloats;
-  // joins the pieces `ids`, each thread 4 channels of a row at a time
-  auto join = [&](uint32_t ids, int rows, bool out, int owner, float* to) {
-    for (int e = threadIdx.x; e < rows * (D / 4); e += WARPS * 32) {
-      const int row = e / (D / 4), ch = (e - row * (D / 4)) * 4;
+  const int set = threadIdx.x / (RB * V);
+  int k = 0;
+  for (uint32_t lead = tails | (pieces & (0u - pieces)); lead; lead &= lead - 1, ++k) {
+    const uint32_t first = lead & (0u - lead), rest = lead & (lead - 1);
+    const uint32_t ids = pieces & (rest ? (rest & (0u - rest)) - first : 0u - first);
+    const bool begun = (first & tails) != 0, ended = (ids & closing) != 0;
+    const int owner = (__ffs(first) - 1) >> 1;
+    if (threadIdx.x == 0) {
+      CtaMeta* cm = &out_meta[blockIdx.x];
+      if (k == 0) {
+        cm->head = begun ? 0 : ended ? 1 : 2;
+        cm->tail = 0;
+      }
+      if (begun && !ended) {
+        cm->tail = 1;
+        cm->begin = meta[owner].begin;
+        cm->nq = meta[owner].nq;
+        cm->h = meta[owner].h;
+        cm->rb = meta[owner].rb;
+      }
+    }
+    if (kSets > 1 && k % kSets != set) continue;
+    const int rows = begun ? meta[owner].rows : meta[owner].head_rows;
+    float* const to = cta_slots + (begun ? S::kFloats : 0);
+    for (int e = threadIdx.x - (kSets > 1 ? set * RB * V : 0); e < rows * V; e += kSets > 1 ? RB * V : WARPS * 32) {
+      const int row = e / V, ch = (e - row * V) * 4;
       Acc acc;
       for (uint32_t b = ids; b; b &= b - 1) {
-        const float* s = slot_of(__ffs(b) - 1);
+        const int id = __ffs(b) - 1, w = id >> 1;
+        const float* s = (id & 1) == 0 && meta[w].head_global
+                             ? ws + ((size_t)blockIdx.x * WARPS + w) * S::kFloats
+                             : reinterpret_cast<const float*>(smem + (size_t)w * p.stages * stage_bytes);
         acc.add(S::ml(s)[row], *reinterpret_cast<const float4*>(s + row * D + ch));
       }
-      if (out) {
+      if (begun && ended) {
         const PieceMeta& m = meta[owner];
         write_out<D>(p, out_row(p, m.begin, m.h, m.rb, RB, row), ch, acc.m, acc.l, acc.o);
       } else {
@@ -718,38 +811,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
         if (ch == 0) S::ml(to)[row] = make_float2(acc.m, acc.l);
       }
     }
-  };
-  CtaMeta cm = {0, 0, 0, 0, 0, 0};
-  uint32_t group = 0;       // ids of the group's pieces, as bits
-  bool begun = false;       // the group's item began in this CTA
-  int rows = 0, owner = 0;  // owner: the warp that knows the begun item
-  for (int id = 0; id < 2 * WARPS; ++id) {
-    const int w = id >> 1;
-    const bool is_tail = id & 1;
-    const int state = is_tail ? meta[w].tail : meta[w].head;
-    if (state == 0) continue;
-    if (is_tail) begun = true, owner = w, group = 0;
-    rows = is_tail ? meta[w].rows : meta[w].head_rows;
-    group |= 1u << id;
-    if (is_tail || state == 2) continue;
-    join(group, rows, begun, owner, cta_slots);  // the item ends here
-    if (!begun) cm.head = 1;
-    group = 0;
-    begun = false;
   }
-  if (group) {
-    join(group, rows, false, owner, cta_slots + (begun ? S::kFloats : 0));
-    if (begun) {
-      cm.tail = 1;
-      cm.begin = meta[owner].begin;
-      cm.nq = meta[owner].nq;
-      cm.h = meta[owner].h;
-      cm.rb = meta[owner].rb;
-    } else {
-      cm.head = 2;
-    }
-  }
-  if (threadIdx.x == 0) out_meta[blockIdx.x] = cm;
+  if (threadIdx.x == 0 && pieces == 0) out_meta[blockIdx.x].head = out_meta[blockIdx.x].tail = 0;
 }
 
 // Items that cross CTAs: CTA c of this grid joins the one that CTA c of the first began,
@@ -811,16 +874,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
 // ---------------------------------------------------------------------------
 // NT 8-row blocks at a time, NS bf16 parts of q and P, CTAs of WARPS warps, MINB of them
 // on an SM: what the accumulators leave of the 64 K registers.
-template <int D, int NT, int NS, int WARPS, int MINB>
+template <int D, int G, int NT, int NS, int WARPS, int MINB>
 struct Variant {
   static constexpr int kCtas = kMaxSms * MINB;
   static constexpr int kStatic = 4096;  // static shared memory and what the system keeps
   using W = Work<D, 8 * NT, WARPS>;
   static size_t workspace() { return W::meta(kCtas) * sizeof(float) + kCtas * sizeof(CtaMeta); }
   static cudaError_t launch(Params p, int sms, cudaStream_t st) {
-    auto kern = attn_kernel<D, NT, NS, WARPS, MINB>;
+    auto kern = attn_kernel<D, G, NT, NS, WARPS, MINB>;
     const int stage = WARPS * 2 * p.c.tile_bytes();
-    const int room = 228 * 1024 / MINB - kStatic;
+    const int room = 227 * 1024 / MINB - kStatic;
     p.stages = room / stage < 8 ? room / stage : 8;
     // the ring of a warp also takes the sums of its last piece
     if (p.stages < 1 || (size_t)p.stages * stage < W::kSlot * WARPS * sizeof(float))
@@ -850,30 +913,31 @@ struct Variant {
     return cudaLaunchKernelEx(&cfg, join_kernel<D, 8 * NT, WARPS>, p);
   }
 };
-template <int D>
-using Rows8 = Variant<D, 1, 1, 8, 2>;
-template <int D>
-using Rows16 = Variant<D, 2, 1, 4, 3>;
-template <int D>
-using Exact8 = Variant<D, 1, 3, 4, 3>;
+template <int D, int G>
+using Rows8 = Variant<D, G, 1, 1, 16, 1>;
+template <int D, int G>
+using Rows16 = Variant<D, G, 2, 1, 12, 1>;
+template <int D, int G>
+using Exact8 = Variant<D, G, 1, 3, 12, 1>;
 
 }  // namespace cattn
 
-template <int D>
-static size_t attn_workspace(const Cache& c) {
+// The workspace does not depend on the group.
+size_t cache_attn_workspace(const Cache& c) {
   using namespace cattn;
-  size_t n = c.bf16 ? std::max(Rows8<D>::workspace(), Rows16<D>::workspace()) : Exact8<D>::workspace();
+  const size_t n = !c.bf16       ? (c.D == 128 ? Exact8<128, 32>::workspace() : Exact8<64, 32>::workspace())
+                   : c.D == 128 ? std::max(Rows8<128, 32>::workspace(), Rows16<128, 32>::workspace())
+                                : std::max(Rows8<64, 32>::workspace(), Rows16<64, 32>::workspace());
   return (n + 255) / 256 * 256;
 }
-size_t cache_attn_workspace(const Cache& c) { return c.D == 128 ? attn_workspace<128>(c) : attn_workspace<64>(c); }
 
-template <int D>
+template <int D, int G>
 static cudaError_t launch_attn(const cattn::Params& p, int sms, cudaStream_t st) {
   using namespace cattn;
-  if (!p.c.bf16) return Exact8<D>::launch(p, sms, st);
+  if (!p.c.bf16) return Exact8<D, G>::launch(p, sms, st);
   // 8 rows at a time while that is all a request has
-  if ((int64_t)p.a.max_q * p.n_rep <= 8) return Rows8<D>::launch(p, sms, st);
-  return Rows16<D>::launch(p, sms, st);
+  if ((int64_t)p.a.max_q * p.n_rep <= 8) return Rows8<D, G>::launch(p, sms, st);
+  return Rows16<D, G>::launch(p, sms, st);
 }
 
 cudaError_t launch_cache_attn(const Cache& c, const CacheAttnArgs& a, cudaStream_t st) {
@@ -883,13 +947,19 @@ cudaError_t launch_cache_attn(const Cache& c, const CacheAttnArgs& a, cudaStream
   p.n_rep = c.Hq / c.Hkv;
   p.stages = 0;
   p.per_sum = (a.n_req + cattn::kSums - 1) / cattn::kSums;
+  p.ones = kOnes;
   p.sl2 = c.scale * 1.44269504088896340736f;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   timing_begin("cache_attn", st);
-  e = c.D == 128 ? launch_attn<128>(p, sms, st) : launch_attn<64>(p, sms, st);
+  if (c.D == 128)
+    e = c.G == 128  ? launch_attn<128, 128>(p, sms, st)
+        : c.G == 64 ? launch_attn<128, 64>(p, sms, st)
+                    : launch_attn<128, 32>(p, sms, st);
+  else
+    e = c.G == 64 ? launch_attn<64, 64>(p, sms, st) : launch_attn<64, 32>(p, sms, st);
   timing_end(st);
   return e;
 }

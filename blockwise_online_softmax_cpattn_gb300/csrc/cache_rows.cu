@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t word = reinterpret_cast<const uint32_t*>(half)[r * tpr + w];
     const uint32_t az =
         reinterpret_cast<const uint32_t*>(half + kCacheTile * c.row_bytes())[r * c.groups() + w * 8 / c.G];
-    if (is_v) codes_to_bf16<false>(word, u);
-    else codes_to_bf16<true>(word, u);
+    if (is_v) codes_to_bf16<false>(word, kOnes, u);
+    else codes_to_bf16<true>(word, kOnes, u);
 #pragma unroll
     for (int p = 0; p < 4; ++p) u[p] = bf16x2_fma(u[p], az_a2(az), az_z2(az));
   }
