@@ -12,8 +12,9 @@
 //   neither ragged lengths nor few requests leave SMs idle, and nothing about lengths
 //   has to be known on the host.  A run ends anywhere: pieces of an item are joined by
 //   the (O, m, l) merge, first among the warps of a CTA in shared memory, then, for
-//   items that cross CTAs, by a second small kernel (a programmatic dependent) from the
-//   workspace.  Pieces are joined in their order: the result is the same every time.
+//   items that cross CTAs, after a grid barrier from the workspace (a second launch in its
+//   place cost 4 to 6 us a call).  Pieces are joined in their order: the result is the same
+//   every time.
 //
 //   Loads.  A tile of 16 tokens of one K/V head is contiguous (codes and their (a, z)):
 //   one bulk copy, of two tiles where a page holds both.  Each warp keeps a ring of
@@ -34,6 +35,7 @@
 //
 // float32 (NS = 3): q and P are sums of three bf16 numbers, the cached values are bf16
 // numbers anyway, so three MMAs give products of float32 quality.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include <algorithm>
@@ -57,6 +59,8 @@ struct Params {
   CacheAttnArgs a;
   int n_rep, stages;
   int per_sum;                       // requests per entry of the prefix sums
+  int page_tiles, unit_in_page;      // tiles of a page; units do not straddle pages
+  int64_t page_bytes;                // of all K/V heads
   float sl2;                         // scale * log2(e)
   uint32_t ones;                     // kOnes
 };
@@ -100,6 +104,12 @@ __device__ __forceinline__ int64_t head_cost(const Params& p, const Req& q, int 
   return n;
 }
 
+// i / n of x, rounded down (the 32-bit division where it does: n, i < 2^8)
+__device__ __forceinline__ int64_t part_of(int64_t x, int i, int n) {
+  if (x < (1 << 24)) return (unsigned)x * (unsigned)i / (unsigned)n;
+  return x * i / n;
+}
+
 // Request, K/V head and row block of an item, and a unit in it.  Items follow each other by
 // row block, K/V head, request.
 struct Place {
@@ -125,7 +135,7 @@ struct Item : Place {
       if (q.nq == 0) continue;
       const int64_t c = head_cost(p, q, RB);
       if (x < c * p.c.Hkv) {
-        h = (int)(x / c);
+        h = x <= 0x7fffffff ? (int)((unsigned)x / (unsigned)min(c, (int64_t)0x7fffffff)) : (int)(x / c);
         x -= h * c;
         break;
       }
@@ -139,14 +149,6 @@ struct Item : Place {
       x -= units + kItemCost;
     }
     u = max(0, min((int)x - kItemCost, units - 1));
-  }
-  __device__ __forceinline__ Item from_lane(int src) const {
-    Item o;
-    const int* a = reinterpret_cast<const int*>(this);
-    int* b = reinterpret_cast<int*>(&o);
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(Item) / sizeof(int)); ++i) b[i] = __shfl_sync(0xffffffffu, a[i], src);
-    return o;
   }
   __device__ __forceinline__ void next(const Params& p, int RB) {
     u = 0;
@@ -184,7 +186,7 @@ struct Work {
   static __host__ __device__ size_t cta_slots(int ctas) { return (size_t)ctas * WARPS * kSlot; }
   static __host__ __device__ size_t meta(int ctas) { return (size_t)ctas * (WARPS + 2) * kSlot; }
 };
-// What a CTA leaves for the second kernel: the state of its head piece (the part of an
+// What a CTA leaves for the joining of items that cross CTAs: the state of its head piece (the part of an
 // item that an earlier CTA began) and whether a tail piece (of an item begun here)
 // is open.
 struct CtaMeta {
@@ -268,41 +270,32 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&u)[NS]) 
   }
 }
 
-template <int D, int G, int NT, int NS, int WARPS, int MINB>
-__global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) {
-  constexpr int RB = 8 * NT;
-  constexpr int KW = D / 32;    // words of a K row per lane (channels 8 KW t4 ..)
-  constexpr int VW = D / 64;    // words of a V row per lane (channels 8 VW g ..)
-  constexpr int MT = D / 16;    // 16-channel tiles of O^T
-  using S = Slot<D, RB>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t sums[kSums];      // inclusive prefix sums of units over requests
-  __shared__ int64_t warp_part[WARPS];
-  __shared__ uint64_t bars_[WARPS * 8];
-  __shared__ int abort_;
-  struct PieceMeta {
-    int head;         // 0 none, 1 ends the item, 2 goes on
-    int head_global;  // the head piece is in the workspace, not in shared memory
-    int tail;         // 1: open
-    int rows, begin, h, rb, nq;  // of the tail's item
-    int head_rows;
-  };
-  __shared__ PieceMeta meta[WARPS];
+// What a warp tells the others of its CTA about its open pieces.
+struct PieceMeta {
+  int head;         // 0 none, 1 ends the item, 2 goes on
+  int head_global;  // the head piece is in the workspace, not in shared memory
+  int tail;         // 1: open
+  int rows, begin, h, rb, nq;  // of the tail's item
+  int head_rows;
+};
+template <int WARPS>
+struct Shared {
+  int64_t sums[kSums];          // inclusive prefix sums of cost over requests
+  int64_t warp_part[WARPS];
+  uint64_t bars[WARPS * 8];
+  int abort;
+  PieceMeta meta[WARPS];
+  // per warp, what the main loop has no registers for: the items that are being loaded and
+  // computed, and the run's end
+  Item in[WARPS], it[WARPS];
+  Place end[WARPS];
+};
 
+// The run of this warp: its first unit and the next warp's, into sh.  (Apart from the kernel,
+// as the last part below is, so that their registers and the main loop's do not mix.)
+template <int RB, int WARPS>
+__device__ __noinline__ void find_run(const Params& p, Shared<WARPS>& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t4 = lane & 3;
-  constexpr int par_words = D / G;
-  constexpr int half = kCacheTile * (D / 2 + 4 * par_words);
-  constexpr int tile_bytes = 2 * half, stage_bytes = 2 * tile_bytes;
-  volatile int* abort = &abort_;
-  if (threadIdx.x == 0) abort_ = 0;
-  if (lane == 0) {
-    for (int s = 0; s < p.stages; ++s) mbar_init(smem_u32(&bars_[warp * 8 + s]), 1);
-    fence_barrier_init();
-  }
-  griddep_launch_dependents();
-
-  // ---- prefix sums of units over the requests --------------------------------
   int64_t total;
   {
     int64_t run = 0;
@@ -328,176 +321,299 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
       const int64_t y = __shfl_up_sync(0xffffffffu, inc, m);
       if (lane >= m) inc += y;
     }
-    if (lane == 31) warp_part[warp] = inc;
+    if (lane == 31) sh.warp_part[warp] = inc;
     __syncthreads();
     int64_t before = 0;
     total = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) before += warp_part[w];
-      total += warp_part[w];
+      if (w < warp) before += sh.warp_part[w];
+      total += sh.warp_part[w];
     }
 #pragma unroll
     for (int i = 0; i < PT; ++i)
-      if (threadIdx.x * PT + i < kSums) sums[threadIdx.x * PT + i] = before + inc - run + mine[i];
+      if (threadIdx.x * PT + i < kSums) sh.sums[threadIdx.x * PT + i] = before + inc - run + mine[i];
     __syncthreads();
   }
 
-  // ---- this warp's run of units ----------------------------------------------
   // An item costs its units and some for its start and end (the request's numbers and its
   // query rows come from memory, its result goes there); every warp gets an equal run of
   // that.  CTAs that would get nothing are not counted, so an item's CTAs are neighbours.
-  using W = Work<D, RB, WARPS>;
-  float* const ws = static_cast<float*>(p.a.ws);
-  CtaMeta* const out_meta = reinterpret_cast<CtaMeta*>(ws + W::meta(gridDim.x));
-  const int ctas = (int)min((int64_t)gridDim.x, total);
-  if ((int)blockIdx.x >= ctas) {
-    if (threadIdx.x == 0) out_meta[blockIdx.x].head = out_meta[blockIdx.x].tail = 0;
-    return;
-  }
-  const int64_t c0 = total * blockIdx.x / ctas, c1 = total * (blockIdx.x + 1) / ctas;
-  float* const slot_smem = reinterpret_cast<float*>(smem + (size_t)warp * p.stages * stage_bytes);
-  float* const slot_ws = ws + ((size_t)blockIdx.x * WARPS + warp) * S::kFloats;
-  if (lane == 0) {
-    meta[warp].head = 0;
-    meta[warp].tail = 0;
-  }
+  const int ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total));
+  const int cta = min((int)blockIdx.x, ctas);
+  const int64_t c0 = part_of(total, cta, ctas), c1 = part_of(total, min(cta + 1, ctas), ctas);
   // the run's first unit, and the next warp's: one half of the lanes looks for each
-  Item in;  // of the copies
-  Place end;
   {
-    const int64_t v = c0 + (c1 - c0) * (warp + (lane >> 4)) / WARPS;
+    const int64_t v = c0 + part_of(c1 - c0, warp + (lane >> 4), WARPS);
     int lo = 0, hi = kSums;  // first entry whose inclusive sum is past v
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (sums[mid] > v) hi = mid;
+      if (sh.sums[mid] > v) hi = mid;
       else lo = mid + 1;
     }
     Item x;
     x.seen = x.units = 0;
     x.q = {0, 0, 0};
-    x.locate(p, RB, lo * p.per_sum, lo < kSums ? v - (lo ? sums[lo - 1] : 0) : 0);
-    in = x.from_lane(0);
-    end.r = __shfl_sync(0xffffffffu, x.r, 16);
-    end.h = __shfl_sync(0xffffffffu, x.h, 16);
-    end.rb = __shfl_sync(0xffffffffu, x.rb, 16);
-    end.u = __shfl_sync(0xffffffffu, x.u, 16);
+    x.locate(p, RB, lo * p.per_sum, lo < kSums ? v - (lo ? sh.sums[lo - 1] : 0) : 0);
+    if (lane == 0) sh.in[warp] = sh.it[warp] = x;
+    if (lane == 16) sh.end[warp] = x;
   }
+}
+
+// The end of the kernel: joins the CTA's open pieces, then the items that cross CTAs.
+template <int D, int RB, int WARPS>
+__device__ __noinline__ void finish(const Params& p, const Shared<WARPS>& sh, uint8_t* smem, int stage_bytes) {
+  using S = Slot<D, RB>;
+  using W = Work<D, RB, WARPS>;
+  const int lane = threadIdx.x & 31;
+  const PieceMeta* meta = sh.meta;
+  float* const ws = static_cast<float*>(p.a.ws);
+  CtaMeta* const out_meta = reinterpret_cast<CtaMeta*>(ws + W::meta(gridDim.x));
+  // ---- the CTA's pieces -------------------------------------------------------
+  // Pieces in order: number 2 w is warp w's head, 2 w + 1 its tail.  A tail begins a group
+  // of pieces of one item, a head that ends the item closes one.  RB D / 4 threads join a
+  // group, each 4 channels of a row; the groups are shared out among such sets of threads.
+  static_assert(2 * WARPS <= 32, "a bit per piece");
+  constexpr int V = D / 4, kSets = WARPS * 32 / (RB * V) > 0 ? WARPS * 32 / (RB * V) : 1;
+  const bool mine = lane < 2 * WARPS;
+  const int state = !mine ? 0 : (lane & 1) ? meta[lane >> 1].tail : meta[lane >> 1].head;
+  const uint32_t pieces = __ballot_sync(0xffffffffu, state != 0);
+  const uint32_t tails = __ballot_sync(0xffffffffu, (lane & 1) && state != 0);
+  const uint32_t closing = __ballot_sync(0xffffffffu, !(lane & 1) && state == 1);
+  float* const cta_slots = ws + W::cta_slots(gridDim.x) + 2 * (size_t)blockIdx.x * S::kFloats;
+  const int set = threadIdx.x / (RB * V);
+  int k = 0;
+  for (uint32_t lead = tails | (pieces & (0u - pieces)); lead; lead &= lead - 1, ++k) {
+    const uint32_t first = lead & (0u - lead), rest = lead & (lead - 1);
+    const uint32_t ids = pieces & (rest ? (rest & (0u - rest)) - first : 0u - first);
+    const bool begun = (first & tails) != 0, ended = (ids & closing) != 0;
+    const int owner = (__ffs(first) - 1) >> 1;
+    if (threadIdx.x == 0) {
+      CtaMeta* cm = &out_meta[blockIdx.x];
+      if (k == 0) {
+        cm->head = begun ? 0 : ended ? 1 : 2;
+        cm->tail = 0;
+      }
+      if (begun && !ended) {
+        cm->tail = 1;
+        cm->begin = meta[owner].begin;
+        cm->nq = meta[owner].nq;
+        cm->h = meta[owner].h;
+        cm->rb = meta[owner].rb;
+      }
+    }
+    if (kSets > 1 && k % kSets != set) continue;
+    const int rows = begun ? meta[owner].rows : meta[owner].head_rows;
+    float* const to = cta_slots + (begun ? S::kFloats : 0);
+    for (int e = threadIdx.x - (kSets > 1 ? set * RB * V : 0); e < rows * V; e += kSets > 1 ? RB * V : WARPS * 32) {
+      const int row = e / V, ch = (e - row * V) * 4;
+      Acc acc;
+      for (uint32_t b = ids; b; b &= b - 1) {
+        const int id = __ffs(b) - 1, w = id >> 1;
+        const float* s = (id & 1) == 0 && meta[w].head_global
+                             ? ws + ((size_t)blockIdx.x * WARPS + w) * S::kFloats
+                             : reinterpret_cast<const float*>(smem + (size_t)w * p.stages * stage_bytes);
+        acc.add(S::ml(s)[row], *reinterpret_cast<const float4*>(s + row * D + ch));
+      }
+      if (begun && ended) {
+        const PieceMeta& m = meta[owner];
+        write_out<D>(p, out_row(p, m.begin, m.h, m.rb, RB, row), ch, acc.m, acc.l, acc.o);
+      } else {
+        *reinterpret_cast<float4*>(to + row * D + ch) = acc.o;
+        if (ch == 0) S::ml(to)[row] = make_float2(acc.m, acc.l);
+      }
+    }
+  }
+  if (threadIdx.x == 0 && pieces == 0) out_meta[blockIdx.x].head = out_meta[blockIdx.x].tail = 0;
+
+  // ---- items that cross CTAs --------------------------------------------------
+  // The CTA that began one joins its tail and the heads of the CTAs behind it up to the one
+  // that ends the item.  Few rows leave threads over: those share the pieces and meet in
+  // shared memory.
+  cooperative_groups::this_grid().sync();
+  const CtaMeta cm = out_meta[blockIdx.x];
+  if (!cm.tail) return;
+  int n = 1;
+  for (int i = blockIdx.x + 1; i < (int)gridDim.x; i += 32) {
+    const bool last = i + lane >= (int)gridDim.x || out_meta[i + lane].head != 2;
+    const uint32_t b = __ballot_sync(0xffffffffu, last);
+    n = i - (int)blockIdx.x + (b ? __ffs(b) : 32);
+    if (b) break;
+  }
+  n = min(n, (int)(gridDim.x - blockIdx.x));
+  const int rows = block_rows(p, cm.nq, cm.rb, RB), parts = rows * V;
+  const int shares = max(1, WARPS * 32 / parts), share = threadIdx.x / parts;
+  Acc* const meet = reinterpret_cast<Acc*>(smem);
+  for (int e = shares > 1 ? threadIdx.x % parts : threadIdx.x; e < parts; e += shares > 1 ? parts : WARPS * 32) {
+    const int row = e / V, ch = (e - row * V) * 4;
+    Acc acc;
+    if (shares == 1 || share < shares) {
+#pragma unroll 4
+      for (int i = shares > 1 ? share : 0; i < n; i += shares) {
+        const float* s = cta_slots + (i ? 2 * (size_t)i : 1) * S::kFloats;
+        acc.add(S::ml(s)[row], *reinterpret_cast<const float4*>(s + row * D + ch));
+      }
+    }
+    if (shares > 1) meet[threadIdx.x] = acc;
+    else write_out<D>(p, out_row(p, cm.begin, cm.h, cm.rb, RB, row), ch, acc.m, acc.l, acc.o);
+  }
+  if (shares == 1) return;
+  __syncthreads();
+  if ((int)threadIdx.x >= parts) return;
+  Acc acc = meet[threadIdx.x];
+  for (int i = 1; i < shares; ++i) {
+    const Acc& x = meet[threadIdx.x + i * parts];
+    acc.add(make_float2(x.m, x.l), x.o);
+  }
+  const int row = threadIdx.x / V, ch = (threadIdx.x - row * V) * 4;
+  write_out<D>(p, out_row(p, cm.begin, cm.h, cm.rb, RB, row), ch, acc.m, acc.l, acc.o);
+}
+
+template <int D, int G, int NT, int NS, int WARPS, int MINB>
+__global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) {
+  constexpr int RB = 8 * NT;
+  constexpr int KW = D / 32;    // words of a K row per lane (channels 8 KW t4 ..)
+  constexpr int VW = D / 64;    // words of a V row per lane (channels 8 VW g ..)
+  constexpr int MT = D / 16;    // 16-channel tiles of O^T
+  using S = Slot<D, RB>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Shared<WARPS> sh;
+  PieceMeta* const meta = sh.meta;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  constexpr int par_words = D / G;
+  constexpr int half = kCacheTile * (D / 2 + 4 * par_words);
+  constexpr int tile_bytes = 2 * half, stage_bytes = 2 * tile_bytes;
+  volatile int* abort = &sh.abort;
+  if (threadIdx.x == 0) sh.abort = 0;
+  if (lane == 0) {
+    for (int s = 0; s < p.stages; ++s) mbar_init(smem_u32(&sh.bars[warp * 8 + s]), 1);
+    fence_barrier_init();
+  }
+
+  find_run<RB>(p, sh);
+  float* const slot_smem = reinterpret_cast<float*>(smem + (size_t)warp * p.stages * stage_bytes);
+  if (lane == 0) {
+    meta[warp].head = 0;
+    meta[warp].tail = 0;
+  }
+  __syncwarp();
   bool ok = true;
-  if (in.r < p.a.n_req && !(in.same(end) && in.u == end.u)) {
-    Item it = in;  // of the arithmetic
-    bool to_issue = true;
-    const uint32_t ring = smem_u32(slot_smem), bar0 = smem_u32(&bars_[warp * 8]);
+  int to_issue = sh.in[warp].r < p.a.n_req ? sh.in[warp].left(sh.end[warp]) : 0;  // units of the item
+  if (to_issue > 0) {
+    const uint32_t ring = smem_u32(slot_smem), bar0 = smem_u32(&sh.bars[warp * 8]);
     int stage_in = 0, stage = 0;
     uint32_t parity = 0, valid = 0;  // two bits a stage: which tiles were loaded
-    // Pages of the coming tiles: lane i knows that of tile tab_at + i, or where a unit is
-    // inside one page (a page is 32 tokens or a multiple), of unit tab_at + i.
-    const bool one_page = p.c.page % kUnit == 0;
-    const int per = p.c.page / kCacheTile;   // tiles of a page
-    const int per_lane = one_page ? 1 : 2;   // entries of a unit
-    int tab = 0, tab_at = 0, tab_end = 0;    // units [tab_at, tab_end) are known
-    int w0 = (in.u * 2) % per;               // the unit's first tile in its page
-    const uint8_t* from = nullptr;           // the request's K/V head in page 0
-    int64_t page_bytes = (int64_t)p.c.Hkv * p.c.block_bytes();
+    // Pages of the coming tiles: lane i knows that of the i-th, or where units are inside
+    // pages (a page is a multiple of 32 tokens), of the i-th unit.
+    const int per_lane = p.unit_in_page ? 1 : 2;
+    int tab = 0, tab_k = 32;         // the next unit's first lane
+    int w0 = 0;                      // the unit's first tile in its page
+    const uint8_t* from = nullptr;   // the item's K/V head in page 0
     // issues the copies of the next unit
     auto issue = [&]() {
-      if (in.u >= tab_end) {
-        tab_at = in.u;
-        tab_end = in.u + 32 / per_lane;
+      if (tab_k == 32) {
+        const Item& in = sh.in[warp];
         const int64_t tok = ((int64_t)in.u * per_lane + lane) * (kUnit / per_lane);
-        tab = tok < in.seen && in.r < p.a.n_req ? p.a.table[(int64_t)in.r * p.a.max_pages + tok / p.c.page] : -1;
+        tab = tok < in.seen ? p.a.table[(int64_t)in.r * p.a.max_pages + tok / p.c.page] : -1;
         from = p.a.cache + in.h * p.c.block_bytes();
+        w0 = (in.u * 2) % p.page_tiles;
+        tab_k = 0;
+        __syncwarp();
+        if (lane == 0) sh.in[warp].u += 32 / per_lane;  // where the next look at the table starts
       }
       const uint32_t bar = bar0 + 8 * stage_in;
       const uint32_t dst = ring + stage_in * stage_bytes;
+      const int pg = __shfl_sync(0xffffffffu, tab, p.unit_in_page ? tab_k : tab_k + (lane & 1));
+      const bool page_ok = (unsigned)pg < (unsigned)p.c.n_pages;
       uint32_t have;
-      if (one_page) {
-        const int pg = __shfl_sync(0xffffffffu, tab, in.u - tab_at);
-        const bool page_ok = (unsigned)pg < (unsigned)p.c.n_pages;
-        const bool both = in.u * kUnit + kCacheTile < in.seen;  // else the second tile is not looked at
-        have = page_ok ? (both ? 3u : 1u) : 0u;
+      if (p.unit_in_page) {
+        // (of an item's last unit the second tile may lie past its end: it is masked)
+        have = page_ok ? 3u : 0u;
         if (lane == 0) {
-          const uint32_t bytes = have == 3u ? 2 * tile_bytes : have * tile_bytes;
-          mbar_expect_tx(bar, bytes);
-          if (have) bulk_load(dst, from + pg * page_bytes + w0 * tile_bytes, bytes, bar);
+          mbar_expect_tx(bar, page_ok ? stage_bytes : 0);
+          if (page_ok) bulk_load(dst, from + pg * p.page_bytes + w0 * tile_bytes, stage_bytes, bar);
         }
-        if ((w0 += 2) == per) w0 = 0;
+        w0 = w0 + 2 == p.page_tiles ? 0 : w0 + 2;
       } else {
         // a lane a tile
-        const int pg = __shfl_sync(0xffffffffu, tab, (in.u - tab_at) * 2 + (lane & 1));
-        const bool page_ok = (unsigned)pg < (unsigned)p.c.n_pages;
         have = __ballot_sync(0xffffffffu, page_ok) & 3u;
-        int w = w0 + (lane & 1);
-        if (w >= per) w -= per;
         if (lane == 0) mbar_expect_tx(bar, __popc(have) * tile_bytes);
         __syncwarp();
+        const int w = w0 + (lane & 1);
         if (lane < 2 && page_ok)
-          bulk_load(dst + lane * tile_bytes, from + pg * page_bytes + w * tile_bytes, tile_bytes, bar);
-        w0 = w0 + 2 >= per ? w0 + 2 - per : w0 + 2;
-        if (per == 1) w0 = 0;
+          bulk_load(dst + lane * tile_bytes, from + pg * p.page_bytes + (w < p.page_tiles ? w : 0) * tile_bytes,
+                    tile_bytes, bar);
+        w0 = (w0 + 2) % p.page_tiles;
       }
+      tab_k += per_lane;
       valid = (valid & ~(3u << (2 * stage_in))) | have << (2 * stage_in);
       if (++stage_in == p.stages) stage_in = 0;
-      ++in.u;
-      if (in.left(end) == 0) {
-        to_issue = !in.same(end);
-        if (to_issue) {
+      if (--to_issue == 0) {
+        Item in = sh.in[warp];
+        if (!in.same(sh.end[warp])) {
           in.next(p, RB);
-          to_issue = in.r < p.a.n_req && in.left(end) > 0;
-          tab_end = 0;
-          w0 = 0;
+          to_issue = in.r < p.a.n_req ? in.left(sh.end[warp]) : 0;
+          tab_k = 32;
+          __syncwarp();
+          if (lane == 0) sh.in[warp] = in;
+          __syncwarp();
         }
       }
     };
-    __syncwarp();
-    for (int s = 0; s < p.stages && to_issue; ++s) issue();
+    for (int s = 0; s < p.stages && to_issue > 0; ++s) issue();
 
     for (bool more = true; more;) {
-      const int here = it.left(end);
-      const bool starts = it.u == 0, ends = it.u + here == it.units;
-      const int rows = block_rows(p, it.q.nq, it.rb, RB);
-      // query fragments: column g of every 8, channels 8 KW t4 ..
+      int here = sh.it[warp].left(sh.end[warp]);
+      const int len = sh.it[warp].q.len;
+      int tok0 = sh.it[warp].u * kUnit;
       uint32_t qf[NT][NS][KW][4];
+      int lim[NT][2], least;
+      {
+        const Item it = sh.it[warp];
+        const int rows = block_rows(p, it.q.nq, it.rb, RB);
+        // query fragments: column g of every 8, channels 8 KW t4 ..
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int rho = n * 8 + g;
+        for (int n = 0; n < NT; ++n) {
+          const int rho = n * 8 + g;
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
+          for (int s = 0; s < NS; ++s)
 #pragma unroll
-          for (int w = 0; w < KW; ++w)
+            for (int w = 0; w < KW; ++w)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) qf[n][s][w][i] = 0;
-        if (rho < rows) {
-          const unsigned x = (unsigned)it.rb * RB + rho, tok = x / (unsigned)p.n_rep;
-          const int64_t at = (it.q.begin + (int)tok) * p.a.qs.token +
-                             (it.h * p.n_rep + (int)(x - tok * p.n_rep)) * p.a.qs.head + 8 * KW * t4;
+              for (int i = 0; i < 4; ++i) qf[n][s][w][i] = 0;
+          if (rho < rows) {
+            const unsigned x = (unsigned)it.rb * RB + rho, tok = x / (unsigned)p.n_rep;
+            const int64_t at = (it.q.begin + (int)tok) * p.a.qs.token +
+                               (it.h * p.n_rep + (int)(x - tok * p.n_rep)) * p.a.qs.head + 8 * KW * t4;
 #pragma unroll
-          for (int w = 0; w < KW; ++w) {
-            if constexpr (NS == 1) {
-              const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) + at + 8 * w);
-              qf[n][0][w][0] = v.x, qf[n][0][w][1] = v.y, qf[n][0][w][2] = v.z, qf[n][0][w][3] = v.w;
-            } else {
-              const float* src = static_cast<const float*>(p.a.q) + at + 8 * w;
-              const float4 x0 = reinterpret_cast<const float4*>(src)[0], x1 = reinterpret_cast<const float4*>(src)[1];
-              const float f[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+            for (int w = 0; w < KW; ++w) {
+              if constexpr (NS == 1) {
+                const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) + at + 8 * w);
+                qf[n][0][w][0] = v.x, qf[n][0][w][1] = v.y, qf[n][0][w][2] = v.z, qf[n][0][w][3] = v.w;
+              } else {
+                const float* src = static_cast<const float*>(p.a.q) + at + 8 * w;
+                const float4 x0 = reinterpret_cast<const float4*>(src)[0], x1 = reinterpret_cast<const float4*>(src)[1];
+                const float f[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t u[NS];
-                split_pair<NS>(f[2 * i], f[2 * i + 1], u);
+                for (int i = 0; i < 4; ++i) {
+                  uint32_t u[NS];
+                  split_pair<NS>(f[2 * i], f[2 * i + 1], u);
 #pragma unroll
-                for (int s = 0; s < NS; ++s) qf[n][s][w][i] = u[s];
+                  for (int s = 0; s < NS; ++s) qf[n][s][w][i] = u[s];
+                }
               }
             }
           }
         }
+        // columns 2 t4, 2 t4 + 1 of every 8: how many keys the row sees
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) lim[n][e] = seen_by(p, it.q, it.rb * RB + n * 8 + 2 * t4 + e);
+        least = seen_by(p, it.q, it.rb * RB);
       }
-      // columns 2 t4, 2 t4 + 1 of every 8: how many keys the row sees
-      int lim[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) lim[n][e] = seen_by(p, it.q, it.rb * RB + n * 8 + 2 * t4 + e);
-      const int least = seen_by(p, it.q, it.rb * RB);
       // m: the maximum in log2 units that P is formed against; top: the raw score above
       // which it moves
       const float slack = 8.f / p.sl2;
@@ -511,14 +627,13 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
         for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
       }
 
-      for (int k = 0; k < here; ++k, ++it.u) {
+      for (; here > 0; --here, tok0 += kUnit) {
         ok = mbar_wait(bar0 + 8 * stage, (parity >> stage) & 1u, abort, p.a.status, kTimeoutNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         parity ^= 1u << stage;
         const uint32_t have = (valid >> (2 * stage)) & 3u;
         const uint8_t* base = reinterpret_cast<const uint8_t*>(slot_smem) + stage * stage_bytes;
-        const int tok0 = it.u * kUnit;
         // every row sees every token of the unit
         const bool whole = have == 3u && tok0 + kUnit <= least;
 
@@ -659,7 +774,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int tok = tok0 + i * kCacheTile + 2 * t4 + (e & 1) + (e >> 1) * 8;
-              if (!((have >> i) & 1u) || tok >= it.q.len) az[e] = 0u;
+              if (!((have >> i) & 1u) || tok >= len) az[e] = 0u;
             }
           }
           const uint32_t a0 = __byte_perm(az[0], az[1], 0x5410), z0 = __byte_perm(az[0], az[1], 0x7632);
@@ -686,7 +801,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
         // the stage has been read
         __syncwarp();
         if (++stage == p.stages) stage = 0;
-        if (to_issue) issue();
+        if (to_issue > 0) issue();
       }
       if (!ok) break;
 
@@ -697,14 +812,18 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int q = 4; q < 32; q <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], q);
+      const Item it = sh.it[warp];
+      const bool starts = it.u == 0, ends = it.u + it.left(sh.end[warp]) == it.units;
+      const int rows = block_rows(p, it.q.nq, it.rb, RB);
       Item after = it;
-      more = !it.same(end);
+      more = !it.same(sh.end[warp]);
       if (more) {
         after.next(p, RB);
-        more = after.r < p.a.n_req && after.left(end) > 0;
+        more = after.r < p.a.n_req && after.left(sh.end[warp]) > 0;
       }
       const bool whole_item = starts && ends;
-      float* const to = more ? slot_ws : slot_smem;
+      float* const to = more ? static_cast<float*>(p.a.ws) + ((size_t)blockIdx.x * WARPS + warp) * S::kFloats
+                             : slot_smem;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -742,131 +861,19 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) 
         meta[warp].h = it.h;
         meta[warp].rb = it.rb;
       }
-      it = after;
+      __syncwarp();
+      if (lane == 0) sh.it[warp] = after;
+      __syncwarp();
     }
     if (!ok && lane == 0) {
       // never leave with a copy still writing into this CTA's shared memory
       int never = 0;
       for (int s = 0; s < p.stages; ++s)
-        mbar_wait(smem_u32(&bars_[warp * 8 + s]), (parity >> s) & 1u, &never, nullptr, kDrainTimeoutNs);
+        mbar_wait(smem_u32(&sh.bars[warp * 8 + s]), (parity >> s) & 1u, &never, nullptr, kDrainTimeoutNs);
     }
   }
   __syncthreads();
-  if (*abort) {
-    if (threadIdx.x == 0) out_meta[blockIdx.x].head = out_meta[blockIdx.x].tail = 0;
-    return;
-  }
-
-  // ---- the CTA's pieces -------------------------------------------------------
-  // Pieces in order: number 2 w is warp w's head, 2 w + 1 its tail.  A tail begins a group
-  // of pieces of one item, a head that ends the item closes one.  RB D / 4 threads join a
-  // group, each 4 channels of a row; the groups are shared out among such sets of threads.
-  static_assert(2 * WARPS <= 32, "a bit per piece");
-  constexpr int V = D / 4, kSets = WARPS * 32 / (RB * V) > 0 ? WARPS * 32 / (RB * V) : 1;
-  const bool mine = lane < 2 * WARPS;
-  const int state = !mine ? 0 : (lane & 1) ? meta[lane >> 1].tail : meta[lane >> 1].head;
-  const uint32_t pieces = __ballot_sync(0xffffffffu, state != 0);
-  const uint32_t tails = __ballot_sync(0xffffffffu, (lane & 1) && state != 0);
-  const uint32_t closing = __ballot_sync(0xffffffffu, !(lane & 1) && state == 1);
-  float* const cta_slots = ws + W::cta_slots(gridDim.x) + 2 * (size_t)blockIdx.x * S::kFloats;
-  const int set = threadIdx.x / (RB * V);
-  int k = 0;
-  for (uint32_t lead = tails | (pieces & (0u - pieces)); lead; lead &= lead - 1, ++k) {
-    const uint32_t first = lead & (0u - lead), rest = lead & (lead - 1);
-    const uint32_t ids = pieces & (rest ? (rest & (0u - rest)) - first : 0u - first);
-    const bool begun = (first & tails) != 0, ended = (ids & closing) != 0;
-    const int owner = (__ffs(first) - 1) >> 1;
-    if (threadIdx.x == 0) {
-      CtaMeta* cm = &out_meta[blockIdx.x];
-      if (k == 0) {
-        cm->head = begun ? 0 : ended ? 1 : 2;
-        cm->tail = 0;
-      }
-      if (begun && !ended) {
-        cm->tail = 1;
-        cm->begin = meta[owner].begin;
-        cm->nq = meta[owner].nq;
-        cm->h = meta[owner].h;
-        cm->rb = meta[owner].rb;
-      }
-    }
-    if (kSets > 1 && k % kSets != set) continue;
-    const int rows = begun ? meta[owner].rows : meta[owner].head_rows;
-    float* const to = cta_slots + (begun ? S::kFloats : 0);
-    for (int e = threadIdx.x - (kSets > 1 ? set * RB * V : 0); e < rows * V; e += kSets > 1 ? RB * V : WARPS * 32) {
-      const int row = e / V, ch = (e - row * V) * 4;
-      Acc acc;
-      for (uint32_t b = ids; b; b &= b - 1) {
-        const int id = __ffs(b) - 1, w = id >> 1;
-        const float* s = (id & 1) == 0 && meta[w].head_global
-                             ? ws + ((size_t)blockIdx.x * WARPS + w) * S::kFloats
-                             : reinterpret_cast<const float*>(smem + (size_t)w * p.stages * stage_bytes);
-        acc.add(S::ml(s)[row], *reinterpret_cast<const float4*>(s + row * D + ch));
-      }
-      if (begun && ended) {
-        const PieceMeta& m = meta[owner];
-        write_out<D>(p, out_row(p, m.begin, m.h, m.rb, RB, row), ch, acc.m, acc.l, acc.o);
-      } else {
-        *reinterpret_cast<float4*>(to + row * D + ch) = acc.o;
-        if (ch == 0) S::ml(to)[row] = make_float2(acc.m, acc.l);
-      }
-    }
-  }
-  if (threadIdx.x == 0 && pieces == 0) out_meta[blockIdx.x].head = out_meta[blockIdx.x].tail = 0;
-}
-
-// Items that cross CTAs: CTA c of this grid joins the one that CTA c of the first began,
-// c's tail and the heads of the CTAs behind it up to the one that ends the item.  Few
-// rows leave threads over: those share the pieces and meet in shared memory.
-constexpr int kJoinThreads = 256;
-template <int D, int RB, int WARPS>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
-  using S = Slot<D, RB>;
-  using W = Work<D, RB, WARPS>;
-  __shared__ Acc meet[kJoinThreads];
-  griddep_wait();
-  const float* const ws = static_cast<const float*>(p.a.ws);
-  const CtaMeta* meta = reinterpret_cast<const CtaMeta*>(ws + W::meta(gridDim.x));
-  const int c = blockIdx.x, lane = threadIdx.x & 31;
-  const CtaMeta cm = meta[c];
-  if (!cm.tail) return;
-  int n = 1;
-  for (int i = c + 1; i < (int)gridDim.x; i += 32) {
-    const bool end = i + lane < (int)gridDim.x && meta[i + lane].head != 2;
-    const uint32_t b = __ballot_sync(0xffffffffu, end);
-    n = i - c + (b ? __ffs(b) : 32);
-    if (b) break;
-  }
-  n = min(n, (int)gridDim.x - c);
-  const float* const slots = ws + W::cta_slots(gridDim.x) + 2 * (size_t)c * S::kFloats;
-  const int rows = block_rows(p, cm.nq, cm.rb, RB), parts = rows * (D / 4);
-  const int shares = max(1, kJoinThreads / parts), share = threadIdx.x / parts;
-  for (int e = shares > 1 ? threadIdx.x % parts : threadIdx.x; e < parts; e += shares > 1 ? parts : kJoinThreads) {
-    const int row = e / (D / 4), ch = (e - row * (D / 4)) * 4;
-    Acc acc;
-    if (shares == 1 || share < shares) {
-#pragma unroll 4
-      for (int i = shares > 1 ? share : 0; i < n; i += shares) {
-        const float* s = slots + (i ? 2 * (size_t)i : 1) * S::kFloats;
-        acc.add(S::ml(s)[row], *reinterpret_cast<const float4*>(s + row * D + ch));
-      }
-    }
-    if (shares > 1) {
-      meet[threadIdx.x] = acc;
-    } else {
-      write_out<D>(p, out_row(p, cm.begin, cm.h, cm.rb, RB, row), ch, acc.m, acc.l, acc.o);
-    }
-  }
-  if (shares == 1) return;
-  __syncthreads();
-  if ((int)threadIdx.x >= parts) return;
-  Acc acc = meet[threadIdx.x];
-  for (int i = 1; i < shares; ++i) {
-    const Acc& x = meet[threadIdx.x + i * parts];
-    acc.add(make_float2(x.m, x.l), x.o);
-  }
-  const int row = threadIdx.x / (D / 4), ch = (threadIdx.x - row * (D / 4)) * 4;
-  write_out<D>(p, out_row(p, cm.begin, cm.h, cm.rb, RB, row), ch, acc.m, acc.l, acc.o);
+  finish<D, RB, WARPS>(p, sh, smem, stage_bytes);
 }
 
 // ---------------------------------------------------------------------------
@@ -877,7 +884,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
 template <int D, int G, int NT, int NS, int WARPS, int MINB>
 struct Variant {
   static constexpr int kCtas = kMaxSms * MINB;
-  static constexpr int kStatic = 4096;  // static shared memory and what the system keeps
+  static constexpr int kStatic = 6144;  // room for the static shared memory
+  static_assert(sizeof(Shared<WARPS>) <= kStatic, "shared memory");
   using W = Work<D, 8 * NT, WARPS>;
   static size_t workspace() { return W::meta(kCtas) * sizeof(float) + kCtas * sizeof(CtaMeta); }
   static cudaError_t launch(Params p, int sms, cudaStream_t st) {
@@ -899,18 +907,17 @@ struct Variant {
       if (dev < 128) set[dev >> 6].fetch_or(bit);
     }
     const int grid = sms * MINB < kCtas ? sms * MINB : kCtas;
-    kern<<<grid, WARPS * 32, p.stages * stage, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = kJoinThreads;
+    cfg.blockDim = WARPS * 32;
+    cfg.dynamicSmemBytes = (size_t)p.stages * stage;
     cfg.stream = st;
     cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
+    at.id = cudaLaunchAttributeCooperative;  // the CTAs meet at a grid barrier
+    at.val.cooperative = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, 8 * NT, WARPS>, p);
+    return cudaLaunchKernelEx(&cfg, kern, p);
   }
 };
 template <int D, int G>
@@ -947,6 +954,9 @@ cudaError_t launch_cache_attn(const Cache& c, const CacheAttnArgs& a, cudaStream
   p.n_rep = c.Hq / c.Hkv;
   p.stages = 0;
   p.per_sum = (a.n_req + cattn::kSums - 1) / cattn::kSums;
+  p.page_tiles = c.page / kCacheTile;
+  p.unit_in_page = c.page % cattn::kUnit == 0;
+  p.page_bytes = c.Hkv * c.block_bytes();
   p.ones = kOnes;
   p.sl2 = c.scale * 1.44269504088896340736f;
   int dev = 0, sms = 0;
