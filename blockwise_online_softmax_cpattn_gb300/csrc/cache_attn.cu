@@ -294,7 +294,7 @@ struct Shared {
 // The run of this warp: its first unit and the next warp's, into sh.  (Apart from the kernel,
 // as the last part below is, so that their registers and the main loop's do not mix.)
 template <int RB, int WARPS>
-__device__ __noinline__ void find_run(const Params& p, Shared<WARPS>& sh) {
+__device__ __forceinline__ void find_run(const Params& p, Shared<WARPS>& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int64_t total;
   {
@@ -362,7 +362,7 @@ __device__ __noinline__ void find_run(const Params& p, Shared<WARPS>& sh) {
 
 // The end of the kernel: joins the CTA's open pieces, then the items that cross CTAs.
 template <int D, int RB, int WARPS>
-__device__ __noinline__ void finish(const Params& p, const Shared<WARPS>& sh, uint8_t* smem, int stage_bytes) {
+__device__ __forceinline__ void finish(const Params& p, const Shared<WARPS>& sh, uint8_t* smem, int stage_bytes) {
   using S = Slot<D, RB>;
   using W = Work<D, RB, WARPS>;
   const int lane = threadIdx.x & 31;
@@ -470,7 +470,7 @@ __device__ __noinline__ void finish(const Params& p, const Shared<WARPS>& sh, ui
 }
 
 template <int D, int G, int NT, int NS, int WARPS, int MINB>
-__global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const Params p) {
+__global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_constant__ Params p) {
   constexpr int RB = 8 * NT;
   constexpr int KW = D / 32;    // words of a K row per lane (channels 8 KW t4 ..)
   constexpr int VW = D / 64;    // words of a V row per lane (channels 8 VW g ..)
