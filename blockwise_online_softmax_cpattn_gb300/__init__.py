@@ -149,12 +149,25 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_current_stream = None  # () -> raw current stream, once torch's CUDA side is up
+
+
 def _stream(stream) -> Optional[int]:
+    global _current_stream
     if stream is None:
+        if _current_stream is not None:
+            return _current_stream()
         import torch
-        if torch.cuda.is_available():
-            return torch.cuda.current_stream().cuda_stream
-        return None
+        if not torch.cuda.is_available():
+            return None
+        raw = torch.cuda.current_stream().cuda_stream
+        # the same number without a Stream object around it: a call of a few microseconds
+        # is launch-bound on the host
+        get_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        get_device = getattr(torch._C, "_cuda_getDevice", None)
+        if get_raw is not None and get_device is not None:
+            _current_stream = lambda: get_raw(get_device())  # noqa: E731
+        return raw
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -300,16 +313,22 @@ def cpattn_cache_plan_workspace(desc, n_req) -> int:
     return _lib.cpattn_cache_plan_workspace(ctypes.byref(desc), n_req)
 
 
-_DTYPE_NAMES = {F32: "torch.float32", BF16: "torch.bfloat16", "i32": "torch.int32"}
+_dtypes = {}  # F32, BF16, "i32" -> torch dtype (torch is imported with the first tensor)
+
+
+def _dtype(key):
+    if not _dtypes:
+        import torch
+        _dtypes.update({F32: torch.float32, BF16: torch.bfloat16, "i32": torch.int32})
+    return _dtypes.get(key)
 
 
 def _typed(x, n, dtype, what) -> Optional[int]:
     """Pointer of a contiguous tensor of the type with at least n numbers."""
-    if x is None or isinstance(x, int):
+    if x is None or type(x) is int:
         return x
-    name = _DTYPE_NAMES[dtype]
-    if str(x.dtype) != name or not x.is_contiguous() or x.numel() < n:
-        raise ValueError(f"{what} must be contiguous {name} with at least {n} entries")
+    if x.dtype is not _dtype(dtype) or x.numel() < n or not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {_dtype(dtype)} with at least {n} entries")
     return x.data_ptr()
 
 
@@ -320,20 +339,23 @@ def _i32(x, n, what) -> Optional[int]:
 def _rows(x, n, heads, desc, what):
     """(pointer, token stride, head stride) of a [n, heads, D] tensor of desc.dtype with
     contiguous channels; a raw pointer stands for a contiguous one."""
-    if x is None or isinstance(x, int):
-        return x, heads * desc.D, desc.D
-    if (x.dim() != 3 or x.shape[0] < n or x.shape[1] != heads or x.shape[2] != desc.D or
-            x.stride(2) != 1 or str(x.dtype) != _DTYPE_NAMES.get(desc.dtype)):
+    D = desc.D
+    if x is None or type(x) is int:
+        return x, heads * D, D
+    shape, stride = x.shape, x.stride()
+    if (x.dtype is not _dtype(desc.dtype) or len(shape) != 3 or shape[0] < n or shape[1] != heads or
+            shape[2] != D or stride[2] != 1):
         raise ValueError(f"{what} must be [n_tokens, heads, D] of the descriptor's dtype with "
                          "contiguous channels")
-    return x.data_ptr(), x.stride(0), x.stride(1)
+    return x.data_ptr(), stride[0], stride[1]
 
 
 def _cache(x, desc) -> Optional[int]:
-    if x is not None and not isinstance(x, int):
-        if x.numel() * x.element_size() < cpattn_cache_bytes(desc):
-            raise ValueError("the cache is smaller than cpattn_cache_bytes(desc)")
-    return _ptr(x)
+    if x is None or type(x) is int:
+        return x
+    if x.numel() * x.element_size() < cpattn_cache_bytes(desc) or not x.is_contiguous():
+        raise ValueError("the cache must be contiguous and hold cpattn_cache_bytes(desc) bytes")
+    return x.data_ptr()
 
 
 def cpattn_cache_plan(desc, n_req, max_pages, len_old, len_new, table, free_list, n_free, n_free_out,

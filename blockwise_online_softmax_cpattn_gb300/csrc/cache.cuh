@@ -18,6 +18,18 @@ constexpr int kCacheTile = 16;            // tokens per tile (the K dimension of
 constexpr float kCacheHuge = 0x1p120f;    // stored values are held within +- this
 constexpr float kCacheTiny = 0x1p-100f;   // a group whose a is below this has a = 0
 
+// n / d for 0 <= n < 2^31 by a multiplication: with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (hi(m n) + n) >> s.
+struct Divider {
+  uint32_t d, m, s;
+  static Divider of(uint32_t d) {
+    uint32_t s = 0;
+    while ((1u << s) < d) ++s;
+    return {d, (uint32_t)((((uint64_t)1 << s) - d << 32) / d + 1), s};
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
+};
+
 struct Cache {
   int Hq, Hkv, D, G, page, n_pages;
   int bf16;        // q, k, v: 1 bf16, 0 f32
@@ -89,6 +101,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float d;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));

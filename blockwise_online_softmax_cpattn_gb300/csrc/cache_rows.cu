@@ -1,110 +1,176 @@
 // Rows into the 4-bit cache and out of it.
 //
-// Both are copies that convert: a thread takes 8 channels of one row (16 or 32 bytes of
-// a tensor, one 32-bit word of codes), the D / 8 threads of a row sit side by side in a
+// Both are copies that convert: a thread takes 8 channels of a row (16 or 32 bytes of a
+// tensor, one 32-bit word of codes), the D / 8 threads of a row sit side by side in a
 // warp, and the D / G groups of the row are runs of G / 8 of them, which find their
-// minimum and maximum with shuffles.  Bound by HBM: 2 (or 4) bytes in and 0.56 out a
-// channel at group 64.
+// minimum and maximum with shuffles.  Each thread does so for kRows tokens, all loads
+// first.  Bound by HBM: 2 (or 4) bytes in and 0.56 out a channel at group 64, and the
+// other way round; close behind, appending, by its instructions, so pairs of channels go
+// through the two-lane float32 operations.
 #include "cache.cuh"
 
 namespace cpattn {
 namespace rows {
 
 constexpr int kThreads = 256;
+// tokens a thread works on: 64 bytes of loads in flight, 2048 threads an SM
+template <typename T>
+constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
 
-// 8 channels of a row as floats
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  x[0] = lo_f(a.x), x[1] = hi_f(a.x), x[2] = lo_f(a.y), x[3] = hi_f(a.y);
-  x[4] = lo_f(a.z), x[5] = hi_f(a.z), x[6] = lo_f(a.w), x[7] = hi_f(a.w);
-}
+
+// 8 channels of a row
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void floats(float2 (&x)[4]) const {
+    x[0] = make_float2(lo_f(w.x), hi_f(w.x));
+    x[1] = make_float2(lo_f(w.y), hi_f(w.y));
+    x[2] = make_float2(lo_f(w.z), hi_f(w.z));
+    x[3] = make_float2(lo_f(w.w), hi_f(w.w));
+  }
+};
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void floats(float2 (&x)[4]) const {
+    x[0] = make_float2(a.x, a.y);
+    x[1] = make_float2(a.z, a.w);
+    x[2] = make_float2(b.x, b.y);
+    x[3] = make_float2(b.z, b.w);
+  }
+};
 
 // The code word of 8 channels (channel 2p + e in bits 4(p + 4e)) and the group's (a, z);
-// `lanes` threads share a group.  The code is the number of borders a (33 + 2j) / 32
-// that d = x - z is above: j near 16 d / a - 16.5 is found by a multiplication with the
-// rounded 16 / a, at most one off, and d is then compared with border j itself, whose
-// product is exact in float32 (8 + 6 bits).
-__device__ __forceinline__ uint32_t quantise8(float (&x)[8], int lanes, uint32_t& az, int* status) {
-  float lo = x[0], hi = x[0];
+// LANES threads share a group.  The code is the number of borders a (33 + 2j) / 32 that
+// d = x - z is above.  16 d / a - 16.5, held to [0, 14] and rounded, is a j such that the
+// code is j or j + 1 (the float32 error of 16 / a matters nowhere near); d is compared with
+// border j itself, whose product is exact in float32 (8 + 6 bits), so the code is exact.
+// The four codes of a half word are summed as float32 numbers: below 2^16, so exactly.
+template <int LANES>
+__device__ __forceinline__ uint32_t quantise8(float2 (&x)[4], uint32_t& az, int* status) {
+  float lo = min_nan(x[0].x, x[0].y), hi = max_nan(x[0].x, x[0].y);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = min_nan(lo, x[i]);
-    hi = max_nan(hi, x[i]);
+  for (int i = 1; i < 4; ++i) {
+    lo = min3_nan(lo, x[i].x, x[i].y);
+    hi = max3_nan(hi, x[i].x, x[i].y);
   }
   if (!(lo >= -kCacheHuge && hi <= kCacheHuge)) {  // also true of a NaN
     latch_status(status, kStatusRange);
+    lo = INFINITY;
+    hi = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = isnan(x[i]) ? 0.f : fminf(fmaxf(x[i], -kCacheHuge), kCacheHuge);
-      lo = i == 0 ? x[0] : fminf(lo, x[i]);
-      hi = i == 0 ? x[0] : fmaxf(hi, x[i]);
+    for (int i = 0; i < 4; ++i) {
+      x[i].x = isnan(x[i].x) ? 0.f : fminf(fmaxf(x[i].x, -kCacheHuge), kCacheHuge);
+      x[i].y = isnan(x[i].y) ? 0.f : fminf(fmaxf(x[i].y, -kCacheHuge), kCacheHuge);
+      lo = fminf(lo, fminf(x[i].x, x[i].y));
+      hi = fmaxf(hi, fmaxf(x[i].x, x[i].y));
     }
   }
-  for (int m = 1; m < lanes; m <<= 1) {
+#pragma unroll
+  for (int m = 1; m < LANES; m <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
   }
   const __nv_bfloat16 ab = __float2bfloat16_rn(__fmul_rn(hi - lo, 16.f / 15.f));
   float a = __bfloat162float(ab);
-  if (a < kCacheTiny) a = 0.f;
+  const bool flat = a < kCacheTiny;
+  if (flat) a = 0.f;
   const __nv_bfloat16 zb = __float2bfloat16_rn(__fsub_rn(lo, a));
-  const float z = __bfloat162float(zb);
-  az = (a == 0.f ? 0u : (uint32_t)__bfloat16_as_ushort(ab)) | (uint32_t)__bfloat16_as_ushort(zb) << 16;
-  if (a == 0.f) return 0u;
-  const float r = 16.f / a, a16 = a * 0.0625f, b0 = a * 1.03125f;
-  uint32_t w = 0;
+  const float nz = -__bfloat162float(zb);
+  az = (flat ? 0u : (uint32_t)__bfloat16_as_ushort(ab)) | (uint32_t)__bfloat16_as_ushort(zb) << 16;
+  const float r = __fdividef(16.f / 14.f, a);  // of a flat group not used
+  const float2 a16 = make_float2(a * 0.0625f, a * 0.0625f), b0 = make_float2(a * 1.03125f, a * 1.03125f);
+  const float2 magic = make_float2(12582912.f, 12582912.f), nmagic = make_float2(-12582912.f, -12582912.f);
+  const float2 k14 = make_float2(14.f, 14.f);
+  float2 sum = make_float2(0.f, 0.f);
+  float scale = 1.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = __fsub_rn(x[i], z);
-    const float t = fminf(fmaxf(fmaf(d, r, -16.5f), 0.f), 14.f);
-    const float m = t + 12582912.f;  // rounds t to a whole number j, in the low bits too
-    const float j = m - 12582912.f;
-    const uint32_t code = (__float_as_uint(m) & 15u) + (d > fmaf(j, a16, b0) ? 1u : 0u);
-    w |= code << (4 * ((i >> 1) + 4 * (i & 1)));
+  for (int i = 0; i < 4; ++i) {
+    const float2 d = add2(x[i], make_float2(nz, nz));
+    const float2 t = make_float2(__saturatef(fmaf(d.x, r, -16.5f / 14.f)), __saturatef(fmaf(d.y, r, -16.5f / 14.f)));
+    const float2 j = add2(fma2(t, k14, magic), nmagic);  // rounded to a whole number
+    const float2 border = fma2(j, a16, b0);
+    const float2 code = add2(j, make_float2(d.x > border.x ? 1.f : 0.f, d.y > border.y ? 1.f : 0.f));
+    sum = fma2(code, make_float2(scale, scale), sum);
+    scale *= 16.f;
   }
-  return w;
+  const uint32_t w = __byte_perm(__float_as_uint(sum.x + 8388608.f), __float_as_uint(sum.y + 8388608.f), 0x5410);
+  return flat ? 0u : w;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    append_kernel(Cache c, int64_t n_rows, int n, const T* k, RowStrides ks, const T* v, RowStrides vs,
-                  const int* slots, uint8_t* cache, int* status) {
-  const int tpr = c.D / 8;  // threads per row
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t row = id / tpr;
-  const int w = (int)(id % tpr);
-  // rows of tokens side by side, then heads, then keys and values
-  const int64_t hv = row / n;
-  const int tok = (int)(row - hv * n);
-  const int is_v = hv >= c.Hkv;
-  const int h = (int)hv - is_v * c.Hkv;
-  const bool in = row < n_rows;
-  const int slot = in ? slots[tok] : -1;
-  const bool live = slot >= 0 && slot < c.slots();
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (live) {
-    const RowStrides s = is_v ? vs : ks;
-    load8((is_v ? v : k) + tok * s.token + h * s.head + w * 8, x);
+// (16.f / 15.f and the roundings above are the format's; add2 rounds to nearest.)
+
+// The cache of one K/V head's keys or values (block: that of page 0).
+template <int D, int G>
+struct Rows {
+  static constexpr int kHalf = kCacheTile * (D / 2 + 4 * (D / G));
+  Divider page;
+  int64_t page_bytes;   // of all heads
+  int64_t block_bytes;
+  unsigned slots;
+  int heads;
+  static Rows of(const Cache& c) {
+    return {Divider::of(c.page), c.Hkv * c.block_bytes(), c.block_bytes(), (unsigned)c.slots(), c.Hkv};
   }
-  uint32_t az;
-  uint32_t word = quantise8(x, c.G / 8, az, status);  // whole warps: shuffles inside
-  if (!live) return;
-  const int pg = slot / c.page, off = slot - pg * c.page;
-  const int t = off % kCacheTile;
-  uint8_t* half = cache + c.tile_at(pg, h, off / kCacheTile) + (is_v ? c.half_tile() : 0);
-  const int r = is_v ? cache_v_row(t) : t;
-  if (!is_v) word = __funnelshift_l(word, word, 3);
-  reinterpret_cast<uint32_t*>(half)[r * tpr + w] = word;
-  const int lanes = c.G / 8;
-  if (w % lanes == 0)
-    reinterpret_cast<uint32_t*>(half + kCacheTile * c.row_bytes())[r * c.groups() + w / lanes] = az;
+  __device__ __forceinline__ int64_t first(int h, int is_v) const { return h * block_bytes + is_v * kHalf; }
+  // the half tile of a slot, from the first, and the slot's row in it
+  __device__ __forceinline__ int64_t half(int slot, int is_v, int& row) const {
+    const int pg = page.div(slot), off = slot - pg * (int)page.d, t = off & (kCacheTile - 1);
+    row = is_v ? cache_v_row(t) : t;
+    return pg * page_bytes + (off / kCacheTile) * (2 * kHalf);
+  }
+};
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kThreads)
+    append_kernel(const Rows<D, G> c, int n, const T* k, RowStrides ks, const T* v, RowStrides vs,
+                  const int* slots, uint8_t* cache, int* status) {
+  constexpr int TPR = D / 8, LANES = G / 8, STEP = kThreads / TPR, N = kRows<T>;
+  const int w = threadIdx.x % TPR;
+  const int is_v = blockIdx.y >= (unsigned)c.heads;
+  const int h = blockIdx.y - is_v * c.heads;
+  const RowStrides st = is_v ? vs : ks;
+  const T* src = (is_v ? v : k) + h * st.head + w * 8;
+  // tokens of a CTA: STEP neighbours at a time
+  const int64_t tok0 = (int64_t)blockIdx.x * (STEP * N) + threadIdx.x / TPR;
+  int slot[N];
+  Raw<T> raw[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t tok = tok0 + i * STEP;
+    slot[i] = tok < n ? slots[tok] : -1;
+    if ((unsigned)slot[i] >= c.slots) slot[i] = -1;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    raw[i].zero();
+    if (slot[i] >= 0) raw[i].load(src + (tok0 + i * STEP) * st.token);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float2 x[4];
+    raw[i].floats(x);
+    uint32_t az;
+    uint32_t word = quantise8<LANES>(x, az, status);  // whole warps: shuffles inside
+    if (slot[i] < 0) continue;
+    int r;
+    uint8_t* half = cache + c.first(h, is_v) + c.half(slot[i], is_v, r);
+    if (!is_v) word = __funnelshift_l(word, word, 3);
+    reinterpret_cast<uint32_t*>(half)[r * TPR + w] = word;
+    if (w % LANES == 0)
+      reinterpret_cast<uint32_t*>(half + kCacheTile * (D / 2))[r * (D / G) + w / LANES] = az;
+  }
 }
 
 __device__ __forceinline__ void store8(float* p, const uint32_t (&u)[4]) {
@@ -115,86 +181,99 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const uint32_t (&u)[4])
   *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-template <typename T>
+template <typename T, int D, int G>
 __global__ void __launch_bounds__(kThreads)
-    read_kernel(Cache c, int64_t n_rows, int n, const int* slots, const uint8_t* cache, T* k,
-                RowStrides ks, T* v, RowStrides vs) {
-  const int tpr = c.D / 8;
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t row = id / tpr;
-  if (row >= n_rows) return;
-  const int w = (int)(id % tpr);
-  const int64_t hv = row / n;
-  const int tok = (int)(row - hv * n);
-  const int is_v = hv >= c.Hkv;
-  const int h = (int)hv - is_v * c.Hkv;
-  const int slot = slots[tok];
-  uint32_t u[4] = {0u, 0u, 0u, 0u};
-  if (slot >= 0 && slot < c.slots()) {
-    const int pg = slot / c.page, off = slot - pg * c.page;
-    const int t = off % kCacheTile;
-    const uint8_t* half = cache + c.tile_at(pg, h, off / kCacheTile) + (is_v ? c.half_tile() : 0);
-    const int r = is_v ? cache_v_row(t) : t;
-    const uint32_t word = reinterpret_cast<const uint32_t*>(half)[r * tpr + w];
-    const uint32_t az =
-        reinterpret_cast<const uint32_t*>(half + kCacheTile * c.row_bytes())[r * c.groups() + w * 8 / c.G];
-    if (is_v) codes_to_bf16<false>(word, kOnes, u);
-    else codes_to_bf16<true>(word, kOnes, u);
+    read_kernel(const Rows<D, G> c, int n, const int* slots, const uint8_t* cache, T* k, RowStrides ks,
+                T* v, RowStrides vs) {
+  constexpr int TPR = D / 8, LANES = G / 8, STEP = kThreads / TPR, N = 4;
+  const int w = threadIdx.x % TPR;
+  const int is_v = blockIdx.y >= (unsigned)c.heads;
+  const int h = blockIdx.y - is_v * c.heads;
+  const RowStrides st = is_v ? vs : ks;
+  T* dst = (is_v ? v : k) + h * st.head + w * 8;
+  const int64_t tok0 = (int64_t)blockIdx.x * (STEP * N) + threadIdx.x / TPR;
+  int slot[N];
+  uint32_t word[N], az[N];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) u[p] = bf16x2_fma(u[p], az_a2(az), az_z2(az));
+  for (int i = 0; i < N; ++i) {
+    const int64_t tok = tok0 + i * STEP;
+    slot[i] = tok < n ? slots[tok] : -1;
   }
-  const RowStrides s = is_v ? vs : ks;
-  store8((is_v ? v : k) + tok * s.token + h * s.head + w * 8, u);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    word[i] = az[i] = 0u;
+    if ((unsigned)slot[i] < c.slots) {
+      int r;
+      const uint8_t* half = cache + c.first(h, is_v) + c.half(slot[i], is_v, r);
+      word[i] = reinterpret_cast<const uint32_t*>(half)[r * TPR + w];
+      az[i] = reinterpret_cast<const uint32_t*>(half + kCacheTile * (D / 2))[r * (D / G) + w / LANES];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t tok = tok0 + i * STEP;
+    if (tok >= n) return;
+    uint32_t u[4];
+    if (is_v) codes_to_bf16<false>(word[i], kOnes, u);
+    else codes_to_bf16<true>(word[i], kOnes, u);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) u[p] = bf16x2_fma(u[p], az_a2(az[i]), az_z2(az[i]));  // (0, 0): zeros
+    store8(dst + tok * st.token, u);
+  }
+}
+
+// f(T, D, G) for the cache's
+template <typename F>
+static cudaError_t dispatch(const Cache& c, F f) {
+  auto by_format = [&](auto t) {
+    using T = decltype(t);
+    if (c.D == 128) {
+      if (c.G == 128) return f(T(), std::integral_constant<int, 128>(), std::integral_constant<int, 128>());
+      if (c.G == 64) return f(T(), std::integral_constant<int, 128>(), std::integral_constant<int, 64>());
+      return f(T(), std::integral_constant<int, 128>(), std::integral_constant<int, 32>());
+    }
+    if (c.G == 64) return f(T(), std::integral_constant<int, 64>(), std::integral_constant<int, 64>());
+    return f(T(), std::integral_constant<int, 64>(), std::integral_constant<int, 32>());
+  };
+  return c.bf16 ? by_format(__nv_bfloat16()) : by_format(0.f);
+}
+
+static dim3 grid_of(const Cache& c, int n, int rows) {
+  const int step = kThreads / (c.D / 8) * rows;
+  return dim3((unsigned)(((int64_t)n + step - 1) / step), 2 * c.Hkv);
 }
 
 }  // namespace rows
 
-static cudaError_t row_grid(const Cache& c, int n, int64_t* rows_out, unsigned* grid) {
-  const int64_t n_rows = (int64_t)2 * c.Hkv * n;
-  const int64_t blocks = (n_rows * (c.D / 8) + rows::kThreads - 1) / rows::kThreads;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  *rows_out = n_rows;
-  *grid = (unsigned)blocks;
-  return cudaSuccess;
-}
-
 cudaError_t launch_cache_append(const Cache& c, int n, const void* k, RowStrides ks, const void* v,
                                 RowStrides vs, const int* slots, void* cache, int* status,
                                 cudaStream_t st) {
-  int64_t n_rows;
-  unsigned grid;
-  cudaError_t e = row_grid(c, n, &n_rows, &grid);
-  if (e != cudaSuccess) return e;
   timing_begin("cache_append", st);
-  if (c.bf16)
-    rows::append_kernel<<<grid, rows::kThreads, 0, st>>>(
-        c, n_rows, n, static_cast<const __nv_bfloat16*>(k), ks, static_cast<const __nv_bfloat16*>(v),
-        vs, slots, static_cast<uint8_t*>(cache), status);
-  else
-    rows::append_kernel<<<grid, rows::kThreads, 0, st>>>(
-        c, n_rows, n, static_cast<const float*>(k), ks, static_cast<const float*>(v), vs, slots,
-        static_cast<uint8_t*>(cache), status);
+  const cudaError_t e = rows::dispatch(c, [&](auto t, auto d, auto g) {
+    using T = decltype(t);
+    rows::append_kernel<T, decltype(d)::value, decltype(g)::value>
+        <<<rows::grid_of(c, n, rows::kRows<T>), rows::kThreads, 0, st>>>(
+            rows::Rows<decltype(d)::value, decltype(g)::value>::of(c), n, static_cast<const T*>(k), ks, static_cast<const T*>(v), vs, slots,
+            static_cast<uint8_t*>(cache), status);
+    return cudaGetLastError();
+  });
   timing_end(st);
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_cache_read(const Cache& c, int n, const int* slots, const void* cache, void* k,
                               RowStrides ks, void* v, RowStrides vs, cudaStream_t st) {
-  int64_t n_rows;
-  unsigned grid;
-  cudaError_t e = row_grid(c, n, &n_rows, &grid);
-  if (e != cudaSuccess) return e;
   timing_begin("cache_read", st);
-  const uint8_t* cb = static_cast<const uint8_t*>(cache);
-  if (c.bf16)
-    rows::read_kernel<<<grid, rows::kThreads, 0, st>>>(c, n_rows, n, slots, cb,
-                                                       static_cast<__nv_bfloat16*>(k), ks,
-                                                       static_cast<__nv_bfloat16*>(v), vs);
-  else
-    rows::read_kernel<<<grid, rows::kThreads, 0, st>>>(c, n_rows, n, slots, cb, static_cast<float*>(k),
-                                                       ks, static_cast<float*>(v), vs);
+  const cudaError_t e = rows::dispatch(c, [&](auto t, auto d, auto g) {
+    using T = decltype(t);
+    rows::read_kernel<T, decltype(d)::value, decltype(g)::value>
+        <<<rows::grid_of(c, n, 4), rows::kThreads, 0, st>>>(rows::Rows<decltype(d)::value, decltype(g)::value>::of(c), n, slots,
+                                                              static_cast<const uint8_t*>(cache),
+                                                              static_cast<T*>(k), ks, static_cast<T*>(v), vs);
+    return cudaGetLastError();
+  });
   timing_end(st);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace cpattn
