@@ -6,15 +6,10 @@
 // kernel's two bounds are the memory and, close behind, the instructions that unpack
 // codes.  What it does about each:
 //
-//   Work.  An item is 8 NT query rows (new tokens x the heads of a K/V group) of one
-//   request and K/V head; it is cut into units of 32 cached tokens.  The units of all
-//   items are numbered through and every warp on the GPU takes an equal run of them, so
-//   neither ragged lengths nor few requests leave SMs idle, and nothing about lengths
-//   has to be known on the host.  A run ends anywhere: pieces of an item are joined by
-//   the (O, m, l) merge, first among the warps of a CTA in shared memory, then, for
-//   items that cross CTAs, after a grid barrier from the workspace (a second launch in its
-//   place cost 4 to 6 us a call).  Pieces are joined in their order: the result is the same
-//   every time.
+//   Work.  Every warp on the GPU takes an equal run of the line of items (8 NT rows each,
+//   units of 32 tokens).  Pieces are joined first among the warps of a CTA in shared
+//   memory, then, for items that cross CTAs, behind a grid barrier from the workspace (a
+//   second launch in its place cost 2 us more a call).
 //
 //   Loads.  A tile of 16 tokens of one K/V head is contiguous (codes and their (a, z)):
 //   one bulk copy, of two tiles where a page holds both.  Each warp keeps a ring of
@@ -41,143 +36,14 @@
 #include <algorithm>
 #include <atomic>
 
-#include "cache.cuh"
+#include "cache_work.cuh"
 
 namespace cpattn {
 namespace cattn {
 
 constexpr int kUnit = 32;            // cached tokens of a unit: two tiles
-constexpr int kItemCost = 3;         // an item's start and end, in units (see below)
-constexpr int kSums = 256;           // entries of the prefix sums over requests
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr uint64_t kDrainTimeoutNs = 200000000ull;
-constexpr int kMaxSms = 160;         // of a GB300, and a few: the grid's and the workspace's size
+constexpr int kItemCost = 3;         // an item's start and end, in units
 
-struct Params {
-  Cache c;
-  CacheAttnArgs a;
-  int n_rep, stages;
-  int per_sum;                       // requests per entry of the prefix sums
-  int page_tiles, unit_in_page;      // tiles of a page; units do not straddle pages
-  int64_t page_bytes;                // of all K/V heads
-  float sl2;                         // scale * log2(e)
-  uint32_t ones;                     // kOnes
-};
-
-// ---------------------------------------------------------------------------
-// items
-// ---------------------------------------------------------------------------
-struct Req {
-  int begin, nq, len;
-};
-__device__ __forceinline__ Req request(const Params& p, int r) {
-  Req q;
-  const int b = min(max(p.a.q_start[r], 0), p.a.n_tokens);
-  const int e = min(max(p.a.q_start[r + 1], b), p.a.n_tokens);
-  q.begin = b;
-  q.nq = e - b;
-  q.len = min(max(p.a.kv_len[r], 0), p.a.max_pages * p.c.page);
-  return q;
-}
-// Rows of q are fewer than 2^31 (checked on the host), and so are a request's.
-// cached tokens that row x of the request sees
-__device__ __forceinline__ int seen_by(const Params& p, const Req& q, int x) {
-  if (!p.c.causal) return q.len;
-  return min(max(q.len - q.nq + (int)((unsigned)x / (unsigned)p.n_rep) + 1, 0), q.len);
-}
-// ... that row block rb (RB rows) sees, and its units
-__device__ __forceinline__ int block_seen(const Params& p, const Req& q, int rb, int RB) {
-  if (!p.c.causal) return q.len;
-  const int last = (int)min((int64_t)q.nq * p.n_rep, (int64_t)(rb + 1) * RB) - 1;
-  return seen_by(p, q, last);
-}
-__device__ __forceinline__ int units_of(int seen) { return max(1, (seen + kUnit - 1) / kUnit); }
-__device__ __forceinline__ int blocks_of(const Params& p, const Req& q, int RB) {
-  return (int)(((unsigned)(q.nq * p.n_rep) + RB - 1) / RB);
-}
-// cost of one K/V head of request r: its units and kItemCost for every item
-__device__ __forceinline__ int64_t head_cost(const Params& p, const Req& q, int RB) {
-  const int nb = blocks_of(p, q, RB);
-  int64_t n = 0;
-  for (int b = 0; b < nb; ++b) n += units_of(block_seen(p, q, b, RB)) + kItemCost;
-  return n;
-}
-
-// i / n of x, rounded down (the 32-bit division where it does: n, i < 2^8)
-__device__ __forceinline__ int64_t part_of(int64_t x, int i, int n) {
-  if (x < (1 << 24)) return (unsigned)x * (unsigned)i / (unsigned)n;
-  return x * i / n;
-}
-
-// Request, K/V head and row block of an item, and a unit in it.  Items follow each other by
-// row block, K/V head, request.
-struct Place {
-  int r, h, rb, u;
-};
-struct Item : Place {
-  Req q;
-  int seen, units;
-  __device__ __forceinline__ void settle(const Params& p, int RB) {
-    seen = block_seen(p, q, rb, RB);
-    units = units_of(seen);
-  }
-  __device__ __forceinline__ bool same(const Place& o) const { return r == o.r && h == o.h && rb == o.rb; }
-  // units of this item before `end`, from u on
-  __device__ __forceinline__ int left(const Place& end) const { return (same(end) ? end.u : units) - u; }
-  // The place at `x` in the numbering of cost that starts with request r0: an item's first
-  // kItemCost numbers are its first unit's.  (The bounds of the searches matter only if
-  // lengths change under the kernel.)
-  __device__ __forceinline__ void locate(const Params& p, int RB, int r0, int64_t x) {
-    h = rb = u = 0;
-    for (r = r0; r < p.a.n_req; ++r) {
-      q = request(p, r);
-      if (q.nq == 0) continue;
-      const int64_t c = head_cost(p, q, RB);
-      if (x < c * p.c.Hkv) {
-        h = x <= 0x7fffffff ? (int)((unsigned)x / (unsigned)min(c, (int64_t)0x7fffffff)) : (int)(x / c);
-        x -= h * c;
-        break;
-      }
-      x -= c * p.c.Hkv;
-    }
-    if (r >= p.a.n_req) return;  // behind the last item
-    const int nb = blocks_of(p, q, RB);
-    for (rb = 0;; ++rb) {
-      settle(p, RB);
-      if (rb == nb - 1 || x < units + kItemCost) break;
-      x -= units + kItemCost;
-    }
-    u = max(0, min((int)x - kItemCost, units - 1));
-  }
-  __device__ __forceinline__ void next(const Params& p, int RB) {
-    u = 0;
-    if (++rb >= blocks_of(p, q, RB)) {
-      rb = 0;
-      if (++h == p.c.Hkv) {
-        h = 0;
-        do {
-          if (++r >= p.a.n_req) return;
-          q = request(p, r);
-        } while (q.nq == 0);
-      }
-    }
-    settle(p, RB);
-  }
-};
-
-// ---------------------------------------------------------------------------
-// pieces: O (not divided by l), m and l of an item's rows
-// ---------------------------------------------------------------------------
-// slot: [rows][D] floats, then [rows] (m, l)
-template <int D, int RB>
-struct Slot {
-  static constexpr int kFloats = RB * (D + 2);
-  static __device__ __forceinline__ float2* ml(float* s) { return reinterpret_cast<float2*>(s + RB * D); }
-  static __device__ __forceinline__ const float2* ml(const float* s) {
-    return reinterpret_cast<const float2*>(s + RB * D);
-  }
-};
 // Workspace of a launch of at most `ctas` CTAs: a slot per warp (head pieces that other
 // work followed), a head and a tail slot per CTA, their states.
 template <int D, int RB, int WARPS>
@@ -185,61 +51,6 @@ struct Work {
   static constexpr size_t kSlot = (size_t)Slot<D, RB>::kFloats;
   static __host__ __device__ size_t cta_slots(int ctas) { return (size_t)ctas * WARPS * kSlot; }
   static __host__ __device__ size_t meta(int ctas) { return (size_t)ctas * (WARPS + 2) * kSlot; }
-};
-// What a CTA leaves for the joining of items that cross CTAs: the state of its head piece (the part of an
-// item that an earlier CTA began) and whether a tail piece (of an item begun here)
-// is open.
-struct CtaMeta {
-  int head;   // 0 none, 1 ends the item, 2 the item goes on
-  int tail;   // 1: open
-  int begin, nq, h, rb;  // the tail's item
-};
-
-// Row rho of a block -> its row of q and o
-__device__ __forceinline__ int64_t out_row(const Params& p, int begin, int h, int rb, int RB, int rho) {
-  const unsigned x = (unsigned)rb * RB + rho, tok = x / (unsigned)p.n_rep;
-  return (int64_t)(begin + (int)tok) * p.c.Hq + h * p.n_rep + (int)(x - tok * p.n_rep);
-}
-__device__ __forceinline__ int block_rows(const Params& p, int nq, int rb, int RB) {
-  return (int)min((int64_t)RB, (int64_t)nq * p.n_rep - (int64_t)rb * RB);
-}
-
-__device__ __forceinline__ void store4(const Params& p, int64_t row, int D, int ch, float4 v) {
-  if (p.c.bf16 && !p.c.o_f32)
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.o) + row * D + ch) =
-        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-  else
-    *reinterpret_cast<float4*>(static_cast<float*>(p.a.o) + row * D + ch) = v;
-}
-// 1 / l for the rows that saw a key (NaN for those that met one)
-__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
-// An item's rows from their sums: divided and written, 4 channels a thread.
-template <int D>
-__device__ __forceinline__ void write_out(const Params& p, int64_t row, int ch, float m, float l, float4 o) {
-  const float inv = inverse(l);
-  store4(p, row, D, ch, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-  if (ch == 0 && p.a.lse) p.a.lse[row] = lse_of(m, l);
-}
-
-// The sums of 4 channels of one row over pieces.  add() keeps the maximum so far.
-struct Acc {
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  __device__ __forceinline__ void add(float2 ml, float4 x) {
-    const float mn = max_nan(m, ml.x);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(m - base), w = ex2(ml.x - base);
-    m = mn;
-    l = fmaf(l, f, w * ml.y);
-    o.x = fmaf(o.x, f, w * x.x);
-    o.y = fmaf(o.y, f, w * x.y);
-    o.z = fmaf(o.z, f, w * x.z);
-    o.w = fmaf(o.w, f, w * x.w);
-  }
 };
 
 // ---------------------------------------------------------------------------
@@ -278,7 +89,7 @@ struct PieceMeta {
   int rows, begin, h, rb, nq;  // of the tail's item
   int head_rows;
 };
-template <int WARPS>
+template <typename It, int WARPS>
 struct Shared {
   int64_t sums[kSums];          // inclusive prefix sums of cost over requests
   int64_t warp_part[WARPS];
@@ -287,82 +98,27 @@ struct Shared {
   PieceMeta meta[WARPS];
   // per warp, what the main loop has no registers for: the items that are being loaded and
   // computed, and the run's end
-  Item in[WARPS], it[WARPS];
+  It in[WARPS], it[WARPS];
   Place end[WARPS];
 };
 
-// The run of this warp: its first unit and the next warp's, into sh.  (Apart from the kernel,
-// as the last part below is, so that their registers and the main loop's do not mix.)
-template <int RB, int WARPS>
-__device__ __forceinline__ void find_run(const Params& p, Shared<WARPS>& sh) {
+// The run of this warp, its first unit and the next warp's, into sh.
+template <typename It, int WARPS>
+__device__ __forceinline__ void find_run(const Params& p, Shared<It, WARPS>& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t total;
-  {
-    int64_t run = 0;
-    constexpr int PT = kSums / (WARPS * 32) > 0 ? kSums / (WARPS * 32) : 1;
-    // thread t's entries are PT neighbours, so one scan over threads gives all sums (threads
-    // past the last entry have no requests)
-    int64_t mine[PT];
-#pragma unroll
-    for (int i = 0; i < PT; ++i) {
-      const int e = threadIdx.x * PT + i;
-      int64_t n = 0;
-      const int64_t r0 = (int64_t)e * p.per_sum;
-      for (int64_t r = r0; r < r0 + p.per_sum && r < p.a.n_req; ++r) {
-        const Req q = request(p, (int)r);
-        if (q.nq > 0) n += head_cost(p, q, RB) * p.c.Hkv;
-      }
-      run += n;
-      mine[i] = run;
-    }
-    int64_t inc = run;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, m);
-      if (lane >= m) inc += y;
-    }
-    if (lane == 31) sh.warp_part[warp] = inc;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) before += sh.warp_part[w];
-      total += sh.warp_part[w];
-    }
-#pragma unroll
-    for (int i = 0; i < PT; ++i)
-      if (threadIdx.x * PT + i < kSums) sh.sums[threadIdx.x * PT + i] = before + inc - run + mine[i];
-    __syncthreads();
-  }
-
-  // An item costs its units and some for its start and end (the request's numbers and its
-  // query rows come from memory, its result goes there); every warp gets an equal run of
-  // that.  CTAs that would get nothing are not counted, so an item's CTAs are neighbours.
-  const int ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total));
-  const int cta = min((int)blockIdx.x, ctas);
-  const int64_t c0 = part_of(total, cta, ctas), c1 = part_of(total, min(cta + 1, ctas), ctas);
-  // the run's first unit, and the next warp's: one half of the lanes looks for each
-  {
-    const int64_t v = c0 + part_of(c1 - c0, warp + (lane >> 4), WARPS);
-    int lo = 0, hi = kSums;  // first entry whose inclusive sum is past v
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (sh.sums[mid] > v) hi = mid;
-      else lo = mid + 1;
-    }
-    Item x;
-    x.seen = x.units = 0;
-    x.q = {0, 0, 0};
-    x.locate(p, RB, lo * p.per_sum, lo < kSums ? v - (lo ? sh.sums[lo - 1] : 0) : 0);
-    if (lane == 0) sh.in[warp] = sh.it[warp] = x;
-    if (lane == 16) sh.end[warp] = x;
-  }
+  const int64_t total = sum_costs<It, WARPS * 32>(p, sh.sums, sh.warp_part);
+  int64_t c0, c1;
+  cta_run(total, c0, c1);
+  // one half of the lanes looks for each
+  const It x = item_at<It>(p, sh.sums, c0 + part_of(c1 - c0, warp + (lane >> 4), WARPS));
+  if (lane == 0) sh.in[warp] = sh.it[warp] = x;
+  if (lane == 16) sh.end[warp] = x;
 }
 
 // The end of the kernel: joins the CTA's open pieces, then the items that cross CTAs.
-template <int D, int RB, int WARPS>
-__device__ __forceinline__ void finish(const Params& p, const Shared<WARPS>& sh, uint8_t* smem, int stage_bytes) {
+template <int D, typename It, int WARPS>
+__device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>& sh, uint8_t* smem, int stage_bytes) {
+  constexpr int RB = It::kRows;
   using S = Slot<D, RB>;
   using W = Work<D, RB, WARPS>;
   const int lane = threadIdx.x & 31;
@@ -426,47 +182,8 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<WARPS>& sh,
   }
   if (threadIdx.x == 0 && pieces == 0) out_meta[blockIdx.x].head = out_meta[blockIdx.x].tail = 0;
 
-  // ---- items that cross CTAs --------------------------------------------------
-  // The CTA that began one joins its tail and the heads of the CTAs behind it up to the one
-  // that ends the item.  Few rows leave threads over: those share the pieces and meet in
-  // shared memory.
   cooperative_groups::this_grid().sync();
-  const CtaMeta cm = out_meta[blockIdx.x];
-  if (!cm.tail) return;
-  int n = 1;
-  for (int i = blockIdx.x + 1; i < (int)gridDim.x; i += 32) {
-    const bool last = i + lane >= (int)gridDim.x || out_meta[i + lane].head != 2;
-    const uint32_t b = __ballot_sync(0xffffffffu, last);
-    n = i - (int)blockIdx.x + (b ? __ffs(b) : 32);
-    if (b) break;
-  }
-  n = min(n, (int)(gridDim.x - blockIdx.x));
-  const int rows = block_rows(p, cm.nq, cm.rb, RB), parts = rows * V;
-  const int shares = max(1, WARPS * 32 / parts), share = threadIdx.x / parts;
-  Acc* const meet = reinterpret_cast<Acc*>(smem);
-  for (int e = shares > 1 ? threadIdx.x % parts : threadIdx.x; e < parts; e += shares > 1 ? parts : WARPS * 32) {
-    const int row = e / V, ch = (e - row * V) * 4;
-    Acc acc;
-    if (shares == 1 || share < shares) {
-#pragma unroll 4
-      for (int i = shares > 1 ? share : 0; i < n; i += shares) {
-        const float* s = cta_slots + (i ? 2 * (size_t)i : 1) * S::kFloats;
-        acc.add(S::ml(s)[row], *reinterpret_cast<const float4*>(s + row * D + ch));
-      }
-    }
-    if (shares > 1) meet[threadIdx.x] = acc;
-    else write_out<D>(p, out_row(p, cm.begin, cm.h, cm.rb, RB, row), ch, acc.m, acc.l, acc.o);
-  }
-  if (shares == 1) return;
-  __syncthreads();
-  if ((int)threadIdx.x >= parts) return;
-  Acc acc = meet[threadIdx.x];
-  for (int i = 1; i < shares; ++i) {
-    const Acc& x = meet[threadIdx.x + i * parts];
-    acc.add(make_float2(x.m, x.l), x.o);
-  }
-  const int row = threadIdx.x / V, ch = (threadIdx.x - row * V) * 4;
-  write_out<D>(p, out_row(p, cm.begin, cm.h, cm.rb, RB, row), ch, acc.m, acc.l, acc.o);
+  join_ctas<D, RB, WARPS * 32>(p, out_meta, ws + W::cta_slots(gridDim.x), reinterpret_cast<Acc*>(smem));
 }
 
 template <int D, int G, int NT, int NS, int WARPS, int MINB>
@@ -477,7 +194,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
   constexpr int MT = D / 16;    // 16-channel tiles of O^T
   using S = Slot<D, RB>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Shared<WARPS> sh;
+  using It = Item<RB, kUnit, kItemCost>;
+  __shared__ Shared<It, WARPS> sh;
   PieceMeta* const meta = sh.meta;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -492,7 +210,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
     fence_barrier_init();
   }
 
-  find_run<RB>(p, sh);
+  find_run(p, sh);
   float* const slot_smem = reinterpret_cast<float*>(smem + (size_t)warp * p.stages * stage_bytes);
   if (lane == 0) {
     meta[warp].head = 0;
@@ -514,7 +232,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
     // issues the copies of the next unit
     auto issue = [&]() {
       if (tab_k == 32) {
-        const Item& in = sh.in[warp];
+        const It& in = sh.in[warp];
         const int64_t tok = ((int64_t)in.u * per_lane + lane) * (kUnit / per_lane);
         tab = tok < in.seen ? p.a.table[(int64_t)in.r * p.a.max_pages + tok / p.c.page] : -1;
         from = p.a.cache + in.h * p.c.block_bytes();
@@ -551,9 +269,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
       valid = (valid & ~(3u << (2 * stage_in))) | have << (2 * stage_in);
       if (++stage_in == p.stages) stage_in = 0;
       if (--to_issue == 0) {
-        Item in = sh.in[warp];
+        It in = sh.in[warp];
         if (!in.same(sh.end[warp])) {
-          in.next(p, RB);
+          in.next(p);
           to_issue = in.r < p.a.n_req ? in.left(sh.end[warp]) : 0;
           tab_k = 32;
           __syncwarp();
@@ -571,7 +289,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
       uint32_t qf[NT][NS][KW][4];
       int lim[NT][2], least;
       {
-        const Item it = sh.it[warp];
+        const It it = sh.it[warp];
         const int rows = block_rows(p, it.q.nq, it.rb, RB);
         // query fragments: column g of every 8, channels 8 KW t4 ..
 #pragma unroll
@@ -812,13 +530,13 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int q = 4; q < 32; q <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], q);
-      const Item it = sh.it[warp];
+      const It it = sh.it[warp];
       const bool starts = it.u == 0, ends = it.u + it.left(sh.end[warp]) == it.units;
       const int rows = block_rows(p, it.q.nq, it.rb, RB);
-      Item after = it;
+      It after = it;
       more = !it.same(sh.end[warp]);
       if (more) {
-        after.next(p, RB);
+        after.next(p);
         more = after.r < p.a.n_req && after.left(sh.end[warp]) > 0;
       }
       const bool whole_item = starts && ends;
@@ -873,7 +591,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
     }
   }
   __syncthreads();
-  finish<D, RB, WARPS>(p, sh, smem, stage_bytes);
+  finish<D>(p, sh, smem, stage_bytes);
 }
 
 // ---------------------------------------------------------------------------
@@ -885,7 +603,7 @@ template <int D, int G, int NT, int NS, int WARPS, int MINB>
 struct Variant {
   static constexpr int kCtas = kMaxSms * MINB;
   static constexpr int kStatic = 6144;  // room for the static shared memory
-  static_assert(sizeof(Shared<WARPS>) <= kStatic, "shared memory");
+  static_assert(sizeof(Shared<Item<8 * NT, kUnit, kItemCost>, WARPS>) <= kStatic, "shared memory");
   using W = Work<D, 8 * NT, WARPS>;
   static size_t workspace() { return W::meta(kCtas) * sizeof(float) + kCtas * sizeof(CtaMeta); }
   static cudaError_t launch(Params p, int sms, cudaStream_t st) {
@@ -933,8 +651,10 @@ using Exact8 = Variant<D, G, 1, 3, 12, 1>;
 size_t cache_attn_workspace(const Cache& c) {
   using namespace cattn;
   const size_t n = !c.bf16       ? (c.D == 128 ? Exact8<128, 32>::workspace() : Exact8<64, 32>::workspace())
-                   : c.D == 128 ? std::max(Rows8<128, 32>::workspace(), Rows16<128, 32>::workspace())
-                                : std::max(Rows8<64, 32>::workspace(), Rows16<64, 32>::workspace());
+                   : c.D == 128 ? std::max({Rows8<128, 32>::workspace(), Rows16<128, 32>::workspace(),
+                                            cache_prompt_workspace(128)})
+                                : std::max({Rows8<64, 32>::workspace(), Rows16<64, 32>::workspace(),
+                                            cache_prompt_workspace(64)});
   return (n + 255) / 256 * 256;
 }
 
@@ -942,8 +662,10 @@ template <int D, int G>
 static cudaError_t launch_attn(const cattn::Params& p, int sms, cudaStream_t st) {
   using namespace cattn;
   if (!p.c.bf16) return Exact8<D, G>::launch(p, sms, st);
+  const int64_t rows = (int64_t)p.a.max_q * p.n_rep;
+  if (rows > 16) return launch_cache_prompt(p, sms, st);
   // 8 rows at a time while that is all a request has
-  if ((int64_t)p.a.max_q * p.n_rep <= 8) return Rows8<D, G>::launch(p, sms, st);
+  if (rows <= 8) return Rows8<D, G>::launch(p, sms, st);
   return Rows16<D, G>::launch(p, sms, st);
 }
 

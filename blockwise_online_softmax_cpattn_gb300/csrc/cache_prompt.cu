@@ -1,0 +1,576 @@
+// Attention of many new tokens over the 4-bit cache (chunks of a prompt, drafts of many
+// heads) on the 5th-generation tensor cores.
+//
+// An item is 256 query rows of one request and K/V head; its units are 128 cached tokens.
+// One CTA an SM takes an equal run of the line of items.  Two softmax warpgroups, sides a
+// and b, each own 128 rows' scores and output in TMEM: with more than 128 rows the sides
+// are the item's two halves and work on the same tokens, so every tile of codes is turned
+// into numbers once for 256 rows; an item of at most 128 rows goes to both sides, a taking
+// its even and b its odd tiles, and their sums are joined at the end.  While one side
+// forms its P, the tensor cores work for the other.
+//
+// Roles (512 threads):
+//   warp 0       issues the MMAs: per side S = Q K^T (both operands in shared memory) and
+//                O += P V (P in TMEM, over the scores it came from).
+//   warp 1       loads codes: 16-token tiles, their K halves and their V halves apart, so
+//                one is loaded while the other is read.
+//   warps 4-7    side a's softmax, a thread a row; warps 8-11 side b's.
+//   warps 12-15  turn codes into bf16 K and V tiles of 128 tokens with the 128-byte
+//                swizzle that the MMA reads, two of each.
+// A softmax thread reads its 128 scores from TMEM twice, for their maximum and to form P,
+// which costs less than the registers to keep them.  O is rescaled only when the running
+// maximum grew by more than 2^8 (exact after the division).
+//
+// TMEM (512 columns): S_a [0,128), S_b [128,256), O_a, O_b D columns each from 256; P of a
+// side takes the first 64 columns of its S.
+// Every mbarrier wait is bounded; on a time-out the CTA's roles give up, its copies and MMAs
+// are drained and TMEM is freed before the grid barrier.
+#include <cooperative_groups.h>
+
+#include <atomic>
+
+#include "cache_work.cuh"
+
+namespace cpattn {
+namespace cprompt {
+
+using namespace cattn;
+
+constexpr int kTile = 128;      // cached tokens of a unit, rows of a side
+constexpr int kRows = 256;      // query rows of an item
+constexpr int kThreads = 512;
+constexpr int kItemCost = 3;    // queries in, results out, in units
+using It = Item<kRows, kTile, kItemCost>;
+
+template <int D, int G>
+struct Smem {
+  static constexpr int kOperand = kTile * D * 2;          // bf16 tile, also one side's Q
+  static constexpr int kHalf = kCacheTile * (D / 2 + 4 * (D / G));
+  static constexpr int kCodes = kTile / kCacheTile * kHalf;  // codes of a tile's K or V
+  static constexpr int kQ = 0;
+  static constexpr int kK = 2 * kOperand;
+  static constexpr int kV = kK + 2 * kOperand;
+  static constexpr int kCode = kV + 2 * kOperand;         // K codes, V codes
+  static constexpr int kBar = kCode + 2 * kCodes;
+  // barriers: code_full[2], code_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2],
+  // q_full[2], s_full[2], p_full[2], o_full[2], o_free[2], share (stored, read), done
+  static constexpr int kNumBars = 25;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kBytes = kMisc + 16;
+};
+
+struct Static {
+  int64_t sums[kSums];
+  int64_t warp_part[kThreads / 32];
+  It start;
+  Place end;
+  CtaMeta meta;
+  uint32_t valid[8];   // per tile (the last 8): which of its 16-token tiles are there
+  int abort;
+  uint32_t tmem;
+};
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t par, volatile int* abort, int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, par, abort, status, kTimeoutNs));
+}
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t par) {
+  int never = 0;
+  mbar_wait(bar, par, &never, nullptr, kDrainTimeoutNs);
+}
+// What both sides' walks have in common: the tiles [u, u + n) of an item, and which of them
+// side x takes.
+struct Part {
+  int n, rows;
+  bool split;   // the sides share the rows and alternate between tiles
+  __device__ __forceinline__ int count(int x) const { return split ? (n + 1 - x) >> 1 : (x == 0 || rows > kTile ? n : 0); }
+  __device__ __forceinline__ int tile(int x, int i) const { return split ? 2 * i + x : i; }
+};
+__device__ __forceinline__ Part part(const Params& p, const It& it, const Place& end) {
+  Part t;
+  t.n = it.left(end);
+  t.rows = block_rows(p, it.q.nq, it.rb, kRows);
+  t.split = t.rows <= kTile;
+  return t;
+}
+// The next item of the run; false at its end.
+__device__ __forceinline__ bool advance(const Params& p, It& it, const Place& end) {
+  if (it.same(end)) return false;
+  it.next(p);
+  return it.r < p.a.n_req && it.left(end) > 0;
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Params p) {
+  using L = Smem<D, G>;
+  using S = Slot<D, kRows>;
+  constexpr int kTiles = kTile / kCacheTile;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Static sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bars = sbase + L::kBar;
+  auto bar = [&](int group, int i) { return bars + 8 * (2 * group + i); };
+  enum { CODE_FULL, CODE_EMPTY, K_FULL, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, S_FULL, P_FULL, O_FULL, O_FREE, SHARE, DONE };
+  volatile int* abort = &sh.abort;
+  int* const status = p.a.status;
+  float* const ws = static_cast<float*>(p.a.ws);
+  CtaMeta* const out_meta = reinterpret_cast<CtaMeta*>(ws + 2 * (size_t)gridDim.x * S::kFloats);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      const int group = i >> 1;
+      int n = 1;
+      if (group == CODE_EMPTY || group == K_FULL || group == V_FULL) n = 4;  // the warps that dequantise
+      if (group == Q_FULL || group == P_FULL || group == O_FREE || group == SHARE) n = 128;  // a side's threads
+      mbar_init(bars + 8 * i, n);
+    }
+    sh.abort = (sbase & 1023u) ? 1 : 0;  // the layout has no alignment slack
+    if (sh.abort) latch_status(status, kStatusLaunch);
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&sh.tmem), 512);
+    tmem_relinquish();
+  }
+  const int64_t total = sum_costs<It, kThreads>(p, sh.sums, sh.warp_part);
+  if (warp == 0) {
+    int64_t c0, c1;
+    cta_run(total, c0, c1);
+    const It x = item_at<It>(p, sh.sums, lane < 16 ? c0 : c1);
+    if (lane == 0) sh.start = x;
+    if (lane == 16) sh.end = x;
+    if (lane == 0) sh.meta.head = sh.meta.tail = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const Place end = sh.end;
+  const bool any = sh.start.r < p.a.n_req && sh.start.left(end) > 0 && !*abort;
+  bool ok = true;
+
+  if (!any) {
+    // nothing to do
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ codes
+    It it = sh.start;
+    uint32_t n = 0;   // tiles so far
+    do {
+      const Part t = part(p, it, end);
+      const uint8_t* from = p.a.cache + it.h * p.c.block_bytes();
+      for (int i = 0; ok && i < t.n; ++i, ++n) {
+        // lane j < 8 loads tile j of the unit
+        const int tok = (it.u + i) * kTile + lane * kCacheTile;
+        int pg = -1;
+        if (lane < kTiles && tok < it.seen) pg = p.a.table[(int64_t)it.r * p.a.max_pages + tok / p.c.page];
+        const bool there = (unsigned)pg < (unsigned)p.c.n_pages;
+        const uint32_t have = __ballot_sync(0xffffffffu, there);
+        const uint8_t* src = from + (there ? pg * p.page_bytes : 0) + tok % p.c.page / kCacheTile * (2 * L::kHalf);
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!(ok = warp_wait(bar(CODE_EMPTY, kv), (n & 1) ^ 1, abort, status))) break;
+          if (kv == 0 && lane == 0) sh.valid[n & 7] = have;
+          __syncwarp();
+          if (lane == 0) mbar_expect_tx(bar(CODE_FULL, kv), __popc(have) * L::kHalf);
+          __syncwarp();
+          if (there)
+            bulk_load(sbase + L::kCode + kv * L::kCodes + lane * L::kHalf, src + kv * L::kHalf, L::kHalf,
+                      bar(CODE_FULL, kv));
+        }
+      }
+    } while (ok && advance(p, it, end));
+    if (!ok && lane == 0 && n > 0) {
+      // never leave with a copy still writing into this CTA's shared memory
+      drain_wait(bar(CODE_FULL, 0), (n - 1) & 1);
+      drain_wait(bar(CODE_FULL, 0), n & 1);
+      drain_wait(bar(CODE_FULL, 1), (n - 1) & 1);
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ codes -> bf16 operands
+    // A thread takes 4 words (32 channels) of a row: 4 neighbours a row, 8 rows a warp.  The
+    // word order of every second pair of lanes is turned so that the eight 16-byte stores of
+    // a quarter of the warp hit eight different bank groups under the swizzle.
+    constexpr int Q = D / 32;                 // threads of a row
+    constexpr int kRowsAtOnce = 128 / Q, kSteps = kTile / kRowsAtOnce;
+    const int tid = threadIdx.x - 384, q = tid % Q, r0 = tid / Q;
+    It it = sh.start;
+    uint32_t n = 0;
+    do {
+      const Part t = part(p, it, end);
+      for (int i = 0; ok && i < t.n; ++i, ++n) {
+        const int left = it.q.len - (it.u + i) * kTile;  // tokens from the tile's first on
+        const uint32_t st = n & 1, par = (n >> 1) & 1;
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t full = bar(kv ? V_FULL : K_FULL, st), empty = bar(kv ? V_EMPTY : K_EMPTY, st);
+          if (!(ok = warp_wait(bar(CODE_FULL, kv), n & 1, abort, status))) break;
+          if (!(ok = warp_wait(empty, par ^ 1, abort, status))) break;
+          const uint32_t have = sh.valid[n & 7];
+          const uint8_t* codes = smem + L::kCode + kv * L::kCodes;
+          uint8_t* dst = smem + (kv ? L::kV : L::kK) + st * L::kOperand;
+#pragma unroll 2
+          for (int s = 0; s < kSteps; ++s) {
+            const int stored = s * kRowsAtOnce + r0;              // row as stored
+            const int tile = stored / kCacheTile, rr = stored % kCacheTile;
+            // stored row t + 4e of eight is token 2t + e
+            const int row = kv ? (stored & ~7) | ((stored & 3) << 1) | ((stored >> 2) & 1) : stored;
+            uint4 w = *reinterpret_cast<const uint4*>(codes + tile * L::kHalf + rr * (D / 2) + q * 16);
+            uint32_t az = *reinterpret_cast<const uint32_t*>(codes + tile * L::kHalf + kCacheTile * (D / 2) +
+                                                            (rr * (D / G) + q * 32 / G) * 4);
+            // rows nothing was appended to, or that were not loaded, hold anything: as zeros
+            if (row >= left || !((have >> tile) & 1u)) az = 0u;
+            const uint32_t a2 = az_a2(az), z2 = az_z2(az);
+            // turned word order: see above (rows of a quarter differ by 1, as stored V rows by 2)
+            const int turn = q & 2 ? (kv ? 1 : 2) : 0;
+            if (turn == 2) w = make_uint4(w.z, w.w, w.x, w.y);
+            if (turn == 1) w = make_uint4(w.y, w.x, w.w, w.z);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            uint8_t* line = dst + (q >> 1) * (kTile * 128) + row * 128;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t u[4];
+              if (kv) codes_to_bf16<false>(ww[x], p.ones, u);
+              else codes_to_bf16<true>(ww[x], p.ones, u);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) u[y] = bf16x2_fma(u[y], a2, z2);
+              const int chunk = (q & 1) * 4 + (x ^ turn);
+              *reinterpret_cast<uint4*>(line + ((chunk ^ (row & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(CODE_EMPTY, kv));
+            mbar_arrive(full);
+          }
+        }
+      }
+    } while (ok && advance(p, it, end));
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ MMAs
+    const bool leader = elect_one();
+    constexpr uint32_t kIdescS = idesc_bf16(128, 128, false, false);
+    constexpr uint32_t kIdescPV = idesc_bf16(128, D, false, true);
+    constexpr uint32_t kOp = L::kOperand >> 4;
+    const uint64_t qd = sdesc_sw128(sbase + L::kQ, 16, 1024);
+    const uint64_t kd = sdesc_sw128(sbase + L::kK, 16, 1024);
+    const uint64_t vd = sdesc_sw128(sbase + L::kV, kTile * 128, 1024);
+    It it = sh.start;
+    uint32_t base = 0;                      // tiles of the items before
+    uint32_t items[2] = {0, 0}, sides[2] = {0, 0};  // per side: items and tiles so far
+    do {
+      const Part t = part(p, it, end);
+      const int c0 = t.count(0), c1 = t.count(1);
+      for (int i = 0; ok && i <= c0; ++i) {
+        for (int x = 0; ok && x < 2; ++x) {
+          const int cnt = x ? c1 : c0;
+          if (i > 0 && i - 1 < cnt) {
+            // O += P V of the side's tile i - 1
+            const uint32_t g = base + t.tile(x, i - 1);
+            if (i == 1 && items[x] > 0 && !(ok = warp_wait(bar(O_FREE, x), (items[x] - 1) & 1, abort, status))) break;
+            if (!(ok = warp_wait(bar(V_FULL, g & 1), (g >> 1) & 1, abort, status))) break;
+            if (!(ok = warp_wait(bar(P_FULL, x), (sides[x] - 1) & 1, abort, status))) break;
+            tc_fence_after();
+            const uint64_t v = vd + (uint64_t)((g & 1) * kOp);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              if (leader)
+                mma_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, v + (uint64_t)(kk * 128), kIdescPV,
+                       (i > 1 || kk > 0) ? 1u : 0u);
+            if (leader) {
+              if (t.split || x == 1 || c1 == 0) mma_commit(bar(V_EMPTY, g & 1));
+              if (i == cnt) mma_commit(bar(O_FULL, x));
+            }
+            __syncwarp();
+          }
+          if (i < cnt) {
+            const uint32_t g = base + t.tile(x, i);
+            if (i == 0 && !(ok = warp_wait(bar(Q_FULL, x), items[x] & 1, abort, status))) break;
+            if (!(ok = warp_wait(bar(K_FULL, g & 1), (g >> 1) & 1, abort, status))) break;
+            tc_fence_after();
+            const uint64_t k = kd + (uint64_t)((g & 1) * kOp), q = qd + (uint64_t)(x * kOp);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;  // 16 KiB blocks, 32 B steps
+              if (leader) mma_ss(tmem + x * 128, q + off, k + off, kIdescS, kk > 0);
+            }
+            if (leader) {
+              mma_commit(bar(S_FULL, x));
+              if (t.split || x == 1 || c1 == 0) mma_commit(bar(K_EMPTY, g & 1));
+            }
+            __syncwarp();
+            ++sides[x];
+          }
+        }
+      }
+      base += t.n;
+      if (c0) ++items[0];
+      if (c1) ++items[1];
+    } while (ok && advance(p, it, end));
+    // every MMA has finished before TMEM can be freed
+    if (leader) mma_commit(bar(DONE, 0));
+    __syncwarp();
+    drain_wait(bar(DONE, 0), 0);
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int x = (warp - 4) >> 2;            // side
+    const int row = (warp & 3) * 32 + lane;   // of the side; TMEM lane quadrant warp % 4
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + x * 128, t_o = tmem + lanes + 256 + x * D;
+    const float2 sl2 = make_float2(p.sl2, p.sl2);
+    const float slack = 8.f / p.sl2;
+    It it = sh.start;
+    uint32_t n = 0, base = 0, items = 0;      // the side's tiles, all tiles, the side's items
+    uint32_t shared = 0;                      // items whose rows both sides had
+    bool more = true;
+    // this thread's query row into shared memory (zeros behind the item's rows)
+    auto load_q = [&](const It& a, const Part& t) {
+      const int rho = t.split ? row : x * kTile + row;
+      uint8_t* dst = smem + L::kQ + x * L::kOperand;
+      const bool in = rho < t.rows;
+      const uint4* src = nullptr;
+      if (in) {
+        const unsigned y = (unsigned)a.rb * kRows + rho, tok = y / (unsigned)p.n_rep;
+        src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
+                                             (a.q.begin + (int)tok) * p.a.qs.token +
+                                             (a.h * p.n_rep + (int)(y - tok * p.n_rep)) * p.a.qs.head);
+      }
+#pragma unroll 8
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 v = in ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(Q_FULL, x));
+    };
+    Part t = part(p, it, end);
+    if (t.count(x) > 0) load_q(it, t);
+    while (more && ok) {
+      const int cnt = t.count(x);
+      const int rho = t.split ? row : x * kTile + row;
+      const int lim = seen_by(p, it.q, it.rb * kRows + rho);
+      const int least = seen_by(p, it.q, it.rb * kRows + (t.split ? 0 : x * kTile));
+      float m = -INFINITY, top = -INFINITY, l = 0.f;
+      for (int i = 0; i < cnt; ++i, ++n) {
+        const int tile = t.tile(x, i);
+        if (!(ok = warp_wait(bar(S_FULL, x), n & 1, abort, status))) break;
+        tc_fence_after();
+        const int tok0 = (it.u + tile) * kTile;
+        const uint32_t have = sh.valid[(base + tile) & 7];
+        const bool whole = have == (1u << kTiles) - 1 && tok0 + kTile <= least;
+        uint32_t r[32];
+        auto load = [&](int c) {
+          tmem_ld32(t_s + 32 * c, r);
+          tmem_wait_ld();
+          if (!whole) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (tok0 + 32 * c + j >= lim || !((have >> (2 * c + (j >> 4))) & 1u)) r[j] = __float_as_uint(-INFINITY);
+          }
+        };
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          load(c);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            mx[(j >> 1) & 3] = max3_nan(mx[(j >> 1) & 3], __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+        }
+        const float hi = max_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]);
+        const bool over = !(hi <= top);
+        float f = 1.f;
+        if (over) {
+          const float mn = max_nan(m, hi * p.sl2);
+          f = ex2(m - mn);
+          m = mn;
+          top = hi + slack;
+          l *= f;
+        }
+        if (i > 0 && __any_sync(0xffffffffu, over)) {
+          // S complete means that the PV before it is
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            tmem_ld32(t_o + c * 32, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+            tmem_st32(t_o + c * 32, r);
+          }
+        }
+        const float nm = m == -INFINITY ? 0.f : -m;
+        const float2 nm2 = make_float2(nm, nm);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          load(c);
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 y = fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), sl2, nm2);
+            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+            sum[j & 1] = add2(sum[j & 1], e);
+            pk[j] = pack_bf16(e.x, e.y);
+          }
+          tmem_st16(t_s + c * 16, pk);   // columns whose scores have been read
+        }
+        const float2 s2 = add2(sum[0], sum[1]);
+        l += s2.x + s2.y;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(P_FULL, x));
+      }
+      if (!ok) break;
+      // the next item's queries, so that its first scores can start
+      const It cur = it;
+      const Part ct = t;
+      more = advance(p, it, end);
+      if (more) {
+        t = part(p, it, end);
+        if (t.count(x) > 0) load_q(it, t);
+      }
+      // ---------------------------------------------------------- the piece is done
+      if (cnt > 0) {
+        if (!(ok = warp_wait(bar(O_FULL, x), items & 1, abort, status))) break;
+        tc_fence_after();
+        ++items;
+      }
+      const bool starts = cur.u == 0, ends = cur.u + ct.n == cur.units, all = starts && ends;
+      float* const slot = ws + (2 * (size_t)blockIdx.x + (starts ? 1 : 0)) * S::kFloats;
+      // side b's share of the tiles of split rows goes through the slot's upper half
+      const bool other = ct.split && ct.n > 1;
+      const int out = other && x == 1 ? kTile + row : rho;
+      const bool live = rho < ct.rows && (cnt > 0);
+      if (other && x == 1) {
+        if (shared > 0 && !(ok = warp_wait(bar(SHARE, 1), (shared - 1) & 1, abort, status))) break;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(t_o + c * 32, r);
+          tmem_wait_ld();
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(slot + (size_t)out * D + c * 32 + j) =
+                  make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]),
+                              __uint_as_float(r[j + 3]));
+          }
+        }
+        if (live) S::ml(slot)[out] = make_float2(m, l);
+        mbar_arrive(bar(SHARE, 0));
+      }
+      if (other && x == 0 && !(ok = warp_wait(bar(SHARE, 0), shared & 1, abort, status))) break;
+      if (!(ct.split && x == 1) && cnt > 0) {
+        float m1 = -INFINITY, l1 = 0.f;
+        if (other && live) {
+          const float2 ml = S::ml(slot)[kTile + row];
+          m1 = ml.x;
+          l1 = ml.y;
+        }
+        const float mm = max_nan(m, m1), mb = mm == -INFINITY ? 0.f : mm;
+        const float w0 = ex2(m - mb), w1 = ex2(m1 - mb);
+        const float ll = w0 * l + w1 * l1;
+        const float inv = all ? inverse(ll) : 1.f;
+        const int64_t orow = all && live ? out_row(p, cur.q.begin, cur.h, cur.rb, kRows, rho) : 0;
+        const float a0 = w0 * inv, a1 = w1 * inv;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(t_o + c * 32, r);
+          tmem_wait_ld();
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              float4 v = make_float4(a0 * __uint_as_float(r[j]), a0 * __uint_as_float(r[j + 1]),
+                                     a0 * __uint_as_float(r[j + 2]), a0 * __uint_as_float(r[j + 3]));
+              if (other) {
+                const float4 y = *reinterpret_cast<const float4*>(slot + (size_t)(kTile + row) * D + c * 32 + j);
+                v = make_float4(fmaf(a1, y.x, v.x), fmaf(a1, y.y, v.y), fmaf(a1, y.z, v.z), fmaf(a1, y.w, v.w));
+              }
+              if (all) store4(p, orow, D, c * 32 + j, v);
+              else *reinterpret_cast<float4*>(slot + (size_t)rho * D + c * 32 + j) = v;
+            }
+          }
+        }
+        if (live) {
+          if (!all) S::ml(slot)[rho] = make_float2(mm, ll);
+          else if (p.a.lse) p.a.lse[orow] = lse_of(mm, ll);
+        }
+      }
+      if (other) {
+        if (x == 0) mbar_arrive(bar(SHARE, 1));  // the slot's upper half may be written again
+        ++shared;
+      }
+      if (cnt > 0) {
+        tc_fence_before();
+        mbar_arrive(bar(O_FREE, x));
+      }
+      if (row == 0 && x == 0 && !all) {
+        if (!starts) {
+          sh.meta.head = ends ? 1 : 2;
+        } else {
+          sh.meta.tail = 1;
+          sh.meta.begin = cur.q.begin;
+          sh.meta.nq = cur.q.nq;
+          sh.meta.h = cur.h;
+          sh.meta.rb = cur.rb;
+        }
+      }
+      base += ct.n;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0) out_meta[blockIdx.x] = sh.meta;
+  cooperative_groups::this_grid().sync();
+  join_ctas<D, kRows, kThreads>(p, out_meta, ws, reinterpret_cast<Acc*>(smem));
+}
+
+template <int D, int G>
+static cudaError_t launch(Params p, int sms, cudaStream_t st) {
+  auto kern = prompt_kernel<D, G>;
+  constexpr int kSmem = Smem<D, G>::kBytes;
+  static_assert(kSmem + sizeof(Static) <= 227 * 1024, "shared memory");
+  static_assert(kThreads * sizeof(Acc) <= (size_t)Smem<D, G>::kBar, "scratch of the join");
+  static std::atomic<uint64_t> set[2];  // devices whose limit is raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev >= 128 || !(set[dev >> 6].load() & bit)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess)
+      return e;
+    if (dev < 128) set[dev >> 6].fetch_or(bit);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = sms < kMaxSms ? sms : kMaxSms;
+  cfg.blockDim = kThreads;
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeCooperative;  // the CTAs meet at a grid barrier
+  at.val.cooperative = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace cprompt
+
+size_t cache_prompt_workspace(int D) {
+  using namespace cprompt;
+  const size_t slot = D == 128 ? Slot<128, kRows>::kFloats : Slot<64, kRows>::kFloats;
+  return kMaxSms * (2 * slot * sizeof(float) + sizeof(CtaMeta));
+}
+
+cudaError_t launch_cache_prompt(const cattn::Params& p, int sms, cudaStream_t st) {
+  using namespace cprompt;
+  if (p.c.D == 128)
+    return p.c.G == 128  ? launch<128, 128>(p, sms, st)
+           : p.c.G == 64 ? launch<128, 64>(p, sms, st)
+                         : launch<128, 32>(p, sms, st);
+  return p.c.G == 64 ? launch<64, 64>(p, sms, st) : launch<64, 32>(p, sms, st);
+}
+
+}  // namespace cpattn

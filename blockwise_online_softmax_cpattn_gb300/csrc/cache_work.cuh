@@ -1,0 +1,348 @@
+// How the 4-bit cache's attention kernels divide their work and join its pieces (device
+// code, internal to libcpattn).
+//
+// An item is RB query rows (new tokens x the heads of a K/V group) of one request and K/V
+// head; it is cut into units of UNIT cached tokens.  The items of all requests stand in
+// one line, by row block, K/V head and request, each with a cost: its units and COST for
+// its start and end (the request's numbers and its query rows come from memory, its
+// result goes there).  A worker takes an equal run of that line, so neither ragged
+// lengths nor few requests leave SMs idle, and nothing about lengths has to be known on
+// the host.  A run ends anywhere: what its worker knows of an item that it did not see
+// whole is a piece (O, m, l), and pieces are joined in their order by the (O, LSE) merge.
+#pragma once
+
+#include <math.h>
+
+#include "cache.cuh"
+
+namespace cpattn {
+namespace cattn {
+
+constexpr int kSums = 256;           // entries of the prefix sums over requests
+constexpr int kMaxSms = 160;         // of a GB300, and a few: the workspace's size
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr uint64_t kDrainTimeoutNs = 200000000ull;
+
+struct Params {
+  Cache c;
+  CacheAttnArgs a;
+  int n_rep, stages;                 // stages: of a ring of copies
+  int per_sum;                       // requests per entry of the prefix sums
+  int page_tiles, unit_in_page;      // tiles of a page; units do not straddle pages
+  int64_t page_bytes;                // of all K/V heads
+  float sl2;                         // scale * log2(e)
+  uint32_t ones;                     // kOnes
+};
+
+// ---------------------------------------------------------------------------
+// items
+// ---------------------------------------------------------------------------
+struct Req {
+  int begin, nq, len;
+};
+__device__ __forceinline__ Req request(const Params& p, int r) {
+  Req q;
+  const int b = min(max(p.a.q_start[r], 0), p.a.n_tokens);
+  const int e = min(max(p.a.q_start[r + 1], b), p.a.n_tokens);
+  q.begin = b;
+  q.nq = e - b;
+  q.len = min(max(p.a.kv_len[r], 0), p.a.max_pages * p.c.page);
+  return q;
+}
+// Rows of q are fewer than 2^31 (checked on the host), and so are a request's.
+// cached tokens that row x of the request sees
+__device__ __forceinline__ int seen_by(const Params& p, const Req& q, int x) {
+  if (!p.c.causal) return q.len;
+  return min(max(q.len - q.nq + (int)((unsigned)x / (unsigned)p.n_rep) + 1, 0), q.len);
+}
+// ... that row block rb (RB rows) sees, and its units
+__device__ __forceinline__ int block_seen(const Params& p, const Req& q, int rb, int RB) {
+  if (!p.c.causal) return q.len;
+  const int last = (int)min((int64_t)q.nq * p.n_rep, (int64_t)(rb + 1) * RB) - 1;
+  return seen_by(p, q, last);
+}
+__device__ __forceinline__ int units_of(int seen, int unit) { return max(1, (seen + unit - 1) / unit); }
+__device__ __forceinline__ int blocks_of(const Params& p, const Req& q, int RB) {
+  return (int)(((unsigned)(q.nq * p.n_rep) + RB - 1) / RB);
+}
+// i / n of x, rounded down (the 32-bit division where it does: n, i < 2^8)
+__device__ __forceinline__ int64_t part_of(int64_t x, int i, int n) {
+  if (x < (1 << 24)) return (unsigned)x * (unsigned)i / (unsigned)n;
+  return x * i / n;
+}
+
+// Request, K/V head and row block of an item, and a unit in it.  Items follow each other by
+// row block, K/V head, request.
+struct Place {
+  int r, h, rb, u;
+};
+template <int RB, int UNIT, int COST>
+struct Item : Place {
+  static constexpr int kRows = RB;
+  Req q;
+  int seen, units;
+  __device__ __forceinline__ void settle(const Params& p) {
+    seen = block_seen(p, q, rb, RB);
+    units = units_of(seen, UNIT);
+  }
+  // cost of one K/V head of a request
+  static __device__ __forceinline__ int64_t head_cost(const Params& p, const Req& q) {
+    const int nb = blocks_of(p, q, RB);
+    int64_t n = 0;
+    for (int b = 0; b < nb; ++b) n += units_of(block_seen(p, q, b, RB), UNIT) + COST;
+    return n;
+  }
+  __device__ __forceinline__ bool same(const Place& o) const { return r == o.r && h == o.h && rb == o.rb; }
+  // units of this item before `end`, from u on
+  __device__ __forceinline__ int left(const Place& end) const { return (same(end) ? end.u : units) - u; }
+  // The place at `x` in the numbering of cost that starts with request r0: an item's first
+  // COST numbers are its first unit's.  (The bounds of the searches matter only if
+  // lengths change under the kernel.)
+  __device__ __forceinline__ void locate(const Params& p, int r0, int64_t x) {
+    h = rb = u = 0;
+    for (r = r0; r < p.a.n_req; ++r) {
+      q = request(p, r);
+      if (q.nq == 0) continue;
+      const int64_t c = head_cost(p, q);
+      if (x < c * p.c.Hkv) {
+        h = x <= 0x7fffffff ? (int)((unsigned)x / (unsigned)min(c, (int64_t)0x7fffffff)) : (int)(x / c);
+        x -= h * c;
+        break;
+      }
+      x -= c * p.c.Hkv;
+    }
+    if (r >= p.a.n_req) return;  // behind the last item
+    const int nb = blocks_of(p, q, RB);
+    for (rb = 0;; ++rb) {
+      settle(p);
+      if (rb == nb - 1 || x < units + COST) break;
+      x -= units + COST;
+    }
+    u = max(0, min((int)x - COST, units - 1));
+  }
+  __device__ __forceinline__ void next(const Params& p) {
+    u = 0;
+    if (++rb >= blocks_of(p, q, RB)) {
+      rb = 0;
+      if (++h == p.c.Hkv) {
+        h = 0;
+        do {
+          if (++r >= p.a.n_req) return;
+          q = request(p, r);
+        } while (q.nq == 0);
+      }
+    }
+    settle(p);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// pieces: O (not divided by l), m and l of an item's rows
+// ---------------------------------------------------------------------------
+// slot: [rows][D] floats, then [rows] (m, l)
+template <int D, int RB>
+struct Slot {
+  static constexpr int kFloats = RB * (D + 2);
+  static __device__ __forceinline__ float2* ml(float* s) { return reinterpret_cast<float2*>(s + RB * D); }
+  static __device__ __forceinline__ const float2* ml(const float* s) {
+    return reinterpret_cast<const float2*>(s + RB * D);
+  }
+};
+// What a CTA leaves for the joining of items that cross CTAs: the state of its head piece
+// (the part of an item that an earlier CTA began) and whether a tail piece (of an item
+// begun here) is open.
+struct CtaMeta {
+  int head;   // 0 none, 1 ends the item, 2 the item goes on
+  int tail;   // 1: open
+  int begin, nq, h, rb;  // the tail's item
+};
+
+// Row rho of a block -> its row of q and o
+__device__ __forceinline__ int64_t out_row(const Params& p, int begin, int h, int rb, int RB, int rho) {
+  const unsigned x = (unsigned)rb * RB + rho, tok = x / (unsigned)p.n_rep;
+  return (int64_t)(begin + (int)tok) * p.c.Hq + h * p.n_rep + (int)(x - tok * p.n_rep);
+}
+__device__ __forceinline__ int block_rows(const Params& p, int nq, int rb, int RB) {
+  return (int)min((int64_t)RB, (int64_t)nq * p.n_rep - (int64_t)rb * RB);
+}
+
+__device__ __forceinline__ void store4(const Params& p, int64_t row, int D, int ch, float4 v) {
+  if (p.c.bf16 && !p.c.o_f32)
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.o) + row * D + ch) =
+        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(p.a.o) + row * D + ch) = v;
+}
+// 1 / l for the rows that saw a key (NaN for those that met one)
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// An item's rows from their sums: divided and written, 4 channels a thread.
+template <int D>
+__device__ __forceinline__ void write_out(const Params& p, int64_t row, int ch, float m, float l, float4 o) {
+  const float inv = inverse(l);
+  store4(p, row, D, ch, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (ch == 0 && p.a.lse) p.a.lse[row] = lse_of(m, l);
+}
+
+// The sums of 4 channels of one row over pieces.  add() keeps the maximum so far.
+struct Acc {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float2 ml, float4 x) {
+    const float mn = max_nan(m, ml.x);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(m - base), w = ex2(ml.x - base);
+    m = mn;
+    l = fmaf(l, f, w * ml.y);
+    o.x = fmaf(o.x, f, w * x.x);
+    o.y = fmaf(o.y, f, w * x.y);
+    o.z = fmaf(o.z, f, w * x.z);
+    o.w = fmaf(o.w, f, w * x.w);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// finding a run
+// ---------------------------------------------------------------------------
+// Inclusive prefix sums of cost over the requests, per_sum of them an entry, and the total.
+// Every thread of the CTA takes part.
+template <typename It, int THREADS>
+__device__ __forceinline__ int64_t sum_costs(const Params& p, int64_t* sums, int64_t* warp_part) {
+  constexpr int PT = kSums / THREADS > 0 ? kSums / THREADS : 1, WARPS = THREADS / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // thread t's entries are PT neighbours, so one scan over threads gives all sums (threads
+  // past the last entry have no requests)
+  int64_t mine[PT], run = 0;
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    const int64_t r0 = (int64_t)(threadIdx.x * PT + i) * p.per_sum;
+    for (int64_t r = r0; r < r0 + p.per_sum && r < p.a.n_req; ++r) {
+      const Req q = request(p, (int)r);
+      if (q.nq > 0) run += It::head_cost(p, q) * p.c.Hkv;
+    }
+    mine[i] = run;
+  }
+  int64_t inc = run;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, inc, m);
+    if (lane >= m) inc += y;
+  }
+  if (lane == 31) warp_part[warp] = inc;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += warp_part[w];
+    total += warp_part[w];
+  }
+#pragma unroll
+  for (int i = 0; i < PT; ++i)
+    if (threadIdx.x * PT + i < kSums) sums[threadIdx.x * PT + i] = before + inc - run + mine[i];
+  __syncthreads();
+  return total;
+}
+// This CTA's run of the line.  CTAs that would get nothing are not counted, so an item's
+// CTAs are neighbours.
+__device__ __forceinline__ void cta_run(int64_t total, int64_t& c0, int64_t& c1) {
+  const int ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total));
+  const int cta = min((int)blockIdx.x, ctas);
+  c0 = part_of(total, cta, ctas);
+  c1 = part_of(total, min(cta + 1, ctas), ctas);
+}
+// The item and unit at place v of the line (r = n_req behind its end).
+template <typename It>
+__device__ __forceinline__ It item_at(const Params& p, const int64_t* sums, int64_t v) {
+  int lo = 0, hi = kSums;  // first entry whose sum is past v
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] > v) hi = mid;
+    else lo = mid + 1;
+  }
+  It x;
+  x.seen = x.units = 0;
+  x.q = {0, 0, 0};
+  x.locate(p, lo * p.per_sum, lo < kSums ? v - (lo ? sums[lo - 1] : 0) : 0);
+  return x;
+}
+
+// ---------------------------------------------------------------------------
+// items that cross CTAs (behind a grid barrier)
+// ---------------------------------------------------------------------------
+// An item's CTAs are the one that began it (its tail piece) and those behind it up to the one
+// that ends it (their head pieces); each joins a part of the item's numbers.  slots: a head
+// and a tail slot per CTA; scratch: THREADS Accs of shared memory.  Few numbers leave threads
+// over: those share the pieces and meet in the scratch.
+template <int D, int RB, int THREADS>
+__device__ __forceinline__ void join_ctas(const Params& p, const CtaMeta* meta, const float* slots, Acc* scratch) {
+  using S = Slot<D, RB>;
+  constexpr int V = D / 4;
+  const int lane = threadIdx.x & 31, me = blockIdx.x, ctas = gridDim.x;
+  for (int which = 0; which < 2; ++which) {  // the item of this CTA's head, that of its tail
+    int owner = me;
+    if (which == 0) {
+      if (meta[me].head == 0) continue;
+      owner = -1;
+      for (int i = me - 1; i >= 0 && owner < 0; i -= 32) {
+        const uint32_t b = __ballot_sync(0xffffffffu, i - lane >= 0 && meta[max(i - lane, 0)].tail != 0);
+        if (b) owner = i - (__ffs(b) - 1);
+      }
+      if (owner < 0) continue;  // (only if a CTA gave up)
+    } else if (meta[me].tail == 0) {
+      continue;
+    }
+    const CtaMeta cm = meta[owner];
+    int n = ctas - owner;  // the item's CTAs
+    for (int i = owner + 1; i < ctas; i += 32) {
+      const uint32_t b = __ballot_sync(0xffffffffu, i + lane < ctas && meta[min(i + lane, ctas - 1)].head != 2);
+      if (b) {
+        n = i - owner + __ffs(b);
+        break;
+      }
+    }
+    n = min(n, ctas - owner);
+    const int all = block_rows(p, cm.nq, cm.rb, RB) * V;
+    const int e0 = (int)((int64_t)all * (me - owner) / n), e1 = (int)((int64_t)all * (me - owner + 1) / n);
+    const int parts = e1 - e0;
+    if (parts <= 0) continue;
+    const int shares = max(1, min(THREADS / parts, n)), share = threadIdx.x / parts;
+    const float* const first = slots + 2 * (size_t)owner * S::kFloats;
+    if (shares > 1) __syncthreads();  // the scratch of the item before
+    for (int i0 = shares > 1 ? threadIdx.x % parts : threadIdx.x; i0 < parts; i0 += shares > 1 ? parts : THREADS) {
+      const int row = (e0 + i0) / V, ch = (e0 + i0 - row * V) * 4;
+      Acc acc;
+      if (share < shares || shares == 1) {
+#pragma unroll 4
+        for (int i = shares > 1 ? share : 0; i < n; i += shares) {
+          const float* s = first + (i ? 2 * (size_t)i : 1) * S::kFloats;
+          acc.add(S::ml(s)[row], *reinterpret_cast<const float4*>(s + row * D + ch));
+        }
+      }
+      if (shares > 1) scratch[threadIdx.x] = acc;
+      else write_out<D>(p, out_row(p, cm.begin, cm.h, cm.rb, RB, row), ch, acc.m, acc.l, acc.o);
+    }
+    if (shares == 1) continue;
+    __syncthreads();
+    if ((int)threadIdx.x < parts) {
+      Acc acc = scratch[threadIdx.x];
+      for (int i = 1; i < shares; ++i) {
+        const Acc& x = scratch[threadIdx.x + i * parts];
+        acc.add(make_float2(x.m, x.l), x.o);
+      }
+      const int e = e0 + threadIdx.x, row = e / V, ch = (e - row * V) * 4;
+      write_out<D>(p, out_row(p, cm.begin, cm.h, cm.rb, RB, row), ch, acc.m, acc.l, acc.o);
+    }
+  }
+}
+
+}  // namespace cattn
+
+// ---- cache_prompt.cu: many query rows per K/V head, bf16 --------------------
+size_t cache_prompt_workspace(int D);
+cudaError_t launch_cache_prompt(const cattn::Params& p, int sms, cudaStream_t st);
+
+}  // namespace cpattn
