@@ -12,18 +12,19 @@
 // Roles (512 threads):
 //   warp 0       issues the MMAs: per side S = Q K^T (both operands in shared memory) and
 //                O += P V (P in TMEM, over the scores it came from).
-//   warp 1       loads codes: 16-token tiles, their K halves and their V halves apart, so
-//                one is loaded while the other is read.
 //   warps 4-7    side a's softmax, a thread a row; warps 8-11 side b's.
 //   warps 12-15  turn codes into bf16 K and V tiles of 128 tokens with the 128-byte
-//                swizzle that the MMA reads, two of each.
+//                swizzle that the MMA reads, two of each.  The codes come through
+//                registers, a tile ahead: with bulk copies to shared memory, which has
+//                room for one tile of codes beside the operands, every tile waited for
+//                its load (1.23 ms for the chunk that now takes 0.98).
 // A softmax thread reads its 128 scores from TMEM twice, for their maximum and to form P,
 // which costs less than the registers to keep them.  O is rescaled only when the running
 // maximum grew by more than 2^8 (exact after the division).
 //
 // TMEM (512 columns): S_a [0,128), S_b [128,256), O_a, O_b D columns each from 256; P of a
 // side takes the first 64 columns of its S.
-// Every mbarrier wait is bounded; on a time-out the CTA's roles give up, its copies and MMAs
+// Every mbarrier wait is bounded; on a time-out the CTA's roles give up, its MMAs
 // are drained and TMEM is freed before the grid barrier.
 #include <cooperative_groups.h>
 
@@ -45,16 +46,14 @@ using It = Item<kRows, kTile, kItemCost>;
 template <int D, int G>
 struct Smem {
   static constexpr int kOperand = kTile * D * 2;          // bf16 tile, also one side's Q
-  static constexpr int kHalf = kCacheTile * (D / 2 + 4 * (D / G));
-  static constexpr int kCodes = kTile / kCacheTile * kHalf;  // codes of a tile's K or V
+  static constexpr int kHalf = kCacheTile * (D / 2 + 4 * (D / G));  // of a tile in the cache
   static constexpr int kQ = 0;
   static constexpr int kK = 2 * kOperand;
   static constexpr int kV = kK + 2 * kOperand;
-  static constexpr int kCode = kV + 2 * kOperand;         // K codes, V codes
-  static constexpr int kBar = kCode + 2 * kCodes;
-  // barriers: code_full[2], code_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2],
-  // q_full[2], s_full[2], p_full[2], o_full[2], o_free[2], share (stored, read), done
-  static constexpr int kNumBars = 25;
+  static constexpr int kBar = kV + 2 * kOperand;
+  // barriers: k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], s_full[2], p_full[2],
+  // o_full[2], o_free[2], share (stored, read), done
+  static constexpr int kNumBars = 21;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16;
 };
@@ -110,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + L::kBar;
   auto bar = [&](int group, int i) { return bars + 8 * (2 * group + i); };
-  enum { CODE_FULL, CODE_EMPTY, K_FULL, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, S_FULL, P_FULL, O_FULL, O_FREE, SHARE, DONE };
+  enum { K_FULL, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, S_FULL, P_FULL, O_FULL, O_FREE, SHARE, DONE };
   volatile int* abort = &sh.abort;
   int* const status = p.a.status;
   float* const ws = static_cast<float*>(p.a.ws);
@@ -120,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     for (int i = 0; i < L::kNumBars; ++i) {
       const int group = i >> 1;
       int n = 1;
-      if (group == CODE_EMPTY || group == K_FULL || group == V_FULL) n = 4;  // the warps that dequantise
+      if (group == K_FULL || group == V_FULL) n = 4;  // the warps that dequantise
       if (group == Q_FULL || group == P_FULL || group == O_FREE || group == SHARE) n = 128;  // a side's threads
       mbar_init(bars + 8 * i, n);
     }
@@ -151,99 +150,108 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 
   if (!any) {
     // nothing to do
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ codes
-    It it = sh.start;
-    uint32_t n = 0;   // tiles so far
-    do {
-      const Part t = part(p, it, end);
-      const uint8_t* from = p.a.cache + it.h * p.c.block_bytes();
-      for (int i = 0; ok && i < t.n; ++i, ++n) {
-        // lane j < 8 loads tile j of the unit
-        const int tok = (it.u + i) * kTile + lane * kCacheTile;
-        int pg = -1;
-        if (lane < kTiles && tok < it.seen) pg = p.a.table[(int64_t)it.r * p.a.max_pages + tok / p.c.page];
-        const bool there = (unsigned)pg < (unsigned)p.c.n_pages;
-        const uint32_t have = __ballot_sync(0xffffffffu, there);
-        const uint8_t* src = from + (there ? pg * p.page_bytes : 0) + tok % p.c.page / kCacheTile * (2 * L::kHalf);
-        for (int kv = 0; kv < 2; ++kv) {
-          if (!(ok = warp_wait(bar(CODE_EMPTY, kv), (n & 1) ^ 1, abort, status))) break;
-          if (kv == 0 && lane == 0) sh.valid[n & 7] = have;
-          __syncwarp();
-          if (lane == 0) mbar_expect_tx(bar(CODE_FULL, kv), __popc(have) * L::kHalf);
-          __syncwarp();
-          if (there)
-            bulk_load(sbase + L::kCode + kv * L::kCodes + lane * L::kHalf, src + kv * L::kHalf, L::kHalf,
-                      bar(CODE_FULL, kv));
-        }
-      }
-    } while (ok && advance(p, it, end));
-    if (!ok && lane == 0 && n > 0) {
-      // never leave with a copy still writing into this CTA's shared memory
-      drain_wait(bar(CODE_FULL, 0), (n - 1) & 1);
-      drain_wait(bar(CODE_FULL, 0), n & 1);
-      drain_wait(bar(CODE_FULL, 1), (n - 1) & 1);
-    }
   } else if (warp >= 12) {
     // ------------------------------------------------------------ codes -> bf16 operands
-    // A thread takes 4 words (32 channels) of a row: 4 neighbours a row, 8 rows a warp.  The
-    // word order of every second pair of lanes is turned so that the eight 16-byte stores of
-    // a quarter of the warp hit eight different bank groups under the swizzle.
+    // A thread takes 4 words (32 channels) of a row: Q neighbours a row, so that a warp has
+    // rows of one 16-token tile at a time.  Its codes of a tile wait in registers, loaded
+    // while it works on the tile before; the tile's pages are looked up one tile earlier
+    // still.
     constexpr int Q = D / 32;                 // threads of a row
     constexpr int kRowsAtOnce = 128 / Q, kSteps = kTile / kRowsAtOnce;
-    const int tid = threadIdx.x - 384, q = tid % Q, r0 = tid / Q;
+    const int wq = warp - 12, q = lane % Q;
+    // row of step s as stored: s kRowsAtOnce + r0, in 16-token tile s kTilesAtOnce + tile0
+    constexpr int kTilesAtOnce = kRowsAtOnce / kCacheTile;
+    const int r0 = wq * (kRowsAtOnce / 4) + lane / Q, tile0 = r0 / kCacheTile, rr = r0 % kCacheTile;
+    const int code_at = rr * (D / 2) + q * 16, az_at = kCacheTile * (D / 2) + (rr * (D / G) + q * 32 / G) * 4;
+    // a tile ahead: lane j < 8 knows where its 16-token tile j is
+    struct Ahead {
+      const uint8_t* at;
+      uint32_t have;   // the tiles that are there
+      int left;        // tokens of the request from the tile's first on
+      bool is;
+    };
     It it = sh.start;
-    uint32_t n = 0;
-    do {
-      const Part t = part(p, it, end);
-      for (int i = 0; ok && i < t.n; ++i, ++n) {
-        const int left = it.q.len - (it.u + i) * kTile;  // tokens from the tile's first on
-        const uint32_t st = n & 1, par = (n >> 1) & 1;
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t full = bar(kv ? V_FULL : K_FULL, st), empty = bar(kv ? V_EMPTY : K_EMPTY, st);
-          if (!(ok = warp_wait(bar(CODE_FULL, kv), n & 1, abort, status))) break;
-          if (!(ok = warp_wait(empty, par ^ 1, abort, status))) break;
-          const uint32_t have = sh.valid[n & 7];
-          const uint8_t* codes = smem + L::kCode + kv * L::kCodes;
-          uint8_t* dst = smem + (kv ? L::kV : L::kK) + st * L::kOperand;
-#pragma unroll 2
-          for (int s = 0; s < kSteps; ++s) {
-            const int stored = s * kRowsAtOnce + r0;              // row as stored
-            const int tile = stored / kCacheTile, rr = stored % kCacheTile;
-            // stored row t + 4e of eight is token 2t + e
-            const int row = kv ? (stored & ~7) | ((stored & 3) << 1) | ((stored >> 2) & 1) : stored;
-            uint4 w = *reinterpret_cast<const uint4*>(codes + tile * L::kHalf + rr * (D / 2) + q * 16);
-            uint32_t az = *reinterpret_cast<const uint32_t*>(codes + tile * L::kHalf + kCacheTile * (D / 2) +
-                                                            (rr * (D / G) + q * 32 / G) * 4);
-            // rows nothing was appended to, or that were not loaded, hold anything: as zeros
-            if (row >= left || !((have >> tile) & 1u)) az = 0u;
-            const uint32_t a2 = az_a2(az), z2 = az_z2(az);
-            // turned word order: see above (rows of a quarter differ by 1, as stored V rows by 2)
-            const int turn = q & 2 ? (kv ? 1 : 2) : 0;
-            if (turn == 2) w = make_uint4(w.z, w.w, w.x, w.y);
-            if (turn == 1) w = make_uint4(w.y, w.x, w.w, w.z);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-            uint8_t* line = dst + (q >> 1) * (kTile * 128) + row * 128;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t u[4];
-              if (kv) codes_to_bf16<false>(ww[x], p.ones, u);
-              else codes_to_bf16<true>(ww[x], p.ones, u);
-#pragma unroll
-              for (int y = 0; y < 4; ++y) u[y] = bf16x2_fma(u[y], a2, z2);
-              const int chunk = (q & 1) * 4 + (x ^ turn);
-              *reinterpret_cast<uint4*>(line + ((chunk ^ (row & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(CODE_EMPTY, kv));
-            mbar_arrive(full);
-          }
-        }
+    int ti = 0, tn = it.left(end);
+    bool more = true;
+    auto look_up = [&]() {
+      Ahead a = {nullptr, 0u, 0, more};
+      if (!more) return a;
+      const int first = (it.u + ti) * kTile, tok = first + lane * kCacheTile;
+      int pg = -1;
+      if (lane < kTiles && tok < it.seen) pg = p.a.table[(int64_t)it.r * p.a.max_pages + tok / p.c.page];
+      a.have = __ballot_sync(0xffffffffu, (unsigned)pg < (unsigned)p.c.n_pages);
+      a.at = p.a.cache + it.h * p.c.block_bytes() + max(pg, 0) * p.page_bytes +
+             tok % p.c.page / kCacheTile * (2 * L::kHalf);
+      a.left = it.q.len - first;
+      if (++ti == tn) {
+        ti = 0;
+        more = advance(p, it, end);
+        if (more) tn = it.left(end);
       }
-    } while (ok && advance(p, it, end));
+      return a;
+    };
+    uint4 codes[2][kSteps];
+    uint32_t az[2][kSteps];
+    auto load = [&](const Ahead& a, int kv, int s) {
+      const int tile = s * kTilesAtOnce + tile0;
+      const uint8_t* at = reinterpret_cast<const uint8_t*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(a.at), tile));
+      codes[kv][s] = make_uint4(0u, 0u, 0u, 0u);
+      az[kv][s] = 0u;
+      if ((a.have >> tile) & 1u) {
+        codes[kv][s] = *reinterpret_cast<const uint4*>(at + kv * L::kHalf + code_at);
+        az[kv][s] = *reinterpret_cast<const uint32_t*>(at + kv * L::kHalf + az_at);
+      }
+    };
+    Ahead cur = look_up(), next = look_up();
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) load(cur, kv, s);
+    for (uint32_t n = 0; ok && cur.is; ++n) {
+      const uint32_t st = n & 1, par = (n >> 1) & 1;
+      const Ahead later = look_up();
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!(ok = warp_wait(bar(kv ? V_EMPTY : K_EMPTY, st), par ^ 1, abort, status))) break;
+        uint8_t* dst = smem + (kv ? L::kV : L::kK) + st * L::kOperand;
+        if (kv == 0 && warp == 12 && lane == 0) sh.valid[n & 7] = cur.have;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const int stored = s * kRowsAtOnce + r0;
+          // stored row t + 4e of eight is token 2t + e
+          const int row = kv ? (stored & ~7) | ((stored & 3) << 1) | ((stored >> 2) & 1) : stored;
+          uint4 w = codes[kv][s];
+          // rows nothing was appended to hold anything: as zeros
+          const uint32_t par2 = row < cur.left ? az[kv][s] : 0u;
+          const uint32_t a2 = az_a2(par2), z2 = az_z2(par2);
+          // The word order of every second pair of lanes is turned, so that the eight 16-byte
+          // stores of a quarter of the warp hit eight different bank groups under the swizzle
+          // (its rows differ by 1, stored V rows by 2).
+          const int turn = q & 2 ? (kv ? 1 : 2) : 0;
+          if (turn == 2) w = make_uint4(w.z, w.w, w.x, w.y);
+          if (turn == 1) w = make_uint4(w.y, w.x, w.w, w.z);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          uint8_t* line = dst + (q >> 1) * (kTile * 128) + row * 128;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t u[4];
+            if (kv) codes_to_bf16<false>(ww[x], p.ones, u);
+            else codes_to_bf16<true>(ww[x], p.ones, u);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) u[y] = bf16x2_fma(u[y], a2, z2);
+            const int chunk = (q & 1) * 4 + (x ^ turn);
+            *reinterpret_cast<uint4*>(line + ((chunk ^ (row & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+          load(next, kv, s);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kv ? V_FULL : K_FULL, st));
+      }
+      cur = next;
+      next = later;
+    }
   } else if (warp == 0) {
     // ------------------------------------------------------------ MMAs
     const bool leader = elect_one();
@@ -356,23 +364,32 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int tok0 = (it.u + tile) * kTile;
         const uint32_t have = sh.valid[(base + tile) & 7];
         const bool whole = have == (1u << kTiles) - 1 && tok0 + kTile <= least;
-        uint32_t r[32];
-        auto load = [&](int c) {
-          tmem_ld32(t_s + 32 * c, r);
-          tmem_wait_ld();
-          if (!whole) {
+        // Few instructions count here: three roles' loops share an instruction cache, so
+        // the loops over chunks of 32 columns stay rolled.
+        auto mask = [&](int c, uint32_t (&r)[32]) {
+          const int rel = lim - tok0 - 32 * c;   // columns below it are seen
+          const int rel0 = (have >> (2 * c)) & 1u ? rel : 0, rel1 = (have >> (2 * c + 1)) & 1u ? rel : 0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (tok0 + 32 * c + j >= lim || !((have >> (2 * c + (j >> 4))) & 1u)) r[j] = __float_as_uint(-INFINITY);
-          }
+          for (int j = 0; j < 32; ++j)
+            if (j >= (j < 16 ? rel0 : rel1)) r[j] = __float_as_uint(-INFINITY);
         };
+        uint32_t ra[32], rb[32];
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          tmem_ld32(t_s + 32 * c, ra);
+          tmem_ld32(t_s + 32 * c + 32, rb);
+          tmem_wait_ld_of(ra, rb);
+          if (!whole) {
+            mask(c, ra);
+            mask(c + 1, rb);
+          }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          load(c);
-#pragma unroll
-          for (int j = 0; j < 32; j += 2)
-            mx[(j >> 1) & 3] = max3_nan(mx[(j >> 1) & 3], __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+          for (int j = 0; j < 32; j += 2) {
+            mx[(j >> 1) & 1] = max3_nan(mx[(j >> 1) & 1], __uint_as_float(ra[j]), __uint_as_float(ra[j + 1]));
+            mx[2 + ((j >> 1) & 1)] =
+                max3_nan(mx[2 + ((j >> 1) & 1)], __uint_as_float(rb[j]), __uint_as_float(rb[j + 1]));
+          }
         }
         const float hi = max_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]);
         const bool over = !(hi <= top);
@@ -388,19 +405,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           // S complete means that the PV before it is
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
-            tmem_ld32(t_o + c * 32, r);
-            tmem_wait_ld();
+            tmem_ld32(t_o + c * 32, ra);
+            tmem_wait_ld_of(ra);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
-            tmem_st32(t_o + c * 32, r);
+            for (int j = 0; j < 32; ++j) ra[j] = __float_as_uint(__uint_as_float(ra[j]) * f);
+            tmem_st32(t_o + c * 32, ra);
           }
         }
         const float nm = m == -INFINITY ? 0.f : -m;
         const float2 nm2 = make_float2(nm, nm);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          load(c);
+        auto form = [&](int c, uint32_t (&r)[32]) {
+          if (!whole) mask(c, r);
           uint32_t pk[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -410,6 +426,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             pk[j] = pack_bf16(e.x, e.y);
           }
           tmem_st16(t_s + c * 16, pk);   // columns whose scores have been read
+        };
+        tmem_ld32(t_s, ra);
+        tmem_wait_ld_of(ra);
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          tmem_ld32(t_s + 32 * c + 32, rb);
+          form(c, ra);
+          tmem_wait_ld_of(rb);
+          if (c == 0) tmem_ld32(t_s + 64, ra);
+          form(c + 1, rb);
+          tmem_wait_ld_of(ra);
         }
         const float2 s2 = add2(sum[0], sum[1]);
         l += s2.x + s2.y;
@@ -444,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
           tmem_ld32(t_o + c * 32, r);
-          tmem_wait_ld();
+          tmem_wait_ld_of(r);
           if (live) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
@@ -474,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
           tmem_ld32(t_o + c * 32, r);
-          tmem_wait_ld();
+          tmem_wait_ld_of(r);
           if (live) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {

@@ -488,6 +488,20 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+// ... with the loaded registers as operands, so that nothing that reads them can be moved
+// above the wait.
+#define CPATTN_RW8(i) "+r"(r[i + 0]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), \
+                      "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : CPATTN_RW8(0), CPATTN_RW8(8), CPATTN_RW8(16), CPATTN_RW8(24)
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&a)[32], uint32_t (&b)[32]) {
+  tmem_wait_ld_of(a);
+  tmem_wait_ld_of(b);
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
