@@ -2,7 +2,8 @@
 // heads) on the 5th-generation tensor cores.
 //
 // An item is 256 query rows of one request and K/V head; its units are 128 cached tokens.
-// One CTA an SM takes an equal run of the line of items.  Two softmax warpgroups, sides a
+// One CTA an SM takes an equal run of the line of items; items that cross CTAs are joined
+// by a second, small launch.  Two softmax warpgroups, sides a
 // and b, each own 128 rows' scores and output in TMEM: with more than 128 rows the sides
 // are the item's two halves and work on the same tokens, so every tile of codes is turned
 // into numbers once for 256 rows; an item of at most 128 rows goes to both sides, a taking
@@ -10,24 +11,20 @@
 // forms its P, the tensor cores work for the other.
 //
 // Roles (512 threads):
-//   warp 0       issues the MMAs: per side S = Q K^T (both operands in shared memory) and
+//   warp 0       issues S = Q K^T of both sides (both operands in shared memory), warp 1
 //                O += P V (P in TMEM, over the scores it came from).
+//   warp 2       loads codes, K and V of a tile apart, into a ring of three.
 //   warps 4-7    side a's softmax, a thread a row; warps 8-11 side b's.
 //   warps 12-15  turn codes into bf16 K and V tiles of 128 tokens with the 128-byte
-//                swizzle that the MMA reads, two of each.  The codes come through
-//                registers, a tile ahead: with bulk copies to shared memory, which has
-//                room for one tile of codes beside the operands, every tile waited for
-//                its load (1.23 ms for the chunk that now takes 0.98).
-// A softmax thread reads its 128 scores from TMEM twice, for their maximum and to form P,
-// which costs less than the registers to keep them.  O is rescaled only when the running
-// maximum grew by more than 2^8 (exact after the division).
+//                swizzle that the MMA reads, two of each.
+// A softmax thread holds its 128 scores in registers, which the other warpgroups give up
+// (reading them from TMEM a second time to form P cost a third of the time).  O is rescaled
+// only when the running maximum grew by more than 2^8 (exact after the division).
 //
 // TMEM (512 columns): S_a [0,128), S_b [128,256), O_a, O_b D columns each from 256; P of a
 // side takes the first 64 columns of its S.
-// Every mbarrier wait is bounded; on a time-out the CTA's roles give up, its MMAs
-// are drained and TMEM is freed before the grid barrier.
-#include <cooperative_groups.h>
-
+// Every mbarrier wait is bounded; on a time-out the CTA's roles give up, its copies and MMAs
+// are drained and TMEM is freed.
 #include <atomic>
 
 #include "cache_work.cuh"
@@ -40,6 +37,18 @@ using namespace cattn;
 constexpr int kTile = 128;      // cached tokens of a unit, rows of a side
 constexpr int kRows = 256;      // query rows of an item
 constexpr int kThreads = 512;
+constexpr int kRing = 3;        // tiles' K or V codes in shared memory
+// registers a thread: issuers and loader, dequantising, softmax (two warpgroups)
+constexpr int kRegsLaunch = 128, kRegsIssue = 64, kRegsCodes = 80, kRegsSoftmax = 184;
+static_assert(kRegsIssue + kRegsCodes + 2 * kRegsSoftmax <= 4 * kRegsLaunch, "an increase would wait forever");
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 constexpr int kItemCost = 3;    // queries in, results out, in units
 using It = Item<kRows, kTile, kItemCost>;
 
@@ -50,10 +59,12 @@ struct Smem {
   static constexpr int kQ = 0;
   static constexpr int kK = 2 * kOperand;
   static constexpr int kV = kK + 2 * kOperand;
-  static constexpr int kBar = kV + 2 * kOperand;
+  static constexpr int kCode = kV + 2 * kOperand;
+  static constexpr int kCodes = kTile / kCacheTile * kHalf;  // codes of a tile's K or V
+  static constexpr int kBar = kCode + kRing * kCodes;
   // barriers: k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], s_full[2], p_full[2],
-  // o_full[2], o_free[2], share (stored, read), done
-  static constexpr int kNumBars = 21;
+  // pv_done[2], o_free[2], share (stored, read), done[2], codes full, empty
+  static constexpr int kNumBars = 22 + 2 * kRing;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16;
 };
@@ -109,7 +120,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + L::kBar;
   auto bar = [&](int group, int i) { return bars + 8 * (2 * group + i); };
-  enum { K_FULL, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, S_FULL, P_FULL, O_FULL, O_FREE, SHARE, DONE };
+  enum { K_FULL, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, S_FULL, P_FULL, PV_DONE, O_FREE, SHARE, DONE, CODES };
+  auto codes_full = [&](int i) { return bars + 8 * (2 * CODES + i); };
+  auto codes_empty = [&](int i) { return bars + 8 * (2 * CODES + kRing + i); };
   volatile int* abort = &sh.abort;
   int* const status = p.a.status;
   float* const ws = static_cast<float*>(p.a.ws);
@@ -119,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     for (int i = 0; i < L::kNumBars; ++i) {
       const int group = i >> 1;
       int n = 1;
-      if (group == K_FULL || group == V_FULL) n = 4;  // the warps that dequantise
+      if (group == K_FULL || group == V_FULL || i >= 2 * CODES + kRing) n = 4;  // the warps that dequantise
       if (group == Q_FULL || group == P_FULL || group == O_FREE || group == SHARE) n = 128;  // a side's threads
       mbar_init(bars + 8 * i, n);
     }
@@ -148,151 +161,71 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const bool any = sh.start.r < p.a.n_req && sh.start.left(end) > 0 && !*abort;
   bool ok = true;
 
-  if (!any) {
-    // nothing to do
-  } else if (warp >= 12) {
-    // ------------------------------------------------------------ codes -> bf16 operands
-    // A thread takes 4 words (32 channels) of a row: Q neighbours a row, so that a warp has
-    // rows of one 16-token tile at a time.  Its codes of a tile wait in registers, loaded
-    // while it works on the tile before; the tile's pages are looked up one tile earlier
-    // still.
-    constexpr int Q = D / 32;                 // threads of a row
-    constexpr int kRowsAtOnce = 128 / Q, kSteps = kTile / kRowsAtOnce;
-    const int wq = warp - 12, q = lane % Q;
-    // row of step s as stored: s kRowsAtOnce + r0, in 16-token tile s kTilesAtOnce + tile0
-    constexpr int kTilesAtOnce = kRowsAtOnce / kCacheTile;
-    const int r0 = wq * (kRowsAtOnce / 4) + lane / Q, tile0 = r0 / kCacheTile, rr = r0 % kCacheTile;
-    const int code_at = rr * (D / 2) + q * 16, az_at = kCacheTile * (D / 2) + (rr * (D / G) + q * 32 / G) * 4;
-    // a tile ahead: lane j < 8 knows where its 16-token tile j is
-    struct Ahead {
-      const uint8_t* at;
-      uint32_t have;   // the tiles that are there
-      int left;        // tokens of the request from the tile's first on
-      bool is;
-    };
-    It it = sh.start;
-    int ti = 0, tn = it.left(end);
-    bool more = true;
-    auto look_up = [&]() {
-      Ahead a = {nullptr, 0u, 0, more};
-      if (!more) return a;
-      const int first = (it.u + ti) * kTile, tok = first + lane * kCacheTile;
-      int pg = -1;
-      if (lane < kTiles && tok < it.seen) pg = p.a.table[(int64_t)it.r * p.a.max_pages + tok / p.c.page];
-      a.have = __ballot_sync(0xffffffffu, (unsigned)pg < (unsigned)p.c.n_pages);
-      a.at = p.a.cache + it.h * p.c.block_bytes() + max(pg, 0) * p.page_bytes +
-             tok % p.c.page / kCacheTile * (2 * L::kHalf);
-      a.left = it.q.len - first;
-      if (++ti == tn) {
-        ti = 0;
-        more = advance(p, it, end);
-        if (more) tn = it.left(end);
-      }
-      return a;
-    };
-    uint4 codes[2][kSteps];
-    uint32_t az[2][kSteps];
-    auto load = [&](const Ahead& a, int kv, int s) {
-      const int tile = s * kTilesAtOnce + tile0;
-      const uint8_t* at = reinterpret_cast<const uint8_t*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(a.at), tile));
-      codes[kv][s] = make_uint4(0u, 0u, 0u, 0u);
-      az[kv][s] = 0u;
-      if ((a.have >> tile) & 1u) {
-        codes[kv][s] = *reinterpret_cast<const uint4*>(at + kv * L::kHalf + code_at);
-        az[kv][s] = *reinterpret_cast<const uint32_t*>(at + kv * L::kHalf + az_at);
-      }
-    };
-    Ahead cur = look_up(), next = look_up();
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) load(cur, kv, s);
-    for (uint32_t n = 0; ok && cur.is; ++n) {
-      const uint32_t st = n & 1, par = (n >> 1) & 1;
-      const Ahead later = look_up();
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (!(ok = warp_wait(bar(kv ? V_EMPTY : K_EMPTY, st), par ^ 1, abort, status))) break;
-        uint8_t* dst = smem + (kv ? L::kV : L::kK) + st * L::kOperand;
-        if (kv == 0 && warp == 12 && lane == 0) sh.valid[n & 7] = cur.have;
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          const int stored = s * kRowsAtOnce + r0;
-          // stored row t + 4e of eight is token 2t + e
-          const int row = kv ? (stored & ~7) | ((stored & 3) << 1) | ((stored >> 2) & 1) : stored;
-          uint4 w = codes[kv][s];
-          // rows nothing was appended to hold anything: as zeros
-          const uint32_t par2 = row < cur.left ? az[kv][s] : 0u;
-          const uint32_t a2 = az_a2(par2), z2 = az_z2(par2);
-          // The word order of every second pair of lanes is turned, so that the eight 16-byte
-          // stores of a quarter of the warp hit eight different bank groups under the swizzle
-          // (its rows differ by 1, stored V rows by 2).
-          const int turn = q & 2 ? (kv ? 1 : 2) : 0;
-          if (turn == 2) w = make_uint4(w.z, w.w, w.x, w.y);
-          if (turn == 1) w = make_uint4(w.y, w.x, w.w, w.z);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-          uint8_t* line = dst + (q >> 1) * (kTile * 128) + row * 128;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t u[4];
-            if (kv) codes_to_bf16<false>(ww[x], p.ones, u);
-            else codes_to_bf16<true>(ww[x], p.ones, u);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) u[y] = bf16x2_fma(u[y], a2, z2);
-            const int chunk = (q & 1) * 4 + (x ^ turn);
-            *reinterpret_cast<uint4*>(line + ((chunk ^ (row & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-          load(next, kv, s);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kv ? V_FULL : K_FULL, st));
-      }
-      cur = next;
-      next = later;
-    }
-  } else if (warp == 0) {
-    // ------------------------------------------------------------ MMAs
-    const bool leader = elect_one();
-    constexpr uint32_t kIdescS = idesc_bf16(128, 128, false, false);
-    constexpr uint32_t kIdescPV = idesc_bf16(128, D, false, true);
-    constexpr uint32_t kOp = L::kOperand >> 4;
-    const uint64_t qd = sdesc_sw128(sbase + L::kQ, 16, 1024);
-    const uint64_t kd = sdesc_sw128(sbase + L::kK, 16, 1024);
-    const uint64_t vd = sdesc_sw128(sbase + L::kV, kTile * 128, 1024);
-    It it = sh.start;
-    uint32_t base = 0;                      // tiles of the items before
-    uint32_t items[2] = {0, 0}, sides[2] = {0, 0};  // per side: items and tiles so far
-    do {
-      const Part t = part(p, it, end);
-      const int c0 = t.count(0), c1 = t.count(1);
-      for (int i = 0; ok && i <= c0; ++i) {
-        for (int x = 0; ok && x < 2; ++x) {
-          const int cnt = x ? c1 : c0;
-          if (i > 0 && i - 1 < cnt) {
-            // O += P V of the side's tile i - 1
-            const uint32_t g = base + t.tile(x, i - 1);
-            if (i == 1 && items[x] > 0 && !(ok = warp_wait(bar(O_FREE, x), (items[x] - 1) & 1, abort, status))) break;
-            if (!(ok = warp_wait(bar(V_FULL, g & 1), (g >> 1) & 1, abort, status))) break;
-            if (!(ok = warp_wait(bar(P_FULL, x), (sides[x] - 1) & 1, abort, status))) break;
-            tc_fence_after();
-            const uint64_t v = vd + (uint64_t)((g & 1) * kOp);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              if (leader)
-                mma_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, v + (uint64_t)(kk * 128), kIdescPV,
-                       (i > 1 || kk > 0) ? 1u : 0u);
-            if (leader) {
-              if (t.split || x == 1 || c1 == 0) mma_commit(bar(V_EMPTY, g & 1));
-              if (i == cnt) mma_commit(bar(O_FULL, x));
+  if (warp < 4) {
+    regs_down<kRegsIssue>();
+    if (!any) {
+      // nothing to do
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ codes
+      // A ring of three: K and V halves of the tiles in turn.
+      It it = sh.start;
+      uint32_t n = 0;   // halves so far
+      int slot = 0;
+      uint32_t par = 0;
+      do {
+        const int tiles = it.left(end);
+        for (int i = 0; ok && i < tiles; ++i) {
+          // lane j < 8 loads 16-token tile j
+          const int tok = (it.u + i) * kTile + lane * kCacheTile;
+          int pg = -1;
+          if (lane < kTiles && tok < it.seen) pg = p.a.table[(int64_t)it.r * p.a.max_pages + tok / p.c.page];
+          const bool there = (unsigned)pg < (unsigned)p.c.n_pages;
+          const uint32_t have = __ballot_sync(0xffffffffu, there);
+          const uint8_t* src = p.a.cache + it.h * p.c.block_bytes() + (there ? pg * p.page_bytes : 0) +
+                               tok % p.c.page / kCacheTile * (2 * L::kHalf);
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            if (!(ok = warp_wait(codes_empty(slot), par ^ 1, abort, status))) break;
+            if (lane == 0) {
+              if (kv == 0) sh.valid[(n >> 1) & 7] = have;
+              mbar_expect_tx(codes_full(slot), __popc(have) * L::kHalf);
             }
             __syncwarp();
+            if (there)
+              bulk_load(sbase + L::kCode + slot * L::kCodes + lane * L::kHalf, src + kv * L::kHalf, L::kHalf,
+                        codes_full(slot));
+            if (++slot == kRing) slot = 0, par ^= 1;
           }
-          if (i < cnt) {
+        }
+      } while (ok && advance(p, it, end));
+      if (!ok && lane == 0) {
+        // never leave with a copy still writing into this CTA's shared memory
+        for (int i = 0; i < kRing; ++i)
+          if (n >= (uint32_t)kRing - i) {
+            drain_wait(codes_full(slot), par ^ 1);
+            if (++slot == kRing) slot = 0, par ^= 1;
+          }
+      }
+    } else if (warp == 0) {
+      // ------------------------------------------------------------ S = Q K^T
+      const bool leader = elect_one();
+      constexpr uint32_t kIdescS = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t kOp = L::kOperand >> 4;
+      const uint64_t qd = sdesc_sw128(sbase + L::kQ, 16, 1024);
+      const uint64_t kd = sdesc_sw128(sbase + L::kK, 16, 1024);
+      It it = sh.start;
+      uint32_t base = 0;                              // tiles of the items before
+      uint32_t items[2] = {0, 0}, tiles[2] = {0, 0};  // per side so far
+      do {
+        const Part t = part(p, it, end);
+        for (int i = 0; ok && i < t.count(0); ++i) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || i >= t.count(x)) break;
             const uint32_t g = base + t.tile(x, i);
             if (i == 0 && !(ok = warp_wait(bar(Q_FULL, x), items[x] & 1, abort, status))) break;
             if (!(ok = warp_wait(bar(K_FULL, g & 1), (g >> 1) & 1, abort, status))) break;
+            // the side's P before, in the same columns, has been read
+            if (tiles[x] > 0 && !(ok = warp_wait(bar(PV_DONE, x), (tiles[x] - 1) & 1, abort, status))) break;
             tc_fence_after();
             const uint64_t k = kd + (uint64_t)((g & 1) * kOp), q = qd + (uint64_t)(x * kOp);
 #pragma unroll
@@ -302,247 +235,344 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             }
             if (leader) {
               mma_commit(bar(S_FULL, x));
-              if (t.split || x == 1 || c1 == 0) mma_commit(bar(K_EMPTY, g & 1));
+              if (t.split || x == 1) mma_commit(bar(K_EMPTY, g & 1));
             }
             __syncwarp();
-            ++sides[x];
+            ++tiles[x];
           }
         }
-      }
-      base += t.n;
-      if (c0) ++items[0];
-      if (c1) ++items[1];
-    } while (ok && advance(p, it, end));
-    // every MMA has finished before TMEM can be freed
-    if (leader) mma_commit(bar(DONE, 0));
-    __syncwarp();
-    drain_wait(bar(DONE, 0), 0);
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------ softmax
-    const int x = (warp - 4) >> 2;            // side
-    const int row = (warp & 3) * 32 + lane;   // of the side; TMEM lane quadrant warp % 4
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + x * 128, t_o = tmem + lanes + 256 + x * D;
-    const float2 sl2 = make_float2(p.sl2, p.sl2);
-    const float slack = 8.f / p.sl2;
-    It it = sh.start;
-    uint32_t n = 0, base = 0, items = 0;      // the side's tiles, all tiles, the side's items
-    uint32_t shared = 0;                      // items whose rows both sides had
-    bool more = true;
-    // this thread's query row into shared memory (zeros behind the item's rows)
-    auto load_q = [&](const It& a, const Part& t) {
-      const int rho = t.split ? row : x * kTile + row;
-      uint8_t* dst = smem + L::kQ + x * L::kOperand;
-      const bool in = rho < t.rows;
-      const uint4* src = nullptr;
-      if (in) {
-        const unsigned y = (unsigned)a.rb * kRows + rho, tok = y / (unsigned)p.n_rep;
-        src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
-                                             (a.q.begin + (int)tok) * p.a.qs.token +
-                                             (a.h * p.n_rep + (int)(y - tok * p.n_rep)) * p.a.qs.head);
-      }
-#pragma unroll 8
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = in ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(bar(Q_FULL, x));
-    };
-    Part t = part(p, it, end);
-    if (t.count(x) > 0) load_q(it, t);
-    while (more && ok) {
-      const int cnt = t.count(x);
-      const int rho = t.split ? row : x * kTile + row;
-      const int lim = seen_by(p, it.q, it.rb * kRows + rho);
-      const int least = seen_by(p, it.q, it.rb * kRows + (t.split ? 0 : x * kTile));
-      float m = -INFINITY, top = -INFINITY, l = 0.f;
-      for (int i = 0; i < cnt; ++i, ++n) {
-        const int tile = t.tile(x, i);
-        if (!(ok = warp_wait(bar(S_FULL, x), n & 1, abort, status))) break;
-        tc_fence_after();
-        const int tok0 = (it.u + tile) * kTile;
-        const uint32_t have = sh.valid[(base + tile) & 7];
-        const bool whole = have == (1u << kTiles) - 1 && tok0 + kTile <= least;
-        // Few instructions count here: three roles' loops share an instruction cache, so
-        // the loops over chunks of 32 columns stay rolled.
-        auto mask = [&](int c, uint32_t (&r)[32]) {
-          const int rel = lim - tok0 - 32 * c;   // columns below it are seen
-          const int rel0 = (have >> (2 * c)) & 1u ? rel : 0, rel1 = (have >> (2 * c + 1)) & 1u ? rel : 0;
+        base += t.n;
+        ++items[0];
+        if (t.count(1)) ++items[1];
+      } while (ok && advance(p, it, end));
+      // every MMA has finished before TMEM can be freed
+      if (leader) mma_commit(bar(DONE, 0));
+      __syncwarp();
+      drain_wait(bar(DONE, 0), 0);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ O += P V
+      // (an issuer of its own: the next wait of a thread that committed MMAs waits for them)
+      const bool leader = elect_one();
+      constexpr uint32_t kIdescPV = idesc_bf16(128, D, false, true);
+      constexpr uint32_t kOp = L::kOperand >> 4;
+      const uint64_t vd = sdesc_sw128(sbase + L::kV, kTile * 128, 1024);
+      It it = sh.start;
+      uint32_t base = 0, items[2] = {0, 0}, tiles[2] = {0, 0};
+      do {
+        const Part t = part(p, it, end);
+        for (int i = 0; ok && i < t.count(0); ++i) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j >= (j < 16 ? rel0 : rel1)) r[j] = __float_as_uint(-INFINITY);
-        };
-        uint32_t ra[32], rb[32];
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          tmem_ld32(t_s + 32 * c, ra);
-          tmem_ld32(t_s + 32 * c + 32, rb);
-          tmem_wait_ld_of(ra, rb);
-          if (!whole) {
-            mask(c, ra);
-            mask(c + 1, rb);
-          }
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || i >= t.count(x)) break;
+            const uint32_t g = base + t.tile(x, i);
+            if (i == 0 && items[x] > 0 && !(ok = warp_wait(bar(O_FREE, x), (items[x] - 1) & 1, abort, status))) break;
+            if (!(ok = warp_wait(bar(V_FULL, g & 1), (g >> 1) & 1, abort, status))) break;
+            if (!(ok = warp_wait(bar(P_FULL, x), tiles[x] & 1, abort, status))) break;
+            tc_fence_after();
+            const uint64_t v = vd + (uint64_t)((g & 1) * kOp);
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            mx[(j >> 1) & 1] = max3_nan(mx[(j >> 1) & 1], __uint_as_float(ra[j]), __uint_as_float(ra[j + 1]));
-            mx[2 + ((j >> 1) & 1)] =
-                max3_nan(mx[2 + ((j >> 1) & 1)], __uint_as_float(rb[j]), __uint_as_float(rb[j + 1]));
+            for (int kk = 0; kk < 8; ++kk)
+              if (leader)
+                mma_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, v + (uint64_t)(kk * 128), kIdescPV,
+                       (i > 0 || kk > 0) ? 1u : 0u);
+            if (leader) {
+              mma_commit(bar(PV_DONE, x));
+              if (t.split || x == 1) mma_commit(bar(V_EMPTY, g & 1));
+            }
+            __syncwarp();
+            ++tiles[x];
           }
         }
-        const float hi = max_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]);
-        const bool over = !(hi <= top);
-        float f = 1.f;
-        if (over) {
-          const float mn = max_nan(m, hi * p.sl2);
-          f = ex2(m - mn);
-          m = mn;
-          top = hi + slack;
-          l *= f;
-        }
-        if (i > 0 && __any_sync(0xffffffffu, over)) {
-          // S complete means that the PV before it is
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            tmem_ld32(t_o + c * 32, ra);
-            tmem_wait_ld_of(ra);
+        base += t.n;
+        ++items[0];
+        if (t.count(1)) ++items[1];
+      } while (ok && advance(p, it, end));
+      if (leader) mma_commit(bar(DONE, 1));
+      __syncwarp();
+      drain_wait(bar(DONE, 1), 0);
+    }
+  } else if (warp >= 12) {
+    regs_down<kRegsCodes>();
+    if (any) {
+      // ------------------------------------------------------------ codes -> bf16 operands
+      // A thread takes 4 words (32 channels) of a row: Q neighbours a row.  The word order of
+      // every second pair of lanes is turned, so that the eight 16-byte stores of a quarter of
+      // the warp hit eight different bank groups under the swizzle (its rows differ by 1,
+      // stored V rows by 2).
+      constexpr int Q = D / 32;                 // threads of a row
+      constexpr int kRowsAtOnce = 128 / Q, kSteps = kTile / kRowsAtOnce;
+      const int q = lane % Q, r0 = (threadIdx.x - 384) / Q;
+      It it = sh.start;
+      uint32_t n = 0;
+      int slot = 0;
+      uint32_t code_par = 0;
+      do {
+        const int tiles = it.left(end);
+        for (int i = 0; ok && i < tiles; ++i, ++n) {
+          const int left = it.q.len - (it.u + i) * kTile;  // tokens from the tile's first on
+          const uint32_t st = n & 1, par = (n >> 1) & 1;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) ra[j] = __float_as_uint(__uint_as_float(ra[j]) * f);
-            tmem_st32(t_o + c * 32, ra);
-          }
-        }
-        const float nm = m == -INFINITY ? 0.f : -m;
-        const float2 nm2 = make_float2(nm, nm);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        auto form = [&](int c, uint32_t (&r)[32]) {
-          if (!whole) mask(c, r);
-          uint32_t pk[16];
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!(ok = warp_wait(codes_full(slot), code_par, abort, status))) break;
+            if (!(ok = warp_wait(bar(kv ? V_EMPTY : K_EMPTY, st), par ^ 1, abort, status))) break;
+            const uint32_t have = sh.valid[n & 7];
+            const uint8_t* codes = smem + L::kCode + slot * L::kCodes;
+            uint8_t* dst = smem + (kv ? L::kV : L::kK) + st * L::kOperand;
+#pragma unroll 2
+            for (int s = 0; s < kSteps; ++s) {
+              const int stored = s * kRowsAtOnce + r0, tile = stored / kCacheTile, rr = stored % kCacheTile;
+              // stored row t + 4e of eight is token 2t + e
+              const int row = kv ? (stored & ~7) | ((stored & 3) << 1) | ((stored >> 2) & 1) : stored;
+              const uint8_t* half = codes + tile * L::kHalf;
+              uint4 w = *reinterpret_cast<const uint4*>(half + rr * (D / 2) + q * 16);
+              uint32_t az = *reinterpret_cast<const uint32_t*>(half + kCacheTile * (D / 2) + (rr * (D / G) + q * 32 / G) * 4);
+              // rows nothing was appended to, or that were not loaded, hold anything: as zeros
+              if (row >= left || !((have >> tile) & 1u)) az = 0u;
+              const uint32_t a2 = az_a2(az), z2 = az_z2(az);
+              const int turn = q & 2 ? (kv ? 1 : 2) : 0;
+              if (turn == 2) w = make_uint4(w.z, w.w, w.x, w.y);
+              if (turn == 1) w = make_uint4(w.y, w.x, w.w, w.z);
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+              uint8_t* line = dst + (q >> 1) * (kTile * 128) + row * 128;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 y = fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), sl2, nm2);
-            const float2 e = make_float2(ex2(y.x), ex2(y.y));
-            sum[j & 1] = add2(sum[j & 1], e);
-            pk[j] = pack_bf16(e.x, e.y);
-          }
-          tmem_st16(t_s + c * 16, pk);   // columns whose scores have been read
-        };
-        tmem_ld32(t_s, ra);
-        tmem_wait_ld_of(ra);
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          tmem_ld32(t_s + 32 * c + 32, rb);
-          form(c, ra);
-          tmem_wait_ld_of(rb);
-          if (c == 0) tmem_ld32(t_s + 64, ra);
-          form(c + 1, rb);
-          tmem_wait_ld_of(ra);
-        }
-        const float2 s2 = add2(sum[0], sum[1]);
-        l += s2.x + s2.y;
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(P_FULL, x));
-      }
-      if (!ok) break;
-      // the next item's queries, so that its first scores can start
-      const It cur = it;
-      const Part ct = t;
-      more = advance(p, it, end);
-      if (more) {
-        t = part(p, it, end);
-        if (t.count(x) > 0) load_q(it, t);
-      }
-      // ---------------------------------------------------------- the piece is done
-      if (cnt > 0) {
-        if (!(ok = warp_wait(bar(O_FULL, x), items & 1, abort, status))) break;
-        tc_fence_after();
-        ++items;
-      }
-      const bool starts = cur.u == 0, ends = cur.u + ct.n == cur.units, all = starts && ends;
-      float* const slot = ws + (2 * (size_t)blockIdx.x + (starts ? 1 : 0)) * S::kFloats;
-      // side b's share of the tiles of split rows goes through the slot's upper half
-      const bool other = ct.split && ct.n > 1;
-      const int out = other && x == 1 ? kTile + row : rho;
-      const bool live = rho < ct.rows && (cnt > 0);
-      if (other && x == 1) {
-        if (shared > 0 && !(ok = warp_wait(bar(SHARE, 1), (shared - 1) & 1, abort, status))) break;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32(t_o + c * 32, r);
-          tmem_wait_ld_of(r);
-          if (live) {
+              for (int x = 0; x < 4; ++x) {
+                uint32_t u[4];
+                if (kv) codes_to_bf16<false>(ww[x], p.ones, u);
+                else codes_to_bf16<true>(ww[x], p.ones, u);
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<float4*>(slot + (size_t)out * D + c * 32 + j) =
-                  make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]),
-                              __uint_as_float(r[j + 3]));
-          }
-        }
-        if (live) S::ml(slot)[out] = make_float2(m, l);
-        mbar_arrive(bar(SHARE, 0));
-      }
-      if (other && x == 0 && !(ok = warp_wait(bar(SHARE, 0), shared & 1, abort, status))) break;
-      if (!(ct.split && x == 1) && cnt > 0) {
-        float m1 = -INFINITY, l1 = 0.f;
-        if (other && live) {
-          const float2 ml = S::ml(slot)[kTile + row];
-          m1 = ml.x;
-          l1 = ml.y;
-        }
-        const float mm = max_nan(m, m1), mb = mm == -INFINITY ? 0.f : mm;
-        const float w0 = ex2(m - mb), w1 = ex2(m1 - mb);
-        const float ll = w0 * l + w1 * l1;
-        const float inv = all ? inverse(ll) : 1.f;
-        const int64_t orow = all && live ? out_row(p, cur.q.begin, cur.h, cur.rb, kRows, rho) : 0;
-        const float a0 = w0 * inv, a1 = w1 * inv;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32(t_o + c * 32, r);
-          tmem_wait_ld_of(r);
-          if (live) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              float4 v = make_float4(a0 * __uint_as_float(r[j]), a0 * __uint_as_float(r[j + 1]),
-                                     a0 * __uint_as_float(r[j + 2]), a0 * __uint_as_float(r[j + 3]));
-              if (other) {
-                const float4 y = *reinterpret_cast<const float4*>(slot + (size_t)(kTile + row) * D + c * 32 + j);
-                v = make_float4(fmaf(a1, y.x, v.x), fmaf(a1, y.y, v.y), fmaf(a1, y.z, v.z), fmaf(a1, y.w, v.w));
+                for (int y = 0; y < 4; ++y) u[y] = bf16x2_fma(u[y], a2, z2);
+                const int chunk = (q & 1) * 4 + (x ^ turn);
+                *reinterpret_cast<uint4*>(line + ((chunk ^ (row & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
               }
-              if (all) store4(p, orow, D, c * 32 + j, v);
-              else *reinterpret_cast<float4*>(slot + (size_t)rho * D + c * 32 + j) = v;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(codes_empty(slot));
+              mbar_arrive(bar(kv ? V_FULL : K_FULL, st));
+            }
+            if (++slot == kRing) slot = 0, code_par ^= 1;
+          }
+        }
+      } while (ok && advance(p, it, end));
+    }
+  } else {
+    regs_up<kRegsSoftmax>();
+    if (any) {
+      // ------------------------------------------------------------ softmax
+      const int x = (warp - 4) >> 2;            // side
+      const int row = (warp & 3) * 32 + lane;   // of the side; TMEM lane quadrant warp % 4
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t t_s = tmem + lanes + x * 128, t_o = tmem + lanes + 256 + x * D;
+      const float2 sl2 = make_float2(p.sl2, p.sl2);
+      const float slack = 8.f / p.sl2;
+      It it = sh.start;
+      uint32_t n = 0, base = 0;                 // the side's tiles, all tiles
+      uint32_t shared = 0;                      // items whose rows both sides had
+      bool more = true;
+      // this thread's query row into shared memory (zeros behind the item's rows)
+      auto load_q = [&](const It& a, const Part& t) {
+        const int rho = t.split ? row : x * kTile + row;
+        uint8_t* dst = smem + L::kQ + x * L::kOperand;
+        const bool in = rho < t.rows;
+        const uint4* src = nullptr;
+        if (in) {
+          const unsigned y = (unsigned)a.rb * kRows + rho, tok = y / (unsigned)p.n_rep;
+          src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
+                                               (a.q.begin + (int)tok) * p.a.qs.token +
+                                               (a.h * p.n_rep + (int)(y - tok * p.n_rep)) * p.a.qs.head);
+        }
+#pragma unroll 8
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = in ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(Q_FULL, x));
+      };
+      Part t = part(p, it, end);
+      if (t.count(x) > 0) load_q(it, t);
+      while (more && ok) {
+        const int cnt = t.count(x);
+        const int rho = t.split ? row : x * kTile + row;
+        const int lim = seen_by(p, it.q, it.rb * kRows + rho);
+        const int least = seen_by(p, it.q, it.rb * kRows + (t.split ? 0 : x * kTile));
+        float m = -INFINITY, top = -INFINITY, l = 0.f;
+        for (int i = 0; i < cnt; ++i, ++n) {
+          const int tile = t.tile(x, i);
+          if (!(ok = warp_wait(bar(S_FULL, x), n & 1, abort, status))) break;
+          tc_fence_after();
+          const int tok0 = (it.u + tile) * kTile;
+          const uint32_t have = sh.valid[(base + tile) & 7];
+          const bool whole = have == (1u << kTiles) - 1 && tok0 + kTile <= least;
+          // all 128 scores in registers: P goes over them in TMEM
+          uint32_t r[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, r[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_wait_ld_of(r[c]);
+          if (!whole) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int rel = lim - tok0 - 32 * c;   // columns below it are seen
+              const int rel0 = (have >> (2 * c)) & 1u ? rel : 0, rel1 = (have >> (2 * c + 1)) & 1u ? rel : 0;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j >= (j < 16 ? rel0 : rel1)) r[c][j] = __float_as_uint(-INFINITY);
             }
           }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              mx[(j >> 1) & 3] =
+                  max3_nan(mx[(j >> 1) & 3], __uint_as_float(r[c][j]), __uint_as_float(r[c][j + 1]));
+          const float hi = max_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]);
+          const bool over = !(hi <= top);
+          float f = 1.f;
+          if (over) {
+            const float mn = max_nan(m, hi * p.sl2);
+            f = ex2(m - mn);
+            m = mn;
+            top = hi + slack;
+            l *= f;
+          }
+          if (i > 0 && __any_sync(0xffffffffu, over)) {
+            // (these scores were formed after the PV before them was done)
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(t_o + c * 16, o);
+              tmem_wait_ld_of(o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st16(t_o + c * 16, o);
+            }
+          }
+          const float nm = m == -INFINITY ? 0.f : -m;
+          const float2 nm2 = make_float2(nm, nm);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 y =
+                  fma2(make_float2(__uint_as_float(r[c][2 * j]), __uint_as_float(r[c][2 * j + 1])), sl2, nm2);
+              const float2 e = make_float2(ex2(y.x), ex2(y.y));
+              sum[j & 1] = add2(sum[j & 1], e);
+              pk[j] = pack_bf16(e.x, e.y);
+            }
+            tmem_st16(t_s + c * 16, pk);
+          }
+          const float2 s2 = add2(sum[0], sum[1]);
+          l += s2.x + s2.y;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(P_FULL, x));
         }
-        if (live) {
-          if (!all) S::ml(slot)[rho] = make_float2(mm, ll);
-          else if (p.a.lse) p.a.lse[orow] = lse_of(mm, ll);
+        if (!ok) break;
+        // the next item's queries, so that its first scores can start
+        const It cur = it;
+        const Part ct = t;
+        more = advance(p, it, end);
+        if (more) {
+          t = part(p, it, end);
+          if (t.count(x) > 0) load_q(it, t);
         }
-      }
-      if (other) {
-        if (x == 0) mbar_arrive(bar(SHARE, 1));  // the slot's upper half may be written again
-        ++shared;
-      }
-      if (cnt > 0) {
-        tc_fence_before();
-        mbar_arrive(bar(O_FREE, x));
-      }
-      if (row == 0 && x == 0 && !all) {
-        if (!starts) {
-          sh.meta.head = ends ? 1 : 2;
-        } else {
-          sh.meta.tail = 1;
-          sh.meta.begin = cur.q.begin;
-          sh.meta.nq = cur.q.nq;
-          sh.meta.h = cur.h;
-          sh.meta.rb = cur.rb;
+        // ---------------------------------------------------------- the piece is done
+        if (cnt > 0) {
+          if (!(ok = warp_wait(bar(PV_DONE, x), (n - 1) & 1, abort, status))) break;
+          tc_fence_after();
         }
+        const bool starts = cur.u == 0, ends = cur.u + ct.n == cur.units, all = starts && ends;
+        float* const slot = ws + (2 * (size_t)blockIdx.x + (starts ? 1 : 0)) * S::kFloats;
+        // side b's share of the tiles of split rows goes through the slot's upper half
+        const bool other = ct.split && ct.n > 1;
+        const int out = other && x == 1 ? kTile + row : rho;
+        const bool live = rho < ct.rows && (cnt > 0);
+        if (other && x == 1) {
+          if (shared > 0 && !(ok = warp_wait(bar(SHARE, 1), (shared - 1) & 1, abort, status))) break;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32(t_o + c * 32, r);
+            tmem_wait_ld_of(r);
+            if (live) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<float4*>(slot + (size_t)out * D + c * 32 + j) =
+                    make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]),
+                                __uint_as_float(r[j + 3]));
+            }
+          }
+          if (live) S::ml(slot)[out] = make_float2(m, l);
+          mbar_arrive(bar(SHARE, 0));
+        }
+        if (other && x == 0 && !(ok = warp_wait(bar(SHARE, 0), shared & 1, abort, status))) break;
+        if (!(ct.split && x == 1) && cnt > 0) {
+          float m1 = -INFINITY, l1 = 0.f;
+          if (other && live) {
+            const float2 ml = S::ml(slot)[kTile + row];
+            m1 = ml.x;
+            l1 = ml.y;
+          }
+          const float mm = max_nan(m, m1), mb = mm == -INFINITY ? 0.f : mm;
+          const float w0 = ex2(m - mb), w1 = ex2(m1 - mb);
+          const float ll = w0 * l + w1 * l1;
+          const float inv = all ? inverse(ll) : 1.f;
+          const int64_t orow = all && live ? out_row(p, cur.q.begin, cur.h, cur.rb, kRows, rho) : 0;
+          const float a0 = w0 * inv, a1 = w1 * inv;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32(t_o + c * 32, r);
+            tmem_wait_ld_of(r);
+            if (live) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                float4 v = make_float4(a0 * __uint_as_float(r[j]), a0 * __uint_as_float(r[j + 1]),
+                                       a0 * __uint_as_float(r[j + 2]), a0 * __uint_as_float(r[j + 3]));
+                if (other) {
+                  const float4 y = *reinterpret_cast<const float4*>(slot + (size_t)(kTile + row) * D + c * 32 + j);
+                  v = make_float4(fmaf(a1, y.x, v.x), fmaf(a1, y.y, v.y), fmaf(a1, y.z, v.z), fmaf(a1, y.w, v.w));
+                }
+                if (all) store4(p, orow, D, c * 32 + j, v);
+                else *reinterpret_cast<float4*>(slot + (size_t)rho * D + c * 32 + j) = v;
+              }
+            }
+          }
+          if (live) {
+            if (!all) S::ml(slot)[rho] = make_float2(mm, ll);
+            else if (p.a.lse) p.a.lse[orow] = lse_of(mm, ll);
+          }
+        }
+        if (other) {
+          if (x == 0) mbar_arrive(bar(SHARE, 1));  // the slot's upper half may be written again
+          ++shared;
+        }
+        if (cnt > 0) {
+          tc_fence_before();
+          mbar_arrive(bar(O_FREE, x));
+        }
+        if (row == 0 && x == 0 && !all) {
+          if (!starts) {
+            sh.meta.head = ends ? 1 : 2;
+          } else {
+            sh.meta.tail = 1;
+            sh.meta.begin = cur.q.begin;
+            sh.meta.nq = cur.q.nq;
+            sh.meta.h = cur.h;
+            sh.meta.rb = cur.rb;
+          }
+        }
+        base += ct.n;
       }
-      base += ct.n;
     }
   }
+  // (what follows runs on the registers that each warpgroup has left)
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -550,8 +580,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0) out_meta[blockIdx.x] = sh.meta;
-  cooperative_groups::this_grid().sync();
-  join_ctas<D, kRows, kThreads>(p, out_meta, ws, reinterpret_cast<Acc*>(smem));
+}
+
+// Items that cross CTAs, in a launch of its own: the register split above does not leave the
+// first kernel's warps alike enough to do it there.
+template <int D>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Params p) {
+  __shared__ Acc scratch[kThreads];
+  griddep_wait();
+  const float* const ws = static_cast<const float*>(p.a.ws);
+  join_ctas<D, kRows, kThreads>(
+      p, reinterpret_cast<const CtaMeta*>(ws + 2 * (size_t)gridDim.x * Slot<D, kRows>::kFloats), ws, scratch);
 }
 
 template <int D, int G>
@@ -559,7 +598,6 @@ static cudaError_t launch(Params p, int sms, cudaStream_t st) {
   auto kern = prompt_kernel<D, G>;
   constexpr int kSmem = Smem<D, G>::kBytes;
   static_assert(kSmem + sizeof(Static) <= 227 * 1024, "shared memory");
-  static_assert(kThreads * sizeof(Acc) <= (size_t)Smem<D, G>::kBar, "scratch of the join");
   static std::atomic<uint64_t> set[2];  // devices whose limit is raised
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -570,17 +608,23 @@ static cudaError_t launch(Params p, int sms, cudaStream_t st) {
       return e;
     if (dev < 128) set[dev >> 6].fetch_or(bit);
   }
+  // a split that does not fit what the launch allocates would wait forever: refused
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+  const int grid = sms < kMaxSms ? sms : kMaxSms;
+  kern<<<grid, kThreads, kSmem, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = sms < kMaxSms ? sms : kMaxSms;
+  cfg.gridDim = grid;
   cfg.blockDim = kThreads;
-  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeCooperative;  // the CTAs meet at a grid barrier
-  at.val.cooperative = 1;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
 }
 
 }  // namespace cprompt

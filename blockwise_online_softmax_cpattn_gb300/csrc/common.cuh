@@ -498,9 +498,8 @@ __device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
                :
                : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&a)[32], uint32_t (&b)[32]) {
-  tmem_wait_ld_of(a);
-  tmem_wait_ld_of(b);
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : CPATTN_RW8(0), CPATTN_RW8(8) : : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
