@@ -11,8 +11,8 @@
 // forms its P, the tensor cores work for the other.
 //
 // Roles (512 threads):
-//   warp 0       issues S = Q K^T of both sides (both operands in shared memory), warp 1
-//                O += P V (P in TMEM, over the scores it came from).
+//   warps 0, 1   issue side a's and b's MMAs: O += P V (P in TMEM, over the scores it came
+//                from) and the next S = Q K^T (both operands in shared memory).
 //   warp 2       loads codes, K and V of a tile apart, into a ring of three.
 //   warps 4-7    side a's softmax, a thread a row; warps 8-11 side b's.
 //   warps 12-15  turn codes into bf16 K and V tiles of 128 tokens with the 128-byte
@@ -63,7 +63,7 @@ struct Smem {
   static constexpr int kCodes = kTile / kCacheTile * kHalf;  // codes of a tile's K or V
   static constexpr int kBar = kCode + kRing * kCodes;
   // barriers: k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], s_full[2], p_full[2],
-  // pv_done[2], o_free[2], share (stored, read), done[2], codes full, empty
+  // o_full[2], o_free[2], share (stored, read), done[2], codes full, empty
   static constexpr int kNumBars = 22 + 2 * kRing;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16;
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + L::kBar;
   auto bar = [&](int group, int i) { return bars + 8 * (2 * group + i); };
-  enum { K_FULL, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, S_FULL, P_FULL, PV_DONE, O_FREE, SHARE, DONE, CODES };
+  enum { K_FULL, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, S_FULL, P_FULL, O_FULL, O_FREE, SHARE, DONE, CODES };
   auto codes_full = [&](int i) { return bars + 8 * (2 * CODES + i); };
   auto codes_empty = [&](int i) { return bars + 8 * (2 * CODES + kRing + i); };
   volatile int* abort = &sh.abort;
@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const int group = i >> 1;
       int n = 1;
       if (group == K_FULL || group == V_FULL || i >= 2 * CODES + kRing) n = 4;  // the warps that dequantise
+      if (group == K_EMPTY || group == V_EMPTY) n = 2;  // both sides
       if (group == Q_FULL || group == P_FULL || group == O_FREE || group == SHARE) n = 128;  // a side's threads
       mbar_init(bars + 8 * i, n);
     }
@@ -205,91 +206,89 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             if (++slot == kRing) slot = 0, par ^= 1;
           }
       }
-    } else if (warp == 0) {
-      // ------------------------------------------------------------ S = Q K^T
+    } else if (warp < 2) {
+      // ------------------------------------------------------------ MMAs of side `warp`
+      // PV of a tile and the scores of the side's next one are issued back to back (the MMAs
+      // of a thread execute in order, so the scores may overwrite the P that PV reads), with
+      // every wait before them: a thread that committed MMAs waits for their end at its next
+      // access to memory.
       const bool leader = elect_one();
       constexpr uint32_t kIdescS = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t kOp = L::kOperand >> 4;
-      const uint64_t qd = sdesc_sw128(sbase + L::kQ, 16, 1024);
-      const uint64_t kd = sdesc_sw128(sbase + L::kK, 16, 1024);
-      It it = sh.start;
-      uint32_t base = 0;                              // tiles of the items before
-      uint32_t items[2] = {0, 0}, tiles[2] = {0, 0};  // per side so far
-      do {
-        const Part t = part(p, it, end);
-        for (int i = 0; ok && i < t.count(0); ++i) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok || i >= t.count(x)) break;
-            const uint32_t g = base + t.tile(x, i);
-            if (i == 0 && !(ok = warp_wait(bar(Q_FULL, x), items[x] & 1, abort, status))) break;
-            if (!(ok = warp_wait(bar(K_FULL, g & 1), (g >> 1) & 1, abort, status))) break;
-            // the side's P before, in the same columns, has been read
-            if (tiles[x] > 0 && !(ok = warp_wait(bar(PV_DONE, x), (tiles[x] - 1) & 1, abort, status))) break;
-            tc_fence_after();
-            const uint64_t k = kd + (uint64_t)((g & 1) * kOp), q = qd + (uint64_t)(x * kOp);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;  // 16 KiB blocks, 32 B steps
-              if (leader) mma_ss(tmem + x * 128, q + off, k + off, kIdescS, kk > 0);
-            }
-            if (leader) {
-              mma_commit(bar(S_FULL, x));
-              if (t.split || x == 1) mma_commit(bar(K_EMPTY, g & 1));
-            }
-            __syncwarp();
-            ++tiles[x];
-          }
-        }
-        base += t.n;
-        ++items[0];
-        if (t.count(1)) ++items[1];
-      } while (ok && advance(p, it, end));
-      // every MMA has finished before TMEM can be freed
-      if (leader) mma_commit(bar(DONE, 0));
-      __syncwarp();
-      drain_wait(bar(DONE, 0), 0);
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ O += P V
-      // (an issuer of its own: the next wait of a thread that committed MMAs waits for them)
-      const bool leader = elect_one();
       constexpr uint32_t kIdescPV = idesc_bf16(128, D, false, true);
       constexpr uint32_t kOp = L::kOperand >> 4;
+      const int x = warp;
+      const uint64_t qd = sdesc_sw128(sbase + L::kQ + x * L::kOperand, 16, 1024);
+      const uint64_t kd = sdesc_sw128(sbase + L::kK, 16, 1024);
       const uint64_t vd = sdesc_sw128(sbase + L::kV, kTile * 128, 1024);
+      const uint32_t t_s = tmem + x * 128, t_o = tmem + 256 + x * D;
       It it = sh.start;
-      uint32_t base = 0, items[2] = {0, 0}, tiles[2] = {0, 0};
+      uint32_t base = 0, items = 0, n = 0;   // tiles of the items before; the side's items, scores
+      // Each side meets every tile's K and V in their order, the other side's tiles of an item
+      // that they share too: waiting for phase j + 1 of a barrier is only safe for one who has
+      // seen phase j.  A tile is free when both have read it or passed it over.
+      uint32_t seen_k = 0, seen_v = 0;       // tiles met
+      auto pass = [&](uint32_t upto, uint32_t& seen, int full, int empty) {
+        for (; ok && seen < upto; ++seen) {
+          ok = warp_wait(bar(full, seen & 1), (seen >> 1) & 1, abort, status);
+          if (ok && leader) mbar_arrive(bar(empty, seen & 1));
+        }
+        return ok;
+      };
+      auto meet = [&](uint32_t tile, uint32_t& seen, int full, int empty) {
+        if (!pass(tile, seen, full, empty)) return false;
+        ++seen;
+        return warp_wait(bar(full, tile & 1), (tile >> 1) & 1, abort, status);
+      };
       do {
         const Part t = part(p, it, end);
-        for (int i = 0; ok && i < t.count(0); ++i) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok || i >= t.count(x)) break;
-            const uint32_t g = base + t.tile(x, i);
-            if (i == 0 && items[x] > 0 && !(ok = warp_wait(bar(O_FREE, x), (items[x] - 1) & 1, abort, status))) break;
-            if (!(ok = warp_wait(bar(V_FULL, g & 1), (g >> 1) & 1, abort, status))) break;
-            if (!(ok = warp_wait(bar(P_FULL, x), tiles[x] & 1, abort, status))) break;
-            tc_fence_after();
-            const uint64_t v = vd + (uint64_t)((g & 1) * kOp);
+        const int cnt = t.count(x);
+        // (V before K, here and below: the tile of K that is waited for may need the passing of
+        // an earlier V)
+        if (!pass(base, seen_v, V_FULL, V_EMPTY)) break;
+        if (cnt == 0 && !(pass(base + t.n, seen_k, K_FULL, K_EMPTY) && pass(base + t.n, seen_v, V_FULL, V_EMPTY))) break;
+        for (int i = 0; i <= cnt && cnt > 0; ++i) {
+          const uint32_t gk = base + t.tile(x, i), gv = base + t.tile(x, i - 1);
+          if (i > 0 && !(ok = meet(gv, seen_v, V_FULL, V_EMPTY))) break;
+          if (i < cnt && !(ok = meet(gk, seen_k, K_FULL, K_EMPTY))) break;
+          if (i == 0 && !(ok = warp_wait(bar(Q_FULL, x), items & 1, abort, status))) break;
+          if (i > 0) {
+            if (i == 1 && items > 0 && !(ok = warp_wait(bar(O_FREE, x), (items - 1) & 1, abort, status))) break;
+            if (!(ok = warp_wait(bar(P_FULL, x), (n - 1) & 1, abort, status))) break;
+          }
+          tc_fence_after();
+          if (i > 0) {
+            const uint64_t v = vd + (uint64_t)((gv & 1) * kOp);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               if (leader)
-                mma_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, v + (uint64_t)(kk * 128), kIdescPV,
-                       (i > 0 || kk > 0) ? 1u : 0u);
+                mma_ts(t_o, t_s + kk * 8, v + (uint64_t)(kk * 128), kIdescPV, (i > 1 || kk > 0) ? 1u : 0u);
             if (leader) {
-              mma_commit(bar(PV_DONE, x));
-              if (t.split || x == 1) mma_commit(bar(V_EMPTY, g & 1));
+              mma_commit(bar(V_EMPTY, gv & 1));
+              if (i == cnt) mma_commit(bar(O_FULL, x));
             }
-            __syncwarp();
-            ++tiles[x];
           }
+          if (i < cnt) {
+            const uint64_t k = kd + (uint64_t)((gk & 1) * kOp);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;  // 16 KiB blocks, 32 B steps
+              if (leader) mma_ss(t_s, qd + off, k + off, kIdescS, kk > 0);
+            }
+            if (leader) {
+              mma_commit(bar(S_FULL, x));
+              mma_commit(bar(K_EMPTY, gk & 1));
+            }
+            ++n;
+          }
+          __syncwarp();
         }
         base += t.n;
-        ++items[0];
-        if (t.count(1)) ++items[1];
+        if (cnt > 0) ++items;
       } while (ok && advance(p, it, end));
-      if (leader) mma_commit(bar(DONE, 1));
+      // every MMA has finished before TMEM can be freed
+      if (leader) mma_commit(bar(DONE, x));
       __syncwarp();
-      drain_wait(bar(DONE, 1), 0);
+      drain_wait(bar(DONE, x), 0);
     }
   } else if (warp >= 12) {
     regs_down<kRegsCodes>();
@@ -367,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const float2 sl2 = make_float2(p.sl2, p.sl2);
       const float slack = 8.f / p.sl2;
       It it = sh.start;
-      uint32_t n = 0, base = 0;                 // the side's tiles, all tiles
+      uint32_t n = 0, base = 0, items = 0;      // the side's tiles, all tiles, the side's items
       uint32_t shared = 0;                      // items whose rows both sides had
       bool more = true;
       // this thread's query row into shared memory (zeros behind the item's rows)
@@ -483,7 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         // ---------------------------------------------------------- the piece is done
         if (cnt > 0) {
-          if (!(ok = warp_wait(bar(PV_DONE, x), (n - 1) & 1, abort, status))) break;
+          if (!(ok = warp_wait(bar(O_FULL, x), items & 1, abort, status))) break;
+          ++items;
           tc_fence_after();
         }
         const bool starts = cur.u == 0, ends = cur.u + ct.n == cur.units, all = starts && ends;

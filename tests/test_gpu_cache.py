@@ -411,6 +411,23 @@ def test_attn_float32_output_of_bf16(n_q):
     Case(cp_mod(), n_q=[n_q, n_q], kv_len=[400, 150], o_dtype="f32", seed=5).check()
 
 
+@pytest.mark.parametrize("seed", range(3))
+@pytest.mark.parametrize("n_q", [12, 16, 40])
+def test_attn_many_items_of_a_cta(n_q, seed):
+    """Wide drafts: a CTA meets many items of odd and even numbers of tiles, of one half and of
+    two, one after the other, call behind call."""
+    rng = np.random.default_rng(seed)
+    R = 24
+    kv = rng.integers(1, 9, R) * 128 - rng.integers(0, 128, R)
+    kv[rng.integers(0, R, 3)] = 0
+    nq = rng.integers(1, n_q + 1, R)
+    nq[:2] = n_q
+    c = Case(cp_mod(), H_q=32, H_kv=4, n_q=nq, kv_len=kv, seed=seed, page=32)
+    for _ in range(60):
+        cp_mod().check(c.run())
+    c.check()
+
+
 @pytest.mark.parametrize("n_q", [1, 100])
 def test_attn_without_lse(n_q):
     Case(cp_mod(), n_q=[n_q], kv_len=[130], fused=False).check(lse=False)
