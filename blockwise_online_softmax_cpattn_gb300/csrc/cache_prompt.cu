@@ -492,8 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const bool other = ct.split && ct.n > 1;
         const int out = other && x == 1 ? kTile + row : rho;
         const bool live = rho < ct.rows && (cnt > 0);
+        // side b's rows of a slot may hold what side a has yet to read
+        if (x == 1 && shared > 0 && (other || !all) &&
+            !(ok = warp_wait(bar(SHARE, 1), (shared - 1) & 1, abort, status)))
+          break;
         if (other && x == 1) {
-          if (shared > 0 && !(ok = warp_wait(bar(SHARE, 1), (shared - 1) & 1, abort, status))) break;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t r[32];
