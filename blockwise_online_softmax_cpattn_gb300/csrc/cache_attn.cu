@@ -127,42 +127,48 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
   CtaMeta* const out_meta = reinterpret_cast<CtaMeta*>(ws + W::meta(gridDim.x));
   // ---- the CTA's pieces -------------------------------------------------------
   // Pieces in order: number 2 w is warp w's head, 2 w + 1 its tail.  A tail begins a group
-  // of pieces of one item, a head that ends the item closes one.  RB D / 4 threads join a
-  // group, each 4 channels of a row; the groups are shared out among such sets of threads.
+  // of pieces of one item, a head that ends the item closes one.  The rows of the groups are
+  // shared out among the warps, 4 channels a lane.
   static_assert(2 * WARPS <= 32, "a bit per piece");
-  constexpr int V = D / 4, kSets = WARPS * 32 / (RB * V) > 0 ? WARPS * 32 / (RB * V) : 1;
+  const int warp = threadIdx.x >> 5;
   const bool mine = lane < 2 * WARPS;
   const int state = !mine ? 0 : (lane & 1) ? meta[lane >> 1].tail : meta[lane >> 1].head;
   const uint32_t pieces = __ballot_sync(0xffffffffu, state != 0);
   const uint32_t tails = __ballot_sync(0xffffffffu, (lane & 1) && state != 0);
   const uint32_t closing = __ballot_sync(0xffffffffu, !(lane & 1) && state == 1);
+  const uint32_t leads = tails | (pieces & (0u - pieces));
   float* const cta_slots = ws + W::cta_slots(gridDim.x) + 2 * (size_t)blockIdx.x * S::kFloats;
-  const int set = threadIdx.x / (RB * V);
+  if (threadIdx.x == 0) {
+    CtaMeta cm = {0, 0, 0, 0, 0, 0};
+    if (pieces & ~tails & (leads & (0u - leads))) {  // the first group began in an earlier CTA
+      const uint32_t rest = leads & (leads - 1), first = leads & (0u - leads);
+      cm.head = (closing & (rest ? (rest & (0u - rest)) - first : 0u - first)) ? 1 : 2;
+    }
+    if (tails) {
+      const int last = 31 - __clz(tails);
+      if (!(closing >> last)) {
+        const PieceMeta& m = meta[last >> 1];
+        cm.tail = 1;
+        cm.begin = m.begin;
+        cm.nq = m.nq;
+        cm.h = m.h;
+        cm.rb = m.rb;
+      }
+    }
+    out_meta[blockIdx.x] = cm;
+  }
   int k = 0;
-  for (uint32_t lead = tails | (pieces & (0u - pieces)); lead; lead &= lead - 1, ++k) {
+  for (uint32_t lead = leads; lead; lead &= lead - 1, ++k) {
     const uint32_t first = lead & (0u - lead), rest = lead & (lead - 1);
     const uint32_t ids = pieces & (rest ? (rest & (0u - rest)) - first : 0u - first);
     const bool begun = (first & tails) != 0, ended = (ids & closing) != 0;
-    const int owner = (__ffs(first) - 1) >> 1;
-    if (threadIdx.x == 0) {
-      CtaMeta* cm = &out_meta[blockIdx.x];
-      if (k == 0) {
-        cm->head = begun ? 0 : ended ? 1 : 2;
-        cm->tail = 0;
-      }
-      if (begun && !ended) {
-        cm->tail = 1;
-        cm->begin = meta[owner].begin;
-        cm->nq = meta[owner].nq;
-        cm->h = meta[owner].h;
-        cm->rb = meta[owner].rb;
-      }
-    }
-    if (kSets > 1 && k % kSets != set) continue;
-    const int rows = begun ? meta[owner].rows : meta[owner].head_rows;
+    const PieceMeta& own = meta[(__ffs(first) - 1) >> 1];
+    const int rows = begun ? own.rows : own.head_rows;
     float* const to = cta_slots + (begun ? S::kFloats : 0);
-    for (int e = threadIdx.x - (kSets > 1 ? set * RB * V : 0); e < rows * V; e += kSets > 1 ? RB * V : WARPS * 32) {
-      const int row = e / V, ch = (e - row * V) * 4;
+    // RPW rows at a time: row r of group k is the job of warp (k RB + r) / RPW
+    constexpr int V = D / 4, RPW = 32 / V;
+    for (int row = ((warp + 64 * WARPS - k * (RB / RPW)) % WARPS) * RPW + lane / V; row < rows; row += WARPS * RPW) {
+      const int ch = lane % V * 4;
       Acc acc;
       for (uint32_t b = ids; b; b &= b - 1) {
         const int id = __ffs(b) - 1, w = id >> 1;
@@ -172,18 +178,16 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
         acc.add(S::ml(s)[row], *reinterpret_cast<const float4*>(s + row * D + ch));
       }
       if (begun && ended) {
-        const PieceMeta& m = meta[owner];
-        write_out<D>(p, out_row(p, m.begin, m.h, m.rb, RB, row), ch, acc.m, acc.l, acc.o);
+        write_out<D>(p, out_row(p, own.begin, own.h, own.rb, RB, row), ch, acc.m, acc.l, acc.o);
       } else {
         *reinterpret_cast<float4*>(to + row * D + ch) = acc.o;
         if (ch == 0) S::ml(to)[row] = make_float2(acc.m, acc.l);
       }
     }
   }
-  if (threadIdx.x == 0 && pieces == 0) out_meta[blockIdx.x].head = out_meta[blockIdx.x].tail = 0;
 
   cooperative_groups::this_grid().sync();
-  join_ctas<D, RB, WARPS * 32>(p, out_meta, ws + W::cta_slots(gridDim.x), reinterpret_cast<Acc*>(smem));
+  join_ctas<D, RB, WARPS * 32>(p, out_meta, ws + W::cta_slots(gridDim.x), smem);
 }
 
 template <int D, int G, int NT, int NS, int WARPS, int MINB>
@@ -662,11 +666,14 @@ template <int D, int G>
 static cudaError_t launch_attn(const cattn::Params& p, int sms, cudaStream_t st) {
   using namespace cattn;
   if (!p.c.bf16) return Exact8<D, G>::launch(p, sms, st);
+  // 8 rows at a time while that is all a request has, else 16.  Past three blocks of 16 every
+  // one of which unpacks the codes again, 64 rows and 112 us, the tensor memory's kernel is
+  // faster: 99 us for up to 128 rows (32 drafts of up to 8 heads a K/V group, 500 to 12000
+  // cached tokens).
   const int64_t rows = (int64_t)p.a.max_q * p.n_rep;
-  if (rows > 16) return launch_cache_prompt(p, sms, st);
-  // 8 rows at a time while that is all a request has
   if (rows <= 8) return Rows8<D, G>::launch(p, sms, st);
-  return Rows16<D, G>::launch(p, sms, st);
+  if (rows <= 48) return Rows16<D, G>::launch(p, sms, st);
+  return launch_cache_prompt(p, sms, st);
 }
 
 cudaError_t launch_cache_attn(const Cache& c, const CacheAttnArgs& a, cudaStream_t st) {

@@ -13,7 +13,8 @@
 // Roles (512 threads):
 //   warps 0, 1   issue side a's and b's MMAs: O += P V (P in TMEM, over the scores it came
 //                from) and the next S = Q K^T (both operands in shared memory).
-//   warp 2       loads codes, K and V of a tile apart, into a ring of three.
+//   warp 2       loads codes, K and V of a tile apart, into a ring of three; warp 3 keeps count
+//                of the tiles that are ready.
 //   warps 4-7    side a's softmax, a thread a row; warps 8-11 side b's.
 //   warps 12-15  turn codes into bf16 K and V tiles of 128 tokens with the 128-byte
 //                swizzle that the MMA reads, two of each.
@@ -63,8 +64,9 @@ struct Smem {
   static constexpr int kCodes = kTile / kCacheTile * kHalf;  // codes of a tile's K or V
   static constexpr int kBar = kCode + kRing * kCodes;
   // barriers: k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], s_full[2], p_full[2],
-  // o_full[2], o_free[2], share (stored, read), done[2], codes full, empty
-  static constexpr int kNumBars = 22 + 2 * kRing;
+  // o_full[2], o_free[2], share (stored, read), turn[2], done[2], codes full,
+  // empty
+  static constexpr int kNumBars = 24 + 2 * kRing;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16;
 };
@@ -78,7 +80,25 @@ struct Static {
   uint32_t valid[8];   // per tile (the last 8): which of its 16-token tiles are there
   int abort;
   uint32_t tmem;
+  volatile int seen_k, seen_v;   // tiles whose K, V is ready
 };
+
+// Waits until *c reaches `want`, bounded as the waits for barriers are.
+__device__ __forceinline__ bool count_wait(const volatile int* c, int want, volatile int* abort, int* status) {
+  bool ok = *c >= want;
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1; !(ok = *c >= want); ++i)
+      if ((i & 63u) == 0 && (*abort || globaltimer_ns() - t0 > kTimeoutNs)) break;
+    if (!ok && !*abort) {
+      *abort = 1;
+      latch_status(status, kStatusTimeout);
+    }
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  __threadfence_block();
+  return ok;
+}
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t par, volatile int* abort, int* status) {
   return __all_sync(0xffffffffu, mbar_wait(bar, par, abort, status, kTimeoutNs));
@@ -120,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + L::kBar;
   auto bar = [&](int group, int i) { return bars + 8 * (2 * group + i); };
-  enum { K_FULL, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, S_FULL, P_FULL, O_FULL, O_FREE, SHARE, DONE, CODES };
+  enum { K_FULL, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, S_FULL, P_FULL, O_FULL, O_FREE, SHARE, TURN, DONE, CODES };
   auto codes_full = [&](int i) { return bars + 8 * (2 * CODES + i); };
   auto codes_empty = [&](int i) { return bars + 8 * (2 * CODES + kRing + i); };
   volatile int* abort = &sh.abort;
@@ -132,13 +152,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     for (int i = 0; i < L::kNumBars; ++i) {
       const int group = i >> 1;
       int n = 1;
-      if (group == K_FULL || group == V_FULL || i >= 2 * CODES + kRing) n = 4;  // the warps that dequantise
-      if (group == K_EMPTY || group == V_EMPTY) n = 2;  // both sides
+      if (group == K_FULL || group == V_FULL || group == TURN || i >= 2 * CODES + kRing) n = 4;  // a warpgroup's warps
+      if (group == K_EMPTY || group == V_EMPTY) n = 3;  // both sides, the count's keeper
       if (group == Q_FULL || group == P_FULL || group == O_FREE || group == SHARE) n = 128;  // a side's threads
       mbar_init(bars + 8 * i, n);
     }
     sh.abort = (sbase & 1023u) ? 1 : 0;  // the layout has no alignment slack
     if (sh.abort) latch_status(status, kStatusLaunch);
+    sh.seen_k = sh.seen_v = 0;
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -206,7 +227,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             if (++slot == kRing) slot = 0, par ^= 1;
           }
       }
-    } else if (warp < 2) {
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ which tiles are ready
+      // A barrier's phases can only be waited for one by one, and a side that shares an item
+      // passes over every other tile: this warp meets all of them and keeps count.  It takes
+      // part in a tile's release, so no phase goes by it.
+      It it = sh.start;
+      uint32_t n = 0;
+      do {
+        const int tiles = it.left(end);
+        for (int i = 0; ok && i < tiles; ++i, ++n) {
+          if (!(ok = warp_wait(bar(K_FULL, n & 1), (n >> 1) & 1, abort, status))) break;
+          if (lane == 0) {
+            __threadfence_block();
+            sh.seen_k = n + 1;
+            mbar_arrive(bar(K_EMPTY, n & 1));
+          }
+          if (!(ok = warp_wait(bar(V_FULL, n & 1), (n >> 1) & 1, abort, status))) break;
+          if (lane == 0) {
+            __threadfence_block();
+            sh.seen_v = n + 1;
+            mbar_arrive(bar(V_EMPTY, n & 1));
+          }
+        }
+      } while (ok && advance(p, it, end));
+    } else {
       // ------------------------------------------------------------ MMAs of side `warp`
       // PV of a tile and the scores of the side's next one are issued back to back (the MMAs
       // of a thread execute in order, so the scores may overwrite the P that PV reads), with
@@ -223,33 +268,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const uint32_t t_s = tmem + x * 128, t_o = tmem + 256 + x * D;
       It it = sh.start;
       uint32_t base = 0, items = 0, n = 0;   // tiles of the items before; the side's items, scores
-      // Each side meets every tile's K and V in their order, the other side's tiles of an item
-      // that they share too: waiting for phase j + 1 of a barrier is only safe for one who has
-      // seen phase j.  A tile is free when both have read it or passed it over.
-      uint32_t seen_k = 0, seen_v = 0;       // tiles met
-      auto pass = [&](uint32_t upto, uint32_t& seen, int full, int empty) {
-        for (; ok && seen < upto; ++seen) {
-          ok = warp_wait(bar(full, seen & 1), (seen >> 1) & 1, abort, status);
-          if (ok && leader) mbar_arrive(bar(empty, seen & 1));
-        }
-        return ok;
-      };
-      auto meet = [&](uint32_t tile, uint32_t& seen, int full, int empty) {
-        if (!pass(tile, seen, full, empty)) return false;
-        ++seen;
-        return warp_wait(bar(full, tile & 1), (tile >> 1) & 1, abort, status);
-      };
       do {
         const Part t = part(p, it, end);
         const int cnt = t.count(x);
-        // (V before K, here and below: the tile of K that is waited for may need the passing of
-        // an earlier V)
-        if (!pass(base, seen_v, V_FULL, V_EMPTY)) break;
-        if (cnt == 0 && !(pass(base + t.n, seen_k, K_FULL, K_EMPTY) && pass(base + t.n, seen_v, V_FULL, V_EMPTY))) break;
         for (int i = 0; i <= cnt && cnt > 0; ++i) {
           const uint32_t gk = base + t.tile(x, i), gv = base + t.tile(x, i - 1);
-          if (i > 0 && !(ok = meet(gv, seen_v, V_FULL, V_EMPTY))) break;
-          if (i < cnt && !(ok = meet(gk, seen_k, K_FULL, K_EMPTY))) break;
+          if (i > 0 && !(ok = count_wait(&sh.seen_v, gv + 1, abort, status))) break;
+          // (sides that share an item wait for its K tiles one after the other: there PV goes first)
+          if (i < cnt && (i == 0 || !t.split) && !(ok = count_wait(&sh.seen_k, gk + 1, abort, status))) break;
           if (i == 0 && !(ok = warp_wait(bar(Q_FULL, x), items & 1, abort, status))) break;
           if (i > 0) {
             if (i == 1 && items > 0 && !(ok = warp_wait(bar(O_FREE, x), (items - 1) & 1, abort, status))) break;
@@ -263,11 +289,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               if (leader)
                 mma_ts(t_o, t_s + kk * 8, v + (uint64_t)(kk * 128), kIdescPV, (i > 1 || kk > 0) ? 1u : 0u);
             if (leader) {
+              if (t.split) mbar_arrive(bar(V_EMPTY, gv & 1));  // for the side that passes it over
               mma_commit(bar(V_EMPTY, gv & 1));
               if (i == cnt) mma_commit(bar(O_FULL, x));
             }
           }
           if (i < cnt) {
+            if (i > 0 && t.split) {
+              __syncwarp();
+              if (!(ok = count_wait(&sh.seen_k, gk + 1, abort, status))) break;
+              tc_fence_after();
+            }
             const uint64_t k = kd + (uint64_t)((gk & 1) * kOp);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -276,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             }
             if (leader) {
               mma_commit(bar(S_FULL, x));
+              if (t.split) mbar_arrive(bar(K_EMPTY, gk & 1));
               mma_commit(bar(K_EMPTY, gk & 1));
             }
             ++n;
@@ -317,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             const uint32_t have = sh.valid[n & 7];
             const uint8_t* codes = smem + L::kCode + slot * L::kCodes;
             uint8_t* dst = smem + (kv ? L::kV : L::kK) + st * L::kOperand;
-#pragma unroll 2
+#pragma unroll 1
             for (int s = 0; s < kSteps; ++s) {
               const int stored = s * kRowsAtOnce + r0, tile = stored / kCacheTile, rr = stored % kCacheTile;
               // stored row t + 4e of eight is token 2t + e
@@ -367,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const float slack = 8.f / p.sl2;
       It it = sh.start;
       uint32_t n = 0, base = 0, items = 0;      // the side's tiles, all tiles, the side's items
-      uint32_t shared = 0;                      // items whose rows both sides had
+      uint32_t shared = 0, turns = 0;           // items whose rows both sides had; tiles in turn
       bool more = true;
       // this thread's query row into shared memory (zeros behind the item's rows)
       auto load_q = [&](const It& a, const Part& t) {
@@ -400,6 +433,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int i = 0; i < cnt; ++i, ++n) {
           const int tile = t.tile(x, i);
           if (!(ok = warp_wait(bar(S_FULL, x), n & 1, abort, status))) break;
+          // Sides with the same tiles take turns: side a's tile, then side b's once a is halfway.
+          // Left alone they may fall in step, both working and then both waiting for the tensor
+          // cores (0.97 ms of the chunk that takes 0.81 so; a turn of a whole tile: 0.90).
+          if (!t.split) {
+            if ((x == 1 || turns > 0) && !(ok = warp_wait(bar(TURN, x), (turns - (x == 0)) & 1, abort, status))) break;
+            ++turns;
+          }
           tc_fence_after();
           const int tok0 = (it.u + tile) * kTile;
           const uint32_t have = sh.valid[(base + tile) & 7];
@@ -464,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               pk[j] = pack_bf16(e.x, e.y);
             }
             tmem_st16(t_s + c * 16, pk);
+            if (c == 1 && !t.split && lane == 0) mbar_arrive(bar(TURN, 1 - x));
           }
           const float2 s2 = add2(sum[0], sum[1]);
           l += s2.x + s2.y;
@@ -589,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 // first kernel's warps alike enough to do it there.
 template <int D>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Params p) {
-  __shared__ Acc scratch[kThreads];
+  __shared__ __align__(16) uint8_t scratch[kJoinBytes<kThreads>];
   griddep_wait();
   const float* const ws = static_cast<const float*>(p.a.ws);
   join_ctas<D, kRows, kThreads>(

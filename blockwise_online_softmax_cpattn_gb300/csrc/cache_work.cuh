@@ -254,15 +254,17 @@ __device__ __forceinline__ void cta_run(int64_t total, int64_t& c0, int64_t& c1)
   c0 = part_of(total, cta, ctas);
   c1 = part_of(total, min(cta + 1, ctas), ctas);
 }
-// The item and unit at place v of the line (r = n_req behind its end).
+// The item and unit at place v of the line (r = n_req behind its end).  Called by a whole warp;
+// each half looks for a place of its own.
 template <typename It>
 __device__ __forceinline__ It item_at(const Params& p, const int64_t* sums, int64_t v) {
-  int lo = 0, hi = kSums;  // first entry whose sum is past v
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (sums[mid] > v) hi = mid;
-    else lo = mid + 1;
-  }
+  static_assert(kSums == 256, "16 entries of 16");
+  // first entry whose sum is past v: first its sixteen, then it
+  const int lane = threadIdx.x & 31, i = lane & 15, half = lane & 16;
+  const uint32_t b0 = __ballot_sync(0xffffffffu, sums[16 * i + 15] > v) >> half & 0xffffu;
+  const int g = b0 ? __ffs(b0) - 1 : 15;
+  const uint32_t b1 = __ballot_sync(0xffffffffu, sums[16 * g + i] > v) >> half & 0xffffu;
+  const int lo = b1 ? 16 * g + __ffs(b1) - 1 : kSums;
   It x;
   x.seen = x.units = 0;
   x.q = {0, 0, 0};
@@ -275,13 +277,21 @@ __device__ __forceinline__ It item_at(const Params& p, const int64_t* sums, int6
 // ---------------------------------------------------------------------------
 // An item's CTAs are the one that began it (its tail piece) and those behind it up to the one
 // that ends it (their head pieces); each joins a part of the item's numbers.  slots: a head
-// and a tail slot per CTA; scratch: THREADS Accs of shared memory.  Few numbers leave threads
-// over: those share the pieces and meet in the scratch.
+// and a tail slot per CTA; smem: kJoinBytes.  The states come in one load; few numbers leave
+// threads over: those share the pieces and meet in shared memory.
+template <int THREADS>
+constexpr int kJoinBytes = THREADS * (int)sizeof(Acc) + kMaxSms * (int)sizeof(CtaMeta);
 template <int D, int RB, int THREADS>
-__device__ __forceinline__ void join_ctas(const Params& p, const CtaMeta* meta, const float* slots, Acc* scratch) {
+__device__ __forceinline__ void join_ctas(const Params& p, const CtaMeta* states, const float* slots, void* smem) {
   using S = Slot<D, RB>;
   constexpr int V = D / 4;
+  static_assert(THREADS >= kMaxSms, "a state a thread");
+  Acc* const scratch = static_cast<Acc*>(smem);
+  CtaMeta* const meta = reinterpret_cast<CtaMeta*>(scratch + THREADS);
   const int lane = threadIdx.x & 31, me = blockIdx.x, ctas = gridDim.x;
+  if ((int)threadIdx.x < ctas) meta[threadIdx.x] = states[threadIdx.x];
+  __syncthreads();
+#pragma unroll 1
   for (int which = 0; which < 2; ++which) {  // the item of this CTA's head, that of its tail
     int owner = me;
     if (which == 0) {
@@ -295,7 +305,6 @@ __device__ __forceinline__ void join_ctas(const Params& p, const CtaMeta* meta, 
     } else if (meta[me].tail == 0) {
       continue;
     }
-    const CtaMeta cm = meta[owner];
     int n = ctas - owner;  // the item's CTAs
     for (int i = owner + 1; i < ctas; i += 32) {
       const uint32_t b = __ballot_sync(0xffffffffu, i + lane < ctas && meta[min(i + lane, ctas - 1)].head != 2);
@@ -305,27 +314,47 @@ __device__ __forceinline__ void join_ctas(const Params& p, const CtaMeta* meta, 
       }
     }
     n = min(n, ctas - owner);
+    const CtaMeta cm = meta[owner];
     const int all = block_rows(p, cm.nq, cm.rb, RB) * V;
-    const int e0 = (int)((int64_t)all * (me - owner) / n), e1 = (int)((int64_t)all * (me - owner + 1) / n);
+    const int e0 = all * (me - owner) / n, e1 = all * (me - owner + 1) / n;
     const int parts = e1 - e0;
     if (parts <= 0) continue;
     const int shares = max(1, min(THREADS / parts, n)), share = threadIdx.x / parts;
     const float* const first = slots + 2 * (size_t)owner * S::kFloats;
-    if (shares > 1) __syncthreads();  // the scratch of the item before
-    for (int i0 = shares > 1 ? threadIdx.x % parts : threadIdx.x; i0 < parts; i0 += shares > 1 ? parts : THREADS) {
-      const int row = (e0 + i0) / V, ch = (e0 + i0 - row * V) * 4;
+    if (shares == 1) {
+      // four numbers' loads at a time (the stores in between might alias them otherwise)
+      for (int i0 = threadIdx.x; i0 < parts; i0 += 4 * THREADS) {
+        Acc acc[4];
+        for (int i = 0; i < n; ++i) {
+          const float* s = first + (i ? 2 * (size_t)i : 1) * S::kFloats;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int e = e0 + min(i0 + u * THREADS, parts - 1), row = e / V, ch = (e - row * V) * 4;
+            acc[u].add(S::ml(s)[row], *reinterpret_cast<const float4*>(s + row * D + ch));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (i0 + u * THREADS >= parts) break;
+          const int e = e0 + i0 + u * THREADS, row = e / V, ch = (e - row * V) * 4;
+          write_out<D>(p, out_row(p, cm.begin, cm.h, cm.rb, RB, row), ch, acc[u].m, acc[u].l, acc[u].o);
+        }
+      }
+      continue;
+    }
+    __syncthreads();  // the scratch of the item before
+    {
+      const int e = e0 + threadIdx.x % parts, row = e / V, ch = (e - row * V) * 4;
       Acc acc;
-      if (share < shares || shares == 1) {
+      if (share < shares) {
 #pragma unroll 4
-        for (int i = shares > 1 ? share : 0; i < n; i += shares) {
+        for (int i = share; i < n; i += shares) {
           const float* s = first + (i ? 2 * (size_t)i : 1) * S::kFloats;
           acc.add(S::ml(s)[row], *reinterpret_cast<const float4*>(s + row * D + ch));
         }
       }
-      if (shares > 1) scratch[threadIdx.x] = acc;
-      else write_out<D>(p, out_row(p, cm.begin, cm.h, cm.rb, RB, row), ch, acc.m, acc.l, acc.o);
+      scratch[threadIdx.x] = acc;
     }
-    if (shares == 1) continue;
     __syncthreads();
     if ((int)threadIdx.x < parts) {
       Acc acc = scratch[threadIdx.x];
