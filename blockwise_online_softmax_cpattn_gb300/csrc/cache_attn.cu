@@ -8,8 +8,9 @@
 //
 //   Work.  Every warp on the GPU takes an equal run of the line of items (8 NT rows each,
 //   units of 32 tokens).  Pieces are joined first among the warps of a CTA in shared
-//   memory, then, for items that cross CTAs, behind a grid barrier from the workspace (a
-//   second launch in its place cost 2 us more a call).
+//   memory, then, for items that cross CTAs, by the CTA that began the item from the
+//   workspace, with a flag for each piece (a grid barrier in their place cost 2 us more a
+//   call, a second launch 4).
 //
 //   Loads.  A tile of 16 tokens of one K/V head is contiguous (codes and their (a, z)):
 //   one bulk copy, of two tiles where a page holds both.  Each warp keeps a ring of
@@ -30,11 +31,11 @@
 //
 // float32 (NS = 3): q and P are sums of three bf16 numbers, the cached values are bf16
 // numbers anyway, so three MMAs give products of float32 quality.
-#include <cooperative_groups.h>
 #include <math.h>
 
 #include <algorithm>
 #include <atomic>
+#include <chrono>
 
 #include "cache_work.cuh"
 
@@ -45,12 +46,12 @@ constexpr int kUnit = 32;            // cached tokens of a unit: two tiles
 constexpr int kItemCost = 3;         // an item's start and end, in units
 
 // Workspace of a launch of at most `ctas` CTAs: a slot per warp (head pieces that other
-// work followed), a head and a tail slot per CTA, their states.
+// work followed), a head and a tail slot per CTA, a flag per CTA.
 template <int D, int RB, int WARPS>
 struct Work {
   static constexpr size_t kSlot = (size_t)Slot<D, RB>::kFloats;
   static __host__ __device__ size_t cta_slots(int ctas) { return (size_t)ctas * WARPS * kSlot; }
-  static __host__ __device__ size_t meta(int ctas) { return (size_t)ctas * (WARPS + 2) * kSlot; }
+  static __host__ __device__ size_t flags(int ctas) { return (size_t)ctas * (WARPS + 2) * kSlot; }
 };
 
 // ---------------------------------------------------------------------------
@@ -86,7 +87,8 @@ struct PieceMeta {
   int head;         // 0 none, 1 ends the item, 2 goes on
   int head_global;  // the head piece is in the workspace, not in shared memory
   int tail;         // 1: open
-  int rows, begin, h, rb, nq;  // of the tail's item
+  int rows, begin, h, rb;      // of the tail's item
+  int left;                    // its units behind the warp's run
   int head_rows;
 };
 template <typename It, int WARPS>
@@ -95,6 +97,8 @@ struct Shared {
   int64_t warp_part[WARPS];
   uint64_t bars[WARPS * 8];
   int abort;
+  int ctas;                     // that have work
+  int64_t c0, c1, total;        // this CTA's run of the line, the line's length
   PieceMeta meta[WARPS];
   // per warp, what the main loop has no registers for: the items that are being loaded and
   // computed, and the run's end
@@ -109,6 +113,12 @@ __device__ __forceinline__ void find_run(const Params& p, Shared<It, WARPS>& sh)
   const int64_t total = sum_costs<It, WARPS * 32>(p, sh.sums, sh.warp_part);
   int64_t c0, c1;
   cta_run(total, c0, c1);
+  if (threadIdx.x == 0) {
+    sh.ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total));
+    sh.c0 = c0;
+    sh.c1 = c1;
+    sh.total = max((int64_t)1, total);
+  }
   // one half of the lanes looks for each
   const It x = item_at<It>(p, sh.sums, c0 + part_of(c1 - c0, warp + (lane >> 4), WARPS));
   if (lane == 0) sh.in[warp] = sh.it[warp] = x;
@@ -124,7 +134,7 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
   const int lane = threadIdx.x & 31;
   const PieceMeta* meta = sh.meta;
   float* const ws = static_cast<float*>(p.a.ws);
-  CtaMeta* const out_meta = reinterpret_cast<CtaMeta*>(ws + W::meta(gridDim.x));
+  uint64_t* const flags = reinterpret_cast<uint64_t*>(ws + W::flags(gridDim.x));
   // ---- the CTA's pieces -------------------------------------------------------
   // Pieces in order: number 2 w is warp w's head, 2 w + 1 its tail.  A tail begins a group
   // of pieces of one item, a head that ends the item closes one.  The rows of the groups are
@@ -138,25 +148,6 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
   const uint32_t closing = __ballot_sync(0xffffffffu, !(lane & 1) && state == 1);
   const uint32_t leads = tails | (pieces & (0u - pieces));
   float* const cta_slots = ws + W::cta_slots(gridDim.x) + 2 * (size_t)blockIdx.x * S::kFloats;
-  if (threadIdx.x == 0) {
-    CtaMeta cm = {0, 0, 0, 0, 0, 0};
-    if (pieces & ~tails & (leads & (0u - leads))) {  // the first group began in an earlier CTA
-      const uint32_t rest = leads & (leads - 1), first = leads & (0u - leads);
-      cm.head = (closing & (rest ? (rest & (0u - rest)) - first : 0u - first)) ? 1 : 2;
-    }
-    if (tails) {
-      const int last = 31 - __clz(tails);
-      if (!(closing >> last)) {
-        const PieceMeta& m = meta[last >> 1];
-        cm.tail = 1;
-        cm.begin = m.begin;
-        cm.nq = m.nq;
-        cm.h = m.h;
-        cm.rb = m.rb;
-      }
-    }
-    out_meta[blockIdx.x] = cm;
-  }
   int k = 0;
   for (uint32_t lead = leads; lead; lead &= lead - 1, ++k) {
     const uint32_t first = lead & (0u - lead), rest = lead & (lead - 1);
@@ -186,8 +177,65 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
     }
   }
 
-  cooperative_groups::this_grid().sync();
-  join_ctas<D, RB, WARPS * 32>(p, out_meta, ws + W::cta_slots(gridDim.x), smem);
+  // ---- items that cross CTAs ----------------------------------------------------
+  // The CTA that began one waits for the head pieces of the CTAs behind it up to the one that
+  // ends the item (which wait for nobody before they publish theirs; all CTAs are resident)
+  // and joins them with its tail.  How many those are follows from the line.  A flag is this
+  // launch's own number, put there by the piece's CTA and taken away by the one that waits.
+  __syncthreads();  // the slots are written
+  if (sh.abort) return;
+  if ((pieces & ~tails & (leads & (0u - leads))) && threadIdx.x == 0) {
+    __threadfence();
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(flags + blockIdx.x), "l"(p.nonce) : "memory");
+  }
+  const int last = tails ? 31 - __clz(tails) : 0;
+  if (!tails || (closing >> last)) return;
+  const PieceMeta own = meta[last >> 1];
+  const int64_t item_end = sh.c0 + part_of(sh.c1 - sh.c0, (last >> 1) + 1, WARPS) + own.left;
+  const int behind = min((int)((item_end * sh.ctas + sh.total - 1) / sh.total) - 1, sh.ctas - 1) - (int)blockIdx.x;
+  bool ok = true;
+  for (int i = threadIdx.x; i < behind; i += WARPS * 32) {
+    uint64_t* const f = flags + blockIdx.x + 1 + i;
+    uint64_t v = 0, t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(f) : "memory");
+      if (v == p.nonce || ((it & 63u) == 0 && globaltimer_ns() - t0 > kTimeoutNs)) break;
+    }
+    ok = ok && v == p.nonce;
+    *f = 0;
+  }
+  if (!__syncthreads_and(ok)) {
+    if (threadIdx.x == 0) latch_status(p.a.status, kStatusTimeout);
+    return;
+  }
+  // few numbers leave threads over: those share the pieces and meet in shared memory
+  constexpr int V = D / 4, THREADS = WARPS * 32;
+  const int parts = own.rows * V, n = behind + 1;
+  const int shares = max(1, min(THREADS / parts, n)), share = threadIdx.x / parts;
+  Acc* const meet = reinterpret_cast<Acc*>(smem);
+  for (int e = shares > 1 ? threadIdx.x % parts : threadIdx.x; e < parts; e += shares > 1 ? parts : THREADS) {
+    const int row = e / V, ch = (e - row * V) * 4;
+    Acc acc;
+    if (share < shares || shares == 1) {
+#pragma unroll 4
+      for (int i = shares > 1 ? share : 0; i < n; i += shares) {
+        const float* q = cta_slots + (i ? 2 * (size_t)i : 1) * S::kFloats;
+        acc.add(__ldcg(S::ml(q) + row), __ldcg(reinterpret_cast<const float4*>(q + row * D + ch)));
+      }
+    }
+    if (shares > 1) meet[threadIdx.x] = acc;
+    else write_out<D>(p, out_row(p, own.begin, own.h, own.rb, RB, row), ch, acc.m, acc.l, acc.o);
+  }
+  if (shares == 1) return;
+  __syncthreads();
+  if ((int)threadIdx.x >= parts) return;
+  Acc acc = meet[threadIdx.x];
+  for (int i = 1; i < shares; ++i) {
+    const Acc& x = meet[threadIdx.x + i * parts];
+    acc.add(make_float2(x.m, x.l), x.o);
+  }
+  const int row = threadIdx.x / V, ch = (threadIdx.x - row * V) * 4;
+  write_out<D>(p, out_row(p, own.begin, own.h, own.rb, RB, row), ch, acc.m, acc.l, acc.o);
 }
 
 template <int D, int G, int NT, int NS, int WARPS, int MINB>
@@ -579,7 +627,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
         // of the last open piece: the tail if there is one
         meta[warp].rows = rows;
         meta[warp].begin = it.q.begin;
-        meta[warp].nq = it.q.nq;
+        meta[warp].left = it.units - it.u - it.left(sh.end[warp]);
         meta[warp].h = it.h;
         meta[warp].rb = it.rb;
       }
@@ -609,7 +657,7 @@ struct Variant {
   static constexpr int kStatic = 6144;  // room for the static shared memory
   static_assert(sizeof(Shared<Item<8 * NT, kUnit, kItemCost>, WARPS>) <= kStatic, "shared memory");
   using W = Work<D, 8 * NT, WARPS>;
-  static size_t workspace() { return W::meta(kCtas) * sizeof(float) + kCtas * sizeof(CtaMeta); }
+  static size_t workspace() { return W::flags(kCtas) * sizeof(float) + kCtas * sizeof(uint64_t); }
   static cudaError_t launch(Params p, int sms, cudaStream_t st) {
     auto kern = attn_kernel<D, G, NT, NS, WARPS, MINB>;
     const int stage = WARPS * 2 * p.c.tile_bytes();
@@ -635,7 +683,7 @@ struct Variant {
     cfg.dynamicSmemBytes = (size_t)p.stages * stage;
     cfg.stream = st;
     cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeCooperative;  // the CTAs meet at a grid barrier
+    at.id = cudaLaunchAttributeCooperative;  // CTAs wait for one another
     at.val.cooperative = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
@@ -662,6 +710,18 @@ size_t cache_attn_workspace(const Cache& c) {
   return (n + 255) / 256 * 256;
 }
 
+namespace cattn {
+// A number that no flag in a workspace holds: unlike any before it, and unlike what memory
+// holds by chance.  A captured launch keeps its number; its flags are taken away in each run.
+static uint64_t next_nonce() {
+  static std::atomic<uint64_t> count{(uint64_t)std::chrono::steady_clock::now().time_since_epoch().count()};
+  uint64_t x = count.fetch_add(1) * 0x9E3779B97F4A7C15ull;
+  x = (x ^ (x >> 30)) * 0xBF58476D1CE4E5B9ull;
+  x = (x ^ (x >> 27)) * 0x94D049BB133111EBull;
+  return (x ^ (x >> 31)) | 1ull;
+}
+}  // namespace cattn
+
 template <int D, int G>
 static cudaError_t launch_attn(const cattn::Params& p, int sms, cudaStream_t st) {
   using namespace cattn;
@@ -686,6 +746,7 @@ cudaError_t launch_cache_attn(const Cache& c, const CacheAttnArgs& a, cudaStream
   p.page_tiles = c.page / kCacheTile;
   p.unit_in_page = c.page % cattn::kUnit == 0;
   p.page_bytes = c.Hkv * c.block_bytes();
+  p.nonce = cattn::next_nonce();
   p.ones = kOnes;
   p.sl2 = c.scale * 1.44269504088896340736f;
   int dev = 0, sms = 0;

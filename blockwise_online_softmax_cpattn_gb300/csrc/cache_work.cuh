@@ -33,6 +33,7 @@ struct Params {
   int64_t page_bytes;                // of all K/V heads
   float sl2;                         // scale * log2(e)
   uint32_t ones;                     // kOnes
+  uint64_t nonce;                    // of this launch's flags
 };
 
 // ---------------------------------------------------------------------------
