@@ -98,22 +98,24 @@ struct Item : Place {
   // units of this item before `end`, from u on
   __device__ __forceinline__ int left(const Place& end) const { return (same(end) ? end.u : units) - u; }
   // The place at `x` in the numbering of cost that starts with request r0: an item's first
-  // COST numbers are its first unit's.  (The bounds of the searches matter only if
-  // lengths change under the kernel.)
+  // COST numbers are its first unit's.  (The bounds of the searches matter only if lengths
+  // change under the kernel.)
   __device__ __forceinline__ void locate(const Params& p, int r0, int64_t x) {
     h = rb = u = 0;
     for (r = r0; r < p.a.n_req; ++r) {
       q = request(p, r);
       if (q.nq == 0) continue;
-      const int64_t c = head_cost(p, q);
-      if (x < c * p.c.Hkv) {
-        h = x <= 0x7fffffff ? (int)((unsigned)x / (unsigned)min(c, (int64_t)0x7fffffff)) : (int)(x / c);
-        x -= h * c;
-        break;
-      }
-      x -= c * p.c.Hkv;
+      const int64_t all = head_cost(p, q) * p.c.Hkv;
+      if (x < all) break;
+      x -= all;
     }
-    if (r >= p.a.n_req) return;  // behind the last item
+    if (r < p.a.n_req) within(p, x);  // else behind the last item
+  }
+  // ... that starts with this request, which is not empty
+  __device__ __forceinline__ void within(const Params& p, int64_t x) {
+    const int64_t c = head_cost(p, q);
+    h = x <= 0x7fffffff ? (int)((unsigned)x / (unsigned)min(c, (int64_t)0x7fffffff)) : (int)(x / c);
+    x -= h * c;
     const int nb = blocks_of(p, q, RB);
     for (rb = 0;; ++rb) {
       settle(p);
