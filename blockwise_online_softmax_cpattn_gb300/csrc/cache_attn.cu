@@ -106,49 +106,63 @@ struct Shared {
   Place end[WARPS];
 };
 
+// Steps an item kept in shared memory to the next one (see cache_work.cuh: out of line).
+template <typename It>
+__device__ __noinline__ void next_item(const Params& p, It* it, const It* from) {
+  It x = *from;
+  x.next(p);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) *it = x;
+  __syncwarp();
+}
+
 // The run of this warp, its first unit and the next warp's, into sh.
 template <typename It, int WARPS>
 __device__ __forceinline__ void find_run(const Params& p, Shared<It, WARPS>& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (p.a.n_req <= 32) {
     // Few requests: each warp finds its run by itself, a request a lane, with nothing to wait
-    // for but the loads (1 us of the 3 that the other way takes before the first copy).
+    // for but the loads, and in 32 bits (the other way takes 1 us more to the first copy).
     Req q = {0, 0, 0};
     if (lane < p.a.n_req) q = request(p, lane);
-    int64_t inc = q.nq > 0 ? It::head_cost(p, q) * p.c.Hkv : 0;
+    const int64_t wide = q.nq > 0 ? It::head_cost(p, q) * p.c.Hkv : 0;
+    if (!__any_sync(0xffffffffu, wide >= (1 << 26))) {
+      const int mine = (int)wide;
+      int inc = mine;
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, m);
-      if (lane >= m) inc += y;
-    }
-    const int64_t total = __shfl_sync(0xffffffffu, inc, 31);
-    int64_t c0, c1;
-    cta_run(total, c0, c1);
-    if (threadIdx.x == 0) {
-      sh.ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total));
-      sh.c0 = c0;
-      sh.c1 = c1;
-      sh.total = max((int64_t)1, total);
-    }
-#pragma unroll 1
-    for (int e = 0; e < 2; ++e) {
-      const int64_t v = c0 + part_of(c1 - c0, warp + e, WARPS);
-      const uint32_t past = __ballot_sync(0xffffffffu, inc > v);
-      It x;
-      x.h = x.rb = x.u = x.seen = x.units = 0;
-      x.r = past ? __ffs(past) - 1 : p.a.n_req;
-      const int from = min(x.r, 31);
-      x.q.begin = __shfl_sync(0xffffffffu, q.begin, from);
-      x.q.nq = __shfl_sync(0xffffffffu, q.nq, from);
-      x.q.len = __shfl_sync(0xffffffffu, q.len, from);
-      const int64_t before = __shfl_sync(0xffffffffu, inc, max(from - 1, 0));
-      if (past) x.within(p, v - (from ? before : 0));
-      if (lane == 0) {
-        if (e == 0) sh.in[warp] = sh.it[warp] = x;
-        else sh.end[warp] = x;
+      for (int m = 1; m < 32; m <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, m);
+        if (lane >= m) inc += y;
       }
+      const int total = __shfl_sync(0xffffffffu, inc, 31);
+      int c0, c1;
+      cta_run(total, c0, c1);
+      if (threadIdx.x == 0) {
+        sh.ctas = max(1, min((int)gridDim.x, total));
+        sh.c0 = c0;
+        sh.c1 = c1;
+        sh.total = max(1, total);
+      }
+#pragma unroll 1
+      for (int e = 0; e < 2; ++e) {
+        const int v = c0 + part_of(c1 - c0, warp + e, WARPS);
+        const uint32_t past = __ballot_sync(0xffffffffu, inc > v);
+        const int from = past ? __ffs(past) - 1 : 31;
+        It x;
+        x.h = x.rb = x.u = x.seen = x.units = 0;
+        x.r = past ? from : p.a.n_req;
+        x.q.begin = __shfl_sync(0xffffffffu, q.begin, from);
+        x.q.nq = __shfl_sync(0xffffffffu, q.nq, from);
+        x.q.len = __shfl_sync(0xffffffffu, q.len, from);
+        const int all = __shfl_sync(0xffffffffu, mine, from), first = __shfl_sync(0xffffffffu, inc, from) - all;
+        if (past) x.within(p, v - first, all / p.c.Hkv);
+        if (lane == 0) {
+          if (e == 0) sh.in[warp] = sh.it[warp] = x;
+          else sh.end[warp] = x;
+        }
+      }
+      return;
     }
-    return;
   }
   const int64_t total = sum_costs<It, WARPS * 32>(p, sh.sums, sh.warp_part);
   int64_t c0, c1;
@@ -189,6 +203,7 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
   const uint32_t leads = tails | (pieces & (0u - pieces));
   float* const cta_slots = ws + W::cta_slots(gridDim.x) + 2 * (size_t)blockIdx.x * S::kFloats;
   int k = 0;
+#pragma unroll 1
   for (uint32_t lead = leads; lead; lead &= lead - 1, ++k) {
     const uint32_t first = lead & (0u - lead), rest = lead & (lead - 1);
     const uint32_t ids = pieces & (rest ? (rest & (0u - rest)) - first : 0u - first);
@@ -198,9 +213,11 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
     float* const to = cta_slots + (begun ? S::kFloats : 0);
     // RPW rows at a time: row r of group k is the job of warp (k RB + r) / RPW
     constexpr int V = D / 4, RPW = 32 / V;
+#pragma unroll 1
     for (int row = ((warp + 64 * WARPS - k * (RB / RPW)) % WARPS) * RPW + lane / V; row < rows; row += WARPS * RPW) {
       const int ch = lane % V * 4;
       Acc acc;
+#pragma unroll 1
       for (uint32_t b = ids; b; b &= b - 1) {
         const int id = __ffs(b) - 1, w = id >> 1;
         const float* s = (id & 1) == 0 && meta[w].head_global
@@ -232,7 +249,9 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
   if (!tails || (closing >> last)) return;
   const PieceMeta own = meta[last >> 1];
   const int64_t item_end = sh.c0 + part_of(sh.c1 - sh.c0, (last >> 1) + 1, WARPS) + own.left;
-  const int behind = min((int)((item_end * sh.ctas + sh.total - 1) / sh.total) - 1, sh.ctas - 1) - (int)blockIdx.x;
+  const int64_t scaled = item_end * sh.ctas + sh.total - 1;
+  const int past = scaled <= 0x7fffffff ? (int)((unsigned)scaled / (unsigned)sh.total) : (int)divide(scaled, sh.total);
+  const int behind = min(past - 1, sh.ctas - 1) - (int)blockIdx.x;
   bool ok = true;
   for (int i = threadIdx.x; i < behind; i += WARPS * 32) {
     uint64_t* const f = flags + blockIdx.x + 1 + i;
@@ -253,6 +272,7 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
   const int parts = own.rows * V, n = behind + 1;
   const int shares = max(1, min(THREADS / parts, n)), share = threadIdx.x / parts;
   Acc* const meet = reinterpret_cast<Acc*>(smem);
+#pragma unroll 1
   for (int e = shares > 1 ? threadIdx.x % parts : threadIdx.x; e < parts; e += shares > 1 ? parts : THREADS) {
     const int row = e / V, ch = (e - row * V) * 4;
     Acc acc;
@@ -270,6 +290,7 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
   __syncthreads();
   if ((int)threadIdx.x >= parts) return;
   Acc acc = meet[threadIdx.x];
+#pragma unroll 1
   for (int i = 1; i < shares; ++i) {
     const Acc& x = meet[threadIdx.x + i * parts];
     acc.add(make_float2(x.m, x.l), x.o);
@@ -298,6 +319,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
   volatile int* abort = &sh.abort;
   if (threadIdx.x == 0) sh.abort = 0;
   if (lane == 0) {
+#pragma unroll 1
     for (int s = 0; s < p.stages; ++s) mbar_init(smem_u32(&sh.bars[warp * 8 + s]), 1);
     fence_barrier_init();
   }
@@ -362,19 +384,17 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
       valid = (valid & ~(3u << (2 * stage_in))) | have << (2 * stage_in);
       if (++stage_in == p.stages) stage_in = 0;
       if (--to_issue == 0) {
-        It in = sh.in[warp];
-        if (!in.same(sh.end[warp])) {
-          in.next(p);
-          to_issue = in.r < p.a.n_req ? in.left(sh.end[warp]) : 0;
+        if (!sh.in[warp].same(sh.end[warp])) {
+          next_item(p, &sh.in[warp], &sh.in[warp]);
+          to_issue = sh.in[warp].r < p.a.n_req ? sh.in[warp].left(sh.end[warp]) : 0;
           tab_k = 32;
-          __syncwarp();
-          if (lane == 0) sh.in[warp] = in;
-          __syncwarp();
         }
       }
     };
+#pragma unroll 1
     for (int s = 0; s < p.stages && to_issue > 0; ++s) issue();
 
+#pragma unroll 1
     for (bool more = true; more;) {
       int here = sh.it[warp].left(sh.end[warp]);
       const int len = sh.it[warp].q.len;
@@ -438,6 +458,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
         for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
       }
 
+#pragma unroll 1
       for (; here > 0; --here, tok0 += kUnit) {
         ok = mbar_wait(bar0 + 8 * stage, (parity >> stage) & 1u, abort, p.a.status, kTimeoutNs);
         ok = __all_sync(0xffffffffu, ok);
@@ -626,11 +647,10 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
       const It it = sh.it[warp];
       const bool starts = it.u == 0, ends = it.u + it.left(sh.end[warp]) == it.units;
       const int rows = block_rows(p, it.q.nq, it.rb, RB);
-      It after = it;
       more = !it.same(sh.end[warp]);
       if (more) {
-        after.next(p);
-        more = after.r < p.a.n_req && after.left(sh.end[warp]) > 0;
+        next_item(p, &sh.it[warp], &sh.it[warp]);
+        more = sh.it[warp].r < p.a.n_req && sh.it[warp].left(sh.end[warp]) > 0;
       }
       const bool whole_item = starts && ends;
       float* const to = more ? static_cast<float*>(p.a.ws) + ((size_t)blockIdx.x * WARPS + warp) * S::kFloats
@@ -672,13 +692,11 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
         meta[warp].h = it.h;
         meta[warp].rb = it.rb;
       }
-      __syncwarp();
-      if (lane == 0) sh.it[warp] = after;
-      __syncwarp();
     }
     if (!ok && lane == 0) {
       // never leave with a copy still writing into this CTA's shared memory
       int never = 0;
+#pragma unroll 1
       for (int s = 0; s < p.stages; ++s)
         mbar_wait(smem_u32(&sh.bars[warp * 8 + s]), (parity >> s) & 1u, &never, nullptr, kDrainTimeoutNs);
     }

@@ -59,18 +59,26 @@ __device__ __forceinline__ int seen_by(const Params& p, const Req& q, int x) {
 }
 // ... that row block rb (RB rows) sees, and its units
 __device__ __forceinline__ int block_seen(const Params& p, const Req& q, int rb, int RB) {
-  if (!p.c.causal) return q.len;
-  const int last = (int)min((int64_t)q.nq * p.n_rep, (int64_t)(rb + 1) * RB) - 1;
-  return seen_by(p, q, last);
+  // the last block's last row is the last token's, which sees all
+  if (!p.c.causal || (int64_t)(rb + 1) * RB >= (int64_t)q.nq * p.n_rep) return q.len;
+  return seen_by(p, q, (rb + 1) * RB - 1);
 }
 __device__ __forceinline__ int units_of(int seen, int unit) { return max(1, (seen + unit - 1) / unit); }
 __device__ __forceinline__ int blocks_of(const Params& p, const Req& q, int RB) {
   return (int)(((unsigned)(q.nq * p.n_rep) + RB - 1) / RB);
 }
-// i / n of x, rounded down (the 32-bit division where it does: n, i < 2^8)
+// Most of these kernels' instructions run once a launch, and an instruction that has to be
+// fetched takes as long as many that are there: what runs once is kept small, its loops
+// rolled, 64-bit divisions and steps from item to item out of line.
+static __device__ __noinline__ int64_t divide(int64_t x, int64_t y) { return x / y; }
+
+// i / n of x, rounded down (in 32 bits where they do; i <= n < 2^8)
+__device__ __forceinline__ int part_of(int x, int i, int n) {
+  const unsigned q = (unsigned)x / (unsigned)n, r = (unsigned)x - q * n;
+  return (int)(q * i + r * i / (unsigned)n);
+}
 __device__ __forceinline__ int64_t part_of(int64_t x, int i, int n) {
-  if (x < (1 << 24)) return (unsigned)x * (unsigned)i / (unsigned)n;
-  return x * i / n;
+  return x <= 0x7fffffff ? part_of((int)x, i, n) : divide(x * i, n);
 }
 
 // Request, K/V head and row block of an item, and a unit in it.  Items follow each other by
@@ -91,6 +99,7 @@ struct Item : Place {
   static __device__ __forceinline__ int64_t head_cost(const Params& p, const Req& q) {
     const int nb = blocks_of(p, q, RB);
     int64_t n = 0;
+#pragma unroll 1
     for (int b = 0; b < nb; ++b) n += units_of(block_seen(p, q, b, RB), UNIT) + COST;
     return n;
   }
@@ -102,6 +111,7 @@ struct Item : Place {
   // change under the kernel.)
   __device__ __forceinline__ void locate(const Params& p, int r0, int64_t x) {
     h = rb = u = 0;
+#pragma unroll 1
     for (r = r0; r < p.a.n_req; ++r) {
       q = request(p, r);
       if (q.nq == 0) continue;
@@ -114,9 +124,22 @@ struct Item : Place {
   // ... that starts with this request, which is not empty
   __device__ __forceinline__ void within(const Params& p, int64_t x) {
     const int64_t c = head_cost(p, q);
-    h = x <= 0x7fffffff ? (int)((unsigned)x / (unsigned)min(c, (int64_t)0x7fffffff)) : (int)(x / c);
-    x -= h * c;
+    if (c > 0x7fffffff || x > 0x7fffffff) {
+      h = (int)divide(x, c);
+      within_head(p, x - h * c);
+    } else {
+      within(p, (int)x, (int)c);
+    }
+  }
+  // c: the cost of one of its K/V heads
+  __device__ __forceinline__ void within(const Params& p, int x, int c) {
+    h = (unsigned)x / (unsigned)c;
+    within_head(p, x - h * c);
+  }
+  template <typename Int>
+  __device__ __forceinline__ void within_head(const Params& p, Int x) {
     const int nb = blocks_of(p, q, RB);
+#pragma unroll 1
     for (rb = 0;; ++rb) {
       settle(p);
       if (rb == nb - 1 || x < units + COST) break;
@@ -130,6 +153,7 @@ struct Item : Place {
       rb = 0;
       if (++h == p.c.Hkv) {
         h = 0;
+#pragma unroll 1
         do {
           if (++r >= p.a.n_req) return;
           q = request(p, r);
@@ -223,6 +247,7 @@ __device__ __forceinline__ int64_t sum_costs(const Params& p, int64_t* sums, int
 #pragma unroll
   for (int i = 0; i < PT; ++i) {
     const int64_t r0 = (int64_t)(threadIdx.x * PT + i) * p.per_sum;
+#pragma unroll 1
     for (int64_t r = r0; r < r0 + p.per_sum && r < p.a.n_req; ++r) {
       const Req q = request(p, (int)r);
       if (q.nq > 0) run += It::head_cost(p, q) * p.c.Hkv;
@@ -238,7 +263,7 @@ __device__ __forceinline__ int64_t sum_costs(const Params& p, int64_t* sums, int
   if (lane == 31) warp_part[warp] = inc;
   __syncthreads();
   int64_t before = 0, total = 0;
-#pragma unroll
+#pragma unroll 4
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += warp_part[w];
     total += warp_part[w];
@@ -251,8 +276,9 @@ __device__ __forceinline__ int64_t sum_costs(const Params& p, int64_t* sums, int
 }
 // This CTA's run of the line.  CTAs that would get nothing are not counted, so an item's
 // CTAs are neighbours.
-__device__ __forceinline__ void cta_run(int64_t total, int64_t& c0, int64_t& c1) {
-  const int ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total));
+template <typename Int>
+__device__ __forceinline__ void cta_run(Int total, Int& c0, Int& c1) {
+  const int ctas = (int)max((Int)1, min((Int)gridDim.x, total));
   const int cta = min((int)blockIdx.x, ctas);
   c0 = part_of(total, cta, ctas);
   c1 = part_of(total, min(cta + 1, ctas), ctas);
