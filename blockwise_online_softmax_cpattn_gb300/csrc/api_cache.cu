@@ -35,6 +35,12 @@ static cpattn_status validate_cache(const cpattn_cache_desc* d, Cache* c) {
   return CPATTN_OK;
 }
 
+// A request's tokens, the table's entries and what is counted over requests are kept in 32
+// bits, with room for a page, a tile or a step of a loop behind the last one.
+static bool lengths_fit(const Cache& c, int n_req, int max_pages) {
+  return n_req <= (1 << 24) && (int64_t)n_req * max_pages <= INT_MAX && (int64_t)max_pages * c.page <= (1 << 30);
+}
+
 static bool aligned4(const void* p) { return p && ((uintptr_t)p % 4 == 0); }
 
 // Strides keep every row on a 16-byte boundary; a stride may be 0 or negative for a
@@ -77,9 +83,7 @@ cpattn_status cpattn_cache_plan(const cpattn_cache_desc* desc, int n_req, int ma
       (n_slots > 0 && !aligned4(slots)) || !aligned16(workspace))
     return CPATTN_ERR_INVALID_ARG;
   if (ws_bytes < cache_plan_workspace(n_req)) return CPATTN_ERR_INVALID_ARG;
-  // page counts and a row's tokens are kept in 32 bits
-  if ((int64_t)n_req * max_pages > INT_MAX || (int64_t)max_pages * c.page > INT_MAX)
-    return CPATTN_ERR_UNSUPPORTED;
+  if (!lengths_fit(c, n_req, max_pages)) return CPATTN_ERR_UNSUPPORTED;
   PlanArgs a;
   a.n_req = n_req;
   a.max_pages = max_pages;
@@ -159,8 +163,7 @@ cpattn_status cpattn_cache_attn(const cpattn_cache_desc* desc, int n_req, int ma
       !strides_ok(c, n_tokens, c.Hq, q_token_stride, q_head_stride))
     return CPATTN_ERR_INVALID_ARG;
   if (ws_bytes < cache_attn_workspace(c)) return CPATTN_ERR_INVALID_ARG;
-  if ((int64_t)n_req * max_pages > INT_MAX || (int64_t)max_pages * c.page > INT_MAX ||
-      (int64_t)n_tokens * c.Hq > INT_MAX)
+  if (!lengths_fit(c, n_req, max_pages) || (int64_t)n_tokens * c.Hq > INT_MAX)
     return CPATTN_ERR_UNSUPPORTED;
   CacheAttnArgs a;
   a.n_req = n_req;

@@ -36,18 +36,13 @@ struct Cache {
   int o_f32;       // o: 1 f32, 0 as q
   int causal;
   float scale;
-  __host__ __device__ int row_bytes() const { return D / 2; }           // codes of one row
-  __host__ __device__ int groups() const { return D / G; }
-  __host__ __device__ int half_tile() const { return kCacheTile * (D / 2 + 4 * (D / G)); }
-  __host__ __device__ int tile_bytes() const { return 2 * half_tile(); }  // K half, V half
+  // a K half and a V half: codes of 16 rows, their (a, z)
+  __host__ __device__ int tile_bytes() const { return 2 * kCacheTile * (D / 2 + 4 * (D / G)); }
+  // of one page and K/V head
   __host__ __device__ int64_t block_bytes() const {
     return (int64_t)(page / kCacheTile) * tile_bytes();
   }
   __host__ __device__ int64_t slots() const { return (int64_t)n_pages * page; }
-  // first byte of tile `t` of page `pg`, K/V head h
-  __host__ __device__ int64_t tile_at(int pg, int h, int t) const {
-    return ((int64_t)pg * Hkv + h) * block_bytes() + (int64_t)t * tile_bytes();
-  }
 };
 
 // Row of token t (of its tile) in the V half: 2t + e of every eight is in row t + 4e,

@@ -416,14 +416,15 @@ cpattn_status cpattn_layout_batch(int permute, const cpattn_desc* desc, int n,
  *
  * Shared conventions: tokens are packed, one request's after the other's, and come
  * first: q and o are [n_tokens][H_q][D], k and v [n_tokens][H_kv][D], lse
- * [n_tokens][H_q].  Inputs q,
- * k, v (and the outputs k, v of cpattn_cache_read) take strides in elements between
- * tokens and between heads, multiples of 16 bytes, so slices of a fused projection
- * or the ring's [H_kv][T][D] tensors are passed as they are; channels are contiguous.
- * Lengths, tables and slots are device int32.  Lengths are taken as clamped to
- * [0, max_pages * page].  A page or slot outside the cache is never touched: append
- * skips it, read gives zeros, attention sees no key there.  All other rules (who owns
- * buffers, alignment, streams, errors) are those of the calls above.
+ * [n_tokens][H_q].  Inputs q, k, v (and the outputs k, v of cpattn_cache_read) take
+ * strides in elements between tokens and between heads, multiples of 16 bytes, so
+ * slices of a fused projection or the ring's [H_kv][T][D] tensors are passed as they
+ * are; channels are contiguous.  Lengths, tables and slots are device int32.  Lengths
+ * are taken as clamped to [0, max_pages * page].  A page or slot outside the cache is
+ * never touched: append skips it, read gives zeros, attention sees no key there.
+ * CPATTN_ERR_UNSUPPORTED: max_pages * page past 2^30 (a request's tokens), n_req past
+ * 2^24, n_req * max_pages or n_tokens * H_q not below 2^31, H_q past 32767.  All other
+ * rules (who owns buffers, alignment, streams, errors) are those of the calls above.
  */
 typedef struct cpattn_cache_desc {
   int32_t H_q;     /* query heads (a multiple of H_kv) */
@@ -466,7 +467,8 @@ size_t cpattn_cache_plan_workspace(const cpattn_cache_desc* desc, int n_req);
  * the requests and of their pages; then the requests take theirs in order, each from
  * the list's end backwards.  The first request that finds too few pages left, and
  * every later one that needs a page, keeps its old length in len_out, takes none, and
- * its new tokens' slots are -1 (they still count in q_start); else len_out is len_new.
+ * its new tokens' slots are -1 (they still count in q_start, and what attention gives
+ * them means nothing); else len_out is len_new.
  *   workspace  : at least cpattn_cache_plan_workspace(desc, n_req) bytes
  * Total new tokens must stay below 2^31.  Of desc only page and n_pages matter.
  */
@@ -496,13 +498,15 @@ cpattn_status cpattn_cache_append(const cpattn_cache_desc* desc, int n_tokens, c
 /*
  * Gives the rows of n_tokens slots back as keys and values of desc->dtype, for example
  * a cached prefix for cpattn_ring_fwd.  A slot outside the cache gives rows of zeros.
+ * The rows of k and of v must not overlap.
  */
 cpattn_status cpattn_cache_read(const cpattn_cache_desc* desc, int n_tokens, const int32_t* slots,
                                 const void* cache, void* k, int64_t k_token_stride,
                                 int64_t k_head_stride, void* v, int64_t v_token_stride,
                                 int64_t v_head_stride, void* stream);
 
-/* Bytes of device workspace of cpattn_cache_attn (partial results of long rows). */
+/* Bytes of device workspace of cpattn_cache_attn (partial results of rows that several
+ * thread blocks share, and their flags; it needs no initial value). */
 size_t cpattn_cache_attn_workspace(const cpattn_cache_desc* desc);
 
 /*
@@ -519,8 +523,10 @@ size_t cpattn_cache_attn_workspace(const cpattn_cache_desc* desc);
  *   table     : [n_req][max_pages], as cpattn_cache_plan leaves it
  *   o         : [n_tokens][H_q][D] of desc->o_dtype, contiguous
  *   lse       : [n_tokens][H_q] float32 or null
- *   workspace : at least cpattn_cache_attn_workspace(desc) bytes; calls that share it
- *               must be ordered (one stream)
+ *   workspace : at least cpattn_cache_attn_workspace(desc) bytes; calls that share it,
+ *               replays of captured ones among them, must be ordered (one stream).
+ *               After CPATTN_ERR_TIMEOUT it is cleared (zeros) before a captured call
+ *               that uses it is replayed.
  * A row that sees no key gets o = 0, lse = -inf.  Heads as above: query head h reads
  * K/V head h / (H_q / H_kv).  The result does not depend on the order in which the
  * GPU runs the work: repeated calls are bitwise equal.

@@ -147,6 +147,10 @@ def test_plan_refuses(cp):
     assert call(ws=0) == 1 and call(ws=FAKE + 8) == 1 and call(size=need - 1) == 1
     assert call(max_pages=1 << 30) == 2                       # n_req * max_pages past 32 bits
     assert call(n_req=1, max_pages=1 << 26, size=1 << 30) == 2   # a row's tokens past 32 bits
+    # sums of a length and a page, or of a count and a loop's step, past 32 bits
+    assert call(n_req=1, max_pages=(1 << 25) - 1, size=1 << 30) == 2
+    assert call(n_req=1, max_pages=(1 << 24) + 1, size=1 << 30) == 2
+    assert call(n_req=(1 << 24) + 1, max_pages=1, size=1 << 40) == 2
 
 
 def test_rows_refuse(cp):
@@ -189,6 +193,9 @@ def test_attention_refuses(cp):
     assert call(size=need - 1) == 1
     assert call(max_pages=1 << 30) == 2
     assert call(n_req=1, max_pages=1 << 26) == 2
+    assert call(n_req=1, max_pages=(1 << 25) - 1) == 2
+    assert call(n_req=1, max_pages=(1 << 24) + 1) == 2
+    assert call(n_req=(1 << 24) + 1, max_pages=1) == 2
     assert call(n=1 << 29) == 2
 
 

@@ -149,6 +149,48 @@ def test_append_reports_what_it_cannot_hold(dtype):
     assert code == cp.OK and np.array_equal(got, ref)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_on_16_byte_boundaries(dtype):
+    """Rows that lie on 16-byte boundaries and on no wider ones."""
+    cp = cp_mod()
+    rng = np.random.default_rng(21)
+    d = cp.make_cache_desc(2, 2, 64, 16, 8, group=32, dtype=dtype)
+    n, vec = 50, 4 if dtype == "f32" else 8
+    kt, vt = (to_dt(x, dtype) for x in rng.normal(size=(2, n, 2, 64)))
+    slots = rng.permutation(128)[:n]
+    bufs = [torch.full((n, 2 * 64 + vec), 7.0, dtype=kt.dtype, device=dev()) for _ in range(4)]
+    kd, vd, ko, vo = (b[:, vec:].unflatten(1, (2, 64)) for b in bufs)
+    assert all(x.data_ptr() % 32 == 16 for x in (kd, vd, ko, vo))
+    kd.copy_(kt)
+    vd.copy_(vt)
+    c, s = torch.zeros(cp.cpattn_cache_bytes(d), dtype=torch.uint8, device=dev()), i32(slots)
+    checked(cp, cp.cpattn_cache_append(d, n, kd, vd, s, c))
+    ref = np.zeros(tuple(make_cache(cp, d, fill=0).shape), np.uint8)
+    OC.append(ref, 16, 32, f32_of(kt), f32_of(vt), slots)
+    assert np.array_equal(c.cpu().numpy().reshape(ref.shape), ref)
+    checked(cp, cp.cpattn_cache_read(d, n, s, c, ko, vo))
+    for got, want, buf in zip((ko, vo), OC.read(ref, 16, 32, 64, slots), bufs[2:]):
+        assert np.array_equal(f32_of(got), want)
+        assert (buf[:, :vec] == 7.0).all()      # the gaps between rows
+
+
+def test_append_of_one_slot_twice_touches_no_other():
+    cp = cp_mod()
+    rng = np.random.default_rng(22)
+    d = cp.make_cache_desc(1, 1, 128, 32, 4)
+    n = 300
+    k, v = (to_dt(x, "bf16") for x in rng.normal(size=(2, n, 1, 128)))
+    slots = rng.integers(0, 100, n)
+    ref = make_cache(cp, d, rng)
+    c, s, kd, vd = torch.from_numpy(ref.copy()).to(dev()), i32(slots), k.to(dev()), v.to(dev())
+    checked(cp, cp.cpattn_cache_append(d, n, kd, vd, s, c))
+    once = np.flatnonzero(np.bincount(slots, minlength=128)[slots] == 1)
+    OC.append(ref, 32, 64, f32_of(k)[once], f32_of(v)[once], slots[once])
+    keep = np.array([x for x in range(128) if (slots == x).sum() < 2])
+    for got, want in zip(OC.read(c.cpu().numpy(), 32, 64, 128, keep), OC.read(ref, 32, 64, 128, keep)):
+        assert np.array_equal(got, want, equal_nan=True)
+
+
 def test_append_past_32_bits():
     """A cache of over 4 GB: the last page's bytes."""
     cp = cp_mod()
@@ -501,6 +543,87 @@ def test_attn_is_deterministic_and_replays(dtype, n_q):
         assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [32, 33, 257, 700])
+def test_attn_many_requests(dtype, R):
+    rng = np.random.default_rng(R)
+    kv = rng.integers(0, 40, R)
+    kv[rng.integers(0, R, 3)] = 500
+    Case(cp_mod(), H_q=4, H_kv=2, D=64, group=32, page=16, n_q=rng.integers(0, 3, R), kv_len=kv, dtype=dtype,
+         seed=R).check()
+
+
+def test_attn_many_prompts():
+    rng = np.random.default_rng(3)
+    n_q = rng.integers(0, 30, 280)
+    Case(cp_mod(), H_q=4, H_kv=1, D=64, group=64, page=16, n_q=n_q, kv_len=n_q + rng.integers(0, 100, 280)).check()
+
+
+@pytest.mark.parametrize("H_q,n_q", [(8, 1), (9, 1), (4, 2), (3, 3), (4, 12), (7, 7), (1, 48), (1, 49), (16, 3), (17, 3)])
+def test_attn_rows_where_kernels_change(H_q, n_q):
+    Case(cp_mod(), H_q=H_q, H_kv=1, n_q=[n_q, 1, n_q], kv_len=[n_q, 300, 1100], seed=H_q).check()
+
+
+@pytest.mark.parametrize("dtype,n_q", [("bf16", 2), ("bf16", 100), ("f32", 2)])
+def test_attn_clamps_what_it_is_told(dtype, n_q):
+    """Offsets outside the rows and lengths outside the table."""
+    c = Case(cp_mod(), n_q=[n_q, n_q, n_q], kv_len=[90, 320, 150], dtype=dtype, tail=0)
+    cap = c.table.shape[1] * c.d.page
+    c.dev[0].copy_(i32([-5, n_q, 2 * n_q, 2 ** 31 - 1]))
+    c.dev[1].copy_(i32([-7, 2 ** 31 - 1, 150]))
+    c.kv_len = np.array([0, cap, 150])
+    c.check()
+    # a request that ends before it begins has no rows
+    c = Case(cp_mod(), n_q=[n_q, 0, 0], kv_len=[90, 300, 150], dtype=dtype, tail=0)
+    c.dev[0].copy_(i32([0, n_q, n_q - 1, -2 ** 31]))
+    c.check()
+
+
+def test_attn_graphs_that_share_a_workspace():
+    """Captured calls of all kernels on one workspace, replayed in turn, and eager ones between."""
+    cp = cp_mod()
+    cases = [Case(cp, n_q=[1] * 3, kv_len=[1200, 37, 3000]), Case(cp, n_q=[5] * 2, kv_len=[900, 2000], seed=1),
+             Case(cp, n_q=[150, 20], kv_len=[1500, 1024], seed=2), Case(cp, n_q=[2], kv_len=[2500], dtype="f32", seed=3)]
+    ws = max((c.ws for c in cases), key=lambda x: x.numel())
+    graphs = []
+    for c in cases:
+        c.ws = ws
+        c.check()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            cp.check(c.run())
+        graphs.append(g)
+    want = [(c.o.clone(), c.lse.clone()) for c in cases]
+    for i in (0, 1, 0, 2, 3, 0, 2, 2, 1, 3, 1, 0):
+        cases[i].o.fill_(77.0)
+        cases[i].lse.fill_(77.0)
+        graphs[i].replay()
+        cp.check(cases[(i + 1) % 4].run())
+    checked(cp, 0)
+    for c, (o, lse) in zip(cases, want):
+        assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.parametrize("n_q", [(1, 1), (1, 150), (150, 130)])
+def test_attn_on_two_streams(n_q):
+    """Two calls at once, each with a workspace of its own."""
+    cp = cp_mod()
+    cases = [Case(cp, n_q=[n, n], kv_len=[2000, 900], seed=n) for n in n_q]
+    for c in cases:
+        c.check()
+    want = [(c.o.clone(), c.lse.clone()) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                cp.check(c.run())
+    torch.cuda.synchronize()
+    checked(cp, 0)
+    for c, (o, lse) in zip(cases, want):
+        assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+
+
 def test_attn_with_a_device_side_batch_that_changes():
     """A captured call follows lengths and tables that change between replays."""
     c = Case(cp_mod(), n_q=[1] * 5, kv_len=[300, 5, 0, 129, 64], tail=0)
@@ -562,6 +685,59 @@ def test_a_server_step_by_step():
         old = new
     held = sum(-(-x // page) for x in old)
     assert n_free.item() == n_pages - held
+
+
+def test_a_captured_decoding_step():
+    """plan, append, read and attention of one step in a graph, replayed token by token: the
+    same cache, table and results as eager calls."""
+    cp = cp_mod()
+    rng = np.random.default_rng(14)
+    H_q, H, D, page, R, cols, n_pages, steps = 8, 2, 128, 16, 3, 4, 12, 20
+    d = cp.make_cache_desc(H_q, H, D, page, n_pages)
+    first = rng.integers(1, 20, R)
+    rows = to_dt(rng.normal(size=(steps, R, H_q + 2 * H, D)), "bf16").to(dev())
+    prompt = to_dt(rng.normal(size=(int(first.sum()), 2 * H, D)), "bf16").to(dev())
+
+    def server():
+        s = dict(cache=torch.zeros(cp.cpattn_cache_bytes(d), dtype=torch.uint8, device=dev()),
+                 table=i32(np.full((R, cols), -1)), free=i32(np.arange(n_pages)), n_free=i32([n_pages]),
+                 lens=i32(np.zeros(R)), new=i32(first), start=i32(np.zeros(R + 1)), slots=i32(np.zeros(80)),
+                 x=torch.zeros(R, H_q + 2 * H, D, dtype=torch.bfloat16, device=dev()),
+                 o=torch.zeros(R, H_q, D, dtype=torch.bfloat16, device=dev()), lse=torch.zeros(R, H_q, device=dev()),
+                 back=torch.zeros(2, R, H, D, dtype=torch.bfloat16, device=dev()),
+                 ws=torch.zeros(max(cp.cpattn_cache_plan_workspace(d, R), cp.cpattn_cache_attn_workspace(d)),
+                                dtype=torch.uint8, device=dev()))
+        plan(s)
+        cp.check(cp.cpattn_cache_append(d, prompt.shape[0], prompt[:, :H], prompt[:, H:], s["slots"], s["cache"]))
+        return s
+
+    def plan(s):
+        cp.check(cp.cpattn_cache_plan(d, R, cols, s["lens"], s["new"], s["table"], s["free"], s["n_free"], s["n_free"],
+                                      s["lens"], s["start"], s["slots"], 80, s["ws"]))
+
+    def step(s):
+        torch.add(s["lens"], 1, out=s["new"])
+        plan(s)
+        q, k, v = s["x"][:, :H_q], s["x"][:, H_q:H_q + H], s["x"][:, H_q + H:]
+        cp.check(cp.cpattn_cache_append(d, R, k, v, s["slots"], s["cache"]))
+        cp.check(cp.cpattn_cache_read(d, R, s["slots"], s["cache"], s["back"][0], s["back"][1]))
+        cp.check(cp.cpattn_cache_attn(d, R, cols, R, 1, q, s["start"], s["lens"], s["table"], s["cache"], s["o"],
+                                      s["lse"], s["ws"]))
+
+    a, b = server(), server()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(b)
+    for i in range(steps):
+        for s in (a, b):
+            s["x"].copy_(rows[i])
+        step(a)
+        g.replay()
+        checked(cp, 0)
+        for name in ("table", "n_free", "lens", "start", "slots", "cache", "back", "o", "lse"):
+            assert torch.equal(a[name], b[name]), (i, name)
+    assert a["lens"].tolist() == [int(x) + steps for x in first]
 
 
 def test_ring_prompt_then_sharded_decoding():
