@@ -15,6 +15,7 @@
 namespace cpattn {
 
 constexpr int kCacheTile = 16;            // tokens per tile (the K dimension of one MMA)
+constexpr int kStatusRange = 6;           // device status: a value the cache cannot hold
 constexpr float kCacheHuge = 0x1p120f;    // stored values are held within +- this
 constexpr float kCacheTiny = 0x1p-100f;   // a group whose a is below this has a = 0
 

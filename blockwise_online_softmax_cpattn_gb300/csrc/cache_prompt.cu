@@ -83,6 +83,20 @@ struct Static {
   volatile int seen_k, seen_v;   // tiles whose K, V is ready
 };
 
+// tmem_wait_ld with the loaded registers as operands, so that nothing that reads them can be
+// moved above the wait.
+#define CPATTN_RW8(i) "+r"(r[i + 0]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), \
+                      "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : CPATTN_RW8(0), CPATTN_RW8(8), CPATTN_RW8(16), CPATTN_RW8(24)
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : CPATTN_RW8(0), CPATTN_RW8(8) : : "memory");
+}
+
 // Waits until *c reaches `want`, bounded as the waits for barriers are.
 __device__ __forceinline__ bool count_wait(const volatile int* c, int want, volatile int* abort, int* status) {
   bool ok = *c >= want;

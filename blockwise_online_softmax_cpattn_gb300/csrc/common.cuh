@@ -16,7 +16,6 @@ namespace cpattn {
 constexpr int kStatusLaunch = 3;   // a kernel found its launch unusable (reported as a CUDA error)
 constexpr int kStatusTimeout = 4;
 constexpr int kStatusBounds = 5;   // a bounds check of a CPATTN_DEBUG build failed
-constexpr int kStatusRange = 6;    // a value the 4-bit cache cannot hold
 
 // ---------------------------------------------------------------------------
 // Token position maps.  Slot = index on the layout-order token axis; position =
@@ -487,19 +486,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-// ... with the loaded registers as operands, so that nothing that reads them can be moved
-// above the wait.
-#define CPATTN_RW8(i) "+r"(r[i + 0]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), \
-                      "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
-__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : CPATTN_RW8(0), CPATTN_RW8(8), CPATTN_RW8(16), CPATTN_RW8(24)
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : CPATTN_RW8(0), CPATTN_RW8(8) : : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
