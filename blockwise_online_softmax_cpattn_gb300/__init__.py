@@ -48,7 +48,7 @@ class CpattnCacheDesc(ctypes.Structure):
     _fields_ = [("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("D", ctypes.c_int32),
                 ("group", ctypes.c_int32), ("page", ctypes.c_int32), ("n_pages", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("o_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
-                ("causal", ctypes.c_int32)]
+                ("causal", ctypes.c_int32), ("debug_fault", ctypes.c_int32)]
 
 
 class CpattnError(RuntimeError):
@@ -66,14 +66,14 @@ def make_desc(B, H_q, H_kv, T, D, cp, layout="zigzag", dtype="bf16", a2a=1, scal
 
 
 def make_cache_desc(H_q, H_kv, D, page, n_pages, group=64, dtype="bf16", o_dtype=None, scale=None,
-                    causal=1) -> CpattnCacheDesc:
+                    causal=1, debug_fault=0) -> CpattnCacheDesc:
     """Descriptor of one layer's 4-bit key/value cache; o_dtype defaults to dtype."""
     dts = {"f32": F32, "bf16": BF16}
     dt = dts.get(dtype, dtype)
     odt = dt if o_dtype is None else dts.get(o_dtype, o_dtype)
     if scale is None:
         scale = 1.0 / math.sqrt(D) if D > 0 else 0.0  # the calls refuse such a D
-    return CpattnCacheDesc(H_q, H_kv, D, group, page, n_pages, dt, odt, scale, causal)
+    return CpattnCacheDesc(H_q, H_kv, D, group, page, n_pages, dt, odt, scale, causal, debug_fault)
 
 
 _vp = ctypes.c_void_p

@@ -19,6 +19,7 @@ static cpattn_status validate_cache(const cpattn_cache_desc* d, Cache* c) {
   if (d->o_dtype != CPATTN_F32 && d->o_dtype != d->dtype) return CPATTN_ERR_INVALID_ARG;
   if (!(d->scale > 0.f) || !isfinite(d->scale)) return CPATTN_ERR_INVALID_ARG;
   if (d->causal != 0 && d->causal != 1) return CPATTN_ERR_INVALID_ARG;
+  if (d->debug_fault < 0 || d->debug_fault > 3) return CPATTN_ERR_INVALID_ARG;
   if ((int64_t)d->n_pages * d->page > INT_MAX || d->H_q > 32767) return CPATTN_ERR_UNSUPPORTED;
   if (c) {
     c->Hq = d->H_q;
@@ -31,6 +32,7 @@ static cpattn_status validate_cache(const cpattn_cache_desc* d, Cache* c) {
     c->o_f32 = d->o_dtype == CPATTN_F32;
     c->causal = d->causal;
     c->scale = d->scale;
+    c->debug_fault = d->debug_fault;
   }
   return CPATTN_OK;
 }

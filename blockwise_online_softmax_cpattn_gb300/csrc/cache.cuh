@@ -36,6 +36,7 @@ struct Cache {
   int bf16;        // q, k, v: 1 bf16, 0 f32
   int o_f32;       // o: 1 f32, 0 as q
   int causal;
+  int debug_fault; // cpattn_cache_desc
   float scale;
   // a K half and a V half: codes of 16 rows, their (a, z)
   __host__ __device__ int tile_bytes() const { return 2 * kCacheTile * (D / 2 + 4 * (D / G)); }

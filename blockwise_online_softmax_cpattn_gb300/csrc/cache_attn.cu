@@ -243,7 +243,7 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
   if (sh.abort) return;
   if ((pieces & ~tails & (leads & (0u - leads))) && threadIdx.x == 0) {
     __threadfence();
-    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(flags + blockIdx.x), "l"(p.nonce) : "memory");
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(flags + blockIdx.x), "l"(p.publish) : "memory");
   }
   const int last = tails ? 31 - __clz(tails) : 0;
   if (!tails || (closing >> last)) return;
@@ -258,7 +258,7 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
     uint64_t v = 0, t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
       asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(f) : "memory");
-      if (v == p.nonce || ((it & 63u) == 0 && globaltimer_ns() - t0 > kTimeoutNs)) break;
+      if (v == p.nonce || ((it & 63u) == 0 && globaltimer_ns() - t0 > p.timeout_ns)) break;
     }
     ok = ok && v == p.nonce;
     *f = 0;
@@ -320,7 +320,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
   if (threadIdx.x == 0) sh.abort = 0;
   if (lane == 0) {
 #pragma unroll 1
-    for (int s = 0; s < p.stages; ++s) mbar_init(smem_u32(&sh.bars[warp * 8 + s]), 1);
+    for (int s = 0; s < p.stages; ++s)  // fault hook: one arrival more than there will be
+      mbar_init(smem_u32(&sh.bars[warp * 8 + s]), p.c.debug_fault == 1 ? 2 : 1);
     fence_barrier_init();
   }
   __syncthreads();
@@ -349,7 +350,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
       if (tab_k == 32) {
         const It& in = sh.in[warp];
         const int64_t tok = ((int64_t)in.u * per_lane + lane) * (kUnit / per_lane);
-        tab = tok < in.seen ? p.a.table[(int64_t)in.r * p.a.max_pages + tok / p.c.page] : -1;
+        const int64_t at = (int64_t)in.r * p.a.max_pages + tok / p.c.page;
+        tab = tok < in.seen && page_at_ok(p, at) ? p.a.table[at] : -1;
         from = p.a.cache + in.h * p.c.block_bytes();
         w0 = (in.u * 2) % p.page_tiles;
         tab_k = 0;
@@ -414,8 +416,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
             for (int w = 0; w < KW; ++w)
 #pragma unroll
               for (int i = 0; i < 4; ++i) qf[n][s][w][i] = 0;
-          if (rho < rows) {
-            const unsigned x = (unsigned)it.rb * RB + rho, tok = x / (unsigned)p.n_rep;
+          const unsigned x = (unsigned)it.rb * RB + rho, tok = x / (unsigned)p.n_rep;
+          if (rho < rows && token_ok(p, it.q.begin + (int)tok)) {
             const int64_t at = (it.q.begin + (int)tok) * p.a.qs.token +
                                (it.h * p.n_rep + (int)(x - tok * p.n_rep)) * p.a.qs.head + 8 * KW * t4;
 #pragma unroll
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
 
 #pragma unroll 1
       for (; here > 0; --here, tok0 += kUnit) {
-        ok = mbar_wait(bar0 + 8 * stage, (parity >> stage) & 1u, abort, p.a.status, kTimeoutNs);
+        ok = mbar_wait(bar0 + 8 * stage, (parity >> stage) & 1u, abort, p.a.status, p.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         parity ^= 1u << stage;
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
             }
             if (g == 0) {
               if (!whole_item) S::ml(to)[rho] = make_float2(m[n][e], l[n][e]);
-              else if (p.a.lse) p.a.lse[row] = lse_of(m[n][e], l[n][e]);
+              else store_lse(p, row, m[n][e], l[n][e]);
             }
           }
         }
@@ -698,7 +700,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
       int never = 0;
 #pragma unroll 1
       for (int s = 0; s < p.stages; ++s)
-        mbar_wait(smem_u32(&sh.bars[warp * 8 + s]), (parity >> s) & 1u, &never, nullptr, kDrainTimeoutNs);
+        mbar_wait(smem_u32(&sh.bars[warp * 8 + s]), (parity >> s) & 1u, &never, nullptr, p.drain_ns());
     }
   }
   __syncthreads();
@@ -806,6 +808,8 @@ cudaError_t launch_cache_attn(const Cache& c, const CacheAttnArgs& a, cudaStream
   p.unit_in_page = c.page % cattn::kUnit == 0;
   p.page_bytes = c.Hkv * c.block_bytes();
   p.nonce = cattn::next_nonce();
+  p.publish = c.debug_fault == 3 ? 0 : p.nonce;
+  p.timeout_ns = c.debug_fault ? cattn::kDebugTimeoutNs : cattn::kTimeoutNs;
   p.ones = kOnes;
   p.sl2 = c.scale * 1.44269504088896340736f;
   int dev = 0, sms = 0;

@@ -98,15 +98,15 @@ __device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[16]) {
 }
 
 // Waits until *c reaches `want`, bounded as the waits for barriers are.
-__device__ __forceinline__ bool count_wait(const volatile int* c, int want, volatile int* abort, int* status) {
+__device__ __forceinline__ bool count_wait(const volatile int* c, int want, volatile int* abort, const Params& p) {
   bool ok = *c >= want;
   if (!ok) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t i = 1; !(ok = *c >= want); ++i)
-      if ((i & 63u) == 0 && (*abort || globaltimer_ns() - t0 > kTimeoutNs)) break;
+      if ((i & 63u) == 0 && (*abort || globaltimer_ns() - t0 > p.timeout_ns)) break;
     if (!ok && !*abort) {
       *abort = 1;
-      latch_status(status, kStatusTimeout);
+      latch_status(p.a.status, kStatusTimeout);
     }
   }
   ok = __all_sync(0xffffffffu, ok);
@@ -114,12 +114,12 @@ __device__ __forceinline__ bool count_wait(const volatile int* c, int want, vola
   return ok;
 }
 
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t par, volatile int* abort, int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, par, abort, status, kTimeoutNs));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t par, volatile int* abort, const Params& p) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, par, abort, p.a.status, p.timeout_ns));
 }
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t par) {
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t par, const Params& p) {
   int never = 0;
-  mbar_wait(bar, par, &never, nullptr, kDrainTimeoutNs);
+  mbar_wait(bar, par, &never, nullptr, p.drain_ns());
 }
 // What both sides' walks have in common: the tiles [u, u + n) of an item, and which of them
 // side x takes.
@@ -158,7 +158,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   auto codes_full = [&](int i) { return bars + 8 * (2 * CODES + i); };
   auto codes_empty = [&](int i) { return bars + 8 * (2 * CODES + kRing + i); };
   volatile int* abort = &sh.abort;
-  int* const status = p.a.status;
   float* const ws = static_cast<float*>(p.a.ws);
   CtaMeta* const out_meta = reinterpret_cast<CtaMeta*>(ws + 2 * (size_t)gridDim.x * S::kFloats);
 
@@ -169,10 +168,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       if (group == K_FULL || group == V_FULL || group == TURN || i >= 2 * CODES + kRing) n = 4;  // a warpgroup's warps
       if (group == K_EMPTY || group == V_EMPTY) n = 3;  // both sides, the count's keeper
       if (group == Q_FULL || group == P_FULL || group == O_FREE || group == SHARE) n = 128;  // a side's threads
+      // fault hook: one arrival more than there will be
+      if (p.c.debug_fault == 2 && i == 2 * CODES) n = 2;
       mbar_init(bars + 8 * i, n);
     }
     sh.abort = (sbase & 1023u) ? 1 : 0;  // the layout has no alignment slack
-    if (sh.abort) latch_status(status, kStatusLaunch);
+    if (sh.abort) latch_status(p.a.status, kStatusLaunch);
     sh.seen_k = sh.seen_v = 0;
     fence_barrier_init();
   }
@@ -214,13 +215,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           // lane j < 8 loads 16-token tile j
           const int tok = (it.u + i) * kTile + lane * kCacheTile;
           int pg = -1;
-          if (lane < kTiles && tok < it.seen) pg = p.a.table[(int64_t)it.r * p.a.max_pages + tok / p.c.page];
+          const int64_t at = (int64_t)it.r * p.a.max_pages + tok / p.c.page;
+          if (lane < kTiles && tok < it.seen && page_at_ok(p, at)) pg = p.a.table[at];
           const bool there = (unsigned)pg < (unsigned)p.c.n_pages;
           const uint32_t have = __ballot_sync(0xffffffffu, there);
           const uint8_t* src = p.a.cache + it.h * p.c.block_bytes() + (there ? pg * p.page_bytes : 0) +
                                tok % p.c.page / kCacheTile * (2 * L::kHalf);
           for (int kv = 0; kv < 2; ++kv, ++n) {
-            if (!(ok = warp_wait(codes_empty(slot), par ^ 1, abort, status))) break;
+            if (!(ok = warp_wait(codes_empty(slot), par ^ 1, abort, p))) break;
             if (lane == 0) {
               if (kv == 0) sh.valid[(n >> 1) & 7] = have;
               mbar_expect_tx(codes_full(slot), __popc(have) * L::kHalf);
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         // never leave with a copy still writing into this CTA's shared memory
         for (int i = 0; i < kRing; ++i)
           if (n >= (uint32_t)kRing - i) {
-            drain_wait(codes_full(slot), par ^ 1);
+            drain_wait(codes_full(slot), par ^ 1, p);
             if (++slot == kRing) slot = 0, par ^= 1;
           }
       }
@@ -251,13 +253,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       do {
         const int tiles = it.left(end);
         for (int i = 0; ok && i < tiles; ++i, ++n) {
-          if (!(ok = warp_wait(bar(K_FULL, n & 1), (n >> 1) & 1, abort, status))) break;
+          if (!(ok = warp_wait(bar(K_FULL, n & 1), (n >> 1) & 1, abort, p))) break;
           if (lane == 0) {
             __threadfence_block();
             sh.seen_k = n + 1;
             mbar_arrive(bar(K_EMPTY, n & 1));
           }
-          if (!(ok = warp_wait(bar(V_FULL, n & 1), (n >> 1) & 1, abort, status))) break;
+          if (!(ok = warp_wait(bar(V_FULL, n & 1), (n >> 1) & 1, abort, p))) break;
           if (lane == 0) {
             __threadfence_block();
             sh.seen_v = n + 1;
@@ -287,13 +289,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int cnt = t.count(x);
         for (int i = 0; i <= cnt && cnt > 0; ++i) {
           const uint32_t gk = base + t.tile(x, i), gv = base + t.tile(x, i - 1);
-          if (i > 0 && !(ok = count_wait(&sh.seen_v, gv + 1, abort, status))) break;
+          if (i > 0 && !(ok = count_wait(&sh.seen_v, gv + 1, abort, p))) break;
           // (sides that share an item wait for its K tiles one after the other: there PV goes first)
-          if (i < cnt && (i == 0 || !t.split) && !(ok = count_wait(&sh.seen_k, gk + 1, abort, status))) break;
-          if (i == 0 && !(ok = warp_wait(bar(Q_FULL, x), items & 1, abort, status))) break;
+          if (i < cnt && (i == 0 || !t.split) && !(ok = count_wait(&sh.seen_k, gk + 1, abort, p))) break;
+          if (i == 0 && !(ok = warp_wait(bar(Q_FULL, x), items & 1, abort, p))) break;
           if (i > 0) {
-            if (i == 1 && items > 0 && !(ok = warp_wait(bar(O_FREE, x), (items - 1) & 1, abort, status))) break;
-            if (!(ok = warp_wait(bar(P_FULL, x), (n - 1) & 1, abort, status))) break;
+            if (i == 1 && items > 0 && !(ok = warp_wait(bar(O_FREE, x), (items - 1) & 1, abort, p))) break;
+            if (!(ok = warp_wait(bar(P_FULL, x), (n - 1) & 1, abort, p))) break;
           }
           tc_fence_after();
           if (i > 0) {
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (i < cnt) {
             if (i > 0 && t.split) {
               __syncwarp();
-              if (!(ok = count_wait(&sh.seen_k, gk + 1, abort, status))) break;
+              if (!(ok = count_wait(&sh.seen_k, gk + 1, abort, p))) break;
               tc_fence_after();
             }
             const uint64_t k = kd + (uint64_t)((gk & 1) * kOp);
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       // every MMA has finished before TMEM can be freed
       if (leader) mma_commit(bar(DONE, x));
       __syncwarp();
-      drain_wait(bar(DONE, x), 0);
+      drain_wait(bar(DONE, x), 0, p);
     }
   } else if (warp >= 12) {
     regs_down<kRegsCodes>();
@@ -359,8 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           const uint32_t st = n & 1, par = (n >> 1) & 1;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            if (!(ok = warp_wait(codes_full(slot), code_par, abort, status))) break;
-            if (!(ok = warp_wait(bar(kv ? V_EMPTY : K_EMPTY, st), par ^ 1, abort, status))) break;
+            if (!(ok = warp_wait(codes_full(slot), code_par, abort, p))) break;
+            if (!(ok = warp_wait(bar(kv ? V_EMPTY : K_EMPTY, st), par ^ 1, abort, p))) break;
             const uint32_t have = sh.valid[n & 7];
             const uint8_t* codes = smem + L::kCode + slot * L::kCodes;
             uint8_t* dst = smem + (kv ? L::kV : L::kK) + st * L::kOperand;
@@ -420,10 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       auto load_q = [&](const It& a, const Part& t) {
         const int rho = t.split ? row : x * kTile + row;
         uint8_t* dst = smem + L::kQ + x * L::kOperand;
-        const bool in = rho < t.rows;
+        const unsigned y = (unsigned)a.rb * kRows + rho, tok = y / (unsigned)p.n_rep;
+        const bool in = rho < t.rows && token_ok(p, a.q.begin + (int)tok);
         const uint4* src = nullptr;
         if (in) {
-          const unsigned y = (unsigned)a.rb * kRows + rho, tok = y / (unsigned)p.n_rep;
           src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
                                                (a.q.begin + (int)tok) * p.a.qs.token +
                                                (a.h * p.n_rep + (int)(y - tok * p.n_rep)) * p.a.qs.head);
@@ -446,12 +448,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         float m = -INFINITY, top = -INFINITY, l = 0.f;
         for (int i = 0; i < cnt; ++i, ++n) {
           const int tile = t.tile(x, i);
-          if (!(ok = warp_wait(bar(S_FULL, x), n & 1, abort, status))) break;
+          if (!(ok = warp_wait(bar(S_FULL, x), n & 1, abort, p))) break;
           // Sides with the same tiles take turns: side a's tile, then side b's once a is halfway.
           // Left alone they may fall in step, both working and then both waiting for the tensor
           // cores (0.97 ms of the chunk that takes 0.81 so; a turn of a whole tile: 0.90).
           if (!t.split) {
-            if ((x == 1 || turns > 0) && !(ok = warp_wait(bar(TURN, x), (turns - (x == 0)) & 1, abort, status))) break;
+            if ((x == 1 || turns > 0) && !(ok = warp_wait(bar(TURN, x), (turns - (x == 0)) & 1, abort, p))) break;
             ++turns;
           }
           tc_fence_after();
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         // ---------------------------------------------------------- the piece is done
         if (cnt > 0) {
-          if (!(ok = warp_wait(bar(O_FULL, x), items & 1, abort, status))) break;
+          if (!(ok = warp_wait(bar(O_FULL, x), items & 1, abort, p))) break;
           ++items;
           tc_fence_after();
         }
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const bool live = rho < ct.rows && (cnt > 0);
         // side b's rows of a slot may hold what side a has yet to read
         if (x == 1 && shared > 0 && (other || !all) &&
-            !(ok = warp_wait(bar(SHARE, 1), (shared - 1) & 1, abort, status)))
+            !(ok = warp_wait(bar(SHARE, 1), (shared - 1) & 1, abort, p)))
           break;
         if (other && x == 1) {
 #pragma unroll 1
@@ -568,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (live) S::ml(slot)[out] = make_float2(m, l);
           mbar_arrive(bar(SHARE, 0));
         }
-        if (other && x == 0 && !(ok = warp_wait(bar(SHARE, 0), shared & 1, abort, status))) break;
+        if (other && x == 0 && !(ok = warp_wait(bar(SHARE, 0), shared & 1, abort, p))) break;
         if (!(ct.split && x == 1) && cnt > 0) {
           float m1 = -INFINITY, l1 = 0.f;
           if (other && live) {
@@ -603,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           }
           if (live) {
             if (!all) S::ml(slot)[rho] = make_float2(mm, ll);
-            else if (p.a.lse) p.a.lse[orow] = lse_of(mm, ll);
+            else store_lse(p, orow, mm, ll);
           }
         }
         if (other) {

@@ -22,7 +22,7 @@ constexpr int kSums = 256;           // entries of the prefix sums over requests
 constexpr int kMaxSms = 160;         // of a GB300, and a few: the workspace's size
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr uint64_t kDrainTimeoutNs = 200000000ull;
+constexpr uint64_t kDebugTimeoutNs = 50000000ull;  // under the fault hook
 
 struct Params {
   Cache c;
@@ -34,6 +34,10 @@ struct Params {
   float sl2;                         // scale * log2(e)
   uint32_t ones;                     // kOnes
   uint64_t nonce;                    // of this launch's flags
+  uint64_t publish;                  // what a piece's flag is set to: nonce, but for the fault hook
+  uint64_t timeout_ns;               // of a wait
+  // ... for copies and MMAs in flight, before a CTA that gave up leaves
+  __device__ __forceinline__ uint64_t drain_ns() const { return timeout_ns / 10; }
 };
 
 // ---------------------------------------------------------------------------
@@ -194,7 +198,18 @@ __device__ __forceinline__ int block_rows(const Params& p, int nq, int rb, int R
   return (int)min((int64_t)RB, (int64_t)nq * p.n_rep - (int64_t)rb * RB);
 }
 
+// (rows are checked in a CPATTN_DEBUG build, as everywhere in the library)
+__device__ __forceinline__ bool row_ok(const Params& p, int64_t row) {
+  return in_bounds(row, 1, (int64_t)p.a.n_tokens * p.c.Hq, p.a.status);
+}
+__device__ __forceinline__ bool token_ok(const Params& p, int64_t token) {
+  return in_bounds(token, 1, p.a.n_tokens, p.a.status);
+}
+__device__ __forceinline__ bool page_at_ok(const Params& p, int64_t at) {  // an entry of the table
+  return in_bounds(at, 1, (int64_t)p.a.n_req * p.a.max_pages, p.a.status);
+}
 __device__ __forceinline__ void store4(const Params& p, int64_t row, int D, int ch, float4 v) {
+  if (!row_ok(p, row)) return;
   if (p.c.bf16 && !p.c.o_f32)
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.o) + row * D + ch) =
         make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
@@ -207,12 +222,16 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+__device__ __forceinline__ void store_lse(const Params& p, int64_t row, float m, float l) {
+  if (p.a.lse && row_ok(p, row)) p.a.lse[row] = lse_of(m, l);
+}
+
 // An item's rows from their sums: divided and written, 4 channels a thread.
 template <int D>
 __device__ __forceinline__ void write_out(const Params& p, int64_t row, int ch, float m, float l, float4 o) {
   const float inv = inverse(l);
   store4(p, row, D, ch, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-  if (ch == 0 && p.a.lse) p.a.lse[row] = lse_of(m, l);
+  if (ch == 0) store_lse(p, row, m, l);
 }
 
 // The sums of 4 channels of one row over pieces.  add() keeps the maximum so far.

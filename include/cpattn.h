@@ -439,6 +439,12 @@ typedef struct cpattn_cache_desc {
   int32_t causal;  /* 1: query i of a request's n_q new tokens sees the keys up to position
                       kv_len - n_q + i; 0: all kv_len keys (a shard of a cache that holds
                       only keys before the queries; its o and lse merge by cpattn_merge) */
+  int32_t debug_fault; /* 0.  Test hook of the bounded waits of cpattn_cache_attn: 1 lets
+                      the loads of the kernel for few rows, 2 those of the one for many
+                      never count as done, 3 keeps the thread blocks of the first from
+                      announcing their pieces, so that the waits on them run out
+                      (CPATTN_ERR_TIMEOUT via cpattn_check; any non-zero value shortens
+                      these kernels' waits to 50 ms) */
 } cpattn_cache_desc;
 
 /* Bytes of the cache of one layer (0 for an invalid descriptor). */

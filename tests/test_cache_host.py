@@ -106,6 +106,7 @@ BAD_DESC = [
     (dict(page=-16), 1), (dict(n_pages=0), 1), (dict(n_pages=1 << 30), 2), (dict(dtype=7), 1),
     (dict(dtype="f32", o_dtype="bf16"), 1), (dict(o_dtype=9), 1), (dict(scale=0.0), 1),
     (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(causal=2), 1),
+    (dict(debug_fault=-1), 1), (dict(debug_fault=4), 1),
 ]
 
 

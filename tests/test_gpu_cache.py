@@ -11,12 +11,18 @@ ds + 2^-20 (1 + |lse|).
 A probability below float32's least normal number, 2^-126 of the row's largest (which is at
 least 1 in the kernel's units, and so is the sum), may count as zero: where all the weight is
 on keys whose value is 0 that is what is left of o, at most 2^-126 sum |v|."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
+from conftest import ROOT
 from gpu_helpers import cp_mod, dev
 from oracle import cache as OC
+from test_gpu_canary import Guarded, check_all
 
 pytestmark = pytest.mark.gpu
 
@@ -637,6 +643,69 @@ def test_attn_with_a_device_side_batch_that_changes():
         g.replay()
         checked(c.cp, 0)
         c.compare()
+
+
+# ---------------------------------------------------------------------------
+# bounded waits, buffers' ends, the bounds-checked build
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("hook,dtype,n_q,kv", [(1, "bf16", [1, 1], [1200, 300]), (1, "bf16", [4, 1], [1200, 300]),
+                                               (1, "f32", [2], [700]), (2, "bf16", [150, 20], [1200, 300]),
+                                               (2, "bf16", [30], [2000]), (3, "bf16", [1], [9001]),
+                                               (3, "f32", [3], [4000])])
+def test_attn_timeout_is_reported_and_context_survives(hook, dtype, n_q, kv):
+    """A wait that nothing ends runs out (50 ms), is reported once, and the next call is right."""
+    c = Case(cp_mod(), H_q=4, H_kv=1, n_q=n_q, kv_len=kv, dtype=dtype)
+    c.d.debug_fault = hook
+    c.cp.check(c.run())
+    assert c.cp.cpattn_check() == c.cp.ERR_TIMEOUT
+    assert c.cp.cpattn_check() == c.cp.OK
+    c.d.debug_fault = 0
+    c.o.fill_(77.0)
+    c.lse.fill_(77.0)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype,n_q,kv,D", [("bf16", [1, 2], [100, 3001], 128), ("bf16", [4, 5], [77, 2000], 64),
+                                            ("bf16", [130, 61], [400, 1500], 128), ("f32", [1, 3], [900, 50], 64)])
+def test_calls_stay_in_their_buffers(dtype, n_q, kv, D):
+    """Every output and workspace between guard bytes, every row written."""
+    cp = cp_mod()
+    rng = np.random.default_rng(5)
+    R, H_q, H, page, cols = 2, 8, 2, 16, -(-max(kv) // 16)
+    n_pages = sum(-(-x // page) for x in kv)
+    d = cp.make_cache_desc(H_q, H, D, page, n_pages, group=32, dtype=dtype)
+    tdt = torch.float32 if dtype == "f32" else torch.bfloat16
+    i, n, new = torch.int32, sum(n_q), sum(kv)
+    b = dict(table=Guarded((R, cols), i), free=Guarded((n_pages,), i), n_free=Guarded((1,), i), lens=Guarded((R,), i),
+             start=Guarded((R + 1,), i), slots=Guarded((new,), i),
+             plan_ws=Guarded((cp.cpattn_cache_plan_workspace(d, R),), torch.uint8),
+             cache=Guarded((cp.cpattn_cache_bytes(d),), torch.uint8), k=Guarded((new, H, D), tdt),
+             v=Guarded((new, H, D), tdt), o=Guarded((n, H_q, D), tdt), lse=Guarded((n, H_q), torch.float32),
+             ws=Guarded((cp.cpattn_cache_attn_workspace(d),), torch.uint8))
+    t = {name: g.t for name, g in b.items()}
+    t["free"].copy_(i32(rng.permutation(n_pages)))
+    t["n_free"].fill_(n_pages)
+    t["lens"].zero_()
+    checked(cp, cp.cpattn_cache_plan(d, R, cols, t["lens"], i32(kv), t["table"], t["free"], t["n_free"], t["n_free"],
+                                     t["lens"], t["start"], t["slots"], new, t["plan_ws"]))
+    assert t["lens"].tolist() == kv and t["n_free"].item() == 0
+    k, v = (to_dt(rng.normal(size=(new, H, D)), dtype).to(dev()) for _ in range(2))
+    checked(cp, cp.cpattn_cache_append(d, new, k, v, t["slots"], t["cache"]))
+    checked(cp, cp.cpattn_cache_read(d, new, t["slots"], t["cache"], t["k"], t["v"]))
+    q = to_dt(rng.normal(size=(n, H_q, D)), dtype).to(dev())
+    checked(cp, cp.cpattn_cache_attn(d, R, cols, n, max(n_q), q, i32(np.concatenate([[0], np.cumsum(n_q)])), t["lens"],
+                                     t["table"], t["cache"], t["o"], t["lse"], t["ws"]))
+    check_all(b, written=("k", "v", "o", "lse"))
+
+
+@pytest.mark.skipif(os.environ.get("CPATTN_DEBUG_LIB") == "1", reason="is that build")
+def test_the_bounds_checked_build():
+    import __graft_entry__
+    __graft_entry__._build_lib().build(debug=True)
+    r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_gpu_cache.py", "-m", "gpu", "-x", "-q", "-p",
+                        "no:cacheprovider"], cwd=ROOT, env=dict(os.environ, CPATTN_DEBUG_LIB="1"), capture_output=True,
+                       text=True, timeout=900)
+    assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-2000:]
 
 
 # ---------------------------------------------------------------------------
