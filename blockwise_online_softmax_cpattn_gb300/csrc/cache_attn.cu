@@ -31,6 +31,19 @@
 //
 // float32 (NS = 3): q and P are sums of three bf16 numbers, the cached values are bf16
 // numbers anyway, so three MMAs give products of float32 quality.
+//
+// Measured (D 128, group 64, 32 query heads and 8 K/V heads where not said):
+//   128 requests of 100 to 16000 tokens, 0.94 GB: 188 us, 5.0 TB/s; a copy's rate is 6.8.
+//   The arithmetic pipe that does shifts and logic is 63 % busy, 2.5 instructions a clock
+//   issue: unpacking and the loads share the time.  (Shifts as high halves of products, on
+//   the other pipe, took 238 us: they issue at half the rate.)
+//   One request of 4096 tokens 14 us, of 131072 (8 heads each with its own, group 128) 45 us:
+//   some 14 us of a call are no work on keys, but a launch, finding the run (3), the first
+//   copy, the joins (3) and instructions that are fetched for the first time.
+//   32 requests of 500 to 12000 tokens and up to 5 new ones on 4 K/V heads, 40 rows: 76 us,
+//   three passes over the codes.  24, 32 and 40 rows at a time, queries in shared memory, took
+//   88 to 99: fewer warps, each waiting for itself.
+//   float32, 16 requests of 700 to 9000 tokens on 4 K/V heads: 29 us.
 #include <math.h>
 
 #include <algorithm>
@@ -787,10 +800,13 @@ template <int D, int G>
 static cudaError_t launch_attn(const cattn::Params& p, int sms, cudaStream_t st) {
   using namespace cattn;
   if (!p.c.bf16) return Exact8<D, G>::launch(p, sms, st);
-  // 8 rows at a time while that is all a request has, else 16.  Past three blocks of 16 every
-  // one of which unpacks the codes again, 64 rows and 112 us, the tensor memory's kernel is
-  // faster: 99 us for up to 128 rows (32 drafts of up to 8 heads a K/V group, 500 to 12000
-  // cached tokens).
+  // 8 rows at a time while that is all a request has, else 16; past three blocks of 16, each
+  // of which unpacks the codes again, the tensor memory's kernel.  32 requests of 500 to 12000
+  // cached tokens, us (8 rows, 16 rows, tensor memory):
+  //   4 K/V heads of 8 query heads: 8 rows 41, 51, 98; 16 rows 64, 55, 107; 32: 108, 89, 121;
+  //     48: 152, 121, 124; 64: 196, 152, 129; 128: 371, 273, 150
+  //   8 K/V heads of 4: 8 rows 64, 82, 179; 16 rows 109, 89, 199; 32: 197, 153, 222;
+  //     48: 283, 215, 230; 64: 370, 273, 235
   const int64_t rows = (int64_t)p.a.max_q * p.n_rep;
   if (rows <= 8) return Rows8<D, G>::launch(p, sms, st);
   if (rows <= 48) return Rows16<D, G>::launch(p, sms, st);

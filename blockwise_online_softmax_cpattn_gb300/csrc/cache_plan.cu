@@ -16,7 +16,9 @@
 // all of it is one launch of one CTA with the sums in shared memory.  A batch of prompts
 // has more tokens than one SM writes quickly: there the sums stay in the workspace and
 // a second launch, a programmatic dependent of the first, spreads pages and tokens over
-// the GPU.
+// the GPU.  Measured: 64 requests that each add a token 7 us; 700 requests, 240 000 tokens,
+// 15 us, of which the second launch is 10 (a chain of loads: sums, the search, the request's
+// numbers, the table; the sums in shared memory instead changed nothing).
 #include "cache.cuh"
 
 namespace cpattn {

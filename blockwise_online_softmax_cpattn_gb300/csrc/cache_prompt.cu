@@ -3,18 +3,19 @@
 //
 // An item is 256 query rows of one request and K/V head; its units are 128 cached tokens.
 // One CTA an SM takes an equal run of the line of items; items that cross CTAs are joined
-// by a second, small launch.  Two softmax warpgroups, sides a
-// and b, each own 128 rows' scores and output in TMEM: with more than 128 rows the sides
-// are the item's two halves and work on the same tokens, so every tile of codes is turned
-// into numbers once for 256 rows; an item of at most 128 rows goes to both sides, a taking
-// its even and b its odd tiles, and their sums are joined at the end.  While one side
-// forms its P, the tensor cores work for the other.
+// by a second, small launch.  Two softmax warpgroups, sides a and b, each own 128 rows'
+// scores and output in TMEM: with more than 128 rows the sides are the item's two halves and
+// work on the same tokens, so every tile of codes is turned into numbers once for 256 rows;
+// an item of at most 128 rows goes to both sides, a taking its even and b its odd tiles, and
+// their sums are joined at the end.  While one side forms its P, the tensor cores work for
+// the other.
 //
 // Roles (512 threads):
 //   warps 0, 1   issue side a's and b's MMAs: O += P V (P in TMEM, over the scores it came
 //                from) and the next S = Q K^T (both operands in shared memory).
-//   warp 2       loads codes, K and V of a tile apart, into a ring of three; warp 3 keeps count
-//                of the tiles that are ready.
+//   warp 2       loads codes, K and V of a tile apart, into a ring of three.
+//   warp 3       keeps count of the tiles that are ready: sides that take turns pass over
+//                tiles, and a barrier's phases can only be waited for one by one.
 //   warps 4-7    side a's softmax, a thread a row; warps 8-11 side b's.
 //   warps 12-15  turn codes into bf16 K and V tiles of 128 tokens with the 128-byte
 //                swizzle that the MMA reads, two of each.
@@ -24,8 +25,19 @@
 //
 // TMEM (512 columns): S_a [0,128), S_b [128,256), O_a, O_b D columns each from 256; P of a
 // side takes the first 64 columns of its S.
-// Every mbarrier wait is bounded; on a time-out the CTA's roles give up, its copies and MMAs
-// are drained and TMEM is freed.
+// Every wait is bounded; on a time-out the CTA's roles give up, its copies and MMAs are
+// drained and TMEM is freed.
+//
+// Measured (2048 new tokens behind 30000, 32 query heads, 8 K/V heads, D 128, group 64): 830 to
+// 860 us, 1210 to 1260 TFLOP/s, the tensor pipe 54 % busy.
+// Bound by a side's chain from one tile's scores to the next's (read 128 scores a thread, a
+// maximum, 128 exponentials, P out, PV and the next QK): both sides' take the time that the
+// tensor cores are not busy.  Turning codes into numbers takes 2500 clocks a tile on four
+// warps, of about 3300 that a tile takes, so it is hidden, and what bounds the kernel for
+// few rows (98 us for 8 rows where the kernel of cache_attn.cu takes 41).
+// Tried and slower: one warp that issues for both sides, or QK and PV apart; the dequantising
+// loop unrolled; its words, or the table's entries, loaded a step ahead (no change); masks
+// through TMEM.
 #include <atomic>
 
 #include "cache_work.cuh"
@@ -451,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (!(ok = warp_wait(bar(S_FULL, x), n & 1, abort, p))) break;
           // Sides with the same tiles take turns: side a's tile, then side b's once a is halfway.
           // Left alone they may fall in step, both working and then both waiting for the tensor
-          // cores (0.97 ms of the chunk that takes 0.81 so; a turn of a whole tile: 0.90).
+          // cores (up to 0.97 ms where this takes 0.83; with turns of a whole tile: 0.90).
           if (!t.split) {
             if ((x == 1 || turns > 0) && !(ok = warp_wait(bar(TURN, x), (turns - (x == 0)) & 1, abort, p))) break;
             ++turns;

@@ -4,9 +4,13 @@
 // tensor, two 32-bit words of codes), the D / 16 threads of a row sit side by side in a
 // warp, and the D / G groups of the row are runs of G / 16 of them, which find their
 // minimum and maximum with shuffles.  (With 8 channels a thread the work per group and
-// address made it 30 % slower.)  Each thread does so for kRows tokens, all loads first.  Bound by HBM: 2 (or 4) bytes in and 0.56 out a channel at group 64, and the
-// other way round; close behind, appending, by its instructions, so pairs of channels go
-// through the two-lane float32 operations.
+// address made it 30 % slower.)  Each thread does so for kRows tokens, all loads first.
+// Bound by HBM: 2 (or 4) bytes in and 0.56 out a channel at group 64, and the other way
+// round; close behind, appending, by its instructions, so pairs of channels go through the
+// two-lane float32 operations.
+// Measured (32768 tokens of 8 heads, D 128, group 64, bf16; 172 MB each): append 38 us, 4.5
+// TB/s, 3.0 instructions a clock issue, 15 a value; read 33 us, 5.2 TB/s.  float32, 5003
+// tokens of 12 heads of 64, group 32: 19 us for both.
 #include "cache.cuh"
 
 namespace cpattn {
@@ -275,8 +279,8 @@ cudaError_t launch_cache_append(const Cache& c, int n, const void* k, RowStrides
     using T = decltype(t);
     rows::append_kernel<T, decltype(d)::value, decltype(g)::value>
         <<<rows::grid_of(c, n, rows::kRows<T>, 16), rows::kThreads, 0, st>>>(
-            rows::Rows<decltype(d)::value, decltype(g)::value>::of(c), n, static_cast<const T*>(k), ks, static_cast<const T*>(v), vs, slots,
-            static_cast<uint8_t*>(cache), status);
+            rows::Rows<decltype(d)::value, decltype(g)::value>::of(c), n, static_cast<const T*>(k), ks,
+            static_cast<const T*>(v), vs, slots, static_cast<uint8_t*>(cache), status);
     return cudaGetLastError();
   });
   timing_end(st);
@@ -291,9 +295,9 @@ cudaError_t launch_cache_read(const Cache& c, int n, const int* slots, const voi
   const cudaError_t e = rows::dispatch(c, [&](auto t, auto d, auto g) {
     using T = decltype(t);
     rows::read_kernel<T, decltype(d)::value, decltype(g)::value>
-        <<<rows::grid_of(c, n, rows::kReadRows, 8), rows::kThreads, 0, st>>>(rows::Rows<decltype(d)::value, decltype(g)::value>::of(c), kOnes, wide, n, slots,
-                                                              static_cast<const uint8_t*>(cache),
-                                                              static_cast<T*>(k), ks, static_cast<T*>(v), vs);
+        <<<rows::grid_of(c, n, rows::kReadRows, 8), rows::kThreads, 0, st>>>(
+            rows::Rows<decltype(d)::value, decltype(g)::value>::of(c), kOnes, wide, n, slots,
+            static_cast<const uint8_t*>(cache), static_cast<T*>(k), ks, static_cast<T*>(v), vs);
     return cudaGetLastError();
   });
   timing_end(st);
