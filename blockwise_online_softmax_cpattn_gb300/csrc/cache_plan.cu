@@ -27,7 +27,10 @@ namespace plan {
 constexpr int kScanThreads = 1024;
 constexpr int kFillThreads = 256;
 constexpr int kSmallReq = 1024;       // the sums of this many requests stay on chip
-constexpr int kSmallItems = 4096;     // tokens one CTA fills as fast as a second launch starts
+// Tokens that one CTA fills about as fast as a second launch starts, us (one CTA, two
+// launches): 64 requests, 512 tokens 6.2, 8.3; 2048: 8.3, 8.6; 4096: 9.4, 8.3; 512 requests, 4096:
+// 10.3, 10.8; 1024 requests, 4096: 11.4, 12.3.
+constexpr int kSmallItems = 4096;
 
 // The per-request results of the sums: exclusive prefix sums of t, n (of the served: a
 // request that is not adds nothing) and g, and what pages and tokens are found from.
