@@ -28,8 +28,8 @@
 // Every wait is bounded; on a time-out the CTA's roles give up, its copies and MMAs are
 // drained and TMEM is freed.
 //
-// Measured (2048 new tokens behind 30000, 32 query heads, 8 K/V heads, D 128, group 64): 830 to
-// 860 us, 1210 to 1260 TFLOP/s, the tensor pipe 54 % busy.
+// Measured (2048 new tokens behind 30000, 32 query heads, 8 K/V heads, D 128, group 64): 831
+// us, 1252 TFLOP/s, the tensor pipe 54 % busy.
 // Bound by a side's chain from one tile's scores to the next's (read 128 scores a thread, a
 // maximum, 128 exponentials, P out, PV and the next QK): both sides' take the time that the
 // tensor cores are not busy.  Turning codes into numbers takes 2500 clocks a tile on four
@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       // stored V rows by 2).
       constexpr int Q = D / 32;                 // threads of a row
       constexpr int kRowsAtOnce = 128 / Q, kSteps = kTile / kRowsAtOnce;
+      static_assert(kSteps % 2 == 0, "two rows at a time");
       const int q = lane % Q, r0 = (threadIdx.x - 384) / Q;
       It it = sh.start;
       uint32_t n = 0;
@@ -371,39 +372,55 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int i = 0; ok && i < tiles; ++i, ++n) {
           const int left = it.q.len - (it.u + i) * kTile;  // tokens from the tile's first on
           const uint32_t st = n & 1, par = (n >> 1) & 1;
-#pragma unroll
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
             if (!(ok = warp_wait(codes_full(slot), code_par, abort, p))) break;
             if (!(ok = warp_wait(bar(kv ? V_EMPTY : K_EMPTY, st), par ^ 1, abort, p))) break;
             const uint32_t have = sh.valid[n & 7];
             const uint8_t* codes = smem + L::kCode + slot * L::kCodes;
             uint8_t* dst = smem + (kv ? L::kV : L::kK) + st * L::kOperand;
+            // Two rows at a time, keys and values by the same instructions (one rotation more for
+            // values): the only such warp of its scheduler has nothing else to wait with, and
+            // what is fetched once serves both (851 -> 831 us).
 #pragma unroll 1
-            for (int s = 0; s < kSteps; ++s) {
-              const int stored = s * kRowsAtOnce + r0, tile = stored / kCacheTile, rr = stored % kCacheTile;
-              // stored row t + 4e of eight is token 2t + e
-              const int row = kv ? (stored & ~7) | ((stored & 3) << 1) | ((stored >> 2) & 1) : stored;
-              const uint8_t* half = codes + tile * L::kHalf;
-              uint4 w = *reinterpret_cast<const uint4*>(half + rr * (D / 2) + q * 16);
-              uint32_t az = *reinterpret_cast<const uint32_t*>(half + kCacheTile * (D / 2) + (rr * (D / G) + q * 32 / G) * 4);
-              // rows nothing was appended to, or that were not loaded, hold anything: as zeros
-              if (row >= left || !((have >> tile) & 1u)) az = 0u;
-              const uint32_t a2 = az_a2(az), z2 = az_z2(az);
+            for (int s = 0; s < kSteps; s += 2) {
+              uint4 w[2];
+              uint32_t a2[2], z2[2];
+              uint8_t* line[2];
+              int swz[2];
               const int turn = q & 2 ? (kv ? 1 : 2) : 0;
-              if (turn == 2) w = make_uint4(w.z, w.w, w.x, w.y);
-              if (turn == 1) w = make_uint4(w.y, w.x, w.w, w.z);
-              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-              uint8_t* line = dst + (q >> 1) * (kTile * 128) + row * 128;
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                uint32_t u[4];
-                if (kv) codes_to_bf16<false>(ww[x], p.ones, u);
-                else codes_to_bf16<true>(ww[x], p.ones, u);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) u[y] = bf16x2_fma(u[y], a2, z2);
-                const int chunk = (q & 1) * 4 + (x ^ turn);
-                *reinterpret_cast<uint4*>(line + ((chunk ^ (row & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+              for (int e = 0; e < 2; ++e) {
+                const int stored = (s + e) * kRowsAtOnce + r0, tile = stored / kCacheTile, rr = stored % kCacheTile;
+                // stored row t + 4e of eight is token 2t + e
+                const int row = kv ? (stored & ~7) | ((stored & 3) << 1) | ((stored >> 2) & 1) : stored;
+                const uint8_t* half = codes + tile * L::kHalf;
+                w[e] = *reinterpret_cast<const uint4*>(half + rr * (D / 2) + q * 16);
+                uint32_t az = *reinterpret_cast<const uint32_t*>(half + kCacheTile * (D / 2) + (rr * (D / G) + q * 32 / G) * 4);
+                // rows nothing was appended to, or that were not loaded, hold anything: as zeros
+                if (row >= left || !((have >> tile) & 1u)) az = 0u;
+                a2[e] = az_a2(az);
+                z2[e] = az_z2(az);
+                line[e] = dst + (q >> 1) * (kTile * 128) + row * 128;
+                swz[e] = row & 7;
               }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if (turn == 2) w[e] = make_uint4(w[e].z, w[e].w, w[e].x, w[e].y);
+                if (turn == 1) w[e] = make_uint4(w[e].y, w[e].x, w[e].w, w[e].z);
+              }
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t ww = x == 0 ? w[e].x : x == 1 ? w[e].y : x == 2 ? w[e].z : w[e].w;
+                  uint32_t u[4];
+                  codes_to_bf16<true>(__funnelshift_l(ww, ww, kv ? 3 : 0), p.ones, u);
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) u[y] = bf16x2_fma(u[y], a2[e], z2[e]);
+                  const int chunk = (q & 1) * 4 + (x ^ turn);
+                  *reinterpret_cast<uint4*>(line[e] + ((chunk ^ swz[e]) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
