@@ -30,14 +30,16 @@
 //
 // Measured (2048 new tokens behind 30000, 32 query heads, 8 K/V heads, D 128, group 64): 831
 // us, 1252 TFLOP/s, the tensor pipe 54 % busy.
-// Bound by a side's chain from one tile's scores to the next's (read 128 scores a thread, a
-// maximum, 128 exponentials, P out, PV and the next QK): both sides' take the time that the
-// tensor cores are not busy.  Turning codes into numbers takes 2500 clocks a tile on four
-// warps, of about 3300 that a tile takes, so it is hidden, and what bounds the kernel for
-// few rows (98 us for 8 rows where the kernel of cache_attn.cu takes 41).
-// Tried and slower: one warp that issues for both sides, or QK and PV apart; the dequantising
-// loop unrolled; its words, or the table's entries, loaded a step ahead (no change); masks
-// through TMEM.
+// Bound by shared memory, which feeds the tensor cores and takes the unpacked codes: of 3800
+// clocks that a tile takes, the MMAs' operands need 1540 at its 128 bytes a clock (QK reads both
+// from there, 1024), unpacking 640 to write and read codes, and both come in bursts; and by a
+// side's chain from one tile's scores to the next's (128 scores a thread, a maximum, 128
+// exponentials, P out, PV and the next QK), which the other side fills only in part.
+// Tried and slower: one warp that issues for both sides, or QK and PV apart; scores in halves
+// of 64 tokens, the next half's formed under a half's softmax (939 us: queries are read twice
+// as often); masks through TMEM; eight warps that unpack where 64 rows leave softmax warps over
+// (132 us for 8 rows where this takes 97).  No change: codes, or the table's entries, loaded a
+// step ahead.
 #include <atomic>
 
 #include "cache_work.cuh"
