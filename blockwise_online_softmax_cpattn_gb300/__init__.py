@@ -327,13 +327,11 @@ def _typed(x, n, dtype, what) -> Optional[int]:
     """Pointer of a contiguous tensor of the type with at least n numbers."""
     if x is None or type(x) is int:
         return x
-    if x.dtype is not _dtype(dtype) or x.numel() < n or not x.is_contiguous():
+    # (the table is looked into directly, and its type asked for only when that fails: these
+    # checks are a good part of what a call of a few microseconds costs)
+    if x.dtype is not (_dtypes.get(dtype) or _dtype(dtype)) or x.numel() < n or not x.is_contiguous():
         raise ValueError(f"{what} must be contiguous {_dtype(dtype)} with at least {n} entries")
     return x.data_ptr()
-
-
-def _i32(x, n, what) -> Optional[int]:
-    return _typed(x, n, "i32", what)
 
 
 def _rows(x, n, heads, desc, what):
@@ -363,11 +361,11 @@ def cpattn_cache_plan(desc, n_req, max_pages, len_old, len_new, table, free_list
     """Pages for requests that go from len_old to len_new tokens; block table, query
     offsets and the slot of every new token."""
     return _lib.cpattn_cache_plan(
-        ctypes.byref(desc), n_req, max_pages, _i32(len_old, n_req, "len_old"),
-        _i32(len_new, n_req, "len_new"), _i32(table, n_req * max_pages, "table"),
-        _i32(free_list, desc.n_pages, "free_list"), _i32(n_free, 1, "n_free"),
-        _i32(n_free_out, 1, "n_free_out"), _i32(len_out, n_req, "len_out"),
-        _i32(q_start, n_req + 1, "q_start"), _i32(slots, n_slots, "slots"), n_slots, _ptr(workspace),
+        ctypes.byref(desc), n_req, max_pages, _typed(len_old, n_req, "i32", "len_old"),
+        _typed(len_new, n_req, "i32", "len_new"), _typed(table, n_req * max_pages, "i32", "table"),
+        _typed(free_list, desc.n_pages, "i32", "free_list"), _typed(n_free, 1, "i32", "n_free"),
+        _typed(n_free_out, 1, "i32", "n_free_out"), _typed(len_out, n_req, "i32", "len_out"),
+        _typed(q_start, n_req + 1, "i32", "q_start"), _typed(slots, n_slots, "i32", "slots"), n_slots, _ptr(workspace),
         _ws_bytes(workspace, ws_bytes), _stream(stream))
 
 
@@ -375,12 +373,12 @@ def cpattn_cache_append(desc, n_tokens, k, v, slots, cache, stream=None) -> int:
     """Quantises the rows of k and v ([n_tokens, H_kv, D], strided) into their slots."""
     return _lib.cpattn_cache_append(ctypes.byref(desc), n_tokens, *_rows(k, n_tokens, desc.H_kv, desc, "k"),
                                     *_rows(v, n_tokens, desc.H_kv, desc, "v"),
-                                    _i32(slots, n_tokens, "slots"), _cache(cache, desc), _stream(stream))
+                                    _typed(slots, n_tokens, "i32", "slots"), _cache(cache, desc), _stream(stream))
 
 
 def cpattn_cache_read(desc, n_tokens, slots, cache, k, v, stream=None) -> int:
     """The rows of the slots as keys and values ([n_tokens, H_kv, D], strided)."""
-    return _lib.cpattn_cache_read(ctypes.byref(desc), n_tokens, _i32(slots, n_tokens, "slots"),
+    return _lib.cpattn_cache_read(ctypes.byref(desc), n_tokens, _typed(slots, n_tokens, "i32", "slots"),
                                   _cache(cache, desc), *_rows(k, n_tokens, desc.H_kv, desc, "k"),
                                   *_rows(v, n_tokens, desc.H_kv, desc, "v"), _stream(stream))
 
@@ -395,8 +393,8 @@ def cpattn_cache_attn(desc, n_req, max_pages, n_tokens, max_q, q, q_start, kv_le
     be None."""
     return _lib.cpattn_cache_attn(
         ctypes.byref(desc), n_req, max_pages, n_tokens, max_q, *_rows(q, n_tokens, desc.H_q, desc, "q"),
-        _i32(q_start, n_req + 1, "q_start"), _i32(kv_len, n_req, "kv_len"),
-        _i32(table, n_req * max_pages, "table"), _cache(cache, desc),
+        _typed(q_start, n_req + 1, "i32", "q_start"), _typed(kv_len, n_req, "i32", "kv_len"),
+        _typed(table, n_req * max_pages, "i32", "table"), _cache(cache, desc),
         _typed(o, n_tokens * desc.H_q * desc.D, desc.o_dtype, "o"),
         _typed(lse, n_tokens * desc.H_q, F32, "lse"), _ptr(workspace),
         _ws_bytes(workspace, ws_bytes), _stream(stream))
