@@ -766,12 +766,14 @@ struct Variant {
     return cudaLaunchKernelEx(&cfg, kern, p);
   }
 };
+// (12 warps where their registers are full, 16 else: 16 of Exact8 at D 128 spill, 33 us for 29;
+// at D 64 16 take 92 us for 96, 16 of Rows16 70 for 74)
 template <int D, int G>
 using Rows8 = Variant<D, G, 1, 1, 16, 1>;
 template <int D, int G>
-using Rows16 = Variant<D, G, 2, 1, 12, 1>;
+using Rows16 = Variant<D, G, 2, 1, D == 64 ? 16 : 12, 1>;
 template <int D, int G>
-using Exact8 = Variant<D, G, 1, 3, 12, 1>;
+using Exact8 = Variant<D, G, 1, 3, D == 64 ? 16 : 12, 1>;
 
 }  // namespace cattn
 
@@ -809,6 +811,8 @@ static cudaError_t launch_attn(const cattn::Params& p, int sms, cudaStream_t st)
   //     48: 152, 121, 124; 64: 196, 152, 129; 128: 371, 273, 150
   //   8 K/V heads of 4: 8 rows 64, 82, 179; 16 rows 109, 89, 199; 32: 197, 153, 222;
   //     48: 283, 215, 230; 64: 370, 273, 235
+  // and 64 requests of 200 to 8000, D 64, 4 K/V heads of 8 (16 rows, tensor memory): 16 rows 44,
+  // 95; 32: 69, 112; 48: 94, 111; 56: 119, 110; 128: 221, 124.
   const int64_t rows = (int64_t)p.a.max_q * p.n_rep;
   if (rows <= 8) return Rows8<D, G>::launch(p, sms, st);
   if (rows <= 48) return Rows16<D, G>::launch(p, sms, st);
