@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
         have = page_ok ? 3u : 0u;
         if (lane == 0) {
           mbar_expect_tx(bar, page_ok ? stage_bytes : 0);
-          if (page_ok) bulk_load(dst, from + pg * p.page_bytes + w0 * tile_bytes, stage_bytes, bar);
+          if (page_ok) bulk_load(dst, from + pg * p.page_bytes + (int64_t)w0 * tile_bytes, stage_bytes, bar);
         }
         w0 = w0 + 2 == p.page_tiles ? 0 : w0 + 2;
       } else {
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
         __syncwarp();
         const int w = w0 + (lane & 1);
         if (lane < 2 && page_ok)
-          bulk_load(dst + lane * tile_bytes, from + pg * p.page_bytes + (w < p.page_tiles ? w : 0) * tile_bytes,
+          bulk_load(dst + lane * tile_bytes, from + pg * p.page_bytes + (int64_t)(w < p.page_tiles ? w : 0) * tile_bytes,
                     tile_bytes, bar);
         w0 = (w0 + 2) % p.page_tiles;
       }

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           const bool there = (unsigned)pg < (unsigned)p.c.n_pages;
           const uint32_t have = __ballot_sync(0xffffffffu, there);
           const uint8_t* src = p.a.cache + it.h * p.c.block_bytes() + (there ? pg * p.page_bytes : 0) +
-                               tok % p.c.page / kCacheTile * (2 * L::kHalf);
+                               (int64_t)(tok % p.c.page / kCacheTile) * (2 * L::kHalf);
           for (int kv = 0; kv < 2; ++kv, ++n) {
             if (!(ok = warp_wait(codes_empty(slot), par ^ 1, abort, p))) break;
             if (lane == 0) {

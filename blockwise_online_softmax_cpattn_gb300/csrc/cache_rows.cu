@@ -145,7 +145,7 @@ struct Rows {
   __device__ __forceinline__ int64_t half(int slot, int is_v, int& row) const {
     const int pg = page.div(slot), off = slot - pg * (int)page.d, t = off & (kCacheTile - 1);
     row = is_v ? cache_v_row(t) : t;
-    return pg * page_bytes + (off / kCacheTile) * (2 * kHalf);
+    return pg * page_bytes + (int64_t)(off / kCacheTile) * (2 * kHalf);
   }
 };
 

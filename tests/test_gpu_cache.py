@@ -223,6 +223,46 @@ def test_append_past_32_bits():
     assert torch.equal(o, vo)  # one key: its value
 
 
+@pytest.mark.parametrize("page,n_q", [(16 * 900000, 1), (16 * 900001, 2), (16 * 900000, 60)])
+def test_a_page_past_32_bits(page, n_q):
+    """A page whose bytes pass 32 bits: its last tokens through append, read and attention.  All
+    other keys are zeros and all other values too, so the answer is a sum of few terms."""
+    cp = cp_mod()
+    rng = np.random.default_rng(31)
+    d = cp.make_cache_desc(1, 1, 128, page, 1, group=32, causal=0, scale=1.0)
+    assert cp.cpattn_cache_bytes(d) > 1 << 31
+    c = torch.zeros(cp.cpattn_cache_bytes(d), dtype=torch.uint8, device=dev())
+    n = 20
+    slots = i32(page - n + np.arange(n))
+    k, v = np.zeros((n, 1, 128)), rng.normal(size=(n, 1, 128))
+    k[7, 0, :32] = 1.0
+    kd, vd = to_dt(k, "bf16").to(dev()), to_dt(v, "bf16").to(dev())
+    checked(cp, cp.cpattn_cache_append(d, n, kd, vd, slots, c))
+    ko, vo = torch.empty_like(kd), torch.empty_like(vd)
+    checked(cp, cp.cpattn_cache_read(d, n, slots, c, ko, vo))
+    assert np.array_equal(f32_of(ko), k)
+    vals = OC.values(*OC.quantise(f32_of(vd), 32))
+    assert np.array_equal(f32_of(vo), vals)
+    # the score of the one key: 32 q; q is bf16 and its products and their sum are exact
+    q = np.zeros((n_q, 1, 128))
+    q[:, 0, :32] = 0.5 + np.arange(n_q)[:, None] / 128
+    qd = to_dt(q, "bf16").to(dev())
+    o, lse = torch.empty(n_q, 1, 128, dtype=torch.bfloat16, device=dev()), torch.empty(n_q, 1, device=dev())
+    ws = torch.empty(cp.cpattn_cache_attn_workspace(d), dtype=torch.uint8, device=dev())
+    checked(cp, cp.cpattn_cache_attn(d, 1, 1, n_q, n_q, qd, i32([0, n_q]), i32([page]), i32([[0]]), c, o, lse, ws))
+    w = np.ones((n_q, n))
+    w[:, 7] = np.exp(32 * f32_of(qd)[:, 0, 0].astype(np.float64))
+    total = w.sum(1) + (page - n)
+    ref = w @ vals[:, 0].astype(np.float64) / total[:, None]
+    size = w @ np.abs(vals[:, 0]).astype(np.float64) / total[:, None]
+    # as at the head of this file, with exact scores; sums of up to 2^18 equal terms a thread in
+    # float32, each off by 2^-24 of the sum so far
+    got = o[:, 0].double().cpu().numpy()
+    sums = 2.0 ** -24 * 2.0 ** 18
+    assert np.all(np.abs(got - ref) <= (2.0 ** -8 + 2.0 ** -17 + sums) * size + 2.0 ** -8 * np.abs(ref) * 1.02)
+    assert np.all(np.abs(lse[:, 0].double().cpu().numpy() - np.log(total)) <= sums + 2.0 ** -17)
+
+
 # ---------------------------------------------------------------------------
 # plan
 # ---------------------------------------------------------------------------
