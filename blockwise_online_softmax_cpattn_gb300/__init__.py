@@ -323,6 +323,19 @@ def _dtype(key):
     return _dtypes.get(key)
 
 
+def _find_device() -> int:
+    global _here
+    import torch
+    if not torch.cuda.is_available():
+        return -1  # as a CPU tensor's get_device()
+    torch.cuda.init()
+    _here = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _here()
+
+
+_here = _find_device  # () -> the current device, whose memory tensors have to be in
+
+
 def _typed(x, n, dtype, what) -> Optional[int]:
     """Pointer of a contiguous tensor of the type with at least n numbers."""
     if x is None or type(x) is int:
@@ -348,9 +361,18 @@ def _rows(x, n, heads, desc, what):
     return x.data_ptr(), stride[0], stride[1]
 
 
+def _own(x, what):
+    """x, on the current device.  One tensor a call is asked (the block table or the cache, which
+    the others go with): asking each took 3 us of a call of 8."""
+    if x is not None and type(x) is not int and x.get_device() != _here():
+        raise ValueError(f"{what} is not on the current device")
+    return x
+
+
 def _cache(x, desc) -> Optional[int]:
     if x is None or type(x) is int:
         return x
+    _own(x, "the cache")
     if x.numel() * x.element_size() < cpattn_cache_bytes(desc) or not x.is_contiguous():
         raise ValueError("the cache must be contiguous and hold cpattn_cache_bytes(desc) bytes")
     return x.data_ptr()
@@ -362,7 +384,7 @@ def cpattn_cache_plan(desc, n_req, max_pages, len_old, len_new, table, free_list
     offsets and the slot of every new token."""
     return _lib.cpattn_cache_plan(
         ctypes.byref(desc), n_req, max_pages, _typed(len_old, n_req, "i32", "len_old"),
-        _typed(len_new, n_req, "i32", "len_new"), _typed(table, n_req * max_pages, "i32", "table"),
+        _typed(len_new, n_req, "i32", "len_new"), _typed(_own(table, "table"), n_req * max_pages, "i32", "table"),
         _typed(free_list, desc.n_pages, "i32", "free_list"), _typed(n_free, 1, "i32", "n_free"),
         _typed(n_free_out, 1, "i32", "n_free_out"), _typed(len_out, n_req, "i32", "len_out"),
         _typed(q_start, n_req + 1, "i32", "q_start"), _typed(slots, n_slots, "i32", "slots"), n_slots, _ptr(workspace),

@@ -419,7 +419,8 @@ cpattn_status cpattn_layout_batch(int permute, const cpattn_desc* desc, int n,
  * [n_tokens][H_q].  Inputs q, k, v (and the outputs k, v of cpattn_cache_read) take
  * strides in elements between tokens and between heads, multiples of 16 bytes, so
  * slices of a fused projection or the ring's [H_kv][T][D] tensors are passed as they
- * are; channels are contiguous.  Lengths, tables and slots are device int32.  Lengths
+ * are; channels are contiguous (a row's strides are at least D).  Every buffer is the
+ * current device's.  Lengths, tables and slots are device int32.  Lengths
  * are taken as clamped to [0, max_pages * page].  A page or slot outside the cache is
  * never touched: append skips it, read gives zeros, attention sees no key there.
  * CPATTN_ERR_UNSUPPORTED: max_pages * page past 2^30 (a request's tokens), n_req past

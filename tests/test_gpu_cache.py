@@ -796,6 +796,21 @@ def test_a_server_step_by_step():
     assert n_free.item() == n_pages - held
 
 
+def test_state_of_another_device_is_refused():
+    """(a CPU tensor stands for one)"""
+    c = Case(cp_mod(), n_q=[1], kv_len=[20])
+    cache, k, slots = c.dev[3].cpu(), torch.zeros(2, 2, 128, dtype=torch.bfloat16, device=dev()), i32([0, 1])
+    with pytest.raises(ValueError, match="current device"):
+        c.cp.cpattn_cache_attn(c.d, 1, c.table.shape[1], c.qd.shape[0], 1, c.qd, *c.dev[:3], cache, c.o, c.lse, c.ws)
+    with pytest.raises(ValueError, match="current device"):
+        c.cp.cpattn_cache_append(c.d, 2, k, k, slots, cache)
+    with pytest.raises(ValueError, match="current device"):
+        c.cp.cpattn_cache_read(c.d, 2, slots, cache, k, k)
+    x, ws = i32(np.zeros(8)), torch.zeros(4096, dtype=torch.uint8, device=dev())
+    with pytest.raises(ValueError, match="current device"):
+        c.cp.cpattn_cache_plan(c.cp.make_cache_desc(1, 1, 64, 16, 8), 2, 2, x, x, x.cpu(), *[x] * 6, 2, ws)
+
+
 def test_a_captured_decoding_step():
     """plan, append, read and attention of one step in a graph, replayed token by token: the
     same cache, table and results as eager calls."""
