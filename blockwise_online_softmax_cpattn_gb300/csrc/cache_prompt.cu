@@ -28,8 +28,8 @@
 // Every wait is bounded; on a time-out the CTA's roles give up, its copies and MMAs are
 // drained and TMEM is freed.
 //
-// Measured (2048 new tokens behind 30000, 32 query heads, 8 K/V heads, D 128, group 64): 831
-// us, 1252 TFLOP/s, the tensor pipe 54 % busy.
+// Measured (2048 new tokens behind 30000, 32 query heads, 8 K/V heads, D 128, group 64): 831 to
+// 846 us, 1230 to 1252 TFLOP/s, the tensor pipe 54 % busy.
 // Bound by shared memory, which feeds the tensor cores and takes the unpacked codes: of 3800
 // clocks that a tile takes, the MMAs' operands need 1540 at its 128 bytes a clock (QK reads both
 // from there, 1024), unpacking 640 to write and read codes, and both come in bursts; and by a
