@@ -689,20 +689,20 @@ static cudaError_t launch(Params p, int sms, cudaStream_t st) {
   auto kern = prompt_kernel<D, G>;
   constexpr int kSmem = Smem<D, G>::kBytes;
   static_assert(kSmem + sizeof(Static) <= 227 * 1024, "shared memory");
-  static std::atomic<uint64_t> set[2];  // devices whose limit is raised
+  static std::atomic<uint64_t> set[2];  // devices that are ready
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (dev >= 128 || !(set[dev >> 6].load() & bit)) {
+    // a split that does not fit what the launch allocates would wait forever: refused
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess)
       return e;
     if (dev < 128) set[dev >> 6].fetch_or(bit);
   }
-  // a split that does not fit what the launch allocates would wait forever: refused
-  cudaFuncAttributes fa;
-  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
   const int grid = sms < kMaxSms ? sms : kMaxSms;
   kern<<<grid, kThreads, kSmem, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
