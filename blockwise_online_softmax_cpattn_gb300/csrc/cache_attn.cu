@@ -113,6 +113,7 @@ struct Shared {
   uint64_t bars[WARPS * 8];
   int abort;
   int ctas;                     // that have work
+  uint64_t began;               // this CTA, in ns
   int64_t c0, c1, total;        // this CTA's run of the line, the line's length
   PieceMeta meta[WARPS];
   // per warp, what the main loop has no registers for: the items that are being loaded and
@@ -267,13 +268,15 @@ __device__ __forceinline__ void finish(const Params& p, const Shared<It, WARPS>&
   const int64_t scaled = item_end * sh.ctas + sh.total - 1;
   const int past = scaled <= 0x7fffffff ? (int)((unsigned)scaled / (unsigned)sh.total) : (int)divide(scaled, sh.total);
   const int behind = min(past - 1, sh.ctas - 1) - (int)blockIdx.x;
+  // (CTAs begin together and their runs are equal: one that takes as long again has failed)
   bool ok = true;
   for (int i = threadIdx.x; i < behind; i += WARPS * 32) {
     uint64_t* const f = flags + blockIdx.x + 1 + i;
-    uint64_t v = 0, t0 = globaltimer_ns();
+    uint64_t v = 0;
+    const uint64_t t0 = globaltimer_ns(), limit = p.timeout_ns + (t0 - sh.began);
     for (uint32_t it = 1;; ++it) {
       asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(f) : "memory");
-      if (v == p.nonce || ((it & 63u) == 0 && globaltimer_ns() - t0 > p.timeout_ns)) break;
+      if (v == p.nonce || ((it & 63u) == 0 && globaltimer_ns() - t0 > limit)) break;
     }
     ok = ok && v == p.nonce;
     *f = 0;
@@ -332,7 +335,10 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
   constexpr int half = kCacheTile * (D / 2 + 4 * par_words);
   constexpr int tile_bytes = 2 * half, stage_bytes = 2 * tile_bytes;
   volatile int* abort = &sh.abort;
-  if (threadIdx.x == 0) sh.abort = 0;
+  if (threadIdx.x == 0) {
+    sh.abort = 0;
+    sh.began = globaltimer_ns();
+  }
   if (lane == 0) {
 #pragma unroll 1
     for (int s = 0; s < p.stages; ++s)  // fault hook: one arrival more than there will be
