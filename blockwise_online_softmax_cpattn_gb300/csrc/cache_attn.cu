@@ -32,18 +32,26 @@
 // float32 (NS = 3): q and P are sums of three bf16 numbers, the cached values are bf16
 // numbers anyway, so three MMAs give products of float32 quality.
 //
+//   Sums.  An MMA cuts its sum off where a float32 addition rounds: up to 2^-23 of the sum so
+//   far is lost a step, always downwards, which grows with the tokens that one warp walks (o
+//   6e-5 too small after 20000 tokens, 6e-3 after a million).  So O, m and l are kept a span of
+//   units at a time and folded into float32 sums in the workspace after each (kSpan).  In
+//   float32 a tile's O is an MMA sum of its own besides, which float32 additions join.
+//
 // Measured (D 128, group 64, 32 query heads and 8 K/V heads where not said):
-//   128 requests of 100 to 16000 tokens, 0.94 GB: 188 us, 5.0 TB/s; a copy's rate is 6.8.
+//   128 requests of 100 to 16000 tokens, 0.94 GB: 191 us, 4.9 TB/s; a copy's rate is 6.8.
 //   The arithmetic pipe that does shifts and logic is 63 % busy, 2.5 instructions a clock
 //   issue: unpacking and the loads share the time.  (Shifts as high halves of products, on
 //   the other pipe, took 238 us: they issue at half the rate.)
-//   One request of 4096 tokens 14 us, of 131072 (8 heads each with its own, group 128) 45 us:
+//   One request of 4096 tokens 14 us, of 131072 (8 heads each with its own, group 128) 46 us:
 //   some 14 us of a call are no work on keys, but a launch, finding the run (3), the first
 //   copy, the joins (3) and instructions that are fetched for the first time.
-//   32 requests of 500 to 12000 tokens and up to 5 new ones on 4 K/V heads, 40 rows: 76 us,
+//   32 requests of 500 to 12000 tokens and up to 5 new ones on 4 K/V heads, 40 rows: 79 us,
 //   three passes over the codes.  24, 32 and 40 rows at a time, queries in shared memory, took
 //   88 to 99: fewer warps, each waiting for itself.
-//   float32, 16 requests of 700 to 9000 tokens on 4 K/V heads: 29 us.
+//   float32, 16 requests of 700 to 9000 tokens on 4 K/V heads: 31 us; 4000 new tokens
+//   of 4 heads behind 20000: 1.8 ms.
+//   The spans and the sums of a tile cost 1 to 4 % of all this (0 where items are short).
 #include <math.h>
 
 #include <algorithm>
@@ -60,13 +68,22 @@ constexpr int kUnit = 32;            // cached tokens of a unit: two tiles
 // 64 take 56, 49, 47, 50, 53 us; 128 of 100 to 16000 198, 189, 189, 190, 192.
 constexpr int kItemCost = 3;
 
+// Units after which the sums are folded (of few tokens: never).  bf16: 512 steps of an MMA, at
+// most 2^-14 of the span's sum lost, little beside P's 2^-9 a term.  float32: 64 additions, each
+// rounded to nearest, off by at most 2^-18 of it.
+template <int NS>
+constexpr int kSpan = NS == 1 ? 256 : 32;
+
 // Workspace of a launch of at most `ctas` CTAs: a slot per warp (head pieces that other
-// work followed), a head and a tail slot per CTA, a flag per CTA.
+// work followed), a head and a tail slot per CTA, the spans' sums per warp, a flag per CTA.
 template <int D, int RB, int WARPS>
 struct Work {
   static constexpr size_t kSlot = (size_t)Slot<D, RB>::kFloats;
+  // a lane's numbers as the registers hold them, (m, l) of its rows and O: float4s side by side
+  static constexpr size_t kSums = (size_t)RB / 8 * (1 + D / 16) * 32 * 4;
   static __host__ __device__ size_t cta_slots(int ctas) { return (size_t)ctas * WARPS * kSlot; }
-  static __host__ __device__ size_t flags(int ctas) { return (size_t)ctas * (WARPS + 2) * kSlot; }
+  static __host__ __device__ size_t sums(int ctas) { return (size_t)ctas * (WARPS + 2) * kSlot; }
+  static __host__ __device__ size_t flags(int ctas) { return sums(ctas) + (size_t)ctas * WARPS * kSums; }
 };
 
 // ---------------------------------------------------------------------------
@@ -121,6 +138,12 @@ struct Shared {
   It in[WARPS], it[WARPS];
   Place end[WARPS];
 };
+
+// Cached tokens up to the end of the run's part of an item.
+template <typename It>
+__device__ __forceinline__ int piece_end(const It& it, const Place& end) {
+  return (it.u + it.left(end)) * kUnit;
+}
 
 // Steps an item kept in shared memory to the next one (see cache_work.cuh: out of line).
 template <typename It>
@@ -324,6 +347,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
   constexpr int VW = D / 64;    // words of a V row per lane (channels 8 VW g ..)
   constexpr int MT = D / 16;    // 16-channel tiles of O^T
   using S = Slot<D, RB>;
+  using W = Work<D, RB, WARPS>;
   extern __shared__ __align__(128) uint8_t smem[];
   using It = Item<RB, kUnit, kItemCost>;
   __shared__ Shared<It, WARPS> sh;
@@ -419,7 +443,6 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
 
 #pragma unroll 1
     for (bool more = true; more;) {
-      int here = sh.it[warp].left(sh.end[warp]);
       const int len = sh.it[warp].q.len;
       int tok0 = sh.it[warp].u * kUnit;
       uint32_t qf[NT][NS][KW][4];
@@ -472,201 +495,248 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attn_kernel(const __grid_con
       // which it moves
       const float slack = 8.f / p.sl2;
       float m[NT][2], top[NT][2], l[NT][2], o[NT][MT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = -INFINITY;
-        top[n][0] = top[n][1] = -INFINITY;
-        l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
-      }
-
 #pragma unroll 1
-      for (; here > 0; --here, tok0 += kUnit) {
-        ok = mbar_wait(bar0 + 8 * stage, (parity >> stage) & 1u, abort, p.a.status, p.timeout_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        parity ^= 1u << stage;
-        const uint32_t have = (valid >> (2 * stage)) & 3u;
-        const uint8_t* base = reinterpret_cast<const uint8_t*>(slot_smem) + stage * stage_bytes;
-        // every row sees every token of the unit
-        const bool whole = have == 3u && tok0 + kUnit <= least;
-
-        // ---- S^T = K Q^T -------------------------------------------------------
-        float sc[2][NT][4];
+      for (;;) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint8_t* kt = base + i * tile_bytes;
-          uint32_t w0[KW], w1[KW];
-          if constexpr (KW == 4) {
-            const uint4 x = *reinterpret_cast<const uint4*>(kt + g * (D / 2) + 16 * t4);
-            const uint4 y = *reinterpret_cast<const uint4*>(kt + (g + 8) * (D / 2) + 16 * t4);
-            w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
-            w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(kt + g * (D / 2) + 8 * t4);
-            const uint2 y = *reinterpret_cast<const uint2*>(kt + (g + 8) * (D / 2) + 8 * t4);
-            w0[0] = x.x, w0[1] = x.y;
-            w1[0] = y.x, w1[1] = y.y;
-          }
-          const uint32_t* par = reinterpret_cast<const uint32_t*>(kt + kCacheTile * (D / 2));
-          const int grp = 8 * KW * t4 / G;
-          const uint32_t az0 = par[g * par_words + grp], az1 = par[(g + 8) * par_words + grp];
-          const uint32_t a0 = az_a2(az0), z0 = az_z2(az0), a1 = az_a2(az1), z1 = az_z2(az1);
+        for (int n = 0; n < NT; ++n) {
+          m[n][0] = m[n][1] = -INFINITY;
+          top[n][0] = top[n][1] = -INFINITY;
+          l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) sc[i][n][0] = sc[i][n][1] = sc[i][n][2] = sc[i][n][3] = 0.f;
-#pragma unroll
-          for (int w = 0; w < KW; ++w) {
-            uint32_t x[4], y[4];
-            codes_to_bf16<true>(w0[w], p.ones, x);
-            codes_to_bf16<true>(w1[w], p.ones, y);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              x[q] = bf16x2_fma(x[q], a0, z0);
-              y[q] = bf16x2_fma(y[q], a1, z1);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int s = NS - 1; s >= 0; --s) {
-                mma16816(sc[i][n], x[0], y[0], x[1], y[1], qf[n][s][w][0], qf[n][s][w][1]);
-                mma16816(sc[i][n], x[2], y[2], x[3], y[3], qf[n][s][w][2], qf[n][s][w][3]);
-              }
-          }
+          for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
         }
 
-        // ---- softmax -----------------------------------------------------------
-        if (!whole) {
+        const int stop = min(tok0 + kSpan<NS> * kUnit, piece_end(sh.it[warp], sh.end[warp]));
+#pragma unroll 1
+        for (; tok0 < stop; tok0 += kUnit) {
+          ok = mbar_wait(bar0 + 8 * stage, (parity >> stage) & 1u, abort, p.a.status, p.timeout_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          parity ^= 1u << stage;
+          const uint32_t have = (valid >> (2 * stage)) & 3u;
+          const uint8_t* base = reinterpret_cast<const uint8_t*>(slot_smem) + stage * stage_bytes;
+          // every row sees every token of the unit
+          const bool whole = have == 3u && tok0 + kUnit <= least;
+
+          // ---- S^T = K Q^T -------------------------------------------------------
+          float sc[2][NT][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int tok = tok0 + i * kCacheTile + g + (j >> 1) * 8;
-                if (!((have >> i) & 1u) || tok >= lim[n][j & 1]) sc[i][n][j] = -INFINITY;
-              }
-        }
-        uint32_t pf[2][NT][NS][2];
-        {
-          float mx[NT][2];
-          bool over = false;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              mx[n][e] = max3_nan(sc[0][n][e], sc[0][n][e + 2], max_nan(sc[1][n][e], sc[1][n][e + 2]));
-              over |= !(mx[n][e] <= top[n][e]);
+          for (int i = 0; i < 2; ++i) {
+            const uint8_t* kt = base + i * tile_bytes;
+            uint32_t w0[KW], w1[KW];
+            if constexpr (KW == 4) {
+              const uint4 x = *reinterpret_cast<const uint4*>(kt + g * (D / 2) + 16 * t4);
+              const uint4 y = *reinterpret_cast<const uint4*>(kt + (g + 8) * (D / 2) + 16 * t4);
+              w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
+              w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(kt + g * (D / 2) + 8 * t4);
+              const uint2 y = *reinterpret_cast<const uint2*>(kt + (g + 8) * (D / 2) + 8 * t4);
+              w0[0] = x.x, w0[1] = x.y;
+              w1[0] = y.x, w1[1] = y.y;
             }
-          if (__any_sync(0xffffffffu, over)) {
+            const uint32_t* par = reinterpret_cast<const uint32_t*>(kt + kCacheTile * (D / 2));
+            const int grp = 8 * KW * t4 / G;
+            const uint32_t az0 = par[g * par_words + grp], az1 = par[(g + 8) * par_words + grp];
+            const uint32_t a0 = az_a2(az0), z0 = az_z2(az0), a1 = az_a2(az1), z1 = az_z2(az1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) sc[i][n][0] = sc[i][n][1] = sc[i][n][2] = sc[i][n][3] = 0.f;
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {
+              uint32_t x[4], y[4];
+              codes_to_bf16<true>(w0[w], p.ones, x);
+              codes_to_bf16<true>(w1[w], p.ones, y);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                x[q] = bf16x2_fma(x[q], a0, z0);
+                y[q] = bf16x2_fma(y[q], a1, z1);
+              }
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int s = NS - 1; s >= 0; --s) {
+                  mma16816(sc[i][n], x[0], y[0], x[1], y[1], qf[n][s][w][0], qf[n][s][w][1]);
+                  mma16816(sc[i][n], x[2], y[2], x[3], y[3], qf[n][s][w][2], qf[n][s][w][3]);
+                }
+            }
+          }
+
+          // ---- softmax -----------------------------------------------------------
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int tok = tok0 + i * kCacheTile + g + (j >> 1) * 8;
+                  if (!((have >> i) & 1u) || tok >= lim[n][j & 1]) sc[i][n][j] = -INFINITY;
+                }
+          }
+          uint32_t pf[2][NT][NS][2];
+          {
+            float mx[NT][2];
+            bool over = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                float x = mx[n][e];
-#pragma unroll
-                for (int q = 4; q < 32; q <<= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, q));
-                // rows whose maximum did not move that far keep it
-                if (x <= top[n][e]) continue;
-                const float mn = max_nan(m[n][e], x * p.sl2);
-                const float f = ex2(m[n][e] - mn);
-                m[n][e] = mn;
-                top[n][e] = x + slack;
-                l[n][e] *= f;
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                  o[n][t][e] *= f;
-                  o[n][t][e + 2] *= f;
-                }
+                mx[n][e] = max3_nan(sc[0][n][e], sc[0][n][e + 2], max_nan(sc[1][n][e], sc[1][n][e + 2]));
+                over |= !(mx[n][e] <= top[n][e]);
               }
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const float2 sl2 = make_float2(p.sl2, p.sl2);
-              const float2 nm = make_float2(m[n][0] == -INFINITY ? 0.f : -m[n][0],
-                                            m[n][1] == -INFINITY ? 0.f : -m[n][1]);
-              const float2 x = fma2(make_float2(sc[i][n][0], sc[i][n][1]), sl2, nm);
-              const float2 y = fma2(make_float2(sc[i][n][2], sc[i][n][3]), sl2, nm);
-              const float pr[4] = {ex2(x.x), ex2(x.y), ex2(y.x), ex2(y.y)};
-              const float2 sum = add2(make_float2(pr[0], pr[1]), make_float2(pr[2], pr[3]));
-              const float2 ll = add2(make_float2(l[n][0], l[n][1]), sum);
-              l[n][0] = ll.x;
-              l[n][1] = ll.y;
-              uint32_t u[NS], v[NS];
-              split_pair<NS>(pr[0], pr[1], u);
-              split_pair<NS>(pr[2], pr[3], v);
-#pragma unroll
-              for (int s = 0; s < NS; ++s) {
-                pf[i][n][s][0] = transpose8x8(u[s]);
-                pf[i][n][s][1] = transpose8x8(v[s]);
-              }
-            }
-        }
-
-        // ---- O^T += V^T P^T ----------------------------------------------------
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint8_t* vt = base + i * tile_bytes + half;
-          const uint32_t* par = reinterpret_cast<const uint32_t*>(vt + kCacheTile * (D / 2));
-          const int grp = 8 * VW * g / G;
-          // tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 are in rows t4, t4 + 4, t4 + 8, t4 + 12
-          uint32_t w[4][VW], az[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int row = t4 + 4 * e;
-            if constexpr (VW == 2) {
-              const uint2 x = *reinterpret_cast<const uint2*>(vt + row * (D / 2) + 8 * g);
-              w[e][0] = x.x, w[e][1] = x.y;
-            } else {
-              w[e][0] = *reinterpret_cast<const uint32_t*>(vt + row * (D / 2) + 4 * g);
-            }
-            az[e] = par[row * par_words + grp];
-          }
-          if (!whole) {
-            // rows nothing was appended to, or that were not loaded, hold anything: as zeros
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int tok = tok0 + i * kCacheTile + 2 * t4 + (e & 1) + (e >> 1) * 8;
-              if (!((have >> i) & 1u) || tok >= len) az[e] = 0u;
-            }
-          }
-          const uint32_t a0 = __byte_perm(az[0], az[1], 0x5410), z0 = __byte_perm(az[0], az[1], 0x7632);
-          const uint32_t a1 = __byte_perm(az[2], az[3], 0x5410), z1 = __byte_perm(az[2], az[3], 0x7632);
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-            uint32_t x0[4], x1[4], y0[4], y1[4];  // even and odd channels of tokens t.., of t + 8..
-            codes_to_bf16<false>(__byte_perm(w[0][j], w[1][j], 0x5410), p.ones, x0);
-            codes_to_bf16<false>(__byte_perm(w[0][j], w[1][j], 0x7632), p.ones, x1);
-            codes_to_bf16<false>(__byte_perm(w[2][j], w[3][j], 0x5410), p.ones, y0);
-            codes_to_bf16<false>(__byte_perm(w[2][j], w[3][j], 0x7632), p.ones, y1);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t f0 = bf16x2_fma(x0[q], a0, z0), f1 = bf16x2_fma(x1[q], a0, z0);
-              const uint32_t f2 = bf16x2_fma(y0[q], a1, z1), f3 = bf16x2_fma(y1[q], a1, z1);
+            if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int s = NS - 1; s >= 0; --s)
-                  mma16816(o[n][j * 4 + q], f0, f1, f2, f3, pf[i][n][s][0], pf[i][n][s][1]);
+                for (int e = 0; e < 2; ++e) {
+                  float x = mx[n][e];
+#pragma unroll
+                  for (int q = 4; q < 32; q <<= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, q));
+                  // rows whose maximum did not move that far keep it
+                  if (x <= top[n][e]) continue;
+                  const float mn = max_nan(m[n][e], x * p.sl2);
+                  const float f = ex2(m[n][e] - mn);
+                  m[n][e] = mn;
+                  top[n][e] = x + slack;
+                  l[n][e] *= f;
+#pragma unroll
+                  for (int t = 0; t < MT; ++t) {
+                    o[n][t][e] *= f;
+                    o[n][t][e + 2] *= f;
+                  }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const float2 sl2 = make_float2(p.sl2, p.sl2);
+                const float2 nm = make_float2(m[n][0] == -INFINITY ? 0.f : -m[n][0],
+                                              m[n][1] == -INFINITY ? 0.f : -m[n][1]);
+                const float2 x = fma2(make_float2(sc[i][n][0], sc[i][n][1]), sl2, nm);
+                const float2 y = fma2(make_float2(sc[i][n][2], sc[i][n][3]), sl2, nm);
+                const float pr[4] = {ex2(x.x), ex2(x.y), ex2(y.x), ex2(y.y)};
+                const float2 sum = add2(make_float2(pr[0], pr[1]), make_float2(pr[2], pr[3]));
+                const float2 ll = add2(make_float2(l[n][0], l[n][1]), sum);
+                l[n][0] = ll.x;
+                l[n][1] = ll.y;
+                uint32_t u[NS], v[NS];
+                split_pair<NS>(pr[0], pr[1], u);
+                split_pair<NS>(pr[2], pr[3], v);
+#pragma unroll
+                for (int s = 0; s < NS; ++s) {
+                  pf[i][n][s][0] = transpose8x8(u[s]);
+                  pf[i][n][s][1] = transpose8x8(v[s]);
+                }
+              }
+          }
+
+          // ---- O^T += V^T P^T ----------------------------------------------------
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint8_t* vt = base + i * tile_bytes + half;
+            const uint32_t* par = reinterpret_cast<const uint32_t*>(vt + kCacheTile * (D / 2));
+            const int grp = 8 * VW * g / G;
+            // tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 are in rows t4, t4 + 4, t4 + 8, t4 + 12
+            uint32_t w[4][VW], az[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int row = t4 + 4 * e;
+              if constexpr (VW == 2) {
+                const uint2 x = *reinterpret_cast<const uint2*>(vt + row * (D / 2) + 8 * g);
+                w[e][0] = x.x, w[e][1] = x.y;
+              } else {
+                w[e][0] = *reinterpret_cast<const uint32_t*>(vt + row * (D / 2) + 4 * g);
+              }
+              az[e] = par[row * par_words + grp];
+            }
+            if (!whole) {
+              // rows nothing was appended to, or that were not loaded, hold anything: as zeros
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int tok = tok0 + i * kCacheTile + 2 * t4 + (e & 1) + (e >> 1) * 8;
+                if (!((have >> i) & 1u) || tok >= len) az[e] = 0u;
+              }
+            }
+            const uint32_t a0 = __byte_perm(az[0], az[1], 0x5410), z0 = __byte_perm(az[0], az[1], 0x7632);
+            const uint32_t a1 = __byte_perm(az[2], az[3], 0x5410), z1 = __byte_perm(az[2], az[3], 0x7632);
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+              uint32_t x0[4], x1[4], y0[4], y1[4];  // even and odd channels of tokens t.., of t + 8..
+              codes_to_bf16<false>(__byte_perm(w[0][j], w[1][j], 0x5410), p.ones, x0);
+              codes_to_bf16<false>(__byte_perm(w[0][j], w[1][j], 0x7632), p.ones, x1);
+              codes_to_bf16<false>(__byte_perm(w[2][j], w[3][j], 0x5410), p.ones, y0);
+              codes_to_bf16<false>(__byte_perm(w[2][j], w[3][j], 0x7632), p.ones, y1);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t f0 = bf16x2_fma(x0[q], a0, z0), f1 = bf16x2_fma(x1[q], a0, z0);
+                const uint32_t f2 = bf16x2_fma(y0[q], a1, z1), f3 = bf16x2_fma(y1[q], a1, z1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  float(&to)[4] = o[n][j * 4 + q];
+                  if constexpr (NS == 1) {
+                    mma16816(to, f0, f1, f2, f3, pf[i][n][0][0], pf[i][n][0][1]);
+                  } else {
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = NS - 1; s >= 0; --s)
+                      mma16816(d, f0, f1, f2, f3, pf[i][n][s][0], pf[i][n][s][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) to[e] += d[e];
+                  }
+                }
+              }
+            }
+          }
+          // the stage has been read
+          __syncwarp();
+          if (++stage == p.stages) stage = 0;
+          if (to_issue > 0) issue();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int q = 4; q < 32; q <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], q);
+        // ---- the span is done ----------------------------------------------------
+        const bool held = sh.it[warp].u * kUnit + kSpan<NS> * kUnit < tok0;   // there were spans before
+        const bool more_spans = tok0 < piece_end(sh.it[warp], sh.end[warp]);
+        if (held || more_spans) {
+          // with the earlier spans' sums, in each lane's own place
+          float4* const sum = reinterpret_cast<float4*>(
+                                  static_cast<float*>(p.a.ws) + W::sums(gridDim.x) +
+                                  ((size_t)blockIdx.x * WARPS + warp) * W::kSums) + lane;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float4* const at = sum + n * (1 + MT) * 32;
+            const float4 ml = held ? at[0] : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+            const float mx0 = max_nan(m[n][0], ml.x), mx1 = max_nan(m[n][1], ml.y);
+            const float b0 = mx0 == -INFINITY ? 0.f : mx0, b1 = mx1 == -INFINITY ? 0.f : mx1;
+            const float f0 = ex2(ml.x - b0), f1 = ex2(ml.y - b1), w0 = ex2(m[n][0] - b0), w1 = ex2(m[n][1] - b1);
+            m[n][0] = mx0;
+            m[n][1] = mx1;
+            l[n][0] = fmaf(ml.z, f0, l[n][0] * w0);
+            l[n][1] = fmaf(ml.w, f1, l[n][1] * w1);
+            if (more_spans) at[0] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              const float4 x = held ? at[(1 + t) * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
+              float(&u)[4] = o[n][t];
+              u[0] = fmaf(x.x, f0, u[0] * w0);
+              u[1] = fmaf(x.y, f1, u[1] * w1);
+              u[2] = fmaf(x.z, f0, u[2] * w0);
+              u[3] = fmaf(x.w, f1, u[3] * w1);
+              if (more_spans) at[(1 + t) * 32] = make_float4(u[0], u[1], u[2], u[3]);
             }
           }
         }
-        // the stage has been read
-        __syncwarp();
-        if (++stage == p.stages) stage = 0;
-        if (to_issue > 0) issue();
+        if (!more_spans) break;
       }
       if (!ok) break;
 
       // ---- the piece is done ---------------------------------------------------
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int q = 4; q < 32; q <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], q);
       const It it = sh.it[warp];
       const bool starts = it.u == 0, ends = it.u + it.left(sh.end[warp]) == it.units;
       const int rows = block_rows(p, it.q.nq, it.rb, RB);

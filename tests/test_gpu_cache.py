@@ -685,6 +685,61 @@ def test_attn_with_a_device_side_batch_that_changes():
         c.compare()
 
 
+def _long_run(dtype, rows, L, R, n_q=1, D=128, group=64, page=64, qs=0.0, seed=0):
+    """R requests of n_q tokens and `rows` query heads over the pages of one prefix of L tokens,
+    float32 results.  Values are positive and of many sizes, so that sums use every bit they have;
+    queries of size qs.  Returns o, lse and, of a few rows, (their index, o, lse, ds) in 64 bits."""
+    cp = cp_mod()
+    rng = np.random.default_rng(seed)
+    n_pages = -(-L // page)
+    d = cp.make_cache_desc(rows, 1, D, page, n_pages, group=group, dtype=dtype, o_dtype="f32", causal=0)
+    cache = make_cache(cp, d, rng).reshape(-1, 2, 16 * (D // 2 + 4 * (D // group)))
+    az = np.zeros((cache.shape[0], 2, 16 * (D // group), 2), np.float32)
+    az[:, 0] = 2.0, -2.9375                            # keys within +-1
+    az[:, 1, :, 0] = np.exp(rng.normal(size=az.shape[:1] + az.shape[2:3]))
+    cache[:, :, 16 * (D // 2):] = OC.bf16_bits(OC.round_bf16(az)).astype("<u2").view(np.uint8).reshape(
+        cache.shape[0], 2, -1)
+    cache = cache.reshape(n_pages, 1, -1)
+    q = to_dt(qs * rng.normal(size=(R * n_q, rows, D)), dtype)
+    o, lse = torch.empty(R * n_q, rows, D, device=dev()), torch.empty(R * n_q, rows, device=dev())
+    ws = torch.empty(cp.cpattn_cache_attn_workspace(d), dtype=torch.uint8, device=dev())
+    table = i32(np.arange(n_pages))[None].repeat(R, 1)
+    checked(cp, cp.cpattn_cache_attn(d, R, n_pages, R * n_q, n_q, q.to(dev()), i32(np.arange(R + 1) * n_q),
+                                     i32(np.full(R, L)), table, torch.from_numpy(cache).to(dev()), o, lse, ws))
+    k, v = OC.read(cache, page, group, D, np.arange(L))
+    out = []
+    for t in rng.integers(0, R * n_q, 6 if qs else 1):
+        h = int(rng.integers(0, rows))
+        ref, ref_lse, _, size = OC.attention(f32_of(q[t:t + 1, h]).astype(np.float64), k[:, 0], v[:, 0], [L], d.scale)
+        out.append((int(t), h, ref[0], ref_lse[0], 2.0 ** -23 * (D + 8) * size))
+    return o, lse, out
+
+
+@pytest.mark.parametrize("rows,D,group", [(8, 128, 64), (3, 128, 32), (8, 64, 64)])
+def test_attn_float32_sums_over_long_runs(rows, D, group):
+    """A warp that walks 750 units of a request.  What the sums may lose, of sum p |v| and of sum p
+    alike: 64 additions a span, each rounded to nearest, 2^-18; 24 folds of two roundings, 2^-18.4;
+    a tile's three products on the tensor cores, 3 2^-23; the exponential, 2^-21: below 2^-17, so o
+    is off by at most 2^-16 sum p |v| and what the scores are (2 ds)."""
+    o, lse, rows64 = _long_run("f32", rows, 24000, 5000, D=D, group=group, qs=0.003)
+    for t, h, ref, ref_lse, ds in rows64:
+        err = np.abs(o[t, h].double().cpu().numpy() - ref)
+        assert np.all(err <= (2 * ds + 2.0 ** -16) * ref), (err / ref).max()
+        assert abs(lse[t, h].item() - ref_lse) <= ds + 2.0 ** -17 + 2.0 ** -20 * (1 + abs(ref_lse))
+
+
+@pytest.mark.parametrize("rows,D,L", [(8, 128, 200000), (16, 128, 200000), (5, 64, 150000), (13, 64, 150000)])
+def test_attn_sums_over_long_runs(rows, D, L):
+    """Scores of zero: P is 1 and its sum exact.  O may lose 2^-23 of its sum at each of the 512
+    steps that a span has on the tensor cores, 2^-14 in all; the folds of the spans (25) two
+    roundings each, below 2^-18.  (One sum of all the steps would be 1e-3 too small.)"""
+    o, lse, rows64 = _long_run("bf16", rows, L, 5000, D=D)
+    for t, h, ref, ref_lse, _ in rows64:
+        err = np.abs(o[t, h].double().cpu().numpy() - ref)
+        assert np.all(err <= (2.0 ** -14 + 2.0 ** -17) * ref), (err / ref).max()
+        assert abs(lse[t, h].item() - ref_lse) <= 2.0 ** -20 * (1 + abs(ref_lse))
+
+
 # ---------------------------------------------------------------------------
 # bounded waits, buffers' ends, the bounds-checked build
 # ---------------------------------------------------------------------------
