@@ -28,8 +28,8 @@
 // Every wait is bounded; on a time-out the CTA's roles give up, its copies and MMAs are
 // drained and TMEM is freed.
 //
-// Measured (2048 new tokens behind 30000, 32 query heads, 8 K/V heads, D 128, group 64): 831 to
-// 846 us, 1230 to 1252 TFLOP/s, the tensor pipe 54 % busy.
+// Measured (2048 new tokens behind 30000, 32 query heads, 8 K/V heads, D 128, group 64): 844 us,
+// 1233 TFLOP/s (without the spans below 830), the tensor pipe 54 % busy.
 // Bound by shared memory, which feeds the tensor cores and takes the unpacked codes: of 3800
 // clocks that a tile takes, the MMAs' operands need 1540 at its 128 bytes a clock (QK reads both
 // from there, 1024), unpacking 640 to write and read codes, and both come in bursts; and by a
@@ -65,6 +65,12 @@ __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 constexpr int kItemCost = 3;    // queries in, results out, in units
+// Tiles of a side after which its sums are folded.  An MMA cuts its sum off where a float32
+// addition rounds: up to 2^-23 of the sum so far is lost at each of a tile's 8 steps, always
+// downwards (a million tokens: o 6e-3 too small).  So O, m and l are kept a span at a time and
+// folded into float32 sums in the workspace: at most 2^-13 of a span's sum is lost, little
+// beside P's 2^-9 a term.
+constexpr int kSpan = 128;   // (a power of 2)
 using It = Item<kRows, kTile, kItemCost>;
 
 template <int D, int G>
@@ -135,6 +141,52 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t par, const Par
   int never = 0;
   mbar_wait(bar, par, &never, nullptr, p.drain_ns());
 }
+// Workspace: a head and a tail slot per CTA, the CTAs' states, the spans' sums per CTA: O as
+// [D / 4][rows] float4, (m, l) of the rows.
+template <int D>
+struct Work {
+  static constexpr size_t kSums = (size_t)kRows * (D + 2);
+  static __host__ __device__ size_t meta(int ctas) { return 2 * (size_t)ctas * Slot<D, kRows>::kFloats; }
+  static __host__ __device__ size_t sums(int ctas) {
+    return meta(ctas) + (ctas * sizeof(CtaMeta) + 15) / 16 * 4;
+  }
+  static __host__ __device__ size_t floats(int ctas) { return sums(ctas) + ctas * kSums; }
+};
+// A span's O (in TMEM), m and l of a thread's row join those of the spans before it (none: first):
+// in the workspace, or, of an item's last span, in TMEM; m and l are returned.  Out of line and out of
+// the loop over tiles: inlined into the softmax it cost 10 %, called from the loop 4.
+template <int D>
+__device__ __noinline__ float2 fold_span(const Params& p, uint32_t t_o, float m, float l, bool first, bool last) {
+  float* const sums = static_cast<float*>(p.a.ws) + Work<D>::sums(gridDim.x) + (size_t)blockIdx.x * Work<D>::kSums;
+  const int row = threadIdx.x - 128;   // of the two softmax warpgroups
+  float4* const sum_o = reinterpret_cast<float4*>(sums) + row;
+  float2* const sum_ml = reinterpret_cast<float2*>(sums + (size_t)kRows * D) + row;
+  const float2 ml = first ? make_float2(-INFINITY, 0.f) : *sum_ml;
+  const float mm = max_nan(m, ml.x), mb = mm == -INFINITY ? 0.f : mm;
+  const float f = ex2(ml.x - mb), w = ex2(m - mb);
+  const float2 joined = make_float2(mm, fmaf(ml.y, f, l * w));
+#pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t o[16];
+    tmem_ld16(t_o + c * 16, o);
+    tmem_wait_ld_of(o);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float4* const at = sum_o + (c * 4 + j) * kRows;
+      const float4 y = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *at;
+      const float4 v = make_float4(
+          fmaf(y.x, f, w * __uint_as_float(o[4 * j])), fmaf(y.y, f, w * __uint_as_float(o[4 * j + 1])),
+          fmaf(y.z, f, w * __uint_as_float(o[4 * j + 2])), fmaf(y.w, f, w * __uint_as_float(o[4 * j + 3])));
+      if (!last) *at = v;
+      o[4 * j] = __float_as_uint(v.x), o[4 * j + 1] = __float_as_uint(v.y);
+      o[4 * j + 2] = __float_as_uint(v.z), o[4 * j + 3] = __float_as_uint(v.w);
+    }
+    if (last) tmem_st16(t_o + c * 16, o);
+  }
+  if (last) tmem_wait_st();
+  else *sum_ml = joined;
+  return joined;
+}
 // What both sides' walks have in common: the tiles [u, u + n) of an item, and which of them
 // side x takes.
 struct Part {
@@ -173,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   auto codes_empty = [&](int i) { return bars + 8 * (2 * CODES + kRing + i); };
   volatile int* abort = &sh.abort;
   float* const ws = static_cast<float*>(p.a.ws);
-  CtaMeta* const out_meta = reinterpret_cast<CtaMeta*>(ws + 2 * (size_t)gridDim.x * S::kFloats);
+  CtaMeta* const out_meta = reinterpret_cast<CtaMeta*>(ws + Work<D>::meta(gridDim.x));
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
@@ -317,7 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               if (leader)
-                mma_ts(t_o, t_s + kk * 8, v + (uint64_t)(kk * 128), kIdescPV, (i > 1 || kk > 0) ? 1u : 0u);
+                mma_ts(t_o, t_s + kk * 8, v + (uint64_t)(kk * 128), kIdescPV,
+                       (((i - 1) & (kSpan - 1)) != 0 || kk > 0) ? 1u : 0u);
             if (leader) {
               if (t.split) mbar_arrive(bar(V_EMPTY, gv & 1));  // for the side that passes it over
               mma_commit(bar(V_EMPTY, gv & 1));
@@ -477,87 +530,99 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int lim = seen_by(p, it.q, it.rb * kRows + rho);
         const int least = seen_by(p, it.q, it.rb * kRows + (t.split ? 0 : x * kTile));
         float m = -INFINITY, top = -INFINITY, l = 0.f;
-        for (int i = 0; i < cnt; ++i, ++n) {
-          const int tile = t.tile(x, i);
-          if (!(ok = warp_wait(bar(S_FULL, x), n & 1, abort, p))) break;
-          // Sides with the same tiles take turns: side a's tile, then side b's once a is halfway.
-          // Left alone they may fall in step, both working and then both waiting for the tensor
-          // cores (up to 0.97 ms where this takes 0.83; with turns of a whole tile: 0.90).
-          if (!t.split) {
-            if ((x == 1 || turns > 0) && !(ok = warp_wait(bar(TURN, x), (turns - (x == 0)) & 1, abort, p))) break;
-            ++turns;
+#pragma unroll 1
+        for (int from = 0, to; ok && from < cnt; from = to) {
+          to = min(cnt, from + kSpan);
+          if (from > 0) {
+            // the span's sums join those before it; its last PV was done before the next scores
+            if (!(ok = warp_wait(bar(S_FULL, x), n & 1, abort, p))) break;
+            tc_fence_after();
+            fold_span<D>(p, t_o, m, l, from == kSpan, false);
+            m = top = -INFINITY;
+            l = 0.f;
           }
-          tc_fence_after();
-          const int tok0 = (it.u + tile) * kTile;
-          const uint32_t have = sh.valid[(base + tile) & 7];
-          const bool whole = have == (1u << kTiles) - 1 && tok0 + kTile <= least;
-          // all 128 scores in registers: P goes over them in TMEM
-          uint32_t r[4][32];
+          for (int i = from; i < to; ++i, ++n) {
+            const int tile = t.tile(x, i);
+            if (!(ok = warp_wait(bar(S_FULL, x), n & 1, abort, p))) break;
+            // Sides with the same tiles take turns: side a's tile, then side b's once a is halfway.
+            // Left alone they may fall in step, both working and then both waiting for the tensor
+            // cores (up to 0.97 ms where this takes 0.83; with turns of a whole tile: 0.90).
+            if (!t.split) {
+              if ((x == 1 || turns > 0) && !(ok = warp_wait(bar(TURN, x), (turns - (x == 0)) & 1, abort, p))) break;
+              ++turns;
+            }
+            tc_fence_after();
+            const int tok0 = (it.u + tile) * kTile;
+            const uint32_t have = sh.valid[(base + tile) & 7];
+            const bool whole = have == (1u << kTiles) - 1 && tok0 + kTile <= least;
+            // all 128 scores in registers: P goes over them in TMEM
+            uint32_t r[4][32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, r[c]);
+            for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, r[c]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_wait_ld_of(r[c]);
-          if (!whole) {
+            for (int c = 0; c < 4; ++c) tmem_wait_ld_of(r[c]);
+            if (!whole) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int rel = lim - tok0 - 32 * c;   // columns below it are seen
+                const int rel0 = (have >> (2 * c)) & 1u ? rel : 0, rel1 = (have >> (2 * c + 1)) & 1u ? rel : 0;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (j >= (j < 16 ? rel0 : rel1)) r[c][j] = __float_as_uint(-INFINITY);
+              }
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int j = 0; j < 32; j += 2)
+                mx[(j >> 1) & 3] =
+                    max3_nan(mx[(j >> 1) & 3], __uint_as_float(r[c][j]), __uint_as_float(r[c][j + 1]));
+            const float hi = max_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]);
+            const bool over = !(hi <= top);
+            float f = 1.f;
+            if (over) {
+              const float mn = max_nan(m, hi * p.sl2);
+              f = ex2(m - mn);
+              m = mn;
+              top = hi + slack;
+              l *= f;
+            }
+            if (i > from && __any_sync(0xffffffffu, over)) {
+              // (these scores were formed after the PV before them was done)
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(t_o + c * 16, o);
+                tmem_wait_ld_of(o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st16(t_o + c * 16, o);
+              }
+            }
+            const float nm = m == -INFINITY ? 0.f : -m;
+            const float2 nm2 = make_float2(nm, nm);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const int rel = lim - tok0 - 32 * c;   // columns below it are seen
-              const int rel0 = (have >> (2 * c)) & 1u ? rel : 0, rel1 = (have >> (2 * c + 1)) & 1u ? rel : 0;
+              uint32_t pk[16];
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (j >= (j < 16 ? rel0 : rel1)) r[c][j] = __float_as_uint(-INFINITY);
+              for (int j = 0; j < 16; ++j) {
+                const float2 y =
+                    fma2(make_float2(__uint_as_float(r[c][2 * j]), __uint_as_float(r[c][2 * j + 1])), sl2, nm2);
+                const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                sum[j & 1] = add2(sum[j & 1], e);
+                pk[j] = pack_bf16(e.x, e.y);
+              }
+              tmem_st16(t_s + c * 16, pk);
+              if (c == 1 && !t.split && lane == 0) mbar_arrive(bar(TURN, 1 - x));
             }
+            const float2 s2 = add2(sum[0], sum[1]);
+            l += s2.x + s2.y;
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(P_FULL, x));
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 32; j += 2)
-              mx[(j >> 1) & 3] =
-                  max3_nan(mx[(j >> 1) & 3], __uint_as_float(r[c][j]), __uint_as_float(r[c][j + 1]));
-          const float hi = max_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]);
-          const bool over = !(hi <= top);
-          float f = 1.f;
-          if (over) {
-            const float mn = max_nan(m, hi * p.sl2);
-            f = ex2(m - mn);
-            m = mn;
-            top = hi + slack;
-            l *= f;
-          }
-          if (i > 0 && __any_sync(0xffffffffu, over)) {
-            // (these scores were formed after the PV before them was done)
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(t_o + c * 16, o);
-              tmem_wait_ld_of(o);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st16(t_o + c * 16, o);
-            }
-          }
-          const float nm = m == -INFINITY ? 0.f : -m;
-          const float2 nm2 = make_float2(nm, nm);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 y =
-                  fma2(make_float2(__uint_as_float(r[c][2 * j]), __uint_as_float(r[c][2 * j + 1])), sl2, nm2);
-              const float2 e = make_float2(ex2(y.x), ex2(y.y));
-              sum[j & 1] = add2(sum[j & 1], e);
-              pk[j] = pack_bf16(e.x, e.y);
-            }
-            tmem_st16(t_s + c * 16, pk);
-            if (c == 1 && !t.split && lane == 0) mbar_arrive(bar(TURN, 1 - x));
-          }
-          const float2 s2 = add2(sum[0], sum[1]);
-          l += s2.x + s2.y;
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(bar(P_FULL, x));
         }
         if (!ok) break;
         // the next item's queries, so that its first scores can start
@@ -580,6 +645,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const bool other = ct.split && ct.n > 1;
         const int out = other && x == 1 ? kTile + row : rho;
         const bool live = rho < ct.rows && (cnt > 0);
+        if (cnt > kSpan) {
+          const float2 ml = fold_span<D>(p, t_o, m, l, false, true);
+          m = ml.x;
+          l = ml.y;
+        }
         // side b's rows of a slot may hold what side a has yet to read
         if (x == 1 && shared > 0 && (other || !all) &&
             !(ok = warp_wait(bar(SHARE, 1), (shared - 1) & 1, abort, p)))
@@ -681,7 +751,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   griddep_wait();
   const float* const ws = static_cast<const float*>(p.a.ws);
   join_ctas<D, kRows, kThreads>(
-      p, reinterpret_cast<const CtaMeta*>(ws + 2 * (size_t)gridDim.x * Slot<D, kRows>::kFloats), ws, scratch);
+      p, reinterpret_cast<const CtaMeta*>(ws + Work<D>::meta(gridDim.x)), ws, scratch);
 }
 
 template <int D, int G>
@@ -722,8 +792,7 @@ static cudaError_t launch(Params p, int sms, cudaStream_t st) {
 
 size_t cache_prompt_workspace(int D) {
   using namespace cprompt;
-  const size_t slot = D == 128 ? Slot<128, kRows>::kFloats : Slot<64, kRows>::kFloats;
-  return kMaxSms * (2 * slot * sizeof(float) + sizeof(CtaMeta));
+  return sizeof(float) * (D == 128 ? Work<128>::floats(kMaxSms) : Work<64>::floats(kMaxSms));
 }
 
 cudaError_t launch_cache_prompt(const cattn::Params& p, int sms, cudaStream_t st) {

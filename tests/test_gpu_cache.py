@@ -686,13 +686,13 @@ def test_attn_with_a_device_side_batch_that_changes():
 
 
 def _long_run(dtype, rows, L, R, n_q=1, D=128, group=64, page=64, qs=0.0, seed=0):
-    """R requests of n_q tokens and `rows` query heads over the pages of one prefix of L tokens,
+    """R requests of n_q tokens and `rows` query heads over the same pages of L tokens, causal,
     float32 results.  Values are positive and of many sizes, so that sums use every bit they have;
     queries of size qs.  Returns o, lse and, of a few rows, (their index, o, lse, ds) in 64 bits."""
     cp = cp_mod()
     rng = np.random.default_rng(seed)
     n_pages = -(-L // page)
-    d = cp.make_cache_desc(rows, 1, D, page, n_pages, group=group, dtype=dtype, o_dtype="f32", causal=0)
+    d = cp.make_cache_desc(rows, 1, D, page, n_pages, group=group, dtype=dtype, o_dtype="f32")
     cache = make_cache(cp, d, rng).reshape(-1, 2, 16 * (D // 2 + 4 * (D // group)))
     az = np.zeros((cache.shape[0], 2, 16 * (D // group), 2), np.float32)
     az[:, 0] = 2.0, -2.9375                            # keys within +-1
@@ -708,9 +708,10 @@ def _long_run(dtype, rows, L, R, n_q=1, D=128, group=64, page=64, qs=0.0, seed=0
                                      i32(np.full(R, L)), table, torch.from_numpy(cache).to(dev()), o, lse, ws))
     k, v = OC.read(cache, page, group, D, np.arange(L))
     out = []
-    for t in rng.integers(0, R * n_q, 6 if qs else 1):
+    for t in rng.integers(0, R * n_q, 6 if qs or n_q > 1 else 1):
         h = int(rng.integers(0, rows))
-        ref, ref_lse, _, size = OC.attention(f32_of(q[t:t + 1, h]).astype(np.float64), k[:, 0], v[:, 0], [L], d.scale)
+        ref, ref_lse, _, size = OC.attention(f32_of(q[t:t + 1, h]).astype(np.float64), k[:, 0], v[:, 0],
+                                               [L - n_q + t % n_q + 1], d.scale)
         out.append((int(t), h, ref[0], ref_lse[0], 2.0 ** -23 * (D + 8) * size))
     return o, lse, out
 
@@ -738,6 +739,33 @@ def test_attn_sums_over_long_runs(rows, D, L):
         err = np.abs(o[t, h].double().cpu().numpy() - ref)
         assert np.all(err <= (2.0 ** -14 + 2.0 ** -17) * ref), (err / ref).max()
         assert abs(lse[t, h].item() - ref_lse) <= 2.0 ** -20 * (1 + abs(ref_lse))
+
+
+@pytest.mark.parametrize("rows,n_q,R,D,group,L", [(4, 20000, 1, 128, 64, 220000), (4, 16, 400, 128, 128, 180000),
+                                                  (6, 9, 400, 64, 32, 150001), (4, 20000, 1, 64, 64, 150000)])
+def test_attn_prompt_sums_over_long_runs(rows, n_q, R, D, group, L):
+    """As above, of many rows (halves of items that share the tokens, and that share the rows): a
+    span has 1024 steps, 2^-13."""
+    o, lse, rows64 = _long_run("bf16", rows, L, R, n_q=n_q, D=D, group=group)
+    for t, h, ref, ref_lse, _ in rows64:
+        err = np.abs(o[t, h].double().cpu().numpy() - ref)
+        assert np.all(err <= (2.0 ** -13 + 2.0 ** -17) * ref), (err / ref).max()
+        assert abs(lse[t, h].item() - ref_lse) <= 2.0 ** -20 * (1 + abs(ref_lse))
+
+
+@pytest.mark.parametrize("dtype,rows,n_q,R,D,qs", [("bf16", 8, 1, 3000, 128, 3.0), ("bf16", 16, 1, 3000, 64, 1.0),
+                                                   ("f32", 8, 1, 3000, 128, 3.0), ("f32", 4, 500, 6, 64, 1.0),
+                                                   ("bf16", 4, 300, 30, 128, 3.0), ("bf16", 4, 16, 310, 128, 1.0),
+                                                   ("bf16", 4, 300, 30, 64, 1.0), ("bf16", 4, 16, 310, 64, 3.0)])
+def test_attn_spans_with_maxima_of_their_own(dtype, rows, n_q, R, D, qs):
+    """Scores that differ, so that every span has its own maximum.  As at the head of this file, and
+    what the spans may lose (2^-13 at most, float32 2^-17; of the probabilities' sum 2^-17)."""
+    o, lse, rows64 = _long_run(dtype, rows, 60017, R, n_q=n_q, D=D, qs=qs)
+    tol = 2.0 ** -16 if dtype == "f32" else 2.0 ** -8 + 2.0 ** -13 + 2.0 ** -16
+    for t, h, ref, ref_lse, ds in rows64:
+        err = np.abs(o[t, h].double().cpu().numpy() - ref)
+        assert np.all(err <= (2 * ds + tol) * ref), (err / ref).max()
+        assert abs(lse[t, h].item() - ref_lse) <= ds + 2.0 ** -17 + 2.0 ** -20 * (1 + abs(ref_lse))
 
 
 # ---------------------------------------------------------------------------
