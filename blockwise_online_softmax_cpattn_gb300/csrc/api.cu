@@ -11,10 +11,11 @@
 #include "api_internal.h"
 #include "kernels.h"
 
-// Device status word (one per device that loads the library): the first error a
-// kernel detects (a bounded wait that ran out) is latched here; cpattn_check
-// reads and clears it.
-static __device__ int g_cpattn_status;
+// Device status (per device that loads the library): the first error a kernel detects (a
+// bounded wait that ran out) is latched in the first word, a value that the cache cannot hold in
+// the second, so that what is said of the data never hides a fault; cpattn_check reads and
+// clears them.
+static __device__ int g_cpattn_status[2];
 
 namespace cpattn {
 
@@ -34,6 +35,11 @@ int* status_ptr() {
     g_status_ptr[dev] = static_cast<int*>(p);
   }
   return g_status_ptr[dev];
+}
+
+int* range_ptr() {
+  int* const p = status_ptr();
+  return p ? p + 1 : nullptr;
 }
 
 // ---------------------------------------------------------------------------
@@ -545,16 +551,16 @@ cpattn_status cpattn_layout(int permute, const cpattn_desc* desc, const void* sr
 
 cpattn_status cpattn_check(void* stream) {
   if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return CPATTN_ERR_CUDA;
-  int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_cpattn_status, sizeof(int)) != cudaSuccess)
-    return CPATTN_ERR_CUDA;
-  if (v != 0) {
-    int zero = 0;
-    if (cudaMemcpyToSymbol(g_cpattn_status, &zero, sizeof(int)) != cudaSuccess)
+  int v[2] = {0, 0};
+  if (cudaMemcpyFromSymbol(v, g_cpattn_status, sizeof(v)) != cudaSuccess) return CPATTN_ERR_CUDA;
+  const int word = v[0] != 0 ? 0 : 1;  // a range report stays until no fault is left to tell
+  if (v[word] != 0) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_cpattn_status, &zero, sizeof(int), word * sizeof(int)) != cudaSuccess)
       return CPATTN_ERR_CUDA;
   }
   if (cudaGetLastError() != cudaSuccess) return CPATTN_ERR_CUDA;
-  return v == 0 ? CPATTN_OK : (cpattn_status)v;
+  return (cpattn_status)v[word];
 }
 
 const char* cpattn_status_string(cpattn_status status) {

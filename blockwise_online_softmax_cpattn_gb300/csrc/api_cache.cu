@@ -121,7 +121,7 @@ cpattn_status cpattn_cache_append(const cpattn_cache_desc* desc, int n_tokens, c
     return CPATTN_ERR_INVALID_ARG;
   cudaGetLastError();
   return from_cuda(launch_cache_append(c, n_tokens, k, {k_token_stride, k_head_stride}, v,
-                                       {v_token_stride, v_head_stride}, slots, cache, status_ptr(),
+                                       {v_token_stride, v_head_stride}, slots, cache, range_ptr(),
                                        (cudaStream_t)stream));
 }
 

@@ -10,6 +10,8 @@ namespace cpattn {
 
 // The current device's status word (null when it cannot be found).
 int* status_ptr();
+// The word beside it for values that the cache cannot hold.
+int* range_ptr();
 
 inline bool aligned16(const void* p) { return p && ((uintptr_t)p % 16 == 0); }
 

@@ -15,7 +15,7 @@
 namespace cpattn {
 
 constexpr int kCacheTile = 16;            // tokens per tile (the K dimension of one MMA)
-constexpr int kStatusRange = 6;           // device status: a value the cache cannot hold
+constexpr int kStatusRange = 6;           // device range word: a value the cache cannot hold
 constexpr float kCacheHuge = 0x1p120f;    // stored values are held within +- this
 constexpr float kCacheTiny = 0x1p-100f;   // a group whose a is below this has a = 0
 
@@ -126,7 +126,7 @@ struct RowStrides {
   int64_t token, head;  // elements
 };
 cudaError_t launch_cache_append(const Cache& c, int n, const void* k, RowStrides ks, const void* v,
-                                RowStrides vs, const int* slots, void* cache, int* status,
+                                RowStrides vs, const int* slots, void* cache, int* range,
                                 cudaStream_t st);
 cudaError_t launch_cache_read(const Cache& c, int n, const int* slots, const void* cache, void* k,
                               RowStrides ks, void* v, RowStrides vs, cudaStream_t st);

@@ -70,7 +70,7 @@ struct Raw<float> {
 // border j itself, whose product is exact in float32 (8 + 6 bits), so the code is exact.
 // The four codes of a half word are summed as float32 numbers: below 2^16, so exactly.
 template <int LANES>
-__device__ __forceinline__ uint2 quantise16(float2 (&x)[8], uint32_t& az, int* status) {
+__device__ __forceinline__ uint2 quantise16(float2 (&x)[8], uint32_t& az, int* range) {
   float lo = min_nan(x[0].x, x[0].y), hi = max_nan(x[0].x, x[0].y);
 #pragma unroll
   for (int i = 1; i < 8; ++i) {
@@ -78,7 +78,7 @@ __device__ __forceinline__ uint2 quantise16(float2 (&x)[8], uint32_t& az, int* s
     hi = max3_nan(hi, x[i].x, x[i].y);
   }
   if (!(lo >= -kCacheHuge && hi <= kCacheHuge)) {  // also true of a NaN
-    latch_status(status, kStatusRange);
+    latch_status(range, kStatusRange);
     lo = INFINITY;
     hi = -INFINITY;
 #pragma unroll
@@ -152,7 +152,7 @@ struct Rows {
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kThreads)
     append_kernel(const Rows<D, G> c, int n, const T* k, RowStrides ks, const T* v, RowStrides vs,
-                  const int* slots, uint8_t* cache, int* status) {
+                  const int* slots, uint8_t* cache, int* range) {
   constexpr int TPR = D / 16, LANES = G / 16, STEP = kThreads / TPR, N = kRows<T>;
   const int w = threadIdx.x % TPR;
   const int is_v = blockIdx.y >= (unsigned)c.heads;
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads)
     float2 x[8];
     raw[i].floats(x);
     uint32_t az;
-    uint2 word = quantise16<LANES>(x, az, status);  // whole warps: shuffles inside
+    uint2 word = quantise16<LANES>(x, az, range);  // whole warps: shuffles inside
     if (slot[i] < 0) continue;
     int r;
     uint8_t* half = cache + c.first(h, is_v) + c.half(slot[i], is_v, r);
@@ -272,7 +272,7 @@ static dim3 grid_of(const Cache& c, int n, int rows, int channels) {
 }  // namespace rows
 
 cudaError_t launch_cache_append(const Cache& c, int n, const void* k, RowStrides ks, const void* v,
-                                RowStrides vs, const int* slots, void* cache, int* status,
+                                RowStrides vs, const int* slots, void* cache, int* range,
                                 cudaStream_t st) {
   timing_begin("cache_append", st);
   const cudaError_t e = rows::dispatch(c, [&](auto t, auto d, auto g) {
@@ -280,7 +280,7 @@ cudaError_t launch_cache_append(const Cache& c, int n, const void* k, RowStrides
     rows::append_kernel<T, decltype(d)::value, decltype(g)::value>
         <<<rows::grid_of(c, n, rows::kRows<T>, 16), rows::kThreads, 0, st>>>(
             rows::Rows<decltype(d)::value, decltype(g)::value>::of(c), n, static_cast<const T*>(k), ks,
-            static_cast<const T*>(v), vs, slots, static_cast<uint8_t*>(cache), status);
+            static_cast<const T*>(v), vs, slots, static_cast<uint8_t*>(cache), range);
     return cudaGetLastError();
   });
   timing_end(st);

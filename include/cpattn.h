@@ -495,7 +495,8 @@ cpattn_status cpattn_cache_plan(const cpattn_cache_desc* desc, int n_req, int ma
  *           one call must differ: where two are the same, what that slot holds
  *           afterwards is unspecified.  No other slot changes.
  * The cache holds finite values only: a NaN is stored as 0 and a value beyond
- * +-2^120 as that, and cpattn_check then reports CPATTN_ERR_RANGE.
+ * +-2^120 as that, and cpattn_check then reports CPATTN_ERR_RANGE (behind an error of another
+ * kernel, if there was one).
  */
 cpattn_status cpattn_cache_append(const cpattn_cache_desc* desc, int n_tokens, const void* k,
                                   int64_t k_token_stride, int64_t k_head_stride, const void* v,
@@ -549,8 +550,9 @@ cpattn_status cpattn_cache_attn(const cpattn_cache_desc* desc, int n_req, int ma
  * Synchronises `stream`, then reads and clears the device status word of the
  * current device.  Returns the first device error since the last check
  * (CPATTN_ERR_TIMEOUT: a kernel's bounded wait ran out; CPATTN_ERR_BOUNDS: a
- * bounds check of a CPATTN_DEBUG build failed; CPATTN_ERR_RANGE: see
- * cpattn_cache_append), CPATTN_ERR_CUDA on a CUDA error, else CPATTN_OK.
+ * bounds check of a CPATTN_DEBUG build failed), CPATTN_ERR_CUDA on a CUDA error;
+ * without one CPATTN_ERR_RANGE (see cpattn_cache_append), which is kept apart, so that it
+ * hides no error and waits behind one for the next check; else CPATTN_OK.
  */
 cpattn_status cpattn_check(void* stream);
 

@@ -788,6 +788,25 @@ def test_attn_timeout_is_reported_and_context_survives(hook, dtype, n_q, kv):
     c.check()
 
 
+@pytest.mark.parametrize("nan_first", [True, False])
+def test_a_value_out_of_range_hides_no_timeout(nan_first):
+    """A NaN appended before (or after) a wait that runs out: both are reported, the fault first."""
+    c = Case(cp_mod(), H_q=4, H_kv=1, n_q=[1], kv_len=[700])
+    k = torch.full((1, 1, 128), float("nan"), dtype=torch.bfloat16, device=dev())
+    last = i32([c.d.n_pages * c.d.page - 1])
+    append = lambda: c.cp.check(c.cp.cpattn_cache_append(c.d, 1, k, k, last, c.dev[3].clone()))  # noqa: E731
+    if nan_first:
+        append()
+    c.d.debug_fault = 1
+    c.cp.check(c.run())
+    c.d.debug_fault = 0
+    if not nan_first:
+        append()
+    assert [c.cp.cpattn_check() for _ in range(3)] == [c.cp.ERR_TIMEOUT, c.cp.ERR_RANGE, c.cp.OK]
+    append()
+    assert [c.cp.cpattn_check() for _ in range(2)] == [c.cp.ERR_RANGE, c.cp.OK]
+
+
 @pytest.mark.parametrize("dtype,n_q,kv,D", [("bf16", [1, 2], [100, 3001], 128), ("bf16", [4, 5], [77, 2000], 64),
                                             ("bf16", [130, 61], [400, 1500], 128), ("f32", [1, 3], [900, 50], 64)])
 def test_calls_stay_in_their_buffers(dtype, n_q, kv, D):
