@@ -39,3 +39,18 @@ def read_golden(name):
 @pytest.fixture
 def rng():
     return np.random.default_rng(1234)
+
+
+@pytest.fixture(autouse=True)
+def one_thread_of_torch(request):
+    """Tests without a GPU compare with torch in float64 to 1e-13 and closer.  On several threads the
+    first torch.logsumexp of a process was off by 1e-9 in 3 of 50 runs (the oracle, and torch on
+    one thread, agree with 80-bit sums to 1e-15 in all)."""
+    if request.node.get_closest_marker("gpu"):
+        yield
+        return
+    import torch
+    n = torch.get_num_threads()
+    torch.set_num_threads(1)
+    yield
+    torch.set_num_threads(n)
