@@ -336,18 +336,24 @@ def _find_device() -> int:
 _here = _find_device  # () -> the current device, whose memory tensors have to be in
 
 
-def _typed(x, n, dtype, what) -> Optional[int]:
-    """Pointer of a contiguous tensor of the type with at least n numbers."""
+def _on(x, here, what):
+    if x.get_device() != here:
+        raise ValueError(f"{what} is not on the current device")
+
+
+def _typed(x, n, dtype, here, what) -> Optional[int]:
+    """Pointer of a contiguous tensor of the type with at least n numbers, on device `here`."""
     if x is None or type(x) is int:
         return x
     # (the table is looked into directly, and its type asked for only when that fails: these
     # checks are a good part of what a call of a few microseconds costs)
     if x.dtype is not (_dtypes.get(dtype) or _dtype(dtype)) or x.numel() < n or not x.is_contiguous():
         raise ValueError(f"{what} must be contiguous {_dtype(dtype)} with at least {n} entries")
+    _on(x, here, what)
     return x.data_ptr()
 
 
-def _rows(x, n, heads, desc, what):
+def _rows(x, n, heads, desc, here, what):
     """(pointer, token stride, head stride) of a [n, heads, D] tensor of desc.dtype with
     contiguous channels; a raw pointer stands for a contiguous one."""
     D = desc.D
@@ -358,23 +364,17 @@ def _rows(x, n, heads, desc, what):
             shape[2] != D or stride[2] != 1):
         raise ValueError(f"{what} must be [n_tokens, heads, D] of the descriptor's dtype with "
                          "contiguous channels")
+    _on(x, here, what)
     return x.data_ptr(), stride[0], stride[1]
 
 
-def _own(x, what):
-    """x, on the current device.  One tensor a call is asked (the block table or the cache, which
-    the others go with): asking each took 3 us of a call of 8."""
-    if x is not None and type(x) is not int and x.get_device() != _here():
-        raise ValueError(f"{what} is not on the current device")
-    return x
-
-
-def _cache(x, desc) -> Optional[int]:
+def _bytes(x, n, here, what) -> Optional[int]:
+    """Pointer of a contiguous tensor of any type with at least n bytes, on device `here`."""
     if x is None or type(x) is int:
         return x
-    _own(x, "the cache")
-    if x.numel() * x.element_size() < cpattn_cache_bytes(desc) or not x.is_contiguous():
-        raise ValueError("the cache must be contiguous and hold cpattn_cache_bytes(desc) bytes")
+    if x.numel() * x.element_size() < n or not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous and hold {n} bytes")
+    _on(x, here, what)
     return x.data_ptr()
 
 
@@ -382,27 +382,32 @@ def cpattn_cache_plan(desc, n_req, max_pages, len_old, len_new, table, free_list
                       len_out, q_start, slots, n_slots, workspace, ws_bytes=None, stream=None) -> int:
     """Pages for requests that go from len_old to len_new tokens; block table, query
     offsets and the slot of every new token."""
+    here = _here()
     return _lib.cpattn_cache_plan(
-        ctypes.byref(desc), n_req, max_pages, _typed(len_old, n_req, "i32", "len_old"),
-        _typed(len_new, n_req, "i32", "len_new"), _typed(_own(table, "table"), n_req * max_pages, "i32", "table"),
-        _typed(free_list, desc.n_pages, "i32", "free_list"), _typed(n_free, 1, "i32", "n_free"),
-        _typed(n_free_out, 1, "i32", "n_free_out"), _typed(len_out, n_req, "i32", "len_out"),
-        _typed(q_start, n_req + 1, "i32", "q_start"), _typed(slots, n_slots, "i32", "slots"), n_slots, _ptr(workspace),
-        _ws_bytes(workspace, ws_bytes), _stream(stream))
+        ctypes.byref(desc), n_req, max_pages, _typed(len_old, n_req, "i32", here, "len_old"),
+        _typed(len_new, n_req, "i32", here, "len_new"), _typed(table, n_req * max_pages, "i32", here, "table"),
+        _typed(free_list, desc.n_pages, "i32", here, "free_list"), _typed(n_free, 1, "i32", here, "n_free"),
+        _typed(n_free_out, 1, "i32", here, "n_free_out"), _typed(len_out, n_req, "i32", here, "len_out"),
+        _typed(q_start, n_req + 1, "i32", here, "q_start"), _typed(slots, n_slots, "i32", here, "slots"), n_slots,
+        _bytes(workspace, 0, here, "workspace"), _ws_bytes(workspace, ws_bytes), _stream(stream))
 
 
 def cpattn_cache_append(desc, n_tokens, k, v, slots, cache, stream=None) -> int:
     """Quantises the rows of k and v ([n_tokens, H_kv, D], strided) into their slots."""
-    return _lib.cpattn_cache_append(ctypes.byref(desc), n_tokens, *_rows(k, n_tokens, desc.H_kv, desc, "k"),
-                                    *_rows(v, n_tokens, desc.H_kv, desc, "v"),
-                                    _typed(slots, n_tokens, "i32", "slots"), _cache(cache, desc), _stream(stream))
+    here = _here()
+    return _lib.cpattn_cache_append(ctypes.byref(desc), n_tokens, *_rows(k, n_tokens, desc.H_kv, desc, here, "k"),
+                                    *_rows(v, n_tokens, desc.H_kv, desc, here, "v"),
+                                    _typed(slots, n_tokens, "i32", here, "slots"),
+                                    _bytes(cache, cpattn_cache_bytes(desc), here, "cache"), _stream(stream))
 
 
 def cpattn_cache_read(desc, n_tokens, slots, cache, k, v, stream=None) -> int:
     """The rows of the slots as keys and values ([n_tokens, H_kv, D], strided)."""
-    return _lib.cpattn_cache_read(ctypes.byref(desc), n_tokens, _typed(slots, n_tokens, "i32", "slots"),
-                                  _cache(cache, desc), *_rows(k, n_tokens, desc.H_kv, desc, "k"),
-                                  *_rows(v, n_tokens, desc.H_kv, desc, "v"), _stream(stream))
+    here = _here()
+    return _lib.cpattn_cache_read(ctypes.byref(desc), n_tokens, _typed(slots, n_tokens, "i32", here, "slots"),
+                                  _bytes(cache, cpattn_cache_bytes(desc), here, "cache"),
+                                  *_rows(k, n_tokens, desc.H_kv, desc, here, "k"),
+                                  *_rows(v, n_tokens, desc.H_kv, desc, here, "v"), _stream(stream))
 
 
 def cpattn_cache_attn_workspace(desc) -> int:
@@ -413,12 +418,14 @@ def cpattn_cache_attn(desc, n_req, max_pages, n_tokens, max_q, q, q_start, kv_le
                       workspace, ws_bytes=None, stream=None) -> int:
     """Attention of the new tokens q ([n_tokens, H_q, D], strided) over the cache; lse may
     be None."""
+    here = _here()
     return _lib.cpattn_cache_attn(
-        ctypes.byref(desc), n_req, max_pages, n_tokens, max_q, *_rows(q, n_tokens, desc.H_q, desc, "q"),
-        _typed(q_start, n_req + 1, "i32", "q_start"), _typed(kv_len, n_req, "i32", "kv_len"),
-        _typed(table, n_req * max_pages, "i32", "table"), _cache(cache, desc),
-        _typed(o, n_tokens * desc.H_q * desc.D, desc.o_dtype, "o"),
-        _typed(lse, n_tokens * desc.H_q, F32, "lse"), _ptr(workspace),
+        ctypes.byref(desc), n_req, max_pages, n_tokens, max_q, *_rows(q, n_tokens, desc.H_q, desc, here, "q"),
+        _typed(q_start, n_req + 1, "i32", here, "q_start"), _typed(kv_len, n_req, "i32", here, "kv_len"),
+        _typed(table, n_req * max_pages, "i32", here, "table"),
+        _bytes(cache, cpattn_cache_bytes(desc), here, "cache"),
+        _typed(o, n_tokens * desc.H_q * desc.D, desc.o_dtype, here, "o"),
+        _typed(lse, n_tokens * desc.H_q, F32, here, "lse"), _bytes(workspace, 0, here, "workspace"),
         _ws_bytes(workspace, ws_bytes), _stream(stream))
 
 

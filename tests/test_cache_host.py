@@ -228,5 +228,24 @@ def test_binding_checks_tensors(cp):
             cp.cpattn_cache_attn(d, 4, 2, 4, 1, *args, 1 << 30, 0)
 
 
+def test_binding_checks_every_tensors_device(cp, monkeypatch):
+    """Each argument of each call as the only tensor, a CPU one where device 0 is current."""
+    import torch
+    monkeypatch.setattr(cp, "_here", lambda: 0)
+    d = _desc(cp)
+    i32 = torch.zeros(128, dtype=torch.int32)
+    k, q = (torch.zeros(4, h, 128, dtype=torch.bfloat16) for h in (2, 8))
+    cache, ws = torch.zeros(cp.cpattn_cache_bytes(d), dtype=torch.uint8), torch.zeros(1 << 20, dtype=torch.uint8)
+    calls = [(lambda a: cp.cpattn_cache_plan(d, 4, 2, *a[:9], 4, a[9], 1 << 20, 0), [i32] * 9 + [ws]),
+             (lambda a: cp.cpattn_cache_append(d, 4, *a, 0), [k, k, i32, cache]),
+             (lambda a: cp.cpattn_cache_read(d, 4, *a, 0), [i32, cache, k, k]),
+             (lambda a: cp.cpattn_cache_attn(d, 4, 2, 4, 1, *a, 1 << 30, 0),
+              [q, i32, i32, i32, cache, q, torch.zeros(4, 8), ws])]
+    for call, tensors in calls:
+        for i, t in enumerate(tensors):
+            with pytest.raises(ValueError, match="current device"):
+                call([t if j == i else FAKE for j in range(len(tensors))])
+
+
 def test_range_has_a_status_string(cp):
     assert cp.cpattn_status_string(cp.ERR_RANGE) not in ("", "unknown status")
