@@ -263,6 +263,38 @@ def test_a_page_past_32_bits(page, n_q):
     assert np.all(np.abs(lse[:, 0].double().cpu().numpy() - np.log(total)) <= sums + 2.0 ** -17)
 
 
+@pytest.mark.parametrize("n_q", [1, 60])
+def test_every_piece_of_a_page_past_32_bits_counts(n_q):
+    """Values that grow along a page of 14.4 million tokens, scores of zero: o is their mean, lse the
+    logarithm of their number.  A CTA's piece is 1/152 of the sum, 2^-7.2; the spans lose 2^-13 of it
+    at most, some 160 joins two roundings each, 2^-16.  P is 1, so its sum is exact."""
+    cp = cp_mod()
+    page, D, group = 16 * 900000, 128, 32
+    d = cp.make_cache_desc(1, 1, D, page, 1, group=group, causal=0, o_dtype="f32")
+    g = torch.Generator(device=dev())
+    g.manual_seed(7)
+    tiles = page // 16
+    c = torch.randint(0, 256, (tiles, 2, 16 * (D // 2 + 4 * (D // group))), dtype=torch.uint8, generator=g, device=dev())
+    codes = c[:, 1, : 16 * (D // 2)].view(torch.int32).reshape(tiles, 16, D // 8)
+    a = 2.0 ** (torch.arange(tiles, device=dev()) * 6 // tiles)     # 1 .. 32, a sixth of the page each
+    az = torch.zeros(tiles, 2, 16 * (D // group), 2, device=dev())
+    az[..., 0] = a[:, None, None]
+    c[:, :, 16 * (D // 2):] = az.to(torch.bfloat16).view(torch.uint8).reshape(tiles, 2, -1)
+    total = torch.zeros(D, dtype=torch.float64, device=dev())
+    for ch in range(8):   # channel 2p + e of a word in bits 4 (p + 4e)
+        x = (codes >> (4 * (ch // 2 + 4 * (ch % 2)))) & 15
+        total[ch::8] = ((16 + x).sum(1).double() * a[:, None].double()).sum(0) / 16
+    ref = (total / page).cpu().numpy()
+    q = torch.zeros(n_q, 1, D, dtype=torch.bfloat16, device=dev())
+    o, lse = torch.empty(n_q, 1, D, device=dev()), torch.empty(n_q, 1, device=dev())
+    ws = torch.empty(cp.cpattn_cache_attn_workspace(d), dtype=torch.uint8, device=dev())
+    checked(cp, cp.cpattn_cache_attn(d, 1, 1, n_q, n_q, q, i32([0, n_q]), i32([page]), i32([[0]]), c.reshape(-1), o,
+                                     lse, ws))
+    err = np.abs(o[:, 0].double().cpu().numpy() - ref)
+    assert np.all(err <= (2.0 ** -13 + 2.0 ** -16) * ref), (err / ref).max()
+    assert np.abs(lse.double().cpu().numpy() - np.log(page)).max() <= 2.0 ** -20 * (1 + np.log(page))
+
+
 # ---------------------------------------------------------------------------
 # plan
 # ---------------------------------------------------------------------------
