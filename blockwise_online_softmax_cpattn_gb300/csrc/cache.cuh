@@ -19,7 +19,8 @@ constexpr int kStatusRange = 6;           // device range word: a value the cach
 constexpr float kCacheHuge = 0x1p120f;    // stored values are held within +- this
 constexpr float kCacheTiny = 0x1p-100f;   // a group whose a is below this has a = 0
 
-// n / d for 0 <= n < 2^31 by a multiplication: with s = ceil(log2 d) and
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery's division by invariant
+// integers): with s = ceil(log2 d) and
 // m = floor(2^32 (2^s - d) / d) + 1, n / d = (hi(m n) + n) >> s.
 struct Divider {
   uint32_t d, m, s;

@@ -32,6 +32,11 @@
 // float32 (NS = 3): q and P are sums of three bf16 numbers, the cached values are bf16
 // numbers anyway, so three MMAs give products of float32 quality.
 //
+//   Roundings.  In bf16 P becomes bf16, half a step 2^-9 of each term, because the MMA takes no
+//   wider operand, as in the library's other tensor-core kernels; l sums P before that.  All else
+//   is kept in float32 up to the result; exponentials are the GPU's base-2 one, scores meet
+//   scale log2 e in one multiplication.
+//
 //   Sums.  An MMA cuts its sum off where a float32 addition rounds: up to 2^-23 of the sum so
 //   far is lost a step, always downwards, which grows with the tokens that one warp walks (o
 //   6e-5 too small after 20000 tokens, 6e-3 after a million).  So O, m and l are kept a span of
@@ -842,8 +847,9 @@ struct Variant {
     return cudaLaunchKernelEx(&cfg, kern, p);
   }
 };
-// (12 warps where their registers are full, 16 else: 16 of Exact8 at D 128 spill, 33 us for 29;
-// at D 64 16 take 92 us for 96, 16 of Rows16 70 for 74)
+// (12 warps where their registers are full, 16 else.  At D 128 Exact8 and Rows16 fill the 168
+// registers of 12 warps and spill up to 20 and 120 bytes a thread; with 16 warps Exact8 spilled
+// more, 33 us for 29.  At D 64 nothing spills: 16 warps take 92 us for 96, of Rows16 70 for 74.)
 template <int D, int G>
 using Rows8 = Variant<D, G, 1, 1, 16, 1>;
 template <int D, int G>
@@ -866,7 +872,8 @@ size_t cache_attn_workspace(const Cache& c) {
 
 namespace cattn {
 // A number that no flag in a workspace holds: unlike any before it, and unlike what memory
-// holds by chance.  A captured launch keeps its number; its flags are taken away in each run.
+// holds by chance (a count through the finaliser of SplitMix64: Steele, Lea, Flood 2014).
+// A captured launch keeps its number; its flags are taken away in each run.
 static uint64_t next_nonce() {
   static std::atomic<uint64_t> count{(uint64_t)std::chrono::steady_clock::now().time_since_epoch().count()};
   uint64_t x = count.fetch_add(1) * 0x9E3779B97F4A7C15ull;
@@ -883,12 +890,14 @@ static cudaError_t launch_attn(const cattn::Params& p, int sms, cudaStream_t st)
   // 8 rows at a time while that is all a request has, else 16; past three blocks of 16, each
   // of which unpacks the codes again, the tensor memory's kernel.  32 requests of 500 to 12000
   // cached tokens, us (8 rows, 16 rows, tensor memory):
-  //   4 K/V heads of 8 query heads: 8 rows 41, 51, 98; 16 rows 64, 55, 107; 32: 108, 89, 121;
-  //     48: 152, 121, 124; 64: 196, 152, 129; 128: 371, 273, 150
-  //   8 K/V heads of 4: 8 rows 64, 82, 179; 16 rows 109, 89, 199; 32: 197, 153, 222;
-  //     48: 283, 215, 230; 64: 370, 273, 235
-  // and 64 requests of 200 to 8000, D 64, 4 K/V heads of 8 (16 rows, tensor memory): 16 rows 44,
-  // 95; 32: 69, 112; 48: 94, 111; 56: 119, 110; 128: 221, 124.
+  //   4 K/V heads of 8 query heads: 8 rows 35, 43, 82; then (16 rows, tensor memory) 16 rows 47,
+  //     94; 32: 73, 108; 48: 100, 110; 56: 122, 113; 64: 125, 114; 128: 219, 136
+  //   8 K/V heads of 4: 8 rows 54, 68, 148; 16 rows 74, 167; 32: 127, 193; 48: 176, 200;
+  //     56: 221, 201; 64: 223, 203; 128: 413, 240
+  // and 64 requests of 200 to 8000, D 64, 4 K/V heads of 8: 8 rows 33, 36, 80; 16 rows 37, 81;
+  // 32: 55, 91; 48: 74, 92; 56: 92, 92; 128: 168, 103.
+  // (One kernel a call: the requests with few rows of a call with a long one are slower than in
+  // a call of their own, 127 decoding ones beside a chunk of 2048 tokens 1534 us, apart 1034.)
   const int64_t rows = (int64_t)p.a.max_q * p.n_rep;
   if (rows <= 8) return Rows8<D, G>::launch(p, sms, st);
   if (rows <= 48) return Rows16<D, G>::launch(p, sms, st);

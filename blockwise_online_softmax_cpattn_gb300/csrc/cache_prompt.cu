@@ -23,6 +23,9 @@
 // (reading them from TMEM a second time to form P cost a third of the time).  O is rescaled
 // only when the running maximum grew by more than 2^8 (exact after the division).
 //
+// Roundings: P becomes bf16, half a step 2^-9 of each term, because the MMA takes no wider operand;
+// l sums it before that; all else is float32 up to the result.
+//
 // TMEM (512 columns): S_a [0,128), S_b [128,256), O_a, O_b D columns each from 256; P of a
 // side takes the first 64 columns of its S.
 // Every wait is bounded; on a time-out the CTA's roles give up, its copies and MMAs are
@@ -30,11 +33,12 @@
 //
 // Measured (2048 new tokens behind 30000, 32 query heads, 8 K/V heads, D 128, group 64): 844 us,
 // 1233 TFLOP/s (without the spans below 830), the tensor pipe 54 % busy.
-// Bound by shared memory, which feeds the tensor cores and takes the unpacked codes: of 3800
-// clocks that a tile takes, the MMAs' operands need 1540 at its 128 bytes a clock (QK reads both
-// from there, 1024), unpacking 640 to write and read codes, and both come in bursts; and by a
+// No unit is full: of the 3800 clocks that a tile takes, the tensor pipe works 54 %, and shared
+// memory some 57 % by count (the MMAs' operands 1540 at its 128 bytes a clock, of which QK, that
+// reads both from there, 1024; unpacking 640 to write and read codes).  What is left is latency: a
 // side's chain from one tile's scores to the next's (128 scores a thread, a maximum, 128
 // exponentials, P out, PV and the next QK), which the other side fills only in part.
+// D 64: the same chunk with 32 and 8 heads 682 us, 763 TFLOP/s (half the products a score).
 // Tried and slower: one warp that issues for both sides, or QK and PV apart; scores in halves
 // of 64 tokens, the next half's formed under a half's softmax (939 us: queries are read twice
 // as often); masks through TMEM; eight warps that unpack where 64 rows leave softmax warps over

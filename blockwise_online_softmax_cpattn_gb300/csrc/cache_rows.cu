@@ -8,9 +8,10 @@
 // Bound by HBM: 2 (or 4) bytes in and 0.56 out a channel at group 64, and the other way
 // round; close behind, appending, by its instructions, so pairs of channels go through the
 // two-lane float32 operations.
-// Measured (32768 tokens of 8 heads, D 128, group 64, bf16; 172 MB each): append 38 us, 4.5
-// TB/s, 3.0 instructions a clock issue, 15 a value; read 33 us, 5.2 TB/s.  float32, 5003
-// tokens of 12 heads of 64, group 32: 19 us for both.
+// Measured (32768 tokens of 8 heads, D 128, group 64, bf16; 172 MB each): append 39 us, 4.4
+// TB/s, 3.0 instructions a clock issue, 15 a value; read 33 us, 5.2 TB/s.  The same in float32
+// (306 MB each): append 51 us, 6.0 TB/s, read 51.  float32, 5003 tokens of 12 heads of 64, group
+// 32: append 10, read 9.
 #include "cache.cuh"
 
 namespace cpattn {

@@ -321,7 +321,7 @@ __device__ __forceinline__ It item_at(const Params& p, const int64_t* sums, int6
 }
 
 // ---------------------------------------------------------------------------
-// items that cross CTAs (behind a grid barrier)
+// items that cross CTAs (in a launch of its own, behind the one that left the pieces)
 // ---------------------------------------------------------------------------
 // An item's CTAs are the one that began it (its tail piece) and those behind it up to the one
 // that ends it (their head pieces); each joins a part of the item's numbers.  slots: a head

@@ -524,7 +524,10 @@ size_t cpattn_cache_attn_workspace(const cpattn_cache_desc* desc);
  *   max_pages : row length of table
  *   n_tokens  : rows of q, o and lse
  *   max_q     : the largest number of new tokens of one request.  It only chooses the
- *               kernel: the results hold for any q_start.
+ *               kernel: the results hold for any q_start.  One kernel serves the whole call,
+ *               so a batch that mixes chunks of prompts with decoding requests is faster in
+ *               two calls (1.5 to 2 times): with q_start, kv_len and table from a later
+ *               request on, a call computes the rows of its n_req requests alone.
  *   q_start   : [n_req + 1], non-decreasing: request r's new tokens are rows q_start[r]
  *               .. q_start[r + 1] - 1.  Rows behind q_start[n_req] are left as they are.
  *   kv_len    : [n_req] cached tokens, the new ones included

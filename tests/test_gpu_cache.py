@@ -565,6 +565,23 @@ def test_attn_max_q_only_chooses_the_kernel(max_q):
     Case(cp_mod(), n_q=[1, 30, 2], kv_len=[40, 500, 90], page=16).check(max_q=max_q)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attn_a_mixed_batch_in_two_calls(dtype):
+    """Decoding requests and, from a later request on, chunks of prompts: rows that the other call
+    computes are left as they are."""
+    c = Case(cp_mod(), n_q=[1, 1, 2, 1, 150, 77], kv_len=[300, 5, 64, 1100, 400, 77], dtype=dtype)
+    start, lens, table = c.dev[:3]
+    cols, n = c.table.shape[1], c.qd.shape[0]
+    call = lambda a, b, max_q: checked(c.cp, c.cp.cpattn_cache_attn(  # noqa: E731
+        c.d, b - a, cols, n, max_q, c.qd, start[a:], lens[a:], table[a:], c.dev[3], c.o, c.lse, c.ws))
+    call(0, 4, 2)
+    assert (c.o[5:] == 77.0).all() and (c.lse[5:] == 77.0).all()
+    first = c.o[:5].clone()
+    call(4, 6, 150)
+    assert torch.equal(c.o[:5], first)
+    c.compare()
+
+
 @pytest.mark.parametrize("n_q", [1, 150])
 def test_attn_pages_outside_the_cache_hold_no_key(n_q):
     """Entries that are no pages, among them all of a request's, and a hole in the middle."""
