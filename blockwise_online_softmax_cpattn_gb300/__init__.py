@@ -34,6 +34,7 @@ ERR_RANGE = 6
 F32, BF16 = 0, 1
 CONTIGUOUS, ZIGZAG = 0, 1
 ZIGZAG_FWD, ZIGZAG_INV, A2A_FWD, A2A_INV = 0, 1, 2, 3
+HALVES, NEIGHBOURS = 0, 1
 
 
 class CpattnDesc(ctypes.Structure):
@@ -49,6 +50,14 @@ class CpattnCacheDesc(ctypes.Structure):
                 ("group", ctypes.c_int32), ("page", ctypes.c_int32), ("n_pages", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("o_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("causal", ctypes.c_int32), ("debug_fault", ctypes.c_int32)]
+
+
+class CpattnRotateDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+                ("T", ctypes.c_int32), ("D", ctypes.c_int32), ("cp", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("dtype", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("natural_in", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class CpattnError(RuntimeError):
@@ -76,11 +85,22 @@ def make_cache_desc(H_q, H_kv, D, page, n_pages, group=64, dtype="bf16", o_dtype
     return CpattnCacheDesc(H_q, H_kv, D, group, page, n_pages, dt, odt, scale, causal, debug_fault)
 
 
+def make_rotate_desc(B, H_q, H_kv, T, D, cp=1, layout="contiguous", dtype="bf16", rot=None,
+                     pairing="halves", norm=1, natural_in=0, eps=1e-6) -> CpattnRotateDesc:
+    """Descriptor of norm and rotation before attention; rot defaults to D."""
+    lay = {"contiguous": CONTIGUOUS, "zigzag": ZIGZAG}.get(layout, layout)
+    dt = {"f32": F32, "bf16": BF16}.get(dtype, dtype)
+    pair = {"halves": HALVES, "neighbours": NEIGHBOURS}.get(pairing, pairing)
+    return CpattnRotateDesc(B, H_q, H_kv, T, D, cp, lay, dt, D if rot is None else rot, pair,
+                            int(norm), int(natural_in), eps)
+
+
 _vp = ctypes.c_void_p
 _st = ctypes.c_int
 _i = ctypes.c_int
 _i64 = ctypes.c_int64
 _cdesc = ctypes.POINTER(CpattnCacheDesc)
+_rdesc = ctypes.POINTER(CpattnRotateDesc)
 _sigs = {
     "cpattn_partial_fwd": (_st, [ctypes.POINTER(CpattnDesc), ctypes.c_int, ctypes.c_int, _vp, _vp,
                                  _vp, _vp, _vp, _vp]),
@@ -124,6 +144,15 @@ _sigs = {
     "cpattn_cache_attn_workspace": (ctypes.c_size_t, [_cdesc]),
     "cpattn_cache_attn": (_st, [_cdesc, _i, _i, _i, _i, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
                                 _vp, ctypes.c_size_t, _vp]),
+    "cpattn_rotate_fwd": (_st, [_rdesc] + [_vp] * 6 + [_vp] * 4 + [_vp] * 6 + [_vp]),
+    "cpattn_rotate_bwd_workspace": (ctypes.c_size_t, [_rdesc]),
+    "cpattn_rotate_bwd": (_st, [_rdesc] + [_vp] * 4 + [_vp] * 4 + [_vp] * 12 + [_vp] * 3 +
+                          [ctypes.c_size_t, _vp]),
+    "cpattn_linear_workspace": (ctypes.c_size_t, [ctypes.POINTER(CpattnDesc)]),
+    "cpattn_linear_fwd": (_st, [ctypes.POINTER(CpattnDesc)] + [_vp] * 9 + [ctypes.c_size_t, _vp]),
+    "cpattn_linear_bwd_workspace": (ctypes.c_size_t, [ctypes.POINTER(CpattnDesc)]),
+    "cpattn_linear_bwd": (_st, [ctypes.POINTER(CpattnDesc)] + [_vp] * 12 + [ctypes.c_size_t, _vp]),
+    "cpattn_linear_step": (_st, [ctypes.POINTER(CpattnDesc), _i] + [_vp, _i64, _i64] * 3 + [_vp] * 6),
     "cpattn_check": (_st, [_vp]),
     "cpattn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "cpattn_timing_enable": (_st, [ctypes.c_int]),
@@ -313,13 +342,14 @@ def cpattn_cache_plan_workspace(desc, n_req) -> int:
     return _lib.cpattn_cache_plan_workspace(ctypes.byref(desc), n_req)
 
 
-_dtypes = {}  # F32, BF16, "i32" -> torch dtype (torch is imported with the first tensor)
+_dtypes = {}  # F32, BF16, "i32", "f64" -> torch dtype (torch is imported with the first tensor)
 
 
 def _dtype(key):
     if not _dtypes:
         import torch
-        _dtypes.update({F32: torch.float32, BF16: torch.bfloat16, "i32": torch.int32})
+        _dtypes.update({F32: torch.float32, BF16: torch.bfloat16, "i32": torch.int32,
+                        "f64": torch.float64})
     return _dtypes.get(key)
 
 
@@ -427,6 +457,112 @@ def cpattn_cache_attn(desc, n_req, max_pages, n_tokens, max_q, q, q_start, kv_le
         _typed(o, n_tokens * desc.H_q * desc.D, desc.o_dtype, here, "o"),
         _typed(lse, n_tokens * desc.H_q, F32, here, "lse"), _bytes(workspace, 0, here, "workspace"),
         _ws_bytes(workspace, ws_bytes), _stream(stream))
+
+
+_strides3 = ctypes.c_int64 * 3
+
+
+def _view(x, heads, desc, here, what):
+    """(pointer, strides) of a [B, heads, T, D] tensor of desc.dtype with contiguous channels;
+    a raw pointer stands for a contiguous one."""
+    if x is None or type(x) is int:
+        return x, None
+    shape, stride = x.shape, x.stride()
+    if (x.dtype is not _dtype(desc.dtype) or shape != (desc.B, heads, desc.T, desc.D) or
+            stride[3] != 1):
+        raise ValueError(f"{what} must be [B, heads, T, D] of the descriptor's dtype with "
+                         "contiguous channels")
+    _on(x, here, what)
+    return x.data_ptr(), _strides3(stride[0], stride[1], stride[2])
+
+
+def cpattn_rotate_fwd(desc, q, k, v, q_weight, k_weight, inv_freq, positions, q_out, k_out, v_out,
+                      stream=None) -> int:
+    """Norm of each head, rotation by position and the move into the attention's token order, of
+    [B, H, T, D] tensors by any strides; v and v_out, the weights and positions may be None."""
+    here, D = _here(), desc.D
+    return _lib.cpattn_rotate_fwd(
+        ctypes.byref(desc), *_view(q, desc.H_q, desc, here, "q"), *_view(k, desc.H_kv, desc, here, "k"),
+        *_view(v, desc.H_kv, desc, here, "v"), _typed(q_weight, D, desc.dtype, here, "q_weight"),
+        _typed(k_weight, D, desc.dtype, here, "k_weight"),
+        _typed(inv_freq, desc.rot // 2, "f64", here, "inv_freq"),
+        _typed(positions, desc.B * desc.T, "i32", here, "positions"),
+        *_view(q_out, desc.H_q, desc, here, "q_out"), *_view(k_out, desc.H_kv, desc, here, "k_out"),
+        *_view(v_out, desc.H_kv, desc, here, "v_out"), _stream(stream))
+
+
+def cpattn_rotate_bwd_workspace(desc) -> int:
+    return _lib.cpattn_rotate_bwd_workspace(ctypes.byref(desc))
+
+
+def cpattn_rotate_bwd(desc, q, k, q_weight, k_weight, inv_freq, positions, dq_out, dk_out, dv_out, dq,
+                      dk, dv, dq_weight, dk_weight, workspace, ws_bytes=None, stream=None) -> int:
+    """Gradients of cpattn_rotate_fwd's inputs and weights (float32 sums)."""
+    here, D = _here(), desc.D
+    return _lib.cpattn_rotate_bwd(
+        ctypes.byref(desc), *_view(q, desc.H_q, desc, here, "q"), *_view(k, desc.H_kv, desc, here, "k"),
+        _typed(q_weight, D, desc.dtype, here, "q_weight"), _typed(k_weight, D, desc.dtype, here, "k_weight"),
+        _typed(inv_freq, desc.rot // 2, "f64", here, "inv_freq"),
+        _typed(positions, desc.B * desc.T, "i32", here, "positions"),
+        *_view(dq_out, desc.H_q, desc, here, "dq_out"), *_view(dk_out, desc.H_kv, desc, here, "dk_out"),
+        *_view(dv_out, desc.H_kv, desc, here, "dv_out"), *_view(dq, desc.H_q, desc, here, "dq"),
+        *_view(dk, desc.H_kv, desc, here, "dk"), *_view(dv, desc.H_kv, desc, here, "dv"),
+        _typed(dq_weight, D, F32, here, "dq_weight"), _typed(dk_weight, D, F32, here, "dk_weight"),
+        _bytes(workspace, 0, here, "workspace"), _ws_bytes(workspace, ws_bytes), _stream(stream))
+
+
+def cpattn_linear_workspace(desc) -> int:
+    return _lib.cpattn_linear_workspace(ctypes.byref(desc))
+
+
+def cpattn_linear_fwd(desc, q, k, v, log_decay, lengths, state_in, o, state_out, workspace,
+                      ws_bytes=None, stream=None) -> int:
+    """Linear attention with a decay for each head; lengths, state_in and state_out may be None."""
+    here, D = _here(), desc.D
+    nq, nkv, ns = desc.B * desc.H_q * desc.T * D, desc.B * desc.H_kv * desc.T * D, desc.B * desc.H_q * D * D
+    dt = desc.dtype
+    return _lib.cpattn_linear_fwd(
+        ctypes.byref(desc), _typed(q, nq, dt, here, "q"), _typed(k, nkv, dt, here, "k"),
+        _typed(v, nkv, dt, here, "v"), _typed(log_decay, desc.H_q, F32, here, "log_decay"),
+        _typed(lengths, desc.B * desc.a2a, "i32", here, "lengths"), _typed(state_in, ns, F32, here, "state_in"),
+        _typed(o, nq, dt, here, "o"), _typed(state_out, ns, F32, here, "state_out"),
+        _bytes(workspace, 0, here, "workspace"), _ws_bytes(workspace, ws_bytes), _stream(stream))
+
+
+def cpattn_linear_bwd_workspace(desc) -> int:
+    return _lib.cpattn_linear_bwd_workspace(ctypes.byref(desc))
+
+
+def cpattn_linear_bwd(desc, q, k, v, log_decay, state_in, dO, dstate_out, dq, dk, dv, dstate_in,
+                      workspace, ws_bytes=None, stream=None) -> int:
+    """Gradients of cpattn_linear_fwd; the three states may be None."""
+    here, D = _here(), desc.D
+    nq, nkv, ns = desc.B * desc.H_q * desc.T * D, desc.B * desc.H_kv * desc.T * D, desc.B * desc.H_q * D * D
+    dt = desc.dtype
+    return _lib.cpattn_linear_bwd(
+        ctypes.byref(desc), _typed(q, nq, dt, here, "q"), _typed(k, nkv, dt, here, "k"),
+        _typed(v, nkv, dt, here, "v"), _typed(log_decay, desc.H_q, F32, here, "log_decay"),
+        _typed(state_in, ns, F32, here, "state_in"), _typed(dO, nq, dt, here, "dO"),
+        _typed(dstate_out, ns, F32, here, "dstate_out"), _typed(dq, nq, dt, here, "dq"),
+        _typed(dk, nkv, dt, here, "dk"), _typed(dv, nkv, dt, here, "dv"),
+        _typed(dstate_in, ns, F32, here, "dstate_in"), _bytes(workspace, 0, here, "workspace"),
+        _ws_bytes(workspace, ws_bytes), _stream(stream))
+
+
+def cpattn_linear_step(desc, q, k, v, log_decay, slots, state_in, state_out, o, n_states=None,
+                       stream=None) -> int:
+    """One token of each of desc.B requests ([B, H, D], strided) over its state; slots may be None.
+    n_states defaults to the length of state_in."""
+    here, D = _here(), desc.D
+    if n_states is None:
+        n_states = state_in.shape[0]
+    ns = n_states * desc.H_q * D * D
+    return _lib.cpattn_linear_step(
+        ctypes.byref(desc), n_states, *_rows(q, desc.B, desc.H_q, desc, here, "q"),
+        *_rows(k, desc.B, desc.H_kv, desc, here, "k"), *_rows(v, desc.B, desc.H_kv, desc, here, "v"),
+        _typed(log_decay, desc.H_q, F32, here, "log_decay"), _typed(slots, desc.B, "i32", here, "slots"),
+        _typed(state_in, ns, F32, here, "state_in"), _typed(state_out, ns, F32, here, "state_out"),
+        _typed(o, desc.B * desc.H_q * D, desc.dtype, here, "o"), _stream(stream))
 
 
 def cpattn_check(stream=None) -> int:

@@ -135,7 +135,7 @@ void timing_end(cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // validation
 // ---------------------------------------------------------------------------
-static cpattn_status validate(const cpattn_desc* d, Ring* R) {
+cpattn_status validate_ring(const cpattn_desc* d, Ring* R) {
   if (!d) return CPATTN_ERR_INVALID_ARG;
   if (d->B <= 0 || d->H_q <= 0 || d->H_kv <= 0 || d->T <= 0 || d->D <= 0 || d->cp <= 0 ||
       d->a2a <= 0)
@@ -177,7 +177,7 @@ cpattn_status cpattn_partial_fwd(const cpattn_desc* desc, int q_rank, int kv_ran
                                  const void* q, const void* k, const void* v, float* o_part,
                                  float* lse_part, void* stream) {
   Ring R;
-  cpattn_status s = validate(desc, &R);
+  cpattn_status s = validate_ring(desc, &R);
   if (s != CPATTN_OK) return s;
   if (q_rank < 0 || q_rank >= R.cp || kv_rank < 0 || kv_rank >= R.cp)
     return CPATTN_ERR_INVALID_ARG;
@@ -206,7 +206,7 @@ cpattn_status cpattn_merge(int64_t rows, int D, const float* o_a, const float* l
 cpattn_status cpattn_ring_fwd(const cpattn_desc* desc, const void* q, const void* k,
                               const void* v, void* o, float* lse, void* stream) {
   Ring R;
-  cpattn_status s = validate(desc, &R);
+  cpattn_status s = validate_ring(desc, &R);
   if (s != CPATTN_OK) return s;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
     return CPATTN_ERR_INVALID_ARG;
@@ -227,7 +227,7 @@ static size_t ws_section(const cpattn_desc* desc) {
 static constexpr size_t kClaimBytes = 256;
 
 size_t cpattn_ring_bwd_workspace(const cpattn_desc* desc) {
-  if (validate(desc, nullptr) != CPATTN_OK) return 0;
+  if (validate_ring(desc, nullptr) != CPATTN_OK) return 0;
   return 2 * ws_section(desc) + kClaimBytes;
 }
 
@@ -247,7 +247,7 @@ cpattn_status cpattn::ring_bwd_after_dkdv(const cpattn_desc* desc, const void* q
                                           void* workspace, size_t ws_bytes, void* stream,
                                           const AfterDkdv* after, const AfterDqPart* dq_parts) {
   Ring R;
-  cpattn_status s = validate(desc, &R);
+  cpattn_status s = validate_ring(desc, &R);
   if (s != CPATTN_OK) return s;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
       !aligned16(dO) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
@@ -295,7 +295,7 @@ static size_t packed_stats_offset(const cpattn_desc* desc) {
 }
 
 size_t cpattn_packed_workspace(const cpattn_desc* desc) {
-  if (validate(desc, nullptr) != CPATTN_OK || desc->a2a != 1) return 0;
+  if (validate_ring(desc, nullptr) != CPATTN_OK || desc->a2a != 1) return 0;
   return packed_stats_offset(desc) + cpattn_ring_bwd_workspace(desc);
 }
 
@@ -329,7 +329,7 @@ cpattn_status cpattn_ring_fwd_packed(const cpattn_desc* desc, const int32_t* sta
                                      const void* q, const void* k, const void* v, void* o,
                                      float* lse, void* workspace, size_t ws_bytes, void* stream) {
   Ring R;
-  cpattn_status s = validate(desc, &R);
+  cpattn_status s = validate_ring(desc, &R);
   if (s != CPATTN_OK) return s;
   if ((s = packed_args(desc, starts, n_docs, workspace, ws_bytes)) != CPATTN_OK) return s;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
@@ -351,7 +351,7 @@ cpattn_status cpattn_ring_bwd_packed(const cpattn_desc* desc, const int32_t* sta
                                      const float* lse, const void* dO, void* dq, void* dk,
                                      void* dv, void* workspace, size_t ws_bytes, void* stream) {
   Ring R;
-  cpattn_status s = validate(desc, &R);
+  cpattn_status s = validate_ring(desc, &R);
   if (s != CPATTN_OK) return s;
   if ((s = packed_args(desc, starts, n_docs, workspace, ws_bytes)) != CPATTN_OK) return s;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
@@ -388,7 +388,7 @@ cpattn_status cpattn_allgather_fwd(const cpattn_desc* desc, int q_rank, const vo
                                    const void* k, const void* v, void* o, float* lse,
                                    void* stream) {
   Ring R;
-  cpattn_status s = validate(desc, &R);
+  cpattn_status s = validate_ring(desc, &R);
   if (s != CPATTN_OK) return s;
   if (q_rank < 0 || q_rank >= R.cp) return CPATTN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
@@ -409,7 +409,7 @@ static size_t ag_section(const Ring& R) {
 
 size_t cpattn_allgather_bwd_workspace(const cpattn_desc* desc) {
   Ring R;
-  if (validate(desc, &R) != CPATTN_OK) return 0;
+  if (validate_ring(desc, &R) != CPATTN_OK) return 0;
   return 2 * ag_section(R) + kClaimBytes;  // Delta, LSE in base 2, the dQ item counter
 }
 
@@ -419,7 +419,7 @@ cpattn_status cpattn_allgather_bwd(const cpattn_desc* desc, int q_rank, const vo
                                    float* dv_sum, int accumulate, void* workspace,
                                    size_t ws_bytes, void* stream) {
   Ring R;
-  cpattn_status s = validate(desc, &R);
+  cpattn_status s = validate_ring(desc, &R);
   if (s != CPATTN_OK) return s;
   if (q_rank < 0 || q_rank >= R.cp || (accumulate != 0 && accumulate != 1))
     return CPATTN_ERR_INVALID_ARG;
@@ -458,7 +458,7 @@ cpattn_status cpattn_partial_bwd_stats(const cpattn_desc* desc, const void* o, c
                                        const void* dO, void* workspace, size_t ws_bytes,
                                        void* stream) {
   Ring R;
-  cpattn_status s = validate(desc, &R);
+  cpattn_status s = validate_ring(desc, &R);
   if (s != CPATTN_OK) return s;
   if (!aligned16(o) || !aligned16(lse) || !aligned16(dO) || !aligned16(workspace))
     return CPATTN_ERR_INVALID_ARG;
@@ -480,7 +480,7 @@ cpattn_status cpattn_partial_bwd(const cpattn_desc* desc, int q_rank, int kv_ran
                                  float* dq_part, float* dk_part, float* dv_part, int accumulate,
                                  void* workspace, size_t ws_bytes, void* stream) {
   Ring R;
-  cpattn_status s = validate(desc, &R);
+  cpattn_status s = validate_ring(desc, &R);
   if (s != CPATTN_OK) return s;
   if (q_rank < 0 || q_rank >= R.cp || kv_rank < 0 || kv_rank >= R.cp ||
       (accumulate != 0 && accumulate != 1))
@@ -505,7 +505,7 @@ cpattn_status cpattn_partial_bwd(const cpattn_desc* desc, int q_rank, int kv_ran
 // Checks of one tensor of a permute; fills the arguments shared by every tensor.
 static cpattn_status permute_args(int permute, const cpattn_desc* desc, const void* src,
                                   const void* dst, int n_heads, PermuteArgs* out) {
-  cpattn_status s = validate(desc, nullptr);
+  cpattn_status s = validate_ring(desc, nullptr);
   if (s != CPATTN_OK) return s;
   if (permute < CPATTN_ZIGZAG_FWD || permute > CPATTN_A2A_INV || n_heads <= 0)
     return CPATTN_ERR_INVALID_ARG;

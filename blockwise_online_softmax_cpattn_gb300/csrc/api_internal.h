@@ -13,6 +13,9 @@ int* status_ptr();
 // The word beside it for values that the cache cannot hold.
 int* range_ptr();
 
+// Checks the ring's descriptor and, with R given, folds its a2a split into the batch.
+cpattn_status validate_ring(const cpattn_desc* d, Ring* R);
+
 inline bool aligned16(const void* p) { return p && ((uintptr_t)p % 16 == 0); }
 
 inline cpattn_status from_cuda(cudaError_t e) {

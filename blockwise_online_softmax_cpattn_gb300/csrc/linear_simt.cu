@@ -1,0 +1,311 @@
+// Linear attention in float32 on the ordinary units: every type, head dimension and layout that
+// linear_tc.cu does not take (float32 tensors, other head dimensions, zigzag chunks off the
+// 128-token grid).  The sweep, its runs and its direction are described in layer.cuh.
+//
+// A block takes one run of one sweep and head in chunks of 64 tokens: scores a b^T weighted by
+// the decay into shared memory, then out = P c + r^.. (a M), then M = r^n M + b^T c, all as
+// register tiles over shared memory.  M lives in registers (8 x 8 a thread at D 128) with a copy
+// in shared memory as the operand of a M.  Head dimensions in between are padded with zeros to
+// 64 or 128.  Bound by the float32 units: 4 D (D + 32) FLOP a token and head.
+#include "layer.cuh"
+
+namespace cpattn {
+namespace linsimt {
+
+constexpr int kThreads = 256;
+constexpr int C = kLinSimtChunk;
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 r = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u),
+                     __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+}
+
+template <int DP>
+struct Smem {
+  static constexpr int kLd = DP + 4;   // row stride: eight rows meet eight bank groups
+  static constexpr int kPLd = C + 4;
+  static constexpr int kA = 0;
+  static constexpr int kB = kA + C * kLd;
+  static constexpr int kC = kB + C * kLd;
+  static constexpr int kP = kC + C * kLd;
+  static constexpr int kM = kP + C * kPLd;
+  static constexpr int kPow = kM + DP * kLd;
+  static constexpr int kFloats = kPow + C + 2;
+};
+
+template <typename E, int DP>
+__device__ __forceinline__ void load_tile(const Linear& p, const void* t, int64_t head, int pos0, int n,
+                                          float* dst) {
+  constexpr int LD = Smem<DP>::kLd, V = DP / 4;
+  const E* src = static_cast<const E*>(t) + head * p.T * p.D;
+  for (int i = threadIdx.x; i < C * V; i += kThreads) {
+    const int r = i / V, c = 4 * (i - r * V);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < n && c < p.D) x = load4(src + (int64_t)p.m.slot(pos0 + r) * p.D + c);
+    *reinterpret_cast<float4*>(dst + r * LD + c) = x;
+  }
+}
+
+template <typename E, int DP, bool SUM>
+__global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constant__ Linear p) {
+  using L = Smem<DP>;
+  constexpr int LD = L::kLd, PL = L::kPLd, R = DP / 64;  // R: 4-wide tiles of DP a thread
+  extern __shared__ __align__(16) float sm[];
+  float *const sa = sm + L::kA, *const sb = sm + L::kB, *const sc = sm + L::kC;
+  float *const sp = sm + L::kP, *const sM = sm + L::kM, *const pw = sm + L::kPow;
+  const int runs = SUM ? p.segs - 1 : p.segs;  // the last run's own sum is nobody's start
+  const int bh = blockIdx.x / runs, run = blockIdx.x - bh * runs;
+  const LinSweep& w = SUM ? p.sum[blockIdx.y] : p.sweep[blockIdx.y];
+  const int n_tok = lin_tokens(p, bh);
+  const float ld = lin_decay(p, bh);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int b = bh / p.Hq, h = bh - b * p.Hq, late = w.back;
+  const int64_t ha = (int64_t)b * (p.Hq / w.rep_a) + h / w.rep_a;
+  const int64_t hb = (int64_t)b * (p.Hq / w.rep_b) + h / w.rep_b;
+  const int64_t hc = (int64_t)b * (p.Hq / w.rep_c) + h / w.rep_c;
+  for (int i = threadIdx.x; i <= C + 1; i += kThreads) pw[i] = lin_pow(ld, i);
+
+  // M of this thread: rows 4 ty + 64 i + x, columns 4 tx + 64 j + y
+  float M[R][4][R][4];
+  const int64_t DD = (int64_t)p.D * p.D;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int r = 4 * ty + 64 * i + x, c = 4 * tx + 64 * j + y;
+          float m = 0.f;
+          if (!SUM && r < p.D && c < p.D) {
+            const int64_t at = w.trans ? (int64_t)c * p.D + r : (int64_t)r * p.D + c;
+            if (w.init) m = w.init[bh * DD + at] * w.init_mul;
+            for (int s = 0; s < run; ++s)
+              m = fmaf(lin_pow(ld, lin_run_tokens<C>(p, n_tok, w.back, s)), m,
+                       w.sums[((int64_t)bh * p.segs + s) * DD + at]);
+          }
+          M[i][x][j][y] = m;
+        }
+
+  const int m1 = min((run + 1) * p.cps, p.nch);
+  for (int m = run * p.cps; m < m1; ++m) {
+    const int pos0 = lin_chunk(p.nch, w.back, m) * C;
+    const int n = lin_clamp(n_tok - pos0, C);
+    if (n == 0) break;  // a row's padding (sweeps from the front only)
+    __syncthreads();    // the last chunk's tiles have been read
+    if (!SUM) {
+      load_tile<E, DP>(p, w.a, ha, pos0, n, sa);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int j = 0; j < R; ++j)
+            *reinterpret_cast<float4*>(sM + (4 * ty + 64 * i + x) * LD + 4 * tx + 64 * j) =
+                make_float4(M[i][x][j][0], M[i][x][j][1], M[i][x][j][2], M[i][x][j][3]);
+    }
+    load_tile<E, DP>(p, w.b, hb, pos0, n, sb);
+    load_tile<E, DP>(p, w.c, hc, pos0, n, sc);
+    __syncthreads();
+    if (!SUM) {
+      float s[4][4] = {};  // rows ty + 16 i, columns tx + 16 j
+#pragma unroll 4
+      for (int d = 0; d < DP; d += 4) {
+        float4 a[4], v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = *reinterpret_cast<const float4*>(sa + (ty + 16 * i) * LD + d);
+          v[i] = *reinterpret_cast<const float4*>(sb + (tx + 16 * i) * LD + d);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s[i][j] = fmaf(a[i].w, v[j].w, fmaf(a[i].z, v[j].z, fmaf(a[i].y, v[j].y, fmaf(a[i].x, v[j].x, s[i][j]))));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = ty + 16 * i, col = tx + 16 * j;
+          const int e = w.back ? col - row : row - col;
+          sp[row * PL + col] = e >= 0 ? s[i][j] * pw[e] : 0.f;
+        }
+      __syncthreads();
+      float o[4][R][4] = {}, t[4][R][4] = {};  // rows ty + 16 i, columns 4 tx + 64 j + y
+#pragma unroll 4
+      for (int k = 0; k < C; ++k) {
+        float4 v[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) v[j] = *reinterpret_cast<const float4*>(sc + k * LD + 4 * tx + 64 * j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = sp[(ty + 16 * i) * PL + k];
+#pragma unroll
+          for (int j = 0; j < R; ++j) {
+            o[i][j][0] = fmaf(x, v[j].x, o[i][j][0]);
+            o[i][j][1] = fmaf(x, v[j].y, o[i][j][1]);
+            o[i][j][2] = fmaf(x, v[j].z, o[i][j][2]);
+            o[i][j][3] = fmaf(x, v[j].w, o[i][j][3]);
+          }
+        }
+      }
+#pragma unroll 4
+      for (int k = 0; k < DP; ++k) {
+        float4 v[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) v[j] = *reinterpret_cast<const float4*>(sM + k * LD + 4 * tx + 64 * j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = sa[(ty + 16 * i) * LD + k];
+#pragma unroll
+          for (int j = 0; j < R; ++j) {
+            t[i][j][0] = fmaf(x, v[j].x, t[i][j][0]);
+            t[i][j][1] = fmaf(x, v[j].y, t[i][j][1]);
+            t[i][j][2] = fmaf(x, v[j].z, t[i][j][2]);
+            t[i][j][3] = fmaf(x, v[j].w, t[i][j][3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = ty + 16 * i;
+        if (row >= n) continue;
+        const float ow = pw[(w.back ? n - 1 - row : row) + 1 - late];
+        const int64_t at = ((int64_t)bh * p.T + p.m.slot(pos0 + row)) * p.D;
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          const int c = 4 * tx + 64 * j;
+          if (c >= p.D) continue;
+          const float4 y = make_float4(w.mul * fmaf(ow, t[i][j][0], o[i][j][0]), w.mul * fmaf(ow, t[i][j][1], o[i][j][1]),
+                                       w.mul * fmaf(ow, t[i][j][2], o[i][j][2]), w.mul * fmaf(ow, t[i][j][3], o[i][j][3]));
+          if (w.out_f32) store4(static_cast<float*>(w.out) + at + c, y);
+          else store4(static_cast<E*>(w.out) + at + c, y);
+        }
+      }
+    }
+    const float rn = pw[n];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) M[i][x][j][y] *= rn;
+#pragma unroll 2
+    for (int k = 0; k < n; ++k) {
+      const float uw = pw[(w.back ? k : n - 1 - k) + late];
+      float v[R][4], u[R][4];
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const float4 x = *reinterpret_cast<const float4*>(sc + k * LD + 4 * tx + 64 * j);
+        v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+        const float4 y = *reinterpret_cast<const float4*>(sb + k * LD + 4 * ty + 64 * j);
+        u[j][0] = uw * y.x, u[j][1] = uw * y.y, u[j][2] = uw * y.z, u[j][3] = uw * y.w;
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) M[i][x][j][y] = fmaf(u[i][x], v[j][y], M[i][x][j][y]);
+    }
+  }
+
+  float* dst = SUM ? w.sums + ((int64_t)bh * p.segs + run) * DD
+                   : run == p.segs - 1 && w.fin ? w.fin + bh * DD : nullptr;
+  if (!dst) return;
+  const float mul = SUM ? 1.f : w.fin_mul;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const int r = 4 * ty + 64 * i + x, c = 4 * tx + 64 * j;
+        if (r < p.D && c < p.D)
+          store4(dst + (int64_t)r * p.D + c,
+                 make_float4(M[i][x][j][0] * mul, M[i][x][j][1] * mul, M[i][x][j][2] * mul, M[i][x][j][3] * mul));
+      }
+}
+
+template <typename E, int DP>
+static cudaError_t launch(const Linear& p, cudaStream_t st, const char* sums, const char* sweeps) {
+  constexpr int kBytes = Smem<DP>::kFloats * 4;
+  cudaError_t e = cudaFuncSetAttribute(sweep_kernel<E, DP, true>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(sweep_kernel<E, DP, false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e != cudaSuccess) return e;
+  const unsigned bh = (unsigned)(p.B * p.Hq);
+  if (p.segs > 1) {
+    timing_begin(sums, st);
+    sweep_kernel<E, DP, true><<<dim3(bh * (p.segs - 1), p.n_sums), kThreads, kBytes, st>>>(p);
+    e = cudaGetLastError();
+    timing_end(st);
+    if (e != cudaSuccess) return e;
+  }
+  timing_begin(sweeps, st);
+  sweep_kernel<E, DP, false><<<dim3(bh * p.segs, p.n_sweeps), kThreads, kBytes, st>>>(p);
+  e = cudaGetLastError();
+  timing_end(st);
+  return e;
+}
+
+template <typename E>
+__global__ void __launch_bounds__(256) group_kernel(int64_t n4, int n_rep, int64_t row4,
+                                                    const float4* part, E* out) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+    const int64_t g = i / row4, at = i - g * row4;
+    float4 s = __ldcs(part + g * n_rep * row4 + at);
+    for (int r = 1; r < n_rep; ++r) {
+      const float4 x = __ldcs(part + (g * n_rep + r) * row4 + at);
+      s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+    }
+    store4(out + 4 * i, s);
+  }
+}
+
+}  // namespace linsimt
+
+cudaError_t launch_linear_simt(const Linear& p, cudaStream_t st, bool backward) {
+  const char* sums = backward ? "linear_bwd_sums" : "linear_fwd_sums";
+  const char* sweeps = backward ? "linear_bwd" : "linear_fwd";
+  if (p.bf16)
+    return p.D <= 64 ? linsimt::launch<__nv_bfloat16, 64>(p, st, sums, sweeps)
+                     : linsimt::launch<__nv_bfloat16, 128>(p, st, sums, sweeps);
+  return p.D <= 64 ? linsimt::launch<float, 64>(p, st, sums, sweeps)
+                   : linsimt::launch<float, 128>(p, st, sums, sweeps);
+}
+
+cudaError_t launch_linear_group(int64_t groups, int n_rep, int64_t row_elems, const float* part,
+                                void* out, int bf16, cudaStream_t st) {
+  const int64_t n4 = groups * row_elems / 4;
+  const int64_t want = (n4 + 255) / 256, most = 16 * kSms;
+  const unsigned grid = (unsigned)(want < most ? want : most);
+  timing_begin("linear_group", st);
+  if (bf16)
+    linsimt::group_kernel<<<grid, 256, 0, st>>>(n4, n_rep, row_elems / 4,
+                                                reinterpret_cast<const float4*>(part),
+                                                static_cast<__nv_bfloat16*>(out));
+  else
+    linsimt::group_kernel<<<grid, 256, 0, st>>>(n4, n_rep, row_elems / 4,
+                                                reinterpret_cast<const float4*>(part),
+                                                static_cast<float*>(out));
+  const cudaError_t e = cudaGetLastError();
+  timing_end(st);
+  return e;
+}
+
+}  // namespace cpattn

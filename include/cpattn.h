@@ -101,7 +101,8 @@ typedef struct cpattn_desc {
                           withhold one load, so that the waits on it run out
                           (CPATTN_ERR_TIMEOUT via cpattn_check, within about 50 ms;
                           any non-zero value shortens every bounded wait of the
-                          tensor-core kernels to 50 ms). */
+                          tensor-core kernels to 50 ms).  cpattn_linear_*: any non-zero
+                          value withholds one load of each thread block. */
 } cpattn_desc;
 
 /*
@@ -548,6 +549,171 @@ cpattn_status cpattn_cache_attn(const cpattn_cache_desc* desc, int n_req, int ma
                                 const int32_t* kv_len, const int32_t* table, const void* cache,
                                 void* o, float* lse, void* workspace, size_t ws_bytes,
                                 void* stream);
+
+/*
+ * What stands between a layer's projections and its attention, in one pass: the norm of
+ * each head's queries and keys, their rotation by position, and the move into the token
+ * order that the calls above take.  The pages start at q, k and v: these calls are an
+ * addition of this library.  For a row x of D channels at position p,
+ *     n = x / sqrt(mean(x^2) + eps),   u = w * n     (norm 1; else u = x)
+ *     y = u with its first `rot` channels turned: the pair (u_a, u_b) of index i becomes
+ *         (u_a cos t - u_b sin t, u_a sin t + u_b cos t),   t = p * inv_freq[i]
+ * where pair i is channels (i, i + rot / 2) or (2 i, 2 i + 1).  Rows of values are moved
+ * as they are.  Norms and sums run in float32, angles in float64, one rounding at the end.
+ *
+ * Tensors are [B][H][T][D] by any strides: `strides` is a HOST array of three numbers, the
+ * elements from one batch row, one head and one token to the next (multiples of 16 bytes;
+ * channels are contiguous), null for a contiguous tensor.  So slices of a fused projection
+ * [B][T][(H_q + 2 H_kv) D], the ring's tensors and the cache's packed tokens
+ * [n_tokens][H][D] (B 1, T n_tokens) are passed as they are.  The rows of an output must
+ * not overlap.  An output may be its own input with the same strides where the order of
+ * the tokens stays (natural_in 0 or CPATTN_CONTIGUOUS).
+ */
+typedef enum cpattn_pairing { CPATTN_HALVES = 0, CPATTN_NEIGHBOURS = 1 } cpattn_pairing;
+
+typedef struct cpattn_rotate_desc {
+  int32_t B;          /* batch (with a2a > 1: a2a * B, heads and cp divided by a2a) */
+  int32_t H_q;        /* query heads; any number, H_kv need not divide it */
+  int32_t H_kv;       /* key/value heads */
+  int32_t T;          /* tokens per sequence */
+  int32_t D;          /* head dimension: a multiple of 8, at most 128 */
+  int32_t cp;         /* ranks of the token order */
+  int32_t layout;     /* cpattn_seq_layout of the attention's side (outputs, dY) */
+  int32_t dtype;      /* cpattn_dtype of every tensor and of the norms' weights */
+  int32_t rot;        /* rotated channels: a multiple of 8, 0 .. D */
+  int32_t pairing;    /* cpattn_pairing */
+  int32_t norm;       /* 1: RMS norm of each head; 0: rotation alone */
+  int32_t natural_in; /* 1: the projection's side (q, k, v and dq, dk, dv) has its tokens in
+                         natural order; 0: in the order of the attention's side */
+  float eps;          /* >= 0, of the norm */
+} cpattn_rotate_desc;
+
+/*
+ * Forward.
+ *   q, k           : inputs, H_q and H_kv heads
+ *   v, v_out       : moved along; both null without
+ *   q_weight, k_weight : [D] of desc->dtype, or null for ones
+ *   inv_freq       : [rot / 2] float64, 8-byte aligned; may be null when rot is 0
+ *   positions      : [B][T] int32 position of each slot of the attention's order, or null
+ *                    for the order's own (slot t of CPATTN_CONTIGUOUS is position t)
+ */
+cpattn_status cpattn_rotate_fwd(const cpattn_rotate_desc* desc, const void* q,
+                                const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                                const void* v, const int64_t* v_strides, const void* q_weight,
+                                const void* k_weight, const double* inv_freq,
+                                const int32_t* positions, void* q_out,
+                                const int64_t* q_out_strides, void* k_out,
+                                const int64_t* k_out_strides, void* v_out,
+                                const int64_t* v_out_strides, void* stream);
+
+/* Bytes of device workspace of cpattn_rotate_bwd (sums of the weights' gradients; at
+ * least 16, its contents on entry do not matter). */
+size_t cpattn_rotate_bwd_workspace(const cpattn_rotate_desc* desc);
+
+/*
+ * Backward: with g = the upstream gradient turned back,
+ *     dw = sum over rows of g * n,   dx = (w g - n mean(w g n)) / sqrt(mean(x^2) + eps).
+ *   q, k             : the forward's inputs (unused and may be null with norm 0)
+ *   dq_out, dk_out, dv_out : upstream gradients, on the attention's side
+ *   dq, dk, dv       : gradients of the inputs, on the projection's side (dv_out and dv
+ *                      null without values).  dq may be dq_out, with the same strides,
+ *                      where an output may be its own input above.
+ *   dq_weight, dk_weight : [D] float32, overwritten; null where not wanted; must be null
+ *                      with norm 0
+ * The sums run in a fixed order: repeated calls are bitwise equal.
+ */
+cpattn_status cpattn_rotate_bwd(const cpattn_rotate_desc* desc, const void* q,
+                                const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                                const void* q_weight, const void* k_weight,
+                                const double* inv_freq, const int32_t* positions,
+                                const void* dq_out, const int64_t* dq_out_strides,
+                                const void* dk_out, const int64_t* dk_out_strides,
+                                const void* dv_out, const int64_t* dv_out_strides, void* dq,
+                                const int64_t* dq_strides, void* dk, const int64_t* dk_strides,
+                                void* dv, const int64_t* dv_strides, float* dq_weight,
+                                float* dk_weight, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Linear attention with a decay for each head: causal attention without the softmax, whose
+ * keys and values sum up in one D x D state a head.  Models for long contexts mix layers of
+ * it with layers of softmax attention; it is an addition of this library.  With
+ * r = exp(log_decay[h]) in [0, 1] for query head h,
+ *     S_t = r S_(t-1) + k_t v_t^T,    o_t = scale q_t^T S_t        (t by natural position)
+ * Tensors, heads, layouts and a2a are those of cpattn_ring_fwd; the whole sequence is one
+ * call, its chunks run in the order of their positions.  Ranks on several GPUs hand the
+ * state on: state_out of one is state_in of the next.
+ *   log_decay : [H_q] float32, at most 0 (-infinity: a token sees itself only); 4-byte
+ *               aligned.  A positive value or a NaN is taken as 0.  It is a constant of the
+ *               model: no gradient is computed.
+ *   states    : [B'][H_q'][D][D] float32 (B', H_q' as for cpattn_partial_fwd), the key's
+ *               channel first.  Query heads that share a key head have their own decays, so
+ *               their own states.
+ * D is a multiple of 8.  With bf16, D 64 or 128 and (CPATTN_ZIGZAG) 2 cp chunks of a multiple
+ * of 128 tokens the products run on the tensor cores, with float32 sums: the weighted scores
+ * and the state a chunk starts from are rounded to bf16 as operands, while states kept from
+ * chunk to chunk and handed out are float32 throughout, from products of bf16 pairs that
+ * carry 16 bits.  All else runs in float32.  Inputs must be finite: in a chunk of 128 tokens
+ * an infinity or NaN reaches earlier tokens too.
+ */
+
+/* Bytes of device workspace of cpattn_linear_fwd: states of the parts into which a sequence
+ * is cut for a GPU's width (at least 16; contents on entry do not matter; calls that share
+ * it must be ordered). */
+size_t cpattn_linear_workspace(const cpattn_desc* desc);
+
+/*
+ * Forward.
+ *   lengths   : [B'] int32 tokens of each batch row, clamped to [0, T], or null for T.  Tokens
+ *               of later positions are padding: what they hold does not matter (not even a
+ *               NaN), their rows of o are left as they are, and state_out is the state behind
+ *               the row's last token (state_in, or zero, for a row of none).
+ *   state_in  : the state before the first token, or null for zero
+ *   state_out : the state behind the last, or null.  May be state_in.
+ */
+cpattn_status cpattn_linear_fwd(const cpattn_desc* desc, const void* q, const void* k,
+                                const void* v, const float* log_decay, const int32_t* lengths,
+                                const float* state_in, void* o, float* state_out, void* workspace,
+                                size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace of cpattn_linear_bwd (as above; with H_q > H_kv also float32
+ * gradients of the keys and values of each query head). */
+size_t cpattn_linear_bwd_workspace(const cpattn_desc* desc);
+
+/*
+ * Backward of cpattn_linear_fwd without lengths (behind a shorter row's end give dO = 0).
+ *   dO         : [B][H_q][T][D]
+ *   dstate_out : upstream gradient of state_out, or null for zero
+ *   dq, dk, dv : dk and dv sum over the query heads of a group
+ *   dstate_in  : gradient of state_in, or null.  Must not be state_in or dstate_out.
+ * Nothing is kept from the forward pass but its inputs.  No atomics: repeated calls are
+ * bitwise equal.
+ */
+cpattn_status cpattn_linear_bwd(const cpattn_desc* desc, const void* q, const void* k,
+                                const void* v, const float* log_decay, const float* state_in,
+                                const void* dO, const float* dstate_out, void* dq, void* dk,
+                                void* dv, float* dstate_in, void* workspace, size_t ws_bytes,
+                                void* stream);
+
+/*
+ * One token of each of desc->B requests over their states, for answering (desc->T, cp and
+ * a2a are 1):  S' = r S + k v^T,  o = scale q^T S'.
+ *   q, k, v   : [B][H][D] with strides in elements between requests and between heads, as
+ *               for cpattn_cache_append
+ *   slots     : [B] int32: request b's state is states number slots[b] of state_in and
+ *               state_out; null: number b.  A request whose slot is outside [0, n_states) is
+ *               left out: its row of o is left as it is.  Slots of one call must differ:
+ *               where two are the same, what that state and their outputs become is
+ *               unspecified.
+ *   state_in, state_out : [n_states][H_q][D][D] float32.  state_out may be state_in; states
+ *               without a request are left as they are.
+ *   o         : [B][H_q][D] of desc->dtype, contiguous
+ */
+cpattn_status cpattn_linear_step(const cpattn_desc* desc, int n_states, const void* q,
+                                 int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                                 int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                                 int64_t v_token_stride, int64_t v_head_stride,
+                                 const float* log_decay, const int32_t* slots,
+                                 const float* state_in, float* state_out, void* o, void* stream);
 
 /*
  * Synchronises `stream`, then reads and clears the device status word of the
