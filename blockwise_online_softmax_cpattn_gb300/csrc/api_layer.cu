@@ -122,7 +122,7 @@ static LinearWs linear_ws(const Ring& R, const Linear& p, bool backward) {
   return w;
 }
 
-static bool on_tensor_cores(const Ring& R) { return false && R.bf16 && linear_tc_supported(R); }
+static bool on_tensor_cores(const Ring& R) { return R.bf16 && linear_tc_supported(R); }
 
 static void plan_linear(const cpattn_desc* d, const Ring& R, bool backward, bool tc, Linear* p) {
   *p = Linear{};

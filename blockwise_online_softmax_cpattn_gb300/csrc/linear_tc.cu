@@ -1,5 +1,617 @@
+// Linear attention on the 5th-generation tensor cores (sm_103a): bf16, head dimension 64 or 128.
+// The sweep, its runs and its direction are described in layer.cuh; one block takes one run of
+// one sweep and head, in chunks of 128 tokens.  Per chunk, with w the powers of the decay:
+//
+//   S = a b^T            (SS)  P = S * w(i - j), zero where j comes after i, as bf16 into TMEM
+//   O1 = P c             (TS)
+//   O2 = a M             (SS)  M: what went before, as bf16 in shared memory
+//   out_i = mul (O1_i + w(i + 1) O2_i)
+//   U = b^T (w(n - 1 - j) c_j)   (SS, b and c both transposed by their descriptors)
+//   M = w(n) M + U
+//
+// M itself stays in float32, in the registers of one warpgroup (thread r holds row r: one
+// channel of b), and what a chunk adds to it comes from a product whose operand carries 16 bits:
+// the weighted c is split into two bf16 numbers, hi + lo, and U is the sum of two products.  A
+// single bf16 rounding there would leave 2^-9 in every state that is handed out in float32.
+// As operands of O1 and O2, P and M are rounded to bf16 once: like the output's own rounding.
+//
+// Warp roles (384 threads):
+//   warp 0       TMA producer: the tiles a, b, c of a chunk
+//   warp 1       issues S;  warp 2: O1 and O2;  warp 3: U
+//   warps 4-7    the rows of the output: S -> P, then the epilogue.  The output tile is staged
+//                in the chunk's own a tile, which nothing reads any more, and leaves by TMA
+//   warps 8-11   the state: weighted c (hi, then lo) into shared memory, M, its bf16 copy
+// Issuers are whole warps with one elected lane, as in tc_fwd.cu.  TMEM: S/P [0, 128),
+// O1, O2 and U of D columns each behind it.
+//
+// The first launch (SUM) only needs U and M: 256 threads, no a.
+//
+// Bound by memory: 1 KB a token and head at D 128 (four tiles of 32 KB a chunk, 5600 cycles of an
+// SM's share of the bandwidth) against 2600 cycles of MMAs.
+// Every mbarrier wait is bounded, as in tc_fwd.cu.
 #include "layer.cuh"
+
 namespace cpattn {
-bool linear_tc_supported(const Ring&) { return false; }
-cudaError_t launch_linear_tc(const Linear&, cudaStream_t, bool) { return cudaErrorNotSupported; }
+namespace lintc {
+
+constexpr int kTile = kLinTcChunk;
+constexpr uint64_t kTimeoutNs = 2000000000ull;     // 2 s
+constexpr uint64_t kDebugTimeoutNs = 50000000ull;  // 50 ms under the fault hook
+constexpr uint64_t kDrainTimeoutNs = 200000000ull;
+
+template <int D, bool SUM>
+struct Smem {
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kAS = SUM ? 0 : 2;                          // stages of a, b and c
+  static constexpr int kBS = SUM && D == 64 ? 4 : 2;
+  static constexpr int kCS = SUM ? (D == 64 ? 4 : 2) : D == 128 ? 1 : 2;
+  static constexpr int kXS = SUM || D == 64 ? 2 : 1;               // weighted c
+  static constexpr int kA = 0;
+  static constexpr int kB = kA + kAS * kTileBytes;
+  static constexpr int kC = kB + kBS * kTileBytes;
+  static constexpr int kX = kC + kCS * kTileBytes;
+  static constexpr int kM = kX + kXS * kTileBytes;
+  static constexpr int kPow = kM + (SUM ? 0 : D * D * 2);
+  // powers r^e at kPow + 4 (128 + e), zeros for e < 0
+  static constexpr int kBar = kPow + 4 * 264;
+  static constexpr int kNumBars = 2 * (kAS + kBS + kCS + kXS) + 7 + 3;
+  static constexpr int kMisc = kBar + 8 * kNumBars;
+  static constexpr int kBytes = kMisc + 16;
+};
+
+struct Maps {
+  CUtensorMap a, b, c, o;
+};
+struct Params {
+  Linear p;
+  Maps maps[kMaxSweeps];
+};
+
+// Wait in which every lane of the warp takes part; all lanes agree on the result.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t par, volatile int* abort,
+                                          int* status, uint64_t tmo) {
+  bool ok = mbar_wait(bar, par, abort, status, tmo);
+  return __all_sync(0xffffffffu, ok);
 }
+// Wait that ignores the abort flag (used to drain in-flight copies before exit).
+__device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t par) {
+  int never = 0;
+  return mbar_wait(bar, par, &never, nullptr, kDrainTimeoutNs);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+template <int D, bool SUM>
+__global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_constant__ Params prm) {
+  using L = Smem<D, SUM>;
+  constexpr int AS = L::kAS, BS = L::kBS, CS = L::kCS, XS = L::kXS;
+  constexpr uint32_t kTmemCols = SUM ? 128 : 512;
+  const Linear& p = prm.p;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // the layout has no alignment slack
+    if (threadIdx.x == 0) latch_status(p.status, kStatusLaunch);
+    return;
+  }
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bars = sbase + L::kBar;
+  auto a_full = [&](int s) { return bars + 8 * s; };
+  auto a_empty = [&](int s) { return bars + 8 * (AS + s); };
+  auto b_full = [&](int s) { return bars + 8 * (2 * AS + s); };
+  auto b_empty = [&](int s) { return bars + 8 * (2 * AS + BS + s); };
+  auto c_full = [&](int s) { return bars + 8 * (2 * AS + 2 * BS + s); };
+  auto c_empty = [&](int s) { return bars + 8 * (2 * AS + 2 * BS + CS + s); };
+  auto x_full = [&](int s) { return bars + 8 * (2 * AS + 2 * BS + 2 * CS + s); };
+  auto x_empty = [&](int s) { return bars + 8 * (2 * AS + 2 * BS + 2 * CS + XS + s); };
+  const uint32_t one = bars + 8 * 2 * (AS + BS + CS + XS);
+  const uint32_t c_ready = one, s_full = one + 8, p_full = one + 16, o_full = one + 24,
+                 o_free = one + 32, m_full = one + 40, u_full = one + 48, fin = one + 56;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  float* pw = reinterpret_cast<float*>(smem + L::kPow) + 128;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t tmo = p.debug_fault ? kDebugTimeoutNs : kTimeoutNs;
+
+  // ---- this block's run
+  const int runs = SUM ? p.segs - 1 : p.segs;  // the last run's own sum is nobody's start
+  const int bh = blockIdx.x / runs, run = blockIdx.x - bh * runs;
+  const LinSweep& w = SUM ? p.sum[blockIdx.y] : p.sweep[blockIdx.y];
+  const Maps& maps = prm.maps[blockIdx.y];
+  const int n_tok = lin_tokens(p, bh);
+  const float ld = lin_decay(p, bh);
+  const int back = w.back, late = back;
+  const int bb = bh / p.Hq, h = bh - bb * p.Hq;
+  const int head_a = bb * (p.Hq / w.rep_a) + h / w.rep_a;
+  const int head_b = bb * (p.Hq / w.rep_b) + h / w.rep_b;
+  const int head_c = bb * (p.Hq / w.rep_c) + h / w.rep_c;
+  const int64_t rows_q = (int64_t)p.B * p.Hq * p.T;  // (for a CPATTN_DEBUG build's checks)
+  const int m0 = run * p.cps;
+  int n_chunks = min(p.cps, p.nch - m0);
+  if (!back) n_chunks = min(n_chunks, (n_tok + kTile - 1) / kTile - m0);  // chunks of padding
+  // The i-th chunk of the run: first position and tokens.
+  auto chunk_pos = [&](int i) { return lin_chunk(p.nch, back, m0 + i) * kTile; };
+  auto chunk_n = [&](int i) { return min(n_tok - chunk_pos(i), kTile); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bars + 8 * i, 1);
+    // 128 threads of a warpgroup; a_empty: its four warps; b_empty: S and U; c_empty: O1 and
+    // the four warps that weight c
+    for (int i = 0; i < AS; ++i) mbar_init(a_empty(i), 4);
+    for (int i = 0; i < BS; ++i) mbar_init(b_empty(i), SUM ? 1 : 2);
+    for (int i = 0; i < CS; ++i) mbar_init(c_empty(i), SUM ? 4 : 5);
+    for (int i = 0; i < XS; ++i) mbar_init(x_full(i), 128);
+    mbar_init(c_ready, 128);
+    mbar_init(p_full, 128);
+    mbar_init(o_free, 128);
+    mbar_init(m_full, 128);
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < 264; i += blockDim.x) pw[i - 128] = i < 128 ? 0.f : lin_pow(ld, i - 128);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tS = tmem, tO1 = tmem + 128, tO2 = tmem + 128 + D, tU = SUM ? tmem : tmem + 128 + 2 * D;
+
+  if (warp < 4) {
+    if constexpr (!SUM) regs_ctl();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      if (lane == 0) {
+        StageRing<AS == 0 ? 1 : AS> ra;
+        StageRing<BS> rb;
+        StageRing<CS> rc;
+        bool ok = true;
+        for (int i = 0; i < n_chunks && ok; ++i) {
+          const int slot = p.m.slot(chunk_pos(i));
+          auto load = [&](auto& ring, uint32_t full, uint32_t empty, int base, const CUtensorMap* tm, int head,
+                          int heads) {
+            if (!ok || !(ok = mbar_wait(empty, ring.par ^ 1, abort, p.status, tmo))) return;
+            mbar_expect_tx(full, L::kTileBytes);
+            const int row = head * p.T + slot;
+            // (a partial chunk reads on into the next head, or zeros behind the tensor)
+            if (in_bounds(row, 1, (int64_t)heads * p.T, p.status) && !(p.debug_fault && i == 0))
+              for (int kb = 0; kb < D / 64; ++kb)
+                tma_load_2d(sbase + base + ring.stage * L::kTileBytes + kb * (kTile * 128), tm, kb * 64, row, full);
+            ring.mark_issued();
+            ring.advance();
+          };
+          if (!SUM) load(ra, a_full(ra.stage), a_empty(ra.stage), L::kA, &maps.a, head_a, p.B * (p.Hq / w.rep_a));
+          load(rb, b_full(rb.stage), b_empty(rb.stage), L::kB, &maps.b, head_b, p.B * (p.Hq / w.rep_b));
+          load(rc, c_full(rc.stage), c_empty(rc.stage), L::kC, &maps.c, head_c, p.B * (p.Hq / w.rep_c));
+        }
+        // never leave with a copy still writing into this block's shared memory
+        for (int s = 0; s < AS; ++s)
+          if (ra.was_issued(s)) drain_wait(a_full(s), ra.issued_parity(s));
+        for (int s = 0; s < BS; ++s)
+          if (rb.was_issued(s)) drain_wait(b_full(s), rb.issued_parity(s));
+        for (int s = 0; s < CS; ++s)
+          if (rc.was_issued(s)) drain_wait(c_full(s), rc.issued_parity(s));
+      }
+    } else if (warp == 1) {
+      if constexpr (!SUM) {
+        // -------------------------------------------------------- S = a b^T
+        const bool leader = elect_one();
+        constexpr uint32_t kId = idesc_bf16(128, 128, false, false);
+        const uint64_t ad0 = sdesc_sw128(sbase + L::kA, 16, 1024), bd0 = sdesc_sw128(sbase + L::kB, 16, 1024);
+        StageRing<AS> ra;
+        StageRing<BS> rb;
+        for (int i = 0; i < n_chunks; ++i) {
+          if (!warp_wait(a_full(ra.stage), ra.par, abort, p.status, tmo) ||
+              !warp_wait(b_full(rb.stage), rb.par, abort, p.status, tmo))
+            break;
+          // S's buffer is free once O1 of the last chunk has read P there
+          if (i > 0 && !warp_wait(o_full, (i - 1) & 1, abort, p.status, tmo)) break;
+          // a partial chunk's rows of b behind its end are zeroed first
+          if (chunk_n(i) < kTile && !warp_wait(c_ready, i & 1, abort, p.status, tmo)) break;
+          tc_fence_after();
+          const uint64_t ad = ad0 + ra.stage * (L::kTileBytes >> 4), bd = bd0 + rb.stage * (L::kTileBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;  // 16 KiB blocks, 32 B steps
+            if (leader) mma_ss(tS, ad + off, bd + off, kId, kk > 0);
+          }
+          if (leader) {
+            mma_commit(s_full);
+            mma_commit(b_empty(rb.stage));
+          }
+          __syncwarp();
+          ra.advance();
+          rb.advance();
+        }
+        if (leader) mma_commit(fin);
+        __syncwarp();
+        drain_wait(fin, 0);
+      }
+    } else if (warp == 2) {
+      if constexpr (!SUM) {
+        // ----------------------------------------- O1 = P c, O2 = a M
+        const bool leader = elect_one();
+        constexpr uint32_t kId = idesc_bf16(128, D, false, true);
+        const uint64_t cd0 = sdesc_sw128(sbase + L::kC, kTile * 128, 1024);
+        const uint64_t ad0 = sdesc_sw128(sbase + L::kA, 16, 1024);
+        const uint64_t md = sdesc_sw128(sbase + L::kM, D * 128, 1024);
+        StageRing<AS> ra;
+        StageRing<CS> rc;
+        for (int i = 0; i < n_chunks; ++i) {
+          if (!warp_wait(c_full(rc.stage), rc.par, abort, p.status, tmo) ||
+              !warp_wait(c_ready, i & 1, abort, p.status, tmo))
+            break;
+          // the epilogue of the last chunk has read O1 and O2
+          if (i > 0 && !warp_wait(o_free, (i - 1) & 1, abort, p.status, tmo)) break;
+          if (!warp_wait(m_full, i & 1, abort, p.status, tmo) ||
+              !warp_wait(a_full(ra.stage), ra.par, abort, p.status, tmo))
+            break;
+          tc_fence_after();
+          const uint64_t ad = ad0 + ra.stage * (L::kTileBytes >> 4), cd = cd0 + rc.stage * (L::kTileBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            if (leader)
+              mma_ss(tO2, ad + (kk >> 2) * 1024 + (kk & 3) * 2, md + (uint64_t)(kk * 128), kId, kk > 0);
+          __syncwarp();
+          if (!warp_wait(p_full, i & 1, abort, p.status, tmo)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            if (leader) mma_ts(tO1, tS + kk * 8, cd + (uint64_t)(kk * 128), kId, kk > 0);
+          if (leader) {
+            mma_commit(o_full);
+            mma_commit(c_empty(rc.stage));
+          }
+          __syncwarp();
+          ra.advance();
+          rc.advance();
+        }
+        if (leader) mma_commit(fin + 8);
+        __syncwarp();
+        drain_wait(fin + 8, 0);
+      }
+    } else {
+      // ---------------------------------------------- U = b^T (weighted c), hi then lo
+      const bool leader = elect_one();
+      constexpr uint32_t kId = idesc_bf16(128, D, true, true);
+      // (at D 64 the product's lower 64 rows read what lies behind the tile: nobody reads them)
+      const uint64_t bd0 = sdesc_sw128(sbase + L::kB, kTile * 128, 1024);
+      const uint64_t xd0 = sdesc_sw128(sbase + L::kX, kTile * 128, 1024);
+      StageRing<BS> rb;
+      StageRing<XS> rx;
+      bool ok = true;
+      for (int i = 0; i < n_chunks && ok; ++i) {
+        if (!(ok = warp_wait(b_full(rb.stage), rb.par, abort, p.status, tmo))) break;
+        const uint64_t bd = bd0 + rb.stage * (L::kTileBytes >> 4);
+        for (int part = 0; part < 2; ++part) {
+          if (!(ok = warp_wait(x_full(rx.stage), rx.par, abort, p.status, tmo))) break;
+          tc_fence_after();
+          const uint64_t xd = xd0 + rx.stage * (L::kTileBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            if (leader) mma_ss(tU, bd + (uint64_t)(kk * 128), xd + (uint64_t)(kk * 128), kId, part > 0 || kk > 0);
+          if (leader) {
+            mma_commit(x_empty(rx.stage));
+            if (part) {
+              mma_commit(b_empty(rb.stage));
+              mma_commit(u_full);
+            }
+          }
+          __syncwarp();
+          rx.advance();
+        }
+        rb.advance();
+      }
+      if (leader) mma_commit(fin + 16);
+      __syncwarp();
+      drain_wait(fin + 16, 0);
+    }
+  } else if (!SUM && warp < 8) {
+    if constexpr (!SUM) {
+      regs_math();
+      // ------------------------------------------------ P and the epilogue
+      const int quad = warp & 3, row = quad * 32 + lane;
+      const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+      StageRing<AS> ra;
+      for (int i = 0; i < n_chunks; ++i) {
+        const int pos0 = chunk_pos(i), n = chunk_n(i);
+        if (!warp_wait(s_full, i & 1, abort, p.status, tmo)) break;
+        tc_fence_after();
+        // columns j of this row: before it (front) or behind it (back), itself among them; pw is
+        // 0 for the others
+        const float* wrow = back ? pw - row : pw + row;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+          if (back ? c < quad : c > quad) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pk[j] = 0u;
+          } else {
+            uint32_t r[32];
+            tmem_ld32(tS + lane_off + c * 32, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int j0 = c * 32 + 2 * j;
+              const float w0 = back ? wrow[j0] : wrow[-j0], w1 = back ? wrow[j0 + 1] : wrow[-j0 - 1];
+              pk[j] = pack_bf16(__uint_as_float(r[2 * j]) * w0, __uint_as_float(r[2 * j + 1]) * w1);
+            }
+          }
+          tmem_st16(tS + lane_off + c * 16, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_full);
+
+        if (!warp_wait(o_full, i & 1, abort, p.status, tmo)) break;
+        tc_fence_after();
+        const float ow = pw[(back ? n - 1 - min(row, n - 1) : row) + 1 - late];
+        const int64_t tile_row0 = (int64_t)bh * p.T + p.m.slot(pos0);
+        const bool staged = n == kTile && !w.out_f32;
+        const bool store = row < n && in_bounds(tile_row0 + row, 1, rows_q, p.status);
+        uint8_t* const st = smem + L::kA + ra.stage * L::kTileBytes;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o1[32], o2[32];
+          tmem_ld32(tO1 + lane_off + c * 32, o1);
+          tmem_ld32(tO2 + lane_off + c * 32, o2);
+          tmem_wait_ld();
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[j] = w.mul * fmaf(ow, __uint_as_float(o2[j]), __uint_as_float(o1[j]));
+          if (w.out_f32) {
+            if (store) {
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(w.out) + (tile_row0 + row) * D + c * 32);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
+          } else {
+            uint4 u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              u[j] = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                                pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+            if (staged) {
+              // the tensor map's 128-byte swizzle: chunk a of row i at slot a ^ (i & 7)
+              uint4* line = reinterpret_cast<uint4*>(st + (c >> 1) * (kTile * 128) + row * 128);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) line[((c & 1) * 4 + j) ^ (row & 7)] = u[j];
+            } else if (store) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(w.out) + (tile_row0 + row) * D + c * 32);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) dst[j] = u[j];
+            }
+          }
+        }
+        // O1 and O2 have been read
+        tc_fence_before();
+        mbar_arrive(o_free);
+        if (staged) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (in_bounds(tile_row0 + quad * 32, 32, rows_q, p.status))
+              for (int kb = 0; kb < D / 64; ++kb)
+                tma_store_2d(&maps.o, kb * 64, (int)(tile_row0 + quad * 32),
+                             sbase + L::kA + ra.stage * L::kTileBytes + kb * (kTile * 128) + quad * 32 * 128);
+            bulk_commit_group();
+            bulk_wait_read_all();
+          }
+        }
+        if (lane == 0) mbar_arrive(a_empty(ra.stage));
+        ra.advance();
+      }
+      if (lane == 0) bulk_wait_all();
+    }
+  } else {
+    if constexpr (!SUM) regs_math();
+    // -------------------------------------------------------- the state
+    const int quad = warp & 3, row = quad * 32 + lane;  // a channel of b, and a token of a chunk
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    constexpr int DD = D * D;
+    const bool mine = D == 128 || row < D;
+    float M[D];
+    {
+#pragma unroll
+      for (int c = 0; c < D; ++c) M[c] = 0.f;
+      if (!SUM && mine) {
+        if (w.init) {
+          const float* src = w.init + (int64_t)bh * DD;
+          if (w.trans) {
+#pragma unroll
+            for (int c = 0; c < D; ++c) M[c] = src[c * D + row] * w.init_mul;
+          } else {
+#pragma unroll
+            for (int c = 0; c < D; c += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(src + row * D + c);
+              M[c] = x.x * w.init_mul, M[c + 1] = x.y * w.init_mul;
+              M[c + 2] = x.z * w.init_mul, M[c + 3] = x.w * w.init_mul;
+            }
+          }
+        }
+        // the runs before this one, folded in order
+        for (int s = 0; s < run; ++s) {
+          const float f = lin_pow(ld, lin_run_tokens<kTile>(p, n_tok, back, s));
+          const float* src = w.sums + ((int64_t)bh * p.segs + s) * DD;
+          if (!w.trans) {  // a run's sum lies with its columns first (see below)
+#pragma unroll
+            for (int c = 0; c < D; ++c) M[c] = fmaf(f, M[c], src[c * D + row]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < D; c += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(src + row * D + c);
+              M[c] = fmaf(f, M[c], x.x), M[c + 1] = fmaf(f, M[c + 1], x.y);
+              M[c + 2] = fmaf(f, M[c + 2], x.z), M[c + 3] = fmaf(f, M[c + 3], x.w);
+            }
+          }
+        }
+      }
+    }
+    // M as bf16, the operand of O2: rows of b's channels, 128-byte lines of 64 columns, swizzled
+    auto publish = [&]() {
+      if (mine) {
+#pragma unroll
+        for (int c = 0; c < D; c += 8) {
+          uint4* line = reinterpret_cast<uint4*>(smem + L::kM + (c >> 6) * (D * 128) + row * 128);
+          line[((c & 63) >> 3) ^ (row & 7)] =
+              make_uint4(pack_bf16(M[c], M[c + 1]), pack_bf16(M[c + 2], M[c + 3]),
+                         pack_bf16(M[c + 4], M[c + 5]), pack_bf16(M[c + 6], M[c + 7]));
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(m_full);
+    };
+    if (!SUM && n_chunks > 0) publish();
+    StageRing<BS> rb;
+    StageRing<CS> rc;
+    StageRing<XS> rx;
+    bool ok = true;
+    for (int i = 0; i < n_chunks && ok; ++i) {
+      const int n = chunk_n(i);
+      if (!(ok = warp_wait(c_full(rc.stage), rc.par, abort, p.status, tmo))) break;
+      uint8_t* const ct = smem + L::kC + rc.stage * L::kTileBytes;
+      if (n < kTile) {
+        // rows behind the last token hold anything: zeros, in b and in c
+        if (!(ok = warp_wait(b_full(rb.stage), rb.par, abort, p.status, tmo))) break;
+        if (row >= n) {
+          uint8_t* const bt = smem + L::kB + rb.stage * L::kTileBytes;
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            reinterpret_cast<uint4*>(ct + (j >> 3) * (kTile * 128) + row * 128)[j & 7] = zero;
+            reinterpret_cast<uint4*>(bt + (j >> 3) * (kTile * 128) + row * 128)[j & 7] = zero;
+          }
+        }
+        fence_proxy_async_smem();
+      }
+      if (!SUM) mbar_arrive(c_ready);
+      // this token's row of c times its weight, hi = bf16 of it and lo = bf16 of what is left
+      const float uw = row < n ? pw[(back ? row : n - 1 - row) + late] : 0.f;
+      const uint4* const crow = reinterpret_cast<const uint4*>(ct + row * 128);
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        if (!(ok = warp_wait(x_empty(rx.stage), rx.par ^ 1, abort, p.status, tmo))) break;
+        uint8_t* const xt = smem + L::kX + rx.stage * L::kTileBytes + row * 128;
+#pragma unroll 4
+        for (int j = 0; j < D / 8; ++j) {
+          const int at = (j & 7) ^ (row & 7), blk = (j >> 3) * (kTile * 128);
+          const uint4 x = crow[blk / 16 + at];
+          const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+          uint32_t out[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float v0 = bf16_lo(in[k]) * uw, v1 = bf16_hi(in[k]) * uw;
+            out[k] = pack_bf16(v0, v1);
+            if (part) out[k] = pack_bf16(v0 - bf16_lo(out[k]), v1 - bf16_hi(out[k]));
+          }
+          reinterpret_cast<uint4*>(xt + blk)[at] = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();  // (U of the last chunk has been read)
+        mbar_arrive(x_full(rx.stage));
+        rx.advance();
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c_empty(rc.stage));
+      rc.advance();
+      rb.advance();
+      // M = r^n M + U
+      if (!(ok = warp_wait(u_full, i & 1, abort, p.status, tmo))) break;
+      tc_fence_after();
+      const float f = pw[n];
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t u[32];
+        tmem_ld32(tU + lane_off + c * 32, u);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) M[c * 32 + j] = fmaf(f, M[c * 32 + j], __uint_as_float(u[j]));
+      }
+      if (!SUM && i + 1 < n_chunks) {
+        // O2 of this chunk has read the old copy
+        if (!(ok = warp_wait(o_full, i & 1, abort, p.status, tmo))) break;
+        publish();
+      }
+    }
+    if (ok && mine) {
+      if constexpr (SUM) {
+        // columns first: the threads of a warp write, and in most sweeps read, consecutive numbers
+        float* dst = w.sums + ((int64_t)bh * p.segs + run) * DD;
+#pragma unroll
+        for (int c = 0; c < D; ++c) dst[c * D + row] = M[c];
+      } else if (run == p.segs - 1 && w.fin) {
+        float* dst = w.fin + (int64_t)bh * DD;
+#pragma unroll
+        for (int c = 0; c < D; c += 4)
+          *reinterpret_cast<float4*>(dst + row * D + c) = make_float4(
+              M[c] * w.fin_mul, M[c + 1] * w.fin_mul, M[c + 2] * w.fin_mul, M[c + 3] * w.fin_mul);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+static bool make_map(CUtensorMap* m, const void* t, int64_t heads, int T, int D, int box_rows) {
+  return encode_tmap_2d_bf16(m, t, D, (uint64_t)heads * T, 64, box_rows) == CUDA_SUCCESS;
+}
+
+template <int D, bool SUM>
+static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, cudaStream_t st) {
+  Params prm;
+  prm.p = p;
+  for (int i = 0; i < n; ++i) {
+    const LinSweep& w = sweeps[i];
+    Maps& m = prm.maps[i];
+    const int64_t hq = (int64_t)p.B * p.Hq;
+    if (!make_map(&m.b, w.b, hq / w.rep_b, p.T, D, kTile) || !make_map(&m.c, w.c, hq / w.rep_c, p.T, D, kTile))
+      return cudaErrorInvalidValue;
+    m.a = m.o = m.b;
+    if (!SUM && !make_map(&m.a, w.a, hq / w.rep_a, p.T, D, kTile)) return cudaErrorInvalidValue;
+    // the output as 32-row, 64-column boxes (one warp's rows)
+    if (!SUM && !w.out_f32 && !make_map(&m.o, w.out, hq, p.T, D, 32)) return cudaErrorInvalidValue;
+  }
+  constexpr int kSmem = Smem<D, SUM>::kBytes, kThreads = SUM ? 256 : 384;
+  auto kern = sweep_kernel<D, SUM>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  if (!SUM && (e = check_register_split(kern, kThreads)) != cudaSuccess) return e;
+  const unsigned blocks = (unsigned)(p.B * p.Hq * (SUM ? p.segs - 1 : p.segs));
+  kern<<<dim3(blocks, n), kThreads, kSmem, st>>>(prm);
+  return cudaGetLastError();
+}
+
+}  // namespace lintc
+
+bool linear_tc_supported(const Ring& R) {
+  if (!R.bf16 || (R.D != 64 && R.D != 128)) return false;
+  // a chunk of 128 positions is 128 slots: zigzag chunks are whole chunks
+  if (R.zz && (R.T / R.cp / 2) % kLinTcChunk) return false;
+  return (double)R.B * R.Hq * R.T < 2147483647.0 - kLinTcChunk;
+}
+
+cudaError_t launch_linear_tc(const Linear& p, cudaStream_t st, bool backward) {
+  cudaError_t e;
+  if (p.segs > 1) {
+    timing_begin(backward ? "linear_bwd_sums" : "linear_fwd_sums", st);
+    e = p.D == 128 ? lintc::run<128, true>(p, p.n_sums, p.sum, st) : lintc::run<64, true>(p, p.n_sums, p.sum, st);
+    timing_end(st);
+    if (e != cudaSuccess) return e;
+  }
+  timing_begin(backward ? "linear_bwd" : "linear_fwd", st);
+  e = p.D == 128 ? lintc::run<128, false>(p, p.n_sweeps, p.sweep, st)
+                 : lintc::run<64, false>(p, p.n_sweeps, p.sweep, st);
+  timing_end(st);
+  return e;
+}
+
+}  // namespace cpattn
