@@ -25,17 +25,17 @@ struct Rotate {
   // queries, keys, values.  Forward: in = the projection's side, out = the attention's.
   // Backward: in = the upstream gradient (attention's side), x = the forward's input, out =
   // its gradient (projection's side)
-  RowView in[3], x[2], out[3];
+  RowView in[3], x[3], out[3];
   const void* w[2];
   const double* inv_freq;
   const int* positions;
   float* sums;   // backward: a row of 2 D numbers a block
-  // set by the launch: lanes a row, slots a block, parts of the heads
-  int lanes, tile, tile_log2, splits;
+  // set by the launch: pairs a lane, lanes a row, groups of slots, parts of the heads
+  int P, lanes, groups, splits;
   float inv_d;
 };
-// Blocks of the backward kernel at most, each with a row of sums: four an SM.
-constexpr int kBwdBlocks = 4 * kSms;
+// Blocks of the backward kernel at most, each with a row of sums: two an SM.
+constexpr int kBwdBlocks = 2 * kSms;
 size_t rotate_bwd_workspace(int D, int norm);
 cudaError_t launch_rotate_fwd(Rotate p, cudaStream_t st);
 cudaError_t launch_rotate_bwd(Rotate p, float* dq_weight, float* dk_weight, cudaStream_t st);

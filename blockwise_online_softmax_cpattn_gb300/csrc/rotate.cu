@@ -2,19 +2,25 @@
 // RMS norm of each head of the queries and keys, rotation by position, the move into the
 // attention's token order; values move along.  And its backward pass.
 //
-// A row of D channels belongs to D / 8 lanes (rounded up to a power of two: 16 at D 128, so a
-// warp holds two rows).  Lane l owns pairs 4l .. 4l+3 of the rotation, as two vectors of four
-// channels: (4l .., rot/2 + 4l ..) when pairs lie half a rotation apart, else eight channels
-// in a row.  So a pair never crosses lanes, the only exchange is the norm's sum (four shuffles
-// at D 128), and each row is read and written once.
+// A row of D channels belongs to D / 2P lanes, rounded up to a power of two, with P = 8 in bf16 (8
+// lanes at D 128, four rows a warp), or 4 where D or the rotation is no multiple of 16, and 4 in
+// float32: vectors of 16 bytes.  Lane l owns
+// pairs P l .. P l + P-1 of the rotation, as two vectors of P channels: at P l and rot/2 + P l when
+// pairs lie half a rotation apart, else 2P channels in a row.  So a pair never crosses lanes, the
+// only exchange is the norm's sum (three shuffles at D 128), and each row is read and written
+// once.  (With P 4 alone the shuffles and what each head costs anyway held the backward pass at
+// 81 us for 8192 tokens of 48 heads, 3.3 TB/s.)
 //
-// A block takes `tile` consecutive slots and all (or, with few tokens, some) of their heads:
-// the angles of a slot are the same in every head, so their cosines and sines are computed
-// once a block, into shared memory.  The angle p f is formed in float64 and reduced to a
-// fraction of a turn there: at position 10^5 a float32 product alone is off by 2^-8 of a
-// radian.
+// A warp takes the same slots (four at D 128) of a run of heads, one head after the other: a
+// slot's angles are the same in every head, so a lane forms the cosines and sines of its pairs
+// once and keeps them in registers.  The rows of the next heads are on their way into shared memory
+// meanwhile (cp.async, each lane its own 16-byte pieces, so nothing has to be synchronised): some
+// 70 to 90 KB an SM, more than what 7 TB/s at a microsecond's latency takes, and no registers.
+// The angle p f is formed in whole numbers, as 64 binary places of a turn: at position 10^5 a
+// float32 product alone is off by 2^-8 of a radian, and the float64 units, two lanes an SM, took
+// 2 us of a decoding step's 6.6.
 //
-// Bound by memory: 32 (bf16) to 64 (float32) bytes a lane and row against some 70 instructions.
+// Bound by memory: 64 (bf16) to 128 (float32) bytes a lane and row against some 130 instructions.
 #include "layer.cuh"
 
 namespace cpattn {
@@ -22,54 +28,81 @@ namespace rotate {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxTile = 16;
-constexpr int kMaxPairs = 64;
 
-struct V4 {
-  float v[4];
+// P channels in a row as they lie in memory, and as numbers.
+template <typename E, int P>
+struct Vec;
+template <int P>
+struct Vec<__nv_bfloat16, P> {
+  uint32_t w[P / 2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    if constexpr (P == 8) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x, w[1] = x.y;
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+};
+template <int P>
+struct Vec<float, P> {
+  float w[P];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < P; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p + i);
+      w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+    }
+  }
+  __device__ __forceinline__ float at(int i) const { return w[i]; }
 };
 
-__device__ __forceinline__ V4 load4(const __nv_bfloat16* p) {
-  const uint2 r = __ldcs(reinterpret_cast<const uint2*>(p));
-  V4 x;
-  x.v[0] = __uint_as_float(r.x << 16);
-  x.v[1] = __uint_as_float(r.x & 0xFFFF0000u);
-  x.v[2] = __uint_as_float(r.y << 16);
-  x.v[3] = __uint_as_float(r.y & 0xFFFF0000u);
-  return x;
+template <int P>
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[P]) {
+  if constexpr (P == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                              pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
-__device__ __forceinline__ V4 load4(const float* p) {
-  const float4 r = __ldcs(reinterpret_cast<const float4*>(p));
-  return V4{{r.x, r.y, r.z, r.w}};
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-}
-__device__ __forceinline__ void store4(float* p, const float* x) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+template <int P>
+__device__ __forceinline__ void store(float* p, const float (&x)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; i += 4)
+    *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
 }
 
-// Eight channels of a lane as (first, second) of its four pairs, and back.
-template <bool NEAR>
-__device__ __forceinline__ void to_pairs(const V4& x, const V4& y, float (&a)[4], float (&b)[4]) {
-  if constexpr (NEAR) {
-    a[0] = x.v[0], b[0] = x.v[1], a[1] = x.v[2], b[1] = x.v[3];
-    a[2] = y.v[0], b[2] = y.v[1], a[3] = y.v[2], b[3] = y.v[3];
-  } else {
+// A lane's two vectors as (first, second) of its pairs, and back.
+template <bool NEAR, typename E, int P>
+__device__ __forceinline__ void to_pairs(const Vec<E, P>& x, const Vec<E, P>& y, float (&a)[P], float (&b)[P]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = x.v[i], b[i] = y.v[i];
+  for (int i = 0; i < P; ++i) {
+    if constexpr (NEAR) {
+      a[i] = i < P / 2 ? x.at(2 * i) : y.at(2 * i - P);
+      b[i] = i < P / 2 ? x.at(2 * i + 1) : y.at(2 * i + 1 - P);
+    } else {
+      a[i] = x.at(i), b[i] = y.at(i);
+    }
   }
 }
-template <bool NEAR, typename E>
-__device__ __forceinline__ void store_pairs(E* row, int c0, int c1, const float (&a)[4],
-                                            const float (&b)[4]) {
+template <bool NEAR, typename E, int P>
+__device__ __forceinline__ void store_pairs(E* row, int c0, int c1, const float (&a)[P], const float (&b)[P]) {
   if constexpr (NEAR) {
-    const float x[4] = {a[0], b[0], a[1], b[1]}, y[4] = {a[2], b[2], a[3], b[3]};
-    store4(row + c0, x);
-    store4(row + c1, y);
+    float x[P], y[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      x[i] = i & 1 ? b[i / 2] : a[i / 2];
+      y[i] = i & 1 ? b[(P + i) / 2] : a[(P + i) / 2];
+    }
+    store<P>(row + c0, x);
+    store<P>(row + c1, y);
   } else {
-    store4(row + c0, a);
-    store4(row + c1, b);
+    store<P>(row + c0, a);
+    store<P>(row + c1, b);
   }
 }
 
@@ -80,308 +113,366 @@ __device__ __forceinline__ float row_sum(float s, int lanes) {
   return s;
 }
 
-// Channels of a lane: two vectors of four, at c0 and c1.  Past the rotated pairs a lane's
-// eight channels follow each other in either pairing, and the table holds no turn (1, 0).
-template <bool NEAR>
+// Channels of a lane: its two vectors begin at c0 and c1.  Past the rotated pairs its 2P channels
+// follow each other in either pairing, and are not turned.
+template <bool NEAR, int P>
 __device__ __forceinline__ void lane_channels(const Rotate& p, int l, int* c0, int* c1) {
-  *c0 = 8 * l;
-  *c1 = 8 * l + 4;
-  if (!NEAR && 4 * l < p.rot / 2) {
-    *c0 = 4 * l;
-    *c1 = 4 * l + p.rot / 2;
+  *c0 = 2 * P * l;
+  *c1 = 2 * P * l + P;
+  if (!NEAR && P * l < p.rot / 2) {
+    *c0 = P * l;
+    *c1 = P * l + p.rot / 2;
   }
 }
-// (past the rotated pairs the two vectors hold channels as they come: pairs do not matter)
 
-struct __align__(16) Shared {
-  float2 cs[kMaxTile][kMaxPairs];  // cos, sin of every pair of every slot of the tile
-  int from[kMaxTile];              // token of the projection's side
+// f / (2 pi) as 64 binary places of a turn (f = m 2^(e - 1075); whole turns fall away), so that
+// p times it, modulo 2^64, is where position p stands.  Off by 2^-64 for f < 2.
+__device__ __forceinline__ uint64_t turns_of(double f) {
+  const uint64_t bits = (uint64_t)__double_as_longlong(f);
+  const int e = (int)(bits >> 52) & 0x7FF;
+  const uint64_t m = e ? (bits << 11) | 0x8000000000000000ull : 0;  // 64 binary places
+  uint64_t g = __umul64hi(m, 0xA2F9836E4E441529ull);                 // 2^66 / (2 pi)
+  const int s = e - 1024;
+  g = s >= 64 || s <= -64 ? 0 : s >= 0 ? g << s : g >> -s;
+  return bits >> 63 ? 0 - g : g;
+}
+
+// What a lane keeps for its slot: the two tokens (attention's and projection's side) and the turns.
+template <int P>
+struct Slot {
+  int b, t, from;
+  bool live;
+  float co[P], si[P];
 };
 
-// Fills the tile's table.  tile slots from t0 on, of batch row b.
-__device__ __forceinline__ void fill_table(const Rotate& p, int b, int t0, int nt, float dir,
-                                           Shared* s) {
-  const int pairs = p.D / 2;
-  for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
-    const int t = i / pairs, j = i - t * pairs;
-    float2 v = make_float2(1.f, 0.f);
-    if (j < p.rot / 2) {
-      const int slot = t0 + t;
-      const int pos = p.positions ? p.positions[(int64_t)b * p.T + slot] : p.m.pos(slot);
-      const double turns = (double)pos * (p.inv_freq[j] * 0.15915494309189533577);  // 1 / (2 pi)
-      const float f = (float)(turns - rint(turns));
-      sincospif(2.f * f, &v.y, &v.x);
-      v.y *= dir;
+// Slots of the `group`'th group, 32 / lanes of them, counted over the whole batch.  dir -1 turns back.
+template <int P>
+__device__ __forceinline__ Slot<P> make_slot(const Rotate& p, int group, int sub, int l, float dir) {
+  Slot<P> s;
+  const int g = group * (32 / p.lanes) + sub;
+  s.live = g < p.B * p.T && 2 * P * l < p.D;
+  s.b = s.live ? g / p.T : 0;
+  s.t = s.live ? g - s.b * p.T : 0;
+  const int nat = p.m.pos(s.t), j0 = P * l;
+  s.from = p.natural_in ? nat : s.t;
+  const bool turned = s.live && j0 < p.rot / 2;
+  const int pos = turned && p.positions ? p.positions[g] : nat;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    s.co[i] = 1.f;
+    s.si[i] = 0.f;
+    if (turned) {
+      const uint64_t at = (uint64_t)(int64_t)pos * turns_of(p.inv_freq[j0 + i]);
+      sincospif((float)(int32_t)(at >> 32) * 4.656612873077392578125e-10f, &s.si[i], &s.co[i]);  // 2^-31
+      s.si[i] *= dir;
     }
-    s->cs[t][j] = v;
   }
-  for (int t = threadIdx.x; t < nt; t += kThreads)
-    s->from[t] = p.natural_in ? p.m.pos(t0 + t) : t0 + t;
+  return s;
 }
 
+// The rows of a warp's next K heads, in shared memory: [head % K][vector][piece][lane], a vector's
+// P channels in pieces of 16 bytes (8: four bf16).  V vectors a row: two of the row itself, in the
+// backward pass with the norm two of x.
+template <typename E, int P, int V>
+struct Ring {
+  static constexpr int kBytes = P * (int)sizeof(E), kPiece = kBytes < 16 ? kBytes : 16;
+  static constexpr int kPieces = kBytes / kPiece;
+  static constexpr int K = V * kBytes > 64 ? 2 : 4;  // heads
+  static constexpr int kWarpBytes = K * V * kBytes * 32;
+
+  uint32_t base;  // of this lane
+  __device__ __forceinline__ uint32_t at(int head, int v) const {
+    return base + ((head & (K - 1)) * V + v) * (kBytes * 32);
+  }
+  __device__ __forceinline__ void fetch(int head, int v, const E* src) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const char* from = reinterpret_cast<const char*>(src) + i * kPiece;
+      if constexpr (kPiece == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(head, v) + i * 512), "l"(from) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at(head, v)), "l"(from) : "memory");
+    }
+  }
+  __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // all but the last K - 1 heads have come
+  __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(K - 1) : "memory"); }
+  __device__ __forceinline__ Vec<E, P> get(int head, int v) const {
+    Vec<E, P> x;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      if constexpr (kPiece == 16)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(word(x, 4 * i)), "=r"(word(x, 4 * i + 1)), "=r"(word(x, 4 * i + 2)), "=r"(word(x, 4 * i + 3))
+                     : "r"(at(head, v) + i * 512)
+                     : "memory");
+      else
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(word(x, 0)), "=r"(word(x, 1)) : "r"(at(head, v)) : "memory");
+    }
+    return x;
+  }
+  __device__ __forceinline__ void clear() const {
+#pragma unroll
+    for (int i = 0; i < K * V * kPieces; ++i)
+#pragma unroll
+      for (int j = 0; j < kPiece / 4; ++j)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + i * (kPiece * 32) + 4 * j), "r"(0) : "memory");
+  }
+  static __device__ __forceinline__ uint32_t& word(Vec<E, P>& x, int i) {
+    return reinterpret_cast<uint32_t*>(x.w)[i];
+  }
+};
+
+// Rows of all heads (queries, keys, values in this order) by number.
 template <typename E>
-__device__ __forceinline__ E* row_ptr(const RowView& v, int b, int h, int t) {
-  return static_cast<E*>(v.p) + b * v.sb + h * v.sh + t * v.st;
+__device__ __forceinline__ E* head_row(const Rotate& p, const RowView (&v)[3], int b, int t, int head) {
+  const int j = head < p.Hq ? 0 : head < p.Hq + p.Hkv ? 1 : 2;
+  const int h = j == 0 ? head : j == 1 ? head - p.Hq : head - p.Hq - p.Hkv;
+  const RowView& x = v[j];
+  return static_cast<E*>(x.p) + b * x.sb + h * x.sh + t * x.st;
 }
 
-// Row r of the block's rows, heads outermost: head and token.  Whole tiles are a power of two.
-__device__ __forceinline__ void split_row(const Rotate& p, int r, int nt, int* head, int* t) {
-  if (nt == p.tile) *head = r >> p.tile_log2;
-  else *head = r / nt;
-  *t = r - *head * nt;
+// (two pairs an instruction: the backward pass with the norm is close to issue-bound without)
+template <int P>
+__device__ __forceinline__ float2 two(const float (&x)[P], int i) {
+  return make_float2(x[i], x[i + 1]);
+}
+template <int P>
+__device__ __forceinline__ void put(float (&x)[P], int i, float2 v) {
+  x[i] = v.x, x[i + 1] = v.y;
 }
 
-// The head'th of all heads: queries, keys, then values.
-__device__ __forceinline__ int which(const Rotate& p, int head, int* h) {
-  if (head < p.Hq) {
-    *h = head;
-    return 0;
-  }
-  if (head < p.Hq + p.Hkv) {
-    *h = head - p.Hq;
-    return 1;
-  }
-  *h = head - p.Hq - p.Hkv;
-  return 2;
-}
-
-// Four rows a lane in flight: with 32 to 48 registers of loads outstanding and six blocks an SM
-// some 48 KB are under way, what 7 TB/s at a microsecond's latency takes.
-constexpr int kRows = 4;
-
-template <typename E, bool NEAR, bool NORM>
-__global__ void __launch_bounds__(kThreads) fwd_kernel(const Rotate p) {
-  __shared__ Shared s;
-  const int tiles = (p.T + p.tile - 1) / p.tile;
-  const int b = blockIdx.x / tiles, t0 = (blockIdx.x - b * tiles) * p.tile;
-  const int nt = min(p.tile, p.T - t0);
-  fill_table(p, b, t0, nt, 1.f, &s);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int l = lane & (p.lanes - 1), sub = lane / p.lanes, per_warp = 32 / p.lanes;
-  const bool live = 8 * l < p.D;
-  int c0, c1;
-  lane_channels<NEAR>(p, l, &c0, &c1);
-  float wa[2][4], wb[2][4];
+template <int P>
+__device__ __forceinline__ void turn(const Slot<P>& s, float (&a)[P], float (&b)[P]) {
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    V4 x{{1.f, 1.f, 1.f, 1.f}}, y = x;
-    if (NORM && p.w[j] && live) {
-      x = load4(static_cast<const E*>(p.w[j]) + c0);
-      y = load4(static_cast<const E*>(p.w[j]) + c1);
-    }
-    to_pairs<NEAR>(x, y, wa[j], wb[j]);
+  for (int i = 0; i < P; i += 2) {
+    const float2 x = two(a, i), y = two(b, i), co = two(s.co, i), si = two(s.si, i);
+    const float2 ny = make_float2(-y.x, -y.y);
+    put(a, i, fma2(x, co, mul2(ny, si)));
+    put(b, i, fma2(x, si, mul2(y, co)));
   }
+}
+
+template <bool NEAR, typename E, int P>
+__device__ __forceinline__ void load_weights(const Rotate& p, const void* w, int c0, int c1, float (&a)[P],
+                                             float (&b)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) a[i] = b[i] = 1.f;
+  if (w && c0 < p.D) {
+    Vec<E, P> x, y;
+    x.load(static_cast<const E*>(w) + c0);
+    y.load(static_cast<const E*>(w) + c1);
+    to_pairs<NEAR>(x, y, a, b);
+  }
+}
+
+// An item is a group of slots and a part of all heads; parts of a group lie far apart, so that
+// warps of a block write neighbouring slots of the same heads.
+__device__ __forceinline__ void item_of(const Rotate& p, int item, int heads, int* group, int* h0, int* h1) {
+  const int part = item / p.groups;
+  *group = item - part * p.groups;
+  *h0 = (int)((int64_t)heads * part / p.splits);
+  *h1 = (int)((int64_t)heads * (part + 1) / p.splits);
+}
+
+template <typename E, bool NEAR, bool NORM, int P>
+__global__ void __launch_bounds__(kThreads, sizeof(E) == 2 ? 3 : 2) fwd_kernel(const Rotate p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  using R = Ring<E, P, 2>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (p.lanes - 1);
+  const int item = blockIdx.x * kWarps + warp;
+  if (item >= p.groups * p.splits) return;
+  const R ring{smem_u32(smem) + warp * R::kWarpBytes + lane * R::kPiece};
   const int heads = p.Hq + p.Hkv + (p.in[2].p ? p.Hkv : 0);
-  const int h0 = (int)((int64_t)heads * blockIdx.y / gridDim.y);
-  const int h1 = (int)((int64_t)heads * (blockIdx.y + 1) / gridDim.y);
-  const int rows = (h1 - h0) * nt, step = kWarps * per_warp;
-  __syncthreads();
-  for (int base = warp * per_warp + sub; __any_sync(0xffffffffu, base < rows); base += kRows * step) {
-    V4 x[kRows], y[kRows];
-    int kind[kRows], hh[kRows], tt[kRows];
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int r = base + u * step;
-      kind[u] = -1;
-      hh[u] = tt[u] = 0;
-      x[u] = y[u] = V4{{0.f, 0.f, 0.f, 0.f}};
-      if (r < rows && live) {
-        int head;
-        split_row(p, r, nt, &head, &tt[u]);
-        kind[u] = which(p, h0 + head, &hh[u]);
-        const E* row = row_ptr<const E>(p.in[kind[u]], b, hh[u], s.from[tt[u]]);
-        x[u] = load4(row + c0);
-        y[u] = load4(row + c1);
-      }
+  int group, h0, h1;
+  item_of(p, item, heads, &group, &h0, &h1);
+  const Slot<P> s = make_slot<P>(p, group, lane / p.lanes, l, 1.f);
+  int c0, c1;
+  lane_channels<NEAR, P>(p, l, &c0, &c1);
+  if (!s.live) ring.clear();
+  auto fetch = [&](int h) {
+    if (s.live && h < h1) {
+      const E* row = head_row<const E>(p, p.in, s.b, s.from, h);
+      ring.fetch(h, 0, row + c0);
+      ring.fetch(h, 1, row + c1);
     }
+    ring.commit();
+  };
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      float a[4], c[4];
-      to_pairs<NEAR>(x[u], y[u], a, c);
-      if (NORM) {
-        float sum = 0.f;
+  for (int u = 0; u < R::K; ++u) fetch(h0 + u);
+  float wa[P], wb[P];
+  for (int h = h0; h < h1; ++h) {
+    if constexpr (NORM)
+      if (h == h0 || h == p.Hq) load_weights<NEAR, E, P>(p, h < p.Hq ? p.w[0] : p.w[1], c0, c1, wa, wb);
+    ring.wait();
+    float a[P], b[P];
+    to_pairs<NEAR>(ring.get(h, 0), ring.get(h, 1), a, b);
+    fetch(h + R::K);
+    if (h < p.Hq + p.Hkv) {
+      if constexpr (NORM) {
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum = fmaf(a[i], a[i], fmaf(c[i], c[i], sum));
-        const float rs = rsqrtf(row_sum(sum, p.lanes) * p.inv_d + p.eps);
-        if (kind[u] < 2) {
-          const bool k = kind[u] == 1;
+        for (int i = 0; i < P; i += 2) sum = fma2(two(a, i), two(a, i), fma2(two(b, i), two(b, i), sum));
+        const float rs = rsqrtf(row_sum(sum.x + sum.y, p.lanes) * p.inv_d + p.eps);
+        const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a[i] *= rs * (k ? wa[1][i] : wa[0][i]);
-            c[i] *= rs * (k ? wb[1][i] : wb[0][i]);
-          }
+        for (int i = 0; i < P; i += 2) {
+          put(a, i, mul2(two(a, i), mul2(rs2, two(wa, i))));
+          put(b, i, mul2(two(b, i), mul2(rs2, two(wb, i))));
         }
       }
-      if (kind[u] < 0) continue;
-      if (kind[u] < 2) {
-        const float4* cs = reinterpret_cast<const float4*>(&s.cs[tt[u]][4 * l]);
-        const float4 t01 = cs[0], t23 = cs[1];
-        const float co[4] = {t01.x, t01.z, t23.x, t23.z}, si[4] = {t01.y, t01.w, t23.y, t23.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float y0 = a[i] * co[i] - c[i] * si[i];
-          c[i] = a[i] * si[i] + c[i] * co[i];
-          a[i] = y0;
-        }
-      }
-      E* out = row_ptr<E>(p.out[kind[u]], b, hh[u], t0 + tt[u]);
-      store_pairs<NEAR>(out, c0, c1, a, c);
+      turn(s, a, b);
     }
+    if (s.live) store_pairs<NEAR>(head_row<E>(p, p.out, s.b, s.t, h), c0, c1, a, b);
   }
 }
 
-// The backward pass of a row: dY turned back (in: attention's side), with the norm also x.
-// Blocks are persistent: each keeps its share of the weights' gradients in registers (eight
-// channels a lane, queries and keys apart) and leaves one row of sums in the workspace; a
-// second, small kernel adds the rows in order.
-constexpr int kBwdRows = 2;  // rows a lane in flight, two loads each with the norm
-
-template <typename E, bool NEAR, bool NORM>
-__global__ void __launch_bounds__(kThreads) bwd_kernel(const Rotate p) {
-  __shared__ Shared s;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int l = lane & (p.lanes - 1), sub = lane / p.lanes, per_warp = 32 / p.lanes;
-  const bool live = 8 * l < p.D;
-  int c0, c1;
-  lane_channels<NEAR>(p, l, &c0, &c1);
-  float wa[2][4], wb[2][4], da[2][4], db[2][4];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    V4 x{{1.f, 1.f, 1.f, 1.f}}, y = x;
-    if (NORM && p.w[j] && live) {
-      x = load4(static_cast<const E*>(p.w[j]) + c0);
-      y = load4(static_cast<const E*>(p.w[j]) + c1);
-    }
-    to_pairs<NEAR>(x, y, wa[j], wb[j]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) da[j][i] = db[j][i] = 0.f;
-  }
+// Backward: dY turned back (in: attention's side), with the norm also x.  Blocks are persistent and
+// a warp takes an equal stretch of all (group, head) pairs, a group's heads first; each block
+// keeps its share of the weights' gradients in registers and leaves one row of sums in the
+// workspace; a second, small kernel adds the rows in order.
+template <typename E, bool NEAR, bool NORM, int P>
+__global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Rotate p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  using R = Ring<E, P, NORM ? 4 : 2>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (p.lanes - 1), sub = lane / p.lanes;
+  const R ring{smem_u32(smem) + warp * R::kWarpBytes + lane * R::kPiece};
   const int heads = p.Hq + p.Hkv + (p.in[2].p ? p.Hkv : 0);
-  const int tiles = (p.T + p.tile - 1) / p.tile, step = kWarps * per_warp;
-  const int n_items = p.B * tiles * p.splits;
-  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-    const int tl = item / p.splits, part = item - tl * p.splits;
-    const int b = tl / tiles, t0 = (tl - b * tiles) * p.tile;
-    const int nt = min(p.tile, p.T - t0);
-    const int h0 = (int)((int64_t)heads * part / p.splits);
-    const int h1 = (int)((int64_t)heads * (part + 1) / p.splits);
-    const int rows = (h1 - h0) * nt;
-    __syncthreads();  // the last item's table has been read
-    fill_table(p, b, t0, nt, -1.f, &s);
-    __syncthreads();
-    for (int base = warp * per_warp + sub; __any_sync(0xffffffffu, base < rows);
-         base += kBwdRows * step) {
-      V4 x[kBwdRows], y[kBwdRows], gx[kBwdRows], gy[kBwdRows];
-      int kind[kBwdRows], hh[kBwdRows], tt[kBwdRows];
+  int c0, c1;
+  lane_channels<NEAR, P>(p, l, &c0, &c1);
+  // this thread's share of the weights' gradients, queries then keys: in shared memory, so that
+  // only one tensor's is in registers at a time
+  float4* const mine = reinterpret_cast<float4*>(smem + kWarps * R::kWarpBytes) + threadIdx.x;
+  constexpr int kQuads = P / 2;  // 2 P numbers
+  if constexpr (NORM) {
 #pragma unroll
-      for (int u = 0; u < kBwdRows; ++u) {
-        const int r = base + u * step;
-        kind[u] = -1;
-        hh[u] = tt[u] = 0;
-        x[u] = y[u] = gx[u] = gy[u] = V4{{0.f, 0.f, 0.f, 0.f}};
-        if (r < rows && live) {
-          int head;
-          split_row(p, r, nt, &head, &tt[u]);
-          kind[u] = which(p, h0 + head, &hh[u]);
-          const E* row = row_ptr<const E>(p.in[kind[u]], b, hh[u], t0 + tt[u]);
-          gx[u] = load4(row + c0);
-          gy[u] = load4(row + c1);
-          if (NORM && kind[u] < 2) {
-            const E* xr = row_ptr<const E>(p.x[kind[u]], b, hh[u], s.from[tt[u]]);
-            x[u] = load4(xr + c0);
-            y[u] = load4(xr + c1);
+    for (int i = 0; i < 2 * kQuads; ++i) mine[i * kThreads] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const int64_t pairs = (int64_t)p.groups * heads, warps = (int64_t)gridDim.x * kWarps;
+  const int64_t w0 = (int64_t)blockIdx.x * kWarps + warp, end = pairs * (w0 + 1) / warps;
+  for (int64_t at = pairs * w0 / warps; at < end;) {
+    const int group = (int)(at / heads), h0 = (int)(at - (int64_t)group * heads);
+    const int h1 = (int)min((int64_t)heads, h0 + (end - at));
+    at += h1 - h0;
+    const Slot<P> s = make_slot<P>(p, group, sub, l, -1.f);
+    if (!s.live) ring.clear();
+    auto fetch = [&](int h) {
+      if (s.live && h < h1) {
+        const E* row = head_row<const E>(p, p.in, s.b, s.t, h);
+        ring.fetch(h, 0, row + c0);
+        ring.fetch(h, 1, row + c1);
+        if constexpr (NORM)
+          if (h < p.Hq + p.Hkv) {
+            const E* x = head_row<const E>(p, p.x, s.b, s.from, h);
+            ring.fetch(h, 2, x + c0);
+            ring.fetch(h, 3, x + c1);
           }
+      }
+      ring.commit();
+    };
+#pragma unroll
+    for (int u = 0; u < R::K; ++u) fetch(h0 + u);
+    auto tensor = [&](int lo, int hi, auto move, int j) {
+      constexpr bool N = NORM && !decltype(move)::value;
+      if (lo >= hi) return;
+      float wa[P], wb[P], da[P], db[P];
+      if constexpr (N) {
+        load_weights<NEAR, E, P>(p, p.w[j], c0, c1, wa, wb);
+#pragma unroll
+        for (int i = 0; i < P; ++i) da[i] = db[i] = 0.f;
+      }
+      for (int h = lo; h < hi; ++h) {
+        ring.wait();
+        float a[P], b[P], xa[P], xb[P];
+        to_pairs<NEAR>(ring.get(h, 0), ring.get(h, 1), a, b);
+        if constexpr (N) to_pairs<NEAR>(ring.get(h, 2), ring.get(h, 3), xa, xb);
+        fetch(h + R::K);
+        if constexpr (!decltype(move)::value) turn(s, a, b);
+        if constexpr (N) {
+          float2 sum = make_float2(0.f, 0.f), dot = sum;
+#pragma unroll
+          for (int i = 0; i < P; i += 2) {
+            const float2 x = two(xa, i), y = two(xb, i);
+            sum = fma2(x, x, fma2(y, y, sum));
+            dot = fma2(mul2(two(a, i), two(wa, i)), x, fma2(mul2(two(b, i), two(wb, i)), y, dot));
+          }
+          // with r = 1 / sqrt(..): dw += g (r x),  dx = r w g - x (r^3 mean(w g x))
+          const float rs = rsqrtf(row_sum(sum.x + sum.y, p.lanes) * p.inv_d + p.eps);
+          const float m = -row_sum(dot.x + dot.y, p.lanes) * p.inv_d * rs * rs;
+          const float2 rs2 = make_float2(rs, rs), m2 = make_float2(m, m);
+#pragma unroll
+          for (int i = 0; i < P; i += 2) {
+            const float2 x = mul2(two(xa, i), rs2), y = mul2(two(xb, i), rs2);
+            const float2 ga = two(a, i), gb = two(b, i);
+            put(da, i, fma2(ga, x, two(da, i)));
+            put(db, i, fma2(gb, y, two(db, i)));
+            put(a, i, fma2(mul2(ga, two(wa, i)), rs2, mul2(x, m2)));
+            put(b, i, fma2(mul2(gb, two(wb, i)), rs2, mul2(y, m2)));
+          }
+        }
+        if (s.live) store_pairs<NEAR>(head_row<E>(p, p.out, s.b, s.from, h), c0, c1, a, b);
+      }
+      if constexpr (N) {
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+          float4* const at = mine + (j * kQuads + i) * kThreads;
+          const float* d = i < P / 4 ? da + 4 * i : db + 4 * i - P;
+          float4 v = *at;
+          v.x += d[0], v.y += d[1], v.z += d[2], v.w += d[3];
+          *at = v;
         }
       }
-#pragma unroll
-      for (int u = 0; u < kBwdRows; ++u) {
-        float ga[4], gb[4];
-        to_pairs<NEAR>(gx[u], gy[u], ga, gb);
-        if (kind[u] == 0 || kind[u] == 1) {
-          const float4* cs = reinterpret_cast<const float4*>(&s.cs[tt[u]][4 * l]);
-          const float4 t01 = cs[0], t23 = cs[1];
-          const float co[4] = {t01.x, t01.z, t23.x, t23.z}, si[4] = {t01.y, t01.w, t23.y, t23.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float y0 = ga[i] * co[i] - gb[i] * si[i];
-            gb[i] = ga[i] * si[i] + gb[i] * co[i];
-            ga[i] = y0;
-          }
-        }
-        if (NORM) {
-          float xa[4], xb[4], sum = 0.f, dot = 0.f;
-          to_pairs<NEAR>(x[u], y[u], xa, xb);
-          const bool k = kind[u] == 1;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], sum));
-          const float rs = rsqrtf(row_sum(sum, p.lanes) * p.inv_d + p.eps);
-          float na[4], nb[4], ha[4], hb[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            na[i] = xa[i] * rs;
-            nb[i] = xb[i] * rs;
-            ha[i] = ga[i] * (k ? wa[1][i] : wa[0][i]);
-            hb[i] = gb[i] * (k ? wb[1][i] : wb[0][i]);
-            dot = fmaf(ha[i], na[i], fmaf(hb[i], nb[i], dot));
-          }
-          dot = row_sum(dot, p.lanes) * p.inv_d;
-          if (kind[u] == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) da[0][i] += ga[i] * na[i], db[0][i] += gb[i] * nb[i];
-          } else if (kind[u] == 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) da[1][i] += ga[i] * na[i], db[1][i] += gb[i] * nb[i];
-          }
-          if (kind[u] == 0 || kind[u] == 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              ga[i] = rs * (ha[i] - na[i] * dot);
-              gb[i] = rs * (hb[i] - nb[i] * dot);
-            }
-          }
-        }
-        if (kind[u] < 0) continue;
-        E* out = row_ptr<E>(p.out[kind[u]], b, hh[u], s.from[tt[u]]);
-        store_pairs<NEAR>(out, c0, c1, ga, gb);
-      }
-    }
+    };
+    tensor(h0, min(h1, p.Hq), std::false_type{}, 0);
+    tensor(max(h0, p.Hq), min(h1, p.Hq + p.Hkv), std::false_type{}, 1);
+    tensor(max(h0, p.Hq + p.Hkv), h1, std::true_type{}, 2);
   }
   if constexpr (NORM) {
-    // the lanes of a warp that hold the same channels, then the warps in order
-    __shared__ float part[kWarps][2][128];
+    // the lanes of a warp that hold the same channels, then the warps in order; the ring is done
+    griddep_launch_dependents();
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    float* part = reinterpret_cast<float*>(smem);  // [warp][2][D]
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float v = i < 4 ? da[j][i & 3] : db[j][i & 3];
-        for (int o = p.lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        const int c = NEAR ? (i < 4 ? 8 * l + 2 * i : 8 * l + 2 * (i - 4) + 1)
-                           : (i < 4 ? c0 + i : c1 + i - 4);
-        if (sub == 0 && live) part[warp][j][c] = v;
+      for (int q = 0; q < kQuads; ++q) {
+        const float4 d = mine[(j * kQuads + q) * kThreads];
+        const float x[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = 4 * q + k;
+          float v = x[k];
+          for (int o = p.lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          const int c = NEAR ? c0 + 2 * (i % P) + (i >= P) : i < P ? c0 + i : c1 + i - P;
+          if (sub == 0 && c < p.D) part[(warp * 2 + j) * p.D + c] = v;
+        }
       }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * p.D; i += kThreads) {
-      const int j = i / p.D, c = i - j * p.D;
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += part[w][j][c];
+      for (int w = 0; w < kWarps; ++w) v += part[w * 2 * p.D + i];
       p.sums[(int64_t)blockIdx.x * 2 * p.D + i] = v;
     }
   }
 }
 
-// dw[j][c] = the sum of n rows of 2 D numbers; a block takes 32 columns, its warps every 32nd
-// row, then the warps in order.
+// dw[j][c] = the sum of n rows of 2 D numbers.  A block takes eight columns, a thread every 128th
+// row of one, then a warp its threads of a column and the first warp the warps, in order.
 __global__ void __launch_bounds__(1024) sum_kernel(const float* sums, int n, int D, float* dq,
                                                    float* dk) {
-  __shared__ float part[32][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  __shared__ float part[32][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 8 + (lane & 7);
   float v = 0.f;
-  if (c < 2 * D)
-    for (int r = warp; r < n; r += 32) v += sums[(int64_t)r * 2 * D + c];
-  part[warp][lane] = v;
+  griddep_wait();
+#pragma unroll 4
+  for (int r = threadIdx.x >> 3; r < n; r += 128) v += sums[(int64_t)r * 2 * D + c];
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  v += __shfl_xor_sync(0xffffffffu, v, 16);
+  if (lane < 8) part[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && c < 2 * D) {
+  if (threadIdx.x < 8) {
     v = 0.f;
 #pragma unroll
     for (int w = 0; w < 32; ++w) v += part[w][lane];
@@ -390,36 +481,55 @@ __global__ void __launch_bounds__(1024) sum_kernel(const float* sums, int n, int
   }
 }
 
-template <typename E, bool NEAR>
-static void launch_fwd(const Rotate& p, dim3 grid, cudaStream_t st) {
-  if (p.norm) fwd_kernel<E, NEAR, true><<<grid, kThreads, 0, st>>>(p);
-  else fwd_kernel<E, NEAR, false><<<grid, kThreads, 0, st>>>(p);
+template <typename K>
+static cudaError_t launch_kernel(K kern, const Rotate& p, int grid, int bytes, cudaStream_t st) {
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<grid, kThreads, bytes, st>>>(p);
+  return cudaGetLastError();
+}
+template <typename E, bool NEAR, bool NORM, int P>
+static cudaError_t launch_one(const Rotate& p, int grid, bool backward, cudaStream_t st) {
+  // (the ring's space, at least 16 KB with the norm, later takes 8 KB of sums)
+  constexpr int V = NORM ? 4 : 2, kSums = NORM ? 2 * 2 * P * kThreads * 4 : 0;
+  return backward ? launch_kernel(bwd_kernel<E, NEAR, NORM, P>, p, grid, kWarps * Ring<E, P, V>::kWarpBytes + kSums, st)
+                  : launch_kernel(fwd_kernel<E, NEAR, NORM, P>, p, grid, kWarps * Ring<E, P, 2>::kWarpBytes, st);
 }
 template <typename E, bool NEAR>
-static void launch_bwd(const Rotate& p, int grid, cudaStream_t st) {
-  if (p.norm) bwd_kernel<E, NEAR, true><<<grid, kThreads, 0, st>>>(p);
-  else bwd_kernel<E, NEAR, false><<<grid, kThreads, 0, st>>>(p);
+static cudaError_t launch_pairs(const Rotate& p, int grid, bool backward, cudaStream_t st) {
+  if constexpr (sizeof(E) == 2)
+    if (p.P == 8) return p.norm ? launch_one<E, NEAR, true, 8>(p, grid, backward, st) : launch_one<E, NEAR, false, 8>(p, grid, backward, st);
+  return p.norm ? launch_one<E, NEAR, true, 4>(p, grid, backward, st) : launch_one<E, NEAR, false, 4>(p, grid, backward, st);
+}
+static cudaError_t launch(const Rotate& p, int grid, bool backward, cudaStream_t st) {
+  timing_begin(backward ? "rotate_bwd" : "rotate_fwd", st);
+  const cudaError_t e = p.bf16 ? p.near ? launch_pairs<__nv_bfloat16, true>(p, grid, backward, st)
+                                        : launch_pairs<__nv_bfloat16, false>(p, grid, backward, st)
+                        : p.near ? launch_pairs<float, true>(p, grid, backward, st)
+                                 : launch_pairs<float, false>(p, grid, backward, st);
+  timing_end(st);
+  return e;
 }
 
-// Slots a block takes, and parts that the heads are cut into: 16 slots share what a block does
-// once, but a decoding step's few tokens want every SM.
-static void cut(Rotate* p) {
-  p->lanes = 1;
-  while (p->lanes * 8 < p->D) p->lanes *= 2;
-  p->inv_d = 1.f / p->D;
-  const int64_t tokens = (int64_t)p->B * p->T;
-  p->tile = kMaxTile;
-  while (p->tile > 1 && (tokens + p->tile - 1) / p->tile < 2 * kSms) p->tile /= 2;
-  p->tile_log2 = 0;
-  while ((1 << p->tile_log2) < p->tile) ++p->tile_log2;
+// Pairs a lane, groups of slots, and parts that the heads are cut into: one part shares a slot's
+// angles among all its heads, but a decoding step's few tokens want every SM, down to a head a
+// warp.  There eight pairs a lane would mean eight angles one after the other: 5.0 us against 4.3
+// with four (64 tokens of 40 heads).
+static int cut(Rotate* p) {
   const int heads = p->Hq + p->Hkv + (p->in[2].p ? p->Hkv : 0);
-  const int64_t blocks = (int64_t)p->B * ((p->T + p->tile - 1) / p->tile);
-  const int rows_pass = kWarps * (32 / p->lanes);
-  int64_t splits = blocks < 2 * kSms ? (2 * kSms + blocks - 1) / blocks : 1;
-  const int64_t most = ((int64_t)heads * p->tile + rows_pass - 1) / rows_pass;
-  if (splits > most) splits = most;
+  const int64_t want = (int64_t)kSms * 64;  // warps
+  p->P = p->bf16 && p->D % 16 == 0 && p->rot % 16 == 0 && (int64_t)p->B * p->T * heads > 4 * want ? 8 : 4;
+  p->lanes = 1;
+  while (p->lanes * 2 * p->P < p->D) p->lanes *= 2;
+  p->inv_d = 1.f / p->D;
+  const int per = 32 / p->lanes;
+  p->groups = (p->B * p->T + per - 1) / per;
+  int64_t splits = (want + p->groups - 1) / p->groups;
   if (splits > heads) splits = heads;
   p->splits = (int)splits;
+  return (int)(((int64_t)p->groups * splits + kWarps - 1) / kWarps);  // blocks
 }
 
 }  // namespace rotate
@@ -431,40 +541,27 @@ size_t rotate_bwd_workspace(int D, int norm) {
 }
 
 cudaError_t launch_rotate_fwd(Rotate p, cudaStream_t st) {
-  cut(&p);
-  const int64_t blocks = (int64_t)p.B * ((p.T + p.tile - 1) / p.tile);
-  const dim3 grid((unsigned)blocks, (unsigned)p.splits);
-  timing_begin("rotate_fwd", st);
-  if (p.bf16) {
-    if (p.near) launch_fwd<__nv_bfloat16, true>(p, grid, st);
-    else launch_fwd<__nv_bfloat16, false>(p, grid, st);
-  } else {
-    if (p.near) launch_fwd<float, true>(p, grid, st);
-    else launch_fwd<float, false>(p, grid, st);
-  }
-  const cudaError_t e = cudaGetLastError();
-  timing_end(st);
-  return e;
+  const int grid = cut(&p);
+  return launch(p, grid, false, st);
 }
 
 cudaError_t launch_rotate_bwd(Rotate p, float* dqw, float* dkw, cudaStream_t st) {
-  cut(&p);
-  const int64_t items = (int64_t)p.B * ((p.T + p.tile - 1) / p.tile) * p.splits;
-  const int grid = (int)(items < kBwdBlocks ? items : kBwdBlocks);
-  timing_begin("rotate_bwd", st);
-  if (p.bf16) {
-    if (p.near) launch_bwd<__nv_bfloat16, true>(p, grid, st);
-    else launch_bwd<__nv_bfloat16, false>(p, grid, st);
-  } else {
-    if (p.near) launch_bwd<float, true>(p, grid, st);
-    else launch_bwd<float, false>(p, grid, st);
-  }
-  cudaError_t e = cudaGetLastError();
-  timing_end(st);
+  // two blocks an SM, but no more warps than there are heads of groups
+  const int blocks = cut(&p), grid = blocks < kBwdBlocks ? blocks : kBwdBlocks;
+  cudaError_t e = launch(p, grid, true, st);
   if (e != cudaSuccess || !p.norm || (!dqw && !dkw)) return e;
   timing_begin("rotate_bwd_sum", st);
-  sum_kernel<<<(2 * p.D + 31) / 32, 1024, 0, st>>>(p.sums, grid, p.D, dqw, dkw);
-  e = cudaGetLastError();
+  // (started while the blocks before it finish; it waits for them before it reads)
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * p.D / 8);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, sum_kernel, (const float*)p.sums, grid, p.D, dqw, dkw);
   timing_end(st);
   return e;
 }
