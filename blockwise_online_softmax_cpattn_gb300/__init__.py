@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -459,36 +460,35 @@ def cpattn_cache_attn(desc, n_req, max_pages, n_tokens, max_q, q, q_start, kv_le
         _ws_bytes(workspace, ws_bytes), _stream(stream))
 
 
-_strides3 = ctypes.c_int64 * 3
+_pack3 = struct.Struct("3q").pack
 
 
-def _view(x, heads, desc, here, what):
-    """(pointer, strides) of a [B, heads, T, D] tensor of desc.dtype with contiguous channels;
-    a raw pointer stands for a contiguous one."""
+def _view(x, shape, dtype, here, what):
+    """(pointer, strides) of a tensor of this shape [B, heads, T, D] and type with contiguous
+    channels; a raw pointer stands for a contiguous one.  (The strides go as the bytes of three
+    numbers: an array of ctypes' own costs several times as much.)"""
     if x is None or type(x) is int:
         return x, None
-    shape, stride = x.shape, x.stride()
-    if (x.dtype is not _dtype(desc.dtype) or shape != (desc.B, heads, desc.T, desc.D) or
-            stride[3] != 1):
-        raise ValueError(f"{what} must be [B, heads, T, D] of the descriptor's dtype with "
-                         "contiguous channels")
-    _on(x, here, what)
-    return x.data_ptr(), _strides3(stride[0], stride[1], stride[2])
+    sb, sh, st, sc = x.stride() if x.dim() == 4 else (0, 0, 0, 0)
+    if x.dtype is not dtype or x.shape != shape or (sc != 1 and shape[3] > 1):
+        raise ValueError(f"{what} must be {list(shape)} of {dtype} with contiguous channels")
+    if x.get_device() != here:
+        raise ValueError(f"{what} is not on the current device")
+    return x.data_ptr(), _pack3(sb, sh, st)
 
 
 def cpattn_rotate_fwd(desc, q, k, v, q_weight, k_weight, inv_freq, positions, q_out, k_out, v_out,
                       stream=None) -> int:
     """Norm of each head, rotation by position and the move into the attention's token order, of
     [B, H, T, D] tensors by any strides; v and v_out, the weights and positions may be None."""
-    here, D = _here(), desc.D
+    here, B, T, D, t = _here(), desc.B, desc.T, desc.D, desc.dtype
+    dt, sq, sk = _dtype(t), (B, desc.H_q, T, D), (B, desc.H_kv, T, D)
     return _lib.cpattn_rotate_fwd(
-        ctypes.byref(desc), *_view(q, desc.H_q, desc, here, "q"), *_view(k, desc.H_kv, desc, here, "k"),
-        *_view(v, desc.H_kv, desc, here, "v"), _typed(q_weight, D, desc.dtype, here, "q_weight"),
-        _typed(k_weight, D, desc.dtype, here, "k_weight"),
-        _typed(inv_freq, desc.rot // 2, "f64", here, "inv_freq"),
-        _typed(positions, desc.B * desc.T, "i32", here, "positions"),
-        *_view(q_out, desc.H_q, desc, here, "q_out"), *_view(k_out, desc.H_kv, desc, here, "k_out"),
-        *_view(v_out, desc.H_kv, desc, here, "v_out"), _stream(stream))
+        ctypes.byref(desc), *_view(q, sq, dt, here, "q"), *_view(k, sk, dt, here, "k"),
+        *_view(v, sk, dt, here, "v"), _typed(q_weight, D, t, here, "q_weight"),
+        _typed(k_weight, D, t, here, "k_weight"), _typed(inv_freq, desc.rot // 2, "f64", here, "inv_freq"),
+        _typed(positions, B * T, "i32", here, "positions"), *_view(q_out, sq, dt, here, "q_out"),
+        *_view(k_out, sk, dt, here, "k_out"), *_view(v_out, sk, dt, here, "v_out"), _stream(stream))
 
 
 def cpattn_rotate_bwd_workspace(desc) -> int:
@@ -498,15 +498,15 @@ def cpattn_rotate_bwd_workspace(desc) -> int:
 def cpattn_rotate_bwd(desc, q, k, q_weight, k_weight, inv_freq, positions, dq_out, dk_out, dv_out, dq,
                       dk, dv, dq_weight, dk_weight, workspace, ws_bytes=None, stream=None) -> int:
     """Gradients of cpattn_rotate_fwd's inputs and weights (float32 sums)."""
-    here, D = _here(), desc.D
+    here, B, T, D, t = _here(), desc.B, desc.T, desc.D, desc.dtype
+    dt, sq, sk = _dtype(t), (B, desc.H_q, T, D), (B, desc.H_kv, T, D)
     return _lib.cpattn_rotate_bwd(
-        ctypes.byref(desc), *_view(q, desc.H_q, desc, here, "q"), *_view(k, desc.H_kv, desc, here, "k"),
-        _typed(q_weight, D, desc.dtype, here, "q_weight"), _typed(k_weight, D, desc.dtype, here, "k_weight"),
+        ctypes.byref(desc), *_view(q, sq, dt, here, "q"), *_view(k, sk, dt, here, "k"),
+        _typed(q_weight, D, t, here, "q_weight"), _typed(k_weight, D, t, here, "k_weight"),
         _typed(inv_freq, desc.rot // 2, "f64", here, "inv_freq"),
-        _typed(positions, desc.B * desc.T, "i32", here, "positions"),
-        *_view(dq_out, desc.H_q, desc, here, "dq_out"), *_view(dk_out, desc.H_kv, desc, here, "dk_out"),
-        *_view(dv_out, desc.H_kv, desc, here, "dv_out"), *_view(dq, desc.H_q, desc, here, "dq"),
-        *_view(dk, desc.H_kv, desc, here, "dk"), *_view(dv, desc.H_kv, desc, here, "dv"),
+        _typed(positions, B * T, "i32", here, "positions"), *_view(dq_out, sq, dt, here, "dq_out"),
+        *_view(dk_out, sk, dt, here, "dk_out"), *_view(dv_out, sk, dt, here, "dv_out"),
+        *_view(dq, sq, dt, here, "dq"), *_view(dk, sk, dt, here, "dk"), *_view(dv, sk, dt, here, "dv"),
         _typed(dq_weight, D, F32, here, "dq_weight"), _typed(dk_weight, D, F32, here, "dk_weight"),
         _bytes(workspace, 0, here, "workspace"), _ws_bytes(workspace, ws_bytes), _stream(stream))
 

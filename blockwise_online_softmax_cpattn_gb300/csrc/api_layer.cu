@@ -77,7 +77,7 @@ static cpattn_status validate_linear(const cpattn_desc* d, Ring* R) {
   const cpattn_status s = validate_ring(d, R);
   if (s != CPATTN_OK) return s;
   if (d->D % 8) return CPATTN_ERR_UNSUPPORTED;
-  // heads times the runs of a sequence (64 at most) are blocks of one launch
+  // heads times the runs of a sequence (64 at most) are the blocks of one launch
   if ((int64_t)R->B * R->Hq > INT_MAX / 64) return CPATTN_ERR_UNSUPPORTED;
   return CPATTN_OK;
 }
@@ -262,6 +262,7 @@ cpattn_status cpattn_linear_fwd(const cpattn_desc* desc, const void* q, const vo
   f.mul = R.scale;
   f.out = o;
   f.fin = state_out, f.fin_mul = 1.f;
+  f.exact = state_out != nullptr;
   p.sum[0] = f;
   return from_cuda(tc ? launch_linear_tc(p, st, false) : launch_linear_simt(p, st, false));
 }
@@ -321,12 +322,14 @@ cpattn_status cpattn_linear_bwd(const cpattn_desc* desc, const void* q, const vo
   fv.out = rep > 1 ? part_v : dv;
   fv.out_f32 = rep > 1;
   fv.fin = dstate_in, fv.fin_mul = R.scale;
+  fv.exact = dstate_in != nullptr;
   LinSweep& fk = p.sweep[2];
   fk = fv;
   fk.a = v, fk.b = dO, fk.c = q;
   fk.trans = 1;
   fk.out = rep > 1 ? part_k : dk;
   fk.fin = nullptr;
+  fk.exact = 0;
   p.sum[0].b = k, p.sum[0].c = v;
   p.sum[0].rep_a = p.sum[0].rep_b = p.sum[0].rep_c = rep;
   p.sum[0].sums = sums_s;

@@ -72,6 +72,7 @@ struct LinSweep {
   int out_f32;
   float* fin;  // M behind the last run, times fin_mul, or null
   float fin_mul;
+  int exact;   // M is handed out in the end: products on bf16 pairs
 };
 
 constexpr int kMaxSweeps = 3;

@@ -6,28 +6,34 @@
 //   O1 = P c             (TS)
 //   O2 = a M             (SS)  M: what went before, as bf16 in shared memory
 //   out_i = mul (O1_i + w(i + 1) O2_i)
-//   U = b^T (w(n - 1 - j) c_j)   (SS, b and c both transposed by their descriptors)
+//   U = (w(n - 1 - j) b_j)^T c   (SS, both transposed by their descriptors)
 //   M = w(n) M + U
 //
-// M itself stays in float32, in the registers of one warpgroup (thread r holds row r: one
-// channel of b), and what a chunk adds to it comes from a product whose operand carries 16 bits:
-// the weighted c is split into two bf16 numbers, hi + lo, and U is the sum of two products.  A
-// single bf16 rounding there would leave 2^-9 in every state that is handed out in float32.
-// As operands of O1 and O2, P and M are rounded to bf16 once: like the output's own rounding.
+// M itself stays in float32, in registers (two threads a row, one channel of b).  b is weighted in
+// its place in shared memory once S has read it.  As operands P, M and the weighted b are rounded
+// to bf16 once, like the output itself.  Where a state is handed out (`exact`), the weighted b is
+// taken as two bf16 numbers, hi + lo, and U as the sum of two products: a single rounding would
+// leave 2^-9 in a float32 result.  U starts from zero in every chunk, so no sum on the tensor
+// cores runs longer than 256 terms.
 //
-// Warp roles (384 threads):
-//   warp 0       TMA producer: the tiles a, b, c of a chunk
-//   warp 1       issues S;  warp 2: O1 and O2;  warp 3: U
-//   warps 4-7    the rows of the output: S -> P, then the epilogue.  The output tile is staged
-//                in the chunk's own a tile, which nothing reads any more, and leaves by TMA
-//   warps 8-11   the state: weighted c (hi, then lo) into shared memory, M, its bf16 copy
+// Warp roles (512 threads):
+//   warp 0        TMA producer: the tiles a, b, c of a chunk, two stages each
+//   warp 1        issues S;  warp 2: O2 and O1;  warp 3: U
+//   warps 4-7     the rows of the output: S -> P, then the epilogue.  The output tile is staged
+//                 in the chunk's own a tile, which nothing reads any more, and leaves by TMA
+//   warps 8-15    the state: b times its weights, M, its bf16 copy
 // Issuers are whole warps with one elected lane, as in tc_fwd.cu.  TMEM: S/P [0, 128),
 // O1, O2 and U of D columns each behind it.
 //
-// The first launch (SUM) only needs U and M: 256 threads, no a.
+// The first launch (SUM) only needs U and M: no a, 384 threads; M takes a chunk's U while the next
+// one's product runs.
 //
-// Bound by memory: 1 KB a token and head at D 128 (four tiles of 32 KB a chunk, 5600 cycles of an
-// SM's share of the bandwidth) against 2600 cycles of MMAs.
+// Bound by shared memory and by memory, close together: a chunk at D 128 moves 128 KB from and to
+// memory (5600 cycles of an SM's share) and 540 KB through shared memory (4250 cycles at 128 bytes:
+// an SS product reads both its operands there).  That is why a block takes all of a head's
+// channels: in two halves S and the reads of a and b came twice, 960 KB.
+//
+// A barrier that a role may leave behind by a phase comes as a pair, by the chunk's parity.
 // Every mbarrier wait is bounded, as in tc_fwd.cu.
 #include "layer.cuh"
 
@@ -38,23 +44,24 @@ constexpr int kTile = kLinTcChunk;
 constexpr uint64_t kTimeoutNs = 2000000000ull;     // 2 s
 constexpr uint64_t kDebugTimeoutNs = 50000000ull;  // 50 ms under the fault hook
 constexpr uint64_t kDrainTimeoutNs = 200000000ull;
+constexpr int kThreadsOut = 512, kThreadsSum = 384;
+// registers of the warpgroups of the second launch: one of control, three of arithmetic
+constexpr int kRegsOut = 144;
+static_assert(128 * kRegsCtl + 384 * kRegsOut <= 65536, "");
 
 template <int D, bool SUM>
 struct Smem {
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kAS = SUM ? 0 : 2;                          // stages of a, b and c
-  static constexpr int kBS = SUM && D == 64 ? 4 : 2;
-  static constexpr int kCS = SUM ? (D == 64 ? 4 : 2) : D == 128 ? 1 : 2;
-  static constexpr int kXS = SUM || D == 64 ? 2 : 1;               // weighted c
+  static constexpr int kAS = SUM ? 0 : D == 128 ? 2 : 3;  // stages of a; of b and c
+  static constexpr int kBS = SUM ? (D == 128 ? 3 : 6) : kAS;
   static constexpr int kA = 0;
   static constexpr int kB = kA + kAS * kTileBytes;
   static constexpr int kC = kB + kBS * kTileBytes;
-  static constexpr int kX = kC + kCS * kTileBytes;
-  static constexpr int kM = kX + kXS * kTileBytes;
+  static constexpr int kM = kC + kBS * kTileBytes;
   static constexpr int kPow = kM + (SUM ? 0 : D * D * 2);
-  // powers r^e at kPow + 4 (128 + e), zeros for e < 0
-  static constexpr int kBar = kPow + 4 * 264;
-  static constexpr int kNumBars = 2 * (kAS + kBS + kCS + kXS) + 7 + 3;
+  // powers r^e at kPow + 4 (128 + e), zeros for e < 0; then r^31 .. r^0
+  static constexpr int kBar = kPow + 4 * (264 + 32);
+  static constexpr int kNumBars = 2 * (kAS + 2 * kBS) + 13 + 3;
   static constexpr int kMisc = kBar + 8 * kNumBars;
   static constexpr int kBytes = kMisc + 16;
 };
@@ -83,10 +90,11 @@ __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 template <int D, bool SUM>
-__global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_constant__ Params prm) {
+__global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
+    sweep_kernel(const __grid_constant__ Params prm) {
   using L = Smem<D, SUM>;
-  constexpr int AS = L::kAS, BS = L::kBS, CS = L::kCS, XS = L::kXS;
-  constexpr uint32_t kTmemCols = SUM ? 128 : 512;
+  constexpr int AS = L::kAS, BS = L::kBS;
+  constexpr uint32_t kTmemCols = SUM ? 2 * D : 512;
   const Linear& p = prm.p;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the layout has no alignment slack
@@ -100,12 +108,13 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
   auto b_full = [&](int s) { return bars + 8 * (2 * AS + s); };
   auto b_empty = [&](int s) { return bars + 8 * (2 * AS + BS + s); };
   auto c_full = [&](int s) { return bars + 8 * (2 * AS + 2 * BS + s); };
-  auto c_empty = [&](int s) { return bars + 8 * (2 * AS + 2 * BS + CS + s); };
-  auto x_full = [&](int s) { return bars + 8 * (2 * AS + 2 * BS + 2 * CS + s); };
-  auto x_empty = [&](int s) { return bars + 8 * (2 * AS + 2 * BS + 2 * CS + XS + s); };
-  const uint32_t one = bars + 8 * 2 * (AS + BS + CS + XS);
-  const uint32_t c_ready = one, s_full = one + 8, p_full = one + 16, o_full = one + 24,
-                 o_free = one + 32, m_full = one + 40, u_full = one + 48, fin = one + 56;
+  auto c_empty = [&](int s) { return bars + 8 * (2 * AS + 3 * BS + s); };
+  const uint32_t one = bars + 8 * 2 * (AS + 2 * BS);
+  auto s_full = [&](int i) { return one + 8 * (i & 1); };        // pairs
+  auto x_full = [&](int k) { return one + 8 * (2 + (k & 1)); };  // b weighted, the k-th time
+  auto u_full = [&](int i) { return one + 8 * (4 + (i & 1)); };
+  const uint32_t p_full = one + 48, o_full = one + 56, o_free = one + 64, m_full = one + 72,
+                 m_free = one + 80, h_done = one + 88, fixed = one + 96, fin = one + 104;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   float* pw = reinterpret_cast<float*>(smem + L::kPow) + 128;
@@ -121,6 +130,7 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
   const int n_tok = lin_tokens(p, bh);
   const float ld = lin_decay(p, bh);
   const int back = w.back, late = back;
+  const bool exact = w.exact;
   const int bb = bh / p.Hq, h = bh - bb * p.Hq;
   const int head_a = bb * (p.Hq / w.rep_a) + h / w.rep_a;
   const int head_b = bb * (p.Hq / w.rep_b) + h / w.rep_b;
@@ -135,16 +145,14 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) mbar_init(bars + 8 * i, 1);
-    // 128 threads of a warpgroup; a_empty: its four warps; b_empty: S and U; c_empty: O1 and
-    // the four warps that weight c
+    // a_empty: the four warps that store the output; c_empty: O1 and U; the rest by threads
     for (int i = 0; i < AS; ++i) mbar_init(a_empty(i), 4);
-    for (int i = 0; i < BS; ++i) mbar_init(b_empty(i), SUM ? 1 : 2);
-    for (int i = 0; i < CS; ++i) mbar_init(c_empty(i), SUM ? 4 : 5);
-    for (int i = 0; i < XS; ++i) mbar_init(x_full(i), 128);
-    mbar_init(c_ready, 128);
+    for (int i = 0; i < BS; ++i) mbar_init(c_empty(i), SUM ? 1 : 2);
+    for (int i = 0; i < 2; ++i) mbar_init(x_full(i), 256);
     mbar_init(p_full, 128);
     mbar_init(o_free, 128);
-    mbar_init(m_full, 128);
+    mbar_init(m_full, 256);
+    mbar_init(fixed, 256);
     *abort = 0;
     fence_barrier_init();
   }
@@ -152,12 +160,14 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  for (int i = threadIdx.x; i < 264; i += blockDim.x) pw[i - 128] = i < 128 ? 0.f : lin_pow(ld, i - 128);
+  for (int i = threadIdx.x; i < 264 + 32; i += blockDim.x)
+    pw[i - 128] = i < 128 ? 0.f : i < 264 ? lin_pow(ld, i - 128) : lin_pow(ld, 31 - (i - 264));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS = tmem, tO1 = tmem + 128, tO2 = tmem + 128 + D, tU = SUM ? tmem : tmem + 128 + 2 * D;
+  const uint32_t tS = tmem, tO1 = tmem + 128, tO2 = tmem + 128 + D;
+  auto tU = [&](int i) { return SUM ? tmem + (i & 1) * D : tmem + 128 + 2 * D; };
 
   if (warp < 4) {
     if constexpr (!SUM) regs_ctl();
@@ -165,8 +175,7 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
       // ---------------------------------------------------------- producer
       if (lane == 0) {
         StageRing<AS == 0 ? 1 : AS> ra;
-        StageRing<BS> rb;
-        StageRing<CS> rc;
+        StageRing<BS> rb, rc;
         bool ok = true;
         for (int i = 0; i < n_chunks && ok; ++i) {
           const int slot = p.m.slot(chunk_pos(i));
@@ -182,17 +191,17 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
             ring.mark_issued();
             ring.advance();
           };
-          if (!SUM) load(ra, a_full(ra.stage), a_empty(ra.stage), L::kA, &maps.a, head_a, p.B * (p.Hq / w.rep_a));
           load(rb, b_full(rb.stage), b_empty(rb.stage), L::kB, &maps.b, head_b, p.B * (p.Hq / w.rep_b));
+          if (!SUM) load(ra, a_full(ra.stage), a_empty(ra.stage), L::kA, &maps.a, head_a, p.B * (p.Hq / w.rep_a));
           load(rc, c_full(rc.stage), c_empty(rc.stage), L::kC, &maps.c, head_c, p.B * (p.Hq / w.rep_c));
         }
         // never leave with a copy still writing into this block's shared memory
         for (int s = 0; s < AS; ++s)
           if (ra.was_issued(s)) drain_wait(a_full(s), ra.issued_parity(s));
-        for (int s = 0; s < BS; ++s)
+        for (int s = 0; s < BS; ++s) {
           if (rb.was_issued(s)) drain_wait(b_full(s), rb.issued_parity(s));
-        for (int s = 0; s < CS; ++s)
           if (rc.was_issued(s)) drain_wait(c_full(s), rc.issued_parity(s));
+        }
       }
     } else if (warp == 1) {
       if constexpr (!SUM) {
@@ -201,29 +210,24 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
         constexpr uint32_t kId = idesc_bf16(128, 128, false, false);
         const uint64_t ad0 = sdesc_sw128(sbase + L::kA, 16, 1024), bd0 = sdesc_sw128(sbase + L::kB, 16, 1024);
         StageRing<AS> ra;
-        StageRing<BS> rb;
         for (int i = 0; i < n_chunks; ++i) {
           if (!warp_wait(a_full(ra.stage), ra.par, abort, p.status, tmo) ||
-              !warp_wait(b_full(rb.stage), rb.par, abort, p.status, tmo))
+              !warp_wait(b_full(ra.stage), ra.par, abort, p.status, tmo))
             break;
-          // S's buffer is free once O1 of the last chunk has read P there
+          // S's place is free once O1 of the last chunk has read P there
           if (i > 0 && !warp_wait(o_full, (i - 1) & 1, abort, p.status, tmo)) break;
-          // a partial chunk's rows of b behind its end are zeroed first
-          if (chunk_n(i) < kTile && !warp_wait(c_ready, i & 1, abort, p.status, tmo)) break;
+          // a partial chunk's rows of b and c behind its end are zeroed first
+          if (chunk_n(i) < kTile && !warp_wait(fixed, 0, abort, p.status, tmo)) break;
           tc_fence_after();
-          const uint64_t ad = ad0 + ra.stage * (L::kTileBytes >> 4), bd = bd0 + rb.stage * (L::kTileBytes >> 4);
+          const uint32_t st = ra.stage * (L::kTileBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;  // 16 KiB blocks, 32 B steps
-            if (leader) mma_ss(tS, ad + off, bd + off, kId, kk > 0);
+            const uint32_t off = st + (kk >> 2) * 1024 + (kk & 3) * 2;  // 16 KiB blocks, 32 B steps
+            if (leader) mma_ss(tS, ad0 + off, bd0 + off, kId, kk > 0);
           }
-          if (leader) {
-            mma_commit(s_full);
-            mma_commit(b_empty(rb.stage));
-          }
+          if (leader) mma_commit(s_full(i));
           __syncwarp();
           ra.advance();
-          rb.advance();
         }
         if (leader) mma_commit(fin);
         __syncwarp();
@@ -231,76 +235,75 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
       }
     } else if (warp == 2) {
       if constexpr (!SUM) {
-        // ----------------------------------------- O1 = P c, O2 = a M
+        // ----------------------------------------- O2 = a M, O1 = P c
         const bool leader = elect_one();
         constexpr uint32_t kId = idesc_bf16(128, D, false, true);
         const uint64_t cd0 = sdesc_sw128(sbase + L::kC, kTile * 128, 1024);
         const uint64_t ad0 = sdesc_sw128(sbase + L::kA, 16, 1024);
         const uint64_t md = sdesc_sw128(sbase + L::kM, D * 128, 1024);
         StageRing<AS> ra;
-        StageRing<CS> rc;
         for (int i = 0; i < n_chunks; ++i) {
-          if (!warp_wait(c_full(rc.stage), rc.par, abort, p.status, tmo) ||
-              !warp_wait(c_ready, i & 1, abort, p.status, tmo))
+          if (!warp_wait(a_full(ra.stage), ra.par, abort, p.status, tmo) ||
+              !warp_wait(c_full(ra.stage), ra.par, abort, p.status, tmo))
             break;
+          if (chunk_n(i) < kTile && !warp_wait(fixed, 0, abort, p.status, tmo)) break;
           // the epilogue of the last chunk has read O1 and O2
           if (i > 0 && !warp_wait(o_free, (i - 1) & 1, abort, p.status, tmo)) break;
-          if (!warp_wait(m_full, i & 1, abort, p.status, tmo) ||
-              !warp_wait(a_full(ra.stage), ra.par, abort, p.status, tmo))
-            break;
+          if (!warp_wait(m_full, i & 1, abort, p.status, tmo)) break;
           tc_fence_after();
-          const uint64_t ad = ad0 + ra.stage * (L::kTileBytes >> 4), cd = cd0 + rc.stage * (L::kTileBytes >> 4);
+          const uint32_t st = ra.stage * (L::kTileBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             if (leader)
-              mma_ss(tO2, ad + (kk >> 2) * 1024 + (kk & 3) * 2, md + (uint64_t)(kk * 128), kId, kk > 0);
+              mma_ss(tO2, ad0 + st + (kk >> 2) * 1024 + (kk & 3) * 2, md + (uint64_t)(kk * 128), kId, kk > 0);
+          if (leader) mma_commit(m_free);
           __syncwarp();
           if (!warp_wait(p_full, i & 1, abort, p.status, tmo)) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            if (leader) mma_ts(tO1, tS + kk * 8, cd + (uint64_t)(kk * 128), kId, kk > 0);
+            if (leader) mma_ts(tO1, tS + kk * 8, cd0 + st + (uint64_t)(kk * 128), kId, kk > 0);
           if (leader) {
             mma_commit(o_full);
-            mma_commit(c_empty(rc.stage));
+            mma_commit(c_empty(ra.stage));
           }
           __syncwarp();
           ra.advance();
-          rc.advance();
         }
         if (leader) mma_commit(fin + 8);
         __syncwarp();
         drain_wait(fin + 8, 0);
       }
     } else {
-      // ---------------------------------------------- U = b^T (weighted c), hi then lo
+      // ------------------------------------- U = (weighted b)^T c: hi, and lo where it counts
       const bool leader = elect_one();
       constexpr uint32_t kId = idesc_bf16(128, D, true, true);
       // (at D 64 the product's lower 64 rows read what lies behind the tile: nobody reads them)
       const uint64_t bd0 = sdesc_sw128(sbase + L::kB, kTile * 128, 1024);
-      const uint64_t xd0 = sdesc_sw128(sbase + L::kX, kTile * 128, 1024);
+      const uint64_t cd0 = sdesc_sw128(sbase + L::kC, kTile * 128, 1024);
       StageRing<BS> rb;
-      StageRing<XS> rx;
       bool ok = true;
+      int k = 0;
       for (int i = 0; i < n_chunks && ok; ++i) {
-        if (!(ok = warp_wait(b_full(rb.stage), rb.par, abort, p.status, tmo))) break;
-        const uint64_t bd = bd0 + rb.stage * (L::kTileBytes >> 4);
-        for (int part = 0; part < 2; ++part) {
-          if (!(ok = warp_wait(x_full(rx.stage), rx.par, abort, p.status, tmo))) break;
+        if (!(ok = warp_wait(c_full(rb.stage), rb.par, abort, p.status, tmo))) break;
+        const uint32_t st = rb.stage * (L::kTileBytes >> 4);
+        for (int part = 0; part <= (exact ? 1 : 0); ++part, ++k) {
+          if (!(ok = warp_wait(x_full(k), (k >> 1) & 1, abort, p.status, tmo))) break;
           tc_fence_after();
-          const uint64_t xd = xd0 + rx.stage * (L::kTileBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            if (leader) mma_ss(tU, bd + (uint64_t)(kk * 128), xd + (uint64_t)(kk * 128), kId, part > 0 || kk > 0);
+            if (leader)
+              mma_ss(tU(i), bd0 + st + (uint64_t)(kk * 128), cd0 + st + (uint64_t)(kk * 128), kId, part > 0 || kk > 0);
           if (leader) {
-            mma_commit(x_empty(rx.stage));
-            if (part) {
+            if (exact && !part) {
+              mma_commit(h_done);
+            } else {
+              mma_commit(u_full(i));
               mma_commit(b_empty(rb.stage));
-              mma_commit(u_full);
+              mma_commit(c_empty(rb.stage));
             }
           }
           __syncwarp();
-          rx.advance();
         }
         rb.advance();
       }
@@ -310,19 +313,19 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
     }
   } else if (!SUM && warp < 8) {
     if constexpr (!SUM) {
-      regs_math();
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
       // ------------------------------------------------ P and the epilogue
       const int quad = warp & 3, row = quad * 32 + lane;
       const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
       StageRing<AS> ra;
       for (int i = 0; i < n_chunks; ++i) {
         const int pos0 = chunk_pos(i), n = chunk_n(i);
-        if (!warp_wait(s_full, i & 1, abort, p.status, tmo)) break;
+        if (!warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo)) break;
         tc_fence_after();
-        // columns j of this row: before it (front) or behind it (back), itself among them; pw is
-        // 0 for the others
-        const float* wrow = back ? pw - row : pw + row;
-#pragma unroll
+        // 32 columns at a time.  Those wholly before this warp's rows (behind, from the back): the
+        // weight is a row's power times a column's, both from tables with exponents >= 0.  On the
+        // diagonal it is looked up (zero for the columns that come after the row).
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
           if (back ? c < quad : c > quad) {
@@ -332,11 +335,27 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
             uint32_t r[32];
             tmem_ld32(tS + lane_off + c * 32, r);
             tmem_wait_ld();
+            if (c == quad) {
+              const float* wr = back ? pw - lane : pw + lane;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int j0 = c * 32 + 2 * j;
-              const float w0 = back ? wrow[j0] : wrow[-j0], w1 = back ? wrow[j0 + 1] : wrow[-j0 - 1];
-              pk[j] = pack_bf16(__uint_as_float(r[2 * j]) * w0, __uint_as_float(r[2 * j + 1]) * w1);
+              for (int j = 0; j < 16; ++j) {
+                const float w0 = back ? wr[2 * j] : wr[-2 * j], w1 = back ? wr[2 * j + 1] : wr[-2 * j - 1];
+                pk[j] = pack_bf16(__uint_as_float(r[2 * j]) * w0, __uint_as_float(r[2 * j + 1]) * w1);
+              }
+            } else {
+              // from the front r^(row - 32 c - 31) r^(31 - j), from the back r^(32 c - row) r^j
+              const float rw = pw[back ? 32 * c - row : row - 32 * c - 31];
+              const float4* cw = reinterpret_cast<const float4*>(pw + (back ? 0 : 136));
+              const float2 rw2 = make_float2(rw, rw);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float4 x = cw[j];
+                const float2 w0 = mul2(make_float2(x.x, x.y), rw2), w1 = mul2(make_float2(x.z, x.w), rw2);
+                const float2 y0 = mul2(make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])), w0);
+                const float2 y1 = mul2(make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])), w1);
+                pk[2 * j] = pack_bf16(y0.x, y0.y);
+                pk[2 * j + 1] = pack_bf16(y1.x, y1.y);
+              }
             }
           }
           tmem_st16(tS + lane_off + c * 16, pk);
@@ -347,7 +366,8 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
 
         if (!warp_wait(o_full, i & 1, abort, p.status, tmo)) break;
         tc_fence_after();
-        const float ow = pw[(back ? n - 1 - min(row, n - 1) : row) + 1 - late];
+        const float ow = pw[(back ? n - 1 - min(row, n - 1) : row) + 1 - late] * w.mul;
+        const float2 ow2 = make_float2(ow, ow), mul2v = make_float2(w.mul, w.mul);
         const int64_t tile_row0 = (int64_t)bh * p.T + p.m.slot(pos0);
         const bool staged = n == kTile && !w.out_f32;
         const bool store = row < n && in_bounds(tile_row0 + row, 1, rows_q, p.status);
@@ -358,22 +378,23 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
           tmem_ld32(tO1 + lane_off + c * 32, o1);
           tmem_ld32(tO2 + lane_off + c * 32, o2);
           tmem_wait_ld();
-          float v[32];
+          float2 v[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            v[j] = w.mul * fmaf(ow, __uint_as_float(o2[j]), __uint_as_float(o1[j]));
+          for (int j = 0; j < 16; ++j)
+            v[j] = fma2(ow2, make_float2(__uint_as_float(o2[2 * j]), __uint_as_float(o2[2 * j + 1])),
+                        mul2(mul2v, make_float2(__uint_as_float(o1[2 * j]), __uint_as_float(o1[2 * j + 1]))));
           if (w.out_f32) {
             if (store) {
               float4* dst = reinterpret_cast<float4*>(static_cast<float*>(w.out) + (tile_row0 + row) * D + c * 32);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              for (int j = 0; j < 8; ++j) dst[j] = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
             }
           } else {
             uint4 u[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              u[j] = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                                pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+              u[j] = make_uint4(pack_bf16(v[4 * j].x, v[4 * j].y), pack_bf16(v[4 * j + 1].x, v[4 * j + 1].y),
+                                pack_bf16(v[4 * j + 2].x, v[4 * j + 2].y), pack_bf16(v[4 * j + 3].x, v[4 * j + 3].y));
             if (staged) {
               // the tensor map's 128-byte swizzle: chunk a of row i at slot a ^ (i & 7)
               uint4* line = reinterpret_cast<uint4*>(st + (c >> 1) * (kTile * 128) + row * 128);
@@ -407,45 +428,44 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
       if (lane == 0) bulk_wait_all();
     }
   } else {
-    if constexpr (!SUM) regs_math();
+    if constexpr (!SUM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
     // -------------------------------------------------------- the state
+    constexpr int HC = D / 2, DD = D * D;
     const int quad = warp & 3, row = quad * 32 + lane;  // a channel of b, and a token of a chunk
+    const int col0 = (warp >> 2 & 1) * HC;              // of this thread: columns of M, channels of b
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    constexpr int DD = D * D;
     const bool mine = D == 128 || row < D;
-    float M[D];
-    {
+    float M[HC];
 #pragma unroll
-      for (int c = 0; c < D; ++c) M[c] = 0.f;
-      if (!SUM && mine) {
-        if (w.init) {
-          const float* src = w.init + (int64_t)bh * DD;
-          if (w.trans) {
+    for (int c = 0; c < HC; ++c) M[c] = 0.f;
+    if (!SUM && mine) {
+      if (w.init) {
+        const float* src = w.init + (int64_t)bh * DD;
+        if (w.trans) {
 #pragma unroll
-            for (int c = 0; c < D; ++c) M[c] = src[c * D + row] * w.init_mul;
-          } else {
+          for (int c = 0; c < HC; ++c) M[c] = src[(col0 + c) * D + row] * w.init_mul;
+        } else {
 #pragma unroll
-            for (int c = 0; c < D; c += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(src + row * D + c);
-              M[c] = x.x * w.init_mul, M[c + 1] = x.y * w.init_mul;
-              M[c + 2] = x.z * w.init_mul, M[c + 3] = x.w * w.init_mul;
-            }
+          for (int c = 0; c < HC; c += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src + row * D + col0 + c);
+            M[c] = x.x * w.init_mul, M[c + 1] = x.y * w.init_mul;
+            M[c + 2] = x.z * w.init_mul, M[c + 3] = x.w * w.init_mul;
           }
         }
-        // the runs before this one, folded in order
-        for (int s = 0; s < run; ++s) {
-          const float f = lin_pow(ld, lin_run_tokens<kTile>(p, n_tok, back, s));
-          const float* src = w.sums + ((int64_t)bh * p.segs + s) * DD;
-          if (!w.trans) {  // a run's sum lies with its columns first (see below)
+      }
+      // the runs before this one, folded in order
+      for (int s = 0; s < run; ++s) {
+        const float f = lin_pow(ld, lin_run_tokens<kTile>(p, n_tok, back, s));
+        const float* src = w.sums + ((int64_t)bh * p.segs + s) * DD;
+        if (!w.trans) {  // a run's sum lies with its columns first (see below)
 #pragma unroll
-            for (int c = 0; c < D; ++c) M[c] = fmaf(f, M[c], src[c * D + row]);
-          } else {
+          for (int c = 0; c < HC; ++c) M[c] = fmaf(f, M[c], src[(col0 + c) * D + row]);
+        } else {
 #pragma unroll
-            for (int c = 0; c < D; c += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(src + row * D + c);
-              M[c] = fmaf(f, M[c], x.x), M[c + 1] = fmaf(f, M[c + 1], x.y);
-              M[c + 2] = fmaf(f, M[c + 2], x.z), M[c + 3] = fmaf(f, M[c + 3], x.w);
-            }
+          for (int c = 0; c < HC; c += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src + row * D + col0 + c);
+            M[c] = fmaf(f, M[c], x.x), M[c + 1] = fmaf(f, M[c + 1], x.y);
+            M[c + 2] = fmaf(f, M[c + 2], x.z), M[c + 3] = fmaf(f, M[c + 3], x.w);
           }
         }
       }
@@ -453,101 +473,113 @@ __global__ void __launch_bounds__(SUM ? 256 : 384, 1) sweep_kernel(const __grid_
     // M as bf16, the operand of O2: rows of b's channels, 128-byte lines of 64 columns, swizzled
     auto publish = [&]() {
       if (mine) {
+        uint4* const line = reinterpret_cast<uint4*>(smem + L::kM + (col0 >> 6) * (D * 128) + row * 128);
 #pragma unroll
-        for (int c = 0; c < D; c += 8) {
-          uint4* line = reinterpret_cast<uint4*>(smem + L::kM + (c >> 6) * (D * 128) + row * 128);
-          line[((c & 63) >> 3) ^ (row & 7)] =
+        for (int c = 0; c < HC; c += 8)
+          line[(((col0 & 63) + c) >> 3) ^ (row & 7)] =
               make_uint4(pack_bf16(M[c], M[c + 1]), pack_bf16(M[c + 2], M[c + 3]),
                          pack_bf16(M[c + 4], M[c + 5]), pack_bf16(M[c + 6], M[c + 7]));
-        }
       }
       fence_proxy_async_smem();
       mbar_arrive(m_full);
     };
-    if (!SUM && n_chunks > 0) publish();
-    StageRing<BS> rb;
-    StageRing<CS> rc;
-    StageRing<XS> rx;
-    bool ok = true;
-    for (int i = 0; i < n_chunks && ok; ++i) {
-      const int n = chunk_n(i);
-      if (!(ok = warp_wait(c_full(rc.stage), rc.par, abort, p.status, tmo))) break;
-      uint8_t* const ct = smem + L::kC + rc.stage * L::kTileBytes;
-      if (n < kTile) {
-        // rows behind the last token hold anything: zeros, in b and in c
-        if (!(ok = warp_wait(b_full(rb.stage), rb.par, abort, p.status, tmo))) break;
-        if (row >= n) {
-          uint8_t* const bt = smem + L::kB + rb.stage * L::kTileBytes;
-          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            reinterpret_cast<uint4*>(ct + (j >> 3) * (kTile * 128) + row * 128)[j & 7] = zero;
-            reinterpret_cast<uint4*>(bt + (j >> 3) * (kTile * 128) + row * 128)[j & 7] = zero;
-          }
-        }
-        fence_proxy_async_smem();
-      }
-      if (!SUM) mbar_arrive(c_ready);
-      // this token's row of c times its weight, hi = bf16 of it and lo = bf16 of what is left
-      const float uw = row < n ? pw[(back ? row : n - 1 - row) + late] : 0.f;
-      const uint4* const crow = reinterpret_cast<const uint4*>(ct + row * 128);
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        if (!(ok = warp_wait(x_empty(rx.stage), rx.par ^ 1, abort, p.status, tmo))) break;
-        uint8_t* const xt = smem + L::kX + rx.stage * L::kTileBytes + row * 128;
-#pragma unroll 4
-        for (int j = 0; j < D / 8; ++j) {
-          const int at = (j & 7) ^ (row & 7), blk = (j >> 3) * (kTile * 128);
-          const uint4 x = crow[blk / 16 + at];
-          const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-          uint32_t out[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float v0 = bf16_lo(in[k]) * uw, v1 = bf16_hi(in[k]) * uw;
-            out[k] = pack_bf16(v0, v1);
-            if (part) out[k] = pack_bf16(v0 - bf16_lo(out[k]), v1 - bf16_hi(out[k]));
-          }
-          reinterpret_cast<uint4*>(xt + blk)[at] = make_uint4(out[0], out[1], out[2], out[3]);
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();  // (U of the last chunk has been read)
-        mbar_arrive(x_full(rx.stage));
-        rx.advance();
-      }
-      if (!ok) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(c_empty(rc.stage));
-      rc.advance();
-      rb.advance();
-      // M = r^n M + U
-      if (!(ok = warp_wait(u_full, i & 1, abort, p.status, tmo))) break;
+    // M = r^n M + U of chunk i
+    auto take = [&](int i) -> bool {
+      if (!warp_wait(u_full(i), (i >> 1) & 1, abort, p.status, tmo)) return false;
       tc_fence_after();
-      const float f = pw[n];
+      const float f = pw[chunk_n(i)];
+      const float2 f2 = make_float2(f, f);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < HC / 32; ++c) {
         uint32_t u[32];
-        tmem_ld32(tU + lane_off + c * 32, u);
+        tmem_ld32(tU(i) + lane_off + col0 + c * 32, u);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) M[c * 32 + j] = fmaf(f, M[c * 32 + j], __uint_as_float(u[j]));
+        for (int j = 0; j < 32; j += 2) {
+          const float2 x = fma2(f2, make_float2(M[c * 32 + j], M[c * 32 + j + 1]),
+                                make_float2(__uint_as_float(u[j]), __uint_as_float(u[j + 1])));
+          M[c * 32 + j] = x.x, M[c * 32 + j + 1] = x.y;
+        }
       }
-      if (!SUM && i + 1 < n_chunks) {
-        // O2 of this chunk has read the old copy
-        if (!(ok = warp_wait(o_full, i & 1, abort, p.status, tmo))) break;
-        publish();
+      tc_fence_before();
+      return true;
+    };
+    if (!SUM && n_chunks > 0) publish();
+    StageRing<BS> rb;
+    bool ok = true;
+    int k = 0;
+    for (int i = 0; i < n_chunks && ok; ++i) {
+      const int n = chunk_n(i);
+      if (!(ok = warp_wait(b_full(rb.stage), rb.par, abort, p.status, tmo))) break;
+      uint8_t* const bt = smem + L::kB + rb.stage * L::kTileBytes;
+      // this thread's half of its token's row: HC / 8 chunks of eight channels
+      uint4* const line = reinterpret_cast<uint4*>(bt + (col0 >> 6) * (kTile * 128) + row * 128);
+      const int chunk0 = (col0 & 63) >> 3;
+      if (n < kTile) {
+        // rows behind the last token hold anything: zeros, in b and in c
+        if (!(ok = warp_wait(c_full(rb.stage), rb.par, abort, p.status, tmo))) break;
+        if (row >= n) {
+          uint4* const cline = line + (L::kC - L::kB) / 16;
+#pragma unroll
+          for (int j = 0; j < HC / 8; ++j) line[chunk0 + j] = cline[chunk0 + j] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        if (!SUM) mbar_arrive(fixed);
+      }
+      // S has read b
+      if (!SUM && !(ok = warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo))) break;
+      const float uw = row < n ? pw[(back ? row : n - 1 - row) + late] : 0.f;
+      const float2 uw2 = make_float2(uw, uw);
+      uint4 lo[HC / 8];  // what is left of the weighted row
+#pragma unroll
+      for (int j = 0; j < HC / 8; ++j) {
+        uint4* const at = line + ((chunk0 + j) ^ (row & 7));
+        const uint4 x = *at;
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+        uint32_t hi[4], l[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 v = mul2(make_float2(bf16_lo(in[q]), bf16_hi(in[q])), uw2);
+          hi[q] = pack_bf16(v.x, v.y);
+          l[q] = pack_bf16(v.x - bf16_lo(hi[q]), v.y - bf16_hi(hi[q]));
+        }
+        *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        lo[j] = make_uint4(l[0], l[1], l[2], l[3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(x_full(k++));
+      if constexpr (SUM) {
+        if (i > 0 && !(ok = take(i - 1))) break;  // while this chunk's product runs
+      }
+      if (exact) {
+        if (!(ok = warp_wait(h_done, i & 1, abort, p.status, tmo))) break;
+#pragma unroll
+        for (int j = 0; j < HC / 8; ++j) line[(chunk0 + j) ^ (row & 7)] = lo[j];
+        fence_proxy_async_smem();
+        mbar_arrive(x_full(k++));
+      }
+      rb.advance();
+      if constexpr (!SUM) {
+        if (!(ok = take(i))) break;
+        if (i + 1 < n_chunks) {
+          // O2 of this chunk has read the old copy
+          if (!(ok = warp_wait(m_free, i & 1, abort, p.status, tmo))) break;
+          publish();
+        }
       }
     }
+    if (SUM && ok && n_chunks > 0) ok = take(n_chunks - 1);
     if (ok && mine) {
       if constexpr (SUM) {
         // columns first: the threads of a warp write, and in most sweeps read, consecutive numbers
         float* dst = w.sums + ((int64_t)bh * p.segs + run) * DD;
 #pragma unroll
-        for (int c = 0; c < D; ++c) dst[c * D + row] = M[c];
+        for (int c = 0; c < HC; ++c) dst[(col0 + c) * D + row] = M[c];
       } else if (run == p.segs - 1 && w.fin) {
         float* dst = w.fin + (int64_t)bh * DD;
 #pragma unroll
-        for (int c = 0; c < D; c += 4)
-          *reinterpret_cast<float4*>(dst + row * D + c) = make_float4(
+        for (int c = 0; c < HC; c += 4)
+          *reinterpret_cast<float4*>(dst + row * D + col0 + c) = make_float4(
               M[c] * w.fin_mul, M[c + 1] * w.fin_mul, M[c + 2] * w.fin_mul, M[c + 3] * w.fin_mul);
       }
     }
@@ -580,11 +612,15 @@ static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, cudaStrea
     // the output as 32-row, 64-column boxes (one warp's rows)
     if (!SUM && !w.out_f32 && !make_map(&m.o, w.out, hq, p.T, D, 32)) return cudaErrorInvalidValue;
   }
-  constexpr int kSmem = Smem<D, SUM>::kBytes, kThreads = SUM ? 256 : 384;
+  constexpr int kSmem = Smem<D, SUM>::kBytes, kThreads = SUM ? kThreadsSum : kThreadsOut;
   auto kern = sweep_kernel<D, SUM>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  if (!SUM && (e = check_register_split(kern, kThreads)) != cudaSuccess) return e;
+  if (!SUM) {  // a split that does not fit what the launch allocates would wait forever
+    cudaFuncAttributes at;
+    if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
+    if (at.numRegs * kThreads < 128 * (int)kRegsCtl + 384 * kRegsOut) return cudaErrorInvalidConfiguration;
+  }
   const unsigned blocks = (unsigned)(p.B * p.Hq * (SUM ? p.segs - 1 : p.segs));
   kern<<<dim3(blocks, n), kThreads, kSmem, st>>>(prm);
   return cudaGetLastError();
