@@ -16,12 +16,12 @@
 // leave 2^-9 in a float32 result.  U starts from zero in every chunk, so no sum on the tensor
 // cores runs longer than 256 terms.
 //
-// Warp roles (512 threads):
+// Warp roles (640 threads):
 //   warp 0        TMA producer: the tiles a, b, c of a chunk, two stages each
 //   warp 1        issues S;  warp 2: O2 and O1;  warp 3: U
-//   warps 4-7     the rows of the output: S -> P, then the epilogue.  The output tile is staged
-//                 in the chunk's own a tile, which nothing reads any more, and leaves by TMA
-//   warps 8-15    the state: b times its weights, M, its bf16 copy
+//   warps 4-11    the output, two threads a row: S -> P, then the epilogue, stored from registers
+//                 in whole 32-byte sectors
+//   warps 12-19   the state, two threads a row: b times its weights, M, its bf16 copy
 // Issuers are whole warps with one elected lane, as in tc_fwd.cu.  TMEM: S/P [0, 128),
 // O1, O2 and U of D columns each behind it.
 //
@@ -44,10 +44,11 @@ constexpr int kTile = kLinTcChunk;
 constexpr uint64_t kTimeoutNs = 2000000000ull;     // 2 s
 constexpr uint64_t kDebugTimeoutNs = 50000000ull;  // 50 ms under the fault hook
 constexpr uint64_t kDrainTimeoutNs = 200000000ull;
-constexpr int kThreadsOut = 512, kThreadsSum = 384;
-// registers of the warpgroups of the second launch: one of control, three of arithmetic
-constexpr int kRegsOut = 144;
-static_assert(128 * kRegsCtl + 384 * kRegsOut <= 65536, "");
+constexpr int kThreadsOut = 640, kThreadsSum = 384;
+// Registers of the second launch's five warpgroups (control, two of the output, two of the state):
+// at most what 640 threads are launched with, 96 each.
+constexpr int kRegsControl = 64, kRegsOut = 80, kRegsState = 128, kRegsLaunch = 96;
+static_assert(128 * (kRegsControl + 2 * kRegsOut + 2 * kRegsState) <= kThreadsOut * kRegsLaunch, "");
 
 template <int D, bool SUM>
 struct Smem {
@@ -59,20 +60,23 @@ struct Smem {
   static constexpr int kC = kB + kBS * kTileBytes;
   static constexpr int kM = kC + kBS * kTileBytes;
   static constexpr int kPow = kM + (SUM ? 0 : D * D * 2);
-  // powers r^e at kPow + 4 (128 + e), zeros for e < 0; then r^31 .. r^0
-  static constexpr int kBar = kPow + 4 * (264 + 32);
+  // powers r^e at kPow + 4 (128 + e), zeros for e < 0
+  static constexpr int kBar = kPow + 4 * 264;
   static constexpr int kNumBars = 2 * (kAS + 2 * kBS) + 13 + 3;
   static constexpr int kMisc = kBar + 8 * kNumBars;
   static constexpr int kBytes = kMisc + 16;
 };
 
 struct Maps {
-  CUtensorMap a, b, c, o;
+  CUtensorMap a, b, c;
 };
 struct Params {
   Linear p;
   Maps maps[kMaxSweeps];
 };
+
+// Every role runs through its code once a chunk, and together they overran the instruction cache
+// (40 % of its requests missed): loops stay rolled where registers allow.
 
 // Wait in which every lane of the warp takes part; all lanes agree on the result.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t par, volatile int* abort,
@@ -88,6 +92,14 @@ __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t par) {
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// 32 bytes, a whole sector, aligned.
+__device__ __forceinline__ void store32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
+                                        uint32_t f, uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d),
+               "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
 
 template <int D, bool SUM>
 __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
@@ -145,12 +157,12 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) mbar_init(bars + 8 * i, 1);
-    // a_empty: the four warps that store the output; c_empty: O1 and U; the rest by threads
-    for (int i = 0; i < AS; ++i) mbar_init(a_empty(i), 4);
+    // a_empty: S and O2; c_empty: O1 and U; the rest by threads
+    for (int i = 0; i < AS; ++i) mbar_init(a_empty(i), 2);
     for (int i = 0; i < BS; ++i) mbar_init(c_empty(i), SUM ? 1 : 2);
     for (int i = 0; i < 2; ++i) mbar_init(x_full(i), 256);
-    mbar_init(p_full, 128);
-    mbar_init(o_free, 128);
+    mbar_init(p_full, 256);
+    mbar_init(o_free, 256);
     mbar_init(m_full, 256);
     mbar_init(fixed, 256);
     *abort = 0;
@@ -160,8 +172,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  for (int i = threadIdx.x; i < 264 + 32; i += blockDim.x)
-    pw[i - 128] = i < 128 ? 0.f : i < 264 ? lin_pow(ld, i - 128) : lin_pow(ld, 31 - (i - 264));
+  for (int i = threadIdx.x; i < 264; i += blockDim.x) pw[i - 128] = i < 128 ? 0.f : lin_pow(ld, i - 128);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -170,7 +181,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
   auto tU = [&](int i) { return SUM ? tmem + (i & 1) * D : tmem + 128 + 2 * D; };
 
   if (warp < 4) {
-    if constexpr (!SUM) regs_ctl();
+    if constexpr (!SUM) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
@@ -225,7 +236,10 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
             const uint32_t off = st + (kk >> 2) * 1024 + (kk & 3) * 2;  // 16 KiB blocks, 32 B steps
             if (leader) mma_ss(tS, ad0 + off, bd0 + off, kId, kk > 0);
           }
-          if (leader) mma_commit(s_full(i));
+          if (leader) {
+            mma_commit(s_full(i));
+            mma_commit(a_empty(ra.stage));
+          }
           __syncwarp();
           ra.advance();
         }
@@ -256,13 +270,16 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           for (int kk = 0; kk < D / 16; ++kk)
             if (leader)
               mma_ss(tO2, ad0 + st + (kk >> 2) * 1024 + (kk & 3) * 2, md + (uint64_t)(kk * 128), kId, kk > 0);
-          if (leader) mma_commit(m_free);
+          if (leader) {
+            mma_commit(m_free);
+            mma_commit(a_empty(ra.stage));
+          }
           __syncwarp();
           if (!warp_wait(p_full, i & 1, abort, p.status, tmo)) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            if (leader) mma_ts(tO1, tS + kk * 8, cd0 + st + (uint64_t)(kk * 128), kId, kk > 0);
+            if (leader) mma_ts(tO1, tS + (kk >> 2) * 64 + (kk & 3) * 8, cd0 + st + (uint64_t)(kk * 128), kId, kk > 0);
           if (leader) {
             mma_commit(o_full);
             mma_commit(c_empty(ra.stage));
@@ -311,54 +328,47 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       __syncwarp();
       drain_wait(fin + 16, 0);
     }
-  } else if (!SUM && warp < 8) {
+  } else if (!SUM && warp < 12) {
     if constexpr (!SUM) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
       // ------------------------------------------------ P and the epilogue
-      const int quad = warp & 3, row = quad * 32 + lane;
+      const int quad = warp & 3, row = quad * 32 + lane, half = warp >> 2 & 1;
       const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-      StageRing<AS> ra;
+      constexpr int HC = D / 2;
+      const bool aligned32 = (reinterpret_cast<uintptr_t>(w.out) & 31) == 0;
       for (int i = 0; i < n_chunks; ++i) {
         const int pos0 = chunk_pos(i), n = chunk_n(i);
         if (!warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo)) break;
         tc_fence_after();
-        // 32 columns at a time.  Those wholly before this warp's rows (behind, from the back): the
-        // weight is a row's power times a column's, both from tables with exponents >= 0.  On the
-        // diagonal it is looked up (zero for the columns that come after the row).
+        // 32 columns at a time, two times a half: weights from the table (zero for columns that come
+        // after the row; wholly such columns are not read).  P of half h lies over S's columns
+        // [64 h, 64 h + 32), which this thread has read by then.
+        const float* wr = back ? pw - row + half * 64 : pw + row - half * 64;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t pk[16];
-          if (back ? c < quad : c > quad) {
+          const int col = 2 * half + c;
+          if (back ? col < quad : col > quad) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) pk[j] = 0u;
           } else {
             uint32_t r[32];
-            tmem_ld32(tS + lane_off + c * 32, r);
-            tmem_wait_ld();
-            if (c == quad) {
-              const float* wr = back ? pw - lane : pw + lane;
+            tmem_ld32(tS + lane_off + col * 32, r);
+            float f[32];
+            if (back) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float w0 = back ? wr[2 * j] : wr[-2 * j], w1 = back ? wr[2 * j + 1] : wr[-2 * j - 1];
-                pk[j] = pack_bf16(__uint_as_float(r[2 * j]) * w0, __uint_as_float(r[2 * j + 1]) * w1);
-              }
+              for (int j = 0; j < 32; ++j) f[j] = wr[j];
             } else {
-              // from the front r^(row - 32 c - 31) r^(31 - j), from the back r^(32 c - row) r^j
-              const float rw = pw[back ? 32 * c - row : row - 32 * c - 31];
-              const float4* cw = reinterpret_cast<const float4*>(pw + (back ? 0 : 136));
-              const float2 rw2 = make_float2(rw, rw);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float4 x = cw[j];
-                const float2 w0 = mul2(make_float2(x.x, x.y), rw2), w1 = mul2(make_float2(x.z, x.w), rw2);
-                const float2 y0 = mul2(make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])), w0);
-                const float2 y1 = mul2(make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])), w1);
-                pk[2 * j] = pack_bf16(y0.x, y0.y);
-                pk[2 * j + 1] = pack_bf16(y1.x, y1.y);
-              }
+              for (int j = 0; j < 32; ++j) f[j] = wr[-j];
             }
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              pk[j] = pack_bf16(__uint_as_float(r[2 * j]) * f[2 * j], __uint_as_float(r[2 * j + 1]) * f[2 * j + 1]);
           }
-          tmem_st16(tS + lane_off + c * 16, pk);
+          tmem_st16(tS + lane_off + half * 64 + c * 16, pk);
+          wr += back ? 32 : -32;
         }
         tmem_wait_st();
         tc_fence_before();
@@ -369,66 +379,48 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         const float ow = pw[(back ? n - 1 - min(row, n - 1) : row) + 1 - late] * w.mul;
         const float2 ow2 = make_float2(ow, ow), mul2v = make_float2(w.mul, w.mul);
         const int64_t tile_row0 = (int64_t)bh * p.T + p.m.slot(pos0);
-        const bool staged = n == kTile && !w.out_f32;
         const bool store = row < n && in_bounds(tile_row0 + row, 1, rows_q, p.status);
-        uint8_t* const st = smem + L::kA + ra.stage * L::kTileBytes;
+        const int64_t at = (tile_row0 + row) * D + half * HC;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o1[32], o2[32];
-          tmem_ld32(tO1 + lane_off + c * 32, o1);
-          tmem_ld32(tO2 + lane_off + c * 32, o2);
+        for (int c = 0; c < HC / 16; ++c) {
+          uint32_t o1[16], o2[16];
+          tmem_ld16(tO1 + lane_off + half * HC + c * 16, o1);
+          tmem_ld16(tO2 + lane_off + half * HC + c * 16, o2);
           tmem_wait_ld();
-          float2 v[16];
+          if (c == HC / 16 - 1) {  // O1 and O2 have been read
+            tc_fence_before();
+            mbar_arrive(o_free);
+          }
+          float2 v[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
+          for (int j = 0; j < 8; ++j)
             v[j] = fma2(ow2, make_float2(__uint_as_float(o2[2 * j]), __uint_as_float(o2[2 * j + 1])),
                         mul2(mul2v, make_float2(__uint_as_float(o1[2 * j]), __uint_as_float(o1[2 * j + 1]))));
+          if (!store) continue;
           if (w.out_f32) {
-            if (store) {
-              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(w.out) + (tile_row0 + row) * D + c * 32);
+            float* dst = static_cast<float*>(w.out) + at + c * 16;  // (the workspace's: aligned)
 #pragma unroll
-              for (int j = 0; j < 8; ++j) dst[j] = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
-            }
+            for (int j = 0; j < 8; j += 4)
+              store32(dst + 2 * j, __float_as_uint(v[j].x), __float_as_uint(v[j].y), __float_as_uint(v[j + 1].x),
+                      __float_as_uint(v[j + 1].y), __float_as_uint(v[j + 2].x), __float_as_uint(v[j + 2].y),
+                      __float_as_uint(v[j + 3].x), __float_as_uint(v[j + 3].y));
           } else {
-            uint4 u[4];
+            uint32_t u[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              u[j] = make_uint4(pack_bf16(v[4 * j].x, v[4 * j].y), pack_bf16(v[4 * j + 1].x, v[4 * j + 1].y),
-                                pack_bf16(v[4 * j + 2].x, v[4 * j + 2].y), pack_bf16(v[4 * j + 3].x, v[4 * j + 3].y));
-            if (staged) {
-              // the tensor map's 128-byte swizzle: chunk a of row i at slot a ^ (i & 7)
-              uint4* line = reinterpret_cast<uint4*>(st + (c >> 1) * (kTile * 128) + row * 128);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) line[((c & 1) * 4 + j) ^ (row & 7)] = u[j];
-            } else if (store) {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(w.out) + (tile_row0 + row) * D + c * 32);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) dst[j] = u[j];
+            for (int j = 0; j < 8; ++j) u[j] = pack_bf16(v[j].x, v[j].y);
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(w.out) + at + c * 16;
+            if (aligned32) {
+              store32(dst, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
+            } else {
+              reinterpret_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+              reinterpret_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
             }
           }
         }
-        // O1 and O2 have been read
-        tc_fence_before();
-        mbar_arrive(o_free);
-        if (staged) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (in_bounds(tile_row0 + quad * 32, 32, rows_q, p.status))
-              for (int kb = 0; kb < D / 64; ++kb)
-                tma_store_2d(&maps.o, kb * 64, (int)(tile_row0 + quad * 32),
-                             sbase + L::kA + ra.stage * L::kTileBytes + kb * (kTile * 128) + quad * 32 * 128);
-            bulk_commit_group();
-            bulk_wait_read_all();
-          }
-        }
-        if (lane == 0) mbar_arrive(a_empty(ra.stage));
-        ra.advance();
       }
-      if (lane == 0) bulk_wait_all();
     }
   } else {
-    if constexpr (!SUM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+    if constexpr (!SUM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
     // -------------------------------------------------------- the state
     constexpr int HC = D / 2, DD = D * D;
     const int quad = warp & 3, row = quad * 32 + lane;  // a channel of b, and a token of a chunk
@@ -531,21 +523,26 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       const float uw = row < n ? pw[(back ? row : n - 1 - row) + late] : 0.f;
       const float2 uw2 = make_float2(uw, uw);
       uint4 lo[HC / 8];  // what is left of the weighted row
+      auto weight = [&](auto with_lo) {
+        // (lo has to stay in registers)
+#pragma unroll(decltype(with_lo)::value ? HC / 8 : 2)
+        for (int j = 0; j < HC / 8; ++j) {
+          uint4* const at = line + ((chunk0 + j) ^ (row & 7));
+          const uint4 x = *at;
+          const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+          uint32_t hi[4], l[4];
 #pragma unroll
-      for (int j = 0; j < HC / 8; ++j) {
-        uint4* const at = line + ((chunk0 + j) ^ (row & 7));
-        const uint4 x = *at;
-        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-        uint32_t hi[4], l[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 v = mul2(make_float2(bf16_lo(in[q]), bf16_hi(in[q])), uw2);
-          hi[q] = pack_bf16(v.x, v.y);
-          l[q] = pack_bf16(v.x - bf16_lo(hi[q]), v.y - bf16_hi(hi[q]));
+          for (int q = 0; q < 4; ++q) {
+            const float2 v = mul2(make_float2(bf16_lo(in[q]), bf16_hi(in[q])), uw2);
+            hi[q] = pack_bf16(v.x, v.y);
+            if (decltype(with_lo)::value) l[q] = pack_bf16(v.x - bf16_lo(hi[q]), v.y - bf16_hi(hi[q]));
+          }
+          *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if (decltype(with_lo)::value) lo[j] = make_uint4(l[0], l[1], l[2], l[3]);
         }
-        *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        lo[j] = make_uint4(l[0], l[1], l[2], l[3]);
-      }
+      };
+      if (exact) weight(std::true_type{});
+      else weight(std::false_type{});
       fence_proxy_async_smem();
       mbar_arrive(x_full(k++));
       if constexpr (SUM) {
@@ -593,8 +590,8 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
   }
 }
 
-static bool make_map(CUtensorMap* m, const void* t, int64_t heads, int T, int D, int box_rows) {
-  return encode_tmap_2d_bf16(m, t, D, (uint64_t)heads * T, 64, box_rows) == CUDA_SUCCESS;
+static bool make_map(CUtensorMap* m, const void* t, int64_t heads, int T, int D) {
+  return encode_tmap_2d_bf16(m, t, D, (uint64_t)heads * T, 64, kTile) == CUDA_SUCCESS;
 }
 
 template <int D, bool SUM>
@@ -605,12 +602,10 @@ static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, cudaStrea
     const LinSweep& w = sweeps[i];
     Maps& m = prm.maps[i];
     const int64_t hq = (int64_t)p.B * p.Hq;
-    if (!make_map(&m.b, w.b, hq / w.rep_b, p.T, D, kTile) || !make_map(&m.c, w.c, hq / w.rep_c, p.T, D, kTile))
+    if (!make_map(&m.b, w.b, hq / w.rep_b, p.T, D) || !make_map(&m.c, w.c, hq / w.rep_c, p.T, D))
       return cudaErrorInvalidValue;
-    m.a = m.o = m.b;
-    if (!SUM && !make_map(&m.a, w.a, hq / w.rep_a, p.T, D, kTile)) return cudaErrorInvalidValue;
-    // the output as 32-row, 64-column boxes (one warp's rows)
-    if (!SUM && !w.out_f32 && !make_map(&m.o, w.out, hq, p.T, D, 32)) return cudaErrorInvalidValue;
+    m.a = m.b;
+    if (!SUM && !make_map(&m.a, w.a, hq / w.rep_a, p.T, D)) return cudaErrorInvalidValue;
   }
   constexpr int kSmem = Smem<D, SUM>::kBytes, kThreads = SUM ? kThreadsSum : kThreadsOut;
   auto kern = sweep_kernel<D, SUM>;
@@ -619,7 +614,7 @@ static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, cudaStrea
   if (!SUM) {  // a split that does not fit what the launch allocates would wait forever
     cudaFuncAttributes at;
     if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
-    if (at.numRegs * kThreads < 128 * (int)kRegsCtl + 384 * kRegsOut) return cudaErrorInvalidConfiguration;
+    if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
   }
   const unsigned blocks = (unsigned)(p.B * p.Hq * (SUM ? p.segs - 1 : p.segs));
   kern<<<dim3(blocks, n), kThreads, kSmem, st>>>(prm);
