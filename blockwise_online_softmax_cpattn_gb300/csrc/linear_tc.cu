@@ -18,9 +18,10 @@
 //
 // Warp roles (640 threads):
 //   warp 0        TMA producer: the tiles a, b, c of a chunk, two stages each
-//   warp 1        issues S;  warp 2: O2 and O1;  warp 3: U
-//   warps 4-11    the output, two threads a row: S -> P, then the epilogue, stored from registers
-//                 in whole 32-byte sectors
+//   warp 1        issues S;  warp 2: O1;  warp 3: O2 and U
+//   warps 4-11    the output, two threads a row: S -> P, then the epilogue, staged in the chunk's own
+//                 a tile, which nothing reads any more, and out by TMA (stored from registers, every
+//                 instruction touches 32 lines, and the loads from TMEM queued behind them)
 //   warps 12-19   the state, two threads a row: b times its weights, M, its bf16 copy
 // Issuers are whole warps with one elected lane, as in tc_fwd.cu.  TMEM: S/P [0, 128),
 // O1, O2 and U of D columns each behind it.
@@ -34,16 +35,13 @@
 // channels: in two halves S and the reads of a and b came twice, 960 KB.
 //
 // A barrier that a role may leave behind by a phase comes as a pair, by the chunk's parity.
-// Every mbarrier wait is bounded, as in tc_fwd.cu.
+// Every mbarrier wait is bounded.
 #include "layer.cuh"
 
 namespace cpattn {
 namespace lintc {
 
 constexpr int kTile = kLinTcChunk;
-constexpr uint64_t kTimeoutNs = 2000000000ull;     // 2 s
-constexpr uint64_t kDebugTimeoutNs = 50000000ull;  // 50 ms under the fault hook
-constexpr uint64_t kDrainTimeoutNs = 200000000ull;
 constexpr int kThreadsOut = 640, kThreadsSum = 384;
 // Registers of the second launch's five warpgroups (control, two of the output, two of the state):
 // at most what 640 threads are launched with, 96 each.
@@ -59,47 +57,71 @@ struct Smem {
   static constexpr int kB = kA + kAS * kTileBytes;
   static constexpr int kC = kB + kBS * kTileBytes;
   static constexpr int kM = kC + kBS * kTileBytes;
-  static constexpr int kPow = kM + (SUM ? 0 : D * D * 2);
+  // the output's staging, 4 KB a warp: at D 128 the a tile; at D 64 that is too small for float32
+  static constexpr int kO = kM + (SUM ? 0 : D * D * 2);
+  static constexpr int kPow = kO + (SUM || D == 128 ? 0 : 8 * 4096);
   // powers r^e at kPow + 4 (128 + e), zeros for e < 0
   static constexpr int kBar = kPow + 4 * 264;
-  static constexpr int kNumBars = 2 * (kAS + 2 * kBS) + 13 + 3;
+  static constexpr int kNumBars = 2 * (kAS + 2 * kBS) + 14 + 3;
   static constexpr int kMisc = kBar + 8 * kNumBars;
   static constexpr int kBytes = kMisc + 16;
 };
 
 struct Maps {
-  CUtensorMap a, b, c;
+  CUtensorMap a, b, c, o;
 };
 struct Params {
   Linear p;
   Maps maps[kMaxSweeps];
 };
 
-// Every role runs through its code once a chunk, and together they overran the instruction cache
-// (40 % of its requests missed): loops stay rolled where registers allow.
+// Every role runs through its code once a chunk, on every sub-partition, and together they overran
+// the instruction cache (40 % of its requests missed): loops stay rolled where registers allow, and
+// a wait is a few instructions, bounded by a number of tries of up to 20 us each (the hardware
+// suspends the thread meanwhile) instead of by a clock.
+constexpr uint32_t kTryNs = 20000;
+constexpr uint32_t kTries = 500000;       // 10 s at most, 50 ms if a try takes 100 ns only
+constexpr uint32_t kDebugTries = 2500;    // 50 ms at most, under the fault hook
+constexpr uint32_t kDrainTries = 10000;
 
-// Wait in which every lane of the warp takes part; all lanes agree on the result.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t par, volatile int* abort,
-                                          int* status, uint64_t tmo) {
-  bool ok = mbar_wait(bar, par, abort, status, tmo);
-  return __all_sync(0xffffffffu, ok);
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kTryNs)
+      : "memory");
+  return ok != 0;
 }
-// Wait that ignores the abort flag (used to drain in-flight copies before exit).
-__device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t par) {
-  int never = 0;
-  return mbar_wait(bar, par, &never, nullptr, kDrainTimeoutNs);
+// Gives up (false) when *abort is set or the tries run out; then it sets *abort itself, so that
+// every other role of the block stops too, and latches the device status word.
+__device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t par, volatile int* abort, int* status, uint32_t tries) {
+#pragma unroll 1
+  while (!try_wait(bar, par)) {
+    if (*abort) return false;
+    if (--tries == 0) {
+      *abort = 1;
+      latch_status(status, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+// The same with every lane of the warp; all lanes agree on the result.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t par, volatile int* abort, int* status, uint32_t tries) {
+  return __all_sync(0xffffffffu, thread_wait(bar, par, abort, status, tries));
+}
+// Ignores the abort flag (used to drain in-flight copies and products before exit).
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t par) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kDrainTries && !try_wait(bar, par); ++i) {
+  }
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-// 32 bytes, a whole sector, aligned.
-__device__ __forceinline__ void store32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
-                                        uint32_t f, uint32_t g, uint32_t h) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d),
-               "r"(e), "r"(f), "r"(g), "r"(h)
-               : "memory");
-}
 
 template <int D, bool SUM>
 __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
@@ -126,13 +148,13 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
   auto x_full = [&](int k) { return one + 8 * (2 + (k & 1)); };  // b weighted, the k-th time
   auto u_full = [&](int i) { return one + 8 * (4 + (i & 1)); };
   const uint32_t p_full = one + 48, o_full = one + 56, o_free = one + 64, m_full = one + 72,
-                 m_free = one + 80, h_done = one + 88, fixed = one + 96, fin = one + 104;
+                 m_free = one + 80, h_done = one + 88, fixed = one + 96, o2_full = one + 104, fin = one + 112;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   float* pw = reinterpret_cast<float*>(smem + L::kPow) + 128;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint64_t tmo = p.debug_fault ? kDebugTimeoutNs : kTimeoutNs;
+  const uint32_t tmo = p.debug_fault ? kDebugTries : kTries;
 
   // ---- this block's run
   const int runs = SUM ? p.segs - 1 : p.segs;  // the last run's own sum is nobody's start
@@ -157,8 +179,8 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) mbar_init(bars + 8 * i, 1);
-    // a_empty: S and O2; c_empty: O1 and U; the rest by threads
-    for (int i = 0; i < AS; ++i) mbar_init(a_empty(i), 2);
+    // a_empty: the eight warps that stage the output there; c_empty: O1 and U; the rest by threads
+    for (int i = 0; i < AS; ++i) mbar_init(a_empty(i), 8);
     for (int i = 0; i < BS; ++i) mbar_init(c_empty(i), SUM ? 1 : 2);
     for (int i = 0; i < 2; ++i) mbar_init(x_full(i), 256);
     mbar_init(p_full, 256);
@@ -192,7 +214,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           const int slot = p.m.slot(chunk_pos(i));
           auto load = [&](auto& ring, uint32_t full, uint32_t empty, int base, const CUtensorMap* tm, int head,
                           int heads) {
-            if (!ok || !(ok = mbar_wait(empty, ring.par ^ 1, abort, p.status, tmo))) return;
+            if (!ok || !(ok = thread_wait(empty, ring.par ^ 1, abort, p.status, tmo))) return;
             mbar_expect_tx(full, L::kTileBytes);
             const int row = head * p.T + slot;
             // (a partial chunk reads on into the next head, or zeros behind the tensor)
@@ -231,15 +253,12 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           if (chunk_n(i) < kTile && !warp_wait(fixed, 0, abort, p.status, tmo)) break;
           tc_fence_after();
           const uint32_t st = ra.stage * (L::kTileBytes >> 4);
-#pragma unroll
+#pragma unroll 2
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = st + (kk >> 2) * 1024 + (kk & 3) * 2;  // 16 KiB blocks, 32 B steps
             if (leader) mma_ss(tS, ad0 + off, bd0 + off, kId, kk > 0);
           }
-          if (leader) {
-            mma_commit(s_full(i));
-            mma_commit(a_empty(ra.stage));
-          }
+          if (leader) mma_commit(s_full(i));
           __syncwarp();
           ra.advance();
         }
@@ -249,65 +268,69 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       }
     } else if (warp == 2) {
       if constexpr (!SUM) {
-        // ----------------------------------------- O2 = a M, O1 = P c
+        // -------------------------------------------------------- O1 = P c
         const bool leader = elect_one();
         constexpr uint32_t kId = idesc_bf16(128, D, false, true);
         const uint64_t cd0 = sdesc_sw128(sbase + L::kC, kTile * 128, 1024);
-        const uint64_t ad0 = sdesc_sw128(sbase + L::kA, 16, 1024);
-        const uint64_t md = sdesc_sw128(sbase + L::kM, D * 128, 1024);
-        StageRing<AS> ra;
+        StageRing<AS> rc;
         for (int i = 0; i < n_chunks; ++i) {
-          if (!warp_wait(a_full(ra.stage), ra.par, abort, p.status, tmo) ||
-              !warp_wait(c_full(ra.stage), ra.par, abort, p.status, tmo))
-            break;
+          if (!warp_wait(c_full(rc.stage), rc.par, abort, p.status, tmo)) break;
           if (chunk_n(i) < kTile && !warp_wait(fixed, 0, abort, p.status, tmo)) break;
-          // the epilogue of the last chunk has read O1 and O2
+          // the epilogue of the last chunk has read O1
           if (i > 0 && !warp_wait(o_free, (i - 1) & 1, abort, p.status, tmo)) break;
-          if (!warp_wait(m_full, i & 1, abort, p.status, tmo)) break;
-          tc_fence_after();
-          const uint32_t st = ra.stage * (L::kTileBytes >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            if (leader)
-              mma_ss(tO2, ad0 + st + (kk >> 2) * 1024 + (kk & 3) * 2, md + (uint64_t)(kk * 128), kId, kk > 0);
-          if (leader) {
-            mma_commit(m_free);
-            mma_commit(a_empty(ra.stage));
-          }
-          __syncwarp();
           if (!warp_wait(p_full, i & 1, abort, p.status, tmo)) break;
           tc_fence_after();
-#pragma unroll
+          const uint32_t st = rc.stage * (L::kTileBytes >> 4);
+#pragma unroll 2
           for (int kk = 0; kk < kTile / 16; ++kk)
             if (leader) mma_ts(tO1, tS + (kk >> 2) * 64 + (kk & 3) * 8, cd0 + st + (uint64_t)(kk * 128), kId, kk > 0);
           if (leader) {
             mma_commit(o_full);
-            mma_commit(c_empty(ra.stage));
+            mma_commit(c_empty(rc.stage));
           }
           __syncwarp();
-          ra.advance();
+          rc.advance();
         }
         if (leader) mma_commit(fin + 8);
         __syncwarp();
         drain_wait(fin + 8, 0);
       }
     } else {
-      // ------------------------------------- U = (weighted b)^T c: hi, and lo where it counts
+      // --------------- O2 = a M, and U = (weighted b)^T c: hi, and lo where it counts
       const bool leader = elect_one();
-      constexpr uint32_t kId = idesc_bf16(128, D, true, true);
-      // (at D 64 the product's lower 64 rows read what lies behind the tile: nobody reads them)
+      constexpr uint32_t kId = idesc_bf16(128, D, true, true), kId2 = idesc_bf16(128, D, false, true);
+      // (at D 64 U's lower 64 rows read what lies behind the tile: nobody reads them)
       const uint64_t bd0 = sdesc_sw128(sbase + L::kB, kTile * 128, 1024);
       const uint64_t cd0 = sdesc_sw128(sbase + L::kC, kTile * 128, 1024);
+      const uint64_t ad0 = sdesc_sw128(sbase + L::kA, 16, 1024);
+      const uint64_t md = sdesc_sw128(sbase + L::kM, D * 128, 1024);
       StageRing<BS> rb;
       bool ok = true;
       int k = 0;
       for (int i = 0; i < n_chunks && ok; ++i) {
-        if (!(ok = warp_wait(c_full(rb.stage), rb.par, abort, p.status, tmo))) break;
         const uint32_t st = rb.stage * (L::kTileBytes >> 4);
+        if constexpr (!SUM) {
+          // the epilogue of the last chunk has read O2
+          if (!(ok = (i == 0 || warp_wait(o_free, (i - 1) & 1, abort, p.status, tmo)) &&
+                     warp_wait(m_full, i & 1, abort, p.status, tmo) &&
+                     warp_wait(a_full(rb.stage), rb.par, abort, p.status, tmo)))
+            break;
+          tc_fence_after();
+#pragma unroll 2
+          for (int kk = 0; kk < D / 16; ++kk)
+            if (leader)
+              mma_ss(tO2, ad0 + st + (kk >> 2) * 1024 + (kk & 3) * 2, md + (uint64_t)(kk * 128), kId2, kk > 0);
+          if (leader) {
+            mma_commit(m_free);
+            mma_commit(o2_full);
+          }
+          __syncwarp();
+        }
+        if (!(ok = warp_wait(c_full(rb.stage), rb.par, abort, p.status, tmo))) break;
         for (int part = 0; part <= (exact ? 1 : 0); ++part, ++k) {
           if (!(ok = warp_wait(x_full(k), (k >> 1) & 1, abort, p.status, tmo))) break;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 2
           for (int kk = 0; kk < kTile / 16; ++kk)
             if (leader)
               mma_ss(tU(i), bd0 + st + (uint64_t)(kk * 128), cd0 + st + (uint64_t)(kk * 128), kId, part > 0 || kk > 0);
@@ -335,7 +358,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       const int quad = warp & 3, row = quad * 32 + lane, half = warp >> 2 & 1;
       const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
       constexpr int HC = D / 2;
-      const bool aligned32 = (reinterpret_cast<uintptr_t>(w.out) & 31) == 0;
+      StageRing<AS> ra;
       for (int i = 0; i < n_chunks; ++i) {
         const int pos0 = chunk_pos(i), n = chunk_n(i);
         if (!warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo)) break;
@@ -374,13 +397,29 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         tc_fence_before();
         mbar_arrive(p_full);
 
-        if (!warp_wait(o_full, i & 1, abort, p.status, tmo)) break;
+        if (!warp_wait(o_full, i & 1, abort, p.status, tmo) || !warp_wait(o2_full, i & 1, abort, p.status, tmo)) break;
         tc_fence_after();
         const float ow = pw[(back ? n - 1 - min(row, n - 1) : row) + 1 - late] * w.mul;
         const float2 ow2 = make_float2(ow, ow), mul2v = make_float2(w.mul, w.mul);
         const int64_t tile_row0 = (int64_t)bh * p.T + p.m.slot(pos0);
         const bool store = row < n && in_bounds(tile_row0 + row, 1, rows_q, p.status);
         const int64_t at = (tile_row0 + row) * D + half * HC;
+        // whole chunks go by way of shared memory (bf16 rows of D 64 are half lines and do not): this
+        // warp's 32 lines of 128 bytes, 64 bf16 or 32 float32 columns, swizzled as the map has it
+        const bool staged = n == kTile && (D == 128 || w.out_f32);
+        const int area = (D == 128 ? L::kA + ra.stage * L::kTileBytes : L::kO) + (quad * 2 + half) * 4096;
+        uint4* const line = reinterpret_cast<uint4*>(smem + area) + lane * 8;
+        auto leave = [&](int col) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (in_bounds(tile_row0 + quad * 32, 32, rows_q, p.status))
+              tma_store_2d(&maps.o, half * HC + col, (int)(tile_row0 + quad * 32), sbase + area);
+            bulk_commit_group();
+            bulk_wait_read_all();
+          }
+          __syncwarp();
+        };
 #pragma unroll 1
         for (int c = 0; c < HC / 16; ++c) {
           uint32_t o1[16], o2[16];
@@ -396,28 +435,31 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           for (int j = 0; j < 8; ++j)
             v[j] = fma2(ow2, make_float2(__uint_as_float(o2[2 * j]), __uint_as_float(o2[2 * j + 1])),
                         mul2(mul2v, make_float2(__uint_as_float(o1[2 * j]), __uint_as_float(o1[2 * j + 1]))));
-          if (!store) continue;
           if (w.out_f32) {
-            float* dst = static_cast<float*>(w.out) + at + c * 16;  // (the workspace's: aligned)
+            float4* const dst = reinterpret_cast<float4*>(static_cast<float*>(w.out) + at) + c * 4;
 #pragma unroll
-            for (int j = 0; j < 8; j += 4)
-              store32(dst + 2 * j, __float_as_uint(v[j].x), __float_as_uint(v[j].y), __float_as_uint(v[j + 1].x),
-                      __float_as_uint(v[j + 1].y), __float_as_uint(v[j + 2].x), __float_as_uint(v[j + 2].y),
-                      __float_as_uint(v[j + 3].x), __float_as_uint(v[j + 3].y));
+            for (int j = 0; j < 4; ++j) {
+              const float4 x = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+              if (staged) reinterpret_cast<float4*>(line)[((c & 1) * 4 + j) ^ (lane & 7)] = x;
+              else if (store) dst[j] = x;
+            }
+            if (staged && (c & 1)) leave((c >> 1) * 32);
           } else {
-            uint32_t u[8];
+            uint4* const dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(w.out) + at) + c * 2;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] = pack_bf16(v[j].x, v[j].y);
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(w.out) + at + c * 16;
-            if (aligned32) {
-              store32(dst, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
-            } else {
-              reinterpret_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-              reinterpret_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+            for (int j = 0; j < 2; ++j) {
+              const uint4 x = make_uint4(pack_bf16(v[4 * j].x, v[4 * j].y), pack_bf16(v[4 * j + 1].x, v[4 * j + 1].y),
+                                         pack_bf16(v[4 * j + 2].x, v[4 * j + 2].y), pack_bf16(v[4 * j + 3].x, v[4 * j + 3].y));
+              if (staged) line[(c * 2 + j) ^ (lane & 7)] = x;
+              else if (store) dst[j] = x;
             }
           }
         }
+        if (staged && !w.out_f32) leave(0);
+        if (lane == 0) mbar_arrive(a_empty(ra.stage));
+        ra.advance();
       }
+      if (lane == 0) bulk_wait_all();
     }
   } else {
     if constexpr (!SUM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
@@ -604,9 +646,17 @@ static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, cudaStrea
     const int64_t hq = (int64_t)p.B * p.Hq;
     if (!make_map(&m.b, w.b, hq / w.rep_b, p.T, D) || !make_map(&m.c, w.c, hq / w.rep_c, p.T, D))
       return cudaErrorInvalidValue;
-    m.a = m.b;
+    m.a = m.o = m.b;
     if (!SUM && !make_map(&m.a, w.a, hq / w.rep_a, p.T, D)) return cudaErrorInvalidValue;
   }
+  if (!SUM)  // the output's boxes: one warp's 32 rows, a 128-byte line each
+    for (int i = 0; i < n; ++i) {
+      const LinSweep& w = sweeps[i];
+      const uint64_t rows = (uint64_t)p.B * p.Hq * p.T;
+      if ((w.out_f32 ? encode_tmap_2d_f32(&prm.maps[i].o, w.out, D, rows, 32, 32)
+                     : encode_tmap_2d_bf16(&prm.maps[i].o, w.out, D, rows, 64, 32)) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    }
   constexpr int kSmem = Smem<D, SUM>::kBytes, kThreads = SUM ? kThreadsSum : kThreadsOut;
   auto kern = sweep_kernel<D, SUM>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
