@@ -19,9 +19,9 @@
 // Warp roles (640 threads):
 //   warp 0        TMA producer: the tiles a, b, c of a chunk, two stages each
 //   warp 1        issues S;  warp 2: O1;  warp 3: O2 and U
-//   warps 4-11    the output, two threads a row: S -> P, then the epilogue, staged in the chunk's own
-//                 a tile, which nothing reads any more, and out by TMA (stored from registers, every
-//                 instruction touches 32 lines, and the loads from TMEM queued behind them)
+//   warps 4-11    the output, two threads a row: S -> P, then the epilogue.  bf16 is stored from
+//                 registers in whole 32-byte sectors; float32, twice as much, is staged in the
+//                 chunk's own c tile, which nothing reads any more, and leaves by TMA
 //   warps 12-19   the state, two threads a row: b times its weights, M, its bf16 copy
 // Issuers are whole warps with one elected lane, as in tc_fwd.cu.  TMEM: S/P [0, 128),
 // O1, O2 and U of D columns each behind it.
@@ -57,7 +57,7 @@ struct Smem {
   static constexpr int kB = kA + kAS * kTileBytes;
   static constexpr int kC = kB + kBS * kTileBytes;
   static constexpr int kM = kC + kBS * kTileBytes;
-  // the output's staging, 4 KB a warp: at D 128 the a tile; at D 64 that is too small for float32
+  // the output's staging, 4 KB a warp: at D 128 the c tile, at D 64 that is too small
   static constexpr int kO = kM + (SUM ? 0 : D * D * 2);
   static constexpr int kPow = kO + (SUM || D == 128 ? 0 : 8 * 4096);
   // powers r^e at kPow + 4 (128 + e), zeros for e < 0
@@ -123,6 +123,14 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t par) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// 32 bytes, a whole sector, aligned.
+__device__ __forceinline__ void store32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
+                                        uint32_t f, uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d),
+               "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
+
 template <int D, bool SUM>
 __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
     sweep_kernel(const __grid_constant__ Params prm) {
@@ -179,9 +187,10 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) mbar_init(bars + 8 * i, 1);
-    // a_empty: the eight warps that stage the output there; c_empty: O1 and U; the rest by threads
-    for (int i = 0; i < AS; ++i) mbar_init(a_empty(i), 8);
-    for (int i = 0; i < BS; ++i) mbar_init(c_empty(i), SUM ? 1 : 2);
+    // a_empty: S and O2; c_empty: U and the eight warps that may stage the output there; the rest by
+    // threads
+    for (int i = 0; i < AS; ++i) mbar_init(a_empty(i), 2);
+    for (int i = 0; i < BS; ++i) mbar_init(c_empty(i), SUM ? 1 : 9);
     for (int i = 0; i < 2; ++i) mbar_init(x_full(i), 256);
     mbar_init(p_full, 256);
     mbar_init(o_free, 256);
@@ -253,12 +262,15 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           if (chunk_n(i) < kTile && !warp_wait(fixed, 0, abort, p.status, tmo)) break;
           tc_fence_after();
           const uint32_t st = ra.stage * (L::kTileBytes >> 4);
-#pragma unroll 2
+#pragma unroll 4
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = st + (kk >> 2) * 1024 + (kk & 3) * 2;  // 16 KiB blocks, 32 B steps
             if (leader) mma_ss(tS, ad0 + off, bd0 + off, kId, kk > 0);
           }
-          if (leader) mma_commit(s_full(i));
+          if (leader) {
+            mma_commit(s_full(i));
+            mma_commit(a_empty(ra.stage));
+          }
           __syncwarp();
           ra.advance();
         }
@@ -281,13 +293,10 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           if (!warp_wait(p_full, i & 1, abort, p.status, tmo)) break;
           tc_fence_after();
           const uint32_t st = rc.stage * (L::kTileBytes >> 4);
-#pragma unroll 2
+#pragma unroll 4
           for (int kk = 0; kk < kTile / 16; ++kk)
             if (leader) mma_ts(tO1, tS + (kk >> 2) * 64 + (kk & 3) * 8, cd0 + st + (uint64_t)(kk * 128), kId, kk > 0);
-          if (leader) {
-            mma_commit(o_full);
-            mma_commit(c_empty(rc.stage));
-          }
+          if (leader) mma_commit(o_full);
           __syncwarp();
           rc.advance();
         }
@@ -316,13 +325,14 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
                      warp_wait(a_full(rb.stage), rb.par, abort, p.status, tmo)))
             break;
           tc_fence_after();
-#pragma unroll 2
+#pragma unroll 4
           for (int kk = 0; kk < D / 16; ++kk)
             if (leader)
               mma_ss(tO2, ad0 + st + (kk >> 2) * 1024 + (kk & 3) * 2, md + (uint64_t)(kk * 128), kId2, kk > 0);
           if (leader) {
             mma_commit(m_free);
             mma_commit(o2_full);
+            mma_commit(a_empty(rb.stage));
           }
           __syncwarp();
         }
@@ -330,7 +340,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         for (int part = 0; part <= (exact ? 1 : 0); ++part, ++k) {
           if (!(ok = warp_wait(x_full(k), (k >> 1) & 1, abort, p.status, tmo))) break;
           tc_fence_after();
-#pragma unroll 2
+#pragma unroll 4
           for (int kk = 0; kk < kTile / 16; ++kk)
             if (leader)
               mma_ss(tU(i), bd0 + st + (uint64_t)(kk * 128), cd0 + st + (uint64_t)(kk * 128), kId, part > 0 || kk > 0);
@@ -358,7 +368,8 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       const int quad = warp & 3, row = quad * 32 + lane, half = warp >> 2 & 1;
       const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
       constexpr int HC = D / 2;
-      StageRing<AS> ra;
+      const bool aligned32 = (reinterpret_cast<uintptr_t>(w.out) & 31) == 0;
+      StageRing<BS> rc;
       for (int i = 0; i < n_chunks; ++i) {
         const int pos0 = chunk_pos(i), n = chunk_n(i);
         if (!warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo)) break;
@@ -398,28 +409,17 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         mbar_arrive(p_full);
 
         if (!warp_wait(o_full, i & 1, abort, p.status, tmo) || !warp_wait(o2_full, i & 1, abort, p.status, tmo)) break;
+        // float32 chunks, where whole, go by way of shared memory: over c, which U has read then
+        const bool staged = w.out_f32 && n == kTile;
+        if (staged && !warp_wait(u_full(i), (i >> 1) & 1, abort, p.status, tmo)) break;
         tc_fence_after();
         const float ow = pw[(back ? n - 1 - min(row, n - 1) : row) + 1 - late] * w.mul;
         const float2 ow2 = make_float2(ow, ow), mul2v = make_float2(w.mul, w.mul);
         const int64_t tile_row0 = (int64_t)bh * p.T + p.m.slot(pos0);
         const bool store = row < n && in_bounds(tile_row0 + row, 1, rows_q, p.status);
         const int64_t at = (tile_row0 + row) * D + half * HC;
-        // whole chunks go by way of shared memory (bf16 rows of D 64 are half lines and do not): this
-        // warp's 32 lines of 128 bytes, 64 bf16 or 32 float32 columns, swizzled as the map has it
-        const bool staged = n == kTile && (D == 128 || w.out_f32);
-        const int area = (D == 128 ? L::kA + ra.stage * L::kTileBytes : L::kO) + (quad * 2 + half) * 4096;
-        uint4* const line = reinterpret_cast<uint4*>(smem + area) + lane * 8;
-        auto leave = [&](int col) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (in_bounds(tile_row0 + quad * 32, 32, rows_q, p.status))
-              tma_store_2d(&maps.o, half * HC + col, (int)(tile_row0 + quad * 32), sbase + area);
-            bulk_commit_group();
-            bulk_wait_read_all();
-          }
-          __syncwarp();
-        };
+        // this warp's 32 lines of 128 bytes, 32 columns, swizzled as the tensor map has it
+        const int area = (D == 128 ? L::kC + rc.stage * L::kTileBytes : L::kO) + (quad * 2 + half) * 4096;
 #pragma unroll 1
         for (int c = 0; c < HC / 16; ++c) {
           uint32_t o1[16], o2[16];
@@ -436,28 +436,39 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
             v[j] = fma2(ow2, make_float2(__uint_as_float(o2[2 * j]), __uint_as_float(o2[2 * j + 1])),
                         mul2(mul2v, make_float2(__uint_as_float(o1[2 * j]), __uint_as_float(o1[2 * j + 1]))));
           if (w.out_f32) {
-            float4* const dst = reinterpret_cast<float4*>(static_cast<float*>(w.out) + at) + c * 4;
+            float4* const dst = staged ? reinterpret_cast<float4*>(smem + area) + lane * 8
+                                       : reinterpret_cast<float4*>(static_cast<float*>(w.out) + at) + c * 4;
+            const int slot = staged ? (c & 1) * 4 : 0, swz = staged ? lane & 7 : 0;
+            if (staged || store)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 x = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
-              if (staged) reinterpret_cast<float4*>(line)[((c & 1) * 4 + j) ^ (lane & 7)] = x;
-              else if (store) dst[j] = x;
+              for (int j = 0; j < 4; ++j)
+                dst[(slot + j) ^ swz] = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+            if (staged && (c & 1)) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (in_bounds(tile_row0 + quad * 32, 32, rows_q, p.status))
+                  tma_store_2d(&maps.o, half * HC + (c >> 1) * 32, (int)(tile_row0 + quad * 32), sbase + area);
+                bulk_commit_group();
+                bulk_wait_read_all();
+              }
+              __syncwarp();
             }
-            if (staged && (c & 1)) leave((c >> 1) * 32);
-          } else {
-            uint4* const dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(w.out) + at) + c * 2;
+          } else if (store) {
+            uint32_t u[8];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint4 x = make_uint4(pack_bf16(v[4 * j].x, v[4 * j].y), pack_bf16(v[4 * j + 1].x, v[4 * j + 1].y),
-                                         pack_bf16(v[4 * j + 2].x, v[4 * j + 2].y), pack_bf16(v[4 * j + 3].x, v[4 * j + 3].y));
-              if (staged) line[(c * 2 + j) ^ (lane & 7)] = x;
-              else if (store) dst[j] = x;
+            for (int j = 0; j < 8; ++j) u[j] = pack_bf16(v[j].x, v[j].y);
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(w.out) + at + c * 16;
+            if (aligned32) {
+              store32(dst, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
+            } else {
+              reinterpret_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+              reinterpret_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
             }
           }
         }
-        if (staged && !w.out_f32) leave(0);
-        if (lane == 0) mbar_arrive(a_empty(ra.stage));
-        ra.advance();
+        if (lane == 0) mbar_arrive(c_empty(rc.stage));
+        rc.advance();
       }
       if (lane == 0) bulk_wait_all();
     }
@@ -649,14 +660,11 @@ static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, cudaStrea
     m.a = m.o = m.b;
     if (!SUM && !make_map(&m.a, w.a, hq / w.rep_a, p.T, D)) return cudaErrorInvalidValue;
   }
-  if (!SUM)  // the output's boxes: one warp's 32 rows, a 128-byte line each
-    for (int i = 0; i < n; ++i) {
-      const LinSweep& w = sweeps[i];
-      const uint64_t rows = (uint64_t)p.B * p.Hq * p.T;
-      if ((w.out_f32 ? encode_tmap_2d_f32(&prm.maps[i].o, w.out, D, rows, 32, 32)
-                     : encode_tmap_2d_bf16(&prm.maps[i].o, w.out, D, rows, 64, 32)) != CUDA_SUCCESS)
+  if (!SUM)  // a float32 output's boxes: one warp's 32 rows, a 128-byte line each
+    for (int i = 0; i < n; ++i)
+      if (sweeps[i].out_f32 && encode_tmap_2d_f32(&prm.maps[i].o, sweeps[i].out, D, (uint64_t)p.B * p.Hq * p.T, 32,
+                                                  32) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    }
   constexpr int kSmem = Smem<D, SUM>::kBytes, kThreads = SUM ? kThreadsSum : kThreadsOut;
   auto kern = sweep_kernel<D, SUM>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
