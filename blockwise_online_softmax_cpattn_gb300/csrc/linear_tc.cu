@@ -227,10 +227,11 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
             mbar_expect_tx(full, L::kTileBytes);
             const int row = head * p.T + slot;
             // (a partial chunk reads on into the next head, or zeros behind the tensor)
-            if (in_bounds(row, 1, (int64_t)heads * p.T, p.status) && !(p.debug_fault && i == 0))
+            if (in_bounds(row, 1, (int64_t)heads * p.T, p.status) && !(p.debug_fault && i == 0)) {
               for (int kb = 0; kb < D / 64; ++kb)
                 tma_load_2d(sbase + base + ring.stage * L::kTileBytes + kb * (kTile * 128), tm, kb * 64, row, full);
-            ring.mark_issued();
+              ring.mark_issued();
+            }
             ring.advance();
           };
           load(rb, b_full(rb.stage), b_empty(rb.stage), L::kB, &maps.b, head_b, p.B * (p.Hq / w.rep_b));
