@@ -337,9 +337,7 @@ cpattn_status cpattn_linear_bwd(const cpattn_desc* desc, const void* q, const vo
   cudaError_t e = tc ? launch_linear_tc(p, st, true) : launch_linear_simt(p, st, true);
   if (e != cudaSuccess || rep == 1) return from_cuda(e);
   const int64_t groups = (int64_t)R.B * R.Hkv, row = (int64_t)R.T * R.D;
-  e = launch_linear_group(groups, rep, row, part_v, dv, R.bf16, st);
-  if (e == cudaSuccess) e = launch_linear_group(groups, rep, row, part_k, dk, R.bf16, st);
-  return from_cuda(e);
+  return from_cuda(launch_linear_group(groups, rep, row, part_v, part_k, dv, dk, R.bf16, st));
 }
 
 cpattn_status cpattn_linear_step(const cpattn_desc* desc, int n_states, const void* q,

@@ -124,9 +124,9 @@ constexpr int kLinSimtChunk = 64;
 bool linear_tc_supported(const Ring& R);
 cudaError_t launch_linear_tc(const Linear& p, cudaStream_t st, bool backward);
 cudaError_t launch_linear_simt(const Linear& p, cudaStream_t st, bool backward);
-// out[b][g][t][:] = sum over the group's n_rep query heads of part[b][g n_rep + r][t][:].
-cudaError_t launch_linear_group(int64_t groups, int n_rep, int64_t row_elems, const float* part,
-                                void* out, int bf16, cudaStream_t st);
+// dv[b][g][t][:] = sum over the group's n_rep query heads of part_v[b][g n_rep + r][t][:]; dk alike.
+cudaError_t launch_linear_group(int64_t groups, int n_rep, int64_t row_elems, const float* part_v,
+                                const float* part_k, void* dv, void* dk, int bf16, cudaStream_t st);
 
 // ---- linear_step.cu -----------------------------------------------------------
 struct LinStep {

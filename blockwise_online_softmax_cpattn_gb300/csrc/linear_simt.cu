@@ -71,28 +71,39 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
   const int64_t hc = (int64_t)b * (p.Hq / w.rep_c) + h / w.rep_c;
   for (int i = threadIdx.x; i <= C + 1; i += kThreads) pw[i] = lin_pow(ld, i);
 
-  // M of this thread: rows 4 ty + 64 i + x, columns 4 tx + 64 j + y
-  float M[R][4][R][4];
+  // M of this thread: rows 4 ty + 64 i + x, columns 4 tx + 64 j + 2 y and the next
+  float2 M[R][4][R][2] = {};
   const int64_t DD = (int64_t)p.D * p.D;
+  if (!SUM) {
+    // M = f M + g (a state, as it lies or transposed), a vector of four numbers at a time
+    auto fold = [&](float f, float g, const float* src) {
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+      for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+        for (int j = 0; j < R; ++j) {
+          const int r = 4 * ty + 64 * i, c = 4 * tx + 64 * j;
+          if (r >= p.D || c >= p.D) continue;
+          float v[4][4];
 #pragma unroll
-      for (int j = 0; j < R; ++j)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int r = 4 * ty + 64 * i + x, c = 4 * tx + 64 * j + y;
-          float m = 0.f;
-          if (!SUM && r < p.D && c < p.D) {
-            const int64_t at = w.trans ? (int64_t)c * p.D + r : (int64_t)r * p.D + c;
-            if (w.init) m = w.init[bh * DD + at] * w.init_mul;
-            for (int s = 0; s < run; ++s)
-              m = fmaf(lin_pow(ld, lin_run_tokens<C>(p, n_tok, w.back, s)), m,
-                       w.sums[((int64_t)bh * p.segs + s) * DD + at]);
+          for (int x = 0; x < 4; ++x) {
+            const float4 u = *reinterpret_cast<const float4*>(
+                src + (w.trans ? (int64_t)(c + x) * p.D + r : (int64_t)(r + x) * p.D + c));
+            v[x][0] = u.x, v[x][1] = u.y, v[x][2] = u.z, v[x][3] = u.w;
           }
-          M[i][x][j][y] = m;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float2& m = M[i][x][j][y];
+              m.x = fmaf(f, m.x, g * (w.trans ? v[2 * y][x] : v[x][2 * y]));
+              m.y = fmaf(f, m.y, g * (w.trans ? v[2 * y + 1][x] : v[x][2 * y + 1]));
+            }
         }
+    };
+    if (w.init) fold(0.f, w.init_mul, w.init + bh * DD);
+    for (int s = 0; s < run; ++s)
+      fold(lin_pow(ld, lin_run_tokens<C>(p, n_tok, w.back, s)), 1.f, w.sums + ((int64_t)bh * p.segs + s) * DD);
+  }
 
   const int m1 = min((run + 1) * p.cps, p.nch);
   for (int m = run * p.cps; m < m1; ++m) {
@@ -109,14 +120,14 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
 #pragma unroll
           for (int j = 0; j < R; ++j)
             *reinterpret_cast<float4*>(sM + (4 * ty + 64 * i + x) * LD + 4 * tx + 64 * j) =
-                make_float4(M[i][x][j][0], M[i][x][j][1], M[i][x][j][2], M[i][x][j][3]);
+                make_float4(M[i][x][j][0].x, M[i][x][j][0].y, M[i][x][j][1].x, M[i][x][j][1].y);
     }
     load_tile<E, DP>(p, w.b, hb, pos0, n, sb);
     load_tile<E, DP>(p, w.c, hc, pos0, n, sc);
     __syncthreads();
     if (!SUM) {
-      float s[4][4] = {};  // rows ty + 16 i, columns tx + 16 j
-#pragma unroll 4
+      float2 s2[4][4] = {};  // rows ty + 16 i, columns tx + 16 j; even and odd channels apart
+#pragma unroll 2
       for (int d = 0; d < DP; d += 4) {
         float4 a[4], v[4];
 #pragma unroll
@@ -127,8 +138,10 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            s[i][j] = fmaf(a[i].w, v[j].w, fmaf(a[i].z, v[j].z, fmaf(a[i].y, v[j].y, fmaf(a[i].x, v[j].x, s[i][j]))));
+          for (int j = 0; j < 4; ++j) {
+            s2[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(v[j].x, v[j].y), s2[i][j]);
+            s2[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(v[j].z, v[j].w), s2[i][j]);
+          }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -136,44 +149,37 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
         for (int j = 0; j < 4; ++j) {
           const int row = ty + 16 * i, col = tx + 16 * j;
           const int e = w.back ? col - row : row - col;
-          sp[row * PL + col] = e >= 0 ? s[i][j] * pw[e] : 0.f;
+          sp[row * PL + col] = e >= 0 ? (s2[i][j].x + s2[i][j].y) * pw[e] : 0.f;
         }
       __syncthreads();
-      float o[4][R][4] = {}, t[4][R][4] = {};  // rows ty + 16 i, columns 4 tx + 64 j + y
-#pragma unroll 4
-      for (int k = 0; k < C; ++k) {
-        float4 v[R];
+      float2 o[4][R][2] = {}, t[4][R][2] = {};  // rows ty + 16 i, columns 4 tx + 64 j + 2 y
+      // x[row][k] m[k][columns] over k, four of them a step: their rows of x come as one vector
+      auto product = [&](float2(&acc)[4][R][2], const float* x, int ldx, const float* m, int K) {
+#pragma unroll 2
+        for (int k = 0; k < K; k += 4) {
+          float4 xr[4];
 #pragma unroll
-        for (int j = 0; j < R; ++j) v[j] = *reinterpret_cast<const float4*>(sc + k * LD + 4 * tx + 64 * j);
+          for (int i = 0; i < 4; ++i) xr[i] = *reinterpret_cast<const float4*>(x + (ty + 16 * i) * ldx + k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = sp[(ty + 16 * i) * PL + k];
+          for (int kk = 0; kk < 4; ++kk) {
+            float4 v[R];
 #pragma unroll
-          for (int j = 0; j < R; ++j) {
-            o[i][j][0] = fmaf(x, v[j].x, o[i][j][0]);
-            o[i][j][1] = fmaf(x, v[j].y, o[i][j][1]);
-            o[i][j][2] = fmaf(x, v[j].z, o[i][j][2]);
-            o[i][j][3] = fmaf(x, v[j].w, o[i][j][3]);
+            for (int j = 0; j < R; ++j) v[j] = *reinterpret_cast<const float4*>(m + (k + kk) * LD + 4 * tx + 64 * j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float f = kk == 0 ? xr[i].x : kk == 1 ? xr[i].y : kk == 2 ? xr[i].z : xr[i].w;
+              const float2 f2 = make_float2(f, f);
+#pragma unroll
+              for (int j = 0; j < R; ++j) {
+                acc[i][j][0] = fma2(f2, make_float2(v[j].x, v[j].y), acc[i][j][0]);
+                acc[i][j][1] = fma2(f2, make_float2(v[j].z, v[j].w), acc[i][j][1]);
+              }
+            }
           }
         }
-      }
-#pragma unroll 4
-      for (int k = 0; k < DP; ++k) {
-        float4 v[R];
-#pragma unroll
-        for (int j = 0; j < R; ++j) v[j] = *reinterpret_cast<const float4*>(sM + k * LD + 4 * tx + 64 * j);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = sa[(ty + 16 * i) * LD + k];
-#pragma unroll
-          for (int j = 0; j < R; ++j) {
-            t[i][j][0] = fmaf(x, v[j].x, t[i][j][0]);
-            t[i][j][1] = fmaf(x, v[j].y, t[i][j][1]);
-            t[i][j][2] = fmaf(x, v[j].z, t[i][j][2]);
-            t[i][j][3] = fmaf(x, v[j].w, t[i][j][3]);
-          }
-        }
-      }
+      };
+      product(o, sp, PL, sc, C);
+      product(t, sa, LD, sM, DP);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = ty + 16 * i;
@@ -184,14 +190,14 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
         for (int j = 0; j < R; ++j) {
           const int c = 4 * tx + 64 * j;
           if (c >= p.D) continue;
-          const float4 y = make_float4(w.mul * fmaf(ow, t[i][j][0], o[i][j][0]), w.mul * fmaf(ow, t[i][j][1], o[i][j][1]),
-                                       w.mul * fmaf(ow, t[i][j][2], o[i][j][2]), w.mul * fmaf(ow, t[i][j][3], o[i][j][3]));
+          const float4 y = make_float4(w.mul * fmaf(ow, t[i][j][0].x, o[i][j][0].x), w.mul * fmaf(ow, t[i][j][0].y, o[i][j][0].y),
+                                       w.mul * fmaf(ow, t[i][j][1].x, o[i][j][1].x), w.mul * fmaf(ow, t[i][j][1].y, o[i][j][1].y));
           if (w.out_f32) store4(static_cast<float*>(w.out) + at + c, y);
           else store4(static_cast<E*>(w.out) + at + c, y);
         }
       }
     }
-    const float rn = pw[n];
+    const float2 rn = make_float2(pw[n], pw[n]);
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -199,26 +205,29 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
 #pragma unroll
         for (int j = 0; j < R; ++j)
 #pragma unroll
-          for (int y = 0; y < 4; ++y) M[i][x][j][y] *= rn;
+          for (int y = 0; y < 2; ++y) M[i][x][j][y] = mul2(M[i][x][j][y], rn);
 #pragma unroll 2
     for (int k = 0; k < n; ++k) {
       const float uw = pw[(w.back ? k : n - 1 - k) + late];
-      float v[R][4], u[R][4];
+      float2 v[R][2];
+      float u[R][4];
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         const float4 x = *reinterpret_cast<const float4*>(sc + k * LD + 4 * tx + 64 * j);
-        v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+        v[j][0] = make_float2(x.x, x.y), v[j][1] = make_float2(x.z, x.w);
         const float4 y = *reinterpret_cast<const float4*>(sb + k * LD + 4 * ty + 64 * j);
         u[j][0] = uw * y.x, u[j][1] = uw * y.y, u[j][2] = uw * y.z, u[j][3] = uw * y.w;
       }
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int x = 0; x < 4; ++x) {
+          const float2 f2 = make_float2(u[i][x], u[i][x]);
 #pragma unroll
           for (int j = 0; j < R; ++j)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) M[i][x][j][y] = fmaf(u[i][x], v[j][y], M[i][x][j][y]);
+            for (int y = 0; y < 2; ++y) M[i][x][j][y] = fma2(f2, v[j][y], M[i][x][j][y]);
+        }
     }
   }
 
@@ -235,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
         const int r = 4 * ty + 64 * i + x, c = 4 * tx + 64 * j;
         if (r < p.D && c < p.D)
           store4(dst + (int64_t)r * p.D + c,
-                 make_float4(M[i][x][j][0] * mul, M[i][x][j][1] * mul, M[i][x][j][2] * mul, M[i][x][j][3] * mul));
+                 make_float4(M[i][x][j][0].x * mul, M[i][x][j][0].y * mul, M[i][x][j][1].x * mul, M[i][x][j][1].y * mul));
       }
 }
 
@@ -263,14 +272,19 @@ static cudaError_t launch(const Linear& p, cudaStream_t st, const char* sums, co
   return e;
 }
 
+// blockIdx.y: dv or dk.
 template <typename E>
-__global__ void __launch_bounds__(256) group_kernel(int64_t n4, int n_rep, int64_t row4,
-                                                    const float4* part, E* out) {
+__global__ void __launch_bounds__(256) group_kernel(int64_t n4, int n_rep, int64_t row4, const float4* part_v,
+                                                    const float4* part_k, E* dv, E* dk) {
+  const float4* part = blockIdx.y ? part_k : part_v;
+  E* out = blockIdx.y ? dk : dv;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
-    const int64_t g = i / row4, at = i - g * row4;
-    float4 s = __ldcs(part + g * n_rep * row4 + at);
+    const int64_t g = i / row4;
+    const float4* src = part + g * (n_rep - 1) * row4 + i;
+    float4 s = __ldcs(src);
+#pragma unroll 4
     for (int r = 1; r < n_rep; ++r) {
-      const float4 x = __ldcs(part + (g * n_rep + r) * row4 + at);
+      const float4 x = __ldcs(src + r * row4);
       s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
     }
     store4(out + 4 * i, s);
@@ -289,20 +303,19 @@ cudaError_t launch_linear_simt(const Linear& p, cudaStream_t st, bool backward) 
                    : linsimt::launch<float, 128>(p, st, sums, sweeps);
 }
 
-cudaError_t launch_linear_group(int64_t groups, int n_rep, int64_t row_elems, const float* part,
-                                void* out, int bf16, cudaStream_t st) {
+cudaError_t launch_linear_group(int64_t groups, int n_rep, int64_t row_elems, const float* part_v,
+                                const float* part_k, void* dv, void* dk, int bf16, cudaStream_t st) {
   const int64_t n4 = groups * row_elems / 4;
   const int64_t want = (n4 + 255) / 256, most = 16 * kSms;
-  const unsigned grid = (unsigned)(want < most ? want : most);
+  const dim3 grid((unsigned)(want < most ? want : most), 2);
+  const float4 *pv = reinterpret_cast<const float4*>(part_v), *pk = reinterpret_cast<const float4*>(part_k);
   timing_begin("linear_group", st);
   if (bf16)
-    linsimt::group_kernel<<<grid, 256, 0, st>>>(n4, n_rep, row_elems / 4,
-                                                reinterpret_cast<const float4*>(part),
-                                                static_cast<__nv_bfloat16*>(out));
+    linsimt::group_kernel<<<grid, 256, 0, st>>>(n4, n_rep, row_elems / 4, pv, pk, static_cast<__nv_bfloat16*>(dv),
+                                                static_cast<__nv_bfloat16*>(dk));
   else
-    linsimt::group_kernel<<<grid, 256, 0, st>>>(n4, n_rep, row_elems / 4,
-                                                reinterpret_cast<const float4*>(part),
-                                                static_cast<float*>(out));
+    linsimt::group_kernel<<<grid, 256, 0, st>>>(n4, n_rep, row_elems / 4, pv, pk, static_cast<float*>(dv),
+                                                static_cast<float*>(dk));
   const cudaError_t e = cudaGetLastError();
   timing_end(st);
   return e;
