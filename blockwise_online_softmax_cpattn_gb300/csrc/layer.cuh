@@ -72,7 +72,7 @@ struct LinSweep {
   int out_f32;
   float* fin;  // M behind the last run, times fin_mul, or null
   float fin_mul;
-  int exact;   // M is handed out in the end: products on bf16 pairs
+  int exact;   // M is handed out in the end
 };
 
 constexpr int kMaxSweeps = 3;
@@ -95,7 +95,12 @@ __device__ __forceinline__ float lin_decay(const Linear& p, int bh) {
   const int b = bh / p.Hq, h = bh - b * p.Hq;
   return fminf(p.log_decay[(b / p.B_user) * p.Hq + h], 0.f);  // (of a NaN: 0)
 }
-__device__ __forceinline__ float lin_pow(float ld, int n) { return n == 0 ? 1.f : expf(ld * n); }
+// (the product's rounding, up to 2^-24 of the exponent, is made good)
+__device__ __forceinline__ float lin_pow(float ld, int n) {
+  if (n == 0) return 1.f;
+  const float x = ld * n, e = expf(x);
+  return x < -80.f ? e : fmaf(e, fmaf(ld, (float)n, -x), e);
+}
 
 __device__ __forceinline__ int lin_tokens(const Linear& p, int bh) {
   if (!p.lengths) return p.T;

@@ -10,11 +10,13 @@
 //   M = w(n) M + U
 //
 // M itself stays in float32, in registers (two threads a row, one channel of b).  b is weighted in
-// its place in shared memory once S has read it.  As operands P, M and the weighted b are rounded
-// to bf16 once, like the output itself.  Where a state is handed out (`exact`), the weighted b is
-// taken as two bf16 numbers, hi + lo, and U as the sum of two products: a single rounding would
-// leave 2^-9 in a float32 result.  U starts from zero in every chunk, so no sum on the tensor
-// cores runs longer than 256 terms.
+// its place in shared memory once S has read it, as two bf16 numbers one after the other, hi and
+// then what is left, and U is the sum of two products: 16 bits.  For a state that is handed out in
+// float32, in the sums and in the sequence's last run, it is three, 24 bits.  As operands P and M
+// are rounded to bf16 once, like the output itself.  Errors against float64, of the norm (8192
+// tokens, D 128): outputs 2.3e-3, of which the output's own rounding is 1.7e-3 (2.6e-3 with b in
+// one part, 15 % faster); states 2.4e-6 with two parts.  U starts from zero in every chunk, so no
+// sum on the tensor cores runs longer than 384 terms.
 //
 // Warp roles (640 threads):
 //   warp 0        TMA producer: the tiles a, b, c of a chunk, two stages each
@@ -131,6 +133,30 @@ __device__ __forceinline__ void store32(void* p, uint32_t a, uint32_t b, uint32_
                : "memory");
 }
 
+// What is left of a weighted row after the parts above: m1, m2 are -1 for each part taken away, else
+// 0.  (The row's registers are made opaque, so that what is formed of them for one part is not kept
+// for the next: that spilled 1.6 KB a thread.)
+template <int N>
+__device__ __forceinline__ void third(uint4 (&raw)[N], uint4* line, int chunk0, int row, float2 uw2, float m1, float m2) {
+  const float2 m12 = make_float2(m1, m1), m22 = make_float2(m2, m2);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    asm volatile("" : "+r"(raw[j].x), "+r"(raw[j].y), "+r"(raw[j].z), "+r"(raw[j].w));
+    const uint32_t in[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+    uint32_t out[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float2 v = mul2(make_float2(bf16_lo(in[q]), bf16_hi(in[q])), uw2);
+      uint32_t h = pack_bf16(v.x, v.y);
+      v = fma2(make_float2(bf16_lo(h), bf16_hi(h)), m12, v);
+      h = pack_bf16(v.x, v.y);
+      v = fma2(make_float2(bf16_lo(h), bf16_hi(h)), m22, v);
+      out[q] = pack_bf16(v.x, v.y);
+    }
+    line[(chunk0 + j) ^ (row & 7)] = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
 template <int D, bool SUM>
 __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
     sweep_kernel(const __grid_constant__ Params prm) {
@@ -172,7 +198,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
   const int n_tok = lin_tokens(p, bh);
   const float ld = lin_decay(p, bh);
   const int back = w.back, late = back;
-  const bool exact = w.exact;
+  const int parts = w.exact && (SUM || run == p.segs - 1) ? 3 : 2;  // bf16 numbers of a weighted b
   const int bb = bh / p.Hq, h = bh - bb * p.Hq;
   const int head_a = bb * (p.Hq / w.rep_a) + h / w.rep_a;
   const int head_b = bb * (p.Hq / w.rep_b) + h / w.rep_b;
@@ -306,7 +332,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         drain_wait(fin + 8, 0);
       }
     } else {
-      // --------------- O2 = a M, and U = (weighted b)^T c: hi, and lo where it counts
+      // --------------- O2 = a M, and U = (weighted b)^T c, part after part
       const bool leader = elect_one();
       constexpr uint32_t kId = idesc_bf16(128, D, true, true), kId2 = idesc_bf16(128, D, false, true);
       // (at D 64 U's lower 64 rows read what lies behind the tile: nobody reads them)
@@ -338,7 +364,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           __syncwarp();
         }
         if (!(ok = warp_wait(c_full(rb.stage), rb.par, abort, p.status, tmo))) break;
-        for (int part = 0; part <= (exact ? 1 : 0); ++part, ++k) {
+        for (int part = 0; part < parts; ++part, ++k) {
           if (!(ok = warp_wait(x_full(k), (k >> 1) & 1, abort, p.status, tmo))) break;
           tc_fence_after();
 #pragma unroll 4
@@ -346,7 +372,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
             if (leader)
               mma_ss(tU(i), bd0 + st + (uint64_t)(kk * 128), cd0 + st + (uint64_t)(kk * 128), kId, part > 0 || kk > 0);
           if (leader) {
-            if (exact && !part) {
+            if (part + 1 < parts) {
               mma_commit(h_done);
             } else {
               mma_commit(u_full(i));
@@ -553,7 +579,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
     if (!SUM && n_chunks > 0) publish();
     StageRing<BS> rb;
     bool ok = true;
-    int k = 0;
+    int k = 0, hk = 0;
     for (int i = 0; i < n_chunks && ok; ++i) {
       const int n = chunk_n(i);
       if (!(ok = warp_wait(b_full(rb.stage), rb.par, abort, p.status, tmo))) break;
@@ -576,39 +602,50 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       if (!SUM && !(ok = warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo))) break;
       const float uw = row < n ? pw[(back ? row : n - 1 - row) + late] : 0.f;
       const float2 uw2 = make_float2(uw, uw);
-      uint4 lo[HC / 8];  // what is left of the weighted row
-      auto weight = [&](auto with_lo) {
-        // (lo has to stay in registers)
-#pragma unroll(decltype(with_lo)::value ? HC / 8 : 2)
+      // the weighted row in its parts, the smallest first: so the large numbers of the last part
+      // go through eight steps of the tensor cores' sum and not through all
+      uint4 keep[HC / 8];
+      if (parts == 2) {
+#pragma unroll
         for (int j = 0; j < HC / 8; ++j) {
           uint4* const at = line + ((chunk0 + j) ^ (row & 7));
           const uint4 x = *at;
           const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-          uint32_t hi[4], l[4];
+          uint32_t hi[4], lo[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float2 v = mul2(make_float2(bf16_lo(in[q]), bf16_hi(in[q])), uw2);
             hi[q] = pack_bf16(v.x, v.y);
-            if (decltype(with_lo)::value) l[q] = pack_bf16(v.x - bf16_lo(hi[q]), v.y - bf16_hi(hi[q]));
+            lo[q] = pack_bf16(v.x - bf16_lo(hi[q]), v.y - bf16_hi(hi[q]));
           }
-          *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if (decltype(with_lo)::value) lo[j] = make_uint4(l[0], l[1], l[2], l[3]);
+          *at = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          keep[j] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         }
-      };
-      if (exact) weight(std::true_type{});
-      else weight(std::false_type{});
+      } else {
+#pragma unroll
+        for (int j = 0; j < HC / 8; ++j) keep[j] = line[(chunk0 + j) ^ (row & 7)];  // as it came
+        third(keep, line, chunk0, row, uw2, -1.f, -1.f);
+      }
       fence_proxy_async_smem();
       mbar_arrive(x_full(k++));
       if constexpr (SUM) {
         if (i > 0 && !(ok = take(i - 1))) break;  // while this chunk's product runs
       }
-      if (exact) {
-        if (!(ok = warp_wait(h_done, i & 1, abort, p.status, tmo))) break;
-#pragma unroll
-        for (int j = 0; j < HC / 8; ++j) line[(chunk0 + j) ^ (row & 7)] = lo[j];
+      if (parts == 3) {
+        if (!(ok = warp_wait(h_done, hk++ & 1, abort, p.status, tmo))) break;
+        third(keep, line, chunk0, row, uw2, -1.f, 0.f);
         fence_proxy_async_smem();
         mbar_arrive(x_full(k++));
       }
+      if (!(ok = warp_wait(h_done, hk++ & 1, abort, p.status, tmo))) break;
+      if (parts == 3) {
+        third(keep, line, chunk0, row, uw2, 0.f, 0.f);
+      } else {
+#pragma unroll
+        for (int j = 0; j < HC / 8; ++j) line[(chunk0 + j) ^ (row & 7)] = keep[j];
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(x_full(k++));
       rb.advance();
       if constexpr (!SUM) {
         if (!(ok = take(i))) break;
