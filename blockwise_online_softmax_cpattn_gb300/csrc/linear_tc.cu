@@ -9,21 +9,24 @@
 //   U = (w(n - 1 - j) b_j)^T c   (SS, both transposed by their descriptors)
 //   M = w(n) M + U
 //
-// M itself stays in float32, in registers (two threads a row, one channel of b).  b is weighted in
-// its place in shared memory once S has read it, as two bf16 numbers one after the other, hi and
-// then what is left, and U is the sum of two products: 16 bits.  For a state that is handed out in
-// float32, in the sums and in the sequence's last run, it is three, 24 bits.  As operands P and M
-// are rounded to bf16 once, like the output itself.  Errors against float64, of the norm (8192
-// tokens, D 128): outputs 2.3e-3, of which the output's own rounding is 1.7e-3 (2.6e-3 with b in
-// one part, 15 % faster); states 2.4e-6 with two parts.  U starts from zero in every chunk, so no
-// sum on the tensor cores runs longer than 384 terms.
+// M itself stays in float32, in registers (two threads a row, one channel of b).  b is weighted once
+// S has read it, as two bf16 numbers, hi in b's place and what is left, lo, in that of a, which O2
+// has read by then, and U is the sum of two products: 16 bits.  For a state that is handed out in
+// float32, in the sums and in the sequence's last run, it is three, 24 bits.  The smallest part is
+// summed first: so the large numbers go through eight steps of the tensor cores' sum (16 terms
+// each) and not through all.  As operands P and M are rounded to bf16 once, like the output itself.
+// Errors against float64, of the norm (8192 tokens, D 128): outputs 2.3e-3, of which the output's
+// own rounding is 1.7e-3 (2.6e-3 with b in one part); states 1.0e-7 (2.4e-6 in two parts, 5.4e-7 in
+// three with the largest first).  U starts from zero in every chunk: no sum on the tensor cores
+// runs longer than 384 terms.
 //
 // Warp roles (640 threads):
 //   warp 0        TMA producer: the tiles a, b, c of a chunk, two stages each
 //   warp 1        issues S;  warp 2: O1;  warp 3: O2 and U
-//   warps 4-11    the output, two threads a row: S -> P, then the epilogue.  bf16 is stored from
-//                 registers in whole 32-byte sectors; float32, twice as much, is staged in the
-//                 chunk's own c tile, which nothing reads any more, and leaves by TMA
+//   warps 4-11    the output, two threads a row: S -> P, then the epilogue, staged where M lies as
+//                 bf16 (O2 has read it, and the next M comes last) and out by TMA: stored from
+//                 registers, every instruction touches 32 lines, and loads and stores of the other
+//                 warps wait for that, 15 % of the time
 //   warps 12-19   the state, two threads a row: b times its weights, M, its bf16 copy
 // Issuers are whole warps with one elected lane, as in tc_fwd.cu.  TMEM: S/P [0, 128),
 // O1, O2 and U of D columns each behind it.
@@ -54,17 +57,20 @@ template <int D, bool SUM>
 struct Smem {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kAS = SUM ? 0 : D == 128 ? 2 : 3;  // stages of a; of b and c
-  static constexpr int kBS = SUM ? (D == 128 ? 3 : 6) : kAS;
+  static constexpr int kBS = SUM ? (D == 128 ? 2 : 4) : kAS;
+  static constexpr int kXS = SUM ? (D == 128 ? 3 : 5) : 1;  // parts of the weighted b (else unused)
   static constexpr int kA = 0;
   static constexpr int kB = kA + kAS * kTileBytes;
   static constexpr int kC = kB + kBS * kTileBytes;
-  static constexpr int kM = kC + kBS * kTileBytes;
-  // the output's staging, 4 KB a warp: at D 128 the c tile, at D 64 that is too small
+  static constexpr int kX = kC + kBS * kTileBytes;
+  // (at D 64 U reads on behind a part's tile, as far as another one)
+  static constexpr int kM = kX + (SUM ? (kXS + (D == 64)) * kTileBytes : 0);
+  // the output's staging, 4 KB a warp: at D 128 where M lies, at D 64 that is too small
   static constexpr int kO = kM + (SUM ? 0 : D * D * 2);
   static constexpr int kPow = kO + (SUM || D == 128 ? 0 : 8 * 4096);
   // powers r^e at kPow + 4 (128 + e), zeros for e < 0
   static constexpr int kBar = kPow + 4 * 264;
-  static constexpr int kNumBars = 2 * (kAS + 2 * kBS) + 14 + 3;
+  static constexpr int kNumBars = 2 * (kAS + 2 * kBS) + 15 + 3 + kXS;
   static constexpr int kMisc = kBar + 8 * kNumBars;
   static constexpr int kBytes = kMisc + 16;
 };
@@ -125,43 +131,11 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t par) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// 32 bytes, a whole sector, aligned.
-__device__ __forceinline__ void store32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
-                                        uint32_t f, uint32_t g, uint32_t h) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d),
-               "r"(e), "r"(f), "r"(g), "r"(h)
-               : "memory");
-}
-
-// What is left of a weighted row after the parts above: m1, m2 are -1 for each part taken away, else
-// 0.  (The row's registers are made opaque, so that what is formed of them for one part is not kept
-// for the next: that spilled 1.6 KB a thread.)
-template <int N>
-__device__ __forceinline__ void third(uint4 (&raw)[N], uint4* line, int chunk0, int row, float2 uw2, float m1, float m2) {
-  const float2 m12 = make_float2(m1, m1), m22 = make_float2(m2, m2);
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    asm volatile("" : "+r"(raw[j].x), "+r"(raw[j].y), "+r"(raw[j].z), "+r"(raw[j].w));
-    const uint32_t in[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-    uint32_t out[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float2 v = mul2(make_float2(bf16_lo(in[q]), bf16_hi(in[q])), uw2);
-      uint32_t h = pack_bf16(v.x, v.y);
-      v = fma2(make_float2(bf16_lo(h), bf16_hi(h)), m12, v);
-      h = pack_bf16(v.x, v.y);
-      v = fma2(make_float2(bf16_lo(h), bf16_hi(h)), m22, v);
-      out[q] = pack_bf16(v.x, v.y);
-    }
-    line[(chunk0 + j) ^ (row & 7)] = make_uint4(out[0], out[1], out[2], out[3]);
-  }
-}
-
 template <int D, bool SUM>
 __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
     sweep_kernel(const __grid_constant__ Params prm) {
   using L = Smem<D, SUM>;
-  constexpr int AS = L::kAS, BS = L::kBS;
+  constexpr int AS = L::kAS, BS = L::kBS, XS = L::kXS;
   constexpr uint32_t kTmemCols = SUM ? 2 * D : 512;
   const Linear& p = prm.p;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -179,10 +153,11 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
   auto c_empty = [&](int s) { return bars + 8 * (2 * AS + 3 * BS + s); };
   const uint32_t one = bars + 8 * 2 * (AS + 2 * BS);
   auto s_full = [&](int i) { return one + 8 * (i & 1); };        // pairs
-  auto x_full = [&](int k) { return one + 8 * (2 + (k & 1)); };  // b weighted, the k-th time
+  auto x_full = [&](int k) { return one + 8 * (2 + (k & 1)); };  // parts written, the k-th time
   auto u_full = [&](int i) { return one + 8 * (4 + (i & 1)); };
   const uint32_t p_full = one + 48, o_full = one + 56, o_free = one + 64, m_full = one + 72,
-                 m_free = one + 80, h_done = one + 88, fixed = one + 96, o2_full = one + 104, fin = one + 112;
+                 m_free = one + 80, h_done = one + 88, fixed = one + 96, o2_full = one + 104, e_done = one + 112, fin = one + 120;
+  auto x_empty = [&](int s) { return one + 144 + 8 * s; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   float* pw = reinterpret_cast<float*>(smem + L::kPow) + 128;
@@ -198,7 +173,8 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
   const int n_tok = lin_tokens(p, bh);
   const float ld = lin_decay(p, bh);
   const int back = w.back, late = back;
-  const int parts = w.exact && (SUM || run == p.segs - 1) ? 3 : 2;  // bf16 numbers of a weighted b
+  // bf16 numbers of a weighted b: in the sums of the runs one does (2.36e-3 against 2.35e-3)
+  const int parts = w.exact && (SUM || run == p.segs - 1) ? 3 : SUM ? 1 : 2;
   const int bb = bh / p.Hq, h = bh - bb * p.Hq;
   const int head_a = bb * (p.Hq / w.rep_a) + h / w.rep_a;
   const int head_b = bb * (p.Hq / w.rep_b) + h / w.rep_b;
@@ -213,10 +189,9 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) mbar_init(bars + 8 * i, 1);
-    // a_empty: S and O2; c_empty: U and the eight warps that may stage the output there; the rest by
-    // threads
-    for (int i = 0; i < AS; ++i) mbar_init(a_empty(i), 2);
-    for (int i = 0; i < BS; ++i) mbar_init(c_empty(i), SUM ? 1 : 9);
+    // c_empty: O1 and U; e_done: the eight warps that stage the output; the rest by threads
+    mbar_init(e_done, 8);
+    for (int i = 0; i < BS; ++i) mbar_init(c_empty(i), SUM ? 1 : 2);
     for (int i = 0; i < 2; ++i) mbar_init(x_full(i), 256);
     mbar_init(p_full, 256);
     mbar_init(o_free, 256);
@@ -294,10 +269,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
             const uint32_t off = st + (kk >> 2) * 1024 + (kk & 3) * 2;  // 16 KiB blocks, 32 B steps
             if (leader) mma_ss(tS, ad0 + off, bd0 + off, kId, kk > 0);
           }
-          if (leader) {
-            mma_commit(s_full(i));
-            mma_commit(a_empty(ra.stage));
-          }
+          if (leader) mma_commit(s_full(i));
           __syncwarp();
           ra.advance();
         }
@@ -323,7 +295,10 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
 #pragma unroll 4
           for (int kk = 0; kk < kTile / 16; ++kk)
             if (leader) mma_ts(tO1, tS + (kk >> 2) * 64 + (kk & 3) * 8, cd0 + st + (uint64_t)(kk * 128), kId, kk > 0);
-          if (leader) mma_commit(o_full);
+          if (leader) {
+            mma_commit(o_full);
+            mma_commit(c_empty(rc.stage));
+          }
           __syncwarp();
           rc.advance();
         }
@@ -340,9 +315,11 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       const uint64_t cd0 = sdesc_sw128(sbase + L::kC, kTile * 128, 1024);
       const uint64_t ad0 = sdesc_sw128(sbase + L::kA, 16, 1024);
       const uint64_t md = sdesc_sw128(sbase + L::kM, D * 128, 1024);
+      const uint64_t al0 = sdesc_sw128(sbase + L::kA, kTile * 128, 1024);
+      const uint64_t xd0 = sdesc_sw128(sbase + L::kX, kTile * 128, 1024);
       StageRing<BS> rb;
       bool ok = true;
-      int k = 0;
+      int k = 0, x = 0;
       for (int i = 0; i < n_chunks && ok; ++i) {
         const uint32_t st = rb.stage * (L::kTileBytes >> 4);
         if constexpr (!SUM) {
@@ -359,29 +336,46 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           if (leader) {
             mma_commit(m_free);
             mma_commit(o2_full);
-            mma_commit(a_empty(rb.stage));
           }
           __syncwarp();
         }
         if (!(ok = warp_wait(c_full(rb.stage), rb.par, abort, p.status, tmo))) break;
-        for (int part = 0; part < parts; ++part, ++k) {
-          if (!(ok = warp_wait(x_full(k), (k >> 1) & 1, abort, p.status, tmo))) break;
-          tc_fence_after();
+        // a part: b's place, a's place (its tile is laid out alike), or a buffer of the sums'
+        auto product = [&](uint64_t pd, bool first) {
 #pragma unroll 4
           for (int kk = 0; kk < kTile / 16; ++kk)
-            if (leader)
-              mma_ss(tU(i), bd0 + st + (uint64_t)(kk * 128), cd0 + st + (uint64_t)(kk * 128), kId, part > 0 || kk > 0);
-          if (leader) {
-            if (part + 1 < parts) {
-              mma_commit(h_done);
-            } else {
-              mma_commit(u_full(i));
-              mma_commit(b_empty(rb.stage));
-              mma_commit(c_empty(rb.stage));
-            }
+            if (leader) mma_ss(tU(i), pd + (uint64_t)(kk * 128), cd0 + st + (uint64_t)(kk * 128), kId, !first || kk > 0);
+        };
+        if (!(ok = warp_wait(x_full(k), (k >> 1) & 1, abort, p.status, tmo))) break;
+        ++k;
+        tc_fence_after();
+        if constexpr (SUM) {
+          for (int part = 0; part + 1 < parts; ++part) {
+            product(xd0 + x * (L::kTileBytes >> 4), part == 0);
+            if (leader) mma_commit(x_empty(x));
+            __syncwarp();
+            if (++x == XS) x = 0;
           }
-          __syncwarp();
+          product(bd0 + st, parts == 1);
+        } else {
+          if (parts > 1) product(al0 + st, true);
+          product(bd0 + st, parts == 1);
+          if (parts == 3) {
+            if (leader) mma_commit(h_done);
+            __syncwarp();
+            if (!(ok = warp_wait(x_full(k), (k >> 1) & 1, abort, p.status, tmo))) break;
+            ++k;
+            tc_fence_after();
+            product(bd0 + st, false);
+          }
         }
+        if (leader) {
+          mma_commit(u_full(i));
+          mma_commit(b_empty(rb.stage));
+          mma_commit(c_empty(rb.stage));
+          if (!SUM) mma_commit(a_empty(rb.stage));
+        }
+        __syncwarp();
         rb.advance();
       }
       if (leader) mma_commit(fin + 16);
@@ -395,8 +389,6 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       const int quad = warp & 3, row = quad * 32 + lane, half = warp >> 2 & 1;
       const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
       constexpr int HC = D / 2;
-      const bool aligned32 = (reinterpret_cast<uintptr_t>(w.out) & 31) == 0;
-      StageRing<BS> rc;
       for (int i = 0; i < n_chunks; ++i) {
         const int pos0 = chunk_pos(i), n = chunk_n(i);
         if (!warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo)) break;
@@ -436,17 +428,29 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         mbar_arrive(p_full);
 
         if (!warp_wait(o_full, i & 1, abort, p.status, tmo) || !warp_wait(o2_full, i & 1, abort, p.status, tmo)) break;
-        // float32 chunks, where whole, go by way of shared memory: over c, which U has read then
-        const bool staged = w.out_f32 && n == kTile;
-        if (staged && !warp_wait(u_full(i), (i >> 1) & 1, abort, p.status, tmo)) break;
         tc_fence_after();
         const float ow = pw[(back ? n - 1 - min(row, n - 1) : row) + 1 - late] * w.mul;
         const float2 ow2 = make_float2(ow, ow), mul2v = make_float2(w.mul, w.mul);
         const int64_t tile_row0 = (int64_t)bh * p.T + p.m.slot(pos0);
         const bool store = row < n && in_bounds(tile_row0 + row, 1, rows_q, p.status);
         const int64_t at = (tile_row0 + row) * D + half * HC;
-        // this warp's 32 lines of 128 bytes, 32 columns, swizzled as the tensor map has it
-        const int area = (D == 128 ? L::kC + rc.stage * L::kTileBytes : L::kO) + (quad * 2 + half) * 4096;
+        // whole chunks go by way of shared memory: this warp's 32 lines of 64 bf16 or 32 float32
+        // columns (at D 64 of 32 bf16: half lines), swizzled as the tensor map has it
+        const bool staged = n == kTile;
+        const int area = (D == 128 ? L::kM : L::kO) + (quad * 2 + half) * 4096;
+        const int lchunks = D == 64 && !w.out_f32 ? 4 : 8, lswz = D == 64 && !w.out_f32 ? lane >> 1 & 3 : lane & 7;
+        uint4* const line = reinterpret_cast<uint4*>(smem + area) + lane * lchunks;
+        auto leave = [&](int col) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (in_bounds(tile_row0 + quad * 32, 32, rows_q, p.status))
+              tma_store_2d(&maps.o, half * HC + col, (int)(tile_row0 + quad * 32), sbase + area);
+            bulk_commit_group();
+            bulk_wait_read_all();
+          }
+          __syncwarp();
+        };
 #pragma unroll 1
         for (int c = 0; c < HC / 16; ++c) {
           uint32_t o1[16], o2[16];
@@ -463,39 +467,27 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
             v[j] = fma2(ow2, make_float2(__uint_as_float(o2[2 * j]), __uint_as_float(o2[2 * j + 1])),
                         mul2(mul2v, make_float2(__uint_as_float(o1[2 * j]), __uint_as_float(o1[2 * j + 1]))));
           if (w.out_f32) {
-            float4* const dst = staged ? reinterpret_cast<float4*>(smem + area) + lane * 8
-                                       : reinterpret_cast<float4*>(static_cast<float*>(w.out) + at) + c * 4;
-            const int slot = staged ? (c & 1) * 4 : 0, swz = staged ? lane & 7 : 0;
-            if (staged || store)
+            float4* const dst = reinterpret_cast<float4*>(static_cast<float*>(w.out) + at) + c * 4;
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                dst[(slot + j) ^ swz] = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
-            if (staged && (c & 1)) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                if (in_bounds(tile_row0 + quad * 32, 32, rows_q, p.status))
-                  tma_store_2d(&maps.o, half * HC + (c >> 1) * 32, (int)(tile_row0 + quad * 32), sbase + area);
-                bulk_commit_group();
-                bulk_wait_read_all();
-              }
-              __syncwarp();
+            for (int j = 0; j < 4; ++j) {
+              const float4 x = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+              if (staged) reinterpret_cast<float4*>(line)[((c & 1) * 4 + j) ^ lswz] = x;
+              else if (store) dst[j] = x;
             }
-          } else if (store) {
-            uint32_t u[8];
+            if (staged && (c & 1)) leave((c >> 1) * 32);
+          } else {
+            uint4* const dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(w.out) + at) + c * 2;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] = pack_bf16(v[j].x, v[j].y);
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(w.out) + at + c * 16;
-            if (aligned32) {
-              store32(dst, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
-            } else {
-              reinterpret_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-              reinterpret_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+            for (int j = 0; j < 2; ++j) {
+              const uint4 x = make_uint4(pack_bf16(v[4 * j].x, v[4 * j].y), pack_bf16(v[4 * j + 1].x, v[4 * j + 1].y),
+                                         pack_bf16(v[4 * j + 2].x, v[4 * j + 2].y), pack_bf16(v[4 * j + 3].x, v[4 * j + 3].y));
+              if (staged) line[(c * 2 + j) ^ lswz] = x;
+              else if (store) dst[j] = x;
             }
           }
         }
-        if (lane == 0) mbar_arrive(c_empty(rc.stage));
-        rc.advance();
+        if (staged && !w.out_f32) leave(0);
+        if (lane == 0) mbar_arrive(e_done);
       }
       if (lane == 0) bulk_wait_all();
     }
@@ -579,7 +571,8 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
     if (!SUM && n_chunks > 0) publish();
     StageRing<BS> rb;
     bool ok = true;
-    int k = 0, hk = 0;
+    int k = 0, x = 0;
+    uint32_t xpar = 0;
     for (int i = 0; i < n_chunks && ok; ++i) {
       const int n = chunk_n(i);
       if (!(ok = warp_wait(b_full(rb.stage), rb.par, abort, p.status, tmo))) break;
@@ -602,56 +595,87 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       if (!SUM && !(ok = warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo))) break;
       const float uw = row < n ? pw[(back ? row : n - 1 - row) + late] : 0.f;
       const float2 uw2 = make_float2(uw, uw);
-      // the weighted row in its parts, the smallest first: so the large numbers of the last part
-      // go through eight steps of the tensor cores' sum and not through all
-      uint4 keep[HC / 8];
-      if (parts == 2) {
+      // the parts of eight channels
+      auto split = [&](uint4 x, uint4& hi, uint4& mid, uint4& lo, bool three) {
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+        uint32_t h[4], m[4], l[4];
 #pragma unroll
-        for (int j = 0; j < HC / 8; ++j) {
-          uint4* const at = line + ((chunk0 + j) ^ (row & 7));
-          const uint4 x = *at;
-          const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 v = mul2(make_float2(bf16_lo(in[q]), bf16_hi(in[q])), uw2);
-            hi[q] = pack_bf16(v.x, v.y);
-            lo[q] = pack_bf16(v.x - bf16_lo(hi[q]), v.y - bf16_hi(hi[q]));
-          }
-          *at = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          keep[j] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        for (int q = 0; q < 4; ++q) {
+          float2 v = mul2(make_float2(bf16_lo(in[q]), bf16_hi(in[q])), uw2);
+          h[q] = pack_bf16(v.x, v.y);
+          v = fma2(make_float2(bf16_lo(h[q]), bf16_hi(h[q])), make_float2(-1.f, -1.f), v);
+          m[q] = pack_bf16(v.x, v.y);
+          if (three) l[q] = pack_bf16(v.x - bf16_lo(m[q]), v.y - bf16_hi(m[q]));
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < HC / 8; ++j) keep[j] = line[(chunk0 + j) ^ (row & 7)];  // as it came
-        third(keep, line, chunk0, row, uw2, -1.f, -1.f);
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(x_full(k++));
+        hi = make_uint4(h[0], h[1], h[2], h[3]);
+        mid = make_uint4(m[0], m[1], m[2], m[3]);
+        if (three) lo = make_uint4(l[0], l[1], l[2], l[3]);
+      };
       if constexpr (SUM) {
+        int x0 = x, x1 = x + 1 == XS ? 0 : x + 1;
+        const uint32_t par0 = xpar, par1 = x1 == 0 ? xpar ^ 1u : xpar;
+        if (!(ok = (parts == 1 || warp_wait(x_empty(x0), par0 ^ 1u, abort, p.status, tmo)) &&
+                   (parts < 3 || warp_wait(x_empty(x1), par1 ^ 1u, abort, p.status, tmo))))
+          break;
+        // smallest first: two parts, mid in x0; three, lo in x0 and mid in x1
+        uint4* const l0 = line + (L::kX - L::kB + (x0 - rb.stage) * L::kTileBytes) / 16;
+        uint4* const l1 = line + (L::kX - L::kB + (x1 - rb.stage) * L::kTileBytes) / 16;
+#pragma unroll 4
+        for (int j = 0; j < HC / 8; ++j) {
+          const int at = (chunk0 + j) ^ (row & 7);
+          uint4 hi, mid, lo;
+          split(line[at], hi, mid, lo, parts == 3);
+          line[at] = hi;
+          if (parts == 3) {
+            l0[at] = lo;
+            l1[at] = mid;
+          } else if (parts == 2) {
+            l0[at] = mid;
+          }
+        }
+        for (int q = 1; q < parts; ++q)
+          if (++x == XS) x = 0, xpar ^= 1u;
+        fence_proxy_async_smem();
+        mbar_arrive(x_full(k++));
         if (i > 0 && !(ok = take(i - 1))) break;  // while this chunk's product runs
-      }
-      if (parts == 3) {
-        if (!(ok = warp_wait(h_done, hk++ & 1, abort, p.status, tmo))) break;
-        third(keep, line, chunk0, row, uw2, -1.f, 0.f);
+      } else {
+        // O2 has read a: its tile takes the smallest part
+        if (!(ok = warp_wait(m_free, i & 1, abort, p.status, tmo))) break;
+        uint4* const aline = line - (L::kB - L::kA) / 16;
+        if (parts < 3) {
+#pragma unroll 2
+          for (int j = 0; j < HC / 8; ++j) {
+            const int at = (chunk0 + j) ^ (row & 7);
+            uint4 hi, mid, lo;
+            split(line[at], hi, mid, lo, false);
+            line[at] = hi;
+            if (parts == 2) aline[at] = mid;
+          }
+        } else {
+          uint4 hi[HC / 8];
+#pragma unroll
+          for (int j = 0; j < HC / 8; ++j) {
+            const int at = (chunk0 + j) ^ (row & 7);
+            uint4 mid, lo;
+            split(line[at], hi[j], mid, lo, true);
+            line[at] = mid;
+            aline[at] = lo;
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(x_full(k++));
+          if (!(ok = warp_wait(h_done, i & 1, abort, p.status, tmo))) break;
+#pragma unroll
+          for (int j = 0; j < HC / 8; ++j) line[(chunk0 + j) ^ (row & 7)] = hi[j];
+        }
         fence_proxy_async_smem();
         mbar_arrive(x_full(k++));
       }
-      if (!(ok = warp_wait(h_done, hk++ & 1, abort, p.status, tmo))) break;
-      if (parts == 3) {
-        third(keep, line, chunk0, row, uw2, 0.f, 0.f);
-      } else {
-#pragma unroll
-        for (int j = 0; j < HC / 8; ++j) line[(chunk0 + j) ^ (row & 7)] = keep[j];
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(x_full(k++));
       rb.advance();
       if constexpr (!SUM) {
         if (!(ok = take(i))) break;
         if (i + 1 < n_chunks) {
-          // O2 of this chunk has read the old copy
-          if (!(ok = warp_wait(m_free, i & 1, abort, p.status, tmo))) break;
+          // O2 of this chunk has read the old copy (m_free), and the output staged over it has left
+          if (!(ok = warp_wait(e_done, i & 1, abort, p.status, tmo))) break;
           publish();
         }
       }
@@ -698,11 +722,14 @@ static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, cudaStrea
     m.a = m.o = m.b;
     if (!SUM && !make_map(&m.a, w.a, hq / w.rep_a, p.T, D)) return cudaErrorInvalidValue;
   }
-  if (!SUM)  // a float32 output's boxes: one warp's 32 rows, a 128-byte line each
-    for (int i = 0; i < n; ++i)
-      if (sweeps[i].out_f32 && encode_tmap_2d_f32(&prm.maps[i].o, sweeps[i].out, D, (uint64_t)p.B * p.Hq * p.T, 32,
-                                                  32) != CUDA_SUCCESS)
+  if (!SUM)  // the output's boxes: one warp's 32 rows, a line of 128 bytes each (bf16 at D 64: 64)
+    for (int i = 0; i < n; ++i) {
+      const LinSweep& w = sweeps[i];
+      const uint64_t rows = (uint64_t)p.B * p.Hq * p.T;
+      if ((w.out_f32 ? encode_tmap_2d_f32(&prm.maps[i].o, w.out, D, rows, 32, 32)
+                     : encode_tmap_2d_bf16(&prm.maps[i].o, w.out, D, rows, D / 2, 32)) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
+    }
   constexpr int kSmem = Smem<D, SUM>::kBytes, kThreads = SUM ? kThreadsSum : kThreadsOut;
   auto kern = sweep_kernel<D, SUM>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
