@@ -276,6 +276,7 @@ static cudaError_t launch(const Linear& p, cudaStream_t st, const char* sums, co
 template <typename E>
 __global__ void __launch_bounds__(256) group_kernel(int64_t n4, int n_rep, int64_t row4, const float4* part_v,
                                                     const float4* part_k, E* dv, E* dk) {
+  griddep_wait();  // (started while the sweeps' last blocks finish)
   const float4* part = blockIdx.y ? part_k : part_v;
   E* out = blockIdx.y ? dk : dv;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
@@ -310,13 +311,21 @@ cudaError_t launch_linear_group(int64_t groups, int n_rep, int64_t row_elems, co
   const dim3 grid((unsigned)(want < most ? want : most), 2);
   const float4 *pv = reinterpret_cast<const float4*>(part_v), *pk = reinterpret_cast<const float4*>(part_k);
   timing_begin("linear_group", st);
-  if (bf16)
-    linsimt::group_kernel<<<grid, 256, 0, st>>>(n4, n_rep, row_elems / 4, pv, pk, static_cast<__nv_bfloat16*>(dv),
-                                                static_cast<__nv_bfloat16*>(dk));
-  else
-    linsimt::group_kernel<<<grid, 256, 0, st>>>(n4, n_rep, row_elems / 4, pv, pk, static_cast<float*>(dv),
-                                                static_cast<float*>(dk));
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const int64_t row4 = row_elems / 4;
+  const cudaError_t e =
+      bf16 ? cudaLaunchKernelEx(&cfg, linsimt::group_kernel<__nv_bfloat16>, n4, n_rep, row4, pv, pk,
+                                static_cast<__nv_bfloat16*>(dv), static_cast<__nv_bfloat16*>(dk))
+           : cudaLaunchKernelEx(&cfg, linsimt::group_kernel<float>, n4, n_rep, row4, pv, pk, static_cast<float*>(dv),
+                                static_cast<float*>(dk));
   timing_end(st);
   return e;
 }

@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();  // (the next launch's blocks start as this one's end)
   const uint32_t tS = tmem, tO1 = tmem + 128, tO2 = tmem + 128 + D;
   auto tU = [&](int i) { return SUM ? tmem + (i & 1) * D : tmem + 128 + 2 * D; };
 
@@ -517,7 +518,8 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           }
         }
       }
-      // the runs before this one, folded in order
+      // the runs before this one, folded in order, once the launch that sums them is through
+      if (run > 0) griddep_wait();
       for (int s = 0; s < run; ++s) {
         const float f = lin_pow(ld, lin_run_tokens<kTile>(p, n_tok, back, s));
         const float* src = w.sums + ((int64_t)bh * p.segs + s) * DD;
@@ -710,7 +712,7 @@ static bool make_map(CUtensorMap* m, const void* t, int64_t heads, int T, int D)
 }
 
 template <int D, bool SUM>
-static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, cudaStream_t st) {
+static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, bool dependent, cudaStream_t st) {
   Params prm;
   prm.p = p;
   for (int i = 0; i < n; ++i) {
@@ -740,8 +742,17 @@ static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, cudaStrea
     if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
   }
   const unsigned blocks = (unsigned)(p.B * p.Hq * (SUM ? p.segs - 1 : p.segs));
-  kern<<<dim3(blocks, n), kThreads, kSmem, st>>>(prm);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, n);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, prm);
 }
 
 }  // namespace lintc
@@ -757,13 +768,14 @@ cudaError_t launch_linear_tc(const Linear& p, cudaStream_t st, bool backward) {
   cudaError_t e;
   if (p.segs > 1) {
     timing_begin(backward ? "linear_bwd_sums" : "linear_fwd_sums", st);
-    e = p.D == 128 ? lintc::run<128, true>(p, p.n_sums, p.sum, st) : lintc::run<64, true>(p, p.n_sums, p.sum, st);
+    e = p.D == 128 ? lintc::run<128, true>(p, p.n_sums, p.sum, false, st)
+                   : lintc::run<64, true>(p, p.n_sums, p.sum, false, st);
     timing_end(st);
     if (e != cudaSuccess) return e;
   }
   timing_begin(backward ? "linear_bwd" : "linear_fwd", st);
-  e = p.D == 128 ? lintc::run<128, false>(p, p.n_sweeps, p.sweep, st)
-                 : lintc::run<64, false>(p, p.n_sweeps, p.sweep, st);
+  e = p.D == 128 ? lintc::run<128, false>(p, p.n_sweeps, p.sweep, p.segs > 1, st)
+                 : lintc::run<64, false>(p, p.n_sweeps, p.sweep, p.segs > 1, st);
   timing_end(st);
   return e;
 }

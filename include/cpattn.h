@@ -568,7 +568,7 @@ cpattn_status cpattn_cache_attn(const cpattn_cache_desc* desc, int n_req, int ma
  * [B][T][(H_q + 2 H_kv) D], the ring's tensors and the cache's packed tokens
  * [n_tokens][H][D] (B 1, T n_tokens) are passed as they are.  The rows of an output must
  * not overlap.  An output may be its own input with the same strides where the order of
- * the tokens stays (natural_in 0 or CPATTN_CONTIGUOUS).
+ * the tokens stays (natural_in 0 or CPATTN_CONTIGUOUS); otherwise no output meets an input.
  */
 typedef enum cpattn_pairing { CPATTN_HALVES = 0, CPATTN_NEIGHBOURS = 1 } cpattn_pairing;
 
@@ -651,10 +651,11 @@ cpattn_status cpattn_rotate_bwd(const cpattn_rotate_desc* desc, const void* q,
  *               their own states.
  * D is a multiple of 8.  With bf16, D 64 or 128 and (CPATTN_ZIGZAG) 2 cp chunks of a multiple
  * of 128 tokens the products run on the tensor cores, with float32 sums: the weighted scores
- * and the state a chunk starts from are rounded to bf16 as operands, while states kept from
- * chunk to chunk and handed out are float32 throughout, from products of bf16 pairs that
- * carry 16 bits.  All else runs in float32.  Inputs must be finite: in a chunk of 128 tokens
- * an infinity or NaN reaches earlier tokens too.
+ * and the state that a chunk of 128 tokens starts from are rounded to bf16 as operands, weighted
+ * keys to two bf16 numbers.  States are float32 throughout; what goes into one that is handed out
+ * carries 24 bits.  (Of 8192 tokens the outputs are off by 2.4e-3 of their norm, 1.7e-3 of it their
+ * own rounding to bf16, and the state by 1e-7.)  All else runs in float32.  Inputs must be finite:
+ * in a chunk an infinity or NaN reaches earlier tokens too.
  */
 
 /* Bytes of device workspace of cpattn_linear_fwd: states of the parts into which a sequence
