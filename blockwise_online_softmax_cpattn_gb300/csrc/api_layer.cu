@@ -3,6 +3,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <initializer_list>
+
 #include "api_internal.h"
 #include "layer.cuh"
 
@@ -10,6 +12,18 @@ namespace cpattn {
 
 static bool aligned(const void* p, unsigned n) { return p && ((uintptr_t)p % n == 0); }
 static bool null_or_aligned(const void* p, unsigned n) { return !p || ((uintptr_t)p % n == 0); }
+
+// Does one of the outputs begin where an input or another output does?
+static bool meet(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    if (!*o) continue;
+    for (const void* i : ins)
+      if (*o == i) return true;
+    for (auto u = outs.begin(); u != o; ++u)
+      if (*o == *u) return true;
+  }
+  return false;
+}
 
 // ---------------------------------------------------------------------------
 // norm and rotation
@@ -166,6 +180,9 @@ cpattn_status cpattn_rotate_fwd(const cpattn_rotate_desc* desc, const void* q,
   if (!null_or_aligned(q_weight, 16) || !null_or_aligned(k_weight, 16) || !null_or_aligned(positions, 4) ||
       !null_or_aligned(inv_freq, 8) || (p.rot > 0 && !inv_freq))
     return CPATTN_ERR_INVALID_ARG;
+  // in place only where every row stays where it is
+  const bool moves = p.natural_in && p.m.zz && p.m.cp > 1;
+  if (meet({q_out, k_out, v_out}, {}) || (moves && meet({q_out, k_out, v_out}, {q, k, v}))) return CPATTN_ERR_INVALID_ARG;
   p.w[0] = q_weight;
   p.w[1] = k_weight;
   p.inv_freq = inv_freq;
@@ -207,6 +224,8 @@ cpattn_status cpattn_rotate_bwd(const cpattn_rotate_desc* desc, const void* q,
       !null_or_aligned(dk_weight, 4) || (!p.norm && (dq_weight || dk_weight)))
     return CPATTN_ERR_INVALID_ARG;
   if (!aligned16(workspace) || ws_bytes < rotate_bwd_workspace(p.D, p.norm)) return CPATTN_ERR_INVALID_ARG;
+  const bool moves = p.natural_in && p.m.zz && p.m.cp > 1;
+  if (meet({dq, dk, dv}, {}) || (moves && meet({dq, dk, dv}, {dq_out, dk_out, dv_out}))) return CPATTN_ERR_INVALID_ARG;
   p.w[0] = q_weight;
   p.w[1] = k_weight;
   p.inv_freq = inv_freq;
@@ -233,7 +252,7 @@ cpattn_status cpattn_linear_fwd(const cpattn_desc* desc, const void* q, const vo
   if (s != CPATTN_OK) return s;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned(log_decay, 4) ||
       !null_or_aligned(lengths, 4) || !null_or_aligned(state_in, 16) || !null_or_aligned(state_out, 16) ||
-      !aligned16(workspace))
+      !aligned16(workspace) || meet({o, state_out}, {q, k, v}))
     return CPATTN_ERR_INVALID_ARG;
   const bool tc = on_tensor_cores(R);
   Linear p;
@@ -287,7 +306,7 @@ cpattn_status cpattn_linear_bwd(const cpattn_desc* desc, const void* q, const vo
       !aligned16(dk) || !aligned16(dv) || !aligned(log_decay, 4) || !null_or_aligned(state_in, 16) ||
       !null_or_aligned(dstate_out, 16) || !null_or_aligned(dstate_in, 16) || !aligned16(workspace))
     return CPATTN_ERR_INVALID_ARG;
-  if (dstate_in && (dstate_in == state_in || dstate_in == dstate_out)) return CPATTN_ERR_INVALID_ARG;
+  if (meet({dq, dk, dv, dstate_in}, {q, k, v, dO, state_in, dstate_out})) return CPATTN_ERR_INVALID_ARG;
   const bool tc = on_tensor_cores(R);
   Linear p;
   plan_linear(desc, R, true, tc, &p);
@@ -356,7 +375,7 @@ cpattn_status cpattn_linear_step(const cpattn_desc* desc, int n_states, const vo
   };
   if (!rows(q, q_token_stride, q_head_stride, R.Hq) || !rows(k, k_token_stride, k_head_stride, R.Hkv) ||
       !rows(v, v_token_stride, v_head_stride, R.Hkv) || !aligned(log_decay, 4) || !null_or_aligned(slots, 4) ||
-      !aligned16(state_in) || !aligned16(state_out) || !aligned16(o))
+      !aligned16(state_in) || !aligned16(state_out) || !aligned16(o) || meet({o, state_out}, {q, k, v}))
     return CPATTN_ERR_INVALID_ARG;
   LinStep p;
   p.n = R.B;

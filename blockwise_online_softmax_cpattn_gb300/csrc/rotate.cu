@@ -20,7 +20,10 @@
 // float32 product alone is off by 2^-8 of a radian, and the float64 units, two lanes an SM, took
 // 2 us of a decoding step's 6.6.
 //
-// Bound by memory: 64 (bf16) to 128 (float32) bytes a lane and row against some 130 instructions.
+// Bound by memory: 64 bytes a lane and row against some 130 instructions.  32768 tokens of 40 heads
+// of 128 (bf16): 107 us, 6.3 TB/s, 92 % of a copy's rate.  Backward, 8192 tokens of 48 heads: 56 us,
+// 5.1 TB/s (75 %); 16 warps an SM at 128 registers leave a dependent instruction's wait (2.2 cycles
+// of 7.6 an issue) as its largest stall.  A decoding step's 64 tokens: 4.1 us.
 #include "layer.cuh"
 
 namespace cpattn {

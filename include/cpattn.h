@@ -568,7 +568,8 @@ cpattn_status cpattn_cache_attn(const cpattn_cache_desc* desc, int n_req, int ma
  * [B][T][(H_q + 2 H_kv) D], the ring's tensors and the cache's packed tokens
  * [n_tokens][H][D] (B 1, T n_tokens) are passed as they are.  The rows of an output must
  * not overlap.  An output may be its own input with the same strides where the order of
- * the tokens stays (natural_in 0 or CPATTN_CONTIGUOUS); otherwise no output meets an input.
+ * the tokens stays (natural_in 0 or CPATTN_CONTIGUOUS).  Else no output may meet an input or
+ * another output (the same pointer: CPATTN_ERR_INVALID_ARG).
  */
 typedef enum cpattn_pairing { CPATTN_HALVES = 0, CPATTN_NEIGHBOURS = 1 } cpattn_pairing;
 
@@ -646,6 +647,8 @@ cpattn_status cpattn_rotate_bwd(const cpattn_rotate_desc* desc, const void* q,
  *   log_decay : [H_q] float32, at most 0 (-infinity: a token sees itself only); 4-byte
  *               aligned.  A positive value or a NaN is taken as 0.  It is a constant of the
  *               model: no gradient is computed.
+ * Outputs meet neither inputs nor each other, but where it is said below (the same pointer:
+ * CPATTN_ERR_INVALID_ARG).
  *   states    : [B'][H_q'][D][D] float32 (B', H_q' as for cpattn_partial_fwd), the key's
  *               channel first.  Query heads that share a key head have their own decays, so
  *               their own states.
@@ -686,7 +689,7 @@ size_t cpattn_linear_bwd_workspace(const cpattn_desc* desc);
  *   dO         : [B][H_q][T][D]
  *   dstate_out : upstream gradient of state_out, or null for zero
  *   dq, dk, dv : dk and dv sum over the query heads of a group
- *   dstate_in  : gradient of state_in, or null.  Must not be state_in or dstate_out.
+ *   dstate_in  : gradient of state_in, or null
  * Nothing is kept from the forward pass but its inputs.  No atomics: repeated calls are
  * bitwise equal.
  */

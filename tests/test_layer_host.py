@@ -122,16 +122,21 @@ def _rot(mod, **kw):
     return mod.make_rotate_desc(**base)
 
 
+def fake(n):
+    """n distinct aligned pointers."""
+    return [FAKE * (i + 1) for i in range(n)]
+
+
 def _fwd(cp, d, **kw):
-    a = dict(q=FAKE, k=FAKE, v=FAKE, qw=FAKE, kw=FAKE, f=FAKE, pos=None, qo=FAKE, ko=FAKE, vo=FAKE)
+    a = dict(zip(("q", "k", "v", "qw", "kw", "f", "qo", "ko", "vo"), fake(9)), pos=None)
     a.update(kw)
     return cp.cpattn_rotate_fwd(d, a["q"], a["k"], a["v"], a["qw"], a["kw"], a["f"], a["pos"], a["qo"],
                                 a["ko"], a["vo"], 0)
 
 
 def _bwd(cp, d, **kw):
-    a = dict(q=FAKE, k=FAKE, qw=FAKE, kw=FAKE, f=FAKE, pos=None, dqo=FAKE, dko=FAKE, dvo=FAKE, dq=FAKE,
-             dk=FAKE, dv=FAKE, dqw=FAKE, dkw=FAKE, ws=FAKE, n=1 << 30)
+    names = ("q", "k", "qw", "kw", "f", "dqo", "dko", "dvo", "dq", "dk", "dv", "dqw", "dkw", "ws")
+    a = dict(zip(names, fake(14)), pos=None, n=1 << 30)
     a.update(kw)
     return cp.cpattn_rotate_bwd(d, a["q"], a["k"], a["qw"], a["kw"], a["f"], a["pos"], a["dqo"], a["dko"],
                                 a["dvo"], a["dq"], a["dk"], a["dv"], a["dqw"], a["dkw"], a["ws"], a["n"], 0)
@@ -157,7 +162,7 @@ def test_rotation_descriptors(cp, kw, code):
 def test_rotation_arguments(cp):
     d = _rot(cp)
     for name in ("q", "k", "qo", "ko", "v", "vo"):
-        assert _fwd(cp, d, **{name: FAKE + 8}) == 1, name
+        assert _fwd(cp, d, **{name: 32 * FAKE + 8}) == 1, name
         if name not in ("v", "vo"):
             assert _fwd(cp, d, **{name: None}) == 1, name
     assert _fwd(cp, d, v=None) == 1 and _fwd(cp, d, vo=None) == 1  # both or neither
@@ -165,12 +170,22 @@ def test_rotation_arguments(cp):
     assert _fwd(cp, d, pos=FAKE + 2) == 1 and _fwd(cp, d, qw=FAKE + 2) == 1
     for name in ("q", "k", "dqo", "dko", "dq", "dk", "ws"):
         assert _bwd(cp, d, **{name: None}) == 1, name
-        assert _bwd(cp, d, **{name: FAKE + 8}) == 1, name
+        assert _bwd(cp, d, **{name: 32 * FAKE + 8}) == 1, name
     assert _bwd(cp, d, dv=None) == 1 and _bwd(cp, d, dqw=FAKE + 2) == 1
     assert _bwd(cp, d, n=cp.cpattn_rotate_bwd_workspace(d) - 1) == 1
     plain = _rot(cp, norm=0)
     assert cp.cpattn_rotate_bwd_workspace(plain) == 16
     assert _bwd(cp, plain, q=None, k=None) == 1            # weights' gradients without a norm
+
+
+def test_rotation_outputs_that_meet(cp):
+    """The permuting call is not made in place, and no two outputs are one."""
+    d = _rot(cp, natural_in=1)
+    q, k, v = fake(3)
+    assert _fwd(cp, d, qo=q) == 1 and _fwd(cp, d, ko=q) == 1 and _fwd(cp, d, vo=v) == 1
+    assert _fwd(cp, _rot(cp), qo=7 * FAKE, ko=7 * FAKE) == 1
+    assert _bwd(cp, d, dq=6 * FAKE) == 1 and _bwd(cp, d, dk=11 * FAKE) == 1   # (dq_out; dv)
+    assert _bwd(cp, _rot(cp), dq=10 * FAKE) == 1
 
 
 def test_rotation_strides(cp):
@@ -181,7 +196,8 @@ def test_rotation_strides(cp):
     def call(in_strides, out_strides):
         i = (ctypes.c_int64 * 3)(*in_strides)
         o = (ctypes.c_int64 * 3)(*out_strides)
-        return lib(ctypes.byref(d), FAKE, i, FAKE, None, None, None, None, None, FAKE, None, FAKE, o, FAKE,
+        p = fake(5)
+        return lib(ctypes.byref(d), p[0], i, p[1], None, None, None, None, None, p[2], None, p[3], o, p[4],
                    None, None, None, 0)
 
     ok = (64 * 64 * 4, 64 * 64, 64)
@@ -211,22 +227,27 @@ def test_linear_descriptors(cp, kw, code):
 def test_linear_arguments(cp):
     d = cp.make_desc(1, 4, 2, 4096, 64, 2, "zigzag", "bf16")
     fwd = lambda *a, n=1 << 40: cp.cpattn_linear_fwd(d, *a, n, 0)  # noqa: E731
-    good = [FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE]
+    p = fake(6)
+    good = [p[0], p[1], p[2], p[3], None, None, p[4], None, p[5]]
     for i in (0, 1, 2, 3, 6, 8):
-        for bad in (None, FAKE + 2):
+        for bad in (None, 64 * FAKE + 2):
             assert fwd(*good[:i], bad, *good[i + 1:]) == 1, i
     for i in (4, 5, 7):
-        assert fwd(*good[:i], FAKE + 2, *good[i + 1:]) == 1, i
+        assert fwd(*good[:i], 64 * FAKE + 2, *good[i + 1:]) == 1, i
+    for x in p[:3]:                                     # o or the state over an input
+        assert fwd(*good[:6], x, *good[7:]) == 1 and fwd(*good[:7], x, good[8]) == 1
     n = cp.cpattn_linear_workspace(d)
     assert n > 16 and fwd(*good, n=n - 1) == 1
     bwd = lambda *a, n=1 << 40: cp.cpattn_linear_bwd(d, *a, n, 0)  # noqa: E731
-    good = [FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE + 64, FAKE]
+    good = fake(12)
     for i in (0, 1, 2, 3, 5, 7, 8, 9, 11):
-        for bad in (None, FAKE + 2):
+        for bad in (None, 64 * FAKE + 2):
             assert bwd(*good[:i], bad, *good[i + 1:]) == 1, i
     for i in (4, 6, 10):
-        assert bwd(*good[:i], FAKE + 2, *good[i + 1:]) == 1, i
-    assert bwd(*good[:10], FAKE, FAKE) == 1           # dstate_in over state_in
+        assert bwd(*good[:i], 64 * FAKE + 2, *good[i + 1:]) == 1, i
+    for i in (7, 8, 9, 10):                             # an output over an input or another output
+        for x in good[:3] + good[4:7] + [y for j, y in enumerate(good[7:11], 7) if j != i]:
+            assert bwd(*good[:i], x, *good[i + 1:]) == 1, i
     assert bwd(*good, n=cp.cpattn_linear_bwd_workspace(d) - 1) == 1
     # shared key heads: the query heads' own gradients
     same = cp.make_desc(1, 4, 4, 4096, 64, 2, "zigzag", "bf16")
@@ -237,12 +258,15 @@ def test_step_arguments(cp):
     d = cp.make_desc(3, 4, 2, 1, 64, 1, "contiguous", "bf16")
     lib = cp._lib.cpattn_linear_step
 
-    def call(q=FAKE, ts=256, hs=64, ld=FAKE, slots=None, s0=FAKE, s1=FAKE, o=FAKE, n=3, desc=d):
-        return lib(ctypes.byref(desc), n, q, ts, hs, FAKE, 128, 64, FAKE, 128, 64, ld, slots, s0, s1, o, 0)
+    p = fake(7)
+
+    def call(q=p[0], ts=256, hs=64, ld=p[3], slots=None, s0=p[4], s1=p[5], o=p[6], n=3, desc=d):
+        return lib(ctypes.byref(desc), n, q, ts, hs, p[1], 128, 64, p[2], 128, 64, ld, slots, s0, s1, o, 0)
 
     assert call(q=None) == 1 and call(q=FAKE + 8) == 1 and call(ts=252) == 1 and call(hs=60) == 1
-    assert call(ts=-256) == 1 and call(ld=None) == 1 and call(slots=FAKE + 2) == 1 and call(n=-1) == 1
-    assert call(s0=None) == 1 and call(s1=FAKE + 4) == 1 and call(o=None) == 1
+    assert call(ts=-256) == 1 and call(ld=None) == 1 and call(slots=64 * FAKE + 2) == 1 and call(n=-1) == 1
+    assert call(s0=None) == 1 and call(s1=64 * FAKE + 4) == 1 and call(o=None) == 1
+    assert call(o=p[1]) == 1 and call(s1=p[0]) == 1 and call(o=p[5]) == 1
     for kw in (dict(T=2), dict(T=2, cp=2), dict(a2a=2, cp=2, T=2)):
         base = dict(B=3, H_q=4, H_kv=2, T=1, D=64, cp=1, layout="contiguous", dtype="bf16")
         base.update(kw)
