@@ -102,7 +102,11 @@ static cpattn_status validate_linear(const cpattn_desc* d, Ring* R) {
 // a chunk of a sweep 1, of a sum 0.6, a block's start 1, folding a predecessor's state 0.25.
 static void cut_runs(const Ring& R, bool tc, int sweeps, int sums, Linear* p) {
   const int C = tc ? kLinTcChunk : kLinSimtChunk;
-  p->nch = (int)(((int64_t)R.T + C - 1) / C);
+  // (off the tensor cores a chunk's slots are looked up one by one)
+  const int half = R.zz ? R.T / R.cp / 2 : R.T;
+  p->seg = tc && half % C ? half : R.T;
+  p->per = (p->seg + C - 1) / C;
+  p->nch = p->per * (R.T / p->seg);
   const double heads = (double)R.B * R.Hq;
   double best = 0;
   for (int segs = 1; segs <= 64 && segs <= p->nch; ++segs) {

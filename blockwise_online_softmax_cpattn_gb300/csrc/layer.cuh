@@ -84,6 +84,10 @@ struct Linear {
   const float* log_decay;
   const int* lengths;
   int segs, cps, nch;   // runs, chunks a run, chunks of a sequence
+  // A chunk's positions are consecutive slots: where the token order has stretches (zigzag) off the
+  // chunks' grid, chunks begin anew with each of them, `per` chunks for its `seg` tokens.  Else one
+  // stretch, of the whole sequence.
+  int seg, per;
   int n_sums, n_sweeps; // sweeps of the first (sums) and second launch
   LinSweep sum[2], sweep[kMaxSweeps];
   int* status;
@@ -108,19 +112,36 @@ __device__ __forceinline__ int lin_tokens(const Linear& p, int bh) {
   return n < 0 ? 0 : n > p.T ? p.T : n;
 }
 
-// Chunk number of a sweep's m-th chunk, and the tokens of chunks of C.
+// Chunk number of a sweep's m-th chunk.
 __device__ __forceinline__ int lin_chunk(int nch, int back, int m) { return back ? nch - 1 - m : m; }
 __device__ __forceinline__ int lin_clamp(int n, int most) { return n < 0 ? 0 : n > most ? most : n; }
-// Tokens of run s of a sweep over n_tok tokens.
-template <int C>
+// First position of chunk c (of the one behind the last: T), and its tokens in a row of n_tok.
+// PIECES: the token order has more stretches than one.
+template <int C, bool PIECES>
+__device__ __forceinline__ int lin_first(const Linear& p, int c) {
+  if (!PIECES) return min(c * C, p.T);
+  const int q = c < p.per ? 0 : c / p.per;
+  return c == p.nch ? p.T : q * p.seg + (c - q * p.per) * C;
+}
+template <int C, bool PIECES>
+__device__ __forceinline__ int lin_size(const Linear& p, int n_tok, int c) {
+  if (!PIECES) return lin_clamp(n_tok - c * C, C);
+  const int q = c < p.per ? 0 : c / p.per, at = (c - q * p.per) * C;
+  return lin_clamp(n_tok - q * p.seg - at, min(C, p.seg - at));
+}
+// Chunks that a row of n_tok tokens has.
+template <int C, bool PIECES>
+__device__ __forceinline__ int lin_chunks(const Linear& p, int n_tok) {
+  if (!PIECES) return (n_tok + C - 1) / C;
+  const int q = n_tok / p.seg;
+  return q * p.per + (n_tok - q * p.seg + C - 1) / C;
+}
+// Tokens of run s of a sweep over n_tok tokens (from the back: whole rows).
+template <int C, bool PIECES>
 __device__ __forceinline__ int lin_run_tokens(const Linear& p, int n_tok, int back, int s) {
-  const int per = p.cps * C;
-  if (!back) return lin_clamp(n_tok - s * per, per);
-  // from the back the first run holds the partial chunk
-  const int last = p.nch * C - n_tok;  // (backward sweeps take whole rows: < C)
-  const int first = s * p.cps, most = p.nch - first;
-  const int chunks = lin_clamp(most, p.cps);
-  return chunks * C - (s == 0 ? last : 0);
+  const int m0 = s * p.cps, m1 = min(m0 + p.cps, p.nch);
+  if (back) return lin_first<C, PIECES>(p, p.nch - m0) - lin_first<C, PIECES>(p, p.nch - m1);
+  return min(lin_first<C, PIECES>(p, m1), n_tok) - min(lin_first<C, PIECES>(p, m0), n_tok);
 }
 
 // ---- linear_tc.cu (bf16, D 64 or 128) / linear_simt.cu (all else) -------------

@@ -1,6 +1,6 @@
 // Linear attention in float32 on the ordinary units: every type, head dimension and layout that
-// linear_tc.cu does not take (float32 tensors, other head dimensions, zigzag chunks off the
-// 128-token grid).  The sweep, its runs and its direction are described in layer.cuh.
+// linear_tc.cu does not take (float32 tensors, other head dimensions, zigzag chunks of fewer
+// than 16 tokens).  The sweep, its runs and its direction are described in layer.cuh.
 //
 // A block takes one run of one sweep and head in chunks of 64 tokens: scores a b^T weighted by
 // the decay into shared memory, then out = P c + r^.. (a M), then M = r^n M + b^T c, all as
@@ -104,13 +104,13 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
     };
     if (w.init) fold(0.f, w.init_mul, w.init + bh * DD);
     for (int s = 0; s < run; ++s)
-      fold(lin_pow(ld, lin_run_tokens<C>(p, n_tok, w.back, s)), 1.f, w.sums + ((int64_t)bh * p.segs + s) * DD);
+      fold(lin_pow(ld, lin_run_tokens<C, false>(p, n_tok, w.back, s)), 1.f, w.sums + ((int64_t)bh * p.segs + s) * DD);
   }
 
   const int m1 = min((run + 1) * p.cps, p.nch);
   for (int m = run * p.cps; m < m1; ++m) {
-    const int pos0 = lin_chunk(p.nch, w.back, m) * C;
-    const int n = lin_clamp(n_tok - pos0, C);
+    const int chunk = lin_chunk(p.nch, w.back, m), pos0 = lin_first<C, false>(p, chunk);
+    const int n = lin_size<C, false>(p, n_tok, chunk);
     if (n == 0) break;  // a row's padding (sweeps from the front only)
     __syncthreads();    // the last chunk's tiles have been read
     if (!SUM) {

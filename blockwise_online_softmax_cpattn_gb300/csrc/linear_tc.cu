@@ -134,7 +134,9 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t par) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-template <int D, bool SUM>
+// PIECES: the chunks of a zigzag order off their grid (layer.cuh).  A kernel of its own, since its
+// divisions cost the other orders 8 % (T 8192, 32 heads of 128: 62 -> 67 us).
+template <int D, bool SUM, bool PIECES>
 __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
     sweep_kernel(const __grid_constant__ Params prm) {
   using L = Smem<D, SUM>;
@@ -185,10 +187,10 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
   const int64_t rows_q = (int64_t)p.B * p.Hq * p.T;  // (for a CPATTN_DEBUG build's checks)
   const int m0 = run * p.cps;
   int n_chunks = min(p.cps, p.nch - m0);
-  if (!back) n_chunks = min(n_chunks, (n_tok + kTile - 1) / kTile - m0);  // chunks of padding
+  if (!back) n_chunks = min(n_chunks, lin_chunks<kTile, PIECES>(p, n_tok) - m0);  // (else chunks of padding)
   // The i-th chunk of the run: first position and tokens.
-  auto chunk_pos = [&](int i) { return lin_chunk(p.nch, back, m0 + i) * kTile; };
-  auto chunk_n = [&](int i) { return min(n_tok - chunk_pos(i), kTile); };
+  auto chunk_pos = [&](int i) { return lin_first<kTile, PIECES>(p, lin_chunk(p.nch, back, m0 + i)); };
+  auto chunk_n = [&](int i) { return lin_size<kTile, PIECES>(p, n_tok, lin_chunk(p.nch, back, m0 + i)); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) mbar_init(bars + 8 * i, 1);
@@ -258,6 +260,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         constexpr uint32_t kId = idesc_bf16(128, 128, false, false);
         const uint64_t ad0 = sdesc_sw128(sbase + L::kA, 16, 1024), bd0 = sdesc_sw128(sbase + L::kB, 16, 1024);
         StageRing<AS> ra;
+        int nf = 0;  // partial chunks
         for (int i = 0; i < n_chunks; ++i) {
           if (!warp_wait(a_full(ra.stage), ra.par, abort, p.status, tmo) ||
               !warp_wait(b_full(ra.stage), ra.par, abort, p.status, tmo))
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           // S's place is free once O1 of the last chunk has read P there
           if (i > 0 && !warp_wait(o_full, (i - 1) & 1, abort, p.status, tmo)) break;
           // a partial chunk's rows of b and c behind its end are zeroed first
-          if (chunk_n(i) < kTile && !warp_wait(fixed, 0, abort, p.status, tmo)) break;
+          if (chunk_n(i) < kTile && !warp_wait(fixed, nf++ & 1, abort, p.status, tmo)) break;
           tc_fence_after();
           const uint32_t st = ra.stage * (L::kTileBytes >> 4);
 #pragma unroll 4
@@ -288,9 +291,10 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         constexpr uint32_t kId = idesc_bf16(128, D, false, true);
         const uint64_t cd0 = sdesc_sw128(sbase + L::kC, kTile * 128, 1024);
         StageRing<AS> rc;
+        int nf = 0;
         for (int i = 0; i < n_chunks; ++i) {
           if (!warp_wait(c_full(rc.stage), rc.par, abort, p.status, tmo)) break;
-          if (chunk_n(i) < kTile && !warp_wait(fixed, 0, abort, p.status, tmo)) break;
+          if (chunk_n(i) < kTile && !warp_wait(fixed, nf++ & 1, abort, p.status, tmo)) break;
           // the epilogue of the last chunk has read O1
           if (i > 0 && !warp_wait(o_free, (i - 1) & 1, abort, p.status, tmo)) break;
           if (!warp_wait(p_full, i & 1, abort, p.status, tmo)) break;
@@ -524,7 +528,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       // the runs before this one, folded in order, once the launch that sums them is through
       if (run > 0) griddep_wait();
       for (int s = 0; s < run; ++s) {
-        const float f = lin_pow(ld, lin_run_tokens<kTile>(p, n_tok, back, s));
+        const float f = lin_pow(ld, lin_run_tokens<kTile, PIECES>(p, n_tok, back, s));
         const float* src = w.sums + ((int64_t)bh * p.segs + s) * DD;
         if (!w.trans) {  // a run's sum lies with its columns first (see below)
 #pragma unroll
@@ -714,7 +718,7 @@ static bool make_map(CUtensorMap* m, const void* t, int64_t heads, int T, int D)
   return encode_tmap_2d_bf16(m, t, D, (uint64_t)heads * T, 64, kTile) == CUDA_SUCCESS;
 }
 
-template <int D, bool SUM>
+template <int D, bool SUM, bool PIECES>
 static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, bool dependent, cudaStream_t st) {
   Params prm;
   prm.p = p;
@@ -736,7 +740,7 @@ static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, bool depe
         return cudaErrorInvalidValue;
     }
   constexpr int kSmem = Smem<D, SUM>::kBytes, kThreads = SUM ? kThreadsSum : kThreadsOut;
-  auto kern = sweep_kernel<D, SUM>;
+  auto kern = sweep_kernel<D, SUM, PIECES>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   if (!SUM) {  // a split that does not fit what the launch allocates would wait forever
@@ -762,23 +766,33 @@ static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, bool depe
 
 bool linear_tc_supported(const Ring& R) {
   if (!R.bf16 || (R.D != 64 && R.D != 128)) return false;
-  // a chunk of 128 positions is 128 slots: zigzag chunks are whole chunks
-  if (R.zz && (R.T / R.cp / 2) % kLinTcChunk) return false;
+  // A chunk's positions are consecutive slots, so a zigzag half of h tokens takes h / 128 chunks,
+  // rounded up, and a chunk costs the same whatever it holds.  Halves of 16 against float32
+  // arithmetic at 15: 4 heads of 128 (T 128, 120) 24 against 53 us, of 64 16 against 26; 32 heads
+  // (T 1024, 960) of 128 160 against 156, of 64 102 against 75; at 64 tokens 142 against some 600.
+  if (R.zz && R.T / R.cp / 2 < 16) return false;
   return (double)R.B * R.Hq * R.T < 2147483647.0 - kLinTcChunk;
+}
+
+template <bool SUM>
+static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, bool dependent, cudaStream_t st) {
+  if (p.seg < p.T)
+    return p.D == 128 ? lintc::run<128, SUM, true>(p, n, sweeps, dependent, st)
+                      : lintc::run<64, SUM, true>(p, n, sweeps, dependent, st);
+  return p.D == 128 ? lintc::run<128, SUM, false>(p, n, sweeps, dependent, st)
+                    : lintc::run<64, SUM, false>(p, n, sweeps, dependent, st);
 }
 
 cudaError_t launch_linear_tc(const Linear& p, cudaStream_t st, bool backward) {
   cudaError_t e;
   if (p.segs > 1) {
     timing_begin(backward ? "linear_bwd_sums" : "linear_fwd_sums", st);
-    e = p.D == 128 ? lintc::run<128, true>(p, p.n_sums, p.sum, false, st)
-                   : lintc::run<64, true>(p, p.n_sums, p.sum, false, st);
+    e = run<true>(p, p.n_sums, p.sum, false, st);
     timing_end(st);
     if (e != cudaSuccess) return e;
   }
   timing_begin(backward ? "linear_bwd" : "linear_fwd", st);
-  e = p.D == 128 ? lintc::run<128, false>(p, p.n_sweeps, p.sweep, p.segs > 1, st)
-                 : lintc::run<64, false>(p, p.n_sweeps, p.sweep, p.segs > 1, st);
+  e = run<false>(p, p.n_sweeps, p.sweep, p.segs > 1, st);
   timing_end(st);
   return e;
 }

@@ -652,8 +652,8 @@ cpattn_status cpattn_rotate_bwd(const cpattn_rotate_desc* desc, const void* q,
  *   states    : [B'][H_q'][D][D] float32 (B', H_q' as for cpattn_partial_fwd), the key's
  *               channel first.  Query heads that share a key head have their own decays, so
  *               their own states.
- * D is a multiple of 8.  With bf16, D 64 or 128 and (CPATTN_ZIGZAG) 2 cp chunks of a multiple
- * of 128 tokens the products run on the tensor cores, with float32 sums: the weighted scores
+ * D is a multiple of 8.  With bf16, D 64 or 128 and (CPATTN_ZIGZAG) 2 cp chunks of 16 tokens or
+ * more the products run on the tensor cores, with float32 sums: the weighted scores
  * and the state that a chunk of 128 tokens starts from are rounded to bf16 as operands, weighted
  * keys to two bf16 numbers.  States are float32 throughout; what goes into one that is handed out
  * carries 24 bits.  (Of 8192 tokens the outputs are off by 2.4e-3 of their norm, 1.7e-3 of it their

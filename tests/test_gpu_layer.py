@@ -284,7 +284,7 @@ class LinearCase:
             (self.S0, s0), (self.dS1, ds1) = (self._state(rng, B, Hq, D) for _ in range(2))
         self.states = s0, ds1
         # where the products run: on tensor cores or in float32
-        self.tc = dtype == "bf16" and D in (64, 128) and (layout == "contiguous" or T // (ranks // a2a) // 2 % 128 == 0)
+        self.tc = dtype == "bf16" and D in (64, 128) and (layout == "contiguous" or T // (ranks // a2a) // 2 >= 16)
 
     def _tensor(self, rng, shape):
         """Natural order for the oracle; layout order, head-sharded for a2a > 1, on the GPU."""
@@ -395,7 +395,12 @@ SHAPES = [
     (1, 2, 1, 1025, 64, "bf16", 1, "contiguous", 1),
     (2, 4, 2, 1024, 128, "bf16", 4, "zigzag", 1),
     (1, 8, 4, 512, 64, "bf16", 4, "zigzag", 2),          # head-sharded: decays by the whole head number
-    (1, 2, 2, 320, 128, "bf16", 2, "zigzag", 1),         # chunks off the 128-token grid: float32
+    (1, 2, 2, 320, 128, "bf16", 2, "zigzag", 1),         # halves of 80 tokens: a chunk each
+    (2, 4, 2, 1200, 128, "bf16", 3, "zigzag", 1),        # of 200: a whole and a partial one, and runs
+    (1, 4, 4, 528, 64, "bf16", 4, "zigzag", 2),          # of 132
+    (1, 2, 1, 520, 128, "bf16", 2, "zigzag", 1),         # of 130
+    (1, 2, 2, 512, 64, "bf16", 16, "zigzag", 1),         # of 16
+    (1, 2, 2, 120, 64, "bf16", 4, "zigzag", 1),          # of 15: float32
     (1, 2, 1, 200, 32, "bf16", 1, "contiguous", 1),
     (1, 2, 2, 1, 128, "f32", 1, "contiguous", 1),
     (2, 4, 2, 63, 128, "f32", 1, "contiguous", 1),
@@ -436,6 +441,19 @@ def test_linear_lengths(dtype, D, T):
         n = min(max(n, 0), T)
         for i, x in enumerate((c.q, c.k, c.v)):
             x.view(len(lengths), -1, T, D)[b, :, n:] = (float("nan"), float("inf"), float("-inf"))[(i + b) % 3]
+    c.check_forward()
+
+
+@pytest.mark.parametrize("T,ranks", [(320, 2), (1200, 3), (1024, 4)])
+def test_linear_lengths_in_zigzag_order(T, ranks):
+    """Positions, not slots, count; rows that end in every kind of chunk."""
+    h = T // ranks // 2
+    lengths = [0, 1, h - 1, h, h + 1, 2 * h + min(h, 129), T - 1, T]
+    c = LinearCase(len(lengths), 2, 1, T, 64, "bf16", ranks, "zigzag", lengths=lengths)
+    slots = torch.from_numpy(c.slots).to(dev())
+    for b, n in enumerate(lengths):
+        for x in (c.q, c.k, c.v):
+            x[0][b][:, slots[n:]] = float("nan")
     c.check_forward()
 
 
