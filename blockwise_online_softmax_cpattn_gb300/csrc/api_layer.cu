@@ -83,6 +83,25 @@ static bool view(const Rotate& p, const void* t, const int64_t* strides, int hea
   return aligned16(t);
 }
 
+// Does an output begin where another one or an input does?  In place, over the same rows of its
+// own input, only where every row stays where it is (not of x: the backward pass's other input).
+static bool rotate_meet(const Rotate& p) {
+  const bool stays = !p.natural_in || !p.m.zz || p.m.cp == 1;
+  for (int o = 0; o < 3; ++o) {
+    const RowView& y = p.out[o];
+    if (!y.p) continue;
+    const int heads = o == 0 ? p.Hq : p.Hkv;
+    for (int i = 0; i < 3; ++i) {
+      const RowView& a = p.in[i];
+      const bool same = a.p == y.p && (p.B == 1 || a.sb == y.sb) && (heads == 1 || a.sh == y.sh) &&
+                        (p.T == 1 || a.st == y.st);
+      if (a.p == y.p && !(i == o && same && stays)) return true;
+      if (p.x[i].p == y.p || (i < o && p.out[i].p == y.p)) return true;
+    }
+  }
+  return false;
+}
+
 // ---------------------------------------------------------------------------
 // linear attention
 // ---------------------------------------------------------------------------
@@ -184,9 +203,7 @@ cpattn_status cpattn_rotate_fwd(const cpattn_rotate_desc* desc, const void* q,
   if (!null_or_aligned(q_weight, 16) || !null_or_aligned(k_weight, 16) || !null_or_aligned(positions, 4) ||
       !null_or_aligned(inv_freq, 8) || (p.rot > 0 && !inv_freq))
     return CPATTN_ERR_INVALID_ARG;
-  // in place only where every row stays where it is
-  const bool moves = p.natural_in && p.m.zz && p.m.cp > 1;
-  if (meet({q_out, k_out, v_out}, {}) || (moves && meet({q_out, k_out, v_out}, {q, k, v}))) return CPATTN_ERR_INVALID_ARG;
+  if (rotate_meet(p) || meet({q_out, k_out, v_out}, {q_weight, k_weight, inv_freq, positions})) return CPATTN_ERR_INVALID_ARG;
   p.w[0] = q_weight;
   p.w[1] = k_weight;
   p.inv_freq = inv_freq;
@@ -228,8 +245,9 @@ cpattn_status cpattn_rotate_bwd(const cpattn_rotate_desc* desc, const void* q,
       !null_or_aligned(dk_weight, 4) || (!p.norm && (dq_weight || dk_weight)))
     return CPATTN_ERR_INVALID_ARG;
   if (!aligned16(workspace) || ws_bytes < rotate_bwd_workspace(p.D, p.norm)) return CPATTN_ERR_INVALID_ARG;
-  const bool moves = p.natural_in && p.m.zz && p.m.cp > 1;
-  if (meet({dq, dk, dv}, {}) || (moves && meet({dq, dk, dv}, {dq_out, dk_out, dv_out}))) return CPATTN_ERR_INVALID_ARG;
+  if (rotate_meet(p) || meet({dq, dk, dv, dq_weight, dk_weight, workspace}, {q_weight, k_weight, inv_freq, positions}) ||
+      meet({dq_weight, dk_weight, workspace}, {q, k, dq_out, dk_out, dv_out}))
+    return CPATTN_ERR_INVALID_ARG;
   p.w[0] = q_weight;
   p.w[1] = k_weight;
   p.inv_freq = inv_freq;
@@ -256,7 +274,8 @@ cpattn_status cpattn_linear_fwd(const cpattn_desc* desc, const void* q, const vo
   if (s != CPATTN_OK) return s;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned(log_decay, 4) ||
       !null_or_aligned(lengths, 4) || !null_or_aligned(state_in, 16) || !null_or_aligned(state_out, 16) ||
-      !aligned16(workspace) || meet({o, state_out}, {q, k, v}))
+      !aligned16(workspace) || meet({o, state_out, workspace}, {q, k, v, log_decay, lengths}) ||
+      meet({o, workspace}, {state_in}))
     return CPATTN_ERR_INVALID_ARG;
   const bool tc = on_tensor_cores(R);
   Linear p;
@@ -310,7 +329,10 @@ cpattn_status cpattn_linear_bwd(const cpattn_desc* desc, const void* q, const vo
       !aligned16(dk) || !aligned16(dv) || !aligned(log_decay, 4) || !null_or_aligned(state_in, 16) ||
       !null_or_aligned(dstate_out, 16) || !null_or_aligned(dstate_in, 16) || !aligned16(workspace))
     return CPATTN_ERR_INVALID_ARG;
-  if (meet({dq, dk, dv, dstate_in}, {q, k, v, dO, state_in, dstate_out})) return CPATTN_ERR_INVALID_ARG;
+  if (meet({dq, dk, dv, dstate_in, workspace}, {q, k, v, log_decay, dO, state_in, dstate_out}))
+    return CPATTN_ERR_INVALID_ARG;
+  // the state's gradient is carried divided by the scale
+  if (dstate_out && R.scale < 0x1p-64f) return CPATTN_ERR_UNSUPPORTED;
   const bool tc = on_tensor_cores(R);
   Linear p;
   plan_linear(desc, R, true, tc, &p);
@@ -379,7 +401,8 @@ cpattn_status cpattn_linear_step(const cpattn_desc* desc, int n_states, const vo
   };
   if (!rows(q, q_token_stride, q_head_stride, R.Hq) || !rows(k, k_token_stride, k_head_stride, R.Hkv) ||
       !rows(v, v_token_stride, v_head_stride, R.Hkv) || !aligned(log_decay, 4) || !null_or_aligned(slots, 4) ||
-      !aligned16(state_in) || !aligned16(state_out) || !aligned16(o) || meet({o, state_out}, {q, k, v}))
+      !aligned16(state_in) || !aligned16(state_out) || !aligned16(o) || meet({o, state_out}, {q, k, v, log_decay, slots}) ||
+      o == state_in)
     return CPATTN_ERR_INVALID_ARG;
   LinStep p;
   p.n = R.B;

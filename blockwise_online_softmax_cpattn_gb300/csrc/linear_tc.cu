@@ -769,7 +769,7 @@ bool linear_tc_supported(const Ring& R) {
   // A chunk's positions are consecutive slots, so a zigzag half of h tokens takes h / 128 chunks,
   // rounded up, and a chunk costs the same whatever it holds.  Halves of 16 against float32
   // arithmetic at 15: 4 heads of 128 (T 128, 120) 24 against 53 us, of 64 16 against 26; 32 heads
-  // (T 1024, 960) of 128 160 against 156, of 64 102 against 75; at 64 tokens 142 against some 600.
+  // (T 1024, 960) of 128 160 against 156, of 64 102 against 75; at 64 tokens 142, where float32 would take some 650 (in proportion to 15).
   if (R.zz && R.T / R.cp / 2 < 16) return false;
   return (double)R.B * R.Hq * R.T < 2147483647.0 - kLinTcChunk;
 }

@@ -569,7 +569,7 @@ cpattn_status cpattn_cache_attn(const cpattn_cache_desc* desc, int n_req, int ma
  * [n_tokens][H][D] (B 1, T n_tokens) are passed as they are.  The rows of an output must
  * not overlap.  An output may be its own input with the same strides where the order of
  * the tokens stays (natural_in 0 or CPATTN_CONTIGUOUS).  Else no output may meet an input or
- * another output (the same pointer: CPATTN_ERR_INVALID_ARG).
+ * another output (the same pointer, or its own input by other strides: CPATTN_ERR_INVALID_ARG).
  */
 typedef enum cpattn_pairing { CPATTN_HALVES = 0, CPATTN_NEIGHBOURS = 1 } cpattn_pairing;
 
@@ -687,7 +687,8 @@ size_t cpattn_linear_bwd_workspace(const cpattn_desc* desc);
 /*
  * Backward of cpattn_linear_fwd without lengths (behind a shorter row's end give dO = 0).
  *   dO         : [B][H_q][T][D]
- *   dstate_out : upstream gradient of state_out, or null for zero
+ *   dstate_out : upstream gradient of state_out, or null for zero.  Must be null for a scale below
+ *                2^-64 (CPATTN_ERR_UNSUPPORTED): it is carried divided by the scale
  *   dq, dk, dv : dk and dv sum over the query heads of a group
  *   dstate_in  : gradient of state_in, or null
  * Nothing is kept from the forward pass but its inputs.  No atomics: repeated calls are

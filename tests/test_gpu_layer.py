@@ -233,6 +233,39 @@ def test_rotation_in_place_and_packed_tokens():
     assert np.array_equal(got[:, Hq + Hkv:], heads[:, Hq + Hkv:])
 
 
+@pytest.mark.parametrize("dtype,D,norm", [("bf16", 128, 1), ("f32", 48, 1), ("bf16", 64, 0)])
+def test_rotation_backward_in_place(dtype, D, norm):
+    """Gradients over the upstream gradients: the same numbers as apart from them."""
+    cp = cp_mod()
+    rng = np.random.default_rng(7)
+    d = cp.make_rotate_desc(2, 3, 2, 700, D, dtype=dtype, norm=norm)
+    shapes = [(2, h, 700, D) for h in (3, 2, 2)]
+    x = [draw(rng, sh, dtype)[0] for sh in shapes]
+    dy = [draw(rng, sh, dtype)[0] for sh in shapes]
+    f = torch.from_numpy(100.0 ** (-np.arange(D // 2) / D)).to(dev())
+    ws = torch.empty(cp.cpattn_rotate_bwd_workspace(d), dtype=torch.uint8, device=dev())
+    dw = [torch.empty(D, device=dev()) for _ in range(4)]
+
+    def run(out, dws):
+        checked(cp, cp.cpattn_rotate_bwd(d, x[0] if norm else None, x[1] if norm else None, None, None, f, None,
+                                         *dy, *out, dws[0] if norm else None, dws[1] if norm else None, ws))
+
+    apart = [torch.empty_like(t) for t in dy]
+    run(apart, dw[:2])
+    run(dy, dw[2:])
+    for a, b in zip(apart, dy):
+        assert torch.equal(a, b)
+    if norm:
+        assert torch.equal(dw[0], dw[2]) and torch.equal(dw[1], dw[3])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D", [(1, 128), (5, 128), (33, 64), (3, 48)])
+def test_rotation_without_epsilon(dtype, T, D):
+    """A warp whose slots are not all of the batch divides nothing by nothing."""
+    rotation_case(cp_mod(), 1, 3, 2, T, D, dtype, eps=0.0)
+
+
 def test_rotation_past_32_bits():
     """Strides and offsets of more than 2^31 elements."""
     cp = cp_mod()

@@ -188,6 +188,21 @@ def test_rotation_outputs_that_meet(cp):
     assert _bwd(cp, _rot(cp), dq=10 * FAKE) == 1
 
 
+def test_rotation_in_place_only_row_by_row(cp):
+    """Where tokens stay, an output may be its own input, but no other and by the same strides."""
+    d = _rot(cp)
+    q, k, v = fake(3)
+    assert _fwd(cp, d, qo=k) == 1 and _fwd(cp, d, ko=q) == 1 and _fwd(cp, d, vo=k) == 1
+    assert _fwd(cp, d, qo=4 * FAKE) == 1                     # (a weight)
+    assert _bwd(cp, d, dq=q) == 1 and _bwd(cp, d, dk=k) == 1  # the forward's inputs
+    assert _bwd(cp, d, dqw=32 * FAKE, dkw=32 * FAKE) == 1 and _bwd(cp, d, ws=q) == 1
+    i = (ctypes.c_int64 * 3)(64 * 64 * 4, 64 * 64, 64)
+    o = (ctypes.c_int64 * 3)(64 * 64 * 4, 64, 64 * 4)
+    p = fake(6)
+    assert cp._lib.cpattn_rotate_fwd(ctypes.byref(d), p[0], i, p[1], None, None, None, None, None, p[5], None,
+                                     p[0], o, p[4], None, None, None, 0) == 1
+
+
 def test_rotation_strides(cp):
     """Off the 16-byte grid, negative, or an output whose rows would meet."""
     d = _rot(cp)
@@ -236,6 +251,9 @@ def test_linear_arguments(cp):
         assert fwd(*good[:i], 64 * FAKE + 2, *good[i + 1:]) == 1, i
     for x in p[:3]:                                     # o or the state over an input
         assert fwd(*good[:6], x, *good[7:]) == 1 and fwd(*good[:7], x, good[8]) == 1
+    s = 40 * FAKE                                       # o over state_in; the workspace over anything
+    assert fwd(*good[:5], s, s, *good[7:]) == 1 and fwd(*good[:5], s, *good[6:8], s) == 1
+    assert fwd(*good[:7], s, s) == 1 and fwd(*good[:8], p[3]) == 1 and fwd(*good[:8], p[4]) == 1
     n = cp.cpattn_linear_workspace(d)
     assert n > 16 and fwd(*good, n=n - 1) == 1
     bwd = lambda *a, n=1 << 40: cp.cpattn_linear_bwd(d, *a, n, 0)  # noqa: E731
@@ -248,7 +266,11 @@ def test_linear_arguments(cp):
     for i in (7, 8, 9, 10):                             # an output over an input or another output
         for x in good[:3] + good[4:7] + [y for j, y in enumerate(good[7:11], 7) if j != i]:
             assert bwd(*good[:i], x, *good[i + 1:]) == 1, i
+    for x in good[:11]:
+        assert bwd(*good[:11], x) == 1
     assert bwd(*good, n=cp.cpattn_linear_bwd_workspace(d) - 1) == 1
+    small = cp.make_desc(1, 4, 2, 4096, 64, 2, "zigzag", "bf16", scale=2.0 ** -65)
+    assert cp.cpattn_linear_bwd(small, *good, 1 << 40, 0) == 2   # 1 / scale times the state's gradient
     # shared key heads: the query heads' own gradients
     same = cp.make_desc(1, 4, 4, 4096, 64, 2, "zigzag", "bf16")
     assert cp.cpattn_linear_bwd_workspace(d) >= cp.cpattn_linear_bwd_workspace(same) + 2 * 4 * 4 * 4096 * 64
@@ -266,7 +288,8 @@ def test_step_arguments(cp):
     assert call(q=None) == 1 and call(q=FAKE + 8) == 1 and call(ts=252) == 1 and call(hs=60) == 1
     assert call(ts=-256) == 1 and call(ld=None) == 1 and call(slots=64 * FAKE + 2) == 1 and call(n=-1) == 1
     assert call(s0=None) == 1 and call(s1=64 * FAKE + 4) == 1 and call(o=None) == 1
-    assert call(o=p[1]) == 1 and call(s1=p[0]) == 1 and call(o=p[5]) == 1
+    assert call(o=p[1]) == 1 and call(s1=p[0]) == 1 and call(o=p[5]) == 1 and call(o=p[4]) == 1
+    assert call(o=p[3]) == 1 and call(slots=p[5]) == 1
     for kw in (dict(T=2), dict(T=2, cp=2), dict(a2a=2, cp=2, T=2)):
         base = dict(B=3, H_q=4, H_kv=2, T=1, D=64, cp=1, layout="contiguous", dtype="bf16")
         base.update(kw)
