@@ -400,7 +400,9 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Rotate p) {
             dot = fma2(mul2(two(a, i), two(wa, i)), x, fma2(mul2(two(b, i), two(wb, i)), y, dot));
           }
           // with r = 1 / sqrt(..): dw += g (r x),  dx = r w g - x (r^3 mean(w g x))
-          const float rs = rsqrtf(row_sum(sum.x + sum.y, p.lanes) * p.inv_d + p.eps);
+          // (lanes without a row add nothing, also where eps is 0)
+          const float all = row_sum(sum.x + sum.y, p.lanes) * p.inv_d + p.eps;
+          const float rs = s.live ? rsqrtf(all) : 0.f;
           const float m = -row_sum(dot.x + dot.y, p.lanes) * p.inv_d * rs * rs;
           const float2 rs2 = make_float2(rs, rs), m2 = make_float2(m, m);
 #pragma unroll
