@@ -7,8 +7,10 @@
 // register tiles over shared memory.  M lives in registers (8 x 8 a thread at D 128) with a copy
 // in shared memory as the operand of a M.  Head dimensions in between are padded with zeros to
 // 64 or 128.  Bound by the float32 units, 4 D (D + 32) FLOP a token and head, and by how two warps
-// a scheduler (a block fills an SM's shared memory) wait for the loads of a chunk: 1500 tokens of 16
-// heads at D 128 take 104 us, the units' part of it 43.  (16 warps, 4 x 4 tiles: 121 us.)
+// a scheduler (a block fills an SM's shared memory) wait for each other's chains: 8192 tokens of 32
+// heads at D 128 take 881 us, the units' part of it 332 (32 heads on 8 with gradients 2.2 ms); 1500
+// tokens of 16 heads, 2 or 3 chunks a block, 98 (43).  With tiles fetched when they were needed, and
+// not ahead, these took 1269, 3018 and 104 us; 16 warps with 4 x 4 tiles were slower, too (121).
 #include "layer.cuh"
 
 namespace cpattn {
@@ -32,26 +34,47 @@ template <int DP>
 struct Smem {
   static constexpr int kLd = DP + 4;   // row stride: eight rows meet eight bank groups
   static constexpr int kPLd = C + 4;
-  static constexpr int kA = 0;
-  static constexpr int kB = kA + C * kLd;
-  static constexpr int kC = kB + C * kLd;
-  static constexpr int kP = kC + C * kLd;
+  static constexpr int kTile = C * kLd;
+  static constexpr int kP = 4 * kTile;  // (four tiles)
   static constexpr int kM = kP + C * kPLd;
   static constexpr int kPow = kM + DP * kLd;
   static constexpr int kFloats = kPow + C + 2;
 };
 
+// Rows of n tokens from pos0 on, zeros behind them and behind D.  float32 comes by asynchronous
+// copies, in flight until wait_tiles; bf16 is widened on its way.
 template <typename E, int DP>
 __device__ __forceinline__ void load_tile(const Linear& p, const void* t, int64_t head, int pos0, int n,
                                           float* dst) {
-  constexpr int LD = Smem<DP>::kLd, V = DP / 4;
+  constexpr int LD = Smem<DP>::kLd, V = DP / 4, kStep = kThreads / V;
+  const int r0 = threadIdx.x / V, c = 4 * (threadIdx.x - r0 * V);
   const E* src = static_cast<const E*>(t) + head * p.T * p.D;
-  for (int i = threadIdx.x; i < C * V; i += kThreads) {
-    const int r = i / V, c = 4 * (i - r * V);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < n && c < p.D) x = load4(src + (int64_t)p.m.slot(pos0 + r) * p.D + c);
-    *reinterpret_cast<float4*>(dst + r * LD + c) = x;
+  if constexpr (sizeof(E) == 4) {
+#pragma unroll
+    for (int r = r0; r < C; r += kStep) {
+      const bool there = r < n && c < p.D;
+      const float* from = there ? src + (int64_t)p.m.slot(pos0 + r) * p.D + c : src;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * LD + c)), "l"(from),
+                   "r"(there ? 16 : 0)
+                   : "memory");
+    }
+  } else {
+    float4 x[C / kStep];
+#pragma unroll
+    for (int i = 0; i < C / kStep; ++i) {
+      const int r = r0 + i * kStep;
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < n && c < p.D) x[i] = load4(src + (int64_t)p.m.slot(pos0 + r) * p.D + c);
+    }
+#pragma unroll
+    for (int i = 0; i < C / kStep; ++i) *reinterpret_cast<float4*>(dst + (r0 + i * kStep) * LD + c) = x[i];
   }
+}
+__device__ __forceinline__ void commit_tile() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the last N groups have come
+template <int N>
+__device__ __forceinline__ void wait_tiles() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <typename E, int DP, bool SUM>
@@ -59,7 +82,8 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
   using L = Smem<DP>;
   constexpr int LD = L::kLd, PL = L::kPLd, R = DP / 64;  // R: 4-wide tiles of DP a thread
   extern __shared__ __align__(16) float sm[];
-  float *const sa = sm + L::kA, *const sb = sm + L::kB, *const sc = sm + L::kC;
+  // tiles of a, b and c, and of the next chunk's a (SUM: b, c and the next b and c)
+  float *sa = sm, *sb = sm + L::kTile, *sc = sm + 2 * L::kTile, *sx = sm + 3 * L::kTile;
   float *const sp = sm + L::kP, *const sM = sm + L::kM, *const pw = sm + L::kPow;
   const int runs = SUM ? p.segs - 1 : p.segs;  // the last run's own sum is nobody's start
   const int bh = blockIdx.x / runs, run = blockIdx.x - bh * runs;
@@ -72,6 +96,19 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
   const int64_t hb = (int64_t)b * (p.Hq / w.rep_b) + h / w.rep_b;
   const int64_t hc = (int64_t)b * (p.Hq / w.rep_c) + h / w.rep_c;
   for (int i = threadIdx.x; i <= C + 1; i += kThreads) pw[i] = lin_pow(ld, i);
+
+  const int m1 = min((run + 1) * p.cps, p.nch);
+  auto pos_of = [&](int m) { return lin_first<C, false>(p, lin_chunk(p.nch, w.back, m)); };
+  // (0: a row's padding, in sweeps from the front, or past the run)
+  auto size_of = [&](int m) { return m < m1 ? lin_size<C, false>(p, n_tok, lin_chunk(p.nch, w.back, m)) : 0; };
+  int m = run * p.cps, n = size_of(m);
+  if (n > 0) {
+    if (!SUM) load_tile<E, DP>(p, w.a, ha, pos_of(m), n, sa);
+    commit_tile();
+    load_tile<E, DP>(p, w.b, hb, pos_of(m), n, sb);
+    if (SUM) load_tile<E, DP>(p, w.c, hc, pos_of(m), n, sc);
+    commit_tile();
+  }
 
   // M of this thread: rows 4 ty + 64 i + x, columns 4 tx + 64 j + 2 y and the next
   float2 M[R][4][R][2] = {};
@@ -107,14 +144,17 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
       fold(lin_pow(ld, lin_run_tokens<C, false>(p, n_tok, w.back, s)), 1.f, w.sums + ((int64_t)bh * p.segs + s) * DD);
   }
 
-  const int m1 = min((run + 1) * p.cps, p.nch);
-  for (int m = run * p.cps; m < m1; ++m) {
-    const int chunk = lin_chunk(p.nch, w.back, m), pos0 = lin_first<C, false>(p, chunk);
-    const int n = lin_size<C, false>(p, n_tok, chunk);
-    if (n == 0) break;  // a row's padding (sweeps from the front only)
+  // A chunk's tiles come ahead of it: a while the chunk before runs, b (in the place of that one's
+  // a) during its last product, c during the scores.
+  for (int next; n > 0; ++m, n = next) {
+    const int pos0 = pos_of(m);
+    next = size_of(m + 1);
     __syncthreads();    // the last chunk's tiles have been read
     if (!SUM) {
-      load_tile<E, DP>(p, w.a, ha, pos0, n, sa);
+      load_tile<E, DP>(p, w.c, hc, pos0, n, sc);
+      commit_tile();
+      if (next > 0) load_tile<E, DP>(p, w.a, ha, pos_of(m + 1), next, sx);
+      commit_tile();
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -123,9 +163,15 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
           for (int j = 0; j < R; ++j)
             *reinterpret_cast<float4*>(sM + (4 * ty + 64 * i + x) * LD + 4 * tx + 64 * j) =
                 make_float4(M[i][x][j][0].x, M[i][x][j][0].y, M[i][x][j][1].x, M[i][x][j][1].y);
+      wait_tiles<2>();
+    } else {
+      if (next > 0) {
+        load_tile<E, DP>(p, w.b, hb, pos_of(m + 1), next, sa);
+        load_tile<E, DP>(p, w.c, hc, pos_of(m + 1), next, sx);
+      }
+      commit_tile();
+      wait_tiles<1>();
     }
-    load_tile<E, DP>(p, w.b, hb, pos0, n, sb);
-    load_tile<E, DP>(p, w.c, hc, pos0, n, sc);
     __syncthreads();
     if (!SUM) {
       float2 s2[4][4] = {};  // rows ty + 16 i, columns tx + 16 j; even and odd channels apart
@@ -153,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
           const int e = w.back ? col - row : row - col;
           sp[row * PL + col] = e >= 0 ? (s2[i][j].x + s2[i][j].y) * pw[e] : 0.f;
         }
+      wait_tiles<1>();  // c
       __syncthreads();
       float2 o[4][R][2] = {}, t[4][R][2] = {};  // rows ty + 16 i, columns 4 tx + 64 j + 2 y
       // x[row][k] m[k][columns] over k, four of them a step: their rows of x come as one vector
@@ -198,6 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
           else store4(static_cast<E*>(w.out) + at + c, y);
         }
       }
+      __syncthreads();  // a has been read
+      if (next > 0) load_tile<E, DP>(p, w.b, hb, pos_of(m + 1), next, sa);
+      commit_tile();
     }
     const float2 rn = make_float2(pw[n], pw[n]);
 #pragma unroll
@@ -230,6 +280,19 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
 #pragma unroll
             for (int y = 0; y < 2; ++y) M[i][x][j][y] = fma2(f2, v[j][y], M[i][x][j][y]);
         }
+    }
+    // the next chunk's tiles: a in sx, b in sa, c (SUM: in sx) yet to come
+    float* const old = sb;
+    sb = sa;
+    if (SUM) {
+      sa = old;
+      float* const o = sc;
+      sc = sx;
+      sx = o;
+    } else {
+      sa = sx;
+      sx = sc;
+      sc = old;
     }
   }
 
