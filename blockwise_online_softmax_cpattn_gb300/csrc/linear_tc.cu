@@ -59,21 +59,22 @@ static_assert(128 * (kRegsControl + 2 * kRegsOut + 2 * kRegsState) <= kThreadsOu
 template <int D, bool SUM>
 struct Smem {
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kAS = SUM ? 0 : D == 128 ? 2 : 3;  // stages of a; of b and c
+  static constexpr int kAS = SUM ? 0 : D == 128 ? 2 : 3;  // stages of a, of b, of c
   static constexpr int kBS = SUM ? (D == 128 ? 2 : 4) : kAS;
-  static constexpr int kXS = SUM ? (D == 128 ? 3 : 5) : 1;  // parts of the weighted b (else unused)
+  static constexpr int kCS = !SUM && D == 128 ? 1 : kBS;
+  static constexpr int kXS = SUM ? (D == 128 ? 3 : 5) : 1;  // parts of the weighted b
   static constexpr int kA = 0;
   static constexpr int kB = kA + kAS * kTileBytes;
   static constexpr int kC = kB + kBS * kTileBytes;
-  static constexpr int kX = kC + kBS * kTileBytes;
+  static constexpr int kX = kC + kCS * kTileBytes;
   // (at D 64 U reads on behind a part's tile, as far as another one)
-  static constexpr int kM = kX + (SUM ? (kXS + (D == 64)) * kTileBytes : 0);
-  // the output's staging, 4 KB a warp: at D 128 where M lies, at D 64 that is too small
+  static constexpr int kM = kX + (kXS + (SUM && D == 64)) * kTileBytes;
+  // the output's staging, 4 KB a warp: at D 128 where a lies, at D 64 that is too small
   static constexpr int kO = kM + (SUM ? 0 : D * D * 2);
   static constexpr int kPow = kO + (SUM || D == 128 ? 0 : 8 * 4096);
   // powers r^e at kPow + 4 (128 + e), zeros for e < 0
   static constexpr int kBar = kPow + 4 * 264;
-  static constexpr int kNumBars = 2 * (kAS + 2 * kBS) + 15 + 3 + kXS;
+  static constexpr int kNumBars = 2 * (kAS + kBS + kCS) + 15 + 3 + kXS;
   static constexpr int kMisc = kBar + 8 * kNumBars;
   static constexpr int kBytes = kMisc + 16;
 };
@@ -140,7 +141,7 @@ template <int D, bool SUM, bool PIECES>
 __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
     sweep_kernel(const __grid_constant__ Params prm) {
   using L = Smem<D, SUM>;
-  constexpr int AS = L::kAS, BS = L::kBS, XS = L::kXS;
+  constexpr int AS = L::kAS, BS = L::kBS, CS = L::kCS, XS = L::kXS;
   constexpr uint32_t kTmemCols = SUM ? 2 * D : 512;
   const Linear& p = prm.p;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -155,13 +156,14 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
   auto b_full = [&](int s) { return bars + 8 * (2 * AS + s); };
   auto b_empty = [&](int s) { return bars + 8 * (2 * AS + BS + s); };
   auto c_full = [&](int s) { return bars + 8 * (2 * AS + 2 * BS + s); };
-  auto c_empty = [&](int s) { return bars + 8 * (2 * AS + 3 * BS + s); };
-  const uint32_t one = bars + 8 * 2 * (AS + 2 * BS);
+  auto c_empty = [&](int s) { return bars + 8 * (2 * AS + 2 * BS + CS + s); };
+  const uint32_t one = bars + 8 * 2 * (AS + BS + CS);
   auto s_full = [&](int i) { return one + 8 * (i & 1); };        // pairs
   auto x_full = [&](int k) { return one + 8 * (2 + (k & 1)); };  // parts written, the k-th time
   auto u_full = [&](int i) { return one + 8 * (4 + (i & 1)); };
   const uint32_t p_full = one + 48, o_full = one + 56, o_free = one + 64, m_full = one + 72,
-                 m_free = one + 80, h_done = one + 88, fixed = one + 96, o2_full = one + 104, e_done = one + 112, fin = one + 120;
+                 m_free = one + 80, h_done = one + 88, o2_full = one + 96, fin = one + 120;
+  auto fixed = [&](int k) { return one + 104 + 8 * (k & 1); };  // partial chunks, a pair
   auto x_empty = [&](int s) { return one + 144 + 8 * s; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
@@ -194,14 +196,16 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) mbar_init(bars + 8 * i, 1);
-    // c_empty: O1 and U; e_done: the eight warps that stage the output; the rest by threads
-    mbar_init(e_done, 8);
-    for (int i = 0; i < BS; ++i) mbar_init(c_empty(i), SUM ? 1 : 2);
-    for (int i = 0; i < 2; ++i) mbar_init(x_full(i), 256);
+    // a_empty: the eight warps that stage the output; c_empty: O1 and U; the rest by threads
+    for (int i = 0; i < AS; ++i) mbar_init(a_empty(i), 8);
+    for (int i = 0; i < CS; ++i) mbar_init(c_empty(i), SUM ? 1 : 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(x_full(i), 256);
+      mbar_init(fixed(i), 256);
+    }
     mbar_init(p_full, 256);
     mbar_init(o_free, 256);
     mbar_init(m_full, 256);
-    mbar_init(fixed, 256);
     *abort = 0;
     fence_barrier_init();
   }
@@ -224,7 +228,8 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       // ---------------------------------------------------------- producer
       if (lane == 0) {
         StageRing<AS == 0 ? 1 : AS> ra;
-        StageRing<BS> rb, rc;
+        StageRing<BS> rb;
+        StageRing<CS> rc;
         bool ok = true;
         for (int i = 0; i < n_chunks && ok; ++i) {
           const int slot = p.m.slot(chunk_pos(i));
@@ -248,10 +253,10 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         // never leave with a copy still writing into this block's shared memory
         for (int s = 0; s < AS; ++s)
           if (ra.was_issued(s)) drain_wait(a_full(s), ra.issued_parity(s));
-        for (int s = 0; s < BS; ++s) {
+        for (int s = 0; s < BS; ++s)
           if (rb.was_issued(s)) drain_wait(b_full(s), rb.issued_parity(s));
+        for (int s = 0; s < CS; ++s)
           if (rc.was_issued(s)) drain_wait(c_full(s), rc.issued_parity(s));
-        }
       }
     } else if (warp == 1) {
       if constexpr (!SUM) {
@@ -265,10 +270,15 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           if (!warp_wait(a_full(ra.stage), ra.par, abort, p.status, tmo) ||
               !warp_wait(b_full(ra.stage), ra.par, abort, p.status, tmo))
             break;
-          // S's place is free once O1 of the last chunk has read P there
+          // S's place is free once O1 of the last chunk has read P there (and s_full of the last but
+          // one has been seen by everyone)
           if (i > 0 && !warp_wait(o_full, (i - 1) & 1, abort, p.status, tmo)) break;
+          if (i > 1 && !warp_wait(u_full(i), (i >> 1 & 1) ^ 1, abort, p.status, tmo)) break;
           // a partial chunk's rows of b and c behind its end are zeroed first
-          if (chunk_n(i) < kTile && !warp_wait(fixed, nf++ & 1, abort, p.status, tmo)) break;
+          if (chunk_n(i) < kTile) {
+            if (!warp_wait(fixed(nf), nf >> 1 & 1, abort, p.status, tmo)) break;
+            ++nf;
+          }
           tc_fence_after();
           const uint32_t st = ra.stage * (L::kTileBytes >> 4);
 #pragma unroll 4
@@ -290,11 +300,14 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         const bool leader = elect_one();
         constexpr uint32_t kId = idesc_bf16(128, D, false, true);
         const uint64_t cd0 = sdesc_sw128(sbase + L::kC, kTile * 128, 1024);
-        StageRing<AS> rc;
+        StageRing<CS> rc;
         int nf = 0;
         for (int i = 0; i < n_chunks; ++i) {
           if (!warp_wait(c_full(rc.stage), rc.par, abort, p.status, tmo)) break;
-          if (chunk_n(i) < kTile && !warp_wait(fixed, nf++ & 1, abort, p.status, tmo)) break;
+          if (chunk_n(i) < kTile) {
+            if (!warp_wait(fixed(nf), nf >> 1 & 1, abort, p.status, tmo)) break;
+            ++nf;
+          }
           // the epilogue of the last chunk has read O1
           if (i > 0 && !warp_wait(o_free, (i - 1) & 1, abort, p.status, tmo)) break;
           if (!warp_wait(p_full, i & 1, abort, p.status, tmo)) break;
@@ -323,13 +336,13 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       const uint64_t cd0 = sdesc_sw128(sbase + L::kC, kTile * 128, 1024);
       const uint64_t ad0 = sdesc_sw128(sbase + L::kA, 16, 1024);
       const uint64_t md = sdesc_sw128(sbase + L::kM, D * 128, 1024);
-      const uint64_t al0 = sdesc_sw128(sbase + L::kA, kTile * 128, 1024);
       const uint64_t xd0 = sdesc_sw128(sbase + L::kX, kTile * 128, 1024);
       StageRing<BS> rb;
+      StageRing<CS> rc;
       bool ok = true;
       int k = 0, x = 0;
       for (int i = 0; i < n_chunks && ok; ++i) {
-        const uint32_t st = rb.stage * (L::kTileBytes >> 4);
+        const uint32_t st = rb.stage * (L::kTileBytes >> 4), stc = rc.stage * (L::kTileBytes >> 4);
         if constexpr (!SUM) {
           // the epilogue of the last chunk has read O2
           if (!(ok = (i == 0 || warp_wait(o_free, (i - 1) & 1, abort, p.status, tmo)) &&
@@ -347,12 +360,12 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           }
           __syncwarp();
         }
-        if (!(ok = warp_wait(c_full(rb.stage), rb.par, abort, p.status, tmo))) break;
-        // a part: b's place, a's place (its tile is laid out alike), or a buffer of the sums'
+        if (!(ok = warp_wait(c_full(rc.stage), rc.par, abort, p.status, tmo))) break;
+        // a part: b's place, or one of its own
         auto product = [&](uint64_t pd, bool first) {
 #pragma unroll 4
           for (int kk = 0; kk < kTile / 16; ++kk)
-            if (leader) mma_ss(tU(i), pd + (uint64_t)(kk * 128), cd0 + st + (uint64_t)(kk * 128), kId, !first || kk > 0);
+            if (leader) mma_ss(tU(i), pd + (uint64_t)(kk * 128), cd0 + stc + (uint64_t)(kk * 128), kId, !first || kk > 0);
         };
         if (!(ok = warp_wait(x_full(k), (k >> 1) & 1, abort, p.status, tmo))) break;
         ++k;
@@ -366,8 +379,8 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           }
           product(bd0 + st, parts == 1);
         } else {
-          if (parts > 1) product(al0 + st, true);
-          product(bd0 + st, parts == 1);
+          product(xd0, true);
+          product(bd0 + st, false);
           if (parts == 3) {
             if (leader) mma_commit(h_done);
             __syncwarp();
@@ -380,11 +393,11 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         if (leader) {
           mma_commit(u_full(i));
           mma_commit(b_empty(rb.stage));
-          mma_commit(c_empty(rb.stage));
-          if (!SUM) mma_commit(a_empty(rb.stage));
+          mma_commit(c_empty(rc.stage));
         }
         __syncwarp();
         rb.advance();
+        rc.advance();
       }
       if (leader) mma_commit(fin + 16);
       __syncwarp();
@@ -397,6 +410,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       const int quad = warp & 3, row = quad * 32 + lane, half = warp >> 2 & 1;
       const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
       constexpr int HC = D / 2;
+      int sa = 0;  // stage of a
       for (int i = 0; i < n_chunks; ++i) {
         const int pos0 = chunk_pos(i), n = chunk_n(i);
         if (!warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo)) break;
@@ -445,7 +459,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         // whole chunks go by way of shared memory: this warp's 32 lines of 64 bf16 or 32 float32
         // columns (at D 64 of 32 bf16: half lines), swizzled as the tensor map has it
         const bool staged = n == kTile;
-        const int area = (D == 128 ? L::kM : L::kO) + (quad * 2 + half) * 4096;
+        const int area = (D == 128 ? L::kA + sa * L::kTileBytes : L::kO) + (quad * 2 + half) * 4096;
         const int lchunks = D == 64 && !w.out_f32 ? 4 : 8, lswz = D == 64 && !w.out_f32 ? lane >> 1 & 3 : lane & 7;
         uint4* const line = reinterpret_cast<uint4*>(smem + area) + lane * lchunks;
         auto leave = [&](int col) {
@@ -495,7 +509,8 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           }
         }
         if (staged && !w.out_f32) leave(0);
-        if (lane == 0) mbar_arrive(e_done);
+        if (lane == 0) mbar_arrive(a_empty(sa));
+        if (++sa == AS) sa = 0;
       }
       if (lane == 0) bulk_wait_all();
     }
@@ -579,8 +594,9 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
     };
     if (!SUM && n_chunks > 0) publish();
     StageRing<BS> rb;
+    StageRing<CS> rc;
     bool ok = true;
-    int k = 0, x = 0;
+    int k = 0, x = 0, nf = 0;
     uint32_t xpar = 0;
     for (int i = 0; i < n_chunks && ok; ++i) {
       const int n = chunk_n(i);
@@ -591,14 +607,14 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       const int chunk0 = (col0 & 63) >> 3;
       if (n < kTile) {
         // rows behind the last token hold anything: zeros, in b and in c
-        if (!(ok = warp_wait(c_full(rb.stage), rb.par, abort, p.status, tmo))) break;
+        if (!(ok = warp_wait(c_full(rc.stage), rc.par, abort, p.status, tmo))) break;
         if (row >= n) {
-          uint4* const cline = line + (L::kC - L::kB) / 16;
+          uint4* const cline = line + (L::kC - L::kB + (rc.stage - rb.stage) * L::kTileBytes) / 16;
 #pragma unroll
           for (int j = 0; j < HC / 8; ++j) line[chunk0 + j] = cline[chunk0 + j] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
-        if (!SUM) mbar_arrive(fixed);
+        if (!SUM) mbar_arrive(fixed(nf++));
       }
       // S has read b
       if (!SUM && !(ok = warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo))) break;
@@ -648,9 +664,8 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         mbar_arrive(x_full(k++));
         if (i > 0 && !(ok = take(i - 1))) break;  // while this chunk's product runs
       } else {
-        // O2 has read a: its tile takes the smallest part
-        if (!(ok = warp_wait(m_free, i & 1, abort, p.status, tmo))) break;
-        uint4* const aline = line - (L::kB - L::kA) / 16;
+        // the smallest part has a place of its own: U of the last chunk has read it
+        uint4* const xline = line + (L::kX - L::kB - rb.stage * L::kTileBytes) / 16;
         if (parts < 3) {
 #pragma unroll 2
           for (int j = 0; j < HC / 8; ++j) {
@@ -658,7 +673,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
             uint4 hi, mid, lo;
             split(line[at], hi, mid, lo, false);
             line[at] = hi;
-            if (parts == 2) aline[at] = mid;
+            xline[at] = mid;
           }
         } else {
           uint4 hi[HC / 8];
@@ -668,7 +683,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
             uint4 mid, lo;
             split(line[at], hi[j], mid, lo, true);
             line[at] = mid;
-            aline[at] = lo;
+            xline[at] = lo;
           }
           fence_proxy_async_smem();
           mbar_arrive(x_full(k++));
@@ -680,11 +695,12 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         mbar_arrive(x_full(k++));
       }
       rb.advance();
+      rc.advance();
       if constexpr (!SUM) {
         if (!(ok = take(i))) break;
         if (i + 1 < n_chunks) {
-          // O2 of this chunk has read the old copy (m_free), and the output staged over it has left
-          if (!(ok = warp_wait(e_done, i & 1, abort, p.status, tmo))) break;
+          // O2 of this chunk has read the old copy
+          if (!(ok = warp_wait(m_free, i & 1, abort, p.status, tmo))) break;
           publish();
         }
       }
