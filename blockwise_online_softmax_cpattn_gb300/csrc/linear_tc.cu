@@ -10,9 +10,9 @@
 //   M = w(n) M + U
 //
 // M itself stays in float32, in registers (two threads a row, one channel of b).  b is weighted once
-// S has read it, as two bf16 numbers, hi in b's place and what is left, lo, in that of a, which O2
-// has read by then, and U is the sum of two products: 16 bits.  For a state that is handed out in
-// float32, in the sums and in the sequence's last run, it is three, 24 bits.  The smallest part is
+// S has read it, as two bf16 numbers, hi in b's place and what is left, lo, in a place of its own,
+// and U is the sum of two products: 16 bits.  For a state that is handed out in float32, in the sums
+// and in the sequence's last run, it is three, 24 bits.  The smallest part is
 // summed first: so the large numbers go through eight steps of the tensor cores' sum (16 terms
 // each) and not through all.  As operands P and M are rounded to bf16 once, like the output itself.
 // Errors against float64, of the norm (8192 tokens, D 128): outputs 2.3e-3, of which the output's
@@ -21,12 +21,12 @@
 // runs longer than 384 terms.
 //
 // Warp roles (640 threads):
-//   warp 0        TMA producer: the tiles a, b, c of a chunk, two stages each
+//   warp 0        TMA producer: the tiles a, b, c of a chunk, two stages of a and b and one of c
+//                 (which is wanted last; three each at D 64)
 //   warp 1        issues S;  warp 2: O1;  warp 3: O2 and U
-//   warps 4-11    the output, two threads a row: S -> P, then the epilogue, staged where M lies as
-//                 bf16 (O2 has read it, and the next M comes last) and out by TMA: stored from
-//                 registers, every instruction touches 32 lines, and loads and stores of the other
-//                 warps wait for that, 15 % of the time
+//   warps 4-11    the output, two threads a row: S -> P, then the epilogue, staged where a lies (S
+//                 and O2 have read it) and out by TMA: stored from registers, every instruction
+//                 touches 32 lines, and loads and stores of the other warps wait for that, 15 %
 //   warps 12-19   the state, two threads a row: b times its weights, M, its bf16 copy
 // Issuers are whole warps with one elected lane, as in tc_fwd.cu.  TMEM: S/P [0, 128),
 // O1, O2 and U of D columns each behind it.
@@ -36,9 +36,15 @@
 //
 // Measured (GB300, D 128, 8192 tokens of 32 heads: 128 runs of 16 chunks): the sums 35 us, 5.2 TB/s
 // of memory reads; the sweep 62 us, 6000 cycles a chunk where 128 KB from and to memory would take
-// 4700 and the products 3100.  It is bound by the chain of steps within a chunk, which the roles
-// overlap but for S -> P -> O1 -> (O's place free) and M -> O2 -> (a's place free) -> U -> M: halving
-// what is loaded, or leaving out seven eighths of the products, changed its time by 5 % at most.
+// 4700 and the products 3100; 131072 tokens of 8 heads 235 us (152 runs).  It is bound by two chains
+// that come to some 6000 cycles each: S -> P -> O1 -> output -> P of the next chunk, and weights ->
+// U -> M -> its copy -> weights of the next.  Code that runs once a chunk in each of 20 warps is
+// fetched cold, so that a wait for what is there already costs 400.  (lo in a's place and the output
+// over M's copy, with two stages of c, linked the chains through O2: 260 us against 235, and the
+// backward pass of 8192 tokens 188 against 176.  Weights a chunk ahead of M, waiting for the
+// output's store a chunk later and prefetches into L2 changed it by -3 to 4 %, each for the worse
+// in most cases.)  Halving what is loaded, or leaving out seven eighths of the products, changed
+// its time by 5 % at most.
 // A block takes all of a head's channels: in two halves, for twice the blocks, S and the reads of a
 // and b came twice, and shared memory (960 KB a chunk, against 670) was the bound, 135 us.
 //
