@@ -475,8 +475,11 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
             if (in_bounds(tile_row0 + quad * 32, 32, rows_q, p.status))
               tma_store_2d(&maps.o, half * HC + col, (int)(tile_row0 + quad * 32), sbase + area);
             bulk_commit_group();
-            bulk_wait_read_all();
           }
+          __syncwarp();
+        };
+        auto left = [&]() {
+          if (lane == 0) bulk_wait_read_all();
           __syncwarp();
         };
 #pragma unroll 1
@@ -495,6 +498,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
             v[j] = fma2(ow2, make_float2(__uint_as_float(o2[2 * j]), __uint_as_float(o2[2 * j + 1])),
                         mul2(mul2v, make_float2(__uint_as_float(o1[2 * j]), __uint_as_float(o1[2 * j + 1]))));
           if (w.out_f32) {
+            if (c == 2 && staged) left();  // the first 32 columns
             float4* const dst = reinterpret_cast<float4*>(static_cast<float*>(w.out) + at) + c * 4;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -515,6 +519,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           }
         }
         if (staged && !w.out_f32) leave(0);
+        left();
         if (lane == 0) mbar_arrive(a_empty(sa));
         if (++sa == AS) sa = 0;
       }
