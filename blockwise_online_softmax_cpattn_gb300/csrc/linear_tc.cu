@@ -56,25 +56,26 @@ namespace cpattn {
 namespace lintc {
 
 constexpr int kTile = kLinTcChunk;
-constexpr int kThreadsOut = 640, kThreadsSum = 384;
+constexpr int kThreads = 640;
 // Registers of the second launch's five warpgroups (control, two of the output, two of the state):
 // at most what 640 threads are launched with, 96 each.
 constexpr int kRegsControl = 64, kRegsOut = 80, kRegsState = 128, kRegsLaunch = 96;
-static_assert(128 * (kRegsControl + 2 * kRegsOut + 2 * kRegsState) <= kThreadsOut * kRegsLaunch, "");
+static_assert(128 * (kRegsControl + 2 * kRegsOut + 2 * kRegsState) <= kThreads * kRegsLaunch, "");
 
-template <int D, bool SUM>
+// EXACT: of a SUM, a state is handed out in the end (keys in three parts).
+template <int D, bool SUM, bool EXACT>
 struct Smem {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kAS = SUM ? 0 : D == 128 ? 2 : 3;  // stages of a, of b, of c
-  static constexpr int kBS = SUM ? (D == 128 ? 2 : 4) : kAS;
+  static constexpr int kBS = !SUM ? kAS : EXACT ? (D == 128 ? 2 : 4) : D == 128 ? 3 : 6;
   static constexpr int kCS = !SUM && D == 128 ? 1 : kBS;
-  static constexpr int kXS = SUM ? (D == 128 ? 3 : 5) : 1;  // parts of the weighted b
+  static constexpr int kXS = !SUM ? 1 : !EXACT ? 0 : D == 128 ? 3 : 5;  // smaller parts of the weighted b
   static constexpr int kA = 0;
   static constexpr int kB = kA + kAS * kTileBytes;
   static constexpr int kC = kB + kBS * kTileBytes;
   static constexpr int kX = kC + kCS * kTileBytes;
   // (at D 64 U reads on behind a part's tile, as far as another one)
-  static constexpr int kM = kX + (kXS + (SUM && D == 64)) * kTileBytes;
+  static constexpr int kM = kX + (kXS + (SUM && EXACT && D == 64)) * kTileBytes;
   // the output's staging, 4 KB a warp: at D 128 where a lies, at D 64 that is too small
   static constexpr int kO = kM + (SUM ? 0 : D * D * 2);
   static constexpr int kPow = kO + (SUM || D == 128 ? 0 : 8 * 4096);
@@ -143,10 +144,10 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 
 // PIECES: the chunks of a zigzag order off their grid (layer.cuh).  A kernel of its own, since its
 // divisions cost the other orders 8 % (T 8192, 32 heads of 128: 62 -> 67 us).
-template <int D, bool SUM, bool PIECES>
-__global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
+template <int D, bool SUM, bool EXACT, bool PIECES>
+__global__ void __launch_bounds__(kThreads, 1)
     sweep_kernel(const __grid_constant__ Params prm) {
-  using L = Smem<D, SUM>;
+  using L = Smem<D, SUM, EXACT>;
   constexpr int AS = L::kAS, BS = L::kBS, CS = L::kCS, XS = L::kXS;
   constexpr uint32_t kTmemCols = SUM ? 2 * D : 512;
   const Linear& p = prm.p;
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
   auto u_full = [&](int i) { return one + 8 * (4 + (i & 1)); };
   const uint32_t p_full = one + 48, o_full = one + 56, o_free = one + 64, m_full = one + 72,
                  m_free = one + 80, h_done = one + 88, o2_full = one + 96, fin = one + 120;
+  auto u_free = [&](int i) { return one + 104 + 8 * (i & 1); };  // SUM, in the place of fixed
   auto fixed = [&](int k) { return one + 104 + 8 * (k & 1); };  // partial chunks, a pair
   auto x_empty = [&](int s) { return one + 144 + 8 * s; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
   const float ld = lin_decay(p, bh);
   const int back = w.back, late = back;
   // bf16 numbers of a weighted b: in the sums of the runs one does (2.36e-3 against 2.35e-3)
-  const int parts = w.exact && (SUM || run == p.segs - 1) ? 3 : SUM ? 1 : 2;
+  const int parts = !SUM ? (w.exact && run == p.segs - 1 ? 3 : 2) : EXACT && w.exact ? 3 : 1;
   const int bb = bh / p.Hq, h = bh - bb * p.Hq;
   const int head_a = bb * (p.Hq / w.rep_a) + h / w.rep_a;
   const int head_b = bb * (p.Hq / w.rep_b) + h / w.rep_b;
@@ -228,8 +230,119 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
   const uint32_t tS = tmem, tO1 = tmem + 128, tO2 = tmem + 128 + D;
   auto tU = [&](int i) { return SUM ? tmem + (i & 1) * D : tmem + 128 + 2 * D; };
 
+  // ---- b times its weights, in its parts: two threads a token, half the channels each
+  constexpr int HC = D / 2, DD = D * D;
+  const int quad = warp & 3, row = quad * 32 + lane;  // a token of a chunk (for M: a channel of b)
+  const int col0 = (warp >> 2 & 1) * HC;              // channels of b (columns of M)
+  StageRing<BS> wb;
+  StageRing<CS> wc;
+  int wk = 0, wx = 0, wf = 0;
+  uint32_t xpar = 0;
+  auto weigh = [&](int i) -> bool {
+    const int n = chunk_n(i);
+    // (x_full of the last but one has been seen)
+    if (SUM && i > 1 && !warp_wait(u_full(i), (i >> 1 & 1) ^ 1, abort, p.status, tmo)) return false;
+    if (!warp_wait(b_full(wb.stage), wb.par, abort, p.status, tmo)) return false;
+    uint8_t* const bt = smem + L::kB + wb.stage * L::kTileBytes;
+    // this thread's half of its token's row: HC / 8 chunks of eight channels
+    uint4* const line = reinterpret_cast<uint4*>(bt + (col0 >> 6) * (kTile * 128) + row * 128);
+    const int chunk0 = (col0 & 63) >> 3;
+    if (n < kTile) {
+      // rows behind the last token hold anything: zeros, in b and in c
+      if (!warp_wait(c_full(wc.stage), wc.par, abort, p.status, tmo)) return false;
+      if (row >= n) {
+        uint4* const cline = line + (L::kC - L::kB + (wc.stage - wb.stage) * L::kTileBytes) / 16;
+#pragma unroll
+        for (int j = 0; j < HC / 8; ++j) line[chunk0 + j] = cline[chunk0 + j] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      if (!SUM) mbar_arrive(fixed(wf++));
+    }
+    // S has read b
+    if (!SUM && !warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo)) return false;
+    const float uw = row < n ? pw[(back ? row : n - 1 - row) + late] : 0.f;
+    const float2 uw2 = make_float2(uw, uw);
+    // the parts of eight channels
+    auto split = [&](uint4 x, uint4& hi, uint4& mid, uint4& lo, bool three) {
+      const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+      uint32_t h[4], m[4], l[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float2 v = mul2(make_float2(bf16_lo(in[q]), bf16_hi(in[q])), uw2);
+        h[q] = pack_bf16(v.x, v.y);
+        v = fma2(make_float2(bf16_lo(h[q]), bf16_hi(h[q])), make_float2(-1.f, -1.f), v);
+        m[q] = pack_bf16(v.x, v.y);
+        if (three) l[q] = pack_bf16(v.x - bf16_lo(m[q]), v.y - bf16_hi(m[q]));
+      }
+      hi = make_uint4(h[0], h[1], h[2], h[3]);
+      mid = make_uint4(m[0], m[1], m[2], m[3]);
+      if (three) lo = make_uint4(l[0], l[1], l[2], l[3]);
+    };
+    // a place for each of the smaller parts, two numbers ahead of the product; or (!SUM) for the smallest
+    // alone, which U of the last chunk has read
+    uint4* const xline = line + (L::kX - L::kB - wb.stage * L::kTileBytes) / 16;
+    if (SUM && parts == 1) {
+#pragma unroll 4
+      for (int j = 0; j < HC / 8; ++j) {
+        const int at = (chunk0 + j) ^ (row & 7);
+        const uint4 x = line[at];
+        auto times = [&](uint32_t v) {
+          const float2 y = mul2(make_float2(bf16_lo(v), bf16_hi(v)), uw2);
+          return pack_bf16(y.x, y.y);
+        };
+        line[at] = make_uint4(times(x.x), times(x.y), times(x.z), times(x.w));
+      }
+    } else if (SUM) {
+      const int x0 = wx, x1 = wx + 1 == XS ? 0 : wx + 1;
+      const uint32_t par0 = xpar, par1 = x1 == 0 ? xpar ^ 1u : xpar;
+      if (!warp_wait(x_empty(x0), par0 ^ 1u, abort, p.status, tmo) ||
+          !warp_wait(x_empty(x1), par1 ^ 1u, abort, p.status, tmo))
+        return false;
+      uint4* const l0 = xline + x0 * (L::kTileBytes / 16);
+      uint4* const l1 = xline + x1 * (L::kTileBytes / 16);
+#pragma unroll 2
+      for (int j = 0; j < HC / 8; ++j) {
+        const int at = (chunk0 + j) ^ (row & 7);
+        uint4 hi;
+        split(line[at], hi, l1[at], l0[at], true);
+        line[at] = hi;
+      }
+      wx = x1 + 1 == XS ? 0 : x1 + 1;
+      xpar = wx <= x0 ? xpar ^ 1u : xpar;
+    } else if (parts == 2) {
+#pragma unroll 2
+      for (int j = 0; j < HC / 8; ++j) {
+        const int at = (chunk0 + j) ^ (row & 7);
+        uint4 hi, mid, lo;
+        split(line[at], hi, mid, lo, false);
+        line[at] = hi;
+        xline[at] = mid;
+      }
+    } else {
+      uint4 hi[HC / 8];
+#pragma unroll
+      for (int j = 0; j < HC / 8; ++j) {
+        const int at = (chunk0 + j) ^ (row & 7);
+        uint4 mid, lo;
+        split(line[at], hi[j], mid, lo, true);
+        line[at] = mid;
+        xline[at] = lo;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(x_full(wk++));
+      if (!warp_wait(h_done, i & 1, abort, p.status, tmo)) return false;
+#pragma unroll
+      for (int j = 0; j < HC / 8; ++j) line[(chunk0 + j) ^ (row & 7)] = hi[j];
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(x_full(wk++));
+    wb.advance();
+    wc.advance();
+    return true;
+  };
+
   if (warp < 4) {
-    if constexpr (!SUM) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
@@ -373,28 +486,29 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
           for (int kk = 0; kk < kTile / 16; ++kk)
             if (leader) mma_ss(tU(i), pd + (uint64_t)(kk * 128), cd0 + stc + (uint64_t)(kk * 128), kId, !first || kk > 0);
         };
+        // U's place has been read
+        if (SUM && i > 1 && !(ok = warp_wait(u_free(i), (i >> 1 & 1) ^ 1, abort, p.status, tmo))) break;
         if (!(ok = warp_wait(x_full(k), (k >> 1) & 1, abort, p.status, tmo))) break;
         ++k;
         tc_fence_after();
-        if constexpr (SUM) {
-          for (int part = 0; part + 1 < parts; ++part) {
+        if (!SUM) {
+          product(xd0, true);
+        } else if (parts == 3) {
+          for (int part = 0; part < 2; ++part) {
             product(xd0 + x * (L::kTileBytes >> 4), part == 0);
             if (leader) mma_commit(x_empty(x));
             __syncwarp();
             if (++x == XS) x = 0;
           }
-          product(bd0 + st, parts == 1);
-        } else {
-          product(xd0, true);
+        }
+        product(bd0 + st, parts == 1);
+        if (!SUM && parts == 3) {
+          if (leader) mma_commit(h_done);
+          __syncwarp();
+          if (!(ok = warp_wait(x_full(k), (k >> 1) & 1, abort, p.status, tmo))) break;
+          ++k;
+          tc_fence_after();
           product(bd0 + st, false);
-          if (parts == 3) {
-            if (leader) mma_commit(h_done);
-            __syncwarp();
-            if (!(ok = warp_wait(x_full(k), (k >> 1) & 1, abort, p.status, tmo))) break;
-            ++k;
-            tc_fence_after();
-            product(bd0 + st, false);
-          }
         }
         if (leader) {
           mma_commit(u_full(i));
@@ -409,13 +523,15 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       __syncwarp();
       drain_wait(fin + 16, 0);
     }
-  } else if (!SUM && warp < 12) {
-    if constexpr (!SUM) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+    if constexpr (SUM) {
+      for (int i = 0; i < n_chunks; ++i)
+        if (!weigh(i)) break;
+    } else {
       // ------------------------------------------------ P and the epilogue
-      const int quad = warp & 3, row = quad * 32 + lane, half = warp >> 2 & 1;
+      const int half = warp >> 2 & 1;
       const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-      constexpr int HC = D / 2;
       int sa = 0;  // stage of a
       for (int i = 0; i < n_chunks; ++i) {
         const int pos0 = chunk_pos(i), n = chunk_n(i);
@@ -526,11 +642,8 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
       if (lane == 0) bulk_wait_all();
     }
   } else {
-    if constexpr (!SUM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
     // -------------------------------------------------------- the state
-    constexpr int HC = D / 2, DD = D * D;
-    const int quad = warp & 3, row = quad * 32 + lane;  // a channel of b, and a token of a chunk
-    const int col0 = (warp >> 2 & 1) * HC;              // of this thread: columns of M, channels of b
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const bool mine = D == 128 || row < D;
     float M[HC];
@@ -601,122 +714,21 @@ __global__ void __launch_bounds__(SUM ? kThreadsSum : kThreadsOut, 1)
         }
       }
       tc_fence_before();
+      if (SUM) mbar_arrive(u_free(i));
       return true;
     };
     if (!SUM && n_chunks > 0) publish();
-    StageRing<BS> rb;
-    StageRing<CS> rc;
     bool ok = true;
-    int k = 0, x = 0, nf = 0;
-    uint32_t xpar = 0;
     for (int i = 0; i < n_chunks && ok; ++i) {
-      const int n = chunk_n(i);
-      if (!(ok = warp_wait(b_full(rb.stage), rb.par, abort, p.status, tmo))) break;
-      uint8_t* const bt = smem + L::kB + rb.stage * L::kTileBytes;
-      // this thread's half of its token's row: HC / 8 chunks of eight channels
-      uint4* const line = reinterpret_cast<uint4*>(bt + (col0 >> 6) * (kTile * 128) + row * 128);
-      const int chunk0 = (col0 & 63) >> 3;
-      if (n < kTile) {
-        // rows behind the last token hold anything: zeros, in b and in c
-        if (!(ok = warp_wait(c_full(rc.stage), rc.par, abort, p.status, tmo))) break;
-        if (row >= n) {
-          uint4* const cline = line + (L::kC - L::kB + (rc.stage - rb.stage) * L::kTileBytes) / 16;
-#pragma unroll
-          for (int j = 0; j < HC / 8; ++j) line[chunk0 + j] = cline[chunk0 + j] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-        if (!SUM) mbar_arrive(fixed(nf++));
-      }
-      // S has read b
-      if (!SUM && !(ok = warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo))) break;
-      const float uw = row < n ? pw[(back ? row : n - 1 - row) + late] : 0.f;
-      const float2 uw2 = make_float2(uw, uw);
-      // the parts of eight channels
-      auto split = [&](uint4 x, uint4& hi, uint4& mid, uint4& lo, bool three) {
-        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-        uint32_t h[4], m[4], l[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float2 v = mul2(make_float2(bf16_lo(in[q]), bf16_hi(in[q])), uw2);
-          h[q] = pack_bf16(v.x, v.y);
-          v = fma2(make_float2(bf16_lo(h[q]), bf16_hi(h[q])), make_float2(-1.f, -1.f), v);
-          m[q] = pack_bf16(v.x, v.y);
-          if (three) l[q] = pack_bf16(v.x - bf16_lo(m[q]), v.y - bf16_hi(m[q]));
-        }
-        hi = make_uint4(h[0], h[1], h[2], h[3]);
-        mid = make_uint4(m[0], m[1], m[2], m[3]);
-        if (three) lo = make_uint4(l[0], l[1], l[2], l[3]);
-      };
-      if constexpr (SUM) {
-        int x0 = x, x1 = x + 1 == XS ? 0 : x + 1;
-        const uint32_t par0 = xpar, par1 = x1 == 0 ? xpar ^ 1u : xpar;
-        if (!(ok = (parts == 1 || warp_wait(x_empty(x0), par0 ^ 1u, abort, p.status, tmo)) &&
-                   (parts < 3 || warp_wait(x_empty(x1), par1 ^ 1u, abort, p.status, tmo))))
-          break;
-        // smallest first: two parts, mid in x0; three, lo in x0 and mid in x1
-        uint4* const l0 = line + (L::kX - L::kB + (x0 - rb.stage) * L::kTileBytes) / 16;
-        uint4* const l1 = line + (L::kX - L::kB + (x1 - rb.stage) * L::kTileBytes) / 16;
-#pragma unroll 4
-        for (int j = 0; j < HC / 8; ++j) {
-          const int at = (chunk0 + j) ^ (row & 7);
-          uint4 hi, mid, lo;
-          split(line[at], hi, mid, lo, parts == 3);
-          line[at] = hi;
-          if (parts == 3) {
-            l0[at] = lo;
-            l1[at] = mid;
-          } else if (parts == 2) {
-            l0[at] = mid;
-          }
-        }
-        for (int q = 1; q < parts; ++q)
-          if (++x == XS) x = 0, xpar ^= 1u;
-        fence_proxy_async_smem();
-        mbar_arrive(x_full(k++));
-        if (i > 0 && !(ok = take(i - 1))) break;  // while this chunk's product runs
-      } else {
-        // the smallest part has a place of its own: U of the last chunk has read it
-        uint4* const xline = line + (L::kX - L::kB - rb.stage * L::kTileBytes) / 16;
-        if (parts < 3) {
-#pragma unroll 2
-          for (int j = 0; j < HC / 8; ++j) {
-            const int at = (chunk0 + j) ^ (row & 7);
-            uint4 hi, mid, lo;
-            split(line[at], hi, mid, lo, false);
-            line[at] = hi;
-            xline[at] = mid;
-          }
-        } else {
-          uint4 hi[HC / 8];
-#pragma unroll
-          for (int j = 0; j < HC / 8; ++j) {
-            const int at = (chunk0 + j) ^ (row & 7);
-            uint4 mid, lo;
-            split(line[at], hi[j], mid, lo, true);
-            line[at] = mid;
-            xline[at] = lo;
-          }
-          fence_proxy_async_smem();
-          mbar_arrive(x_full(k++));
-          if (!(ok = warp_wait(h_done, i & 1, abort, p.status, tmo))) break;
-#pragma unroll
-          for (int j = 0; j < HC / 8; ++j) line[(chunk0 + j) ^ (row & 7)] = hi[j];
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(x_full(k++));
-      }
-      rb.advance();
-      rc.advance();
-      if constexpr (!SUM) {
-        if (!(ok = take(i))) break;
-        if (i + 1 < n_chunks) {
-          // O2 of this chunk has read the old copy
-          if (!(ok = warp_wait(m_free, i & 1, abort, p.status, tmo))) break;
-          publish();
-        }
+      if constexpr (!SUM)
+        if (!(ok = weigh(i))) break;
+      if (!(ok = take(i))) break;
+      if (!SUM && i + 1 < n_chunks) {
+        // O2 of this chunk has read the old copy
+        if (!(ok = warp_wait(m_free, i & 1, abort, p.status, tmo))) break;
+        publish();
       }
     }
-    if (SUM && ok && n_chunks > 0) ok = take(n_chunks - 1);
     if (ok && mine) {
       if constexpr (SUM) {
         // columns first: the threads of a warp write, and in most sweeps read, consecutive numbers
@@ -745,7 +757,7 @@ static bool make_map(CUtensorMap* m, const void* t, int64_t heads, int T, int D)
   return encode_tmap_2d_bf16(m, t, D, (uint64_t)heads * T, 64, kTile) == CUDA_SUCCESS;
 }
 
-template <int D, bool SUM, bool PIECES>
+template <int D, bool SUM, bool EXACT, bool PIECES>
 static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, bool dependent, cudaStream_t st) {
   Params prm;
   prm.p = p;
@@ -766,15 +778,13 @@ static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, bool depe
                      : encode_tmap_2d_bf16(&prm.maps[i].o, w.out, D, rows, D / 2, 32)) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     }
-  constexpr int kSmem = Smem<D, SUM>::kBytes, kThreads = SUM ? kThreadsSum : kThreadsOut;
-  auto kern = sweep_kernel<D, SUM, PIECES>;
+  constexpr int kSmem = Smem<D, SUM, EXACT>::kBytes;
+  auto kern = sweep_kernel<D, SUM, EXACT, PIECES>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  if (!SUM) {  // a split that does not fit what the launch allocates would wait forever
-    cudaFuncAttributes at;
-    if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
-    if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
-  }
+  cudaFuncAttributes at;  // a split that does not fit what the launch allocates would wait forever
+  if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
+  if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
   const unsigned blocks = (unsigned)(p.B * p.Hq * (SUM ? p.segs - 1 : p.segs));
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -801,25 +811,26 @@ bool linear_tc_supported(const Ring& R) {
   return (double)R.B * R.Hq * R.T < 2147483647.0 - kLinTcChunk;
 }
 
-template <bool SUM>
+template <bool SUM, bool EXACT>
 static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, bool dependent, cudaStream_t st) {
   if (p.seg < p.T)
-    return p.D == 128 ? lintc::run<128, SUM, true>(p, n, sweeps, dependent, st)
-                      : lintc::run<64, SUM, true>(p, n, sweeps, dependent, st);
-  return p.D == 128 ? lintc::run<128, SUM, false>(p, n, sweeps, dependent, st)
-                    : lintc::run<64, SUM, false>(p, n, sweeps, dependent, st);
+    return p.D == 128 ? lintc::run<128, SUM, EXACT, true>(p, n, sweeps, dependent, st)
+                      : lintc::run<64, SUM, EXACT, true>(p, n, sweeps, dependent, st);
+  return p.D == 128 ? lintc::run<128, SUM, EXACT, false>(p, n, sweeps, dependent, st)
+                    : lintc::run<64, SUM, EXACT, false>(p, n, sweeps, dependent, st);
 }
 
 cudaError_t launch_linear_tc(const Linear& p, cudaStream_t st, bool backward) {
   cudaError_t e;
   if (p.segs > 1) {
     timing_begin(backward ? "linear_bwd_sums" : "linear_fwd_sums", st);
-    e = run<true>(p, p.n_sums, p.sum, false, st);
+    e = p.sum[0].exact || p.sum[1].exact ? run<true, true>(p, p.n_sums, p.sum, false, st)
+                                         : run<true, false>(p, p.n_sums, p.sum, false, st);
     timing_end(st);
     if (e != cudaSuccess) return e;
   }
   timing_begin(backward ? "linear_bwd" : "linear_fwd", st);
-  e = run<false>(p, p.n_sweeps, p.sweep, p.segs > 1, st);
+  e = run<false, false>(p, p.n_sweeps, p.sweep, p.segs > 1, st);
   timing_end(st);
   return e;
 }
