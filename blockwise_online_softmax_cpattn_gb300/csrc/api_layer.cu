@@ -118,10 +118,10 @@ static cpattn_status validate_linear(const cpattn_desc* d, Ring* R) {
 // Runs a sequence is cut into, for `sweeps` sweeps and `sums` sums of its heads.  One run needs
 // no sums; more fill the GPU when heads are few, but every run but the last reads its keys and
 // values twice and starts from its predecessors' states.  In units of a chunk's time on one SM
-// (on the tensor cores some 3 us, in float32 some 20): a chunk of a sweep 1, of a sum 0.6, a
-// block's start 1 (0.15), folding a predecessor's state 0.25 (0.1), the second launch 1 (0.5).  On
-// 18 problems of 8 to 128 heads and 300 to 32768 tokens the cut's time was within 9 % of the
-// best's, in all but two within 3 %.
+// (on the tensor cores some 3 us, in float32 some 20): a chunk of a sweep 1, of a sum 0.3 (0.6), a
+// block's start 1 (0.15), folding a predecessor's state 0.25 (0.1), the second launch 2 (0.5).  Of
+// 24 problems of 8 to 128 heads and 300 to 32768 tokens, backward passes among them, every cut's
+// time was within 4.5 % of the best one's, all but three within 2 %.
 static void cut_runs(const Ring& R, bool tc, int sweeps, int sums, Linear* p) {
   const int C = tc ? kLinTcChunk : kLinSimtChunk;
   // (off the tensor cores a chunk's slots are looked up one by one)
@@ -129,13 +129,14 @@ static void cut_runs(const Ring& R, bool tc, int sweeps, int sums, Linear* p) {
   p->seg = tc && half % C ? half : R.T;
   p->per = (p->seg + C - 1) / C;
   p->nch = p->per * (R.T / p->seg);
-  const double heads = (double)R.B * R.Hq, start = tc ? 1 : 0.15, fold = tc ? 0.25 : 0.1, launch = tc ? 1 : 0.5;
+  const double sum = tc ? 0.3 : 0.6, start = tc ? 1 : 0.15, fold = tc ? 0.25 : 0.1, launch = tc ? 2 : 0.5;
+  const double heads = (double)R.B * R.Hq;
   double best = 0;
   for (int segs = 1; segs <= 64 && segs <= p->nch; ++segs) {
     const int cps = (p->nch + segs - 1) / segs;
     if ((p->nch + cps - 1) / cps != segs) continue;  // the same cut as a smaller number of runs
     double t = ceil(heads * sweeps * segs / kSms) * (cps + start + fold * (segs - 1) / 2);
-    if (segs > 1) t += ceil(heads * sums * (segs - 1) / kSms) * (0.6 * cps + start) + launch;
+    if (segs > 1) t += ceil(heads * sums * (segs - 1) / kSms) * (sum * cps + start) + launch;
     if (segs == 1 || t < best) {
       best = t;
       p->segs = segs;

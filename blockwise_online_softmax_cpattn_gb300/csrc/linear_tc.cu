@@ -31,11 +31,13 @@
 // Issuers are whole warps with one elected lane, as in tc_fwd.cu.  TMEM: S/P [0, 128),
 // O1, O2 and U of D columns each behind it.
 //
-// The first launch (SUM) only needs U and M: no a, 384 threads; M takes a chunk's U while the next
-// one's product runs.
+// The first launch (SUM) only needs U and M: no a; warps 4-11 weigh b, ahead of warps 12-19, and U has
+// two places.  b in one part is weighted in place, with three stages of b and c (with two a chunk took
+// the 2500 cycles of a load, the weights and the product: 35 us against 30, below); three parts leave
+// room for two stages.
 //
-// Measured (GB300, D 128, 8192 tokens of 32 heads: 128 runs of 16 chunks): the sums 35 us, 5.2 TB/s
-// of memory reads; the sweep 62 us, 6000 cycles a chunk where 128 KB from and to memory would take
+// Measured (GB300, D 128, 8192 tokens of 32 heads: 128 runs of 16 chunks): the sums 30 us, 3.4 TB/s
+// on 96 SMs; the sweep 62 us, 6000 cycles a chunk where 128 KB from and to memory would take
 // 4700 and the products 3100; 131072 tokens of 8 heads 235 us (152 runs).  It is bound by two chains
 // that come to some 6000 cycles each: S -> P -> O1 -> output -> P of the next chunk, and weights ->
 // U -> M -> its copy -> weights of the next.  Code that runs once a chunk in each of 20 warps is
