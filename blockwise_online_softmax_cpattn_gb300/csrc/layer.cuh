@@ -2,6 +2,8 @@
 // linear attention (linear_tc.cu, linear_simt.cu, linear_step.cu); validation in api_layer.cu.
 #pragma once
 
+#include <atomic>
+
 #include "kernels.h"
 
 namespace cpattn {
@@ -9,6 +11,22 @@ namespace cpattn {
 // SMs of a GB300: what work is cut for.  Workspaces depend on the cut, so it is a constant and
 // not a question to the device.
 constexpr int kSms = 152;
+
+// What a kernel needs set before its first launch on a device: a call on every launch costs the host
+// a microsecond.
+struct ReadyDevices {
+  std::atomic<uint64_t> set[2] = {};
+  template <typename F>
+  cudaError_t once(F prepare) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 128 && (set[dev >> 6].load() & bit)) return cudaSuccess;
+    if ((e = prepare()) == cudaSuccess && dev < 128) set[dev >> 6].fetch_or(bit);
+    return e;
+  }
+};
 
 // ---- rotate.cu ---------------------------------------------------------------
 // A [B][H][T][D] tensor by strides in elements; channels are contiguous.

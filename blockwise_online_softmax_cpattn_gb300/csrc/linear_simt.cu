@@ -316,11 +316,14 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
 template <typename E, int DP>
 static cudaError_t launch(const Linear& p, cudaStream_t st, const char* sums, const char* sweeps) {
   constexpr int kBytes = Smem<DP>::kFloats * 4;
-  cudaError_t e = cudaFuncSetAttribute(sweep_kernel<E, DP, true>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(sweep_kernel<E, DP, false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  static ReadyDevices ready;
+  cudaError_t e = ready.once([] {
+    const cudaError_t r = cudaFuncSetAttribute(sweep_kernel<E, DP, true>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    return r != cudaSuccess ? r
+                            : cudaFuncSetAttribute(sweep_kernel<E, DP, false>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  });
   if (e != cudaSuccess) return e;
   const unsigned bh = (unsigned)(p.B * p.Hq);
   if (p.segs > 1) {

@@ -26,7 +26,7 @@
 //   warp 1        issues S;  warp 2: O1;  warp 3: O2 and U
 //   warps 4-11    the output, two threads a row: S -> P, then the epilogue, staged where a lies (S
 //                 and O2 have read it) and out by TMA: stored from registers, every instruction
-//                 touches 32 lines, and loads and stores of the other warps wait for that, 15 %
+//                 touches 32 lines, and the other warps' loads and stores wait for that (15 % more)
 //   warps 12-19   the state, two threads a row: b times its weights, M, its bf16 copy
 // Issuers are whole warps with one elected lane, as in tc_fwd.cu.  TMEM: S/P [0, 128),
 // O1, O2 and U of D columns each behind it.
@@ -59,8 +59,8 @@ namespace lintc {
 
 constexpr int kTile = kLinTcChunk;
 constexpr int kThreads = 640;
-// Registers of the second launch's five warpgroups (control, two of the output, two of the state):
-// at most what 640 threads are launched with, 96 each.
+// Registers of the five warpgroups (control, two of the output or the weights, two of the state): at
+// most what 640 threads are launched with, 96 each.
 constexpr int kRegsControl = 64, kRegsOut = 80, kRegsState = 128, kRegsLaunch = 96;
 static_assert(128 * (kRegsControl + 2 * kRegsOut + 2 * kRegsState) <= kThreads * kRegsLaunch, "");
 
@@ -782,11 +782,15 @@ static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, bool depe
     }
   constexpr int kSmem = Smem<D, SUM, EXACT>::kBytes;
   auto kern = sweep_kernel<D, SUM, EXACT, PIECES>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static ReadyDevices ready;
+  const cudaError_t e = ready.once([&] {
+    cudaFuncAttributes at;  // a split that does not fit what the launch allocates would wait forever
+    const cudaError_t r = cudaFuncGetAttributes(&at, kern);
+    if (r != cudaSuccess) return r;
+    if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  });
   if (e != cudaSuccess) return e;
-  cudaFuncAttributes at;  // a split that does not fit what the launch allocates would wait forever
-  if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
-  if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
   const unsigned blocks = (unsigned)(p.B * p.Hq * (SUM ? p.segs - 1 : p.segs));
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -486,21 +486,23 @@ __global__ void __launch_bounds__(1024) sum_kernel(const float* sums, int n, int
   }
 }
 
-template <typename K>
-static cudaError_t launch_kernel(K kern, const Rotate& p, int grid, int bytes, cudaStream_t st) {
-  if (bytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+template <auto KERN>
+static cudaError_t launch_kernel(const Rotate& p, int grid, int bytes, cudaStream_t st) {
+  if (bytes > 48 * 1024) {  // (one size a kernel)
+    static ReadyDevices ready;
+    const cudaError_t e =
+        ready.once([&] { return cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
     if (e != cudaSuccess) return e;
   }
-  kern<<<grid, kThreads, bytes, st>>>(p);
+  KERN<<<grid, kThreads, bytes, st>>>(p);
   return cudaGetLastError();
 }
 template <typename E, bool NEAR, bool NORM, int P>
 static cudaError_t launch_one(const Rotate& p, int grid, bool backward, cudaStream_t st) {
   // (the ring's space, at least 16 KB with the norm, later takes 8 KB of sums)
   constexpr int V = NORM ? 4 : 2, kSums = NORM ? 2 * 2 * P * kThreads * 4 : 0;
-  return backward ? launch_kernel(bwd_kernel<E, NEAR, NORM, P>, p, grid, kWarps * Ring<E, P, V>::kWarpBytes + kSums, st)
-                  : launch_kernel(fwd_kernel<E, NEAR, NORM, P>, p, grid, kWarps * Ring<E, P, 2>::kWarpBytes, st);
+  return backward ? launch_kernel<bwd_kernel<E, NEAR, NORM, P>>(p, grid, kWarps * Ring<E, P, V>::kWarpBytes + kSums, st)
+                  : launch_kernel<fwd_kernel<E, NEAR, NORM, P>>(p, grid, kWarps * Ring<E, P, 2>::kWarpBytes, st);
 }
 template <typename E, bool NEAR>
 static cudaError_t launch_pairs(const Rotate& p, int grid, bool backward, cudaStream_t st) {
