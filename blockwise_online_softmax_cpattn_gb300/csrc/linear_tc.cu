@@ -536,7 +536,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
       int sa = 0;  // stage of a
       for (int i = 0; i < n_chunks; ++i) {
-        const int pos0 = chunk_pos(i), n = chunk_n(i);
         if (!warp_wait(s_full(i), (i >> 1) & 1, abort, p.status, tmo)) break;
         tc_fence_after();
         // 32 columns at a time, two times a half: weights from the table (zero for columns that come
@@ -573,13 +572,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(p_full);
 
-        if (!warp_wait(o_full, i & 1, abort, p.status, tmo) || !warp_wait(o2_full, i & 1, abort, p.status, tmo)) break;
-        tc_fence_after();
+        // (while O1 runs)
+        const int n = chunk_n(i);
         const float ow = pw[(back ? n - 1 - min(row, n - 1) : row) + 1 - late] * w.mul;
         const float2 ow2 = make_float2(ow, ow), mul2v = make_float2(w.mul, w.mul);
-        const int64_t tile_row0 = (int64_t)bh * p.T + p.m.slot(pos0);
+        const int64_t tile_row0 = (int64_t)bh * p.T + p.m.slot(chunk_pos(i));
         const bool store = row < n && in_bounds(tile_row0 + row, 1, rows_q, p.status);
         const int64_t at = (tile_row0 + row) * D + half * HC;
+        if (!warp_wait(o_full, i & 1, abort, p.status, tmo) || !warp_wait(o2_full, i & 1, abort, p.status, tmo)) break;
+        tc_fence_after();
         // whole chunks go by way of shared memory: this warp's 32 lines of 64 bf16 or 32 float32
         // columns (at D 64 of 32 bf16: half lines), swizzled as the tensor map has it
         const bool staged = n == kTile;
@@ -615,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 8; ++j)
             v[j] = fma2(ow2, make_float2(__uint_as_float(o2[2 * j]), __uint_as_float(o2[2 * j + 1])),
                         mul2(mul2v, make_float2(__uint_as_float(o1[2 * j]), __uint_as_float(o1[2 * j + 1]))));
+          if (D == 64 && c == 0 && staged) left();  // the last chunk's
           if (w.out_f32) {
             if (c == 2 && staged) left();  // the first 32 columns
             float4* const dst = reinterpret_cast<float4*>(static_cast<float*>(w.out) + at) + c * 4;
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (staged && !w.out_f32) leave(0);
-        left();
+        if (D == 128) left();  // (before a comes there; at D 64 the store has until the next output)
         if (lane == 0) mbar_arrive(a_empty(sa));
         if (++sa == AS) sa = 0;
       }
