@@ -391,15 +391,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!warp_wait(a_full(ra.stage), ra.par, abort, p.status, tmo) ||
               !warp_wait(b_full(ra.stage), ra.par, abort, p.status, tmo))
             break;
-          // S's place is free once O1 of the last chunk has read P there (and s_full of the last but
-          // one has been seen by everyone)
-          if (i > 0 && !warp_wait(o_full, (i - 1) & 1, abort, p.status, tmo)) break;
+          // (everyone has seen s_full of the last but one; what comes last is waited for last)
           if (i > 1 && !warp_wait(u_full(i), (i >> 1 & 1) ^ 1, abort, p.status, tmo)) break;
           // a partial chunk's rows of b and c behind its end are zeroed first
           if (chunk_n(i) < kTile) {
             if (!warp_wait(fixed(nf), nf >> 1 & 1, abort, p.status, tmo)) break;
             ++nf;
           }
+          // S's place is free once O1 of the last chunk has read P there
+          if (i > 0 && !warp_wait(o_full, (i - 1) & 1, abort, p.status, tmo)) break;
           tc_fence_after();
           const uint32_t st = ra.stage * (L::kTileBytes >> 4);
 #pragma unroll 4
@@ -466,9 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t st = rb.stage * (L::kTileBytes >> 4), stc = rc.stage * (L::kTileBytes >> 4);
         if constexpr (!SUM) {
           // the epilogue of the last chunk has read O2
-          if (!(ok = (i == 0 || warp_wait(o_free, (i - 1) & 1, abort, p.status, tmo)) &&
+          if (!(ok = warp_wait(a_full(rb.stage), rb.par, abort, p.status, tmo) &&
                      warp_wait(m_full, i & 1, abort, p.status, tmo) &&
-                     warp_wait(a_full(rb.stage), rb.par, abort, p.status, tmo)))
+                     (i == 0 || warp_wait(o_free, (i - 1) & 1, abort, p.status, tmo))))
             break;
           tc_fence_after();
 #pragma unroll 4
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t tile_row0 = (int64_t)bh * p.T + p.m.slot(chunk_pos(i));
         const bool store = row < n && in_bounds(tile_row0 + row, 1, rows_q, p.status);
         const int64_t at = (tile_row0 + row) * D + half * HC;
-        if (!warp_wait(o_full, i & 1, abort, p.status, tmo) || !warp_wait(o2_full, i & 1, abort, p.status, tmo)) break;
+        if (!warp_wait(o2_full, i & 1, abort, p.status, tmo) || !warp_wait(o_full, i & 1, abort, p.status, tmo)) break;
         tc_fence_after();
         // whole chunks go by way of shared memory: this warp's 32 lines of 64 bf16 or 32 float32
         // columns (at D 64 of 32 bf16: half lines), swizzled as the tensor map has it
