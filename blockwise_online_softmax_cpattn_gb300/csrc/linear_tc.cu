@@ -43,7 +43,7 @@
 // U -> M -> its copy -> weights of the next.  Code that runs once a chunk in each of 20 warps is
 // fetched cold, so that a wait for what is there already costs 400.  (lo in a's place and the output
 // over M's copy, with two stages of c, linked the chains through O2: 260 us against 235, and the
-// backward pass of 8192 tokens 188 against 176.  Weights a chunk ahead of M, waiting for the
+// backward pass of 8192 tokens 188 against 176, now 166.  Weights a chunk ahead of M, waiting for the
 // output's store a chunk later and prefetches into L2 changed it by -3 to 4 %, each for the worse
 // in most cases.)  Halving what is loaded, or leaving out seven eighths of the products, changed
 // its time by 5 % at most.
@@ -97,8 +97,9 @@ struct Params {
 };
 
 // Every role runs through its code once a chunk, on every sub-partition, and together they overran
-// the instruction cache (40 % of its requests missed): loops stay rolled where registers allow, and
-// a wait is a few instructions, bounded by a number of tries of up to 20 us each (the hardware
+// the instruction cache (40 % of its requests missed, 15 % now): loops stay rolled where registers
+// allow (but those that issue products: one at a time, eight chunks at D 64 took 26 us and not 22),
+// and a wait is a few instructions, bounded by a number of tries of up to 20 us each (the hardware
 // suspends the thread meanwhile) instead of by a clock.
 constexpr uint32_t kTryNs = 20000;
 constexpr uint32_t kTries = 500000;       // 10 s at most, 50 ms if a try takes 100 ns only
@@ -402,12 +403,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i > 0 && !warp_wait(o_full, (i - 1) & 1, abort, p.status, tmo)) break;
           tc_fence_after();
           const uint32_t st = ra.stage * (L::kTileBytes >> 4);
+          if (leader) {
 #pragma unroll 4
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = st + (kk >> 2) * 1024 + (kk & 3) * 2;  // 16 KiB blocks, 32 B steps
-            if (leader) mma_ss(tS, ad0 + off, bd0 + off, kId, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = st + (kk >> 2) * 1024 + (kk & 3) * 2;  // 16 KiB blocks, 32 B steps
+              mma_ss(tS, ad0 + off, bd0 + off, kId, kk > 0);
+            }
+            mma_commit(s_full(i));
           }
-          if (leader) mma_commit(s_full(i));
           __syncwarp();
           ra.advance();
         }
@@ -434,10 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!warp_wait(p_full, i & 1, abort, p.status, tmo)) break;
           tc_fence_after();
           const uint32_t st = rc.stage * (L::kTileBytes >> 4);
-#pragma unroll 4
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            if (leader) mma_ts(tO1, tS + (kk >> 2) * 64 + (kk & 3) * 8, cd0 + st + (uint64_t)(kk * 128), kId, kk > 0);
           if (leader) {
+#pragma unroll 4
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_ts(tO1, tS + (kk >> 2) * 64 + (kk & 3) * 8, cd0 + st + (uint64_t)(kk * 128), kId, kk > 0);
             mma_commit(o_full);
             mma_commit(c_empty(rc.stage));
           }
@@ -471,11 +474,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                      (i == 0 || warp_wait(o_free, (i - 1) & 1, abort, p.status, tmo))))
             break;
           tc_fence_after();
-#pragma unroll 4
-          for (int kk = 0; kk < D / 16; ++kk)
-            if (leader)
-              mma_ss(tO2, ad0 + st + (kk >> 2) * 1024 + (kk & 3) * 2, md + (uint64_t)(kk * 128), kId2, kk > 0);
           if (leader) {
+#pragma unroll 4
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(tO2, ad0 + st + (kk >> 2) * 1024 + (kk & 3) * 2, md + (uint64_t)(kk * 128), kId2, kk > 0);
             mma_commit(m_free);
             mma_commit(o2_full);
           }
@@ -484,9 +486,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = warp_wait(c_full(rc.stage), rc.par, abort, p.status, tmo))) break;
         // a part: b's place, or one of its own
         auto product = [&](uint64_t pd, bool first) {
+          if (leader)
 #pragma unroll 4
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            if (leader) mma_ss(tU(i), pd + (uint64_t)(kk * 128), cd0 + stc + (uint64_t)(kk * 128), kId, !first || kk > 0);
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_ss(tU(i), pd + (uint64_t)(kk * 128), cd0 + stc + (uint64_t)(kk * 128), kId, !first || kk > 0);
         };
         // U's place has been read
         if (SUM && i > 1 && !(ok = warp_wait(u_free(i), (i >> 1 & 1) ^ 1, abort, p.status, tmo))) break;
@@ -494,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++k;
         tc_fence_after();
         if (!SUM) {
-          product(xd0, true);
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) product(part ? bd0 + st : xd0, part == 0);
         } else if (parts == 3) {
           for (int part = 0; part < 2; ++part) {
             product(xd0 + x * (L::kTileBytes >> 4), part == 0);
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (++x == XS) x = 0;
           }
         }
-        product(bd0 + st, parts == 1);
+        if (SUM) product(bd0 + st, parts == 1);
         if (!SUM && parts == 3) {
           if (leader) mma_commit(h_done);
           __syncwarp();
