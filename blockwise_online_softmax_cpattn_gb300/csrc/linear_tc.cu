@@ -97,7 +97,7 @@ struct Params {
 };
 
 // Every role runs through its code once a chunk, on every sub-partition, and together they overran
-// the instruction cache (40 % of its requests missed, 15 % now): loops stay rolled where registers
+// the instruction cache (40 % of its requests missed, 10 % now): loops stay rolled where registers
 // allow (but those that issue products: one at a time, eight chunks at D 64 took 26 us and not 22),
 // and a wait is a few instructions, bounded by a number of tries of up to 20 us each (the hardware
 // suspends the thread meanwhile) instead of by a clock.

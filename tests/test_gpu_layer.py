@@ -707,6 +707,61 @@ def test_another_stream_and_captured_calls():
     assert all(torch.equal(a, b) for a, b in zip(outs[0], refs[1]))
 
 
+def test_two_streams_at_once():
+    """Calls side by side, each with its own workspace: what each gives alone."""
+    cp = cp_mod()
+    cases = [LinearCase(1, 4, 2, 3000, 128, "bf16", seed=1), LinearCase(2, 4, 4, 640, 64, "bf16", 2, "zigzag", seed=2),
+             LinearCase(1, 2, 2, 900, 128, "f32", seed=3)]
+    refs, outs, wss = [], [], []
+    for c in cases:
+        n = max(cp.cpattn_linear_workspace(c.d), cp.cpattn_linear_bwd_workspace(c.d))
+        wss.append(torch.empty(n, dtype=torch.uint8, device=dev()))
+        ref = [torch.empty_like(x) for x in (c.q, c.S0, c.q, c.k, c.v, c.S0)]
+        c.forward(ref[0], ref[1], wss[-1])
+        c.backward(ref[2:], wss[-1])
+        refs.append(ref)
+        outs.append([torch.empty_like(x) for x in ref])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        for c, out, ws, st in zip(cases, outs, wss, streams):
+            c.forward(out[0], out[1], ws, st)
+            c.backward(out[2:], ws, st)
+    torch.cuda.synchronize()
+    cp.check(cp.cpattn_check())
+    for out, ref in zip(outs, refs):
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("f32", 40)])
+def test_linear_on_16_byte_boundaries(dtype, D):
+    """Tensors that begin 16 bytes behind a coarser boundary."""
+    cp = cp_mod()
+    c = LinearCase(1, 2, 1, 700, D, dtype, seed=4)
+    ws = torch.empty(max(cp.cpattn_linear_workspace(c.d), cp.cpattn_linear_bwd_workspace(c.d)), dtype=torch.uint8,
+                     device=dev())
+
+    def off(x):
+        n = 16 // x.element_size()
+        y = torch.empty(x.numel() + n, dtype=x.dtype, device=dev())[n:].view(x.shape)
+        return y.copy_(x)
+
+    def run():
+        out = [off(torch.zeros_like(x)) if shifted else torch.empty_like(x) for x in (c.q, c.S0, c.q, c.k, c.v, c.S0)]
+        c.forward(out[0], out[1], ws)
+        c.backward(out[2:], ws)
+        cp.check(cp.cpattn_check())
+        return out
+
+    shifted = False
+    ref = run()
+    shifted = True
+    c.q, c.k, c.v, c.do, c.S0, c.dS1 = (off(x) for x in (c.q, c.k, c.v, c.do, c.S0, c.dS1))
+    assert c.q.data_ptr() % 32 == 16
+    for a, b in zip(run(), ref):
+        assert torch.equal(a, b)
+
+
 def test_rotation_captured():
     cp = cp_mod()
     rng = np.random.default_rng(3)
