@@ -817,8 +817,9 @@ bool linear_tc_supported(const Ring& R) {
   if (!R.bf16 || (R.D != 64 && R.D != 128)) return false;
   // A chunk's positions are consecutive slots, so a zigzag half of h tokens takes h / 128 chunks,
   // rounded up, and a chunk costs the same whatever it holds.  Halves of 16 against float32
-  // arithmetic at 15: 4 heads of 128 (T 128, 120) 24 against 53 us, of 64 16 against 26; 32 heads
-  // (T 1024, 960) of 128 160 against 156, of 64 102 against 75; at 64 tokens 142, where float32 would take some 650 (in proportion to 15).
+  // arithmetic at 15: 4 heads of 128 (T 128, 120) 25 against 54 us, of 64 16 against 27; 32 heads
+  // (T 1024, 960) of 128 151 against 159, of 64 95 against 76; at 64 tokens 130, where float32 would
+  // take some 650 (in proportion to 15).
   if (R.zz && R.T / R.cp / 2 < 16) return false;
   return (double)R.B * R.Hq * R.T < 2147483647.0 - kLinTcChunk;
 }
