@@ -250,13 +250,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this thread's half of its token's row: HC / 8 chunks of eight channels
     uint4* const line = reinterpret_cast<uint4*>(bt + (col0 >> 6) * (kTile * 128) + row * 128);
     const int chunk0 = (col0 & 63) >> 3;
+    // Where they lie.  At D 64 the row's other thread has the line's other half, and nothing orders
+    // the two in the sums: each clears, reads and writes its own pieces alone.
+    auto piece = [&](int j) { return (chunk0 + j) ^ (row & 7); };
     if (n < kTile) {
       // rows behind the last token hold anything: zeros, in b and in c
       if (!warp_wait(c_full(wc.stage), wc.par, abort, p.status, tmo)) return false;
       if (row >= n) {
         uint4* const cline = line + (L::kC - L::kB + (wc.stage - wb.stage) * L::kTileBytes) / 16;
 #pragma unroll
-        for (int j = 0; j < HC / 8; ++j) line[chunk0 + j] = cline[chunk0 + j] = make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < HC / 8; ++j) line[piece(j)] = cline[piece(j)] = make_uint4(0u, 0u, 0u, 0u);
       }
       fence_proxy_async_smem();
       if (!SUM) mbar_arrive(fixed(wf++));
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (SUM && parts == 1) {
 #pragma unroll 4
       for (int j = 0; j < HC / 8; ++j) {
-        const int at = (chunk0 + j) ^ (row & 7);
+        const int at = piece(j);
         const uint4 x = line[at];
         auto times = [&](uint32_t v) {
           const float2 y = mul2(make_float2(bf16_lo(v), bf16_hi(v)), uw2);
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint4* const l1 = xline + x1 * (L::kTileBytes / 16);
 #pragma unroll 2
       for (int j = 0; j < HC / 8; ++j) {
-        const int at = (chunk0 + j) ^ (row & 7);
+        const int at = piece(j);
         uint4 hi;
         split(line[at], hi, l1[at], l0[at], true);
         line[at] = hi;
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (parts == 2) {
 #pragma unroll 2
       for (int j = 0; j < HC / 8; ++j) {
-        const int at = (chunk0 + j) ^ (row & 7);
+        const int at = piece(j);
         uint4 hi, mid, lo;
         split(line[at], hi, mid, lo, false);
         line[at] = hi;
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint4 hi[HC / 8];
 #pragma unroll
       for (int j = 0; j < HC / 8; ++j) {
-        const int at = (chunk0 + j) ^ (row & 7);
+        const int at = piece(j);
         uint4 mid, lo;
         split(line[at], hi[j], mid, lo, true);
         line[at] = mid;
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(x_full(wk++));
       if (!warp_wait(h_done, i & 1, abort, p.status, tmo)) return false;
 #pragma unroll
-      for (int j = 0; j < HC / 8; ++j) line[(chunk0 + j) ^ (row & 7)] = hi[j];
+      for (int j = 0; j < HC / 8; ++j) line[piece(j)] = hi[j];
     }
     fence_proxy_async_smem();
     mbar_arrive(x_full(wk++));
