@@ -18,7 +18,7 @@
 // 70 to 90 KB an SM, more than what 7 TB/s at a microsecond's latency takes, and no registers.
 // The angle p f is formed in whole numbers, as 64 binary places of a turn: at position 10^5 a
 // float32 product alone is off by 2^-8 of a radian, and the float64 units, two lanes an SM, took
-// 2 us of a decoding step's 6.6.
+// 2 us of a decoding step's 6.6.  Only what is left by whole quarter turns becomes a float32.
 //
 // Bound by memory: 64 bytes a lane and row against some 130 instructions.  32768 tokens of 40 heads
 // of 128 (bf16): 107 us, 6.3 TB/s, 92 % of a copy's rate.  Backward, 8192 tokens of 48 heads: 56 us,
@@ -140,6 +140,20 @@ __device__ __forceinline__ uint64_t turns_of(double f) {
   return bits >> 63 ? 0 - g : g;
 }
 
+// Sine and cosine of `at` 2^-64 turns.  The nearest quarter turn is taken off in whole numbers: the
+// rest, an eighth at most, is rounded to a float32 off by less than 2^-25 radians (a float32 over a
+// half turn: 2^-23.3).
+__device__ __forceinline__ void sin_cos(uint64_t at, float* si, float* co) {
+  const uint64_t up = at + (1ull << 61);
+  const uint32_t q = (uint32_t)(up >> 62);
+  const int64_t rest = (int64_t)(at - ((uint64_t)q << 62));
+  float s, c;
+  sincospif((float)(int32_t)(rest >> 30) * 1.16415321826934814453125e-10f, &s, &c);  // 2^-33
+  const float x = q & 1 ? s : c, y = q & 1 ? c : s;
+  *co = __uint_as_float(__float_as_uint(x) ^ ((q + 1) & 2) << 30);
+  *si = __uint_as_float(__float_as_uint(y) ^ (q & 2) << 30);
+}
+
 // What a lane keeps for its slot: the two tokens (attention's and projection's side) and the turns.
 template <int P>
 struct Slot {
@@ -166,7 +180,7 @@ __device__ __forceinline__ Slot<P> make_slot(const Rotate& p, int group, int sub
     s.si[i] = 0.f;
     if (turned) {
       const uint64_t at = (uint64_t)(int64_t)pos * turns_of(p.inv_freq[j0 + i]);
-      sincospif((float)(int32_t)(at >> 32) * 4.656612873077392578125e-10f, &s.si[i], &s.co[i]);  // 2^-31
+      sin_cos(at, &s.si[i], &s.co[i]);
       s.si[i] *= dir;
     }
   }

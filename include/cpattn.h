@@ -559,8 +559,9 @@ cpattn_status cpattn_cache_attn(const cpattn_cache_desc* desc, int n_req, int ma
  *     y = u with its first `rot` channels turned: the pair (u_a, u_b) of index i becomes
  *         (u_a cos t - u_b sin t, u_a sin t + u_b cos t),   t = p * inv_freq[i]
  * where pair i is channels (i, i + rot / 2) or (2 i, 2 i + 1).  Rows of values are moved
- * as they are.  Norms and sums run in float32, angles in 64-bit fixed point
- * (t is off by less than 2^-30 for |inv_freq| < 2), one rounding at the end.
+ * as they are.  Norms and sums run in float32, one rounding at the end.  Angles are formed in
+ * 64-bit fixed point (off by less than 2^-30 for |inv_freq| < 2), and what is left of one by whole
+ * quarter turns is a float32: t is off by less than 2^-25.
  *
  * Tensors are [B][H][T][D] by any strides: `strides` is a HOST array of three numbers, the
  * elements from one batch row, one head and one token to the next (multiples of 16 bytes;

@@ -48,3 +48,47 @@ def test_padding_never_shows(D, state):
         assert torch.equal(o, ref)
         if state:
             assert torch.equal(S, S0)
+
+
+# ---------------------------------------------------------------------------
+# angles
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("pairing", ["halves", "neighbours"])
+def test_angles_and_their_turns(pairing):
+    """Cosines and sines themselves, forward and backward: rows whose pairs are (1, 0) and (0, 1).
+
+    The angle is off by less than 2^-25 and sincospif by a unit in the last place (2^-23 of the
+    value); the products with 1 and 0 are exact.  The oracle's own angle in float64, below 2^18, is off
+    by 2^-35.  Angles near every quarter turn are among them, where one of the two is small."""
+    cp = cp_mod()
+    T, D, half = 1024, 64, 32
+    rng = np.random.default_rng(2)
+    near = np.concatenate([2 ** -np.arange(0.0, 16.0), 1.9999999 * rng.random(half - 16)])
+    f = np.where(near > 0, near, 1.0)
+    # the first positions: those whose angle at f = 1 is nearest to a quarter turn's multiple
+    p = np.arange(1, 131072)
+    off = np.abs(p / (np.pi / 2) - np.round(p / (np.pi / 2)))
+    pos = np.concatenate([p[np.argsort(off)[:T // 2]], rng.integers(-131072, 131072, T - T // 2 - 2), [0, -1]])
+    first = np.zeros(D)
+    first[:half if pairing == "halves" else D:1 if pairing == "halves" else 2] = 1
+    x = torch.from_numpy(np.stack([first, 1 - first])).float().to(dev())[None, :, None].expand(1, 2, T, D)
+    d = cp.make_rotate_desc(1, 2, 1, T, D, dtype="f32", pairing=pairing, norm=0)
+    q, k = x.contiguous(), x[:, :1].contiguous()
+    inv_freq, p_dev = torch.from_numpy(f).to(dev()), torch.from_numpy(pos.astype(np.int32))[None].to(dev())
+    t = pos[:, None] * f
+    c, s = np.cos(t), np.sin(t)
+
+    def compare(got, s):
+        got = got.double().cpu().numpy()[0]
+        a, b = (slice(0, half), slice(half, D)) if pairing == "halves" else (slice(0, D, 2), slice(1, D, 2))
+        for have, want, slope in ((got[0][:, a], c, s), (got[0][:, b], s, c), (got[1][:, a], -s, c), (got[1][:, b], c, s)):
+            err = np.abs(have - want)
+            bound = 2.0 ** -25 * np.abs(slope) + 2.0 ** -23 * np.abs(want) + 2.0 ** -34
+            assert (err <= bound).all(), (err / bound).max()
+
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    checked(cp, cp.cpattn_rotate_fwd(d, q, k, None, None, None, inv_freq, p_dev, qo, ko, None))
+    compare(qo, s)
+    ws = torch.empty(cp.cpattn_rotate_bwd_workspace(d), dtype=torch.uint8, device=dev())
+    checked(cp, cp.cpattn_rotate_bwd(d, None, None, None, None, inv_freq, p_dev, q, k, None, qo, ko, None, None, None, ws))
+    compare(qo, -s)
