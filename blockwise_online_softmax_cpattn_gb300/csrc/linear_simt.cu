@@ -3,7 +3,7 @@
 // than 16 tokens).  The sweep, its runs and its direction are described in layer.cuh.
 //
 // A block takes one run of one sweep and head in chunks of 64 tokens: scores a b^T weighted by
-// the decay into shared memory, then out = P c + r^.. (a M), then M = r^n M + b^T c, all as
+// the decay into shared memory, then out = P c + r^.. (a M), then U = b^T c and M = r^n M + U, all as
 // register tiles over shared memory.  M lives in registers (8 x 8 a thread at D 128) with a copy
 // in shared memory as the operand of a M.  Head dimensions in between are padded with zeros to
 // 64 or 128.  Bound by the float32 units, 4 D (D + 32) FLOP a token and head, and by how two warps
@@ -249,15 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
       if (next > 0) load_tile<E, DP>(p, w.b, hb, pos_of(m + 1), next, sa);
       commit_tile();
     }
-    const float2 rn = make_float2(pw[n], pw[n]);
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int j = 0; j < R; ++j)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) M[i][x][j][y] = mul2(M[i][x][j][y], rn);
+    // U = the chunk's own sum, from zero: the rounding errors of M grow with its chunks, not its tokens
+    float2 U[R][4][R][2] = {};
 #pragma unroll 2
     for (int k = 0; k < n; ++k) {
       const float uw = pw[(w.back ? k : n - 1 - k) + late];
@@ -278,9 +271,18 @@ __global__ void __launch_bounds__(kThreads, 1) sweep_kernel(const __grid_constan
 #pragma unroll
           for (int j = 0; j < R; ++j)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) M[i][x][j][y] = fma2(f2, v[j][y], M[i][x][j][y]);
+            for (int y = 0; y < 2; ++y) U[i][x][j][y] = fma2(f2, v[j][y], U[i][x][j][y]);
         }
     }
+    const float2 rn = make_float2(pw[n], pw[n]);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) M[i][x][j][y] = fma2(rn, M[i][x][j][y], U[i][x][j][y]);
     // the next chunk's tiles: a in sx, b in sa, c (SUM: in sx) yet to come
     float* const old = sb;
     sb = sa;

@@ -92,3 +92,49 @@ def test_angles_and_their_turns(pairing):
     ws = torch.empty(cp.cpattn_rotate_bwd_workspace(d), dtype=torch.uint8, device=dev())
     checked(cp, cp.cpattn_rotate_bwd(d, None, None, None, None, inv_freq, p_dev, q, k, None, qo, ko, None, None, None, ws))
     compare(qo, -s)
+
+
+# ---------------------------------------------------------------------------
+# long sums
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sums_over_long_runs_off_the_tensor_cores(dtype):
+    """One run of 65536 tokens that add up without decay, each the same: the errors of a single
+    accumulator all point one way (up to 1e-3 of the sum).
+
+    A chunk's sum has 64 terms, a run's one a chunk, each rounded once: (64 + T / 64) 2^-24 of the
+    sum; an output is a product over D channels of it and two of at most max(D, 64) terms, its
+    weights and the scale.  All terms are positive, so this is relative to the values."""
+    cp = cp_mod()
+    H, T, D = 152, 65536, 8
+    d = cp.make_desc(1, H, H, T, D, 1, "contiguous", dtype)
+    assert cp.cpattn_linear_workspace(d) == cp.cpattn_linear_bwd_workspace(d) == 16  # one run a head
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    half = 2.0 ** -24 if dtype == "f32" else 2.0 ** -8
+    gen = torch.Generator().manual_seed(5)
+    rows = [(0.5 + torch.rand(H, D, generator=gen)).to(dt) for _ in range(4)]
+    q, k, v, do = (x.to(dev())[None, :, None].expand(1, H, T, D).contiguous() for x in rows)
+    ld = torch.zeros(H, device=dev())
+    o, dq, dk, dv = (torch.empty_like(q) for _ in range(4))
+    S, dS = (torch.empty(1, H, D, D, device=dev()) for _ in range(2))
+    ws = torch.empty(16, dtype=torch.uint8, device=dev())
+    checked(cp, cp.cpattn_linear_fwd(d, q, k, v, ld, None, None, o, S, ws))
+    checked(cp, cp.cpattn_linear_bwd(d, q, k, v, ld, None, do, None, dq, dk, dv, dS, ws))
+    q, k, v, do = (x.double() for x in rows)
+    scale, sums = float(d.scale), (64 + T / 64) * 2.0 ** -24
+    outs = sums + (D + 2 * 64 + 8) * 2.0 ** -24 + half
+
+    def close(got, ref, tol):
+        err = (got.double().cpu() / ref - 1).abs().max().item()
+        assert err <= tol, (err, tol)
+
+    kv, qdo = k[:, :, None] * v[:, None], q[:, :, None] * do[:, None]
+    close(S[0], T * kv, sums + 2.0 ** -22)
+    close(dS[0], scale * T * qdo, sums + 2.0 ** -22)
+    t = torch.arange(T, dtype=torch.float64)[None, :, None]
+    for h in range(0, H, 19):
+        at = slice(h, h + 1)
+        close(o[0, at], scale * (t + 1) * torch.einsum("hd,hde->he", q[at], kv[at])[:, None], outs)
+        close(dq[0, at], scale * (t + 1) * torch.einsum("he,hde->hd", do[at], kv[at])[:, None], outs)
+        close(dk[0, at], scale * (T - t) * torch.einsum("he,hde->hd", v[at], qdo[at])[:, None], outs)
+        close(dv[0, at], scale * (T - t) * torch.einsum("hd,hde->he", k[at], qdo[at])[:, None], outs)
