@@ -11,13 +11,13 @@
 //
 // M itself stays in float32, in registers (two threads a row, one channel of b).  b is weighted once
 // S has read it, as two bf16 numbers, hi in b's place and what is left, lo, in a place of its own,
-// and U is the sum of two products: 16 bits.  For a state that is handed out in float32, in the sums
-// and in the sequence's last run, it is three, 24 bits.  The smallest part is
+// and U is the sum of two products: 16 bits, in the runs' sums too.  For a state that is handed out in
+// float32, in the sums and in the sequence's last run, it is three, 24 bits.  The smallest part is
 // summed first: so the large numbers go through eight steps of the tensor cores' sum (16 terms
 // each) and not through all.  As operands P and M are rounded to bf16 once, like the output itself.
-// Errors against float64, of the norm (8192 tokens, D 128): outputs 2.3e-3, of which the output's
-// own rounding is 1.7e-3 (2.6e-3 with b in one part); states 1.0e-7 (2.4e-6 in two parts, 5.4e-7 in
-// three with the largest first).  U starts from zero in every chunk: no sum on the tensor cores
+// Errors against float64, of the norm: outputs 2.35e-3 whatever the decays, which is sqrt(2) times
+// their own rounding of 1.66e-3 (with b in one part in the sums 2.4e-3 to 2.8e-3, the more the longer
+// the memory); states 1.0e-7 (8192 tokens; 2.4e-6 in two parts, 5.4e-7 in three with the largest first).  U starts from zero in every chunk: no sum on the tensor cores
 // runs longer than 384 terms.
 //
 // Warp roles (640 threads):
@@ -32,9 +32,8 @@
 // O1, O2 and U of D columns each behind it.
 //
 // The first launch (SUM) only needs U and M: no a; warps 4-11 weigh b, ahead of warps 12-19, and U has
-// two places.  b in one part is weighted in place, with three stages of b and c (with two a chunk took
-// the 2500 cycles of a load, the weights and the product: 35 us against 30, below); three parts leave
-// room for two stages.
+// two places.  At D 128 two parts leave room for three stages of b and two of c (81.8 us for the
+// forward pass of 8192 tokens; two of b and three of c 84.3), three parts for two of each.
 //
 // Measured (GB300, D 128, 8192 tokens of 32 heads: 128 runs of 16 chunks): the sums 30 us, 3.4 TB/s
 // on 96 SMs; the sweep 62 us, 6000 cycles a chunk where 128 KB from and to memory would take
@@ -69,15 +68,15 @@ template <int D, bool SUM, bool EXACT>
 struct Smem {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kAS = SUM ? 0 : D == 128 ? 2 : 3;  // stages of a, of b, of c
-  static constexpr int kBS = !SUM ? kAS : EXACT ? (D == 128 ? 2 : 4) : D == 128 ? 3 : 6;
-  static constexpr int kCS = !SUM && D == 128 ? 1 : kBS;
-  static constexpr int kXS = !SUM ? 1 : !EXACT ? 0 : D == 128 ? 3 : 5;  // smaller parts of the weighted b
+  static constexpr int kBS = !SUM ? kAS : EXACT ? (D == 128 ? 2 : 4) : D == 128 ? 3 : 5;
+  static constexpr int kCS = D == 128 ? (SUM ? 2 : 1) : kBS;
+  static constexpr int kXS = !SUM ? 1 : EXACT ? (D == 128 ? 3 : 5) : D == 128 ? 2 : 3;  // smaller parts of the weighted b
   static constexpr int kA = 0;
   static constexpr int kB = kA + kAS * kTileBytes;
   static constexpr int kC = kB + kBS * kTileBytes;
   static constexpr int kX = kC + kCS * kTileBytes;
   // (at D 64 U reads on behind a part's tile, as far as another one)
-  static constexpr int kM = kX + (kXS + (SUM && EXACT && D == 64)) * kTileBytes;
+  static constexpr int kM = kX + (kXS + (SUM && D == 64)) * kTileBytes;
   // the output's staging, 4 KB a warp: at D 128 where a lies, at D 64 that is too small
   static constexpr int kO = kM + (SUM ? 0 : D * D * 2);
   static constexpr int kPow = kO + (SUM || D == 128 ? 0 : 8 * 4096);
@@ -191,8 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_tok = lin_tokens(p, bh);
   const float ld = lin_decay(p, bh);
   const int back = w.back, late = back;
-  // bf16 numbers of a weighted b: in the sums of the runs one does (2.36e-3 against 2.35e-3)
-  const int parts = !SUM ? (w.exact && run == p.segs - 1 ? 3 : 2) : EXACT && w.exact ? 3 : 1;
+  // bf16 numbers of a weighted b
+  const int parts = (SUM ? EXACT && w.exact : w.exact && run == p.segs - 1) ? 3 : 2;
   const int bb = bh / p.Hq, h = bh - bb * p.Hq;
   const int head_a = bb * (p.Hq / w.rep_a) + h / w.rep_a;
   const int head_b = bb * (p.Hq / w.rep_b) + h / w.rep_b;
@@ -287,34 +286,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a place for each of the smaller parts, two numbers ahead of the product; or (!SUM) for the smallest
     // alone, which U of the last chunk has read
     uint4* const xline = line + (L::kX - L::kB - wb.stage * L::kTileBytes) / 16;
-    if (SUM && parts == 1) {
-#pragma unroll 4
-      for (int j = 0; j < HC / 8; ++j) {
-        const int at = piece(j);
-        const uint4 x = line[at];
-        auto times = [&](uint32_t v) {
-          const float2 y = mul2(make_float2(bf16_lo(v), bf16_hi(v)), uw2);
-          return pack_bf16(y.x, y.y);
-        };
-        line[at] = make_uint4(times(x.x), times(x.y), times(x.z), times(x.w));
-      }
-    } else if (SUM) {
-      const int x0 = wx, x1 = wx + 1 == XS ? 0 : wx + 1;
-      const uint32_t par0 = xpar, par1 = x1 == 0 ? xpar ^ 1u : xpar;
-      if (!warp_wait(x_empty(x0), par0 ^ 1u, abort, p.status, tmo) ||
-          !warp_wait(x_empty(x1), par1 ^ 1u, abort, p.status, tmo))
-        return false;
-      uint4* const l0 = xline + x0 * (L::kTileBytes / 16);
-      uint4* const l1 = xline + x1 * (L::kTileBytes / 16);
+    if (SUM) {
+      auto place = [&](uint4*& l) -> bool {
+        if (!warp_wait(x_empty(wx), xpar ^ 1u, abort, p.status, tmo)) return false;
+        l = xline + wx * (L::kTileBytes / 16);
+        if (++wx == XS) wx = 0, xpar ^= 1u;
+        return true;
+      };
+      uint4 *l0, *l1;  // the smallest part's, the middle one's (of two parts: l0)
+      if (!place(l0)) return false;
+      if (EXACT && parts == 3) {
+        if (!place(l1)) return false;
 #pragma unroll 2
-      for (int j = 0; j < HC / 8; ++j) {
-        const int at = piece(j);
-        uint4 hi;
-        split(line[at], hi, l1[at], l0[at], true);
-        line[at] = hi;
+        for (int j = 0; j < HC / 8; ++j) {
+          const int at = piece(j);
+          uint4 hi;
+          split(line[at], hi, l1[at], l0[at], true);
+          line[at] = hi;
+        }
+      } else {
+#pragma unroll 2
+        for (int j = 0; j < HC / 8; ++j) {
+          const int at = piece(j);
+          uint4 hi, lo;
+          split(line[at], hi, l0[at], lo, false);
+          line[at] = hi;
+        }
       }
-      wx = x1 + 1 == XS ? 0 : x1 + 1;
-      xpar = wx <= x0 ? xpar ^ 1u : xpar;
     } else if (parts == 2) {
 #pragma unroll 2
       for (int j = 0; j < HC / 8; ++j) {
@@ -502,15 +500,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!SUM) {
 #pragma unroll 1
           for (int part = 0; part < 2; ++part) product(part ? bd0 + st : xd0, part == 0);
-        } else if (parts == 3) {
-          for (int part = 0; part < 2; ++part) {
+        } else {
+#pragma unroll 1
+          for (int part = 0; part < parts - 1; ++part) {
             product(xd0 + x * (L::kTileBytes >> 4), part == 0);
             if (leader) mma_commit(x_empty(x));
             __syncwarp();
             if (++x == XS) x = 0;
           }
         }
-        if (SUM) product(bd0 + st, parts == 1);
+        if (SUM) product(bd0 + st, false);
         if (!SUM && parts == 3) {
           if (leader) mma_commit(h_done);
           __syncwarp();

@@ -138,3 +138,58 @@ def test_sums_over_long_runs_off_the_tensor_cores(dtype):
         close(dq[0, at], scale * (t + 1) * torch.einsum("he,hde->hd", do[at], kv[at])[:, None], outs)
         close(dk[0, at], scale * (T - t) * torch.einsum("he,hde->hd", v[at], qdo[at])[:, None], outs)
         close(dv[0, at], scale * (T - t) * torch.einsum("hd,hde->he", k[at], qdo[at])[:, None], outs)
+
+
+# ---------------------------------------------------------------------------
+# roundings on the tensor cores, by norm
+# ---------------------------------------------------------------------------
+def by_chunks(a, b, c, ld, scale):
+    """out_i = scale sum over j <= i of r^(i-j) (a_i . b_j) c_j in float64, and the sum of
+    r^(T-1-j) b_j c_j^T, by chunks of 256 on the GPU."""
+    B, H, T, D = a.shape
+    out = torch.empty(B, H, T, D, dtype=torch.float64, device=a.device)
+    S = torch.zeros(B, H, D, D, dtype=torch.float64, device=a.device)
+    ld = ld.double()[:, None]
+    for at in range(0, T, 256):
+        x, y, z = (u[:, :, at:at + 256].double() for u in (a, b, c))
+        n = x.shape[2]
+        i = torch.arange(n, device=a.device, dtype=torch.float64)
+        w = torch.exp(ld[:, :, None] * (i[:, None] - i).clamp(min=0)) * (i[:, None] >= i)
+        out[:, :, at:at + n] = scale * ((x @ y.transpose(-1, -2) * w) @ z + torch.exp(ld * (i + 1))[..., None] * (x @ S))
+        S = torch.exp(ld * n)[..., None] * S + (y * torch.exp(ld * (n - 1 - i))[..., None]).transpose(-1, -2) @ z
+    return out, S
+
+
+def off(got, ref):
+    return ((got.double() - ref).norm() / ref.norm()).item()
+
+
+@pytest.mark.parametrize("H,T,D", [(32, 2048, 128), (8, 8192, 128), (12, 4096, 64), (4, 2048, 64)])
+@pytest.mark.parametrize("memory", [256, 16384])
+def test_outputs_by_norm(H, T, D, memory):
+    """Outputs and gradients of sequences in several runs, with memories short and long, with the
+    states handed out and without.
+
+    A rounding to bf16 is off by 2^-8 / sqrt(3) * sqrt(3 / 8 / ln 2) = 1.66e-3 of a number, root mean
+    square.  An output has its own, and each term of its sum one more, of the weighted score or of
+    the state as an operand, independent of each other: 1.66e-3 sqrt(2) = 2.35e-3 of the norm.  Keys in
+    two numbers add 1e-5, keys in one up to another 1.66e-3: 2.87e-3 in all."""
+    cp = cp_mod()
+    d = cp.make_desc(1, H, H, T, D, 1, "contiguous", "bf16")
+    assert cp.cpattn_linear_workspace(d) > 16  # runs
+    gen = torch.Generator(dev()).manual_seed(3)
+    q, k, v, do = (torch.randn(1, H, T, D, device=dev(), generator=gen).bfloat16() for _ in range(4))
+    ld = -torch.logspace(0, -np.log10(memory), H, device=dev())
+    ws = torch.empty(max(cp.cpattn_linear_workspace(d), cp.cpattn_linear_bwd_workspace(d)), dtype=torch.uint8, device=dev())
+    flip = lambda x: x.flip(2)  # noqa: E731
+    scale = float(d.scale)
+    want = {"o": by_chunks(q, k, v, ld, scale)[0], "dq": by_chunks(do, v, k, ld, scale)[0],
+            "dk": flip(by_chunks(flip(v), flip(do), flip(q), ld, scale)[0]),
+            "dv": flip(by_chunks(flip(k), flip(q), flip(do), ld, scale)[0])}
+    for state in (False, True):
+        S, dS = (torch.empty(1, H, D, D, device=dev()) if state else None for _ in range(2))
+        got = {n: torch.empty_like(q) for n in want}
+        checked(cp, cp.cpattn_linear_fwd(d, q, k, v, ld, None, None, got["o"], S, ws))
+        checked(cp, cp.cpattn_linear_bwd(d, q, k, v, ld, None, do, None, got["dq"], got["dk"], got["dv"], dS, ws))
+        for n in want:
+            assert off(got[n], want[n]) < 2.4e-3, (n, state, off(got[n], want[n]))
