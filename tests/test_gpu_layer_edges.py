@@ -193,3 +193,26 @@ def test_outputs_by_norm(H, T, D, memory):
         checked(cp, cp.cpattn_linear_bwd(d, q, k, v, ld, None, do, None, got["dq"], got["dk"], got["dv"], dS, ws))
         for n in want:
             assert off(got[n], want[n]) < 2.4e-3, (n, state, off(got[n], want[n]))
+
+
+@pytest.mark.parametrize("H,T,D", [(32, 2048, 128), (12, 4096, 64), (152, 1024, 128), (152, 1000, 64), (3, 100, 128)])
+def test_states_handed_out_by_norm(H, T, D):
+    """state_out and dstate_in, from sequences in several runs and in one.
+
+    Keys in two bf16 numbers would leave (1.66e-3)^2 = 2.7e-6 of each product, in three 5e-9.  What is
+    left is float32's: a chunk's sum rounds 24 times (three parts of eight steps), the state once a chunk,
+    and memories here span a few chunks; taken as 2^-23 each and half of them one way, 2e-7 to 4e-7."""
+    cp = cp_mod()
+    d = cp.make_desc(1, H, H, T, D, 1, "contiguous", "bf16")
+    gen = torch.Generator(dev()).manual_seed(4)
+    q, k, v, do = (torch.randn(1, H, T, D, device=dev(), generator=gen).bfloat16() for _ in range(4))
+    ld = -torch.logspace(-0.5, -2.5, H, device=dev())
+    ws = torch.empty(max(cp.cpattn_linear_workspace(d), cp.cpattn_linear_bwd_workspace(d)), dtype=torch.uint8, device=dev())
+    S, dS = (torch.empty(1, H, D, D, device=dev()) for _ in range(2))
+    o, dq, dk, dv = (torch.empty_like(q) for _ in range(4))
+    checked(cp, cp.cpattn_linear_fwd(d, q, k, v, ld, None, None, o, S, ws))
+    checked(cp, cp.cpattn_linear_bwd(d, q, k, v, ld, None, do, None, dq, dk, dv, dS, ws))
+    assert off(S, by_chunks(q, k, v, ld, 1.0)[1]) < 5e-7
+    # sum of r^(i+1) q_i dO_i^T: the state of the reversed sequence, decayed once more
+    ref = by_chunks(q.flip(2), q.flip(2), do.flip(2), ld, 1.0)[1] * torch.exp(ld.double())[:, None, None]
+    assert off(dS, float(d.scale) * ref) < 5e-7
