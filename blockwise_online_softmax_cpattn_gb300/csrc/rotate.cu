@@ -3,13 +3,13 @@
 // attention's token order; values move along.  And its backward pass.
 //
 // A row of D channels belongs to D / 2P lanes, rounded up to a power of two, with P = 8 in bf16 (8
-// lanes at D 128, four rows a warp), or 4 where D or the rotation is no multiple of 16, and 4 in
-// float32: vectors of 16 bytes.  Lane l owns
+// lanes at D 128, four rows a warp), or 4 where D or the rotation is no multiple of 16 or rows are few
+// (cut, below), and 4 in float32: vectors of 16 bytes.  Lane l owns
 // pairs P l .. P l + P-1 of the rotation, as two vectors of P channels: at P l and rot/2 + P l when
 // pairs lie half a rotation apart, else 2P channels in a row.  So a pair never crosses lanes, the
 // only exchange is the norm's sum (three shuffles at D 128), and each row is read and written
-// once.  (With P 4 alone the shuffles and what each head costs anyway held the backward pass at
-// 81 us for 8192 tokens of 48 heads, 3.3 TB/s.)
+// once.  (With P 4 the shuffles and what each head costs anyway take 58.8 us in the backward pass of
+// 8000 tokens of 40 heads, with P 8 47.7.)
 //
 // A warp takes the same slots (four at D 128) of a run of heads, one head after the other: a
 // slot's angles are the same in every head, so a lane forms the cosines and sines of its pairs
@@ -536,14 +536,25 @@ static cudaError_t launch(const Rotate& p, int grid, bool backward, cudaStream_t
 
 // Pairs a lane, groups of slots, and parts that the heads are cut into: one part shares a slot's
 // angles among all its heads, but a decoding step's few tokens want every SM, down to a head a
-// warp.  There eight pairs a lane would mean eight angles one after the other: 5.0 us against 4.3
-// with four (64 tokens of 40 heads).
-static int cut(Rotate* p) {
+// warp.  Eight pairs a lane cost half the warps and shuffles a row, but twice the angles one after
+// the other, and half the warps are there to wait for memory: they pay from 8 warps' rows (of four pairs
+// a lane) a warp on, in the backward pass from 4.  Four and eight, us, forward / backward, 40 heads of
+// 128: 64 tokens 4.3 / 7.2 and 4.8 / 9.1; 975 12.7 / 14.0 and 16.2 / 15.1; 2000 16.6 / 20.6 and 18.9 /
+// 19.5; 3250 21.3 / 28.3 and 21.6 / 24.7; 5000 28.5 / 40.5 and 26.9 / 35.0.  48 heads of 64, half the
+// lanes a row: 1666 12.9 / 14.4 and 16.4 / 15.6; 3333 16.2 / 20.2 and 18.7 / 19.9; 6666 23.7 / 32.6
+// and 23.4 / 29.3.
+static int cut(Rotate* p, bool backward) {
   const int heads = p->Hq + p->Hkv + (p->in[2].p ? p->Hkv : 0);
   const int64_t want = (int64_t)kSms * 64;  // warps
-  p->P = p->bf16 && p->D % 16 == 0 && p->rot % 16 == 0 && (int64_t)p->B * p->T * heads > 4 * want ? 8 : 4;
-  p->lanes = 1;
-  while (p->lanes * 2 * p->P < p->D) p->lanes *= 2;
+  auto set_pairs = [&](int P) {
+    p->P = P;
+    p->lanes = 1;
+    while (p->lanes * 2 * P < p->D) p->lanes *= 2;
+  };
+  set_pairs(4);
+  if (p->bf16 && p->D % 16 == 0 && p->rot % 16 == 0 &&
+      (int64_t)p->B * p->T * heads * p->lanes / 32 > (backward ? 4 : 8) * want)
+    set_pairs(8);
   p->inv_d = 1.f / p->D;
   const int per = 32 / p->lanes;
   p->groups = (p->B * p->T + per - 1) / per;
@@ -562,13 +573,13 @@ size_t rotate_bwd_workspace(int D, int norm) {
 }
 
 cudaError_t launch_rotate_fwd(Rotate p, cudaStream_t st) {
-  const int grid = cut(&p);
+  const int grid = cut(&p, false);
   return launch(p, grid, false, st);
 }
 
 cudaError_t launch_rotate_bwd(Rotate p, float* dqw, float* dkw, cudaStream_t st) {
   // two blocks an SM, but no more warps than there are heads of groups
-  const int blocks = cut(&p), grid = blocks < kBwdBlocks ? blocks : kBwdBlocks;
+  const int blocks = cut(&p, true), grid = blocks < kBwdBlocks ? blocks : kBwdBlocks;
   cudaError_t e = launch(p, grid, true, st);
   if (e != cudaSuccess || !p.norm || (!dqw && !dkw)) return e;
   timing_begin("rotate_bwd_sum", st);

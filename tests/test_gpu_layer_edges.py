@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from gpu_helpers import cp_mod, dev
-from test_gpu_layer import checked, spread_decays
+from oracle import layer as L
+from test_gpu_layer import LinearCase, checked, draw, f64, pair_sum, rotation_case, spread_decays, within
 
 pytestmark = pytest.mark.gpu
 
@@ -216,3 +217,13 @@ def test_states_handed_out_by_norm(H, T, D):
     # sum of r^(i+1) q_i dO_i^T: the state of the reversed sequence, decayed once more
     ref = by_chunks(q.flip(2), q.flip(2), do.flip(2), ld, 1.0)[1] * torch.exp(ld.double())[:, None, None]
     assert off(dS, float(d.scale) * ref) < 5e-7
+
+
+# ---------------------------------------------------------------------------
+# norm and rotation: many rows (eight pairs a lane in the backward pass, then in both)
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T,D,kw", [(1500, 128, {}), (2900, 128, {}), (2900, 128, {"pairing": "neighbours", "rot": 96}),
+                                    (2900, 96, {"rot": 32}), (2900, 112, {"pairing": "neighbours", "rot": 16}),
+                                    (2900, 128, {"norm": False, "rot": 64})])
+def test_rotation_of_many_rows(T, D, kw):
+    rotation_case(cp_mod(), 1, 40, 8, T, D, "bf16", seed=T + D, **kw)
