@@ -227,3 +227,47 @@ def test_states_handed_out_by_norm(H, T, D):
                                     (2900, 128, {"norm": False, "rot": 64})])
 def test_rotation_of_many_rows(T, D, kw):
     rotation_case(cp_mod(), 1, 40, 8, T, D, "bf16", seed=T + D, **kw)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_rotation_of_packed_tokens_in_float32(D):
+    """A server's tokens in float32, [n, heads, D], each at its own position; output over input."""
+    cp = cp_mod()
+    rng = np.random.default_rng(6)
+    n, Hq, Hkv = 45, 6, 2
+    x, x64 = draw(rng, (n, Hq + 2 * Hkv, D), "f32")
+    pos = rng.integers(0, 10 ** 6, (1, n)).astype(np.int32)
+    f = 1e6 ** (-2 * np.arange(D // 2) / D)
+    w, w64 = draw(rng, (D,), "f32")
+    d = cp.make_rotate_desc(1, Hq, Hkv, n, D, dtype="f32")
+    q, k, v = (x[:, a:b].transpose(0, 1).unsqueeze(0) for a, b in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, Hq + 2 * Hkv)))
+    checked(cp, cp.cpattn_rotate_fwd(d, q, k, v, w, w, torch.from_numpy(f).to(dev()), torch.from_numpy(pos).to(dev()),
+                                     q, k, v))
+    heads, got = x64.transpose(1, 0, 2)[None], f64(x).transpose(1, 0, 2)[None]
+    turned = heads[:, :Hq + Hkv]
+    ref = L.rotate_fwd(turned, w64, 1e-6, pos, f, D, "halves")
+    # 2^-18 of the pair for the norm, the cosine and the sine (an angle off by 2^-25), and the rounding
+    u = pair_sum(turned / np.sqrt((turned ** 2).mean(-1, keepdims=True) + 1e-6) * w64, D, "halves")
+    within(got[:, :Hq + Hkv], ref, 2.0 ** -18 * u + 2.0 ** -24 * np.abs(ref))
+    assert np.array_equal(got[:, Hq + Hkv:], heads[:, Hq + Hkv:])
+
+
+# ---------------------------------------------------------------------------
+# waits that run out, in the kernels of other sizes and orders
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("D,T,ranks,layout", [(64, 700, 1, "contiguous"), (128, 1200, 3, "zigzag"), (64, 528, 2, "zigzag")])
+def test_timeouts_of_other_kernels(D, T, ranks, layout):
+    """The first chunk's loads never count as done: the status says so, and the next call is right."""
+    c = LinearCase(1, 2, 2, T, D, "bf16", ranks, layout)
+    cp = c.cp
+    for backward in (False, True):
+        c.d.debug_fault = 1
+        if backward:
+            outs = [torch.empty_like(x) for x in (c.q, c.k, c.v, c.S0)]
+            c.backward(outs, torch.empty(cp.cpattn_linear_bwd_workspace(c.d), dtype=torch.uint8, device=dev()))
+        else:
+            c.forward()
+        assert cp.cpattn_check() == cp.ERR_TIMEOUT
+        assert cp.cpattn_check() == cp.OK
+        c.d.debug_fault = 0
+        c.check_forward()
