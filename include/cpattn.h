@@ -686,7 +686,9 @@ cpattn_status cpattn_linear_fwd(const cpattn_desc* desc, const void* q, const vo
 size_t cpattn_linear_bwd_workspace(const cpattn_desc* desc);
 
 /*
- * Backward of cpattn_linear_fwd without lengths (behind a shorter row's end give dO = 0).
+ * Backward of cpattn_linear_fwd without lengths.  A shorter row's gradients come with dO = 0
+ * behind its end, anything finite in q, k and v there, and no dstate_out (it is the gradient
+ * of the state behind token T).
  *   dO         : [B][H_q][T][D]
  *   dstate_out : upstream gradient of state_out, or null for zero.  Must be null for a scale below
  *                2^-64 (CPATTN_ERR_UNSUPPORTED): it is carried divided by the scale

@@ -271,3 +271,32 @@ def test_timeouts_of_other_kernels(D, T, ranks, layout):
         assert cp.cpattn_check() == cp.OK
         c.d.debug_fault = 0
         c.check_forward()
+
+
+# ---------------------------------------------------------------------------
+# gradients of padded rows
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("f32", 40)])
+def test_gradients_of_padded_rows(dtype, D):
+    """With dO = 0 behind the rows' ends and no dstate_out: the gradients of the rows cut there, and
+    zeros behind."""
+    T, ends = 700, [1, 130, 640, 700]
+    c = LinearCase(len(ends), 2, 1, T, D, dtype)
+    for b, n in enumerate(ends):
+        c.do[0, b, :, n:] = 0
+    outs = [torch.empty_like(x) for x in (c.q, c.k, c.v, c.S0)]
+    ws = torch.empty(c.cp.cpattn_linear_bwd_workspace(c.d), dtype=torch.uint8, device=dev())
+    c.dS1 = None
+    c.backward(outs, ws)
+    c.cp.check(c.cp.cpattn_check())
+    got = [c.unshard(x) for x in outs[:3]] + [c.unshard(outs[3], False)]
+    for b, n in enumerate(ends):
+        cut = lambda x: x[b:b + 1, :, :n]  # noqa: E731
+        q, k, v, do = map(cut, c.nat)
+        S0 = c.states[0][b:b + 1]
+        ref = L.linear_bwd(q, k, v, c.ld, c.scale, do, S0)
+        A = L.linear_bwd(*map(np.abs, (q, k, v)), c.ld, c.scale, np.abs(do), np.abs(S0))
+        for i, name in enumerate(("dq", "dk", "dv")):
+            within(got[i][b:b + 1, :, :n], ref[i], c.bounds(ref[i], A[i], dtype), name)
+            assert not got[i][b, :, n:].any()
+        within(got[3][b:b + 1], ref[3], c.state_bounds(ref[3], A[3]), "dstate")
