@@ -120,8 +120,8 @@ static cpattn_status validate_linear(const cpattn_desc* d, Ring* R) {
 // values twice and starts from its predecessors' states.  In units of a chunk's time on one SM
 // (on the tensor cores some 3 us, in float32 some 20): a chunk of a sweep 1, of a sum 0.3 (0.6), a
 // block's start 1 (0.15), folding a predecessor's state 0.25 (0.1), the second launch 2 (0.5).  Of
-// 24 problems of 8 to 128 heads and 300 to 32768 tokens, backward passes among them, every cut's
-// time was within 4.5 % of the best one's, all but three within 2 %.
+// 22 problems of 2 to 128 heads and 300 to 32768 tokens, backward passes among them, every cut's
+// time was within 2 % of the best one's of up to 20 others.
 static void cut_runs(const Ring& R, bool tc, int sweeps, int sums, Linear* p) {
   const int C = tc ? kLinTcChunk : kLinSimtChunk;
   // (off the tensor cores a chunk's slots are looked up one by one)

@@ -8,8 +8,8 @@
 // in shared memory as the operand of a M.  Head dimensions in between are padded with zeros to
 // 64 or 128.  Bound by the float32 units, 4 D (D + 32) FLOP a token and head, and by how two warps
 // a scheduler (a block fills an SM's shared memory) wait for each other's chains: 8192 tokens of 32
-// heads at D 128 take 881 us, the units' part of it 332 (32 heads on 8 with gradients 2.2 ms); 1500
-// tokens of 16 heads, 2 or 3 chunks a block, 98 (43).  With tiles fetched when they were needed, and
+// heads at D 128 take 889 us, the units' part of it 332 (32 heads on 8 with gradients 2.2 ms); 1500
+// tokens of 16 heads, 2 or 3 chunks a block, 99 (43).  With tiles fetched when they were needed, and
 // not ahead, these took 1269, 3018 and 104 us; 16 warps with 4 x 4 tiles were slower, too (121).
 #include "layer.cuh"
 

@@ -35,8 +35,8 @@
 // two places.  At D 128 two parts leave room for three stages of b and two of c (81.8 us for the
 // forward pass of 8192 tokens; two of b and three of c 84.3), three parts for two of each.
 //
-// Measured (GB300, D 128, 8192 tokens of 32 heads: 128 runs of 16 chunks): the sums 30 us, 3.4 TB/s
-// on 96 SMs; the sweep 62 us, 6000 cycles a chunk where 128 KB from and to memory would take
+// Measured (GB300, D 128, 8192 tokens of 32 heads: 128 runs of 16 chunks): the sums 32 us, 3.2 TB/s
+// on 96 SMs; the sweep 60 us, 6000 cycles a chunk where 128 KB from and to memory would take
 // 4700 and the products 3100; 131072 tokens of 8 heads 235 us (152 runs).  It is bound by two chains
 // that come to some 6000 cycles each: S -> P -> O1 -> output -> P of the next chunk, and weights ->
 // U -> M -> its copy -> weights of the next.  Code that runs once a chunk in each of 20 warps is
@@ -818,10 +818,12 @@ static cudaError_t run(const Linear& p, int n, const LinSweep* sweeps, bool depe
 bool linear_tc_supported(const Ring& R) {
   if (!R.bf16 || (R.D != 64 && R.D != 128)) return false;
   // A chunk's positions are consecutive slots, so a zigzag half of h tokens takes h / 128 chunks,
-  // rounded up, and a chunk costs the same whatever it holds.  Halves of 16 against float32
-  // arithmetic at 15: 4 heads of 128 (T 128, 120) 25 against 54 us, of 64 16 against 27; 32 heads
-  // (T 1024, 960) of 128 151 against 159, of 64 95 against 76; at 64 tokens 130, where float32 would
-  // take some 650 (in proportion to 15).
+  // rounded up, and a chunk costs the same whatever it holds; float32 arithmetic packs its chunks.
+  // Forward and backward pass here against there, us, 32 ranks with halves of 12, 16 and 64 tokens:
+  // 32 heads of 128 105 and 231 against 123 and 274, 161 and 437, 774 and 1784; of 64 75 and 172
+  // against 59 and 131, 77 and 209, 291 and 778; 4 heads of 128 56 and 63 against 58 and 66, 63 and
+  // 96, 120 and 252; of 64 37 and 37 against 26 and 29, 28 and 45, 51 and 117.  From 16 on all but the
+  // last's forward pass are faster here.
   if (R.zz && R.T / R.cp / 2 < 16) return false;
   return (double)R.B * R.Hq * R.T < 2147483647.0 - kLinTcChunk;
 }
