@@ -35,8 +35,8 @@
 // two places.  At D 128 two parts leave room for three stages of b and two of c (81.8 us for the
 // forward pass of 8192 tokens; two of b and three of c 84.3), three parts for two of each.
 //
-// Measured (GB300, D 128, 8192 tokens of 32 heads: 128 runs of 16 chunks): the sums 32 us, 3.2 TB/s
-// on 96 SMs; the sweep 60 us, 6000 cycles a chunk where 128 KB from and to memory would take
+// Measured (GB300, D 128, 8192 tokens of 32 heads: 128 runs of 16 chunks): the sums 35 us, 2.9 TB/s
+// on 96 SMs; the sweep 61 us, 6000 cycles a chunk where 128 KB from and to memory would take
 // 4700 and the products 3100; 131072 tokens of 8 heads 235 us (152 runs).  It is bound by two chains
 // that come to some 6000 cycles each: S -> P -> O1 -> output -> P of the next chunk, and weights ->
 // U -> M -> its copy -> weights of the next.  Code that runs once a chunk in each of 20 warps is

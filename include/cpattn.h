@@ -658,8 +658,8 @@ cpattn_status cpattn_rotate_bwd(const cpattn_rotate_desc* desc, const void* q,
  * and the state that a chunk of 128 tokens starts from are rounded to bf16 as operands, weighted
  * keys to two bf16 numbers.  States are float32 throughout; what goes into one that is handed out
  * carries 24 bits.  (Of 8192 tokens the outputs are off by 2.4e-3 of their norm, 1.7e-3 of it their
- * own rounding to bf16, and the state by 1e-7.)  All else runs in float32.  Inputs must be finite:
- * in a chunk an infinity or NaN reaches earlier tokens too.
+ * own rounding to bf16, and the state by 1e-7, or 6e-7 where hardly anything fades.)  All else runs
+ * in float32.  Inputs must be finite: in a chunk an infinity or NaN reaches earlier tokens too.
  */
 
 /* Bytes of device workspace of cpattn_linear_fwd: states of the parts into which a sequence

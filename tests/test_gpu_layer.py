@@ -5,7 +5,7 @@ Tolerances (half a step of a rounding: bf16 2^-8, float32 2^-24 of the value).
 
 Rotation, forward.  u = w x r: r = rsqrt of a sum of D squares, off by less than 2^-19 (D
 additions of 2^-24 each in chains of at most 20, rsqrtf 2^-22); cosine and sine off by less
-than 2^-21 (sincospif, and an angle off by 2^-30); so y is off by at most 2^-18 (|u_a| + |u_b|)
+than 2^-21 (sincospif, and an angle off by 2^-25); so y is off by at most 2^-18 (|u_a| + |u_b|)
 of its pair, and its own rounding.
 Backward.  With h = w g and n = x r, dx = r (h - n mean(h n)) is off by at most
 2^-17 r (|h_a| + |h_b| + |n| mean(|h| |n|)) and its rounding; dw, a sum of N rows of terms off by
@@ -13,9 +13,10 @@ Backward.  With h = w g and n = x r, dx = r (h - n mean(h n)) is off by at most
 
 Linear attention.  Everything is bounded by the same sums with magnitudes in place of values
 (A: the oracle run on |q|, |k|, |v|, |S|).  On the tensor cores P, the state as an operand and
-the weighted keys are each rounded to bf16, so an output is off by at most two such roundings,
-2 * 2^-8 A (second order and float32: 2^-12 A), and its own.  States handed out carry 16 bits of
-every product (2^-16), float32 folds (2^-22 each chunk) and weights off by 2^-17: 2^-14 A.  In
+the weighted keys are rounded to bf16 (keys to two such numbers, 2^-16), so an output is off by at
+most two such roundings, 2 * 2^-8 A (second order and float32: 2^-12 A), and its own.  States handed
+out carry 24 bits of every product (here 16 would pass, 2^-16; by norm they are held to 24 in
+test_gpu_layer_edges.py), float32 folds (2^-22 each chunk) and weights off by 2^-17: 2^-14 A.  In
 float32 throughout: at most T + D additions in a chain, weights off by 2^-17:
 (2^-24 (T + D) + 2^-16) A.  Gradients are the same sums.
 A power of a decay below float32's least normal number, 2^-126, may count as 0: that is off by at
